@@ -33,6 +33,7 @@ EXPORTS = (
     "adaln_bwd_varlen", "adaln_bwd_varlen_partials", "adaln_bwd_varlen_reduce",
     "adaln_read_status", "adaln_bwd_recompute_workspace_size", "adaln_bwd_recompute",
     "adaln_bwd_varlen_recompute_workspace_size", "adaln_bwd_varlen_recompute", "adaln_bwd_noalloc", "adaln_noalloc_read_status", "adaln_sum_ranks", "adaln_debug_read",
+    "adaln_layernorm_fwd", "adaln_layernorm_bwd_workspace_size", "adaln_layernorm_bwd",
     "adaln_bucket_batch", "adaln_bucket_batch_real",
     "adaln_fit_step_cost", "adaln_bucket_load_cv", "adaln_status_string",
 )
@@ -77,6 +78,9 @@ def _load() -> ctypes.CDLL:
                                         sz, ci, vp], ci),
         "adaln_bwd_noalloc": ([vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, vp], ci),
         "adaln_noalloc_read_status": ([vp], ci),
+        "adaln_layernorm_fwd": ([vp, vp, vp, vp, vp, vp, i64, i64, f32, ci, vp], ci),
+        "adaln_layernorm_bwd_workspace_size": ([i64, i64, ci], sz),
+        "adaln_layernorm_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i64, i64, ci, vp], ci),
         "adaln_sum_ranks": ([vp, vp, i32, i64, vp], ci),
         "adaln_debug_read": ([vp, ci], ci),
         "adaln_bucket_batch": ([i64, i64, i64, i32], i64),
@@ -256,6 +260,23 @@ def adaln_bwd_noalloc(dy, x, mean, rstd, scale, dx, dshift, dscale, Bt, N, D, dt
 
 def adaln_noalloc_read_status(stream=None) -> int:
     return int(lib().adaln_noalloc_read_status(_stream(stream)))
+
+
+def adaln_layernorm_fwd(x, weight, bias, y, mean, rstd, R, D, eps=1e-6, dtype=None, stream=None):
+    _check("adaln_layernorm_fwd", lib().adaln_layernorm_fwd(
+        _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), R, D, eps, _dtype(dtype, x),
+        _stream(stream)))
+
+
+def adaln_layernorm_bwd_workspace_size(R, D, dtype) -> int:
+    return int(lib().adaln_layernorm_bwd_workspace_size(R, D, int(dtype)))
+
+
+def adaln_layernorm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, workspace, workspace_bytes, R, D,
+                        dtype=None, stream=None):
+    _check("adaln_layernorm_bwd", lib().adaln_layernorm_bwd(
+        _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx), _ptr(dweight), _ptr(dbias),
+        _ptr(workspace), workspace_bytes, R, D, _dtype(dtype, dy), _stream(stream)))
 
 
 def adaln_sum_ranks(parts, out, world, n, stream=None):

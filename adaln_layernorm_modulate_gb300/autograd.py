@@ -27,9 +27,11 @@ from . import (ADALN_BF16, ADALN_F32, AdalnError, adaln_bwd, adaln_bwd_recompute
                adaln_bwd_recompute_workspace_size, adaln_bwd_varlen, adaln_bwd_varlen_recompute,
                adaln_bwd_varlen_recompute_workspace_size, adaln_bwd_varlen_workspace_size,
                adaln_bwd_workspace_size, adaln_fwd, adaln_fwd_varlen, adaln_fwd_varlen_workspace_size,
+               adaln_layernorm_bwd, adaln_layernorm_bwd_workspace_size, adaln_layernorm_fwd,
                adaln_read_status)
 
-__all__ = ["AdaLNModulateFunction", "AdaLNModulate", "adaln_modulate"]
+__all__ = ["AdaLNModulateFunction", "AdaLNModulate", "adaln_modulate", "LayerNormFunction", "LayerNorm",
+           "layer_norm"]
 
 
 def _code(t: torch.Tensor) -> int:
@@ -167,3 +169,74 @@ class AdaLNModulate(torch.nn.Module):
 
     def extra_repr(self) -> str:
         return "eps=%g, save_stats=%s" % (self.eps, self.save_stats)
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """y = (x - mean) * rstd * weight + bias over the last dimension of x [..., D], weight and
+    bias [D] (either may be None). Saves x, weight and the fp32 row statistics. Gradients that
+    autograd does not ask for are not computed, except that dx always is."""
+
+    @staticmethod
+    def forward(ctx, x, weight=None, bias=None, eps: float = 1e-6):
+        if not x.is_cuda:
+            raise ValueError("layer_norm runs on CUDA tensors")
+        if x.dim() < 1:
+            raise ValueError("layer_norm input: x [..., D]")
+        D = x.shape[-1]
+        for p in (weight, bias):
+            if p is not None and p.shape != (D,):
+                raise ValueError("layer_norm: weight and bias are [D]")
+            if p is not None and p.dtype != x.dtype:
+                raise TypeError("x, weight and bias must share one dtype")
+            if p is not None and p.device != x.device:
+                raise ValueError("x, weight and bias must be on one device")
+        dt = _code(x)
+        x = x.contiguous()
+        weight = None if weight is None else weight.contiguous()
+        R = x.numel() // D if D else 0
+        y = torch.empty_like(x)
+        mean = torch.empty(R, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(R, dtype=torch.float32, device=x.device)
+        adaln_layernorm_fwd(x, weight, None if bias is None else bias.contiguous(), y, mean, rstd, R, D, eps,
+                            dt)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        dt, D, R = _code(x), x.shape[-1], mean.numel()
+        dy = dy.contiguous()
+        dx = torch.empty_like(x)
+        want_w, want_b = weight is not None and ctx.needs_input_grad[1], ctx.needs_input_grad[2]
+        dweight = torch.empty(D, dtype=torch.float32, device=x.device) if want_w else None
+        dbias = torch.empty(D, dtype=torch.float32, device=x.device) if want_b else None
+        nb = adaln_layernorm_bwd_workspace_size(R, D, dt)
+        ws = _workspace(nb, x.device)
+        adaln_layernorm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, ws, nb, R, D, dt)
+        return (dx, dweight.to(x.dtype) if want_w else None, dbias.to(x.dtype) if want_b else None, None)
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-6) -> torch.Tensor:
+    """Differentiable affine layer norm over the last dimension."""
+    return LayerNormFunction.apply(x, weight, bias, eps)
+
+
+class LayerNorm(torch.nn.Module):
+    """Layer norm with a learned weight (ones) and bias (zeros), each optional."""
+
+    def __init__(self, D: int, eps: float = 1e-6, weight: bool = True, bias: bool = True, device=None,
+                 dtype=None):
+        super().__init__()
+        self.eps = float(eps)
+        self.D = int(D)
+        self.weight = torch.nn.Parameter(torch.ones(D, device=device, dtype=dtype)) if weight else None
+        self.bias = torch.nn.Parameter(torch.zeros(D, device=device, dtype=dtype)) if bias else None
+
+    def forward(self, x):
+        return layer_norm(x, self.weight, self.bias, self.eps)
+
+    def extra_repr(self) -> str:
+        return "%d, eps=%g, weight=%s, bias=%s" % (self.D, self.eps, self.weight is not None,
+                                                   self.bias is not None)

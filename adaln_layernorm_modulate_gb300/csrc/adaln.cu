@@ -145,10 +145,10 @@ size_t ring_round_bytes(Kind kind, const RowCfg& c, int ring) {
 }
 
 // Ring depth and resident CTAs per SM of one kernel variant (cached per device).
-bool ring_shape(Kind kind, adaln_dtype dtype, bool varlen, int dev, Plan* p) {
+bool ring_shape(Kind kind, adaln_dtype dtype, int form, int dev, Plan* p) {
     const size_t round = p->ring ? ring_round_bytes(kind, p->c, p->ring) : 0;
     const auto key = std::make_tuple(dev, (int)kind, (int)dtype, p->c.nv,
-                                     (int)varlen * 8 + p->ring * 2 + (int)p->full, p->c.tpb);
+                                     form * 8 + p->ring * 2 + (int)p->full, p->c.tpb);
     std::pair<int, int> cached{0, 0};  // (stages, CTAs per SM)
     {
         std::lock_guard<std::mutex> lock(g_mu);
@@ -158,8 +158,8 @@ bool ring_shape(Kind kind, adaln_dtype dtype, bool varlen, int dev, Plan* p) {
     if (cached.second == 0) {
         auto occupancy = [&](size_t smem, int* bps) {
             return kind == kFwd
-                       ? fwd_blocks_per_sm((int)dtype, p->c.nv, varlen, p->ring, p->full, p->c.tpb, smem, bps)
-                       : bwd_blocks_per_sm((int)dtype, p->c.nv, varlen, p->ring != kRingNone, p->full,
+                       ? fwd_blocks_per_sm((int)dtype, p->c.nv, form, p->ring, p->full, p->c.tpb, smem, bps)
+                       : bwd_blocks_per_sm((int)dtype, p->c.nv, form, p->ring != kRingNone, p->full,
                                            p->c.tpb, smem, bps);
         };
         int stages = 0, bps = 0;
@@ -196,7 +196,7 @@ bool ring_shape(Kind kind, adaln_dtype dtype, bool varlen, int dev, Plan* p) {
 // CTAs per row tile, each staging half of every row (eight vectors a thread) in a ring of as
 // many rounds as kRingLimit holds (three at D=16384: 3 x 64 KB), one cluster per resident
 // cluster slot (cached per device).
-bool split_plan(int64_t D, bool varlen, int dev, int64_t R, Plan* p) {
+bool split_plan(int64_t D, int form, int dev, int64_t R, Plan* p) {
     const int64_t VC = D / 4 / 2;  // fp32 vectors of half a row
     const int tpb = (int)(((VC + 7) / 8 + 31) / 32 * 32);
     if (tpb > kSplitThreads) return false;
@@ -209,7 +209,7 @@ bool split_plan(int64_t D, bool varlen, int dev, int64_t R, Plan* p) {
     if (st < 2) return false;
     p->stages = (int)st;
     p->smem = kRingHeader + st * round;
-    const auto key = std::make_tuple(dev, (int)kBwd, (int)ADALN_F32, 8, 32 + (int)varlen * 2 + (int)p->full,
+    const auto key = std::make_tuple(dev, (int)kBwd, (int)ADALN_F32, 8, 32 + form * 2 + (int)p->full,
                                      tpb);
     int clusters = 0;  // resident clusters on the device
     {
@@ -218,7 +218,7 @@ bool split_plan(int64_t D, bool varlen, int dev, int64_t R, Plan* p) {
         if (it != g_plans.end()) clusters = it->second.second;
     }
     if (clusters == 0) {
-        if (bwd_split_clusters(varlen, p->full, tpb, p->smem, &clusters) != cudaSuccess || clusters <= 0)
+        if (bwd_split_clusters(form, p->full, tpb, p->smem, &clusters) != cudaSuccess || clusters <= 0)
             return false;
         std::lock_guard<std::mutex> lock(g_mu);
         g_plans[key] = {p->stages, clusters};
@@ -232,7 +232,7 @@ bool split_plan(int64_t D, bool varlen, int dev, int64_t R, Plan* p) {
 
 // Launch plan: staging mode, ring depth, and row tiles = every resident CTA slot of the
 // device (at most one per row).
-bool make_plan(Kind kind, adaln_dtype dtype, int64_t D, bool varlen, int64_t R, Plan* p) {
+bool make_plan(Kind kind, adaln_dtype dtype, int64_t D, int form, int64_t R, Plan* p) {
     int dev = 0;
     const int sms = current_sms(&dev);
     if (sms <= 0) return false;
@@ -242,17 +242,17 @@ bool make_plan(Kind kind, adaln_dtype dtype, int64_t D, bool varlen, int64_t R, 
     // A ring needs two rounds; rows too wide for two rounds in kRingLimit load into registers,
     // except fp32 backward rows, which take the split form.
     p->ring = 2 * ring_round_bytes(kind, p->c, kRingBulk) + kRingHeader <= kRingLimit ? kRingBulk : kRingNone;
-    if (kind == kBwd && p->ring == kRingNone && dtype == ADALN_F32 && split_plan(D, varlen, dev, R, p))
+    if (kind == kBwd && p->ring == kRingNone && dtype == ADALN_F32 && split_plan(D, form, dev, R, p))
         return true;
     p->full = p->ring && p->c.full;
-    if (!ring_shape(kind, dtype, varlen, dev, p)) return false;
+    if (!ring_shape(kind, dtype, form, dev, p)) return false;
     RowCfg copy;
     if (kind == kFwd && p->ring == kRingBulk && copy_ring_cfg(D, dtype, &copy) && R >= kCopyRingRows * p->G) {
         if (2 * ring_round_bytes(kind, copy, kRingCopy) + kRingHeader <= kRingLimit) {
             p->c = copy;
             p->ring = kRingCopy;
             p->full = copy.full;
-            if (!ring_shape(kind, dtype, varlen, dev, p)) return false;
+            if (!ring_shape(kind, dtype, form, dev, p)) return false;
         }
     }
     // Bulk-ring forwards of more than one warp a CTA launch two tiles per resident CTA slot:
@@ -367,10 +367,10 @@ int read_status_words(const void* ws, cudaStream_t stream) {
 // ---- shared bodies of the dense and packed calls -----------------------------------------
 
 int run_fwd(const void* x, const void* shift, const void* scale, void* y, float* mean,
-            float* rstd, const Segments& seg, int64_t D, float eps, void* ws, bool varlen,
+            float* rstd, const Segments& seg, int64_t D, float eps, void* ws, int form,
             adaln_dtype dtype, cudaStream_t stream) {
     Plan p;
-    if (!make_plan(kFwd, dtype, D, varlen, seg.R, &p)) return ADALN_ERR_CUDA;
+    if (!make_plan(kFwd, dtype, D, form, seg.R, &p)) return ADALN_ERR_CUDA;
     FwdArgs a{};
     a.x = x;
     a.shift = shift;
@@ -385,12 +385,12 @@ int run_fwd(const void* x, const void* shift, const void* scale, void* y, float*
     a.header = static_cast<WsHeader*>(ws);
     a.stages = p.stages;
     return launched(
-        launch_fwd(a, (int)dtype, p.c.nv, varlen, p.ring, p.full, p.G, p.c.tpb, p.smem, stream));
+        launch_fwd(a, (int)dtype, p.c.nv, form, p.ring, p.full, p.G, p.c.tpb, p.smem, stream));
 }
 
-int64_t bwd_tiles(int64_t R, int64_t D, bool varlen, adaln_dtype dtype) {
+int64_t bwd_tiles(int64_t R, int64_t D, int form, adaln_dtype dtype) {
     Plan p;
-    if (!make_plan(kBwd, dtype, D, varlen, R, &p)) return -1;
+    if (!make_plan(kBwd, dtype, D, form, R, &p)) return -1;
     return p.G;
 }
 
@@ -398,11 +398,11 @@ enum Stages { kPartials = 1, kReduce = 2, kBoth = 3 };
 
 int run_bwd(const void* dy, const void* x, const float* mean, const float* rstd,
             const void* scale, void* dx, float* dshift, float* dscale, const Segments& seg,
-            int64_t D, void* ws, size_t ws_bytes, bool varlen, adaln_dtype dtype,
+            int64_t D, void* ws, size_t ws_bytes, int form, adaln_dtype dtype,
             cudaStream_t stream, int stages) {
     if (int rc = check_workspace(ws, ws_bytes, kPartialsOffset)) return rc;
     Plan p;
-    if (!make_plan(kBwd, dtype, D, varlen, seg.R, &p)) return ADALN_ERR_CUDA;
+    if (!make_plan(kBwd, dtype, D, form, seg.R, &p)) return ADALN_ERR_CUDA;
     const int64_t G = p.G;
     const int64_t tiles = p.split ? G / 2 : G;
     if (int rc = check_workspace(ws, ws_bytes, bwd_need(G, seg.nseg, D))) return rc;
@@ -423,7 +423,7 @@ int run_bwd(const void* dy, const void* x, const float* mean, const float* rstd,
     a.header = reinterpret_cast<WsHeader*>(base);
     a.stages = p.stages;
     if (stages & kPartials) {
-        if (int rc = launched(launch_bwd(a, (int)dtype, p.c.nv, varlen, p.ring != kRingNone, p.full, G, p.c.tpb,
+        if (int rc = launched(launch_bwd(a, (int)dtype, p.c.nv, form, p.ring != kRingNone, p.full, G, p.c.tpb,
                                          p.smem, p.split, stream)))
             return rc;
     }
@@ -439,7 +439,7 @@ int run_bwd(const void* dy, const void* x, const float* mean, const float* rstd,
     s.cw = stage2_cw(D, seg.nmod, p.sms);
     s.splits = stage2_splits(per_row);
     s.seg = seg;
-    return launched(launch_stage2(s, (int)dtype, varlen, p.sms, stream));
+    return launched(launch_stage2(s, (int)dtype, form, p.sms, stream));
 }
 
 }  // namespace
@@ -827,3 +827,43 @@ extern "C" int adaln_debug_read(uint32_t* word, int reset) {
     return ADALN_ERR_UNSUPPORTED;
 #endif
 }
+
+// ---- Affine layer norm --------------------------------------------------------------------
+// The same kernels in their affine form: one weight row for all rows, the multiplier itself
+// where AdaLN's is 1 + scale[m] (a bf16 weight - 1 would lose bits of it).
+
+extern "C" {
+
+int adaln_layernorm_fwd(const void* x, const void* weight, const void* bias, void* y, float* mean,
+                        float* rstd, int64_t R, int64_t D, float eps, adaln_dtype dtype,
+                        cudaStream_t stream) {
+    if (int rc = check_shape(D, dtype)) return rc;
+    if (R < 0 || !(eps > 0.0f) || !std::isfinite(eps) || !rows_fit(R, D)) return ADALN_ERR_INVALID_ARG;
+    if (R == 0) return ADALN_OK;
+    if (int rc = check_io({x, y}, {mean, rstd})) return rc;
+    if (!aligned(weight, 16) || !aligned(bias, 16)) return ADALN_ERR_ALIGNMENT;
+    return run_fwd(x, bias, weight, y, mean, rstd, dense_segments(1, R), D, eps, nullptr, kAffine, dtype,
+                   stream);
+}
+
+size_t adaln_layernorm_bwd_workspace_size(int64_t R, int64_t D, adaln_dtype dtype) {
+    if (check_shape(D, dtype) || R < 0) return 0;
+    const int64_t G = bwd_tiles(R, D, kAffine, dtype);
+    return G < 0 ? 0 : bwd_need(G, 1, D);
+}
+
+int adaln_layernorm_bwd(const void* dy, const void* x, const float* mean, const float* rstd,
+                        const void* weight, void* dx, float* dweight, float* dbias, void* workspace,
+                        size_t workspace_bytes, int64_t R, int64_t D, adaln_dtype dtype,
+                        cudaStream_t stream) {
+    if (int rc = check_shape(D, dtype)) return rc;
+    if (R < 0 || !rows_fit(R, D)) return ADALN_ERR_INVALID_ARG;
+    if (!aligned(weight, 16) || !aligned(dweight, 16) || !aligned(dbias, 16)) return ADALN_ERR_ALIGNMENT;
+    if (R > 0) {
+        if (int rc = check_io({dy, x, dx}, {mean, rstd})) return rc;
+    }
+    return run_bwd(dy, x, mean, rstd, weight, dx, dbias, dweight, dense_segments(1, R), D, workspace,
+                   workspace_bytes, kAffine, dtype, stream, dweight || dbias ? kBoth : kPartials);
+}
+
+}  // extern "C"

@@ -28,7 +28,10 @@ namespace adaln {
 // two-CTA clusters, a cluster per row tile; CTA r of a cluster stages and owns half r of
 // every row (a ring of half rows), and the two CTAs add their row sums of g and g*xhat after
 // exchanging them through distributed shared memory (the same bits in both).
-template <typename T, int NV, bool VARLEN, bool RING, bool FULL, bool WIDE = false, bool SPLIT = false>
+// AFFINE: the affine layer norm (dense, one weight row): `scale` is the multiplier of dy itself,
+// null for 1.
+template <typename T, int NV, bool VARLEN, bool RING, bool FULL, bool WIDE = false, bool SPLIT = false,
+          bool AFFINE = false>
 __global__ void __launch_bounds__(SPLIT ? kSplitThreads : WIDE ? kWideThreads : max_threads(NV, Io<T>::VE))
     bwd_kernel(const BwdArgs a) {
     pdl_begin();
@@ -256,12 +259,13 @@ __global__ void __launch_bounds__(SPLIT ? kSplitThreads : WIDE ? kWideThreads : 
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 uint4 vc = make_uint4(0, 0, 0, 0);
-                if (cur_ok && ok[k] && ADALN_IN(kDbgMod, m >= 0 && m < a.seg.nmod && colb[k] + 16 <= row_bytes))
+                if ((!AFFINE || a.scale) && cur_ok && ok[k] &&
+                    ADALN_IN(kDbgMod, m >= 0 && m < a.seg.nmod && colb[k] + 16 <= row_bytes))
                     vc = ld_keep(static_cast<const char*>(a.scale) + m * row_bytes + colb[k]);
                 IO::unpackp(vc, sc1[k]);
-                const f2r one = p_splat(1.0f);
+                const f2r base = p_splat(AFFINE && a.scale ? 0.0f : 1.0f);
 #pragma unroll
-                for (int p = 0; p < PV; ++p) sc1[k][p] = p_add(sc1[k][p], one);
+                for (int p = 0; p < PV; ++p) sc1[k][p] = p_add(sc1[k][p], base);
             }
         }
 
@@ -621,9 +625,10 @@ __global__ void __launch_bounds__(kStage2Threads) stage2v_kernel(const Stage2Arg
                 float4* o1 = reinterpret_cast<float4*>(a.dscale + m * a.D + v * VE);
 #pragma unroll
                 for (int j = 0; j < Q; ++j) {
-                    o0[j] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-                    o1[j] = make_float4(acc[VE + 4 * j], acc[VE + 4 * j + 1], acc[VE + 4 * j + 2],
-                                        acc[VE + 4 * j + 3]);
+                    if (a.dshift) o0[j] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+                    if (a.dscale)
+                        o1[j] = make_float4(acc[VE + 4 * j], acc[VE + 4 * j + 1], acc[VE + 4 * j + 2],
+                                            acc[VE + 4 * j + 3]);
                 }
             }
         } else {
@@ -648,7 +653,7 @@ __global__ void __launch_bounds__(kStage2Threads) stage2v_kernel(const Stage2Arg
                     float t = red[vv * wpv][e];
                     for (int w2 = 1; w2 < wpv; ++w2) t += red[vv * wpv + w2][e];
                     float* out = e < VE ? a.dshift : a.dscale;
-                    out[m * a.D + vg * VE + (e % VE)] = t;
+                    if (out) out[m * a.D + vg * VE + (e % VE)] = t;
                 }
             }
         }
@@ -742,29 +747,33 @@ __global__ void __launch_bounds__(kStage2Threads, 4) stage2_kernel(const Stage2A
             __syncthreads();
         }
         if (k == 0 && cok && ADALN_IN(kDbgGrads, m >= 0 && m < a.seg.nmod && c4 >= 0)) {
-            reinterpret_cast<float4*>(a.dshift)[m * D4 + c4] = red[0][tid];
-            reinterpret_cast<float4*>(a.dscale)[m * D4 + c4] = red[1][tid];
+            if (a.dshift) reinterpret_cast<float4*>(a.dshift)[m * D4 + c4] = red[0][tid];
+            if (a.dscale) reinterpret_cast<float4*>(a.dscale)[m * D4 + c4] = red[1][tid];
         }
         __syncthreads();
     }
 }
 
-template <typename T, int NV, bool VARLEN, bool RING, bool FULL, bool WIDE = false, bool SPLIT = false>
+template <typename T, int NV, bool VARLEN, bool RING, bool FULL, bool WIDE = false, bool SPLIT = false,
+          bool AFFINE = false>
 static const void* bwd_fn() {
-    return reinterpret_cast<const void*>(&bwd_kernel<T, NV, VARLEN, RING, FULL, WIDE, SPLIT>);
+    return reinterpret_cast<const void*>(&bwd_kernel<T, NV, VARLEN, RING, FULL, WIDE, SPLIT, AFFINE>);
 }
 
 // The split form: fp32, eight vectors a thread, a ring of half rows.
-static const void* pick_split(bool varlen, bool full) {
-    if (varlen)
+static const void* pick_split(int form, bool full) {
+    if (form == kAffine)
+        return full ? bwd_fn<float, 8, false, true, true, false, true, true>()
+                    : bwd_fn<float, 8, false, true, false, false, true, true>();
+    if (form == kPacked)
         return full ? bwd_fn<float, 8, true, true, true, false, true>()
                     : bwd_fn<float, 8, true, true, false, false, true>();
     return full ? bwd_fn<float, 8, false, true, true, false, true>()
                 : bwd_fn<float, 8, false, true, false, false, true>();
 }
 
-cudaError_t bwd_split_clusters(bool varlen, bool full, int tpb, size_t smem, int* out) {
-    const void* fn = pick_split(varlen, full);
+cudaError_t bwd_split_clusters(int form, bool full, int tpb, size_t smem, int* out) {
+    const void* fn = pick_split(form, full);
     cudaError_t e = allow_dynamic_smem(fn);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -782,31 +791,39 @@ cudaError_t bwd_split_clusters(bool varlen, bool full, int tpb, size_t smem, int
 }
 
 // Instantiated variants: ring + full row, ring + partial row, plain (partial row).
-template <typename T, int NV, bool VARLEN>
+template <typename T, int NV, bool VARLEN, bool AFFINE>
 static const void* pick_variant(bool ring, bool full) {
-    if (ring) return full ? bwd_fn<T, NV, VARLEN, true, true>() : bwd_fn<T, NV, VARLEN, true, false>();
-    return bwd_fn<T, NV, VARLEN, false, false>();
+    if (ring)
+        return full ? bwd_fn<T, NV, VARLEN, true, true, false, false, AFFINE>()
+                    : bwd_fn<T, NV, VARLEN, true, false, false, false, AFFINE>();
+    return bwd_fn<T, NV, VARLEN, false, false, false, false, AFFINE>();
 }
 
-template <typename T, bool VARLEN>
+template <typename T, bool VARLEN, bool AFFINE = false>
 static const void* pick_nv(int nv, bool ring, bool full) {
     switch (nv) {
-        case 1: return pick_variant<T, 1, VARLEN>(ring, full);
-        case 2: return pick_variant<T, 2, VARLEN>(ring, full);
-        case 3: return pick_variant<T, 3, VARLEN>(ring, full);
-        case 4: return pick_variant<T, 4, VARLEN>(ring, full);
-        case 6: return pick_variant<T, 6, VARLEN>(ring, full);
-        case 8: return pick_variant<T, 8, VARLEN>(ring, full);
+        case 1: return pick_variant<T, 1, VARLEN, AFFINE>(ring, full);
+        case 2: return pick_variant<T, 2, VARLEN, AFFINE>(ring, full);
+        case 3: return pick_variant<T, 3, VARLEN, AFFINE>(ring, full);
+        case 4: return pick_variant<T, 4, VARLEN, AFFINE>(ring, full);
+        case 6: return pick_variant<T, 6, VARLEN, AFFINE>(ring, full);
+        case 8: return pick_variant<T, 8, VARLEN, AFFINE>(ring, full);
         default: return nullptr;
     }
 }
 
-static const void* pick_bwd(int dtype, int nv, bool varlen, bool ring, bool full, int tpb) {
+static const void* pick_bwd(int dtype, int nv, int form, bool ring, bool full, int tpb) {
     if (dtype == 1 && nv == 4 && tpb > max_threads(4, 8)) {  // the wide form: ring, full rows
         if (!ring || !full || tpb > kWideThreads) return nullptr;
-        return varlen ? bwd_fn<__nv_bfloat16, 4, true, true, true, true>()
-                      : bwd_fn<__nv_bfloat16, 4, false, true, true, true>();
+        if (form == kAffine) return bwd_fn<__nv_bfloat16, 4, false, true, true, true, false, true>();
+        return form == kPacked ? bwd_fn<__nv_bfloat16, 4, true, true, true, true>()
+                               : bwd_fn<__nv_bfloat16, 4, false, true, true, true>();
     }
+    if (form == kAffine)
+        return dtype == 0   ? pick_nv<float, false, true>(nv, ring, full)
+               : dtype == 1 ? pick_nv<__nv_bfloat16, false, true>(nv, ring, full)
+                            : nullptr;
+    const bool varlen = form == kPacked;
     if (dtype == 0) return varlen ? pick_nv<float, true>(nv, ring, full) : pick_nv<float, false>(nv, ring, full);
     if (dtype == 1)
         return varlen ? pick_nv<__nv_bfloat16, true>(nv, ring, full)
@@ -814,20 +831,20 @@ static const void* pick_bwd(int dtype, int nv, bool varlen, bool ring, bool full
     return nullptr;
 }
 
-cudaError_t bwd_blocks_per_sm(int dtype, int nv, bool varlen, bool ring, bool full, int tpb,
+cudaError_t bwd_blocks_per_sm(int dtype, int nv, int form, bool ring, bool full, int tpb,
                               size_t smem, int* out) {
-    const void* fn = pick_bwd(dtype, nv, varlen, ring, full, tpb);
+    const void* fn = pick_bwd(dtype, nv, form, ring, full, tpb);
     if (!fn) return cudaErrorInvalidValue;
     cudaError_t e = allow_dynamic_smem(fn);
     if (e != cudaSuccess) return e;
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, fn, tpb, smem);
 }
 
-cudaError_t launch_bwd(const BwdArgs& args, int dtype, int nv, bool varlen, bool ring, bool full,
+cudaError_t launch_bwd(const BwdArgs& args, int dtype, int nv, int form, bool ring, bool full,
                        int64_t G, int tpb, size_t smem, bool split, cudaStream_t stream) {
     if (split && (dtype != 0 || nv != 8 || !ring || G % 2 != 0 || tpb > kSplitThreads))
         return cudaErrorInvalidValue;
-    const void* fn = split ? pick_split(varlen, full) : pick_bwd(dtype, nv, varlen, ring, full, tpb);
+    const void* fn = split ? pick_split(form, full) : pick_bwd(dtype, nv, form, ring, full, tpb);
     if (!fn) return cudaErrorInvalidValue;
     BwdArgs a = args;
     void* params[] = {&a};
@@ -836,7 +853,8 @@ cudaError_t launch_bwd(const BwdArgs& args, int dtype, int nv, bool varlen, bool
 
 cudaError_t debug_word_bwd(uint32_t* out, bool reset) { return debug_word(out, reset); }
 
-cudaError_t launch_stage2(const Stage2Args& args, int dtype, bool varlen, int sms, cudaStream_t stream) {
+cudaError_t launch_stage2(const Stage2Args& args, int dtype, int form, int sms, cudaStream_t stream) {
+    const bool varlen = form == kPacked;
     dim3 grid;
     const void* fn;
     const unsigned gy = (unsigned)(args.seg.nmod < 65535 ? args.seg.nmod : 65535);

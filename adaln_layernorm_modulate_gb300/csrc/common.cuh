@@ -11,6 +11,9 @@ namespace adaln {
 constexpr int kMaxCtas = 4096;      // upper bound on the row-tile count of one launch
 constexpr int kStage2Threads = 256;
 constexpr int kMaxStages = 8;       // deepest shared-memory ring, in rounds
+// Which rows an operator call covers and with what: a dense batch, packed segments (a bool
+// `varlen` converts), or the affine layer norm (dense rows, one weight row for all).
+enum Form : int { kDense = 0, kPacked = 1, kAffine = 2 };
 enum : int { kRingNone = 0, kRingBulk = 1, kRingCopy = 2 };  // forward staging modes
 
 // Largest CTA the host may pick for NV vectors a thread of VE-element vectors. It is the
@@ -156,7 +159,7 @@ struct BwdArgs {
 
 struct Stage2Args {
     const float* partials;  // the backward's, in the layout vec_major names
-    float* dshift;
+    float* dshift;       // either may be null: not wanted
     float* dscale;
     int64_t D;
     int64_t G;           // row tiles of the backward launch

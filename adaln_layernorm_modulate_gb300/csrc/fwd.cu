@@ -31,7 +31,11 @@
 
 namespace adaln {
 
-template <typename T, int NV, bool VARLEN, int RING, bool FULL>
+// AFFINE: the affine layer norm (dense, one modulation row for all rows): `scale` is the
+// multiplier itself (null: 1), a null shift is 0, and the stored mean takes a correction, the
+// mean of the row's residuals x - mean: K + mean(x - K) alone is off by a rounding of K =
+// x[row, 0], many roundings of a mean much smaller than K.
+template <typename T, int NV, bool VARLEN, int RING, bool FULL, bool AFFINE = false>
 __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const FwdArgs a) {
     pdl_begin();
     constexpr bool BULK = RING == kRingBulk, COPY = RING == kRingCopy;
@@ -42,6 +46,7 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
     extern __shared__ uint4 ring[];
     __shared__ __align__(16) float red1[RB][32];
     __shared__ __align__(16) float red2[RB][32];
+    __shared__ __align__(16) float red3[AFFINE ? RB : 1][32];  // AFFINE: sums of the residuals
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int TPB = blockDim.x;
@@ -73,6 +78,7 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
 
     zero_absent_warps<RB>(red1, nwarps);
     zero_absent_warps<RB>(red2, nwarps);
+    if constexpr (AFFINE) zero_absent_warps<RB>(red3, nwarps);
     uint32_t err = validate_segments<VARLEN>(a.seg, b, G);
     if constexpr (BULK) {
         if (tid == 0) {
@@ -205,14 +211,16 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
             for (int k = 0; k < NV; ++k) {
                 uint4 vs = make_uint4(0, 0, 0, 0), vc = make_uint4(0, 0, 0, 0);
                 if (cur_ok && ok[k] && ADALN_IN(kDbgMod, m >= 0 && m < a.seg.nmod && colb[k] + 16 <= row_bytes)) {
-                    vs = ld_keep(static_cast<const char*>(a.shift) + m * row_bytes + colb[k]);
-                    vc = ld_keep(static_cast<const char*>(a.scale) + m * row_bytes + colb[k]);
+                    if (!AFFINE || a.shift)
+                        vs = ld_keep(static_cast<const char*>(a.shift) + m * row_bytes + colb[k]);
+                    if (!AFFINE || a.scale)
+                        vc = ld_keep(static_cast<const char*>(a.scale) + m * row_bytes + colb[k]);
                 }
                 IO::unpackp(vs, sh[k]);
                 IO::unpackp(vc, sc1[k]);
-                const f2r one = p_splat(1.0f);
+                const f2r base = p_splat(AFFINE && a.scale ? 0.0f : 1.0f);
 #pragma unroll
-                for (int p = 0; p < PV; ++p) sc1[k][p] = p_add(sc1[k][p], one);
+                for (int p = 0; p < PV; ++p) sc1[k][p] = p_add(sc1[k][p], base);
             }
         }
 
@@ -249,7 +257,7 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
             float s2[RB], md[RB];
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
-                md[i] = s1[i] * invD;
+                md[i] = AFFINE ? __fmul_rn(s1[i], invD) : s1[i] * invD;
                 const f2r pm = p_splat(md[i]);
                 f2r acc0 = kPairZero, acc1 = kPairZero;
 #pragma unroll
@@ -269,8 +277,28 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
 #pragma unroll
                 for (int i = 0; i < RB; ++i) red2[i][warp] = s2[i];
             }
+            float s3[RB];
+#pragma unroll
+            for (int i = 0; i < RB; ++i) s3[i] = 0.0f;
+            if constexpr (AFFINE) {
+#pragma unroll
+                for (int i = 0; i < RB; ++i) {
+                    f2r acc = kPairZero;
+#pragma unroll
+                    for (int k = 0; k < NV; ++k)
+#pragma unroll
+                        for (int p = 0; p < PV; ++p) acc = p_add(acc, d[i][k][p]);
+                    s3[i] = p_hsum(acc);
+                }
+                warp_sum(s3);
+                if (lane == 0) {
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) red3[i][warp] = s3[i];
+                }
+            }
             __syncthreads();
             cta_sum(red2, ng, lane, s2);
+            if constexpr (AFFINE) cta_sum(red3, ng, lane, s3);
             // Pass 3: y = (d - mean_d) * rstd * (1 + scale) + shift.
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
@@ -287,7 +315,10 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
                     if (ADALN_IN_ROW(row + i, R, colb[k], 16, row_bytes)) st_vec(yr + colb[k], IO::packp(o));
                 }
                 if (tid == 0 && ADALN_IN(kDbgStats, row + i >= 0 && row + i < R)) {
-                    a.mean[row + i] = K[i] + md[i];
+                    if constexpr (AFFINE)  // the sum with md as rounded above, which the residuals used
+                        a.mean[row + i] = __fadd_rn(K[i], md[i]) + s3[i] * invD;
+                    else
+                        a.mean[row + i] = K[i] + md[i];
                     a.rstd[row + i] = rs;
                 }
             }
@@ -322,40 +353,45 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
     publish_status(err, a.status, a.header);
 }
 
-template <typename T, int NV, bool VARLEN, int RING, bool FULL>
+template <typename T, int NV, bool VARLEN, int RING, bool FULL, bool AFFINE>
 static const void* fwd_fn() {
-    return reinterpret_cast<const void*>(&fwd_kernel<T, NV, VARLEN, RING, FULL>);
+    return reinterpret_cast<const void*>(&fwd_kernel<T, NV, VARLEN, RING, FULL, AFFINE>);
 }
 
 // Instantiated variants: the bulk ring with a full or a partial row; the copy ring only with
 // the one mapping the host plans it with (bf16, three vectors a thread, full rows); plain
 // loads (partial row).
-template <typename T, int NV, bool VARLEN>
+template <typename T, int NV, bool VARLEN, bool AFFINE>
 static const void* pick_variant(int ring, bool full) {
     if (ring == kRingBulk)
-        return full ? fwd_fn<T, NV, VARLEN, kRingBulk, true>() : fwd_fn<T, NV, VARLEN, kRingBulk, false>();
+        return full ? fwd_fn<T, NV, VARLEN, kRingBulk, true, AFFINE>() : fwd_fn<T, NV, VARLEN, kRingBulk, false, AFFINE>();
     if (ring == kRingCopy) {
         if constexpr (NV == 3 && std::is_same<T, __nv_bfloat16>::value)
-            if (full) return fwd_fn<T, NV, VARLEN, kRingCopy, true>();
+            if (full) return fwd_fn<T, NV, VARLEN, kRingCopy, true, AFFINE>();
         return nullptr;
     }
-    return fwd_fn<T, NV, VARLEN, kRingNone, false>();
+    return fwd_fn<T, NV, VARLEN, kRingNone, false, AFFINE>();
 }
 
-template <typename T, bool VARLEN>
+template <typename T, bool VARLEN, bool AFFINE = false>
 static const void* pick_nv(int nv, int ring, bool full) {
     switch (nv) {
-        case 1: return pick_variant<T, 1, VARLEN>(ring, full);
-        case 2: return pick_variant<T, 2, VARLEN>(ring, full);
-        case 3: return pick_variant<T, 3, VARLEN>(ring, full);
-        case 4: return pick_variant<T, 4, VARLEN>(ring, full);
-        case 6: return pick_variant<T, 6, VARLEN>(ring, full);
-        case 8: return pick_variant<T, 8, VARLEN>(ring, full);
+        case 1: return pick_variant<T, 1, VARLEN, AFFINE>(ring, full);
+        case 2: return pick_variant<T, 2, VARLEN, AFFINE>(ring, full);
+        case 3: return pick_variant<T, 3, VARLEN, AFFINE>(ring, full);
+        case 4: return pick_variant<T, 4, VARLEN, AFFINE>(ring, full);
+        case 6: return pick_variant<T, 6, VARLEN, AFFINE>(ring, full);
+        case 8: return pick_variant<T, 8, VARLEN, AFFINE>(ring, full);
         default: return nullptr;
     }
 }
 
-static const void* pick_fwd(int dtype, int nv, bool varlen, int ring, bool full) {
+static const void* pick_fwd(int dtype, int nv, int form, int ring, bool full) {
+    if (form == kAffine)
+        return dtype == 0   ? pick_nv<float, false, true>(nv, ring, full)
+               : dtype == 1 ? pick_nv<__nv_bfloat16, false, true>(nv, ring, full)
+                            : nullptr;
+    const bool varlen = form == kPacked;
     if (dtype == 0) return varlen ? pick_nv<float, true>(nv, ring, full) : pick_nv<float, false>(nv, ring, full);
     if (dtype == 1)
         return varlen ? pick_nv<__nv_bfloat16, true>(nv, ring, full)
@@ -363,18 +399,18 @@ static const void* pick_fwd(int dtype, int nv, bool varlen, int ring, bool full)
     return nullptr;
 }
 
-cudaError_t fwd_blocks_per_sm(int dtype, int nv, bool varlen, int ring, bool full, int tpb,
+cudaError_t fwd_blocks_per_sm(int dtype, int nv, int form, int ring, bool full, int tpb,
                               size_t smem, int* out) {
-    const void* fn = pick_fwd(dtype, nv, varlen, ring, full);
+    const void* fn = pick_fwd(dtype, nv, form, ring, full);
     if (!fn) return cudaErrorInvalidValue;
     cudaError_t e = allow_dynamic_smem(fn);
     if (e != cudaSuccess) return e;
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, fn, tpb, smem);
 }
 
-cudaError_t launch_fwd(const FwdArgs& args, int dtype, int nv, bool varlen, int ring, bool full,
+cudaError_t launch_fwd(const FwdArgs& args, int dtype, int nv, int form, int ring, bool full,
                        int64_t G, int tpb, size_t smem, cudaStream_t stream) {
-    const void* fn = pick_fwd(dtype, nv, varlen, ring, full);
+    const void* fn = pick_fwd(dtype, nv, form, ring, full);
     if (!fn) return cudaErrorInvalidValue;
     FwdArgs a = args;
     void* params[] = {&a};

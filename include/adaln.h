@@ -227,6 +227,25 @@ int adaln_bwd_noalloc(const void* dy, const void* x, const float* mean, const fl
  * nothing on the device. Like adaln_bwd_noalloc, this call has no counterpart in the paper. */
 int adaln_noalloc_read_status(cudaStream_t stream);
 
+/* ---- Affine layer norm ------------------------------------------------------------------
+ * The network's norms with a learned weight and bias [D] (in `dtype`) in place of a
+ * conditioned modulation row, e.g. the final norm before a vocabulary head:
+ *     y  = xhat * weight + bias                     (null weight: 1, null bias: 0)
+ *     dx = rstd * (g - mean_d(g) - xhat * mean_d(g * xhat)),  g = dy * weight
+ *     dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy    (fp32, overwritten)
+ * x, y, dy, dx [R, D]; mean, rstd [R] as in adaln_fwd. dweight and dbias may each be null (not
+ * wanted; with both null the reduction is not launched). R = 0 is valid: the forward does
+ * nothing, the backward writes zero dweight and dbias. Checks, reduction order, launches and
+ * status as adaln_fwd / adaln_bwd. */
+int adaln_layernorm_fwd(const void* x, const void* weight, const void* bias, void* y, float* mean,
+                        float* rstd, int64_t R, int64_t D, float eps, adaln_dtype dtype,
+                        cudaStream_t stream);
+size_t adaln_layernorm_bwd_workspace_size(int64_t R, int64_t D, adaln_dtype dtype);
+int adaln_layernorm_bwd(const void* dy, const void* x, const float* mean, const float* rstd,
+                        const void* weight, void* dx, float* dweight, float* dbias, void* workspace,
+                        size_t workspace_bytes, int64_t R, int64_t D, adaln_dtype dtype,
+                        cudaStream_t stream);
+
 /* ---- Row sharding across ranks ----------------------------------------------------------
  * A batch can be split into contiguous, segment-aligned row shards, one per rank (the pages
  * train on 8- and 16-GPU clusters, AdaptiveLoad technical summary sections 2.A and 4). The
