@@ -26,6 +26,7 @@ STATUS = {
     0: "ADALN_OK", 1: "ADALN_ERR_INVALID_ARG", 2: "ADALN_ERR_UNSUPPORTED",
     3: "ADALN_ERR_ALIGNMENT", 4: "ADALN_ERR_WORKSPACE", 5: "ADALN_ERR_CUDA",
     6: "ADALN_ERR_BAD_SEQLENS", 7: "ADALN_ERR_BAD_MOD_IDX", 8: "ADALN_ERR_TIMEOUT",
+    9: "ADALN_ERR_BAD_TARGET",
 }
 EXPORTS = (
     "adaln_fwd", "adaln_bwd_workspace_size", "adaln_bwd", "adaln_bwd_partials", "adaln_bwd_reduce",
@@ -34,6 +35,8 @@ EXPORTS = (
     "adaln_read_status", "adaln_bwd_recompute_workspace_size", "adaln_bwd_recompute",
     "adaln_bwd_varlen_recompute_workspace_size", "adaln_bwd_varlen_recompute", "adaln_bwd_noalloc", "adaln_noalloc_read_status", "adaln_sum_ranks", "adaln_debug_read",
     "adaln_layernorm_fwd", "adaln_layernorm_bwd_workspace_size", "adaln_layernorm_bwd",
+    "adaln_linear_xent_fwd_workspace_size", "adaln_linear_xent_fwd",
+    "adaln_linear_xent_bwd_workspace_size", "adaln_linear_xent_bwd",
     "adaln_bucket_batch", "adaln_bucket_batch_real",
     "adaln_fit_step_cost", "adaln_bucket_load_cv", "adaln_status_string",
 )
@@ -81,6 +84,10 @@ def _load() -> ctypes.CDLL:
         "adaln_layernorm_fwd": ([vp, vp, vp, vp, vp, vp, i64, i64, f32, ci, vp], ci),
         "adaln_layernorm_bwd_workspace_size": ([i64, i64, ci], sz),
         "adaln_layernorm_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i64, i64, ci, vp], ci),
+        "adaln_linear_xent_fwd_workspace_size": ([i64, i64, i64, ci], sz),
+        "adaln_linear_xent_fwd": ([vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, sz, ci, vp], ci),
+        "adaln_linear_xent_bwd_workspace_size": ([i64, i64, i64, ci], sz),
+        "adaln_linear_xent_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, sz, ci, vp], ci),
         "adaln_sum_ranks": ([vp, vp, i32, i64, vp], ci),
         "adaln_debug_read": ([vp, ci], ci),
         "adaln_bucket_batch": ([i64, i64, i64, i32], i64),
@@ -279,13 +286,35 @@ def adaln_layernorm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, workspace
         _ptr(workspace), workspace_bytes, R, D, _dtype(dtype, dy), _stream(stream)))
 
 
+def adaln_linear_xent_fwd_workspace_size(N, V, D, dtype) -> int:
+    return int(lib().adaln_linear_xent_fwd_workspace_size(N, V, D, int(dtype)))
+
+
+def adaln_linear_xent_fwd(x, weight, target, loss, lse, N, V, D, ignore_index, workspace, workspace_bytes,
+                          dtype=None, stream=None):
+    _check("adaln_linear_xent_fwd", lib().adaln_linear_xent_fwd(
+        _ptr(x), _ptr(weight), _ptr(target), _ptr(loss), _ptr(lse), N, V, D, ignore_index, _ptr(workspace),
+        workspace_bytes, _dtype(dtype, x), _stream(stream)))
+
+
+def adaln_linear_xent_bwd_workspace_size(N, V, D, dtype) -> int:
+    return int(lib().adaln_linear_xent_bwd_workspace_size(N, V, D, int(dtype)))
+
+
+def adaln_linear_xent_bwd(x, weight, target, lse, dloss, dlse, dx, dweight, N, V, D, ignore_index, workspace,
+                          workspace_bytes, dtype=None, stream=None):
+    _check("adaln_linear_xent_bwd", lib().adaln_linear_xent_bwd(
+        _ptr(x), _ptr(weight), _ptr(target), _ptr(lse), _ptr(dloss), _ptr(dlse), _ptr(dx), _ptr(dweight),
+        N, V, D, ignore_index, _ptr(workspace), workspace_bytes, _dtype(dtype, x), _stream(stream)))
+
+
 def adaln_sum_ranks(parts, out, world, n, stream=None):
     """out[i] = parts[0][i] + ... + parts[world - 1][i], added in rank order (device fp32)."""
     _check("adaln_sum_ranks", lib().adaln_sum_ranks(_ptr(parts), _ptr(out), world, n, _stream(stream)))
 
 
 DEBUG_CLASSES = {1: "rows", 2: "stats", 4: "mod", 8: "partials", 16: "segments", 32: "shared",
-                 64: "grads", 128: "ranks", 256: "status"}  # ADALN_DEBUG_* bits
+                 64: "grads", 128: "ranks", 256: "status", 512: "loss"}  # ADALN_DEBUG_* bits
 
 
 def adaln_debug_read(reset=False) -> int:

@@ -28,10 +28,11 @@ from . import (ADALN_BF16, ADALN_F32, AdalnError, adaln_bwd, adaln_bwd_recompute
                adaln_bwd_varlen_recompute_workspace_size, adaln_bwd_varlen_workspace_size,
                adaln_bwd_workspace_size, adaln_fwd, adaln_fwd_varlen, adaln_fwd_varlen_workspace_size,
                adaln_layernorm_bwd, adaln_layernorm_bwd_workspace_size, adaln_layernorm_fwd,
-               adaln_read_status)
+               adaln_linear_xent_bwd, adaln_linear_xent_bwd_workspace_size, adaln_linear_xent_fwd,
+               adaln_linear_xent_fwd_workspace_size, adaln_read_status)
 
 __all__ = ["AdaLNModulateFunction", "AdaLNModulate", "adaln_modulate", "LayerNormFunction", "LayerNorm",
-           "layer_norm"]
+           "layer_norm", "LinearCrossEntropyFunction", "linear_cross_entropy"]
 
 
 def _code(t: torch.Tensor) -> int:
@@ -240,3 +241,74 @@ class LayerNorm(torch.nn.Module):
     def extra_repr(self) -> str:
         return "%d, eps=%g, weight=%s, bias=%s" % (self.D, self.eps, self.weight is not None,
                                                    self.bias is not None)
+
+
+class LinearCrossEntropyFunction(torch.autograd.Function):
+    """(loss, lse) of each row of x [..., D] under the vocabulary head weight [V, D]:
+    loss = lse - z_target, lse = log sum exp z, z = x weight^T, both fp32 and differentiable.
+    Rows with target == ignore_index have loss and lse 0. Saves x, weight, target and lse, no
+    logits. ``check_targets`` reads the call's device status (it synchronises the stream)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, target, ignore_index: int = -100, check_targets: bool = False):
+        if not x.is_cuda:
+            raise ValueError("linear_cross_entropy runs on CUDA tensors")
+        if x.dim() < 1 or weight.dim() != 2 or weight.shape[1] != x.shape[-1]:
+            raise ValueError("linear_cross_entropy: x [..., D] and weight [V, D]")
+        if target.shape != x.shape[:-1] or target.dtype != torch.int64:
+            raise ValueError("linear_cross_entropy: target [...] of int64, one per row of x")
+        if weight.device != x.device or target.device != x.device:
+            raise ValueError("x, weight and target must be on one device")
+        if x.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+            raise TypeError("linear_cross_entropy takes bfloat16 x and weight, got %s and %s"
+                            % (x.dtype, weight.dtype))
+        x, weight, target = x.contiguous(), weight.contiguous(), target.contiguous()
+        V, D = weight.shape
+        N = target.numel()
+        loss = torch.empty(target.shape, dtype=torch.float32, device=x.device)
+        lse = torch.empty(target.shape, dtype=torch.float32, device=x.device)
+        nb = adaln_linear_xent_fwd_workspace_size(N, V, D, ADALN_BF16)
+        ws = _workspace(nb, x.device)
+        adaln_linear_xent_fwd(x, weight, target, loss, lse, N, V, D, ignore_index, ws, nb, ADALN_BF16)
+        if check_targets:
+            _check_status(ws, "adaln_linear_xent_fwd")
+        ctx.save_for_backward(x, weight, target, lse)
+        ctx.ignore_index = ignore_index
+        ctx.set_materialize_grads(False)
+        return loss, lse
+
+    @staticmethod
+    def backward(ctx, dloss, dlse):
+        x, weight, target, lse = ctx.saved_tensors
+        want_x, want_w = ctx.needs_input_grad[:2]
+        if dloss is None and dlse is None:
+            return None, None, None, None, None
+        V, D = weight.shape
+        N = target.numel()
+        dloss = torch.zeros_like(lse) if dloss is None else dloss.contiguous()
+        dlse = None if dlse is None else dlse.contiguous()
+        dx = torch.empty_like(x) if want_x else None
+        dweight = torch.empty_like(weight) if want_w else None
+        nb = adaln_linear_xent_bwd_workspace_size(N, V, D, ADALN_BF16)
+        ws = _workspace(nb, x.device)
+        adaln_linear_xent_bwd(x, weight, target, lse, dloss, dlse, dx, dweight, N, V, D, ctx.ignore_index, ws,
+                              nb, ADALN_BF16)
+        return dx, dweight, None, None, None
+
+
+def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor,
+                         ignore_index: int = -100, reduction: str = "mean", z_loss: float = 0.0,
+                         check_targets: bool = False) -> torch.Tensor:
+    """Softmax cross entropy of the vocabulary head ``x @ weight.T`` without its logits.
+
+    reduction: "none" (a loss per row), "sum", or "mean" over the rows whose target is not
+    ignore_index (0 if there is none). z_loss adds z_loss * lse^2 to each such row's loss."""
+    if reduction not in ("none", "sum", "mean"):
+        raise ValueError("reduction must be none, sum or mean, got %r" % (reduction,))
+    loss, lse = LinearCrossEntropyFunction.apply(x, weight, target, ignore_index, check_targets)
+    if z_loss:
+        loss = loss + z_loss * lse * lse
+    if reduction == "none":
+        return loss
+    total = loss.sum()
+    return total if reduction == "sum" else total / (target != ignore_index).sum().clamp(min=1)

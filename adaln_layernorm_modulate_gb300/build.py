@@ -18,7 +18,7 @@ BUILD = os.path.join(ROOT, "_build", "adaln")
 LIB = os.path.join(PKG, "libadaln.so")
 DEBUG_BUILD = os.path.join(ROOT, "_build", "adaln_debug")
 DEBUG_LIB = os.path.join(PKG, "libadaln_debug.so")
-SOURCES = ["adaln.cu", "fwd.cu", "bwd.cu", "schedule.cu"]
+SOURCES = ["adaln.cu", "fwd.cu", "bwd.cu", "xent.cu", "schedule.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "launch.h"
+#include "xent.h"
 
 using namespace adaln;
 
@@ -360,6 +361,7 @@ int read_status_words(const void* ws, cudaStream_t stream) {
     for (uint32_t w : words) all |= w;
     if (all & kErrSeqlens) return ADALN_ERR_BAD_SEQLENS;
     if (all & kErrModIdx) return ADALN_ERR_BAD_MOD_IDX;
+    if (all & kErrTarget) return ADALN_ERR_BAD_TARGET;
     if (all & kErrTimeout) return ADALN_ERR_TIMEOUT;
     return ADALN_OK;
 }
@@ -626,13 +628,14 @@ const char* adaln_status_string(int status) {
     switch (status) {
         case ADALN_OK: return "ADALN_OK";
         case ADALN_ERR_INVALID_ARG: return "ADALN_ERR_INVALID_ARG: invalid argument";
-        case ADALN_ERR_UNSUPPORTED: return "ADALN_ERR_UNSUPPORTED: D must be a multiple of 8 in [8, 16384]";
+        case ADALN_ERR_UNSUPPORTED: return "ADALN_ERR_UNSUPPORTED: D must be a multiple of 8 in [8, 16384], and the dtype one the call takes";
         case ADALN_ERR_ALIGNMENT: return "ADALN_ERR_ALIGNMENT: misaligned pointer";
         case ADALN_ERR_WORKSPACE: return "ADALN_ERR_WORKSPACE: workspace missing, too small or without status";
         case ADALN_ERR_CUDA: return "ADALN_ERR_CUDA: CUDA runtime error";
         case ADALN_ERR_BAD_SEQLENS: return "ADALN_ERR_BAD_SEQLENS: malformed cu_seqlens";
         case ADALN_ERR_BAD_MOD_IDX: return "ADALN_ERR_BAD_MOD_IDX: mod_idx out of range";
         case ADALN_ERR_TIMEOUT: return "ADALN_ERR_TIMEOUT: a kernel timed out waiting for its input copies";
+        case ADALN_ERR_BAD_TARGET: return "ADALN_ERR_BAD_TARGET: target neither in the vocabulary nor ignore_index";
         default: return "unknown adaln status";
     }
 }
@@ -816,10 +819,11 @@ extern "C" int adaln_debug_read(uint32_t* word, int reset) {
 #ifdef ADALN_DEBUG
     if (word == nullptr) return ADALN_ERR_INVALID_ARG;
     if (cudaDeviceSynchronize() != cudaSuccess) return ADALN_ERR_CUDA;
-    uint32_t f = 0, b = 0;
-    if (debug_word_fwd(&f, reset != 0) != cudaSuccess || debug_word_bwd(&b, reset != 0) != cudaSuccess)
+    uint32_t f = 0, b = 0, x = 0;
+    if (debug_word_fwd(&f, reset != 0) != cudaSuccess || debug_word_bwd(&b, reset != 0) != cudaSuccess ||
+        debug_word_xent(&x, reset != 0) != cudaSuccess)
         return ADALN_ERR_CUDA;
-    *word = f | b;
+    *word = f | b | x;
     return ADALN_OK;
 #else
     (void)word;
@@ -864,6 +868,224 @@ int adaln_layernorm_bwd(const void* dy, const void* x, const float* mean, const 
     }
     return run_bwd(dy, x, mean, rstd, weight, dx, dbias, dweight, dense_segments(1, R), D, workspace,
                    workspace_bytes, kAffine, dtype, stream, dweight || dbias ? kBoth : kPartials);
+}
+
+}  // extern "C"
+
+// ---- Softmax cross entropy over a vocabulary ----------------------------------------------
+
+namespace {
+
+// Pieces of the vocabulary in the backward: dz of one piece is at most this large unless a
+// piece would be narrower than kMinPiece columns. 128 MiB is about the L2, so that most of a
+// piece is read back from there; narrower pieces read and write the fp32 dx once more each.
+constexpr int64_t kProbsBytes = (int64_t)128 << 20;
+constexpr int64_t kMinPiece = 2048;
+constexpr int64_t kXentSms = 152;  // the SM count the split of dx's sums is made for
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+struct XentPlan {
+    int64_t Np;          // rows of the packed buffers: whole row tiles, at least one
+    int64_t tiles;       // forward: column tiles
+    int64_t piece;       // backward: columns of a piece (a multiple of kTileN)
+    int splits;          // backward: parts of dx's sum over a piece
+    size_t nact, row, tgt, f0, f1, f2, xp, big, dxacc, bytes;  // workspace offsets
+};
+
+// Workspace: [header | status words | nact | row | tgt | three row arrays | packed x |
+// partials (forward) or dz (backward) | dx in fp32 (backward)].
+XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
+    XentPlan p{};
+    p.Np = std::max<int64_t>(round_up(N, kTileM), kTileM);
+    p.tiles = (V + kTileN - 1) / kTileN;
+    const int64_t wide = std::max<int64_t>(kProbsBytes / 2 / p.Np / kTileN * kTileN, kMinPiece);
+    const int64_t pieces = (V + wide - 1) / wide;
+    p.piece = round_up((V + pieces - 1) / pieces, kTileN);
+    // dx sums over a piece's columns, dweight over the rows: with few rows the dx tiles are few
+    // and long. They are split until one is no longer than an SM's share of all the K steps (at
+    // least 16 of them, below which filling the pipeline costs more).
+    const int64_t dt = (D + kTileN - 1) / kTileN, mt = p.Np / kTileM, kv = p.piece / kTileK;
+    const int64_t steps = mt * dt * kv + p.piece / kTileM * dt * (p.Np / kTileK);
+    const int64_t share = std::max<int64_t>(steps / kXentSms, 16);
+    p.splits = (int)std::min<int64_t>(std::max<int64_t>((kv + share - 1) / share, 1), 16);
+    size_t at = kPartialsOffset;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at = (at + bytes + 255) / 256 * 256;
+        return o;
+    };
+    const size_t rows = (size_t)p.Np;
+    p.nact = take(sizeof(int32_t));
+    p.row = take(rows * 4);
+    p.tgt = take(rows * 4);
+    p.f0 = take(rows * 4);
+    p.f1 = take(rows * 4);
+    p.f2 = take(rows * 4);
+    p.xp = take(rows * (size_t)D * 2);
+    p.big = take(bwd ? rows * (size_t)p.piece * 2 : rows * (size_t)p.tiles * 2 * sizeof(float2));
+    if (bwd) p.dxacc = take(rows * (size_t)p.splits * (size_t)D * 4);
+    p.bytes = at;
+    return p;
+}
+
+int xent_check(int64_t N, int64_t V, int64_t D, adaln_dtype dtype) {
+    if (int rc = check_shape(D, dtype)) return rc;
+    if (dtype != ADALN_BF16) return ADALN_ERR_UNSUPPORTED;
+    if (N < 0 || N > INT32_MAX - kTileM || V < 1 || V > INT32_MAX - kTileN) return ADALN_ERR_INVALID_ARG;
+    return ADALN_OK;
+}
+
+template <typename T>
+T* at(void* ws, size_t offset) {
+    return reinterpret_cast<T*>(static_cast<char*>(ws) + offset);
+}
+
+int pack_ctas(int64_t N) { return (int)std::min<int64_t>(std::max<int64_t>((N + 7) / 8, 1), kPackCtas); }
+
+PackArgs xent_pack(const XentPlan& p, void* ws, const void* x, const int64_t* target, int64_t N, int64_t V,
+                   int64_t D, int64_t ignore) {
+    PackArgs a{};
+    a.x = x;
+    a.target = target;
+    a.xp = at<void>(ws, p.xp);
+    a.row = at<int32_t>(ws, p.row);
+    a.tgt = at<int32_t>(ws, p.tgt);
+    a.nact = at<int32_t>(ws, p.nact);
+    a.status = at<uint32_t>(ws, kHeaderBytes);
+    a.header = at<WsHeader>(ws, 0);
+    a.N = N;
+    a.Np = p.Np;
+    a.D = D;
+    a.V = V;
+    a.ignore = ignore;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t adaln_linear_xent_fwd_workspace_size(int64_t N, int64_t V, int64_t D, adaln_dtype dtype) {
+    return xent_check(N, V, D, dtype) ? 0 : xent_plan(N, V, D, false).bytes;
+}
+
+int adaln_linear_xent_fwd(const void* x, const void* weight, const int64_t* target, float* loss, float* lse,
+                          int64_t N, int64_t V, int64_t D, int64_t ignore_index, void* workspace,
+                          size_t workspace_bytes, adaln_dtype dtype, cudaStream_t stream) {
+    if (int rc = xent_check(N, V, D, dtype)) return rc;
+    if (int rc = check_io({weight}, {})) return rc;
+    if (N > 0) {
+        if (int rc = check_io({x}, {loss, lse})) return rc;
+        if (!target) return ADALN_ERR_INVALID_ARG;
+        if (!aligned(target, 8)) return ADALN_ERR_ALIGNMENT;
+    }
+    const XentPlan p = xent_plan(N, V, D, false);
+    if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
+    int dev = 0;
+    const int sms = current_sms(&dev);
+    if (sms <= 0) return ADALN_ERR_CUDA;
+    PackArgs k = xent_pack(p, workspace, x, target, N, V, D, ignore_index);
+    k.loss_out = loss;
+    k.lse_out = lse;
+    const int ctas = pack_ctas(N);
+    if (int rc = launched(launch_pack(k, ctas, stream))) return rc;
+    LogitsArgs g{};
+    g.nact = k.nact;
+    g.tgt = k.tgt;
+    g.parts = at<float2>(workspace, p.big);
+    g.zt = at<float>(workspace, p.f0);
+    g.status = k.status + ctas;
+    g.Np = p.Np;
+    g.D = D;
+    g.V = V;
+    g.v1 = V;
+    if (int rc = launched(launch_logits(g, false, k.xp, weight, sms, stream))) return rc;
+    LseArgs l{};
+    l.nact = k.nact;
+    l.row = k.row;
+    l.parts = g.parts;
+    l.zt = g.zt;
+    l.loss = loss;
+    l.lse = lse;
+    l.N = N;
+    l.Np = p.Np;
+    l.nparts = (int)(2 * p.tiles);
+    return launched(launch_lse(l, sms, stream));
+}
+
+size_t adaln_linear_xent_bwd_workspace_size(int64_t N, int64_t V, int64_t D, adaln_dtype dtype) {
+    return xent_check(N, V, D, dtype) ? 0 : xent_plan(N, V, D, true).bytes;
+}
+
+int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* target, const float* lse,
+                          const float* dloss, const float* dlse, void* dx, void* dweight, int64_t N, int64_t V,
+                          int64_t D, int64_t ignore_index, void* workspace, size_t workspace_bytes,
+                          adaln_dtype dtype, cudaStream_t stream) {
+    if (int rc = xent_check(N, V, D, dtype)) return rc;
+    if (int rc = check_io({weight}, {})) return rc;
+    if (!dx && !dweight && N > 0) return ADALN_ERR_INVALID_ARG;
+    if (!aligned(dx, 16) || !aligned(dweight, 16) || !aligned(dlse, 4)) return ADALN_ERR_ALIGNMENT;
+    if (N > 0) {
+        if (int rc = check_io({x}, {lse, dloss})) return rc;
+        if (!target) return ADALN_ERR_INVALID_ARG;
+        if (!aligned(target, 8)) return ADALN_ERR_ALIGNMENT;
+    }
+    const XentPlan p = xent_plan(N, V, D, true);
+    if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
+    int dev = 0;
+    const int sms = current_sms(&dev);
+    if (sms <= 0) return ADALN_ERR_CUDA;
+    PackArgs k = xent_pack(p, workspace, x, target, N, V, D, ignore_index);
+    k.lse = lse;
+    k.dloss = dloss;
+    k.dlse = dlse;
+    k.row_lse2 = at<float>(workspace, p.f0);
+    k.row_gs = at<float>(workspace, p.f1);
+    k.row_gt = at<float>(workspace, p.f2);
+    k.dx = dx;
+    const int ctas = pack_ctas(N);
+    if (int rc = launched(launch_pack(k, ctas, stream))) return rc;
+    for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
+        LogitsArgs g{};
+        g.nact = k.nact;
+        g.tgt = k.tgt;
+        g.row_lse2 = k.row_lse2;
+        g.row_gs = k.row_gs;
+        g.row_gt = k.row_gt;
+        g.probs = at<__nv_bfloat16>(workspace, p.big);
+        g.ldp = p.piece;
+        g.status = k.status + ctas;
+        g.Np = p.Np;
+        g.D = D;
+        g.V = V;
+        g.v0 = v0;
+        g.v1 = std::min(V, v0 + p.piece);
+        if (int rc = launched(launch_logits(g, true, k.xp, weight, sms, stream))) return rc;
+        GradArgs d{};
+        d.nact = k.nact;
+        d.dxacc = dx ? at<float>(workspace, p.dxacc) : nullptr;
+        d.dweight = static_cast<__nv_bfloat16*>(dweight);
+        d.status = g.status;
+        d.Np = p.Np;
+        d.D = D;
+        d.V = V;
+        d.v0 = v0;
+        d.v1 = g.v1;
+        d.splits = p.splits;
+        if (int rc = launched(launch_grad(d, g.probs, p.piece, k.xp, weight, sms, stream))) return rc;
+    }
+    if (!dx) return ADALN_OK;
+    DxArgs d{};
+    d.nact = k.nact;
+    d.row = k.row;
+    d.dxacc = at<float>(workspace, p.dxacc);
+    d.dx = dx;
+    d.N = N;
+    d.Np = p.Np;
+    d.D = D;
+    d.splits = p.splits;
+    return launched(launch_dx(d, sms, stream));
 }
 
 }  // extern "C"

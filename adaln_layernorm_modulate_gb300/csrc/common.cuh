@@ -59,6 +59,7 @@ enum : uint32_t {
     kDbgGrads = 64u,     // dshift, dscale: [0, nmod) x [0, D)
     kDbgRanks = 128u,    // rank sum: [0, n) of each rank's array and of the output
     kDbgStatus = 256u,   // status words: [0, kMaxCtas)
+    kDbgLoss = 512u,     // vocabulary loss: rows, packed rows, partials, dz, dx and dweight
 };
 #ifdef ADALN_DEBUG
 static __device__ unsigned int g_adaln_debug;  // one per translation unit (module)
@@ -100,7 +101,7 @@ constexpr size_t kStatusWordsBytes = sizeof(uint32_t) * kMaxCtas;
 constexpr size_t kPartialsOffset = kHeaderBytes + kStatusWordsBytes;
 constexpr uint32_t kStatusMagic = 0x4E4C4441u;  // "ADLN"
 
-enum : uint32_t { kErrSeqlens = 1u, kErrModIdx = 2u, kErrTimeout = 4u };
+enum : uint32_t { kErrSeqlens = 1u, kErrModIdx = 2u, kErrTimeout = 4u, kErrTarget = 8u };
 
 struct WsHeader {
     uint32_t magic;

@@ -1,0 +1,627 @@
+// Softmax cross entropy over a vocabulary, from hidden rows and the head's weight, with its
+// gradient; the logits are never kept.
+//
+//     z = x W^T,  lse = log sum_v exp(z_v),  loss = lse - z_target
+//     dz = softmax(z) * (dloss + dlse) - onehot(target) * dloss,  dx = dz W,  dW = dz^T x
+//
+// Rows whose target is ignore_index carry no loss. Masked-token training has many of them, so
+// the first kernel packs the other rows densely (and their count stays on the device: the
+// kernels after it read it). Then
+//   forward:  logits_kernel<kStats>: tiles of z in tensor memory, reduced to (max, sum exp) a
+//             row and half tile; lse_kernel joins them in a fixed order;
+//   backward, a piece of the vocabulary at a time: logits_kernel<kProbs> computes the piece's
+//             tiles again and writes dz in bf16; grad_kernel forms dW of the piece (whole) and
+//             adds the piece's part of dx to an fp32 buffer; dx_kernel rounds dx once.
+// The products run on the tensor cores with fp32 accumulators; exp, sums and lse are fp32. dz is
+// rounded to bf16 as an operand of the next two products (half a step, 2^-9, of each factor).
+#include "tensor.cuh"
+#include "xent.h"
+
+namespace adaln {
+
+constexpr int kAccs = 2;              // accumulator tiles in tensor memory
+constexpr int kEpiWarp = 4;           // first epilogue warp
+constexpr int kEpiWarps = 8;          // two per 32 lanes of tensor memory, half the columns each
+constexpr int kGemmThreads = (kEpiWarp + kEpiWarps) * 32;
+constexpr uint32_t kABytes = kTileM * kTileK * 2, kBBytes = kTileN * kTileK * 2;
+constexpr uint32_t kStageBytes = kABytes + kBBytes;
+constexpr int kGemmStages = 4;
+constexpr size_t kGemmSmem = 1024 + (size_t)kGemmStages * kStageBytes;
+constexpr uint32_t kMnBlock = 64 * kTileK * 2;  // 64 m of all the tile's k (MN-major operands)
+constexpr float kLog2e = 1.4426950408889634f;
+
+#define ADALN_IN_LOSS(cond) ADALN_IN(::adaln::kDbgLoss, cond)
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+
+// ---------------------------------------------------------------------------------------
+// Packing: CTA b counts the rows that carry a loss before its range, then places its own
+// behind them, so the packed order is the row order, whatever the CTAs' timing.
+// ---------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
+    pdl_begin();
+    __shared__ int warp_tot[kPackThreads / 32];
+    __shared__ int list[kPackThreads];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int NW = kPackThreads / 32;
+    const int64_t G = gridDim.x, b = blockIdx.x;
+    const int64_t r0 = tile_begin(b, a.N, G), r1 = tile_begin(b + 1, a.N, G);
+    bool bad = false;
+    auto counts = [&](int64_t r, int64_t* t) {
+        if (!ADALN_IN_LOSS(r >= 0 && r < a.N)) return false;
+        *t = a.target[r];
+        return *t != a.ignore && *t >= 0 && *t < a.V;
+    };
+    // Rows that count before r0.
+    int n = 0;
+    for (int64_t r = tid; r < r0; r += kPackThreads) {
+        int64_t t;
+        n += counts(r, &t) ? 1 : 0;
+    }
+    for (int o = 16; o >= 1; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+    if (lane == 0) warp_tot[warp] = n;
+    __syncthreads();
+    int base = 0;
+    for (int w = 0; w < NW; ++w) base += warp_tot[w];
+    const int64_t vecs = a.D / 8;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int64_t c0 = r0; c0 < r1; c0 += kPackThreads) {
+        const int64_t r = c0 + tid;
+        int64_t t = 0;
+        const bool in = r < r1;
+        const bool on = in && counts(r, &t);
+        if (in && !on && t != a.ignore) bad = true;
+        const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, on);
+        __syncthreads();  // the last chunk's list and totals have been read
+        if (lane == 0) warp_tot[warp] = __popc(ballot);
+        __syncthreads();
+        int at = base, all = 0;
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) at += warp_tot[w];
+            all += warp_tot[w];
+        }
+        at += __popc(ballot & ((1u << lane) - 1u));
+        list[tid] = on ? at : -1;
+        if (on && ADALN_IN_LOSS(at < a.Np)) {
+            a.row[at] = (int32_t)r;
+            a.tgt[at] = (int32_t)t;
+            if (a.lse) {
+                a.row_lse2[at] = a.lse[r] * kLog2e;
+                const float up = a.dloss[r];
+                a.row_gt[at] = up;
+                a.row_gs[at] = a.dlse ? up + a.dlse[r] : up;
+            }
+        } else if (in && !on && a.loss_out) {
+            a.loss_out[r] = 0.0f;
+            a.lse_out[r] = 0.0f;
+        }
+        __syncthreads();
+        // One warp a row: pack the rows that count, zero the gradient rows of the others.
+        for (int i = warp; i < kPackThreads && c0 + i < r1; i += NW) {
+            const int to = list[i];
+            if (to >= 0) {
+                const uint4* src = reinterpret_cast<const uint4*>(a.x) + (c0 + i) * vecs;
+                uint4* dst = reinterpret_cast<uint4*>(a.xp) + (int64_t)to * vecs;
+                for (int64_t v = lane; v < vecs; v += 32)
+                    if (ADALN_IN_LOSS(c0 + i < a.N && to < a.Np)) dst[v] = ld_stream(src + v);
+            } else if (a.dx) {
+                uint4* dst = reinterpret_cast<uint4*>(a.dx) + (c0 + i) * vecs;
+                for (int64_t v = lane; v < vecs; v += 32)
+                    if (ADALN_IN_LOSS(c0 + i < a.N)) dst[v] = zero;
+            }
+        }
+        base += all;
+    }
+    if (b == G - 1) {
+        // The rest of the last row tile: zero rows without a target.
+        const int64_t end = ((int64_t)base + kTileM - 1) / kTileM * kTileM;
+        for (int64_t r = base + tid; r < end; r += kPackThreads) {
+            if (!ADALN_IN_LOSS(r < a.Np)) continue;
+            a.tgt[r] = -1;
+            if (a.lse) a.row_lse2[r] = a.row_gt[r] = a.row_gs[r] = 0.0f;
+        }
+        uint4* dst = reinterpret_cast<uint4*>(a.xp);
+        for (int64_t v = base * vecs + tid; v < end * vecs; v += kPackThreads)
+            if (ADALN_IN_LOSS(v < a.Np * vecs)) dst[v] = zero;
+        if (tid == 0) *a.nact = base;
+    }
+    const bool any_bad = __syncthreads_or(bad);
+    if (tid == 0) {
+        a.status[b] = any_bad ? kErrTarget : 0u;
+        if (b == 0) {
+            a.status[G] = 0u;  // the tensor-core kernels' word
+            a.header->magic = kStatusMagic;
+            a.header->nwords = (uint32_t)G + 1u;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// Matrix products. A persistent CTA per SM walks its units (output tiles): warp 0 fills a ring
+// of shared-memory stages by TMA, warp 1 issues the products into one of two accumulators,
+// warps 4.. read the other one back and run the epilogue.
+// ---------------------------------------------------------------------------------------
+struct Unit {
+    const CUtensorMap* ma;
+    const CUtensorMap* mb;
+    int64_t m0, n0;     // output tile: rows of A, rows of B
+    int64_t k0;         // first k of A
+    int64_t kb0;        // first k of B
+    int iters;          // K steps of kTileK
+    bool a_mn, b_mn;    // operand layouts
+    int kind;           // 0: logits; 1: dx; 2: dweight
+    int64_t slot;       // dx: which part of the K range
+};
+
+template <class Decode, class Epilogue>
+__device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decode decode, Epilogue epilogue) {
+    extern __shared__ uint4 dyn[];
+    __shared__ __align__(8) uint64_t bars[2 * kGemmStages + 2 * kAccs + 1];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t data = (smem_addr(dyn) + 1023u) & ~1023u;
+    const uint32_t full = smem_addr(bars), empty = full + 8u * kGemmStages;
+    const uint32_t afull = empty + 8u * kGemmStages, aempty = afull + 8u * kAccs, drain = aempty + 8u * kAccs;
+    if (tid == 0) {
+        for (int i = 0; i < kGemmStages; ++i) {
+            mbar_init(full + 8u * i, 1);
+            mbar_init(empty + 8u * i, 1);
+        }
+        for (int i = 0; i < kAccs; ++i) {
+            mbar_init(afull + 8u * i, 1);
+            mbar_init(aempty + 8u * i, kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == 2) tmem_alloc(smem_addr(&tmem_base), kAccs * kTileN);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            fence_async_proxy();
+            int s = 0;
+            uint32_t lap = 0;
+            bool live = true;
+            for (int64_t u = blockIdx.x; live && u < units; u += gridDim.x) {
+                const Unit t = decode(u);
+                for (int i = 0; i < t.iters; ++i) {
+                    if (lap > 0 && !mbar_wait_bounded(empty + 8u * s, (lap - 1) & 1u, &abort_flag)) {
+                        live = false;
+                        break;
+                    }
+                    const uint32_t bar = full + 8u * s, as = data + s * kStageBytes, bs = as + kABytes;
+                    mbar_arrive_expect_tx(bar, kStageBytes);
+                    const int ka = (int)(t.k0 + (int64_t)i * kTileK), kb = (int)(t.kb0 + (int64_t)i * kTileK);
+                    if (t.a_mn) {
+                        for (int j = 0; j < kTileM / 64; ++j)
+                            tma_load(as + j * kMnBlock, t.ma, (int)t.m0 + 64 * j, ka, bar);
+                    } else {
+                        tma_load(as, t.ma, ka, (int)t.m0, bar);
+                    }
+                    if (t.b_mn) {
+                        for (int j = 0; j < kTileN / 64; ++j)
+                            tma_load(bs + j * kMnBlock, t.mb, (int)t.n0 + 64 * j, kb, bar);
+                    } else {
+                        tma_load(bs, t.mb, kb, (int)t.n0, bar);
+                    }
+                    if (++s == kGemmStages) {
+                        s = 0;
+                        ++lap;
+                    }
+                }
+            }
+            // After a timeout, copies may still be on their way into this CTA's memory: give
+            // each stage's last one a further bounded wait.
+            if (*(volatile int*)&abort_flag) {
+                volatile int never = 0;
+                for (int q = 0; q < kGemmStages; ++q) {
+                    if (q >= s && lap == 0) continue;
+                    const uint32_t last = q < s ? lap : lap - 1;
+                    mbar_wait_bounded(full + 8u * q, last & 1u, &never);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int s = 0, acc = 0;
+            uint32_t lap = 0, alap = 0;
+            bool live = true;
+            for (int64_t u = blockIdx.x; live && u < units; u += gridDim.x) {
+                const Unit t = decode(u);
+                const uint32_t idesc = mma_desc(kTileM, kTileN, t.a_mn, t.b_mn);
+                // 16 k: 32 bytes of a K-major row, 16 rows of an MN-major tile.
+                const uint32_t ak = (t.a_mn ? 2048u : 32u) >> 4, bk = (t.b_mn ? 2048u : 32u) >> 4;
+                if (alap > 0 && !mbar_wait_bounded(aempty + 8u * acc, (alap - 1) & 1u, &abort_flag)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)acc * kTileN;
+                for (int i = 0; i < t.iters; ++i) {
+                    if (!mbar_wait_bounded(full + 8u * s, lap & 1u, &abort_flag)) {
+                        live = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t as = data + s * kStageBytes;
+                    const uint64_t da = smem_desc(as, kMnBlock), db = smem_desc(as + kABytes, kMnBlock);
+#pragma unroll
+                    for (int k = 0; k < kTileK / 16; ++k)
+                        mma_bf16(d, da + (uint64_t)(k * ak), db + (uint64_t)(k * bk), idesc, i > 0 || k > 0);
+                    mma_commit(empty + 8u * s);
+                    if (++s == kGemmStages) {
+                        s = 0;
+                        ++lap;
+                    }
+                }
+                if (!live) break;
+                mma_commit(afull + 8u * acc);
+                if (++acc == kAccs) {
+                    acc = 0;
+                    ++alap;
+                }
+            }
+            if (*(volatile int*)&abort_flag) {  // products in flight end before their memory is given back
+                volatile int never = 0;
+                mma_commit(drain);
+                mbar_wait_bounded(drain, 0, &never);
+            }
+        }
+    } else if (warp >= kEpiWarp) {
+        const int q = warp & 3, half = (warp - kEpiWarp) >> 2;
+        int acc = 0;
+        uint32_t alap = 0;
+        for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+            const Unit t = decode(u);
+            bool ok = mbar_wait_bounded(afull + 8u * acc, alap & 1u, &abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t src = tmem + (uint32_t)acc * kTileN + (uint32_t)half * (kTileN / 2) + ((uint32_t)q << 21);
+            epilogue(t, src, q * 32 + lane, half, [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(aempty + 8u * acc);
+            });
+            if (++acc == kAccs) {
+                acc = 0;
+                ++alap;
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 2) tmem_free(tmem, kAccs * kTileN);
+    if (tid == 0 && abort_flag) atomicOr(status, kErrTimeout);
+}
+
+// The tile's logits, as row statistics (PROBS false) or as dz (PROBS true).
+template <bool PROBS>
+__global__ void __launch_bounds__(kGemmThreads) logits_kernel(const __grid_constant__ CUtensorMap mx,
+                                                              const __grid_constant__ CUtensorMap mw,
+                                                              const LogitsArgs a) {
+    pdl_begin();
+    const int64_t nact = *a.nact;
+    const int64_t mt = (nact + kTileM - 1) / kTileM;
+    const int64_t nt = (a.v1 - a.v0 + kTileN - 1) / kTileN;
+    auto decode = [&](int64_t u) {
+        Unit t{};
+        t.ma = &mx;
+        t.mb = &mw;
+        t.m0 = u % mt * kTileM;
+        t.n0 = a.v0 + u / mt * kTileN;
+        t.iters = (int)((a.D + kTileK - 1) / kTileK);
+        return t;
+    };
+    gemm_loop(mt * nt, a.status, decode, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
+        const int64_t row = t.m0 + r;
+        const bool in = ADALN_IN_LOSS(row < a.Np);
+        const int tgt = in ? a.tgt[row] : -1;
+        const int64_t c0 = t.n0 + half * (kTileN / 2);
+        float mx_ = neg_inf(), sum = 0.0f;
+        float lse2 = 0.0f, gs = 0.0f, gt = 0.0f;
+        if constexpr (PROBS) {
+            if (in) {
+                lse2 = a.row_lse2[row];
+                gs = a.row_gs[row];
+                gt = a.row_gt[row];
+            }
+        }
+#pragma unroll 1
+        for (int c = 0; c < kTileN / 2; c += 32) {
+            float v[32];
+            __syncwarp();
+            tmem_ld32(src + c, v);
+            const int64_t col = c0 + c;
+            const int hit = (int64_t)tgt >= col && (int64_t)tgt < col + 32 ? (int)(tgt - col) : -1;
+            if constexpr (!PROBS) {
+                if (col + 32 > a.V) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (col + j >= a.V) v[j] = neg_inf();
+                }
+                if (hit >= 0) {
+                    float z = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) z = j == hit ? v[j] : z;
+                    if (in) a.zt[row] = z;
+                }
+                float m = mx_;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) m = fmaxf(m, v[j]);
+                // A chunk with no finite value at all adds nothing (and NaN is kept below).
+                const float mm = m == neg_inf() ? 0.0f : m;
+                const float m2 = mm * kLog2e;
+                float s = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) s += exp2f(fmaf(v[j], kLog2e, -m2));
+                sum = sum * exp2f((mx_ - mm) * kLog2e) + s;
+                mx_ = m;
+            } else {
+                uint32_t w[16];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    float p = exp2f(fmaf(v[j], kLog2e, -lse2)) * gs;
+                    if (j == hit) p -= gt;
+                    v[j] = p;
+                }
+                // Columns past the vocabulary and rows past the packed ones are operands too: zeros.
+                if (col + 32 > a.V || row >= nact) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (col + j >= a.V || row >= nact) v[j] = 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
+                if (in && ADALN_IN_LOSS(col - a.v0 + 32 <= a.ldp)) {
+                    uint4* dst = reinterpret_cast<uint4*>(a.probs + row * a.ldp + (col - a.v0));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                }
+            }
+        }
+        release();
+        if constexpr (!PROBS) {
+            const int64_t part = (t.n0 - a.v0) / kTileN * 2 + half;
+            if (in) a.parts[part * a.Np + row] = make_float2(mx_, sum);
+        }
+    });
+}
+
+// dx += dz W and dweight = dz^T x of one piece of the vocabulary, as one list of units: dx
+// tiles, each in `splits` parts of the piece's columns, then dweight tiles.
+__global__ void __launch_bounds__(kGemmThreads) grad_kernel(const __grid_constant__ CUtensorMap mp,
+                                                            const __grid_constant__ CUtensorMap mw,
+                                                            const __grid_constant__ CUtensorMap mx,
+                                                            const __grid_constant__ CUtensorMap mpt,
+                                                            const GradArgs a) {
+    pdl_begin();
+    const int64_t nact = *a.nact;
+    const int64_t mt = (nact + kTileM - 1) / kTileM;
+    const int64_t dt = (a.D + kTileN - 1) / kTileN;
+    const int64_t kv = (a.v1 - a.v0 + kTileK - 1) / kTileK;  // K steps of dx
+    const int64_t vt = (a.v1 - a.v0 + kTileM - 1) / kTileM;
+    const int64_t ndx = a.dxacc ? mt * dt * a.splits : 0, ndw = a.dweight ? vt * dt : 0;
+    auto decode = [&](int64_t u) {
+        Unit t{};
+        t.b_mn = true;
+        if (u < ndx) {
+            t.kind = 1;
+            t.slot = u / (mt * dt);
+            const int64_t w = u % (mt * dt);
+            const int64_t k0 = t.slot * kv / a.splits, k1 = (t.slot + 1) * kv / a.splits;
+            t.ma = &mp;
+            t.mb = &mw;
+            t.m0 = w % mt * kTileM;
+            t.n0 = w / mt * kTileN;
+            t.k0 = k0 * kTileK;
+            t.kb0 = a.v0 + t.k0;
+            t.iters = (int)(k1 - k0);
+        } else {
+            t.kind = 2;
+            const int64_t w = u - ndx;
+            t.ma = &mpt;
+            t.mb = &mx;
+            t.a_mn = true;
+            t.m0 = w / dt * kTileM;
+            t.n0 = w % dt * kTileN;
+            t.iters = (int)((nact + kTileK - 1) / kTileK);
+        }
+        return t;
+    };
+    gemm_loop(ndx + ndw, a.status, decode, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
+        const int64_t row = t.m0 + r;
+        const int64_t c0 = t.n0 + half * (kTileN / 2);
+#pragma unroll 1
+        for (int c = 0; c < kTileN / 2; c += 32) {
+            float v[32];
+            __syncwarp();
+            tmem_ld32(src + c, v);
+            if (t.iters == 0) {  // nothing was accumulated
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+            }
+            const int64_t col = c0 + c;
+            if (t.kind == 1) {
+                float* dst = a.dxacc + (t.slot * a.Np + row) * a.D + col;
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    if (col + j >= a.D || !ADALN_IN_LOSS(row < a.Np && t.slot < a.splits)) continue;
+                    float4 s = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    if (a.v0 > 0) {
+                        const float4 o = *reinterpret_cast<const float4*>(dst + j);
+                        s.x += o.x;
+                        s.y += o.y;
+                        s.z += o.z;
+                        s.w += o.w;
+                    }
+                    *reinterpret_cast<float4*>(dst + j) = s;
+                }
+            } else {
+                const int64_t word = a.v0 + row;
+                uint4* dst = reinterpret_cast<uint4*>(a.dweight + word * a.D + col);
+#pragma unroll
+                for (int j = 0; j < 32; j += 8) {
+                    if (word >= a.v1 || col + j >= a.D || !ADALN_IN_LOSS(word < a.V)) continue;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[j + 2 * i + 1]), "f"(v[j + 2 * i]));
+                    dst[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        release();
+    });
+}
+
+// Joins a row's partial (max, sum exp) in a fixed order: 8 threads a row, each a run of parts,
+// then the 8 in order. 32 rows a CTA, so that a warp reads 32 rows' parts side by side.
+__global__ void __launch_bounds__(256) lse_kernel(const LseArgs a) {
+    pdl_begin();
+    __shared__ float2 red[8][32];
+    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int64_t nact = *a.nact;
+    auto join = [](float2 p, float2 q) {
+        const float m = fmaxf(p.x, q.x), mm = m == neg_inf() ? 0.0f : m;
+        return make_float2(m, p.y * exp2f((p.x - mm) * kLog2e) + q.y * exp2f((q.x - mm) * kLog2e));
+    };
+    for (int64_t t = blockIdx.x; t * 32 < nact; t += gridDim.x) {
+        const int64_t row = t * 32 + lane;
+        float2 acc = make_float2(neg_inf(), 0.0f);
+        if (row < nact) {
+            const int64_t p0 = (int64_t)g * a.nparts / 8, p1 = (int64_t)(g + 1) * a.nparts / 8;
+            for (int64_t p = p0; p < p1; ++p)
+                if (ADALN_IN_LOSS(row < a.Np)) acc = join(acc, a.parts[p * a.Np + row]);
+        }
+        red[g][lane] = acc;
+        __syncthreads();
+        if (g == 0 && row < nact) {
+            for (int i = 1; i < 8; ++i) acc = join(acc, red[i][lane]);
+            const float lse = acc.x + logf(acc.y);
+            const int64_t r = a.row[row];
+            if (ADALN_IN_LOSS(r >= 0 && r < a.N)) {
+                a.lse[r] = lse;
+                a.loss[r] = lse - a.zt[row];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// dx of the packed rows: the parts added in order, rounded once, back to the rows' places.
+__global__ void __launch_bounds__(256) dx_kernel(const DxArgs a) {
+    pdl_begin();
+    const int64_t nact = *a.nact, vecs = a.D / 8;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < nact * vecs; i += (int64_t)gridDim.x * 256) {
+        const int64_t p = i / vecs, v = i % vecs;
+        float s[8] = {};
+        for (int k = 0; k < a.splits; ++k) {
+            if (!ADALN_IN_LOSS(p < a.Np)) continue;
+            const float4* src = reinterpret_cast<const float4*>(a.dxacc + ((int64_t)k * a.Np + p) * a.D + v * 8);
+            const float4 lo = src[0], hi = src[1];
+            s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
+            s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(s[2 * j + 1]), "f"(s[2 * j]));
+        const int64_t r = a.row[p];
+        if (ADALN_IN_LOSS(r >= 0 && r < a.N))
+            reinterpret_cast<uint4*>(a.dx)[r * vecs + v] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// ---- launches ------------------------------------------------------------------------------
+namespace {
+
+unsigned cap(int64_t want, int64_t most) { return (unsigned)(want < 1 ? 1 : want < most ? want : most); }
+
+// Tiled tensor map of a row-major bf16 [rows, cols] matrix (row stride ld elements), boxes of 64
+// columns by `box_rows` rows, 128-byte swizzle.
+bool tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult res;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &res) !=
+                cudaSuccess ||
+            res != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<Encode>(fn);
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_pack(const PackArgs& args, int ctas, cudaStream_t stream) {
+    PackArgs a = args;
+    void* params[] = {&a};
+    return launch_dependent(reinterpret_cast<const void*>(&pack_kernel), dim3((unsigned)ctas), dim3(kPackThreads),
+                            params, 0, stream);
+}
+
+cudaError_t launch_logits(const LogitsArgs& args, bool probs, const void* xp, const void* weight, int sms,
+                          cudaStream_t stream) {
+    LogitsArgs a = args;
+    CUtensorMap mx, mw;
+    if (!tile_map(&mx, xp, a.Np, a.D, a.D, kTileM) || !tile_map(&mw, weight, a.V, a.D, a.D, kTileN))
+        return cudaErrorInvalidValue;
+    const void* fn = probs ? reinterpret_cast<const void*>(&logits_kernel<true>)
+                           : reinterpret_cast<const void*>(&logits_kernel<false>);
+    if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) return e;
+    const int64_t units = (a.Np / kTileM) * ((a.v1 - a.v0 + kTileN - 1) / kTileN);
+    void* params[] = {&mx, &mw, &a};
+    return launch_dependent(fn, dim3(cap(units, sms)), dim3(kGemmThreads), params, kGemmSmem, stream);
+}
+
+cudaError_t launch_grad(const GradArgs& args, const void* probs, int64_t ldp, const void* xp, const void* weight,
+                        int sms, cudaStream_t stream) {
+    GradArgs a = args;
+    CUtensorMap mp, mw, mx, mpt;
+    if (!tile_map(&mp, probs, a.Np, ldp, ldp, kTileM) || !tile_map(&mw, weight, a.V, a.D, a.D, kTileK) ||
+        !tile_map(&mx, xp, a.Np, a.D, a.D, kTileK) || !tile_map(&mpt, probs, a.Np, ldp, ldp, kTileK))
+        return cudaErrorInvalidValue;
+    const void* fn = reinterpret_cast<const void*>(&grad_kernel);
+    if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) return e;
+    const int64_t dt = (a.D + kTileN - 1) / kTileN;
+    const int64_t units = (a.dxacc ? a.Np / kTileM * dt * a.splits : 0) +
+                          (a.dweight ? (a.v1 - a.v0 + kTileM - 1) / kTileM * dt : 0);
+    void* params[] = {&mp, &mw, &mx, &mpt, &a};
+    return launch_dependent(fn, dim3(cap(units, sms)), dim3(kGemmThreads), params, kGemmSmem, stream);
+}
+
+cudaError_t launch_lse(const LseArgs& args, int sms, cudaStream_t stream) {
+    LseArgs a = args;
+    void* params[] = {&a};
+    return launch_dependent(reinterpret_cast<const void*>(&lse_kernel), dim3(cap(a.Np / 32, 8 * (int64_t)sms)),
+                            dim3(256), params, 0, stream);
+}
+
+cudaError_t launch_dx(const DxArgs& args, int sms, cudaStream_t stream) {
+    DxArgs a = args;
+    void* params[] = {&a};
+    const int64_t want = (a.Np * (a.D / 8) + 255) / 256;
+    return launch_dependent(reinterpret_cast<const void*>(&dx_kernel), dim3(cap(want, 8 * (int64_t)sms)), dim3(256),
+                            params, 0, stream);
+}
+
+cudaError_t debug_word_xent(uint32_t* out, bool reset) { return debug_word(out, reset); }
+
+}  // namespace adaln

@@ -1,0 +1,89 @@
+// Host-side entry points of the vocabulary loss's kernels (csrc/xent.cu, internal to libadaln).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+
+namespace adaln {
+
+// Output tile of a matrix product and its K step.
+constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
+constexpr int kPackThreads = 256;
+constexpr int kPackCtas = 304;  // two per SM: every CTA also counts the rows before its own
+
+struct PackArgs {
+    const void* x;          // [N, D]
+    const int64_t* target;  // [N]
+    const float* lse;       // backward: [N], or null
+    const float* dloss;
+    const float* dlse;      // or null
+    void* xp;               // packed rows [Np, D]
+    int32_t* row;           // [Np]: the packed row's row
+    int32_t* tgt;           // [Np]
+    float* row_lse2;        // backward: lse * log2(e), dloss + dlse, dloss of the packed row
+    float* row_gs;
+    float* row_gt;
+    int32_t* nact;          // packed rows
+    float* loss_out;        // forward: zeros for rows without a loss, or null
+    float* lse_out;
+    void* dx;               // backward: zeros for rows without a loss, or null
+    uint32_t* status;
+    WsHeader* header;
+    int64_t N, Np, D, V, ignore;
+};
+
+struct LogitsArgs {
+    const int32_t* nact;
+    const int32_t* tgt;
+    float2* parts;          // statistics: [2 * tiles][Np] (max, sum exp)
+    float* zt;              // statistics: [Np], the target's logit
+    const float* row_lse2;  // dz
+    const float* row_gs;
+    const float* row_gt;
+    __nv_bfloat16* probs;   // dz [Np, ldp]
+    int64_t ldp;
+    uint32_t* status;
+    int64_t Np, D, V, v0, v1;  // columns [v0, v1) of the vocabulary
+};
+
+struct GradArgs {
+    const int32_t* nact;
+    float* dxacc;           // [splits][Np][D] fp32, or null
+    __nv_bfloat16* dweight; // [V, D], or null
+    uint32_t* status;
+    int64_t Np, D, V, v0, v1;
+    int splits;             // parts of dx's K range
+};
+
+struct LseArgs {
+    const int32_t* nact;
+    const int32_t* row;
+    const float2* parts;
+    const float* zt;
+    float* loss;
+    float* lse;
+    int64_t N, Np;
+    int nparts;
+};
+
+struct DxArgs {
+    const int32_t* nact;
+    const int32_t* row;
+    const float* dxacc;
+    void* dx;
+    int64_t N, Np, D;
+    int splits;
+};
+
+cudaError_t launch_pack(const PackArgs& args, int ctas, cudaStream_t stream);
+cudaError_t launch_logits(const LogitsArgs& args, bool probs, const void* xp, const void* weight, int sms,
+                          cudaStream_t stream);
+cudaError_t launch_grad(const GradArgs& args, const void* probs, int64_t ldp, const void* xp, const void* weight,
+                        int sms, cudaStream_t stream);
+cudaError_t launch_lse(const LseArgs& args, int sms, cudaStream_t stream);
+cudaError_t launch_dx(const DxArgs& args, int sms, cudaStream_t stream);
+cudaError_t debug_word_xent(uint32_t* out, bool reset);
+
+}  // namespace adaln

@@ -70,16 +70,20 @@ typedef enum { ADALN_F32 = 0, ADALN_BF16 = 1 } adaln_dtype;
 typedef enum {
     ADALN_OK = 0,
     ADALN_ERR_INVALID_ARG = 1,  /* null pointer, negative size, bad eps or dtype       */
-    ADALN_ERR_UNSUPPORTED = 2,  /* D outside [8, 16384] or not a multiple of 8          */
+    ADALN_ERR_UNSUPPORTED = 2,  /* D outside [8, 16384] or not a multiple of 8; a dtype the
+                                   call does not take                                   */
     ADALN_ERR_ALIGNMENT = 3,    /* a pointer violates the alignment above               */
     ADALN_ERR_WORKSPACE = 4,    /* workspace null or smaller than required              */
     ADALN_ERR_CUDA = 5,         /* a CUDA runtime call or kernel launch failed          */
     ADALN_ERR_BAD_SEQLENS = 6,  /* device data: cu_seqlens malformed (adaln_read_status) */
     ADALN_ERR_BAD_MOD_IDX = 7,  /* device data: mod_idx out of range (adaln_read_status) */
-    ADALN_ERR_TIMEOUT = 8       /* a kernel gave up waiting (1 s) for a bulk copy of its
-                                   input rows, or for the row sums of the other CTA of its
-                                   cluster (fp32 rows wider than 14336); its outputs from
-                                   then on are not valid (adaln_read_status) */
+    ADALN_ERR_TIMEOUT = 8,      /* a kernel gave up waiting (1 s) for a bulk copy of its
+                                   input rows, for the row sums of the other CTA of its
+                                   cluster (fp32 rows wider than 14336) or for a matrix
+                                   product; its outputs from then on are not valid
+                                   (adaln_read_status) */
+    ADALN_ERR_BAD_TARGET = 9    /* device data: a target neither in [0, V) nor ignore_index
+                                   (adaln_read_status)                                  */
 } adaln_status;
 
 /* Forward, dense batch x[Bt, N, D]; token (b, n) uses shift[b], scale[b].
@@ -183,8 +187,8 @@ int adaln_bwd_varlen_recompute(const void* dy, const void* x, const void* scale,
                                adaln_dtype dtype, cudaStream_t stream);
 
 /* Synchronises `stream`, then returns the device-side status recorded in `workspace` by
- * the last packed forward/backward (or backward) that used it: ADALN_OK,
- * ADALN_ERR_BAD_SEQLENS, ADALN_ERR_BAD_MOD_IDX or ADALN_ERR_TIMEOUT, in that order of
+ * the last packed forward/backward (or backward, or vocabulary loss) that used it: ADALN_OK,
+ * ADALN_ERR_BAD_SEQLENS, ADALN_ERR_BAD_MOD_IDX, ADALN_ERR_BAD_TARGET or ADALN_ERR_TIMEOUT, in that order of
  * precedence (ADALN_ERR_CUDA if the copy fails, ADALN_ERR_WORKSPACE if the workspace holds
  * no status). Every wait a kernel makes on its own bulk copies is bounded (1 s); a kernel
  * that runs out of time stops, drains the copies it started and records the timeout. The
@@ -246,6 +250,36 @@ int adaln_layernorm_bwd(const void* dy, const void* x, const float* mean, const 
                         size_t workspace_bytes, int64_t R, int64_t D, adaln_dtype dtype,
                         cudaStream_t stream);
 
+/* ---- Softmax cross entropy over a vocabulary ---------------------------------------------
+ * The loss of a vocabulary head: hidden rows x [N, D], the head's weight [V, D] (bf16), targets
+ * [N] (device int64). The logits are never kept: the forward reduces tiles of them as they are
+ * computed, the backward computes them again, a piece of the vocabulary at a time.
+ *     z = x weight^T,  lse[i] = log sum_v exp(z[i, v]),  loss[i] = lse[i] - z[i, target[i]]
+ *     dz[i, v] = exp(z[i, v] - lse[i]) * (dloss[i] + dlse[i]) - (v == target[i]) * dloss[i]
+ *     dx = dz weight,  dweight = dz^T x
+ * Rows with target == ignore_index carry no loss: their loss, lse and dx are 0, they add
+ * nothing to dweight whatever x holds there, and they cost no products. A target outside
+ * [0, V) that is not ignore_index is treated the same and recorded (ADALN_ERR_BAD_TARGET in
+ * adaln_read_status, after the forward or the backward).
+ *
+ * x, weight, dx, dweight: `dtype` ADALN_BF16 (ADALN_F32 is ADALN_ERR_UNSUPPORTED: the products
+ * run on the tensor cores, whose operands are bf16), 16-byte aligned, contiguous; loss, lse,
+ * dloss, dlse: fp32. Products accumulate in fp32; dz is rounded to bf16 before its two
+ * products, dx and dweight once at the end. Results are bitwise reproducible.
+ * N >= 0, 1 <= V, D as everywhere. dlse may be null (lse is not differentiated); dx or dweight
+ * may be null (not wanted). With N = 0 the backward writes zero dweight. The backward takes the
+ * forward's lse and must get its ignore_index. Workspace as *_workspace_size says (they do not
+ * depend on the device); it keeps nothing between calls. */
+size_t adaln_linear_xent_fwd_workspace_size(int64_t N, int64_t V, int64_t D, adaln_dtype dtype);
+int adaln_linear_xent_fwd(const void* x, const void* weight, const int64_t* target, float* loss, float* lse,
+                          int64_t N, int64_t V, int64_t D, int64_t ignore_index, void* workspace,
+                          size_t workspace_bytes, adaln_dtype dtype, cudaStream_t stream);
+size_t adaln_linear_xent_bwd_workspace_size(int64_t N, int64_t V, int64_t D, adaln_dtype dtype);
+int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* target, const float* lse,
+                          const float* dloss, const float* dlse, void* dx, void* dweight, int64_t N, int64_t V,
+                          int64_t D, int64_t ignore_index, void* workspace, size_t workspace_bytes,
+                          adaln_dtype dtype, cudaStream_t stream);
+
 /* ---- Row sharding across ranks ----------------------------------------------------------
  * A batch can be split into contiguous, segment-aligned row shards, one per rank (the pages
  * train on 8- and 16-GPU clusters, AdaptiveLoad technical summary sections 2.A and 4). The
@@ -278,6 +312,7 @@ int adaln_sum_ranks(const float* parts, float* out, int32_t world, int64_t n, cu
 #define ADALN_DEBUG_GRADS    64u  /* dshift, dscale: [0, nmod) x [0, D)                       */
 #define ADALN_DEBUG_RANKS    128u /* adaln_sum_ranks: [0, n) of each rank's row              */
 #define ADALN_DEBUG_STATUS   256u /* workspace status words                                   */
+#define ADALN_DEBUG_LOSS     512u /* vocabulary loss: rows, packed rows, partials, gradients  */
 int adaln_debug_read(uint32_t* word, int reset);
 
 /* Dual-constraint bucket size, AdaptiveLoad technical summary section 2.A:
