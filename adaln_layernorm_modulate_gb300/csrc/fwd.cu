@@ -32,9 +32,11 @@
 namespace adaln {
 
 // AFFINE: the affine layer norm (dense, one modulation row for all rows): `scale` is the
-// multiplier itself (null: 1), a null shift is 0, and the stored mean takes a correction, the
-// mean of the row's residuals x - mean: K + mean(x - K) alone is off by a rounding of K =
-// x[row, 0], many roundings of a mean much smaller than K.
+// multiplier itself (null: 1) and a null shift is 0. Its rows are not shifted by x[row, 0]: K +
+// mean(x - K) is off by a rounding of K, many roundings of a mean much smaller than K. Instead
+// pass 2 also sums the residuals d = x - m of the first mean m, whose mean r is m's error: mean =
+// m + r, var = mean(d^2) - r^2, xhat = (d - r) * rstd. d is exact where the mean dwarfs the
+// spread, so such rows are as accurate as shifted ones.
 template <typename T, int NV, bool VARLEN, int RING, bool FULL, bool AFFINE = false>
 __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const FwdArgs a) {
     pdl_begin();
@@ -45,8 +47,7 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
     constexpr int RB = RowShape<NV>::kFwdRows;
     extern __shared__ uint4 ring[];
     __shared__ __align__(16) float red1[RB][32];
-    __shared__ __align__(16) float red2[RB][32];
-    __shared__ __align__(16) float red3[AFFINE ? RB : 1][32];  // AFFINE: sums of the residuals
+    __shared__ __align__(16) float red2[AFFINE ? 2 * RB : RB][32];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int TPB = blockDim.x;
@@ -77,8 +78,7 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
     const uint32_t my_k = data + (uint32_t)ns * vslot + (uint32_t)tid * 4u;
 
     zero_absent_warps<RB>(red1, nwarps);
-    zero_absent_warps<RB>(red2, nwarps);
-    if constexpr (AFFINE) zero_absent_warps<RB>(red3, nwarps);
+    zero_absent_warps<AFFINE ? 2 * RB : RB>(red2, nwarps);
     uint32_t err = validate_segments<VARLEN>(a.seg, b, G);
     if constexpr (BULK) {
         if (tid == 0) {
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
                     xv[i][k] = (i < nr && ok[k] && ADALN_IN_RING(bars, my_vec + rowsa + (uint32_t)k * vk, 16))
                                    ? lds128(my_vec + rowsa + (uint32_t)k * vk)
                                    : make_uint4(0, 0, 0, 0);
-                K[i] = (i < nr && ADALN_IN_RING(bars, data + rowsa, 4)) ? IO::first_of_word(lds32(data + rowsa))
+                K[i] = (!AFFINE && i < nr && ADALN_IN_RING(bars, data + rowsa, 4)) ? IO::first_of_word(lds32(data + rowsa))
                                                                           : 0.0f;
             }
         } else if constexpr (COPY) {
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
                     xv[i][k] = (i < nr && ok[k] && ADALN_IN_RING(bars, src + (uint32_t)k * vk, 16))
                                    ? lds128(src + (uint32_t)k * vk)
                                    : make_uint4(0, 0, 0, 0);
-                K[i] = (i < nr && ADALN_IN_RING(bars, my_k + (uint32_t)slot * kslot + (uint32_t)i * krow, 4))
+                K[i] = (!AFFINE && i < nr && ADALN_IN_RING(bars, my_k + (uint32_t)slot * kslot + (uint32_t)i * krow, 4))
                            ? IO::first_of_word(lds32(my_k + (uint32_t)slot * kslot + (uint32_t)i * krow))
                            : 0.0f;
             }
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
                     xv[i][k] = (i < nr && ok[k] && ADALN_IN_ROW(row + i, R, colb[k], 16, row_bytes))
                                    ? ld_stream(src + colb[k])
                                    : make_uint4(0, 0, 0, 0);
-                K[i] = (i < nr && ADALN_IN_ROW(row + i, R, 0, 4, row_bytes)) ? IO::first(src) : 0.0f;
+                K[i] = (!AFFINE && i < nr && ADALN_IN_ROW(row + i, R, 0, 4, row_bytes)) ? IO::first(src) : 0.0f;
             }
         }
 
@@ -237,8 +237,10 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
                     IO::unpackp(xv[i][k], d[i][k]);
 #pragma unroll
                     for (int p = 0; p < PV; ++p) {
-                        d[i][k][p] = p_sub(d[i][k][p], kk);
-                        if (!FULL && !ok[k]) d[i][k][p] = kPairZero;
+                        if constexpr (!AFFINE) {
+                            d[i][k][p] = p_sub(d[i][k][p], kk);
+                            if (!FULL && !ok[k]) d[i][k][p] = kPairZero;
+                        }
                         if (p & 1) acc1 = p_add(acc1, d[i][k][p]);
                         else acc0 = p_add(acc0, d[i][k][p]);
                     }
@@ -253,13 +255,13 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
             }
             __syncthreads();
             cta_sum(red1, ng, lane, s1);
-            // Pass 2: centred sum of squares.
-            float s2[RB], md[RB];
+            // Pass 2: centred sum of squares (AFFINE: and the residuals' sum, s2[RB + i]).
+            float s2[AFFINE ? 2 * RB : RB], md[RB];
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
-                md[i] = AFFINE ? __fmul_rn(s1[i], invD) : s1[i] * invD;
+                md[i] = s1[i] * invD;
                 const f2r pm = p_splat(md[i]);
-                f2r acc0 = kPairZero, acc1 = kPairZero;
+                f2r acc0 = kPairZero, acc1 = kPairZero, res0 = kPairZero, res1 = kPairZero;
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
 #pragma unroll
@@ -268,57 +270,47 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
                         if (!FULL && !ok[k]) d[i][k][p] = kPairZero;
                         if (p & 1) acc1 = p_fma(d[i][k][p], d[i][k][p], acc1);
                         else acc0 = p_fma(d[i][k][p], d[i][k][p], acc0);
+                        if constexpr (AFFINE) {
+                            if (p & 1) res1 = p_add(res1, d[i][k][p]);
+                            else res0 = p_add(res0, d[i][k][p]);
+                        }
                     }
                 }
                 s2[i] = p_hsum(p_add(acc0, acc1));
+                if constexpr (AFFINE) s2[RB + i] = p_hsum(p_add(res0, res1));
             }
             warp_sum(s2);
             if (lane == 0) {
 #pragma unroll
-                for (int i = 0; i < RB; ++i) red2[i][warp] = s2[i];
-            }
-            float s3[RB];
-#pragma unroll
-            for (int i = 0; i < RB; ++i) s3[i] = 0.0f;
-            if constexpr (AFFINE) {
-#pragma unroll
-                for (int i = 0; i < RB; ++i) {
-                    f2r acc = kPairZero;
-#pragma unroll
-                    for (int k = 0; k < NV; ++k)
-#pragma unroll
-                        for (int p = 0; p < PV; ++p) acc = p_add(acc, d[i][k][p]);
-                    s3[i] = p_hsum(acc);
-                }
-                warp_sum(s3);
-                if (lane == 0) {
-#pragma unroll
-                    for (int i = 0; i < RB; ++i) red3[i][warp] = s3[i];
-                }
+                for (int i = 0; i < (AFFINE ? 2 * RB : RB); ++i) red2[i][warp] = s2[i];
             }
             __syncthreads();
             cta_sum(red2, ng, lane, s2);
-            if constexpr (AFFINE) cta_sum(red3, ng, lane, s3);
             // Pass 3: y = (d - mean_d) * rstd * (1 + scale) + shift.
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 if (i >= nr) continue;
-                const float rs = rsqrtf(s2[i] * invD + a.eps);
-                const f2r prs = p_splat(rs);
+                float var = s2[i] * invD, resid = 0.0f;
+                if constexpr (AFFINE) {
+                    resid = s2[RB + i] * invD;
+                    var -= resid * resid;
+                    if (var < 0.0f) var = 0.0f;  // NaN stays
+                }
+                const float rs = rsqrtf(var + a.eps);
+                const f2r prs = p_splat(rs), pshift = p_splat(-resid * rs);
                 char* yr = yb + (row + i) * row_bytes;
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     if (!ok[k]) continue;
                     f2r o[PV];
 #pragma unroll
-                    for (int p = 0; p < PV; ++p) o[p] = p_fma(p_mul(d[i][k][p], prs), sc1[k][p], sh[k][p]);
+                    for (int p = 0; p < PV; ++p)
+                        o[p] = p_fma(AFFINE ? p_fma(d[i][k][p], prs, pshift) : p_mul(d[i][k][p], prs), sc1[k][p],
+                                     sh[k][p]);
                     if (ADALN_IN_ROW(row + i, R, colb[k], 16, row_bytes)) st_vec(yr + colb[k], IO::packp(o));
                 }
                 if (tid == 0 && ADALN_IN(kDbgStats, row + i >= 0 && row + i < R)) {
-                    if constexpr (AFFINE)  // the sum with md as rounded above, which the residuals used
-                        a.mean[row + i] = __fadd_rn(K[i], md[i]) + s3[i] * invD;
-                    else
-                        a.mean[row + i] = K[i] + md[i];
+                    a.mean[row + i] = AFFINE ? md[i] + resid : K[i] + md[i];
                     a.rstd[row + i] = rs;
                 }
             }

@@ -453,15 +453,14 @@ __global__ void __launch_bounds__(kGemmThreads) grad_kernel(const __grid_constan
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     if (col + j >= a.D || !ADALN_IN_LOSS(row < a.Np && t.slot < a.splits)) continue;
-                    float4 s = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                    if (a.v0 > 0) {
-                        const float4 o = *reinterpret_cast<const float4*>(dst + j);
-                        s.x += o.x;
-                        s.y += o.y;
-                        s.z += o.z;
-                        s.w += o.w;
-                    }
-                    *reinterpret_cast<float4*>(dst + j) = s;
+                    // A later piece adds in place (one addition a launch to each element, so the
+                    // order is the pieces'): the thread does not wait for the old value.
+                    if (a.v0 > 0)
+                        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst + j), "f"(v[j]),
+                                     "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3])
+                                     : "memory");
+                    else
+                        *reinterpret_cast<float4*>(dst + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                 }
             } else {
                 const int64_t word = a.v0 + row;
