@@ -248,7 +248,7 @@ bool make_plan(Kind kind, adaln_dtype dtype, int64_t D, int form, int64_t R, Pla
     p->full = p->ring && p->c.full;
     if (!ring_shape(kind, dtype, form, dev, p)) return false;
     RowCfg copy;
-    if (kind == kFwd && p->ring == kRingBulk && copy_ring_cfg(D, dtype, &copy) && R >= kCopyRingRows * p->G) {
+    if (kind == kFwd && form != kAffine && p->ring == kRingBulk && copy_ring_cfg(D, dtype, &copy) && R >= kCopyRingRows * p->G) {
         if (2 * ring_round_bytes(kind, copy, kRingCopy) + kRingHeader <= kRingLimit) {
             p->c = copy;
             p->ring = kRingCopy;

@@ -31,14 +31,37 @@
 
 namespace adaln {
 
+// The affine layer norm's shift of a row, from its first 16 bytes: their first element where they
+// differ by less than an eighth of it, else 0.
+template <typename T>
+__device__ __forceinline__ float row_shift(const uint4& v) {
+    f2r f[Io<T>::VE / 2];
+    Io<T>::unpackp(v, f);
+    const float2 a = p_get(f[0]);
+    float lo = fminf(a.x, a.y), hi = fmaxf(a.x, a.y);
+#pragma unroll
+    for (int p = 1; p < Io<T>::VE / 2; ++p) {
+        const float2 b = p_get(f[p]);
+        lo = fminf(lo, fminf(b.x, b.y));
+        hi = fmaxf(hi, fmaxf(b.x, b.y));
+    }
+    return 8.0f * (hi - lo) < fabsf(a.x) ? a.x : 0.0f;
+}
+
+// Launch bounds of the affine form: as max_threads, but three and four bf16 vectors a thread are
+// held to 136 and 128 registers, as the modulated form uses by itself (142 for four would leave
+// two CTAs of 160 threads an SM instead of three: bf16 [32760, 5120] 137 us against 115).
+__host__ __device__ constexpr int fwd_threads(int nv, int ve, bool affine) {
+    return affine && ve == 8 && nv == 4 ? 512 : affine && ve == 8 && nv == 3 ? 480 : max_threads(nv, ve);
+}
+
 // AFFINE: the affine layer norm (dense, one modulation row for all rows): `scale` is the
-// multiplier itself (null: 1) and a null shift is 0. Its rows are not shifted by x[row, 0]: K +
-// mean(x - K) is off by a rounding of K, many roundings of a mean much smaller than K. Instead
-// pass 2 also sums the residuals d = x - m of the first mean m, whose mean r is m's error: mean =
-// m + r, var = mean(d^2) - r^2, xhat = (d - r) * rstd. d is exact where the mean dwarfs the
-// spread, so such rows are as accurate as shifted ones.
+// multiplier itself (null: 1) and a null shift is 0. Its rows are shifted by x[row, 0] only where
+// their first elements say that a mean may dwarf the spread (row_shift): K + mean(x - K) is off by
+// a rounding of K, which is many roundings of a mean much smaller than K. (Correcting the mean by
+// the mean of the residuals in a further sum costs registers and time.)
 template <typename T, int NV, bool VARLEN, int RING, bool FULL, bool AFFINE = false>
-__global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(fwd_threads(NV, Io<T>::VE, AFFINE)) fwd_kernel(const FwdArgs a) {
     pdl_begin();
     constexpr bool BULK = RING == kRingBulk, COPY = RING == kRingCopy;
     using IO = Io<T>;
@@ -47,7 +70,7 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
     constexpr int RB = RowShape<NV>::kFwdRows;
     extern __shared__ uint4 ring[];
     __shared__ __align__(16) float red1[RB][32];
-    __shared__ __align__(16) float red2[AFFINE ? 2 * RB : RB][32];
+    __shared__ __align__(16) float red2[RB][32];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int TPB = blockDim.x;
@@ -78,7 +101,7 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
     const uint32_t my_k = data + (uint32_t)ns * vslot + (uint32_t)tid * 4u;
 
     zero_absent_warps<RB>(red1, nwarps);
-    zero_absent_warps<AFFINE ? 2 * RB : RB>(red2, nwarps);
+    zero_absent_warps<RB>(red2, nwarps);
     uint32_t err = validate_segments<VARLEN>(a.seg, b, G);
     if constexpr (BULK) {
         if (tid == 0) {
@@ -171,8 +194,11 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
                     xv[i][k] = (i < nr && ok[k] && ADALN_IN_RING(bars, my_vec + rowsa + (uint32_t)k * vk, 16))
                                    ? lds128(my_vec + rowsa + (uint32_t)k * vk)
                                    : make_uint4(0, 0, 0, 0);
-                K[i] = (!AFFINE && i < nr && ADALN_IN_RING(bars, data + rowsa, 4)) ? IO::first_of_word(lds32(data + rowsa))
-                                                                          : 0.0f;
+                if constexpr (AFFINE)
+                    K[i] = (i < nr && ADALN_IN_RING(bars, data + rowsa, 16)) ? row_shift<T>(lds128(data + rowsa)) : 0.0f;
+                else
+                    K[i] = (i < nr && ADALN_IN_RING(bars, data + rowsa, 4)) ? IO::first_of_word(lds32(data + rowsa))
+                                                                              : 0.0f;
             }
         } else if constexpr (COPY) {
             cp_async_wait(ns - 1);  // this thread's copies of this round have landed
@@ -184,7 +210,7 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
                     xv[i][k] = (i < nr && ok[k] && ADALN_IN_RING(bars, src + (uint32_t)k * vk, 16))
                                    ? lds128(src + (uint32_t)k * vk)
                                    : make_uint4(0, 0, 0, 0);
-                K[i] = (!AFFINE && i < nr && ADALN_IN_RING(bars, my_k + (uint32_t)slot * kslot + (uint32_t)i * krow, 4))
+                K[i] = (i < nr && ADALN_IN_RING(bars, my_k + (uint32_t)slot * kslot + (uint32_t)i * krow, 4))
                            ? IO::first_of_word(lds32(my_k + (uint32_t)slot * kslot + (uint32_t)i * krow))
                            : 0.0f;
             }
@@ -197,7 +223,10 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
                     xv[i][k] = (i < nr && ok[k] && ADALN_IN_ROW(row + i, R, colb[k], 16, row_bytes))
                                    ? ld_stream(src + colb[k])
                                    : make_uint4(0, 0, 0, 0);
-                K[i] = (!AFFINE && i < nr && ADALN_IN_ROW(row + i, R, 0, 4, row_bytes)) ? IO::first(src) : 0.0f;
+                if constexpr (AFFINE)
+                    K[i] = (i < nr && ADALN_IN_ROW(row + i, R, 0, 16, row_bytes)) ? row_shift<T>(ld_stream(src)) : 0.0f;
+                else
+                    K[i] = (i < nr && ADALN_IN_ROW(row + i, R, 0, 4, row_bytes)) ? IO::first(src) : 0.0f;
             }
         }
 
@@ -237,10 +266,8 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
                     IO::unpackp(xv[i][k], d[i][k]);
 #pragma unroll
                     for (int p = 0; p < PV; ++p) {
-                        if constexpr (!AFFINE) {
-                            d[i][k][p] = p_sub(d[i][k][p], kk);
-                            if (!FULL && !ok[k]) d[i][k][p] = kPairZero;
-                        }
+                        d[i][k][p] = p_sub(d[i][k][p], kk);
+                        if (!FULL && !ok[k]) d[i][k][p] = kPairZero;
                         if (p & 1) acc1 = p_add(acc1, d[i][k][p]);
                         else acc0 = p_add(acc0, d[i][k][p]);
                     }
@@ -255,13 +282,13 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
             }
             __syncthreads();
             cta_sum(red1, ng, lane, s1);
-            // Pass 2: centred sum of squares (AFFINE: and the residuals' sum, s2[RB + i]).
-            float s2[AFFINE ? 2 * RB : RB], md[RB];
+            // Pass 2: centred sum of squares.
+            float s2[RB], md[RB];
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 md[i] = s1[i] * invD;
                 const f2r pm = p_splat(md[i]);
-                f2r acc0 = kPairZero, acc1 = kPairZero, res0 = kPairZero, res1 = kPairZero;
+                f2r acc0 = kPairZero, acc1 = kPairZero;
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
 #pragma unroll
@@ -270,19 +297,14 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
                         if (!FULL && !ok[k]) d[i][k][p] = kPairZero;
                         if (p & 1) acc1 = p_fma(d[i][k][p], d[i][k][p], acc1);
                         else acc0 = p_fma(d[i][k][p], d[i][k][p], acc0);
-                        if constexpr (AFFINE) {
-                            if (p & 1) res1 = p_add(res1, d[i][k][p]);
-                            else res0 = p_add(res0, d[i][k][p]);
-                        }
                     }
                 }
                 s2[i] = p_hsum(p_add(acc0, acc1));
-                if constexpr (AFFINE) s2[RB + i] = p_hsum(p_add(res0, res1));
             }
             warp_sum(s2);
             if (lane == 0) {
 #pragma unroll
-                for (int i = 0; i < (AFFINE ? 2 * RB : RB); ++i) red2[i][warp] = s2[i];
+                for (int i = 0; i < RB; ++i) red2[i][warp] = s2[i];
             }
             __syncthreads();
             cta_sum(red2, ng, lane, s2);
@@ -290,27 +312,19 @@ __global__ void __launch_bounds__(max_threads(NV, Io<T>::VE)) fwd_kernel(const F
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 if (i >= nr) continue;
-                float var = s2[i] * invD, resid = 0.0f;
-                if constexpr (AFFINE) {
-                    resid = s2[RB + i] * invD;
-                    var -= resid * resid;
-                    if (var < 0.0f) var = 0.0f;  // NaN stays
-                }
-                const float rs = rsqrtf(var + a.eps);
-                const f2r prs = p_splat(rs), pshift = p_splat(-resid * rs);
+                const float rs = rsqrtf(s2[i] * invD + a.eps);
+                const f2r prs = p_splat(rs);
                 char* yr = yb + (row + i) * row_bytes;
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     if (!ok[k]) continue;
                     f2r o[PV];
 #pragma unroll
-                    for (int p = 0; p < PV; ++p)
-                        o[p] = p_fma(AFFINE ? p_fma(d[i][k][p], prs, pshift) : p_mul(d[i][k][p], prs), sc1[k][p],
-                                     sh[k][p]);
+                    for (int p = 0; p < PV; ++p) o[p] = p_fma(p_mul(d[i][k][p], prs), sc1[k][p], sh[k][p]);
                     if (ADALN_IN_ROW(row + i, R, colb[k], 16, row_bytes)) st_vec(yr + colb[k], IO::packp(o));
                 }
                 if (tid == 0 && ADALN_IN(kDbgStats, row + i >= 0 && row + i < R)) {
-                    a.mean[row + i] = AFFINE ? md[i] + resid : K[i] + md[i];
+                    a.mean[row + i] = K[i] + md[i];
                     a.rstd[row + i] = rs;
                 }
             }
@@ -358,7 +372,7 @@ static const void* pick_variant(int ring, bool full) {
     if (ring == kRingBulk)
         return full ? fwd_fn<T, NV, VARLEN, kRingBulk, true, AFFINE>() : fwd_fn<T, NV, VARLEN, kRingBulk, false, AFFINE>();
     if (ring == kRingCopy) {
-        if constexpr (NV == 3 && std::is_same<T, __nv_bfloat16>::value)
+        if constexpr (NV == 3 && std::is_same<T, __nv_bfloat16>::value && !AFFINE)
             if (full) return fwd_fn<T, NV, VARLEN, kRingCopy, true, AFFINE>();
         return nullptr;
     }
