@@ -881,7 +881,7 @@ namespace {
 // piece is read back from there; narrower pieces read and write the fp32 dx once more each.
 constexpr int64_t kProbsBytes = (int64_t)128 << 20;
 constexpr int64_t kMinPiece = 2048;
-constexpr int64_t kXentSms = 152;  // the SM count the split of dx's sums is made for
+constexpr int64_t kXentPairs = 76;  // the SM pairs the split of dx's sums is made for
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
@@ -903,11 +903,11 @@ XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
     const int64_t pieces = (V + wide - 1) / wide;
     p.piece = round_up((V + pieces - 1) / pieces, kTileN);
     // dx sums over a piece's columns, dweight over the rows: with few rows the dx tiles are few
-    // and long. They are split until one is no longer than an SM's share of all the K steps (at
+    // and long. They are split until one is no longer than an SM pair's share of all the K steps (at
     // least 16 of them, below which filling the pipeline costs more).
     const int64_t dt = (D + kTileN - 1) / kTileN, mt = p.Np / kTileM, kv = p.piece / kTileK;
     const int64_t steps = mt * dt * kv + p.piece / kTileM * dt * (p.Np / kTileK);
-    const int64_t share = std::max<int64_t>(steps / kXentSms, 16);
+    const int64_t share = std::max<int64_t>(steps / kXentPairs, 16);
     p.splits = (int)std::min<int64_t>(std::max<int64_t>((kv + share - 1) / share, 1), 16);
     size_t at = kPartialsOffset;
     auto take = [&](size_t bytes) {

@@ -1,5 +1,9 @@
-// Building blocks of the tensor-core kernels: TMA tile loads, tcgen05 matrix products with
-// accumulators in tensor memory, and their descriptors.
+// Building blocks of the tensor-core kernels: TMA tile loads, tcgen05 matrix products of a CTA
+// pair (a cluster of two CTAs on neighbouring SMs, cta_group::2) with accumulators in tensor
+// memory, and their descriptors. A pair's product of M = 256 rows by N columns takes rows
+// 0..127 of A and the first N / 2 rows of B from CTA 0's shared memory and the rest from CTA 1's,
+// at the same addresses, and leaves rows 0..127 of D in CTA 0's tensor memory and the rest in
+// CTA 1's: each SM stages half of what a product of its own would need.
 #pragma once
 
 #include <cuda.h>  // CUtensorMap
@@ -9,33 +13,28 @@
 namespace adaln {
 
 // ---- mbarriers and TMA ---------------------------------------------------------------------
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// Tile load: the box of `map` at element coordinates (x, y) into shared memory. x * 2 bytes is
-// a multiple of 16 at every call (x is a multiple of 64 elements); parts of the box outside the
+// Tile load: the box of `map` at element coordinates (x, y) into this CTA's shared memory,
+// completing on an mbarrier of either CTA of the pair (a cluster address). x * 2 bytes is a
+// multiple of 16 at every call (x is a multiple of 64 elements); parts of the box outside the
 // tensor arrive as zeros and count towards the transaction bytes.
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
         "[%4];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
 
 // ---- tensor memory -------------------------------------------------------------------------
-// One warp allocates `cols` columns (a power of two >= 32) and writes the base address to shared
-// memory; the same warp gives them back.
+// One warp of each CTA of the pair allocates `cols` columns (a power of two >= 32) and writes the
+// base address to its shared memory; the same warps give them back.
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(cols)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(cols)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -71,18 +70,21 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool a_mn, bool b_
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-// D (+)= A * B over one K step of 16; issued by one thread.
+// D (+)= A * B over one K step of 16; issued by one thread of CTA 0.
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
-// Arrives on the mbarrier when every product issued by this thread so far has finished.
+// Arrives on the mbarrier at this address in both CTAs when every product issued by this thread
+// so far has finished.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
 }
 // Orders this thread's view of global memory written by earlier kernels with its TMA reads.
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }

@@ -23,9 +23,9 @@ constexpr int kAccs = 2;              // accumulator tiles in tensor memory
 constexpr int kEpiWarp = 4;           // first epilogue warp
 constexpr int kEpiWarps = 8;          // two per 32 lanes of tensor memory, half the columns each
 constexpr int kGemmThreads = (kEpiWarp + kEpiWarps) * 32;
-constexpr uint32_t kABytes = kTileM * kTileK * 2, kBBytes = kTileN * kTileK * 2;
+constexpr uint32_t kABytes = kCtaM * kTileK * 2, kBBytes = kCtaN * kTileK * 2;
 constexpr uint32_t kStageBytes = kABytes + kBBytes;
-constexpr int kGemmStages = 4;
+constexpr int kGemmStages = 6;
 constexpr size_t kGemmSmem = 1024 + (size_t)kGemmStages * kStageBytes;
 constexpr uint32_t kMnBlock = 64 * kTileK * 2;  // 64 m of all the tile's k (MN-major operands)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -137,9 +137,10 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------
-// Matrix products. A persistent CTA per SM walks its units (output tiles): warp 0 fills a ring
-// of shared-memory stages by TMA, warp 1 issues the products into one of two accumulators,
-// warps 4.. read the other one back and run the epilogue.
+// Matrix products. A persistent CTA pair on every two SMs walks its units (output tiles): warp 0
+// of each CTA fills its half of a ring of shared-memory stages by TMA (both halves complete on
+// CTA 0's barrier), warp 1 of CTA 0 issues the pair's products into one of two accumulators,
+// warps 4.. of each CTA read its rows of the other one back and run the epilogue.
 // ---------------------------------------------------------------------------------------
 struct Unit {
     const CUtensorMap* ma;
@@ -160,6 +161,8 @@ __device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decod
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_ctarank();
+    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;  // units of this pair
     const uint32_t data = (smem_addr(dyn) + 1023u) & ~1023u;
     const uint32_t full = smem_addr(bars), empty = full + 8u * kGemmStages;
     const uint32_t afull = empty + 8u * kGemmStages, aempty = afull + 8u * kAccs, drain = aempty + 8u * kAccs;
@@ -170,7 +173,7 @@ __device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decod
         }
         for (int i = 0; i < kAccs; ++i) {
             mbar_init(afull + 8u * i, 1);
-            mbar_init(aempty + 8u * i, kEpiWarps);
+            mbar_init(aempty + 8u * i, 2 * kEpiWarps);  // CTA 0's: both CTAs' epilogues
         }
         mbar_init(drain, 1);
         abort_flag = 0;
@@ -179,6 +182,7 @@ __device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decod
     if (warp == 2) tmem_alloc(smem_addr(&tmem_base), kAccs * kTileN);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // the other CTA's barriers are ready too
     tc_fence_after();
     const uint32_t tmem = tmem_base;
 
@@ -188,27 +192,26 @@ __device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decod
             int s = 0;
             uint32_t lap = 0;
             bool live = true;
-            for (int64_t u = blockIdx.x; live && u < units; u += gridDim.x) {
+            for (int64_t u = first; live && u < units; u += step) {
                 const Unit t = decode(u);
                 for (int i = 0; i < t.iters; ++i) {
                     if (lap > 0 && !mbar_wait_bounded(empty + 8u * s, (lap - 1) & 1u, &abort_flag)) {
                         live = false;
                         break;
                     }
-                    const uint32_t bar = full + 8u * s, as = data + s * kStageBytes, bs = as + kABytes;
-                    mbar_arrive_expect_tx(bar, kStageBytes);
+                    const uint32_t bar = cluster_map(full + 8u * s, 0), as = data + s * kStageBytes, bs = as + kABytes;
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8u * s, 2 * kStageBytes);
+                    const int m0 = (int)t.m0 + (int)rank * kCtaM, n0 = (int)t.n0 + (int)rank * kCtaN;
                     const int ka = (int)(t.k0 + (int64_t)i * kTileK), kb = (int)(t.kb0 + (int64_t)i * kTileK);
                     if (t.a_mn) {
-                        for (int j = 0; j < kTileM / 64; ++j)
-                            tma_load(as + j * kMnBlock, t.ma, (int)t.m0 + 64 * j, ka, bar);
+                        for (int j = 0; j < kCtaM / 64; ++j) tma_load(as + j * kMnBlock, t.ma, m0 + 64 * j, ka, bar);
                     } else {
-                        tma_load(as, t.ma, ka, (int)t.m0, bar);
+                        tma_load(as, t.ma, ka, m0, bar);
                     }
                     if (t.b_mn) {
-                        for (int j = 0; j < kTileN / 64; ++j)
-                            tma_load(bs + j * kMnBlock, t.mb, (int)t.n0 + 64 * j, kb, bar);
+                        for (int j = 0; j < kCtaN / 64; ++j) tma_load(bs + j * kMnBlock, t.mb, n0 + 64 * j, kb, bar);
                     } else {
-                        tma_load(bs, t.mb, kb, (int)t.n0, bar);
+                        tma_load(bs, t.mb, kb, n0, bar);
                     }
                     if (++s == kGemmStages) {
                         s = 0;
@@ -216,9 +219,9 @@ __device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decod
                     }
                 }
             }
-            // After a timeout, copies may still be on their way into this CTA's memory: give
-            // each stage's last one a further bounded wait.
-            if (*(volatile int*)&abort_flag) {
+            // After a timeout, copies may still be on their way into the pair's memory: CTA 0 gives
+            // each stage's last ones a further bounded wait, CTA 1 meets it at the cluster barrier.
+            if (rank == 0 && *(volatile int*)&abort_flag) {
                 volatile int never = 0;
                 for (int q = 0; q < kGemmStages; ++q) {
                     if (q >= s && lap == 0) continue;
@@ -228,20 +231,21 @@ __device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decod
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             int s = 0, acc = 0;
             uint32_t lap = 0, alap = 0;
             bool live = true;
-            for (int64_t u = blockIdx.x; live && u < units; u += gridDim.x) {
+            for (int64_t u = first; live && u < units; u += step) {
                 const Unit t = decode(u);
                 const uint32_t idesc = mma_desc(kTileM, kTileN, t.a_mn, t.b_mn);
                 // 16 k: 32 bytes of a K-major row, 16 rows of an MN-major tile.
                 const uint32_t ak = (t.a_mn ? 2048u : 32u) >> 4, bk = (t.b_mn ? 2048u : 32u) >> 4;
-                if (alap > 0 && !mbar_wait_bounded(aempty + 8u * acc, (alap - 1) & 1u, &abort_flag)) break;
+                if (alap > 0 && !mbar_wait_cluster_bounded(aempty + 8u * acc, (alap - 1) & 1u, &abort_flag))
+                    break;
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)acc * kTileN;
                 for (int i = 0; i < t.iters; ++i) {
-                    if (!mbar_wait_bounded(full + 8u * s, lap & 1u, &abort_flag)) {
+                    if (!mbar_wait_cluster_bounded(full + 8u * s, lap & 1u, &abort_flag)) {
                         live = false;
                         break;
                     }
@@ -274,17 +278,17 @@ __device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decod
         const int q = warp & 3, half = (warp - kEpiWarp) >> 2;
         int acc = 0;
         uint32_t alap = 0;
-        for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        for (int64_t u = first; u < units; u += step) {
             const Unit t = decode(u);
             bool ok = mbar_wait_bounded(afull + 8u * acc, alap & 1u, &abort_flag);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_fence_after();
             const uint32_t src = tmem + (uint32_t)acc * kTileN + (uint32_t)half * (kTileN / 2) + ((uint32_t)q << 21);
-            epilogue(t, src, q * 32 + lane, half, [&]() {
+            epilogue(t, src, (int)rank * kCtaM + q * 32 + lane, half, [&]() {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(aempty + 8u * acc);
+                if (lane == 0) mbar_arrive_remote(cluster_map(aempty + 8u * acc, 0));
             });
             if (++acc == kAccs) {
                 acc = 0;
@@ -295,14 +299,17 @@ __device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decod
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // no product, copy or arrival of the pair is left
     tc_fence_after();
     if (warp == 2) tmem_free(tmem, kAccs * kTileN);
+    __syncwarp();
+    cluster_sync();
     if (tid == 0 && abort_flag) atomicOr(status, kErrTimeout);
 }
 
 // The tile's logits, as row statistics (PROBS false) or as dz (PROBS true).
 template <bool PROBS>
-__global__ void __launch_bounds__(kGemmThreads) logits_kernel(const __grid_constant__ CUtensorMap mx,
+__global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_constant__ CUtensorMap mx,
                                                               const __grid_constant__ CUtensorMap mw,
                                                               const LogitsArgs a) {
     pdl_begin();
@@ -396,7 +403,7 @@ __global__ void __launch_bounds__(kGemmThreads) logits_kernel(const __grid_const
 
 // dx += dz W and dweight = dz^T x of one piece of the vocabulary, as one list of units: dx
 // tiles, each in `splits` parts of the piece's columns, then dweight tiles.
-__global__ void __launch_bounds__(kGemmThreads) grad_kernel(const __grid_constant__ CUtensorMap mp,
+__global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_constant__ CUtensorMap mp,
                                                             const __grid_constant__ CUtensorMap mw,
                                                             const __grid_constant__ CUtensorMap mx,
                                                             const __grid_constant__ CUtensorMap mpt,
@@ -580,21 +587,21 @@ cudaError_t launch_logits(const LogitsArgs& args, bool probs, const void* xp, co
                           cudaStream_t stream) {
     LogitsArgs a = args;
     CUtensorMap mx, mw;
-    if (!tile_map(&mx, xp, a.Np, a.D, a.D, kTileM) || !tile_map(&mw, weight, a.V, a.D, a.D, kTileN))
+    if (!tile_map(&mx, xp, a.Np, a.D, a.D, kCtaM) || !tile_map(&mw, weight, a.V, a.D, a.D, kCtaN))
         return cudaErrorInvalidValue;
     const void* fn = probs ? reinterpret_cast<const void*>(&logits_kernel<true>)
                            : reinterpret_cast<const void*>(&logits_kernel<false>);
     if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) return e;
     const int64_t units = (a.Np / kTileM) * ((a.v1 - a.v0 + kTileN - 1) / kTileN);
     void* params[] = {&mx, &mw, &a};
-    return launch_dependent(fn, dim3(cap(units, sms)), dim3(kGemmThreads), params, kGemmSmem, stream);
+    return launch_dependent(fn, dim3(2 * cap(units, sms / 2)), dim3(kGemmThreads), params, kGemmSmem, stream, 2);
 }
 
 cudaError_t launch_grad(const GradArgs& args, const void* probs, int64_t ldp, const void* xp, const void* weight,
                         int sms, cudaStream_t stream) {
     GradArgs a = args;
     CUtensorMap mp, mw, mx, mpt;
-    if (!tile_map(&mp, probs, a.Np, ldp, ldp, kTileM) || !tile_map(&mw, weight, a.V, a.D, a.D, kTileK) ||
+    if (!tile_map(&mp, probs, a.Np, ldp, ldp, kCtaM) || !tile_map(&mw, weight, a.V, a.D, a.D, kTileK) ||
         !tile_map(&mx, xp, a.Np, a.D, a.D, kTileK) || !tile_map(&mpt, probs, a.Np, ldp, ldp, kTileK))
         return cudaErrorInvalidValue;
     const void* fn = reinterpret_cast<const void*>(&grad_kernel);
@@ -603,7 +610,7 @@ cudaError_t launch_grad(const GradArgs& args, const void* probs, int64_t ldp, co
     const int64_t units = (a.dxacc ? a.Np / kTileM * dt * a.splits : 0) +
                           (a.dweight ? (a.v1 - a.v0 + kTileM - 1) / kTileM * dt : 0);
     void* params[] = {&mp, &mw, &mx, &mpt, &a};
-    return launch_dependent(fn, dim3(cap(units, sms)), dim3(kGemmThreads), params, kGemmSmem, stream);
+    return launch_dependent(fn, dim3(2 * cap(units, sms / 2)), dim3(kGemmThreads), params, kGemmSmem, stream, 2);
 }
 
 cudaError_t launch_lse(const LseArgs& args, int sms, cudaStream_t stream) {

@@ -8,8 +8,9 @@
 
 namespace adaln {
 
-// Output tile of a matrix product and its K step.
-constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
+// Output tile of a CTA pair's matrix product and its K step; a CTA's share of the operands.
+constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
+constexpr int kCtaM = kTileM / 2, kCtaN = kTileN / 2;
 constexpr int kPackThreads = 256;
 constexpr int kPackCtas = 304;  // two per SM: every CTA also counts the rows before its own
 
