@@ -890,10 +890,10 @@ struct XentPlan {
     int64_t tiles;       // forward: column tiles
     int64_t piece;       // backward: columns of a piece (a multiple of kTileN)
     int splits;          // backward: parts of dx's sum over a piece
-    size_t nact, row, tgt, f0, f1, f2, xp, big, dxacc, bytes;  // workspace offsets
+    size_t nact, row, tgt, f0, f1, f2, f3, xp, big, dxacc, bytes;  // workspace offsets
 };
 
-// Workspace: [header | status words | nact | row | tgt | three row arrays | packed x |
+// Workspace: [header | status words | nact | row | tgt | four row arrays | packed x |
 // partials (forward) or dz (backward) | dx in fp32 (backward)].
 XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
     XentPlan p{};
@@ -922,6 +922,7 @@ XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
     p.f0 = take(rows * 4);
     p.f1 = take(rows * 4);
     p.f2 = take(rows * 4);
+    p.f3 = take(rows * 4);
     p.xp = take(rows * (size_t)D * 2);
     p.big = take(bwd ? rows * (size_t)p.piece * 2 : rows * (size_t)p.tiles * 2 * sizeof(float2));
     if (bwd) p.dxacc = take(rows * (size_t)p.splits * (size_t)D * 4);
@@ -1053,6 +1054,7 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
         g.row_lse2 = k.row_lse2;
         g.row_gs = k.row_gs;
         g.row_gt = k.row_gt;
+        g.row_lo = at<float>(workspace, p.f3);
         g.probs = at<__nv_bfloat16>(workspace, p.big);
         g.ldp = p.piece;
         g.status = k.status + ctas;
@@ -1066,6 +1068,9 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
         d.nact = k.nact;
         d.dxacc = dx ? at<float>(workspace, p.dxacc) : nullptr;
         d.dweight = static_cast<__nv_bfloat16*>(dweight);
+        d.xp = k.xp;
+        d.tgt = k.tgt;
+        d.row_lo = g.row_lo;
         d.status = g.status;
         d.Np = p.Np;
         d.D = D;
@@ -1080,6 +1085,9 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
     d.nact = k.nact;
     d.row = k.row;
     d.dxacc = at<float>(workspace, p.dxacc);
+    d.weight = weight;
+    d.tgt = k.tgt;
+    d.row_lo = at<float>(workspace, p.f3);
     d.dx = dx;
     d.N = N;
     d.Np = p.Np;

@@ -522,6 +522,11 @@ __device__ __forceinline__ float2 p_get(f2r a) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(a));
     return v;
 }
+__device__ __forceinline__ f2r p_make(float lo, float hi) {
+    f2r d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
 __device__ __forceinline__ float p_hsum(f2r a) {
     const float2 v = p_get(a);
     return v.x + v.y;

@@ -29,10 +29,28 @@ constexpr int kGemmStages = 6;
 constexpr size_t kGemmSmem = 1024 + (size_t)kGemmStages * kStageBytes;
 constexpr uint32_t kMnBlock = 64 * kTileK * 2;  // 64 m of all the tile's k (MN-major operands)
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kHits = 8;              // rows a word whose rounded-off part dweight still takes
 
 #define ADALN_IN_LOSS(cond) ADALN_IN(::adaln::kDbgLoss, cond)
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+// 2^x, results below 2^-126 as 0.
+__device__ __forceinline__ float exp2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The epilogue warps' own barrier; true if `ok` is, in all of them.
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)ok), "n"(kEpiWarps * 32)
+        : "memory");
+    return r != 0;
+}
 
 // ---------------------------------------------------------------------------------------
 // Packing: CTA b counts the rows that carry a loss before its range, then places its own
@@ -154,8 +172,12 @@ struct Unit {
     int64_t slot;       // dx: which part of the K range
 };
 
-template <class Decode, class Epilogue>
-__device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decode decode, Epilogue epilogue) {
+// decode(u): unit u. prologue(unit): run by the epilogue threads while the unit's products are
+// still under way. epilogue(unit, accumulator, row of the tile, half of its columns, release):
+// calls release() when it has read the accumulator.
+template <class Decode, class Prologue, class Epilogue>
+__device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decode decode, Prologue prologue,
+                                          Epilogue epilogue) {
     extern __shared__ uint4 dyn[];
     __shared__ __align__(8) uint64_t bars[2 * kGemmStages + 2 * kAccs + 1];
     __shared__ uint32_t tmem_base;
@@ -280,9 +302,9 @@ __device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decod
         uint32_t alap = 0;
         for (int64_t u = first; u < units; u += step) {
             const Unit t = decode(u);
-            bool ok = mbar_wait_bounded(afull + 8u * acc, alap & 1u, &abort_flag);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
+            prologue(t);
+            // All epilogue warps go on or none: they meet at barriers of their own.
+            if (!epilogue_all(mbar_wait_bounded(afull + 8u * acc, alap & 1u, &abort_flag))) break;
             tc_fence_after();
             const uint32_t src = tmem + (uint32_t)acc * kTileN + (uint32_t)half * (kTileN / 2) + ((uint32_t)q << 21);
             epilogue(t, src, (int)rank * kCtaM + q * 32 + lane, half, [&]() {
@@ -325,13 +347,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
         t.iters = (int)((a.D + kTileK - 1) / kTileK);
         return t;
     };
-    gemm_loop(mt * nt, a.status, decode, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
+    gemm_loop(mt * nt, a.status, decode, [](const Unit&) {}, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
         const int64_t row = t.m0 + r;
         const bool in = ADALN_IN_LOSS(row < a.Np);
         const int tgt = in ? a.tgt[row] : -1;
         const int64_t c0 = t.n0 + half * (kTileN / 2);
-        float mx_ = neg_inf(), sum = 0.0f;
-        float lse2 = 0.0f, gs = 0.0f, gt = 0.0f;
+        const f2r l2e = p_splat(kLog2e);
+        [[maybe_unused]] float top = neg_inf(), sum = 0.0f;
+        [[maybe_unused]] float lse2 = 0.0f, gs = 0.0f, gt = 0.0f;
         if constexpr (PROBS) {
             if (in) {
                 lse2 = a.row_lse2[row];
@@ -346,46 +369,60 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
             tmem_ld32(src + c, v);
             const int64_t col = c0 + c;
             const int hit = (int64_t)tgt >= col && (int64_t)tgt < col + 32 ? (int)(tgt - col) : -1;
+            float zt = 0.0f;
+            if (hit >= 0) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) zt = j == hit ? v[j] : zt;
+            }
             if constexpr (!PROBS) {
                 if (col + 32 > a.V) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (col + j >= a.V) v[j] = neg_inf();
                 }
-                if (hit >= 0) {
-                    float z = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) z = j == hit ? v[j] : z;
-                    if (in) a.zt[row] = z;
-                }
-                float m = mx_;
+                if (hit >= 0 && in) a.zt[row] = zt;
+                float m = top;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) m = fmaxf(m, v[j]);
                 // A chunk with no finite value at all adds nothing (and NaN is kept below).
                 const float mm = m == neg_inf() ? 0.0f : m;
-                const float m2 = mm * kLog2e;
-                float s = 0.0f;
+                const f2r m2 = p_splat(-mm * kLog2e);
+                f2r s[2] = {kPairZero, kPairZero};
 #pragma unroll
-                for (int j = 0; j < 32; ++j) s += exp2f(fmaf(v[j], kLog2e, -m2));
-                sum = sum * exp2f((mx_ - mm) * kLog2e) + s;
-                mx_ = m;
+                for (int j = 0; j < 16; ++j) {
+                    const float2 e = p_get(p_fma(p_make(v[2 * j], v[2 * j + 1]), l2e, m2));
+                    s[j & 1] = p_add(s[j & 1], p_make(exp2_ftz(e.x), exp2_ftz(e.y)));
+                }
+                sum = sum * exp2_ftz((top - mm) * kLog2e) + p_hsum(p_add(s[0], s[1]));
+                top = m;
             } else {
+                const f2r nl = p_splat(-lse2), g2 = p_splat(gs);
                 uint32_t w[16];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float p = exp2f(fmaf(v[j], kLog2e, -lse2)) * gs;
-                    if (j == hit) p -= gt;
-                    v[j] = p;
+                for (int j = 0; j < 16; ++j) {
+                    const float2 e = p_get(p_fma(p_make(v[2 * j], v[2 * j + 1]), l2e, nl));
+                    const float2 p = p_get(p_mul(p_make(exp2_ftz(e.x), exp2_ftz(e.y)), g2));
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(p.y), "f"(p.x));
+                }
+                if (hit >= 0) {
+                    // The target's dz, often most of the row's and of its word's gradient: what its
+                    // rounding leaves off is kept and added to both in fp32.
+                    const float d = exp2_ftz(fmaf(zt, kLog2e, -lse2)) * gs - gt;
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(d);
+                    const uint32_t bits = __bfloat16_as_ushort(hi);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j == hit >> 1) w[j] = hit & 1 ? (w[j] & 0xFFFFu) | bits << 16 : (w[j] & 0xFFFF0000u) | bits;
+                    if (in) a.row_lo[row] = d - __bfloat162float(hi);
                 }
                 // Columns past the vocabulary and rows past the packed ones are operands too: zeros.
                 if (col + 32 > a.V || row >= nact) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (col + j >= a.V || row >= nact) v[j] = 0.0f;
+                    for (int j = 0; j < 16; ++j) {
+                        if (col + 2 * j >= a.V || row >= nact) w[j] = 0u;
+                        else if (col + 2 * j + 1 >= a.V) w[j] &= 0xFFFFu;
+                    }
                 }
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
                 if (in && ADALN_IN_LOSS(col - a.v0 + 32 <= a.ldp)) {
                     uint4* dst = reinterpret_cast<uint4*>(a.probs + row * a.ldp + (col - a.v0));
 #pragma unroll
@@ -396,7 +433,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
         release();
         if constexpr (!PROBS) {
             const int64_t part = (t.n0 - a.v0) / kTileN * 2 + half;
-            if (in) a.parts[part * a.Np + row] = make_float2(mx_, sum);
+            if (in) a.parts[part * a.Np + row] = make_float2(top, sum);
         }
     });
 }
@@ -442,7 +479,41 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
         }
         return t;
     };
-    gemm_loop(ndx + ndw, a.status, decode, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
+    // dweight: the packed rows whose target is a word of this CTA's half of the tile, at most kHits
+    // a word, in row order. Rounding dz left row_lo off each; words with more rows than that keep
+    // it off, the rounding errors of many rows averaging out.
+    __shared__ int32_t hits[kCtaM], hit_row[kCtaM][kHits];
+    const int64_t rank0 = (int64_t)cluster_ctarank() * kCtaM;
+    auto prologue = [&](const Unit& t) {
+        if (t.kind != 2) return;
+        const int e = (int)threadIdx.x - kEpiWarp * 32;
+        epilogue_all(true);  // the last unit's lists have been read
+        if (e < kCtaM) hits[e] = 0;
+        epilogue_all(true);
+        const int64_t w0 = a.v0 + t.m0 + rank0;
+        for (int64_t i = e; i < nact; i += kEpiWarps * 32) {
+            const int64_t w = ADALN_IN_LOSS(i < a.Np) ? a.tgt[i] - w0 : -1;
+            if (w < 0 || w >= kCtaM) continue;
+            const int k = atomicAdd(&hits[w], 1);
+            if (k < kHits) hit_row[w][k] = (int32_t)i;
+        }
+        epilogue_all(true);
+        if (e < kCtaM) {
+            const int n = hits[e];
+            if (n > kHits) {
+                hits[e] = 0;
+            } else {
+                for (int i = 1; i < n; ++i) {  // the order in which they came is the threads'
+                    const int32_t r = hit_row[e][i];
+                    int k = i;
+                    for (; k > 0 && hit_row[e][k - 1] > r; --k) hit_row[e][k] = hit_row[e][k - 1];
+                    hit_row[e][k] = r;
+                }
+            }
+        }
+        epilogue_all(true);
+    };
+    gemm_loop(ndx + ndw, a.status, decode, prologue, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
         const int64_t row = t.m0 + r;
         const int64_t c0 = t.n0 + half * (kTileN / 2);
 #pragma unroll 1
@@ -471,6 +542,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
                 }
             } else {
                 const int64_t word = a.v0 + row;
+                const int n = hits[r - rank0];
+                for (int h = 0; h < n; ++h) {
+                    const int64_t i = hit_row[r - rank0][h];
+                    if (!ADALN_IN_LOSS(i >= 0 && i < nact)) continue;
+                    const f2r lo = p_splat(a.row_lo[i]);
+                    const uint4* xr = reinterpret_cast<const uint4*>(a.xp) + (i * a.D + col) / 8;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        if (col + j >= a.D) continue;
+                        f2r x[4];
+                        Io<__nv_bfloat16>::unpackp(xr[j / 8], x);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 s = p_get(p_fma(lo, x[k], p_make(v[j + 2 * k], v[j + 2 * k + 1])));
+                            v[j + 2 * k] = s.x;
+                            v[j + 2 * k + 1] = s.y;
+                        }
+                    }
+                }
                 uint4* dst = reinterpret_cast<uint4*>(a.dweight + word * a.D + col);
 #pragma unroll
                 for (int j = 0; j < 32; j += 8) {
@@ -521,7 +611,8 @@ __global__ void __launch_bounds__(256) lse_kernel(const LseArgs a) {
     }
 }
 
-// dx of the packed rows: the parts added in order, rounded once, back to the rows' places.
+// dx of the packed rows: the parts added in order, then what rounding dz of the target left off,
+// rounded once, back to the rows' places.
 __global__ void __launch_bounds__(256) dx_kernel(const DxArgs a) {
     pdl_begin();
     const int64_t nact = *a.nact, vecs = a.D / 8;
@@ -534,6 +625,17 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxArgs a) {
             const float4 lo = src[0], hi = src[1];
             s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
             s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
+        }
+        if (ADALN_IN_LOSS(p < a.Np)) {
+            const float lo = a.row_lo[p];
+            f2r t[4];
+            Io<__nv_bfloat16>::unpackp(ld_keep(reinterpret_cast<const uint4*>(a.weight) + a.tgt[p] * vecs + v), t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = p_get(t[j]);
+                s[2 * j] = fmaf(lo, f.x, s[2 * j]);
+                s[2 * j + 1] = fmaf(lo, f.y, s[2 * j + 1]);
+            }
         }
         uint32_t w[4];
 #pragma unroll

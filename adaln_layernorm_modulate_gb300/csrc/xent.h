@@ -43,6 +43,7 @@ struct LogitsArgs {
     const float* row_lse2;  // dz
     const float* row_gs;
     const float* row_gt;
+    float* row_lo;          // dz: [Np], what rounding dz of the target left off
     __nv_bfloat16* probs;   // dz [Np, ldp]
     int64_t ldp;
     uint32_t* status;
@@ -53,6 +54,9 @@ struct GradArgs {
     const int32_t* nact;
     float* dxacc;           // [splits][Np][D] fp32, or null
     __nv_bfloat16* dweight; // [V, D], or null
+    const void* xp;
+    const int32_t* tgt;
+    const float* row_lo;
     uint32_t* status;
     int64_t Np, D, V, v0, v1;
     int splits;             // parts of dx's K range
@@ -73,6 +77,9 @@ struct DxArgs {
     const int32_t* nact;
     const int32_t* row;
     const float* dxacc;
+    const void* weight;
+    const int32_t* tgt;
+    const float* row_lo;
     void* dx;
     int64_t N, Np, D;
     int splits;
