@@ -86,6 +86,12 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         "h"((uint16_t)3)
         : "memory");
 }
+// 32 bytes to a 32-byte aligned address: a whole sector a lane.
+__device__ __forceinline__ void st_sector(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
 // Orders this thread's view of global memory written by earlier kernels with its TMA reads.
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
 

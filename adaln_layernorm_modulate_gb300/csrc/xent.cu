@@ -174,9 +174,10 @@ struct Unit {
 
 // decode(u): unit u. prologue(unit): run by the epilogue threads while the unit's products are
 // still under way. epilogue(unit, accumulator, row of the tile, half of its columns, release):
-// calls release() when it has read the accumulator.
-template <class Decode, class Prologue, class Epilogue>
-__device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decode decode, Prologue prologue,
+// calls release() when it has read the accumulator. units() is called, and global memory first
+// read, after the kernel ahead has finished; barriers and tensor memory are set up before.
+template <class Units, class Decode, class Prologue, class Epilogue>
+__device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode decode, Prologue prologue,
                                           Epilogue epilogue) {
     extern __shared__ uint4 dyn[];
     __shared__ __align__(8) uint64_t bars[2 * kGemmStages + 2 * kAccs + 1];
@@ -207,6 +208,8 @@ __device__ __forceinline__ void gemm_loop(int64_t units, uint32_t* status, Decod
     cluster_sync();  // the other CTA's barriers are ready too
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    pdl_wait();
+    const int64_t units = count();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -334,10 +337,14 @@ template <bool PROBS>
 __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_constant__ CUtensorMap mx,
                                                               const __grid_constant__ CUtensorMap mw,
                                                               const LogitsArgs a) {
-    pdl_begin();
-    const int64_t nact = *a.nact;
-    const int64_t mt = (nact + kTileM - 1) / kTileM;
+    pdl_trigger();
+    int64_t nact = 0, mt = 0;
     const int64_t nt = (a.v1 - a.v0 + kTileN - 1) / kTileN;
+    auto count = [&]() {
+        nact = *a.nact;
+        mt = (nact + kTileM - 1) / kTileM;
+        return mt * nt;
+    };
     auto decode = [&](int64_t u) {
         Unit t{};
         t.ma = &mx;
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
         t.iters = (int)((a.D + kTileK - 1) / kTileK);
         return t;
     };
-    gemm_loop(mt * nt, a.status, decode, [](const Unit&) {}, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
+    gemm_loop(count, a.status, decode, [](const Unit&) {}, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
         const int64_t row = t.m0 + r;
         const bool in = ADALN_IN_LOSS(row < a.Np);
         const int tgt = in ? a.tgt[row] : -1;
@@ -424,9 +431,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                     }
                 }
                 if (in && ADALN_IN_LOSS(col - a.v0 + 32 <= a.ldp)) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.probs + row * a.ldp + (col - a.v0));
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                    __nv_bfloat16* dst = a.probs + row * a.ldp + (col - a.v0);
+                    st_sector(dst, w);
+                    st_sector(dst + 16, w + 8);
                 }
             }
         }
@@ -445,13 +452,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
                                                             const __grid_constant__ CUtensorMap mx,
                                                             const __grid_constant__ CUtensorMap mpt,
                                                             const GradArgs a) {
-    pdl_begin();
-    const int64_t nact = *a.nact;
-    const int64_t mt = (nact + kTileM - 1) / kTileM;
+    pdl_trigger();
+    int64_t nact = 0, mt = 0, ndx = 0;
     const int64_t dt = (a.D + kTileN - 1) / kTileN;
     const int64_t kv = (a.v1 - a.v0 + kTileK - 1) / kTileK;  // K steps of dx
     const int64_t vt = (a.v1 - a.v0 + kTileM - 1) / kTileM;
-    const int64_t ndx = a.dxacc ? mt * dt * a.splits : 0, ndw = a.dweight ? vt * dt : 0;
+    auto count = [&]() {
+        nact = *a.nact;
+        mt = (nact + kTileM - 1) / kTileM;
+        ndx = a.dxacc ? mt * dt * a.splits : 0;
+        return ndx + (a.dweight ? vt * dt : 0);
+    };
     auto decode = [&](int64_t u) {
         Unit t{};
         t.b_mn = true;
@@ -462,8 +473,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
             const int64_t k0 = t.slot * kv / a.splits, k1 = (t.slot + 1) * kv / a.splits;
             t.ma = &mp;
             t.mb = &mw;
-            t.m0 = w % mt * kTileM;
-            t.n0 = w / mt * kTileN;
+            // dz is read once, by the units of all columns of dx side by side.
+            t.m0 = w / dt * kTileM;
+            t.n0 = w % dt * kTileN;
             t.k0 = k0 * kTileK;
             t.kb0 = a.v0 + t.k0;
             t.iters = (int)(k1 - k0);
@@ -513,7 +525,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
         }
         epilogue_all(true);
     };
-    gemm_loop(ndx + ndw, a.status, decode, prologue, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
+    gemm_loop(count, a.status, decode, prologue, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
         const int64_t row = t.m0 + r;
         const int64_t c0 = t.n0 + half * (kTileN / 2);
 #pragma unroll 1
@@ -561,15 +573,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
                         }
                     }
                 }
-                uint4* dst = reinterpret_cast<uint4*>(a.dweight + word * a.D + col);
+                __nv_bfloat16* dst = a.dweight + word * a.D + col;
+                uint32_t w[16];
 #pragma unroll
-                for (int j = 0; j < 32; j += 8) {
-                    if (word >= a.v1 || col + j >= a.D || !ADALN_IN_LOSS(word < a.V)) continue;
-                    uint32_t w[4];
+                for (int j = 0; j < 16; ++j)
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
+                if (word < a.v1 && ADALN_IN_LOSS(word < a.V)) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[j + 2 * i + 1]), "f"(v[j + 2 * i]));
-                    dst[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int j = 0; j < 32; j += 16) {
+                        if (a.sectors) {  // D is a multiple of 16: rows are whole sectors
+                            if (col + j < a.D) st_sector(dst + j, w + j / 2);
+                            continue;
+                        }
+#pragma unroll
+                        for (int i = j; i < j + 16; i += 8)
+                            if (col + i < a.D)
+                                *reinterpret_cast<uint4*>(dst + i) =
+                                    make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]);
+                    }
                 }
             }
         }
@@ -577,34 +598,45 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
     });
 }
 
-// Joins a row's partial (max, sum exp) in a fixed order: 8 threads a row, each a run of parts,
-// then the 8 in order. 32 rows a CTA, so that a warp reads 32 rows' parts side by side.
-__global__ void __launch_bounds__(256) lse_kernel(const LseArgs a) {
+// Joins a row's partial (max, sum exp) in a fixed order: 32 threads a row, each a run of parts
+// (its maximum first, then the sums taken to it, so that neither waits for the other's chain),
+// then the 32 in order. 32 rows a CTA, so that a warp reads 32 rows' parts side by side.
+__global__ void __launch_bounds__(1024) lse_kernel(const LseArgs a) {
     pdl_begin();
-    __shared__ float2 red[8][32];
+    __shared__ float2 red[32][33];
     const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int64_t nact = *a.nact;
-    auto join = [](float2 p, float2 q) {
-        const float m = fmaxf(p.x, q.x), mm = m == neg_inf() ? 0.0f : m;
-        return make_float2(m, p.y * exp2f((p.x - mm) * kLog2e) + q.y * exp2f((q.x - mm) * kLog2e));
-    };
     for (int64_t t = blockIdx.x; t * 32 < nact; t += gridDim.x) {
         const int64_t row = t * 32 + lane;
-        float2 acc = make_float2(neg_inf(), 0.0f);
-        if (row < nact) {
-            const int64_t p0 = (int64_t)g * a.nparts / 8, p1 = (int64_t)(g + 1) * a.nparts / 8;
-            for (int64_t p = p0; p < p1; ++p)
-                if (ADALN_IN_LOSS(row < a.Np)) acc = join(acc, a.parts[p * a.Np + row]);
+        const int64_t p0 = (int64_t)g * a.nparts / 32, p1 = (int64_t)(g + 1) * a.nparts / 32;
+        float m = neg_inf(), s = 0.0f;
+        if (row < nact && ADALN_IN_LOSS(row < a.Np)) {
+            const float2* part = a.parts + row;
+#pragma unroll 4
+            for (int64_t p = p0; p < p1; ++p) m = fmaxf(m, part[p * a.Np].x);
+            const float mm = m == neg_inf() ? 0.0f : m;
+#pragma unroll 4
+            for (int64_t p = p0; p < p1; ++p) {
+                const float2 q = part[p * a.Np];
+                s += q.y * exp2_ftz((q.x - mm) * kLog2e);
+            }
         }
-        red[g][lane] = acc;
+        red[g][lane] = make_float2(m, s);
         __syncthreads();
-        if (g == 0 && row < nact) {
-            for (int i = 1; i < 8; ++i) acc = join(acc, red[i][lane]);
-            const float lse = acc.x + logf(acc.y);
-            const int64_t r = a.row[row];
+        // Warp g joins row g of the 32: every lane a part, the same maximum, sums in a fixed tree.
+        const float2 q = red[lane][g];
+        m = q.x;
+        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const float mm = m == neg_inf() ? 0.0f : m;
+        s = q.y * exp2_ftz((q.x - mm) * kLog2e);
+        for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        const int64_t mine = t * 32 + g;
+        if (lane == 0 && mine < nact && ADALN_IN_LOSS(mine < a.Np)) {
+            const float lse = m + logf(s);
+            const int64_t r = a.row[mine];
             if (ADALN_IN_LOSS(r >= 0 && r < a.N)) {
                 a.lse[r] = lse;
-                a.loss[r] = lse - a.zt[row];
+                a.loss[r] = lse - a.zt[mine];
             }
         }
         __syncthreads();
@@ -708,6 +740,7 @@ cudaError_t launch_grad(const GradArgs& args, const void* probs, int64_t ldp, co
         return cudaErrorInvalidValue;
     const void* fn = reinterpret_cast<const void*>(&grad_kernel);
     if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) return e;
+    a.sectors = a.D % 16 == 0 && reinterpret_cast<uintptr_t>(a.dweight) % 32 == 0;
     const int64_t dt = (a.D + kTileN - 1) / kTileN;
     const int64_t units = (a.dxacc ? a.Np / kTileM * dt * a.splits : 0) +
                           (a.dweight ? (a.v1 - a.v0 + kTileM - 1) / kTileM * dt : 0);
@@ -718,8 +751,8 @@ cudaError_t launch_grad(const GradArgs& args, const void* probs, int64_t ldp, co
 cudaError_t launch_lse(const LseArgs& args, int sms, cudaStream_t stream) {
     LseArgs a = args;
     void* params[] = {&a};
-    return launch_dependent(reinterpret_cast<const void*>(&lse_kernel), dim3(cap(a.Np / 32, 8 * (int64_t)sms)),
-                            dim3(256), params, 0, stream);
+    return launch_dependent(reinterpret_cast<const void*>(&lse_kernel), dim3(cap(a.Np / 32, 2 * (int64_t)sms)),
+                            dim3(1024), params, 0, stream);
 }
 
 cudaError_t launch_dx(const DxArgs& args, int sms, cudaStream_t stream) {
