@@ -891,10 +891,11 @@ struct XentPlan {
     int64_t tiles;       // forward: column tiles
     int64_t piece;       // backward: columns of a piece (a multiple of kTileN)
     int splits;          // backward: parts of dx's sum over a piece
-    size_t nact, row, tgt, f0, f1, f2, f3, xp, big, dxacc, bytes;  // workspace offsets
+    size_t nact, row, tgt, f0, f1, f2, f3, hits, words, xp, big, dxacc, bytes;  // workspace offsets
 };
 
-// Workspace: [header | status words | nact | row | tgt | four row arrays | packed x |
+// Workspace: [header | status words | nact | row | tgt | four row arrays | rows of each word as
+// a target (backward) | packed x |
 // partials (forward) or dz (backward) | dx in fp32 (backward)].
 XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
     XentPlan p{};
@@ -924,6 +925,8 @@ XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
     p.f1 = take(rows * 4);
     p.f2 = take(rows * 4);
     p.f3 = take(rows * 4);
+    if (bwd) p.hits = take((size_t)V * 4);
+    if (bwd) p.words = take((size_t)V * kHits * 4);
     p.xp = take(rows * (size_t)D * 2);
     p.big = take(bwd ? rows * (size_t)p.piece * 2 : rows * (size_t)p.tiles * 2 * sizeof(float2));
     if (bwd) p.dxacc = take(rows * (size_t)p.splits * (size_t)D * 4);
@@ -1046,6 +1049,7 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
     k.row_gs = at<float>(workspace, p.f1);
     k.row_gt = at<float>(workspace, p.f2);
     k.dx = dx;
+    k.word_hits = dweight ? at<int32_t>(workspace, p.hits) : nullptr;
     const int ctas = pack_ctas(N);
     if (int rc = launched(launch_pack(k, ctas, stream))) return rc;
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
@@ -1056,6 +1060,8 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
         g.row_gs = k.row_gs;
         g.row_gt = k.row_gt;
         g.row_lo = at<float>(workspace, p.f3);
+        g.word_hits = k.word_hits;
+        g.word_rows = at<int32_t>(workspace, p.words);
         g.probs = at<__nv_bfloat16>(workspace, p.big);
         g.ldp = p.piece;
         g.status = k.status + ctas;
@@ -1070,7 +1076,8 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
         d.dxacc = dx ? at<float>(workspace, p.dxacc) : nullptr;
         d.dweight = static_cast<__nv_bfloat16*>(dweight);
         d.xp = k.xp;
-        d.tgt = k.tgt;
+        d.word_hits = g.word_hits;
+        d.word_rows = g.word_rows;
         d.row_lo = g.row_lo;
         d.status = g.status;
         d.Np = p.Np;

@@ -29,7 +29,6 @@ constexpr int kGemmStages = 6;
 constexpr size_t kGemmSmem = 1024 + (size_t)kGemmStages * kStageBytes;
 constexpr uint32_t kMnBlock = 64 * kTileK * 2;  // 64 m of all the tile's k (MN-major operands)
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kHits = 8;              // rows a word whose rounded-off part dweight still takes
 
 #define ADALN_IN_LOSS(cond) ADALN_IN(::adaln::kDbgLoss, cond)
 
@@ -129,6 +128,9 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
             }
         }
         base += all;
+    }
+    if (a.word_hits) {
+        for (int64_t v = b * kPackThreads + tid; v < a.V; v += G * kPackThreads) a.word_hits[v] = 0;
     }
     if (b == G - 1) {
         // The rest of the last row tile: zero rows without a target.
@@ -421,6 +423,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                     for (int j = 0; j < 16; ++j)
                         if (j == hit >> 1) w[j] = hit & 1 ? (w[j] & 0xFFFFu) | bits << 16 : (w[j] & 0xFFFF0000u) | bits;
                     if (in) a.row_lo[row] = d - __bfloat162float(hi);
+                    if (in && a.word_hits && ADALN_IN_LOSS(tgt < a.V)) {
+                        const int k = atomicAdd(a.word_hits + tgt, 1);
+                        if (k < kHits) a.word_rows[(int64_t)tgt * kHits + k] = (int32_t)row;
+                    }
                 }
                 // Columns past the vocabulary and rows past the packed ones are operands too: zeros.
                 if (col + 32 > a.V || row >= nact) {
@@ -491,39 +497,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
         }
         return t;
     };
-    // dweight: the packed rows whose target is a word of this CTA's half of the tile, at most kHits
-    // a word, in row order. Rounding dz left row_lo off each; words with more rows than that keep
-    // it off, the rounding errors of many rows averaging out.
-    __shared__ int32_t hits[kCtaM], hit_row[kCtaM][kHits];
+    // dweight: the rows whose target is this thread's word, if they are at most kHits.
     const int64_t rank0 = (int64_t)cluster_ctarank() * kCtaM;
+    int hits = 0;
+    int32_t hit_row[kHits];
     auto prologue = [&](const Unit& t) {
+        hits = 0;
         if (t.kind != 2) return;
-        const int e = (int)threadIdx.x - kEpiWarp * 32;
-        epilogue_all(true);  // the last unit's lists have been read
-        if (e < kCtaM) hits[e] = 0;
-        epilogue_all(true);
-        const int64_t w0 = a.v0 + t.m0 + rank0;
-        for (int64_t i = e; i < nact; i += kEpiWarps * 32) {
-            const int64_t w = ADALN_IN_LOSS(i < a.Np) ? a.tgt[i] - w0 : -1;
-            if (w < 0 || w >= kCtaM) continue;
-            const int k = atomicAdd(&hits[w], 1);
-            if (k < kHits) hit_row[w][k] = (int32_t)i;
-        }
-        epilogue_all(true);
-        if (e < kCtaM) {
-            const int n = hits[e];
-            if (n > kHits) {
-                hits[e] = 0;
-            } else {
-                for (int i = 1; i < n; ++i) {  // the order in which they came is the threads'
-                    const int32_t r = hit_row[e][i];
-                    int k = i;
-                    for (; k > 0 && hit_row[e][k - 1] > r; --k) hit_row[e][k] = hit_row[e][k - 1];
-                    hit_row[e][k] = r;
-                }
-            }
-        }
-        epilogue_all(true);
+        const int64_t word = a.v0 + t.m0 + rank0 + (threadIdx.x & 127);
+        if (word >= a.v1 || !ADALN_IN_LOSS(word < a.V)) return;
+        hits = a.word_hits[word];
+        if (hits > kHits) hits = 0;
+        if (hits == 0) return;
+        const int4* list = reinterpret_cast<const int4*>(a.word_rows + word * kHits);
+        const int4 lo = list[0], hi = list[1];
+        const int32_t r[kHits] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int i = 0; i < kHits; ++i) hit_row[i] = i < hits ? r[i] : INT32_MAX;
     };
     gemm_loop(count, a.status, decode, prologue, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
         const int64_t row = t.m0 + r;
@@ -554,12 +544,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
                 }
             } else {
                 const int64_t word = a.v0 + row;
-                const int n = hits[r - rank0];
-                for (int h = 0; h < n; ++h) {
-                    const int64_t i = hit_row[r - rank0][h];
+                int32_t last = -1;
+                for (int h = 0; h < hits; ++h) {
+                    // In row order: the order of the list is that in which the rows came.
+                    int32_t i = INT32_MAX;
+#pragma unroll
+                    for (int k = 0; k < kHits; ++k)
+                        if (hit_row[k] > last && hit_row[k] < i) i = hit_row[k];
+                    last = i;
                     if (!ADALN_IN_LOSS(i >= 0 && i < nact)) continue;
                     const f2r lo = p_splat(a.row_lo[i]);
-                    const uint4* xr = reinterpret_cast<const uint4*>(a.xp) + (i * a.D + col) / 8;
+                    const uint4* xr = reinterpret_cast<const uint4*>(a.xp) + ((int64_t)i * a.D + col) / 8;
 #pragma unroll
                     for (int j = 0; j < 32; j += 8) {
                         if (col + j >= a.D) continue;

@@ -11,6 +11,9 @@ namespace adaln {
 // Output tile of a CTA pair's matrix product and its K step; a CTA's share of the operands.
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
 constexpr int kCtaM = kTileM / 2, kCtaN = kTileN / 2;
+// dweight takes what rounding dz of the target left off in fp32 for words that are the target of
+// at most this many rows; over more rows the roundings average out.
+constexpr int kHits = 8;
 constexpr int kPackThreads = 256;
 constexpr int kPackCtas = 304;  // two per SM: every CTA also counts the rows before its own
 
@@ -27,6 +30,7 @@ struct PackArgs {
     float* row_gs;
     float* row_gt;
     int32_t* nact;          // packed rows
+    int32_t* word_hits;     // backward: zeros [V], or null
     float* loss_out;        // forward: zeros for rows without a loss, or null
     float* lse_out;
     void* dx;               // backward: zeros for rows without a loss, or null
@@ -44,6 +48,8 @@ struct LogitsArgs {
     const float* row_gs;
     const float* row_gt;
     float* row_lo;          // dz: [Np], what rounding dz of the target left off
+    int32_t* word_hits;     // dz: rows whose target each word is [V], and the first kHits of them
+    int32_t* word_rows;     // in the order they came [V, kHits]; or null
     __nv_bfloat16* probs;   // dz [Np, ldp]
     int64_t ldp;
     uint32_t* status;
@@ -55,7 +61,8 @@ struct GradArgs {
     float* dxacc;           // [splits][Np][D] fp32, or null
     __nv_bfloat16* dweight; // [V, D], or null
     const void* xp;
-    const int32_t* tgt;
+    const int32_t* word_hits;
+    const int32_t* word_rows;
     const float* row_lo;
     uint32_t* status;
     int64_t Np, D, V, v0, v1;
