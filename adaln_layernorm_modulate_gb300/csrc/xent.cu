@@ -119,8 +119,9 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
             if (to >= 0) {
                 const uint4* src = reinterpret_cast<const uint4*>(a.x) + (c0 + i) * vecs;
                 uint4* dst = reinterpret_cast<uint4*>(a.xp) + (int64_t)to * vecs;
-                for (int64_t v = lane; v < vecs; v += 32)
-                    if (ADALN_IN_LOSS(c0 + i < a.N && to < a.Np)) dst[v] = ld_stream(src + v);
+                if (!ADALN_IN_LOSS(c0 + i < a.N && to < a.Np)) continue;
+#pragma unroll 4
+                for (int64_t v = lane; v < vecs; v += 32) dst[v] = ld_stream(src + v);
             } else if (a.dx) {
                 uint4* dst = reinterpret_cast<uint4*>(a.dx) + (c0 + i) * vecs;
                 for (int64_t v = lane; v < vecs; v += 32)
@@ -132,17 +133,24 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
     if (a.word_hits) {
         for (int64_t v = b * kPackThreads + tid; v < a.V; v += G * kPackThreads) a.word_hits[v] = 0;
     }
+    // The rows between the packed ones and the next K step of dweight are operands of it: zeros.
+    // Those from N on are shared out, the others (rows without a loss made room) the last CTA's.
+    // The rest of the last row tile only makes rows of products that nothing reads.
+    uint4* xp = reinterpret_cast<uint4*>(a.xp);
+    auto clear = [&](int64_t r0, int64_t r1, int64_t first, int64_t step) {
+        for (int64_t v = r0 * vecs + first; v < r1 * vecs; v += step)
+            if (ADALN_IN_LOSS(v < a.Np * vecs)) xp[v] = zero;
+    };
+    const int64_t kpad = ((int64_t)a.N + kTileK - 1) / kTileK * kTileK;
+    if (a.lse) clear(a.N, kpad, b * kPackThreads + tid, G * kPackThreads);
     if (b == G - 1) {
-        // The rest of the last row tile: zero rows without a target.
+        if (a.lse) clear(base, min(((int64_t)base + kTileK - 1) / kTileK * kTileK, a.N), tid, kPackThreads);
         const int64_t end = ((int64_t)base + kTileM - 1) / kTileM * kTileM;
         for (int64_t r = base + tid; r < end; r += kPackThreads) {
             if (!ADALN_IN_LOSS(r < a.Np)) continue;
             a.tgt[r] = -1;
             if (a.lse) a.row_lse2[r] = a.row_gt[r] = a.row_gs[r] = 0.0f;
         }
-        uint4* dst = reinterpret_cast<uint4*>(a.xp);
-        for (int64_t v = base * vecs + tid; v < end * vecs; v += kPackThreads)
-            if (ADALN_IN_LOSS(v < a.Np * vecs)) dst[v] = zero;
         if (tid == 0) *a.nact = base;
     }
     const bool any_bad = __syncthreads_or(bad);
@@ -359,6 +367,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
     gemm_loop(count, a.status, decode, [](const Unit&) {}, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
         const int64_t row = t.m0 + r;
         const bool in = ADALN_IN_LOSS(row < a.Np);
+        [[maybe_unused]] const int64_t krows = (nact + kTileK - 1) / kTileK * kTileK;
         const int tgt = in ? a.tgt[row] : -1;
         const int64_t c0 = t.n0 + half * (kTileN / 2);
         const f2r l2e = p_splat(kLog2e);
@@ -428,7 +437,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                         if (k < kHits) a.word_rows[(int64_t)tgt * kHits + k] = (int32_t)row;
                     }
                 }
-                // Columns past the vocabulary and rows past the packed ones are operands too: zeros.
+                // Columns past the vocabulary and rows past the packed ones, up to a whole K step of
+                // dweight, are operands too: zeros.
                 if (col + 32 > a.V || row >= nact) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -436,7 +446,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                         else if (col + 2 * j + 1 >= a.V) w[j] &= 0xFFFFu;
                     }
                 }
-                if (in && ADALN_IN_LOSS(col - a.v0 + 32 <= a.ldp)) {
+                if (row < krows && ADALN_IN_LOSS(row < a.Np && col - a.v0 + 32 <= a.ldp)) {
                     __nv_bfloat16* dst = a.probs + row * a.ldp + (col - a.v0);
                     st_sector(dst, w);
                     st_sector(dst + 16, w + 8);
@@ -446,7 +456,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
         release();
         if constexpr (!PROBS) {
             const int64_t part = (t.n0 - a.v0) / kTileN * 2 + half;
-            if (in) a.parts[part * a.Np + row] = make_float2(top, sum);
+            if (in && row < nact) a.parts[part * a.Np + row] = make_float2(top, sum);
         }
     });
 }
@@ -532,7 +542,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
                 float* dst = a.dxacc + (t.slot * a.Np + row) * a.D + col;
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
-                    if (col + j >= a.D || !ADALN_IN_LOSS(row < a.Np && t.slot < a.splits)) continue;
+                    if (row >= nact || col + j >= a.D || !ADALN_IN_LOSS(row < a.Np && t.slot < a.splits)) continue;
                     // A later piece adds in place (one addition a launch to each element, so the
                     // order is the pieces'): the thread does not wait for the old value.
                     if (a.v0 > 0)
