@@ -911,6 +911,7 @@ XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
     const int64_t steps = mt * dt * kv + p.piece / kTileM * dt * (p.Np / kTileK);
     const int64_t share = std::max<int64_t>(steps / kXentPairs, 16);
     p.splits = (int)std::min<int64_t>(std::max<int64_t>((kv + share - 1) / share, 1), 16);
+    if (p.Np > INT32_MAX / p.splits) p.splits = 1;  // rows of the fp32 dx are 32-bit coordinates
     size_t at = kPartialsOffset;
     auto take = [&](size_t bytes) {
         const size_t o = at;

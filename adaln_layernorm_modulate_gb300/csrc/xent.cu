@@ -26,7 +26,8 @@ constexpr int kGemmThreads = (kEpiWarp + kEpiWarps) * 32;
 constexpr uint32_t kABytes = kCtaM * kTileK * 2, kBBytes = kCtaN * kTileK * 2;
 constexpr uint32_t kStageBytes = kABytes + kBBytes;
 constexpr int kGemmStages = 6;
-constexpr size_t kGemmSmem = 1024 + (size_t)kGemmStages * kStageBytes;
+constexpr uint32_t kOutBytes = 32 * 128;  // an epilogue warp's rows on their way out
+constexpr size_t kGemmSmem = 1024 + (size_t)kGemmStages * kStageBytes + (size_t)kEpiWarps * kOutBytes;
 constexpr uint32_t kMnBlock = 64 * kTileK * 2;  // 64 m of all the tile's k (MN-major operands)
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -183,8 +184,9 @@ struct Unit {
 };
 
 // decode(u): unit u. prologue(unit): run by the epilogue threads while the unit's products are
-// still under way. epilogue(unit, accumulator, row of the tile, half of its columns, release):
-// calls release() when it has read the accumulator. units() is called, and global memory first
+// still under way. epilogue(unit, accumulator, row of the tile, half of its columns, out, release):
+// calls release() when it has read the accumulator; `out` is the warp's buffer for results, read
+// by stores that lane 0 issues. units() is called, and global memory first
 // read, after the kernel ahead has finished; barriers and tensor memory are set up before.
 template <class Units, class Decode, class Prologue, class Epilogue>
 __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode decode, Prologue prologue,
@@ -311,6 +313,7 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
         }
     } else if (warp >= kEpiWarp) {
         const int q = warp & 3, half = (warp - kEpiWarp) >> 2;
+        const uint32_t out = data + kGemmStages * kStageBytes + (uint32_t)(warp - kEpiWarp) * kOutBytes;
         int acc = 0;
         uint32_t alap = 0;
         for (int64_t u = first; u < units; u += step) {
@@ -320,7 +323,7 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
             if (!epilogue_all(mbar_wait_bounded(afull + 8u * acc, alap & 1u, &abort_flag))) break;
             tc_fence_after();
             const uint32_t src = tmem + (uint32_t)acc * kTileN + (uint32_t)half * (kTileN / 2) + ((uint32_t)q << 21);
-            epilogue(t, src, (int)rank * kCtaM + q * 32 + lane, half, [&]() {
+            epilogue(t, src, (int)rank * kCtaM + q * 32 + lane, half, out, [&]() {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(cluster_map(aempty + 8u * acc, 0));
@@ -330,6 +333,7 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
                 ++alap;
             }
         }
+        if (lane == 0) tma_store_wait();
     }
     __syncwarp();
     tc_fence_before();
@@ -346,6 +350,7 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
 template <bool PROBS>
 __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_constant__ CUtensorMap mx,
                                                               const __grid_constant__ CUtensorMap mw,
+                                                              const __grid_constant__ CUtensorMap mp,
                                                               const LogitsArgs a) {
     pdl_trigger();
     int64_t nact = 0, mt = 0;
@@ -364,7 +369,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
         t.iters = (int)((a.D + kTileK - 1) / kTileK);
         return t;
     };
-    gemm_loop(count, a.status, decode, [](const Unit&) {}, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
+    gemm_loop(count, a.status, decode, [](const Unit&) {}, [&](const Unit& t, uint32_t src, int r, int half,
+                                                              [[maybe_unused]] uint32_t out, auto release) {
+        [[maybe_unused]] const int lane = threadIdx.x & 31;
         const int64_t row = t.m0 + r;
         const bool in = ADALN_IN_LOSS(row < a.Np);
         [[maybe_unused]] const int64_t krows = (nact + kTileK - 1) / kTileK * kTileK;
@@ -381,33 +388,34 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
             }
         }
 #pragma unroll 1
-        for (int c = 0; c < kTileN / 2; c += 32) {
-            float v[32];
+        for (int c = 0; c < kTileN / 2; c += 64) {
+            float v[64];
             __syncwarp();
-            tmem_ld32(src + c, v);
+            tmem_ld64(src + c, v);
             const int64_t col = c0 + c;
-            const int hit = (int64_t)tgt >= col && (int64_t)tgt < col + 32 ? (int)(tgt - col) : -1;
+            const int hit = (int64_t)tgt >= col && (int64_t)tgt < col + 64 ? (int)(tgt - col) : -1;
             float zt = 0.0f;
             if (hit >= 0) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) zt = j == hit ? v[j] : zt;
+                for (int j = 0; j < 64; ++j) zt = j == hit ? v[j] : zt;
             }
             if constexpr (!PROBS) {
-                if (col + 32 > a.V) {
+                if (col + 64 > a.V) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < 64; ++j)
                         if (col + j >= a.V) v[j] = neg_inf();
                 }
                 if (hit >= 0 && in) a.zt[row] = zt;
-                float m = top;
+                float m4[4] = {top, neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-                for (int j = 0; j < 32; ++j) m = fmaxf(m, v[j]);
+                for (int j = 0; j < 64; ++j) m4[j & 3] = fmaxf(m4[j & 3], v[j]);
+                const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 // A chunk with no finite value at all adds nothing (and NaN is kept below).
                 const float mm = m == neg_inf() ? 0.0f : m;
                 const f2r m2 = p_splat(-mm * kLog2e);
                 f2r s[2] = {kPairZero, kPairZero};
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
+                for (int j = 0; j < 32; ++j) {
                     const float2 e = p_get(p_fma(p_make(v[2 * j], v[2 * j + 1]), l2e, m2));
                     s[j & 1] = p_add(s[j & 1], p_make(exp2_ftz(e.x), exp2_ftz(e.y)));
                 }
@@ -415,9 +423,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                 top = m;
             } else {
                 const f2r nl = p_splat(-lse2), g2 = p_splat(gs);
-                uint32_t w[16];
+                uint32_t w[32];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
+                for (int j = 0; j < 32; ++j) {
                     const float2 e = p_get(p_fma(p_make(v[2 * j], v[2 * j + 1]), l2e, nl));
                     const float2 p = p_get(p_mul(p_make(exp2_ftz(e.x), exp2_ftz(e.y)), g2));
                     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(p.y), "f"(p.x));
@@ -429,7 +437,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                     const __nv_bfloat16 hi = __float2bfloat16_rn(d);
                     const uint32_t bits = __bfloat16_as_ushort(hi);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                    for (int j = 0; j < 32; ++j)
                         if (j == hit >> 1) w[j] = hit & 1 ? (w[j] & 0xFFFFu) | bits << 16 : (w[j] & 0xFFFF0000u) | bits;
                     if (in) a.row_lo[row] = d - __bfloat162float(hi);
                     if (in && a.word_hits && ADALN_IN_LOSS(tgt < a.V)) {
@@ -439,18 +447,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                 }
                 // Columns past the vocabulary and rows past the packed ones, up to a whole K step of
                 // dweight, are operands too: zeros.
-                if (col + 32 > a.V || row >= nact) {
+                if (col + 64 > a.V || row >= nact) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                    for (int j = 0; j < 32; ++j) {
                         if (col + 2 * j >= a.V || row >= nact) w[j] = 0u;
                         else if (col + 2 * j + 1 >= a.V) w[j] &= 0xFFFFu;
                     }
                 }
-                if (row < krows && ADALN_IN_LOSS(row < a.Np && col - a.v0 + 32 <= a.ldp)) {
-                    __nv_bfloat16* dst = a.probs + row * a.ldp + (col - a.v0);
-                    st_sector(dst, w);
-                    st_sector(dst + 16, w + 8);
-                }
+                if (lane == 0) tma_store_read();
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    st_swizzled(out + (uint32_t)lane * 128u, lane, j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                fence_shared_async();
+                __syncwarp();
+                // Rows 32 at a time: krows is a multiple of 32.
+                if (lane == 0 && row < krows && ADALN_IN_LOSS(row + 32 <= a.Np && col - a.v0 + 64 <= a.ldp))
+                    tma_store(&mp, (int)(col - a.v0), (int)row, out, false);
             }
         }
         release();
@@ -467,6 +480,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
                                                             const __grid_constant__ CUtensorMap mw,
                                                             const __grid_constant__ CUtensorMap mx,
                                                             const __grid_constant__ CUtensorMap mpt,
+                                                            const __grid_constant__ CUtensorMap mdx,
+                                                            const __grid_constant__ CUtensorMap mdw,
                                                             const GradArgs a) {
     pdl_trigger();
     int64_t nact = 0, mt = 0, ndx = 0;
@@ -525,32 +540,40 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < kHits; ++i) hit_row[i] = i < hits ? r[i] : INT32_MAX;
     };
-    gemm_loop(count, a.status, decode, prologue, [&](const Unit& t, uint32_t src, int r, int half, auto release) {
+    gemm_loop(count, a.status, decode, prologue, [&](const Unit& t, uint32_t src, int r, int half, uint32_t out,
+                                                     auto release) {
+        const int lane = threadIdx.x & 31;
         const int64_t row = t.m0 + r;
         const int64_t c0 = t.n0 + half * (kTileN / 2);
+        const uint32_t mine = out + (uint32_t)lane * 128u;
 #pragma unroll 1
-        for (int c = 0; c < kTileN / 2; c += 32) {
-            float v[32];
+        for (int c = 0; c < kTileN / 2; c += 64) {
+            float v[64];
             __syncwarp();
-            tmem_ld32(src + c, v);
+            tmem_ld64(src + c, v);
             if (t.iters == 0) {  // nothing was accumulated
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                for (int j = 0; j < 64; ++j) v[j] = 0.0f;
             }
             const int64_t col = c0 + c;
             if (t.kind == 1) {
-                float* dst = a.dxacc + (t.slot * a.Np + row) * a.D + col;
+                // A later piece adds in place (one addition a launch to each element, so the order
+                // is the pieces').
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    if (row >= nact || col + j >= a.D || !ADALN_IN_LOSS(row < a.Np && t.slot < a.splits)) continue;
-                    // A later piece adds in place (one addition a launch to each element, so the
-                    // order is the pieces'): the thread does not wait for the old value.
-                    if (a.v0 > 0)
-                        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst + j), "f"(v[j]),
-                                     "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3])
-                                     : "memory");
-                    else
-                        *reinterpret_cast<float4*>(dst + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                for (int b = 0; b < 2; ++b) {
+                    if (lane == 0) tma_store_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float* f = v + 32 * b + 4 * j;
+                        st_swizzled(mine, lane, j, __float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                    __float_as_uint(f[3]));
+                    }
+                    fence_shared_async();
+                    __syncwarp();
+                    if (lane == 0 && row < nact && col + 32 * b < a.D &&
+                        ADALN_IN_LOSS(row + 32 <= a.Np && t.slot < a.splits))
+                        tma_store(&mdx, (int)col + 32 * b, (int)(t.slot * a.Np + row), out, a.v0 > 0);
                 }
             } else {
                 const int64_t word = a.v0 + row;
@@ -566,7 +589,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
                     const f2r lo = p_splat(a.row_lo[i]);
                     const uint4* xr = reinterpret_cast<const uint4*>(a.xp) + ((int64_t)i * a.D + col) / 8;
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
+                    for (int j = 0; j < 64; j += 8) {
                         if (col + j >= a.D) continue;
                         f2r x[4];
                         Io<__nv_bfloat16>::unpackp(xr[j / 8], x);
@@ -578,25 +601,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
                         }
                     }
                 }
-                __nv_bfloat16* dst = a.dweight + word * a.D + col;
-                uint32_t w[16];
+                uint32_t w[32];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                for (int j = 0; j < 32; ++j)
                     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
-                if (word < a.v1 && ADALN_IN_LOSS(word < a.V)) {
+                if (lane == 0) tma_store_read();
+                __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 32; j += 16) {
-                        if (a.sectors) {  // D is a multiple of 16: rows are whole sectors
-                            if (col + j < a.D) st_sector(dst + j, w + j / 2);
-                            continue;
-                        }
-#pragma unroll
-                        for (int i = j; i < j + 16; i += 8)
-                            if (col + i < a.D)
-                                *reinterpret_cast<uint4*>(dst + i) =
-                                    make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]);
-                    }
-                }
+                for (int j = 0; j < 8; ++j)
+                    st_swizzled(mine, lane, j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                fence_shared_async();
+                __syncwarp();
+                if (lane == 0 && word < a.v1 && col < a.D) tma_store(&mdw, (int)col, (int)word, out, false);
             }
         }
         release();
@@ -689,9 +705,10 @@ namespace {
 
 unsigned cap(int64_t want, int64_t most) { return (unsigned)(want < 1 ? 1 : want < most ? want : most); }
 
-// Tiled tensor map of a row-major bf16 [rows, cols] matrix (row stride ld elements), boxes of 64
-// columns by `box_rows` rows, 128-byte swizzle.
-bool tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+// Tiled tensor map of a row-major bf16 (or fp32) [rows, cols] matrix (row stride ld elements),
+// boxes of 128 bytes of a row by `box_rows` rows, 128-byte swizzle.
+bool tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+              bool f32 = false) {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -706,9 +723,9 @@ bool tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int6
     }();
     if (!encode) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, one,
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * (f32 ? 4 : 2)};
+    const cuuint32_t box[2] = {f32 ? 32u : 64u, (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -725,31 +742,33 @@ cudaError_t launch_pack(const PackArgs& args, int ctas, cudaStream_t stream) {
 cudaError_t launch_logits(const LogitsArgs& args, bool probs, const void* xp, const void* weight, int sms,
                           cudaStream_t stream) {
     LogitsArgs a = args;
-    CUtensorMap mx, mw;
-    if (!tile_map(&mx, xp, a.Np, a.D, a.D, kCtaM) || !tile_map(&mw, weight, a.V, a.D, a.D, kCtaN))
+    CUtensorMap mx, mw, mp{};
+    if (!tile_map(&mx, xp, a.Np, a.D, a.D, kCtaM) || !tile_map(&mw, weight, a.V, a.D, a.D, kCtaN) ||
+        (probs && !tile_map(&mp, a.probs, a.Np, a.ldp, a.ldp, 32)))
         return cudaErrorInvalidValue;
     const void* fn = probs ? reinterpret_cast<const void*>(&logits_kernel<true>)
                            : reinterpret_cast<const void*>(&logits_kernel<false>);
     if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) return e;
     const int64_t units = (a.Np / kTileM) * ((a.v1 - a.v0 + kTileN - 1) / kTileN);
-    void* params[] = {&mx, &mw, &a};
+    void* params[] = {&mx, &mw, &mp, &a};
     return launch_dependent(fn, dim3(2 * cap(units, sms / 2)), dim3(kGemmThreads), params, kGemmSmem, stream, 2);
 }
 
 cudaError_t launch_grad(const GradArgs& args, const void* probs, int64_t ldp, const void* xp, const void* weight,
                         int sms, cudaStream_t stream) {
     GradArgs a = args;
-    CUtensorMap mp, mw, mx, mpt;
+    CUtensorMap mp, mw, mx, mpt, mdx{}, mdw{};
     if (!tile_map(&mp, probs, a.Np, ldp, ldp, kCtaM) || !tile_map(&mw, weight, a.V, a.D, a.D, kTileK) ||
-        !tile_map(&mx, xp, a.Np, a.D, a.D, kTileK) || !tile_map(&mpt, probs, a.Np, ldp, ldp, kTileK))
+        !tile_map(&mx, xp, a.Np, a.D, a.D, kTileK) || !tile_map(&mpt, probs, a.Np, ldp, ldp, kTileK) ||
+        (a.dxacc && !tile_map(&mdx, a.dxacc, a.splits * a.Np, a.D, a.D, 32, true)) ||
+        (a.dweight && !tile_map(&mdw, a.dweight, a.V, a.D, a.D, 32)))
         return cudaErrorInvalidValue;
     const void* fn = reinterpret_cast<const void*>(&grad_kernel);
     if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) return e;
-    a.sectors = a.D % 16 == 0 && reinterpret_cast<uintptr_t>(a.dweight) % 32 == 0;
     const int64_t dt = (a.D + kTileN - 1) / kTileN;
     const int64_t units = (a.dxacc ? a.Np / kTileM * dt * a.splits : 0) +
                           (a.dweight ? (a.v1 - a.v0 + kTileM - 1) / kTileM * dt : 0);
-    void* params[] = {&mp, &mw, &mx, &mpt, &a};
+    void* params[] = {&mp, &mw, &mx, &mpt, &mdx, &mdw, &a};
     return launch_dependent(fn, dim3(2 * cap(units, sms / 2)), dim3(kGemmThreads), params, kGemmSmem, stream, 2);
 }
 

@@ -67,7 +67,6 @@ struct GradArgs {
     uint32_t* status;
     int64_t Np, D, V, v0, v1;
     int splits;             // parts of dx's K range
-    int sectors;            // dweight rows start on 32-byte boundaries (set by launch_grad)
 };
 
 struct LseArgs {
