@@ -882,12 +882,12 @@ namespace {
 // 3.15 ms, 512 MiB 3.20 ms.
 constexpr int64_t kProbsBytes = (int64_t)256 << 20;
 constexpr int64_t kMinPiece = 2048;
-constexpr int64_t kXentPairs = 76;  // the SM pairs the split of dx's sums is made for
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 struct XentPlan {
     int64_t Np;          // rows of the packed buffers: whole row tiles, at least one
+    int tn, tng;         // columns a tile of logits, of gradients
     int64_t tiles;       // forward: column tiles
     int64_t piece;       // backward: columns of a piece (a multiple of kTileN)
     int splits;          // backward: parts of dx's sum over a piece
@@ -900,16 +900,18 @@ struct XentPlan {
 XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
     XentPlan p{};
     p.Np = std::max<int64_t>(round_up(N, kTileM), kTileM);
-    p.tiles = (V + kTileN - 1) / kTileN;
     const int64_t wide = std::max<int64_t>(kProbsBytes / 2 / p.Np / kTileN * kTileN, kMinPiece);
     const int64_t pieces = (V + wide - 1) / wide;
     p.piece = round_up((V + pieces - 1) / pieces, kTileN);
+    p.tn = tile_cols(p.Np / kTileM, bwd ? std::min(V, p.piece) : V);
+    p.tiles = (V + p.tn - 1) / p.tn;
+    p.tng = tile_cols(p.Np / kTileM + p.piece / kTileM, D);
     // dx sums over a piece's columns, dweight over the rows: with few rows the dx tiles are few
     // and long. They are split until one is no longer than an SM pair's share of all the K steps (at
     // least 16 of them, below which filling the pipeline costs more).
-    const int64_t dt = (D + kTileN - 1) / kTileN, mt = p.Np / kTileM, kv = p.piece / kTileK;
+    const int64_t dt = (D + p.tng - 1) / p.tng, mt = p.Np / kTileM, kv = p.piece / kTileK;
     const int64_t steps = mt * dt * kv + p.piece / kTileM * dt * (p.Np / kTileK);
-    const int64_t share = std::max<int64_t>(steps / kXentPairs, 16);
+    const int64_t share = std::max<int64_t>(steps / kPairs, 16);
     p.splits = (int)std::min<int64_t>(std::max<int64_t>((kv + share - 1) / share, 1), 16);
     if (p.Np > INT32_MAX / p.splits) p.splits = 1;  // rows of the fp32 dx are 32-bit coordinates
     size_t at = kPartialsOffset;
@@ -939,6 +941,8 @@ int xent_check(int64_t N, int64_t V, int64_t D, adaln_dtype dtype) {
     if (int rc = check_shape(D, dtype)) return rc;
     if (dtype != ADALN_BF16) return ADALN_ERR_UNSUPPORTED;
     if (N < 0 || N > INT32_MAX - kTileM || V < 1 || V > INT32_MAX - kTileN) return ADALN_ERR_INVALID_ARG;
+    // Tiles are counted in 32 bits (N V of 1.4e14).
+    if ((N / kTileM + 1) * (V / kTileN + 1) > INT32_MAX) return ADALN_ERR_INVALID_ARG;
     return ADALN_OK;
 }
 
@@ -1006,6 +1010,7 @@ int adaln_linear_xent_fwd(const void* x, const void* weight, const int64_t* targ
     g.D = D;
     g.V = V;
     g.v1 = V;
+    g.tn = p.tn;
     if (int rc = launched(launch_logits(g, false, k.xp, weight, sms, stream))) return rc;
     LseArgs l{};
     l.nact = k.nact;
@@ -1071,6 +1076,7 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
         g.V = V;
         g.v0 = v0;
         g.v1 = std::min(V, v0 + p.piece);
+        g.tn = p.tn;
         if (int rc = launched(launch_logits(g, true, k.xp, weight, sms, stream))) return rc;
         GradArgs d{};
         d.nact = k.nact;
@@ -1087,6 +1093,7 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
         d.v0 = v0;
         d.v1 = g.v1;
         d.splits = p.splits;
+        d.tn = p.tng;
         if (int rc = launched(launch_grad(d, g.probs, p.piece, k.xp, weight, sms, stream))) return rc;
     }
     if (!dx) return ADALN_OK;

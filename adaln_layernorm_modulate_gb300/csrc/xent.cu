@@ -21,9 +21,9 @@ namespace adaln {
 
 constexpr int kAccs = 2;              // accumulator tiles in tensor memory
 constexpr int kEpiWarp = 4;           // first epilogue warp
-constexpr int kEpiWarps = 8;          // two per 32 lanes of tensor memory, half the columns each
+constexpr int kEpiWarps = 8;          // two per 32 lanes of tensor memory, every other 64 columns each
 constexpr int kGemmThreads = (kEpiWarp + kEpiWarps) * 32;
-constexpr uint32_t kABytes = kCtaM * kTileK * 2, kBBytes = kCtaN * kTileK * 2;
+constexpr uint32_t kABytes = kCtaM * kTileK * 2, kBBytes = kTileN / 2 * kTileK * 2;
 constexpr uint32_t kStageBytes = kABytes + kBBytes;
 constexpr int kGemmStages = 6;
 constexpr uint32_t kOutBytes = 32 * 128;  // an epilogue warp's rows on their way out
@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------
-// Matrix products. A persistent CTA pair on every two SMs walks its units (output tiles): warp 0
-// of each CTA fills its half of a ring of shared-memory stages by TMA (both halves complete on
+// Matrix products. A persistent CTA pair on every two SMs walks its units (output tiles): warps 0 and 3
+// of each CTA fill its half of a ring of shared-memory stages by TMA (all of a stage completes on
 // CTA 0's barrier), warp 1 of CTA 0 issues the pair's products into one of two accumulators,
 // warps 4.. of each CTA read its rows of the other one back and run the epilogue.
 // ---------------------------------------------------------------------------------------
@@ -184,11 +184,13 @@ struct Unit {
 };
 
 // decode(u): unit u. prologue(unit): run by the epilogue threads while the unit's products are
-// still under way. epilogue(unit, accumulator, row of the tile, half of its columns, out, release):
+// still under way. epilogue(unit, accumulator, row of the tile, half (which 64 columns), out, release):
 // calls release() when it has read the accumulator; `out` is the warp's buffer for results, read
 // by stores that lane 0 issues. units() is called, and global memory first
 // read, after the kernel ahead has finished; barriers and tensor memory are set up before.
-template <class Units, class Decode, class Prologue, class Epilogue>
+// TN: columns a tile (a template argument, as are the operands' layouts below: a producer that
+// takes them from the unit is late, 8192 x 50257 x 2048 backward 3.43 ms against 3.16).
+template <int TN, class Units, class Decode, class Prologue, class Epilogue>
 __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode decode, Prologue prologue,
                                           Epilogue epilogue) {
     extern __shared__ uint4 dyn[];
@@ -197,7 +199,7 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
     __shared__ int abort_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_ctarank();
-    const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;  // units of this pair
+    const uint32_t first = blockIdx.x >> 1, step = gridDim.x >> 1;  // units of this pair
     const uint32_t data = (smem_addr(dyn) + 1023u) & ~1023u;
     const uint32_t full = smem_addr(bars), empty = full + 8u * kGemmStages;
     const uint32_t afull = empty + 8u * kGemmStages, aempty = afull + 8u * kAccs, drain = aempty + 8u * kAccs;
@@ -221,34 +223,37 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
     tc_fence_after();
     const uint32_t tmem = tmem_base;
     pdl_wait();
-    const int64_t units = count();
+    const uint32_t units = count();
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 3) {
+        // Warp 0 loads this CTA's half of A, warp 3 its half of B, both into the same stages: one
+        // thread issuing both is late (the loads of an MN-major operand are one a 64 columns).
         if (lane == 0) {
             fence_async_proxy();
+            const bool is_b = warp == 3;
             int s = 0;
             uint32_t lap = 0;
             bool live = true;
-            for (int64_t u = first; live && u < units; u += step) {
+            for (uint32_t u = first; live && u < units; u += step) {
                 const Unit t = decode(u);
-                for (int i = 0; i < t.iters; ++i) {
+                const CUtensorMap* map = is_b ? t.mb : t.ma;
+                const int x0 = is_b ? (int)t.n0 + (int)rank * (TN / 2) : (int)t.m0 + (int)rank * kCtaM;
+                const int blocks = !(is_b ? t.b_mn : t.a_mn) ? 0 : is_b ? TN / 128 : kCtaM / 64;
+                int k = (int)(is_b ? t.kb0 : t.k0);
+                for (int i = 0; i < t.iters; ++i, k += kTileK) {
                     if (lap > 0 && !mbar_wait_bounded(empty + 8u * s, (lap - 1) & 1u, &abort_flag)) {
                         live = false;
                         break;
                     }
-                    const uint32_t bar = cluster_map(full + 8u * s, 0), as = data + s * kStageBytes, bs = as + kABytes;
-                    if (rank == 0) mbar_arrive_expect_tx(full + 8u * s, 2 * kStageBytes);
-                    const int m0 = (int)t.m0 + (int)rank * kCtaM, n0 = (int)t.n0 + (int)rank * kCtaN;
-                    const int ka = (int)(t.k0 + (int64_t)i * kTileK), kb = (int)(t.kb0 + (int64_t)i * kTileK);
-                    if (t.a_mn) {
-                        for (int j = 0; j < kCtaM / 64; ++j) tma_load(as + j * kMnBlock, t.ma, m0 + 64 * j, ka, bar);
+                    const uint32_t bar = cluster_map(full + 8u * s, 0);
+                    const uint32_t dst = data + s * kStageBytes + (is_b ? kABytes : 0u);
+                    if (rank == 0 && !is_b)
+                        mbar_arrive_expect_tx(full + 8u * s, 2 * kABytes + (uint32_t)TN * kTileK * 2);
+                    if (blocks == 0) {
+                        tma_load(dst, map, k, x0, bar);
                     } else {
-                        tma_load(as, t.ma, ka, m0, bar);
-                    }
-                    if (t.b_mn) {
-                        for (int j = 0; j < kCtaN / 64; ++j) tma_load(bs + j * kMnBlock, t.mb, n0 + 64 * j, kb, bar);
-                    } else {
-                        tma_load(bs, t.mb, kb, n0, bar);
+                        tma_load(dst, map, x0, k, bar);
+                        if (blocks == 2) tma_load(dst + kMnBlock, map, x0 + 64, k, bar);
                     }
                     if (++s == kGemmStages) {
                         s = 0;
@@ -258,7 +263,7 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
             }
             // After a timeout, copies may still be on their way into the pair's memory: CTA 0 gives
             // each stage's last ones a further bounded wait, CTA 1 meets it at the cluster barrier.
-            if (rank == 0 && *(volatile int*)&abort_flag) {
+            if (rank == 0 && !is_b && *(volatile int*)&abort_flag) {
                 volatile int never = 0;
                 for (int q = 0; q < kGemmStages; ++q) {
                     if (q >= s && lap == 0) continue;
@@ -272,9 +277,9 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
             int s = 0, acc = 0;
             uint32_t lap = 0, alap = 0;
             bool live = true;
-            for (int64_t u = first; live && u < units; u += step) {
+            for (uint32_t u = first; live && u < units; u += step) {
                 const Unit t = decode(u);
-                const uint32_t idesc = mma_desc(kTileM, kTileN, t.a_mn, t.b_mn);
+                const uint32_t idesc = mma_desc(kTileM, TN, t.a_mn, t.b_mn);
                 // 16 k: 32 bytes of a K-major row, 16 rows of an MN-major tile.
                 const uint32_t ak = (t.a_mn ? 2048u : 32u) >> 4, bk = (t.b_mn ? 2048u : 32u) >> 4;
                 if (alap > 0 && !mbar_wait_cluster_bounded(aempty + 8u * acc, (alap - 1) & 1u, &abort_flag))
@@ -316,13 +321,13 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
         const uint32_t out = data + kGemmStages * kStageBytes + (uint32_t)(warp - kEpiWarp) * kOutBytes;
         int acc = 0;
         uint32_t alap = 0;
-        for (int64_t u = first; u < units; u += step) {
+        for (uint32_t u = first; u < units; u += step) {
             const Unit t = decode(u);
             prologue(t);
             // All epilogue warps go on or none: they meet at barriers of their own.
             if (!epilogue_all(mbar_wait_bounded(afull + 8u * acc, alap & 1u, &abort_flag))) break;
             tc_fence_after();
-            const uint32_t src = tmem + (uint32_t)acc * kTileN + (uint32_t)half * (kTileN / 2) + ((uint32_t)q << 21);
+            const uint32_t src = tmem + (uint32_t)acc * kTileN + ((uint32_t)q << 21);
             epilogue(t, src, (int)rank * kCtaM + q * 32 + lane, half, out, [&]() {
                 tc_fence_before();
                 __syncwarp();
@@ -347,48 +352,54 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
 }
 
 // The tile's logits, as row statistics (PROBS false) or as dz (PROBS true).
-template <bool PROBS>
+template <bool PROBS, int TN>
 __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_constant__ CUtensorMap mx,
                                                               const __grid_constant__ CUtensorMap mw,
                                                               const __grid_constant__ CUtensorMap mp,
                                                               const LogitsArgs a) {
     pdl_trigger();
-    int64_t nact = 0, mt = 0;
-    const int64_t nt = (a.v1 - a.v0 + kTileN - 1) / kTileN;
+    int64_t nact = 0;
+    uint32_t mt = 0;  // tile counts are 32 bits (checked on the host): their quotients are cheap
+    const uint32_t nt = (uint32_t)((a.v1 - a.v0 + TN - 1) / TN);
     auto count = [&]() {
         nact = *a.nact;
-        mt = (nact + kTileM - 1) / kTileM;
+        mt = (uint32_t)((nact + kTileM - 1) / kTileM);
         return mt * nt;
     };
-    auto decode = [&](int64_t u) {
+    auto decode = [&](uint32_t u) {
         Unit t{};
         t.ma = &mx;
         t.mb = &mw;
-        t.m0 = u % mt * kTileM;
-        t.n0 = a.v0 + u / mt * kTileN;
+        t.m0 = (int64_t)(u % mt) * kTileM;
+        t.n0 = a.v0 + (int64_t)(u / mt) * TN;
         t.iters = (int)((a.D + kTileK - 1) / kTileK);
         return t;
     };
-    gemm_loop(count, a.status, decode, [](const Unit&) {}, [&](const Unit& t, uint32_t src, int r, int half,
-                                                              [[maybe_unused]] uint32_t out, auto release) {
-        [[maybe_unused]] const int lane = threadIdx.x & 31;
+    // This thread's row, read while the tile's products are under way.
+    const int lane = threadIdx.x & 31;
+    const int64_t rank0 = (int64_t)cluster_ctarank() * kCtaM;
+    int tgt = -1;
+    [[maybe_unused]] float lse2 = 0.0f, gs = 0.0f, gt = 0.0f;
+    auto prologue = [&](const Unit& t) {
+        const int64_t row = t.m0 + rank0 + (threadIdx.x & 127);
+        if (!ADALN_IN_LOSS(row < a.Np)) return;
+        tgt = a.tgt[row];
+        if constexpr (PROBS) {
+            lse2 = a.row_lse2[row];
+            gs = a.row_gs[row];
+            gt = a.row_gt[row];
+        }
+    };
+    gemm_loop<TN>(count, a.status, decode, prologue, [&](const Unit& t, uint32_t src, int r, int half,
+                                                     [[maybe_unused]] uint32_t out, auto release) {
         const int64_t row = t.m0 + r;
         const bool in = ADALN_IN_LOSS(row < a.Np);
         [[maybe_unused]] const int64_t krows = (nact + kTileK - 1) / kTileK * kTileK;
-        const int tgt = in ? a.tgt[row] : -1;
-        const int64_t c0 = t.n0 + half * (kTileN / 2);
+        const int64_t c0 = t.n0;
         const f2r l2e = p_splat(kLog2e);
         [[maybe_unused]] float top = neg_inf(), sum = 0.0f;
-        [[maybe_unused]] float lse2 = 0.0f, gs = 0.0f, gt = 0.0f;
-        if constexpr (PROBS) {
-            if (in) {
-                lse2 = a.row_lse2[row];
-                gs = a.row_gs[row];
-                gt = a.row_gt[row];
-            }
-        }
 #pragma unroll 1
-        for (int c = 0; c < kTileN / 2; c += 64) {
+        for (int c = 64 * half; c < TN; c += 128) {
             float v[64];
             __syncwarp();
             tmem_ld64(src + c, v);
@@ -468,7 +479,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
         }
         release();
         if constexpr (!PROBS) {
-            const int64_t part = (t.n0 - a.v0) / kTileN * 2 + half;
+            const int64_t part = (int64_t)((uint32_t)(t.n0 - a.v0) / TN) * 2 + half;
             if (in && row < nact) a.parts[part * a.Np + row] = make_float2(top, sum);
         }
     });
@@ -476,6 +487,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
 
 // dx += dz W and dweight = dz^T x of one piece of the vocabulary, as one list of units: dx
 // tiles, each in `splits` parts of the piece's columns, then dweight tiles.
+template <int TN>
 __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_constant__ CUtensorMap mp,
                                                             const __grid_constant__ CUtensorMap mw,
                                                             const __grid_constant__ CUtensorMap mx,
@@ -484,40 +496,41 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
                                                             const __grid_constant__ CUtensorMap mdw,
                                                             const GradArgs a) {
     pdl_trigger();
-    int64_t nact = 0, mt = 0, ndx = 0;
-    const int64_t dt = (a.D + kTileN - 1) / kTileN;
-    const int64_t kv = (a.v1 - a.v0 + kTileK - 1) / kTileK;  // K steps of dx
-    const int64_t vt = (a.v1 - a.v0 + kTileM - 1) / kTileM;
+    int64_t nact = 0;
+    uint32_t per = 0, ndx = 0;  // units of one part of dx, and of all
+    const uint32_t dt = (uint32_t)((a.D + TN - 1) / TN);
+    const uint32_t kv = (uint32_t)((a.v1 - a.v0 + kTileK - 1) / kTileK);  // K steps of dx
+    const uint32_t vt = (uint32_t)((a.v1 - a.v0 + kTileM - 1) / kTileM);
     auto count = [&]() {
         nact = *a.nact;
-        mt = (nact + kTileM - 1) / kTileM;
-        ndx = a.dxacc ? mt * dt * a.splits : 0;
+        per = (uint32_t)((nact + kTileM - 1) / kTileM) * dt;
+        ndx = a.dxacc ? per * (uint32_t)a.splits : 0;
         return ndx + (a.dweight ? vt * dt : 0);
     };
-    auto decode = [&](int64_t u) {
+    auto decode = [&](uint32_t u) {
         Unit t{};
         t.b_mn = true;
         if (u < ndx) {
             t.kind = 1;
-            t.slot = u / (mt * dt);
-            const int64_t w = u % (mt * dt);
-            const int64_t k0 = t.slot * kv / a.splits, k1 = (t.slot + 1) * kv / a.splits;
+            const uint32_t slot = u / per, w = u - slot * per;
+            const uint32_t k0 = slot * kv / (uint32_t)a.splits, k1 = (slot + 1) * kv / (uint32_t)a.splits;
+            t.slot = slot;
             t.ma = &mp;
             t.mb = &mw;
             // dz is read once, by the units of all columns of dx side by side.
-            t.m0 = w / dt * kTileM;
-            t.n0 = w % dt * kTileN;
-            t.k0 = k0 * kTileK;
+            t.m0 = (int64_t)(w / dt) * kTileM;
+            t.n0 = (int64_t)(w % dt) * TN;
+            t.k0 = (int64_t)k0 * kTileK;
             t.kb0 = a.v0 + t.k0;
             t.iters = (int)(k1 - k0);
         } else {
             t.kind = 2;
-            const int64_t w = u - ndx;
+            const uint32_t w = u - ndx;
             t.ma = &mpt;
             t.mb = &mx;
             t.a_mn = true;
-            t.m0 = w / dt * kTileM;
-            t.n0 = w % dt * kTileN;
+            t.m0 = (int64_t)(w / dt) * kTileM;
+            t.n0 = (int64_t)(w % dt) * TN;
             t.iters = (int)((nact + kTileK - 1) / kTileK);
         }
         return t;
@@ -540,14 +553,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
 #pragma unroll
         for (int i = 0; i < kHits; ++i) hit_row[i] = i < hits ? r[i] : INT32_MAX;
     };
-    gemm_loop(count, a.status, decode, prologue, [&](const Unit& t, uint32_t src, int r, int half, uint32_t out,
+    gemm_loop<TN>(count, a.status, decode, prologue, [&](const Unit& t, uint32_t src, int r, int half, uint32_t out,
                                                      auto release) {
         const int lane = threadIdx.x & 31;
         const int64_t row = t.m0 + r;
-        const int64_t c0 = t.n0 + half * (kTileN / 2);
+        const int64_t c0 = t.n0;
         const uint32_t mine = out + (uint32_t)lane * 128u;
 #pragma unroll 1
-        for (int c = 0; c < kTileN / 2; c += 64) {
+        for (int c = 64 * half; c < TN; c += 128) {
             float v[64];
             __syncwarp();
             tmem_ld64(src + c, v);
@@ -743,13 +756,15 @@ cudaError_t launch_logits(const LogitsArgs& args, bool probs, const void* xp, co
                           cudaStream_t stream) {
     LogitsArgs a = args;
     CUtensorMap mx, mw, mp{};
-    if (!tile_map(&mx, xp, a.Np, a.D, a.D, kCtaM) || !tile_map(&mw, weight, a.V, a.D, a.D, kCtaN) ||
+    if (!tile_map(&mx, xp, a.Np, a.D, a.D, kCtaM) || !tile_map(&mw, weight, a.V, a.D, a.D, a.tn / 2) ||
         (probs && !tile_map(&mp, a.probs, a.Np, a.ldp, a.ldp, 32)))
         return cudaErrorInvalidValue;
-    const void* fn = probs ? reinterpret_cast<const void*>(&logits_kernel<true>)
-                           : reinterpret_cast<const void*>(&logits_kernel<false>);
+    const void* fn = a.tn == kTileN ? (probs ? reinterpret_cast<const void*>(&logits_kernel<true, kTileN>)
+                                             : reinterpret_cast<const void*>(&logits_kernel<false, kTileN>))
+                                    : (probs ? reinterpret_cast<const void*>(&logits_kernel<true, kTileN / 2>)
+                                             : reinterpret_cast<const void*>(&logits_kernel<false, kTileN / 2>));
     if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) return e;
-    const int64_t units = (a.Np / kTileM) * ((a.v1 - a.v0 + kTileN - 1) / kTileN);
+    const int64_t units = (a.Np / kTileM) * ((a.v1 - a.v0 + a.tn - 1) / a.tn);
     void* params[] = {&mx, &mw, &mp, &a};
     return launch_dependent(fn, dim3(2 * cap(units, sms / 2)), dim3(kGemmThreads), params, kGemmSmem, stream, 2);
 }
@@ -763,9 +778,10 @@ cudaError_t launch_grad(const GradArgs& args, const void* probs, int64_t ldp, co
         (a.dxacc && !tile_map(&mdx, a.dxacc, a.splits * a.Np, a.D, a.D, 32, true)) ||
         (a.dweight && !tile_map(&mdw, a.dweight, a.V, a.D, a.D, 32)))
         return cudaErrorInvalidValue;
-    const void* fn = reinterpret_cast<const void*>(&grad_kernel);
+    const void* fn = a.tn == kTileN ? reinterpret_cast<const void*>(&grad_kernel<kTileN>)
+                                    : reinterpret_cast<const void*>(&grad_kernel<kTileN / 2>);
     if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) return e;
-    const int64_t dt = (a.D + kTileN - 1) / kTileN;
+    const int64_t dt = (a.D + a.tn - 1) / a.tn;
     const int64_t units = (a.dxacc ? a.Np / kTileM * dt * a.splits : 0) +
                           (a.dweight ? (a.v1 - a.v0 + kTileM - 1) / kTileM * dt : 0);
     void* params[] = {&mp, &mw, &mx, &mpt, &mdx, &mdw, &a};

@@ -8,9 +8,18 @@
 
 namespace adaln {
 
-// Output tile of a CTA pair's matrix product and its K step; a CTA's share of the operands.
+// Output tile of a CTA pair's matrix product (at most kTileN columns, see tile_cols) and its K
+// step; a CTA's share of the rows.
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
-constexpr int kCtaM = kTileM / 2, kCtaN = kTileN / 2;
+constexpr int kCtaM = kTileM / 2;
+constexpr int kPairs = 76;  // CTA pairs the tiles are shared out to
+// Columns a tile: 256, or 128 where that leaves pairs without one: a pair's product takes the same
+// time a column whatever its rows hold, so a few rows are through sooner in narrower tiles (96 x
+// 8192 x 1024, forward: 14.7 us against 15.4). 64 columns measured 19.8 us: every tile loads all
+// of its rows of the other operand too.
+inline int tile_cols(int64_t row_tiles, int64_t cols) {
+    return row_tiles * ((cols + kTileN - 1) / kTileN) < kPairs ? kTileN / 2 : kTileN;
+}
 // dweight takes what rounding dz of the target left off in fp32 for words that are the target of
 // at most this many rows; over more rows the roundings average out.
 constexpr int kHits = 8;
@@ -54,6 +63,7 @@ struct LogitsArgs {
     int64_t ldp;
     uint32_t* status;
     int64_t Np, D, V, v0, v1;  // columns [v0, v1) of the vocabulary
+    int tn;                 // columns a tile
 };
 
 struct GradArgs {
@@ -67,6 +77,7 @@ struct GradArgs {
     uint32_t* status;
     int64_t Np, D, V, v0, v1;
     int splits;             // parts of dx's K range
+    int tn;                 // columns a tile
 };
 
 struct LseArgs {
