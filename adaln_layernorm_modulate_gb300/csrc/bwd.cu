@@ -32,7 +32,10 @@ namespace adaln {
 // null for 1.
 template <typename T, int NV, bool VARLEN, bool RING, bool FULL, bool WIDE = false, bool SPLIT = false,
           bool AFFINE = false>
-__global__ void __launch_bounds__(SPLIT ? kSplitThreads : WIDE ? kWideThreads : max_threads(NV, Io<T>::VE))
+__global__ void __launch_bounds__(SPLIT                                        ? kSplitThreads
+                                  : WIDE                                       ? kWideThreads
+                                  : AFFINE && NV == 3 && FULL && Io<T>::VE == 4 ? 768  // 85 registers, not 101
+                                                                                : max_threads(NV, Io<T>::VE))
     bwd_kernel(const BwdArgs a) {
     pdl_begin();
     using IO = Io<T>;

@@ -49,10 +49,12 @@ __device__ __forceinline__ float row_shift(const uint4& v) {
 }
 
 // Launch bounds of the affine form: as max_threads, but three and four bf16 vectors a thread are
-// held to 136 and 128 registers, as the modulated form uses by itself (142 for four would leave
-// two CTAs of 160 threads an SM instead of three: bf16 [32760, 5120] 137 us against 115).
+// held to 136 and 128 registers and four fp32 vectors to 72, about what the modulated form uses by
+// itself (142 for four bf16 vectors would leave two CTAs of 160 threads an SM instead of three:
+// [32760, 5120] 137 us against 115).
 __host__ __device__ constexpr int fwd_threads(int nv, int ve, bool affine) {
-    return affine && ve == 8 && nv == 4 ? 512 : affine && ve == 8 && nv == 3 ? 480 : max_threads(nv, ve);
+    if (!affine) return max_threads(nv, ve);
+    return nv == 4 ? (ve == 8 ? 512 : 896) : nv == 3 && ve == 8 ? 480 : max_threads(nv, ve);
 }
 
 // AFFINE: the affine layer norm (dense, one modulation row for all rows): `scale` is the
