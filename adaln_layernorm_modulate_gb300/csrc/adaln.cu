@@ -101,6 +101,11 @@ RowCfg row_cfg(int64_t D, adaln_dtype dtype, bool forward, bool affine = false) 
     // thread where the CTA holds them (D=2040, 8,190 rows: 41.8 us against 49.9 with four; D=680:
     // 33.4 against 38.7). (AdaLN's backward keeps its mapping, and with it its sums' order.)
     if (affine && !forward && !bf16 && target > 2 && ((V + 1) / 2 + 31) / 32 * 32 <= max_threads(2, (int)VE)) target = 2;
+    // Its fp32 forward holds eight vectors a thread only by spilling: four instead (D=2040, 8,190
+    // rows: 29.3 us against 34.0; D=4104, 8,000 rows: 51.5 against 58.4).
+    if (affine && forward && !bf16 && target == 8 && ((V + 3) / 4 + 31) / 32 * 32 <= max_threads(4, (int)VE) &&
+        (V + 31) / 32 > 6)
+        target = 4;
     for (int nv : kNv) {
         if (nv < target) continue;
         const int64_t tpb = ((V + nv - 1) / nv + 31) / 32 * 32;

@@ -33,19 +33,26 @@ namespace adaln {
 
 // The affine layer norm's shift of a row, from its first 16 bytes: their first element where they
 // differ by less than an eighth of it, else 0.
+__device__ __forceinline__ float shift_of(float first, float lo, float hi) {
+    return 8.0f * (hi - lo) < fabsf(first) ? first : 0.0f;
+}
 template <typename T>
-__device__ __forceinline__ float row_shift(const uint4& v) {
-    f2r f[Io<T>::VE / 2];
-    Io<T>::unpackp(v, f);
-    const float2 a = p_get(f[0]);
-    float lo = fminf(a.x, a.y), hi = fmaxf(a.x, a.y);
-#pragma unroll
-    for (int p = 1; p < Io<T>::VE / 2; ++p) {
-        const float2 b = p_get(f[p]);
-        lo = fminf(lo, fminf(b.x, b.y));
-        hi = fmaxf(hi, fmaxf(b.x, b.y));
-    }
-    return 8.0f * (hi - lo) < fabsf(a.x) ? a.x : 0.0f;
+__device__ __forceinline__ float row_shift(const uint4& v);
+template <>
+__device__ __forceinline__ float row_shift<float>(const uint4& v) {
+    const float a = __uint_as_float(v.x), b = __uint_as_float(v.y), c = __uint_as_float(v.z), d = __uint_as_float(v.w);
+    return shift_of(a, fminf(fminf(a, b), fminf(c, d)), fmaxf(fmaxf(a, b), fmaxf(c, d)));
+}
+template <>
+__device__ __forceinline__ float row_shift<__nv_bfloat16>(const uint4& v) {
+    __nv_bfloat162 p[4];
+    p[0] = reinterpret_cast<const __nv_bfloat162&>(v.x);
+    p[1] = reinterpret_cast<const __nv_bfloat162&>(v.y);
+    p[2] = reinterpret_cast<const __nv_bfloat162&>(v.z);
+    p[3] = reinterpret_cast<const __nv_bfloat162&>(v.w);
+    const float2 lo = __bfloat1622float2(__hmin2(__hmin2(p[0], p[1]), __hmin2(p[2], p[3])));
+    const float2 hi = __bfloat1622float2(__hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3])));
+    return shift_of(__low2float(p[0]), fminf(lo.x, lo.y), fmaxf(hi.x, hi.y));
 }
 
 // Launch bounds of the affine form: as max_threads, but three and four bf16 vectors a thread are
