@@ -25,6 +25,11 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// Brings a tensor map of the kernel's parameters to where the first load or store looks for it.
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // ---- tensor memory -------------------------------------------------------------------------
 // One warp of each CTA of the pair allocates `cols` columns (a power of two >= 32) and writes the
 // base address to its shared memory; the same warps give them back.

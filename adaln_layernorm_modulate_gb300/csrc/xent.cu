@@ -72,9 +72,18 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
     };
     // Rows that count before r0.
     int n = 0;
-    for (int64_t r = tid; r < r0; r += kPackThreads) {
+    int64_t first = tid;
+    for (; first + 7 * kPackThreads < r0; first += 8 * kPackThreads) {  // eight loads on their way
+        int64_t t[8];
+        bool on[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) on[i] = counts(first + i * kPackThreads, t + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n += on[i] ? 1 : 0;
+    }
+    for (; first < r0; first += kPackThreads) {
         int64_t t;
-        n += counts(r, &t) ? 1 : 0;
+        n += counts(first, &t) ? 1 : 0;
     }
     for (int o = 16; o >= 1; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
     if (lane == 0) warp_tot[warp] = n;
@@ -358,6 +367,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                                                               const __grid_constant__ CUtensorMap mp,
                                                               const LogitsArgs a) {
     pdl_trigger();
+    if (threadIdx.x == 0) {
+        tma_prefetch_map(&mx);
+        tma_prefetch_map(&mw);
+        if (PROBS) tma_prefetch_map(&mp);
+    }
     int64_t nact = 0;
     uint32_t mt = 0;  // tile counts are 32 bits (checked on the host): their quotients are cheap
     const uint32_t nt = (uint32_t)((a.v1 - a.v0 + TN - 1) / TN);
@@ -496,6 +510,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
                                                             const __grid_constant__ CUtensorMap mdw,
                                                             const GradArgs a) {
     pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (const CUtensorMap* m : {&mp, &mw, &mx, &mpt}) tma_prefetch_map(m);
+        if (a.dxacc) tma_prefetch_map(&mdx);
+        if (a.dweight) tma_prefetch_map(&mdw);
+    }
     int64_t nact = 0;
     uint32_t per = 0, ndx = 0;  // units of one part of dx, and of all
     const uint32_t dt = (uint32_t)((a.D + TN - 1) / TN);
@@ -643,6 +662,10 @@ __global__ void __launch_bounds__(1024) lse_kernel(const LseArgs a) {
     for (int64_t t = blockIdx.x; t * 32 < nact; t += gridDim.x) {
         const int64_t row = t * 32 + lane;
         const int64_t p0 = (int64_t)g * a.nparts / 32, p1 = (int64_t)(g + 1) * a.nparts / 32;
+        const int64_t mine = t * 32 + g;  // the row this warp joins below
+        const bool own = mine < nact && ADALN_IN_LOSS(mine < a.Np);
+        const int64_t r = own ? a.row[mine] : 0;
+        const float zt = own ? a.zt[mine] : 0.0f;
         float m = neg_inf(), s = 0.0f;
         if (row < nact && ADALN_IN_LOSS(row < a.Np)) {
             const float2* part = a.parts + row;
@@ -664,14 +687,10 @@ __global__ void __launch_bounds__(1024) lse_kernel(const LseArgs a) {
         const float mm = m == neg_inf() ? 0.0f : m;
         s = q.y * exp2_ftz((q.x - mm) * kLog2e);
         for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        const int64_t mine = t * 32 + g;
-        if (lane == 0 && mine < nact && ADALN_IN_LOSS(mine < a.Np)) {
+        if (lane == 0 && own && ADALN_IN_LOSS(r >= 0 && r < a.N)) {
             const float lse = m + logf(s);
-            const int64_t r = a.row[mine];
-            if (ADALN_IN_LOSS(r >= 0 && r < a.N)) {
-                a.lse[r] = lse;
-                a.loss[r] = lse - a.zt[mine];
-            }
+            a.lse[r] = lse;
+            a.loss[r] = lse - zt;
         }
         __syncthreads();
     }
@@ -684,30 +703,29 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxArgs a) {
     const int64_t nact = *a.nact, vecs = a.D / 8;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < nact * vecs; i += (int64_t)gridDim.x * 256) {
         const int64_t p = i / vecs, v = i % vecs;
+        if (!ADALN_IN_LOSS(p < a.Np)) continue;
+        const int64_t r = a.row[p];
+        const float rest = a.row_lo[p];
+        const uint4 word = ld_keep(reinterpret_cast<const uint4*>(a.weight) + a.tgt[p] * vecs + v);
         float s[8] = {};
         for (int k = 0; k < a.splits; ++k) {
-            if (!ADALN_IN_LOSS(p < a.Np)) continue;
             const float4* src = reinterpret_cast<const float4*>(a.dxacc + ((int64_t)k * a.Np + p) * a.D + v * 8);
             const float4 lo = src[0], hi = src[1];
             s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
             s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
         }
-        if (ADALN_IN_LOSS(p < a.Np)) {
-            const float lo = a.row_lo[p];
-            f2r t[4];
-            Io<__nv_bfloat16>::unpackp(ld_keep(reinterpret_cast<const uint4*>(a.weight) + a.tgt[p] * vecs + v), t);
+        f2r t[4];
+        Io<__nv_bfloat16>::unpackp(word, t);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = p_get(t[j]);
-                s[2 * j] = fmaf(lo, f.x, s[2 * j]);
-                s[2 * j + 1] = fmaf(lo, f.y, s[2 * j + 1]);
-            }
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = p_get(t[j]);
+            s[2 * j] = fmaf(rest, f.x, s[2 * j]);
+            s[2 * j + 1] = fmaf(rest, f.y, s[2 * j + 1]);
         }
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(s[2 * j + 1]), "f"(s[2 * j]));
-        const int64_t r = a.row[p];
         if (ADALN_IN_LOSS(r >= 0 && r < a.N))
             reinterpret_cast<uint4*>(a.dx)[r * vecs + v] = make_uint4(w[0], w[1], w[2], w[3]);
     }
