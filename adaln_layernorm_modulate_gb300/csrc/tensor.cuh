@@ -25,6 +25,14 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// One lane of the warp (all of whose lanes are here), the same every time. Code that issues loads
+// and products keeps the whole warp in its loops and lets this lane issue: the loops' values then
+// stay warp-uniform, where a branch for one lane moves each operand to a uniform register anew.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
 // Brings a tensor map of the kernel's parameters to where the first load or store looks for it.
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");

@@ -234,28 +234,28 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
     pdl_wait();
     const uint32_t units = count();
 
-    if (warp == 0 || warp == 3) {
+    const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);  // the warp's number, known to be uniform
+    if (role == 0 || role == 3) {
         // Warp 0 loads this CTA's half of A, warp 3 its half of B, both into the same stages: one
         // thread issuing both is late (the loads of an MN-major operand are one a 64 columns).
-        if (lane == 0) {
-            fence_async_proxy();
-            const bool is_b = warp == 3;
-            int s = 0;
-            uint32_t lap = 0;
-            bool live = true;
-            for (uint32_t u = first; live && u < units; u += step) {
-                const Unit t = decode(u);
-                const CUtensorMap* map = is_b ? t.mb : t.ma;
-                const int x0 = is_b ? (int)t.n0 + (int)rank * (TN / 2) : (int)t.m0 + (int)rank * kCtaM;
-                const int blocks = !(is_b ? t.b_mn : t.a_mn) ? 0 : is_b ? TN / 128 : kCtaM / 64;
-                int k = (int)(is_b ? t.kb0 : t.k0);
-                for (int i = 0; i < t.iters; ++i, k += kTileK) {
-                    if (lap > 0 && !mbar_wait_bounded(empty + 8u * s, (lap - 1) & 1u, &abort_flag)) {
-                        live = false;
-                        break;
-                    }
-                    const uint32_t bar = cluster_map(full + 8u * s, 0);
-                    const uint32_t dst = data + s * kStageBytes + (is_b ? kABytes : 0u);
+        fence_async_proxy();
+        const bool is_b = role == 3;
+        const uint32_t base = data + (is_b ? kABytes : 0u), bars0 = cluster_map(full, 0);
+        int s = 0;
+        uint32_t lap = 0;
+        bool live = true;
+        for (uint32_t u = first; live && u < units; u += step) {
+            const Unit t = decode(u);
+            const CUtensorMap* map = is_b ? t.mb : t.ma;
+            const int x0 = is_b ? (int)t.n0 + (int)rank * (TN / 2) : (int)t.m0 + (int)rank * kCtaM;
+            const int blocks = !(is_b ? t.b_mn : t.a_mn) ? 0 : is_b ? TN / 128 : kCtaM / 64;
+            int k = (int)(is_b ? t.kb0 : t.k0);
+            for (int i = 0; i < t.iters; ++i, k += kTileK) {
+                // The lanes go on together or stop together.
+                live = __all_sync(0xFFFFFFFFu, lap == 0 || mbar_wait_bounded(empty + 8u * s, (lap - 1) & 1u, &abort_flag));
+                if (!live) break;
+                if (elect_lane()) {
+                    const uint32_t bar = bars0 + 8u * s, dst = base + s * kStageBytes;
                     if (rank == 0 && !is_b)
                         mbar_arrive_expect_tx(full + 8u * s, 2 * kABytes + (uint32_t)TN * kTileK * 2);
                     if (blocks == 0) {
@@ -264,68 +264,74 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
                         tma_load(dst, map, x0, k, bar);
                         if (blocks == 2) tma_load(dst + kMnBlock, map, x0 + 64, k, bar);
                     }
-                    if (++s == kGemmStages) {
-                        s = 0;
-                        ++lap;
-                    }
                 }
-            }
-            // After a timeout, copies may still be on their way into the pair's memory: CTA 0 gives
-            // each stage's last ones a further bounded wait, CTA 1 meets it at the cluster barrier.
-            if (rank == 0 && !is_b && *(volatile int*)&abort_flag) {
-                volatile int never = 0;
-                for (int q = 0; q < kGemmStages; ++q) {
-                    if (q >= s && lap == 0) continue;
-                    const uint32_t last = q < s ? lap : lap - 1;
-                    mbar_wait_bounded(full + 8u * q, last & 1u, &never);
+                if (++s == kGemmStages) {
+                    s = 0;
+                    ++lap;
                 }
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        // After a timeout, copies may still be on their way into the pair's memory: CTA 0 gives
+        // each stage's last ones a further bounded wait, CTA 1 meets it at the cluster barrier.
+        if (rank == 0 && !is_b && lane == 0 && *(volatile int*)&abort_flag) {
+            volatile int never = 0;
+            for (int q = 0; q < kGemmStages; ++q) {
+                if (q >= s && lap == 0) continue;
+                const uint32_t last = q < s ? lap : lap - 1;
+                mbar_wait_bounded(full + 8u * q, last & 1u, &never);
+            }
+        }
+    } else if (role == 1) {
+        if (rank == 0) {
+            // Descriptors of stage 0; a stage and a K step move the address field (the low bits).
+            const uint64_t da0 = smem_desc(data, kMnBlock), db0 = smem_desc(data + kABytes, kMnBlock);
             int s = 0, acc = 0;
             uint32_t lap = 0, alap = 0;
-            bool live = true;
+            bool live = true, issued = false;
             for (uint32_t u = first; live && u < units; u += step) {
                 const Unit t = decode(u);
                 const uint32_t idesc = mma_desc(kTileM, TN, t.a_mn, t.b_mn);
                 // 16 k: 32 bytes of a K-major row, 16 rows of an MN-major tile.
                 const uint32_t ak = (t.a_mn ? 2048u : 32u) >> 4, bk = (t.b_mn ? 2048u : 32u) >> 4;
-                if (alap > 0 && !mbar_wait_cluster_bounded(aempty + 8u * acc, (alap - 1) & 1u, &abort_flag))
-                    break;
+                live = __all_sync(0xFFFFFFFFu, alap == 0 || mbar_wait_cluster_bounded(aempty + 8u * acc,
+                                                                                      (alap - 1) & 1u, &abort_flag));
+                if (!live) break;
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)acc * kTileN;
                 for (int i = 0; i < t.iters; ++i) {
-                    if (!mbar_wait_cluster_bounded(full + 8u * s, lap & 1u, &abort_flag)) {
-                        live = false;
-                        break;
-                    }
+                    live = __all_sync(0xFFFFFFFFu, mbar_wait_cluster_bounded(full + 8u * s, lap & 1u, &abort_flag));
+                    if (!live) break;
                     tc_fence_after();
-                    const uint32_t as = data + s * kStageBytes;
-                    const uint64_t da = smem_desc(as, kMnBlock), db = smem_desc(as + kABytes, kMnBlock);
+                    if (elect_lane()) {
+                        const uint64_t off = (uint64_t)(uint32_t)(s * (int)(kStageBytes >> 4));
+                        const uint64_t da = da0 + off, db = db0 + off;
 #pragma unroll
-                    for (int k = 0; k < kTileK / 16; ++k)
-                        mma_bf16(d, da + (uint64_t)(k * ak), db + (uint64_t)(k * bk), idesc, i > 0 || k > 0);
-                    mma_commit(empty + 8u * s);
+                        for (int k = 0; k < kTileK / 16; ++k)
+                            mma_bf16(d, da + (uint64_t)(k * ak), db + (uint64_t)(k * bk), idesc, i > 0 || k > 0);
+                        mma_commit(empty + 8u * s);
+                    }
+                    issued = true;
                     if (++s == kGemmStages) {
                         s = 0;
                         ++lap;
                     }
                 }
                 if (!live) break;
-                mma_commit(afull + 8u * acc);
+                if (elect_lane()) mma_commit(afull + 8u * acc);
                 if (++acc == kAccs) {
                     acc = 0;
                     ++alap;
                 }
             }
-            if (*(volatile int*)&abort_flag) {  // products in flight end before their memory is given back
+            __syncwarp();
+            // After a timeout, products in flight end before their memory is given back.
+            if (__any_sync(0xFFFFFFFFu, issued && *(volatile int*)&abort_flag != 0) && elect_lane()) {
                 volatile int never = 0;
                 mma_commit(drain);
                 mbar_wait_bounded(drain, 0, &never);
             }
         }
-    } else if (warp >= kEpiWarp) {
+    } else if (role >= kEpiWarp) {
         const int q = warp & 3, half = (warp - kEpiWarp) >> 2;
         const uint32_t out = data + kGemmStages * kStageBytes + (uint32_t)(warp - kEpiWarp) * kOutBytes;
         int acc = 0;
