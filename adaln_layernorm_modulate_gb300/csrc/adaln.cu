@@ -917,10 +917,10 @@ XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
     p.tng = tile_cols(p.Np / kTileM + p.piece / kTileM, D);
     // dx sums over a piece's columns, dweight over the rows: with few rows the dx tiles are few
     // and long. They are split until one is no longer than an SM pair's share of all the K steps (at
-    // least 16 of them, below which filling the pipeline costs more).
+    // least 8 of them: 1 x 1000 x 512 backward 16.8 us with 8, 17.9 with 16).
     const int64_t dt = (D + p.tng - 1) / p.tng, mt = p.Np / kTileM, kv = p.piece / kTileK;
     const int64_t steps = mt * dt * kv + p.piece / kTileM * dt * (p.Np / kTileK);
-    const int64_t share = std::max<int64_t>(steps / kPairs, 16);
+    const int64_t share = std::max<int64_t>(steps / kPairs, 8);
     p.splits = (int)std::min<int64_t>(std::max<int64_t>((kv + share - 1) / share, 1), 16);
     if (p.Np > INT32_MAX / p.splits) p.splits = 1;  // rows of the fp32 dx are 32-bit coordinates
     size_t at = kPartialsOffset;
