@@ -130,8 +130,15 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
                 const uint4* src = reinterpret_cast<const uint4*>(a.x) + (c0 + i) * vecs;
                 uint4* dst = reinterpret_cast<uint4*>(a.xp) + (int64_t)to * vecs;
                 if (!ADALN_IN_LOSS(c0 + i < a.N && to < a.Np)) continue;
-#pragma unroll 4
-                for (int64_t v = lane; v < vecs; v += 32) dst[v] = ld_stream(src + v);
+                int64_t v = lane;
+                for (; v + 7 * 32 < vecs; v += 8 * 32) {  // eight loads on their way
+                    uint4 q[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) q[j] = ld_stream(src + v + 32 * j);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) dst[v + 32 * j] = q[j];
+                }
+                for (; v < vecs; v += 32) dst[v] = ld_stream(src + v);
             } else if (a.dx) {
                 uint4* dst = reinterpret_cast<uint4*>(a.dx) + (c0 + i) * vecs;
                 for (int64_t v = lane; v < vecs; v += 32)

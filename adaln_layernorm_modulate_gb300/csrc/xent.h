@@ -24,7 +24,7 @@ inline int tile_cols(int64_t row_tiles, int64_t cols) {
 // at most this many rows; over more rows the roundings average out.
 constexpr int kHits = 8;
 constexpr int kPackThreads = 256;
-constexpr int kPackCtas = 304;  // two per SM: every CTA also counts the rows before its own
+constexpr int kPackCtas = 608;  // four per SM: every CTA also counts the rows before its own
 
 struct PackArgs {
     const void* x;          // [N, D]
