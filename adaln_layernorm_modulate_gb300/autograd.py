@@ -1,4 +1,4 @@
-"""Autograd node over libadaln: the fused AdaLN (LayerNorm-Modulate) operator of the
+"""Autograd nodes over libadaln. First the fused AdaLN (LayerNorm-Modulate) operator of the
 AdaptiveLoad technical summary, section 2.B, as one forward launch and one backward call
 (fused dx + D-tile partials, then the fixed-order reduce) in a PyTorch graph.
 
@@ -16,6 +16,9 @@ step runs in the library's kernels; this module only allocates outputs and works
 through PyTorch's allocator and passes pointers. dshift and dscale come out of the
 library in fp32; autograd wants gradients in the parameters' dtype, so they are rounded
 once to it (a no-op for fp32 parameters).
+
+Then the end of such a network: the affine layer norm (``layer_norm``, ``LayerNorm``) and the
+vocabulary loss without its logits (``linear_cross_entropy``).
 """
 from __future__ import annotations
 

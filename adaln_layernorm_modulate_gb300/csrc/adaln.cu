@@ -887,8 +887,8 @@ namespace {
 
 // Pieces of the vocabulary in the backward: dz of one piece is at most this large unless a
 // piece would be narrower than kMinPiece columns. Each piece adds to the fp32 dx once more and ends
-// in a partly filled wave: 8192 x 50257 x 2048, backward: 64 MiB 3.68 ms, 128 MiB 3.45 ms, 256 MiB
-// 3.15 ms, 512 MiB 3.20 ms.
+// in a partly filled wave: 8192 x 50257 x 2048, backward: 64 MiB 3.3 ms, 128 MiB 3.0 ms, 256 MiB
+// 2.9 ms, 512 MiB 2.8 ms.
 constexpr int64_t kProbsBytes = (int64_t)256 << 20;
 constexpr int64_t kMinPiece = 2048;
 

@@ -161,6 +161,29 @@ def test_several_pieces_of_the_vocabulary():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,V,D,ignored", [(8192, 20001, 72, 0.3), (2049, 70000, 136, 0.0)])
+def test_dz_in_several_pieces(N, V, D, ignored):
+    # dz of the whole vocabulary would take more than the 256 MiB of a piece: dx adds up over
+    # launches, dweight comes piece by piece, the last one narrower.
+    assert N * V * 2 > 256 << 20
+    x, w, t, up, ul = inputs(N, V, D, ignored, seed=20)
+    t[0], t[1], t[2] = 0, V - 1, V // 2
+    full = call(x, w, t, up, ul)
+    check(x, w, t, up, ul, full)
+    assert torch.equal(call(x, w, t, up, ul, want_w=False)[2], full[2])
+    assert torch.equal(call(x, w, t, up, ul, want_x=False)[3], full[3])
+
+
+@pytest.mark.gpu
+def test_many_rows_of_one_word():
+    # A word that is every other row's target: more rows than dweight corrects one by one.
+    x, w, t, up, ul = inputs(1500, 3000, 136, 0.1, seed=21)
+    t[::2] = 77
+    t[1:9] = 78  # eight rows and some chance ones: at and past the limit
+    check(x, w, t, up, ul, call(x, w, t, up, ul))
+
+
+@pytest.mark.gpu
 def test_what_rows_without_a_loss_hold_does_not_matter():
     x, w, t, up, ul = inputs(140, 900, 128, 0.4, seed=10)
     want = call(x, w, t, up, ul)
