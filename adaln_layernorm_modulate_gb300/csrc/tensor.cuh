@@ -105,6 +105,13 @@ __device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.w
 // This thread's shared-memory writes before what the async proxy reads after.
 __device__ __forceinline__ void fence_shared_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Arrives on an mbarrier of either CTA of the pair without publishing this thread's memory writes:
+// what it announces is that an accumulator has been read (tensor memory, ordered by the fences
+// above). A releasing arrival waits for the epilogue's stores, 1000 cycles and more a tile.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // ---- matrix products -----------------------------------------------------------------------
 // Shared-memory operand descriptor, 128-byte swizzle (rows of 128 bytes, groups of 8 rows 1024
 // bytes apart; `addr` is 1024-byte aligned plus a K step within the first rows).

@@ -361,7 +361,7 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
             epilogue(t, src, (int)rank * kCtaM + q * 32 + lane, half, out, [&]() {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(cluster_map(aempty + 8u * acc, 0));
+                if (lane == 0) mbar_arrive_relaxed(cluster_map(aempty + 8u * acc, 0));
             });
             if (++acc == kAccs) {
                 acc = 0;
@@ -416,10 +416,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
     const int lane = threadIdx.x & 31;
     const int64_t rank0 = (int64_t)cluster_ctarank() * kCtaM;
     int tgt = -1;
+    int64_t mine = -1;
     [[maybe_unused]] float lse2 = 0.0f, gs = 0.0f, gt = 0.0f;
     auto prologue = [&](const Unit& t) {
         const int64_t row = t.m0 + rank0 + (threadIdx.x & 127);
-        if (!ADALN_IN_LOSS(row < a.Np)) return;
+        if (row == mine || !ADALN_IN_LOSS(row < a.Np)) return;
+        mine = row;
         tgt = a.tgt[row];
         if constexpr (PROBS) {
             lse2 = a.row_lse2[row];
