@@ -18,7 +18,7 @@
 //
 // Bound by the tensor cores from a few hundred rows on: 8192 rows, 50,257 words, D = 2048 take
 // 0.81 ms forward (2.1 PFLOP/s, the tensor pipe 97% active) and 2.8 ms backward; with a few rows by
-// the chain of launches (1 row, 1000 words, D = 512: 9.7 us forward, 17 us backward on the device).
+// the chain of launches (1 row, 1000 words, D = 512: 9.4 us forward, 16.5 us backward on the device).
 #include "tensor.cuh"
 #include "xent.h"
 
@@ -383,7 +383,7 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
 
 // The tile's logits, as row statistics (PROBS false) or as dz (PROBS true). Tiles of all rows first:
 // x stays in L2 and the weight is read once. 8192 x 50257 x 2048: 793 us for the statistics (2.13
-// PFLOP/s); dz, whose epilogue also writes 0.8 GB through shared memory, 925 us (1.82 PFLOP/s).
+// PFLOP/s); dz, whose epilogue also writes 0.8 GB through shared memory, 909 us (1.86 PFLOP/s).
 template <bool PROBS, int TN>
 __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_constant__ CUtensorMap mx,
                                                               const __grid_constant__ CUtensorMap mw,
