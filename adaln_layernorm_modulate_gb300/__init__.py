@@ -130,6 +130,9 @@ def _ptr(t: Any) -> int:
 def _stream(s: Any) -> int:
     if s is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 1 us less than a Stream object
+        if raw is not None:
+            return int(raw(torch.cuda.current_device()))
         return int(torch.cuda.current_stream().cuda_stream)
     if isinstance(s, int):
         return s

@@ -19,6 +19,8 @@
 // Bound by the tensor cores from a few hundred rows on: 8192 rows, 50,257 words, D = 2048 take
 // 0.81 ms forward (2.1 PFLOP/s, the tensor pipe 97% active) and 2.8 ms backward; with a few rows by
 // the chain of launches (1 row, 1000 words, D = 512: 9.4 us forward, 16.5 us backward on the device).
+#include <atomic>
+
 #include "tensor.cuh"
 #include "xent.h"
 
@@ -763,6 +765,18 @@ namespace {
 
 unsigned cap(int64_t want, int64_t most) { return (unsigned)(want < 1 ? 1 : want < most ? want : most); }
 
+// Lets kernel variant `which` use its shared memory, once a device.
+cudaError_t allow_gemm_smem(const void* fn, int which) {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> done[kDevices][6];
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev >= 0 && dev < kDevices && done[dev][which].load(std::memory_order_acquire)) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
+    if (e == cudaSuccess && dev >= 0 && dev < kDevices) done[dev][which].store(true, std::memory_order_release);
+    return e;
+}
+
 // Tiled tensor map of a row-major bf16 (or fp32) [rows, cols] matrix (row stride ld elements),
 // boxes of 128 bytes of a row by `box_rows` rows, 128-byte swizzle.
 bool tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows,
@@ -808,7 +822,7 @@ cudaError_t launch_logits(const LogitsArgs& args, bool probs, const void* xp, co
                                              : reinterpret_cast<const void*>(&logits_kernel<false, kTileN>))
                                     : (probs ? reinterpret_cast<const void*>(&logits_kernel<true, kTileN / 2>)
                                              : reinterpret_cast<const void*>(&logits_kernel<false, kTileN / 2>));
-    if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) return e;
+    if (cudaError_t e = allow_gemm_smem(fn, (a.tn == kTileN ? 0 : 1) + (probs ? 2 : 0))) return e;
     const int64_t units = (a.Np / kTileM) * ((a.v1 - a.v0 + a.tn - 1) / a.tn);
     void* params[] = {&mx, &mw, &mp, &a};
     return launch_dependent(fn, dim3(2 * cap(units, sms / 2)), dim3(kGemmThreads), params, kGemmSmem, stream, 2);
@@ -825,7 +839,7 @@ cudaError_t launch_grad(const GradArgs& args, const void* probs, int64_t ldp, co
         return cudaErrorInvalidValue;
     const void* fn = a.tn == kTileN ? reinterpret_cast<const void*>(&grad_kernel<kTileN>)
                                     : reinterpret_cast<const void*>(&grad_kernel<kTileN / 2>);
-    if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem)) return e;
+    if (cudaError_t e = allow_gemm_smem(fn, a.tn == kTileN ? 4 : 5)) return e;
     const int64_t dt = (a.D + a.tn - 1) / a.tn;
     const int64_t units = (a.dxacc ? a.Np / kTileM * dt * a.splits : 0) +
                           (a.dweight ? (a.v1 - a.v0 + kTileM - 1) / kTileM * dt : 0);
