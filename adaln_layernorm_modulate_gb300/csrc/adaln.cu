@@ -1075,6 +1075,7 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
         LogitsArgs g{};
         g.nact = k.nact;
         g.tgt = k.tgt;
+        g.xp = at<__nv_bfloat16>(workspace, p.xp);
         g.row_lse2 = k.row_lse2;
         g.row_gs = k.row_gs;
         g.row_gt = k.row_gt;

@@ -48,6 +48,18 @@ __device__ __forceinline__ float exp2_ftz(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The bits of d as bf16, rounded away from zero where the draw's upper half is beyond the share of
+// the step that is left, else towards it. The draw comes from what the row holds, not from its
+// place: a row's dx is the same wherever the row stands.
+__device__ __forceinline__ uint32_t target_dz(float d, uint32_t draw) {
+    if (d != d) return 0x7FC0u;
+    return (__float_as_uint(d) + (draw >> 16)) >> 16;
+}
+// A multiplicative hash, twice (the golden ratio's odd multiplier).
+__device__ __forceinline__ uint32_t spread(uint32_t h) {
+    h = (h ^ h >> 16) * 0x9E3779B9u;
+    return (h ^ h >> 15) * 0x9E3779B9u;
+}
 // The epilogue warps' own barrier; true if `ok` is, in all of them.
 __device__ __forceinline__ bool epilogue_all(bool ok) {
     uint32_t r;
@@ -420,6 +432,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
     int tgt = -1;
     int64_t mine = -1;
     [[maybe_unused]] float lse2 = 0.0f, gs = 0.0f, gt = 0.0f;
+    [[maybe_unused]] uint32_t draw = 0;
     auto prologue = [&](const Unit& t) {
         const int64_t row = t.m0 + rank0 + (threadIdx.x & 127);
         if (row == mine || !ADALN_IN_LOSS(row < a.Np)) return;
@@ -429,6 +442,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
             lse2 = a.row_lse2[row];
             gs = a.row_gs[row];
             gt = a.row_gt[row];
+            const uint4 first = *reinterpret_cast<const uint4*>(a.xp + row * a.D);
+            draw = spread(spread(spread(spread(first.x ^ __float_as_uint(lse2)) + first.y) + first.z) + first.w);
         }
     };
     gemm_loop<TN>(count, a.status, decode, prologue, [&](const Unit& t, uint32_t src, int r, int half,
@@ -483,15 +498,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(p.y), "f"(p.x));
                 }
                 if (hit >= 0) {
-                    // The target's dz, often most of the row's and of its word's gradient: what its
-                    // rounding leaves off is kept and added to both in fp32.
+                    // The target's dz: what its rounding leaves off is kept.
                     const float d = exp2_ftz(fmaf(zt, kLog2e, -lse2)) * gs - gt;
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(d);
-                    const uint32_t bits = __bfloat16_as_ushort(hi);
+                    const uint32_t bits = target_dz(d, draw);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (j == hit >> 1) w[j] = hit & 1 ? (w[j] & 0xFFFFu) | bits << 16 : (w[j] & 0xFFFF0000u) | bits;
-                    if (in) a.row_lo[row] = d - __bfloat162float(hi);
+                    if (in) a.row_lo[row] = d - __uint_as_float(bits << 16);
                     if (in && a.word_hits && ADALN_IN_LOSS(tgt < a.V)) {
                         const int k = atomicAdd(a.word_hits + tgt, 1);
                         if (k < kHits) a.word_rows[(int64_t)tgt * kHits + k] = (int32_t)row;

@@ -20,7 +20,7 @@ inline int tile_cols(int64_t row_tiles, int64_t cols) {
     return row_tiles * ((cols + kTileN - 1) / kTileN) < kPairs ? kTileN / 2 : kTileN;
 }
 // dweight takes what rounding dz of the target left off in fp32 for words that are the target of
-// at most this many rows; over more rows the roundings average out.
+// at most this many rows; over more rows the roundings, made by chance (target_dz), average out.
 constexpr int kHits = 8;
 constexpr int kPackThreads = 256;
 constexpr int kPackCtas = 608;  // four per SM: every CTA also counts the rows before its own
@@ -52,7 +52,8 @@ struct LogitsArgs {
     const int32_t* tgt;
     float2* parts;          // statistics: [2 * tiles][Np] (max, sum exp)
     float* zt;              // statistics: [Np], the target's logit
-    const float* row_lse2;  // dz
+    const __nv_bfloat16* xp;  // dz: packed rows [Np, D]
+    const float* row_lse2;
     const float* row_gs;
     const float* row_gt;
     float* row_lo;          // dz: [Np], what rounding dz of the target left off

@@ -357,3 +357,28 @@ def test_outputs_stay_inside_their_buffers():
     check(x, w, t, up, ul, (loss, lse, dx.view(N, D), dw.view(V, D)))
     for whole, part in bufs:
         assert (whole[:guard] == 7).all() and (whole[guard + part.numel():] == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [255, 1020])
+def test_equal_target_gradients_leave_no_scale_error(N):
+    # A mean's dloss: the same for all rows, and with small probabilities dz of the target nearly so.
+    # (1 - p) / N lies almost halfway between two bf16 values here. Half of the rows have one word
+    # as their target; a rounding that goes the same way in all of them would scale its gradient.
+    V, D, word, n = 3000, 512, 77, (N + 1) // 2
+    g = torch.Generator("cuda").manual_seed(22)
+    x = (torch.randn(1, D, generator=g, device="cuda") + 0.5 * torch.randn(N, D, generator=g, device="cuda")).bfloat16()
+    w = (0.2 / D ** 0.5 * torch.randn(V, D, generator=g, device="cuda")).bfloat16()
+    t = torch.randint(V, (N,), generator=g, device="cuda")
+    t[::2] = word
+    up = torch.full((N,), 1.0 / N, device="cuda")
+    got = call(x, w, t, up, None)
+    check(x, w, t, up, None, got)
+    z = x.double() @ w.double().t()
+    dz = torch.exp(z - torch.logsumexp(z, 1, keepdim=True))[:, word] * up.double()
+    dz[t == word] -= up[0].double()
+    ref = dz @ x.double()
+    # A rounding of a row's dz errs by up to a step (2 H), either way: the deviation of their sum is
+    # H / sqrt(n) of it; that of the result's own D roundings, along the result, H / sqrt(D). Four of each.
+    scale = (got[3][word].double() @ ref) / (ref @ ref) - 1
+    assert scale.abs() <= 4 * H * (n ** -0.5 + D ** -0.5) < 0.9 * H  # to nearest it is 0.9 H
