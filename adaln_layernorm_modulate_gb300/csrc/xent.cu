@@ -479,11 +479,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                 const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 // A chunk with no finite value at all adds nothing (and NaN is kept below).
                 const float mm = m == neg_inf() ? 0.0f : m;
-                const f2r m2 = p_splat(-mm * kLog2e);
+                const f2r m2 = p_splat(-mm);
                 f2r s[2] = {kPairZero, kPairZero};
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    const float2 e = p_get(p_fma(p_make(v[2 * j], v[2 * j + 1]), l2e, m2));
+                    // The difference first: the maximum's exponential is exactly 1.
+                    const float2 e = p_get(p_mul(p_add(p_make(v[2 * j], v[2 * j + 1]), m2), l2e));
                     s[j & 1] = p_add(s[j & 1], p_make(exp2_ftz(e.x), exp2_ftz(e.y)));
                 }
                 sum = sum * exp2_ftz((top - mm) * kLog2e) + p_hsum(p_add(s[0], s[1]));
@@ -730,9 +731,11 @@ __global__ void __launch_bounds__(1024) lse_kernel(const LseArgs a) {
         s = q.y * exp2_ftz((q.x - mm) * kLog2e);
         for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
         if (lane == 0 && own && ADALN_IN_LOSS(r >= 0 && r < a.N)) {
-            const float lse = m + logf(s);
-            a.lse[r] = lse;
-            a.loss[r] = lse - zt;
+            // The loss not as lse - zt: where the target's logit is the maximum (or near it), lse has
+            // rounded away what is left of it. As it is here it is never negative.
+            const float l = logf(s);
+            a.lse[r] = m + l;
+            a.loss[r] = (m - zt) + l;
         }
         __syncthreads();
     }

@@ -6,6 +6,8 @@ each off by at most 2^-22 of the sum of the terms' absolute values (two units of
 the direction of its rounding). The exponentials are good to 2^-20 relative (their argument, at
 most 30 or so, is rounded to fp32). dz is rounded to bf16 (h of its value), dx and dweight once;
 below 2^-126, the smallest normal value of fp32 and bf16 alike, any of them may be 0 instead."""
+import math
+
 import pytest
 import torch
 
@@ -382,3 +384,46 @@ def test_equal_target_gradients_leave_no_scale_error(N):
     # H / sqrt(n) of it; that of the result's own D roundings, along the result, H / sqrt(D). Four of each.
     scale = (got[3][word].double() @ ref) / (ref @ ref) - 1
     assert scale.abs() <= 4 * H * (n ** -0.5 + D ** -0.5) < 0.9 * H  # to nearest it is 0.9 H
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [1, 2, 300, 5000])
+def test_losses_of_confident_rows(V):
+    # All logits are 16384 but the target's, 6 to 13 more: lse has steps of 2^-9 there, the loss,
+    # log(1 + (V - 1) exp(-6 ..)), must not. The products are sums of small integers: exact.
+    N, D = 40, 64
+    t = torch.arange(N, device="cuda") % min(V, 8)
+    x = torch.zeros(N, D, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = w[:, 0] = 128
+    x[torch.arange(N, device="cuda"), 1 + t] = 1
+    for k in range(min(V, 8)):
+        w[k, 1 + k] = 6 + k
+    loss, _ = call(x, w, t, torch.ones(N, device="cuda"), None, backward=False)
+    z = x.double() @ w.double().t()
+    want = torch.logsumexp(z, 1) - z.gather(1, t[:, None]).squeeze(1)
+    # The sum is 1 and the others: exponentials good to 2^-20 and at most V / 16 + 64 additions, then
+    # a logarithm and its result, and a difference of the maximum, which is exact.
+    assert (loss >= 0).all()
+    rel = 2.0 ** -20 + 2.0 ** -24 * (V / 16 + 64)
+    assert ((loss.double() - want).abs() <= rel + 2.0 ** -22 * want).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("power", [10, 20, 60])
+def test_losses_of_very_large_logits(power):
+    # Logits of 2^20, 2^40 and 2^120, exact: two words share the maximum of every row, the others lie
+    # at half of it and at its negative.
+    N, V, D = 20, 130, 64
+    x = torch.zeros(N, D, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    x[:, 3] = 2.0 ** power
+    w[:, 3] = -(2.0 ** power)
+    w[70:, 3] = 2.0 ** (power - 1)
+    w[5, 3] = w[101, 3] = 2.0 ** power
+    t = torch.tensor([5, 101, 80, 7], device="cuda").repeat(5)
+    loss, lse = call(x, w, t, torch.ones(N, device="cuda"), None, backward=False)
+    top = 2.0 ** (2 * power)
+    want = (torch.tensor([0.0, 0.0, top / 2, 2 * top], dtype=torch.float64, device="cuda") + math.log(2.0)).repeat(5)
+    assert ((loss.double() - want).abs() <= 2.0 ** -22 * want).all()
+    assert ((lse.double() - (top + math.log(2.0))).abs() <= 2.0 ** -22 * top).all()
