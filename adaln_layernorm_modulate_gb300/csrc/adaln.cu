@@ -1064,7 +1064,7 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
     k.lse = lse;
     k.dloss = dloss;
     k.dlse = dlse;
-    k.row_lse2 = at<float>(workspace, p.f0);
+    k.row_lse = at<float>(workspace, p.f0);
     k.row_gs = at<float>(workspace, p.f1);
     k.row_gt = at<float>(workspace, p.f2);
     k.dx = dx;
@@ -1076,7 +1076,7 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
         g.nact = k.nact;
         g.tgt = k.tgt;
         g.xp = at<__nv_bfloat16>(workspace, p.xp);
-        g.row_lse2 = k.row_lse2;
+        g.row_lse = k.row_lse;
         g.row_gs = k.row_gs;
         g.row_gt = k.row_gt;
         g.row_lo = at<float>(workspace, p.f3);

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
             a.row[at] = (int32_t)r;
             a.tgt[at] = (int32_t)t;
             if (a.lse) {
-                a.row_lse2[at] = a.lse[r] * kLog2e;
+                a.row_lse[at] = a.lse[r];
                 const float up = a.dloss[r];
                 a.row_gt[at] = up;
                 a.row_gs[at] = a.dlse ? up + a.dlse[r] : up;
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
         for (int64_t r = base + tid; r < end; r += kPackThreads) {
             if (!ADALN_IN_LOSS(r < a.Np)) continue;
             a.tgt[r] = -1;
-            if (a.lse) a.row_lse2[r] = a.row_gt[r] = a.row_gs[r] = 0.0f;
+            if (a.lse) a.row_lse[r] = a.row_gt[r] = a.row_gs[r] = 0.0f;
         }
         if (tid == 0) *a.nact = base;
     }
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
     const int64_t rank0 = (int64_t)cluster_ctarank() * kCtaM;
     int tgt = -1;
     int64_t mine = -1;
-    [[maybe_unused]] float lse2 = 0.0f, gs = 0.0f, gt = 0.0f;
+    [[maybe_unused]] float lse = 0.0f, gs = 0.0f, gt = 0.0f;
     [[maybe_unused]] uint32_t draw = 0;
     auto prologue = [&](const Unit& t) {
         const int64_t row = t.m0 + rank0 + (threadIdx.x & 127);
@@ -439,11 +439,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
         mine = row;
         tgt = a.tgt[row];
         if constexpr (PROBS) {
-            lse2 = a.row_lse2[row];
+            lse = a.row_lse[row];
             gs = a.row_gs[row];
             gt = a.row_gt[row];
             const uint4 first = *reinterpret_cast<const uint4*>(a.xp + row * a.D);
-            draw = spread(spread(spread(spread(first.x ^ __float_as_uint(lse2)) + first.y) + first.z) + first.w);
+            draw = spread(spread(spread(spread(first.x ^ __float_as_uint(lse)) + first.y) + first.z) + first.w);
         }
     };
     gemm_loop<TN>(count, a.status, decode, prologue, [&](const Unit& t, uint32_t src, int r, int half,
@@ -490,17 +490,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                 sum = sum * exp2_ftz((top - mm) * kLog2e) + p_hsum(p_add(s[0], s[1]));
                 top = m;
             } else {
-                const f2r nl = p_splat(-lse2), g2 = p_splat(gs);
+                const f2r nl = p_splat(-lse), g2 = p_splat(gs);
                 uint32_t w[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    const float2 e = p_get(p_fma(p_make(v[2 * j], v[2 * j + 1]), l2e, nl));
+                    const float2 e = p_get(p_mul(p_add(p_make(v[2 * j], v[2 * j + 1]), nl), l2e));
                     const float2 p = p_get(p_mul(p_make(exp2_ftz(e.x), exp2_ftz(e.y)), g2));
                     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(p.y), "f"(p.x));
                 }
                 if (hit >= 0) {
                     // The target's dz: what its rounding leaves off is kept.
-                    const float d = exp2_ftz(fmaf(zt, kLog2e, -lse2)) * gs - gt;
+                    const float d = exp2_ftz((zt - lse) * kLog2e) * gs - gt;
                     const uint32_t bits = target_dz(d, draw);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)

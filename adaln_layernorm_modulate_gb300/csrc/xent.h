@@ -34,7 +34,7 @@ struct PackArgs {
     void* xp;               // packed rows [Np, D]
     int32_t* row;           // [Np]: the packed row's row
     int32_t* tgt;           // [Np]
-    float* row_lse2;        // backward: lse * log2(e), dloss + dlse, dloss of the packed row
+    float* row_lse;         // backward: lse, dloss + dlse, dloss of the packed row
     float* row_gs;
     float* row_gt;
     int32_t* nact;          // packed rows
@@ -53,7 +53,7 @@ struct LogitsArgs {
     float2* parts;          // statistics: [2 * tiles][Np] (max, sum exp)
     float* zt;              // statistics: [Np], the target's logit
     const __nv_bfloat16* xp;  // dz: packed rows [Np, D]
-    const float* row_lse2;
+    const float* row_lse;
     const float* row_gs;
     const float* row_gt;
     float* row_lo;          // dz: [Np], what rounding dz of the target left off

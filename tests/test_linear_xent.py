@@ -427,3 +427,25 @@ def test_losses_of_very_large_logits(power):
     want = (torch.tensor([0.0, 0.0, top / 2, 2 * top], dtype=torch.float64, device="cuda") + math.log(2.0)).repeat(5)
     assert ((loss.double() - want).abs() <= 2.0 ** -22 * want).all()
     assert ((lse.double() - (top + math.log(2.0))).abs() <= 2.0 ** -22 * top).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("power", [10, 20, 60])
+def test_gradients_of_very_large_logits(power):
+    # The same logits; a row's lse is what fp32 leaves of it, and dz = exp(z - lse) by that.
+    V, D = 130, 64
+    x = torch.zeros(1, D, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    x[:, 3] = 2.0 ** power
+    w[:, 3] = -(2.0 ** power)
+    w[70:, 3] = 2.0 ** (power - 1)
+    w[5, 3] = w[101, 3] = 2.0 ** power
+    one = torch.ones(1, device="cuda")
+    _, lse, _, dw = call(x, w, torch.tensor([80], device="cuda"), one, None)
+    want = torch.exp(w[:, 3].double() * 2.0 ** power - lse.double())
+    want[80] -= 1
+    want *= 2.0 ** power
+    # Rounded as dz and as dweight (a word of one row has the first back, but not the words that
+    # are no target), an exponential good to 2^-20.
+    assert ((dw[:, 3].double() - want).abs() <= (2 * H + 2.0 ** -19) * want.abs() + TINY).all()
+    assert (dw[:, :3] == 0).all() and (dw[:, 4:] == 0).all()
