@@ -307,8 +307,10 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Te
                          check_targets: bool = False) -> torch.Tensor:
     """Softmax cross entropy of the vocabulary head ``x @ weight.T`` without its logits.
 
-    reduction: "none" (a loss per row), "sum", or "mean" over the rows whose target is not
-    ignore_index (0 if there is none). z_loss adds z_loss * lse^2 to each such row's loss."""
+    reduction: "none" (a loss per row), "sum", or "mean" over the rows that carry a loss, those whose
+    target is a word and not ignore_index (0 if there is none). z_loss adds z_loss * lse^2 to each
+    such row's loss. A target that is neither a word nor ignore_index carries none either, and raises
+    an error with ``check_targets``."""
     if reduction not in ("none", "sum", "mean"):
         raise ValueError("reduction must be none, sum or mean, got %r" % (reduction,))
     loss, lse = LinearCrossEntropyFunction.apply(x, weight, target, ignore_index, check_targets)
@@ -317,4 +319,10 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Te
     if reduction == "none":
         return loss
     total = loss.sum()
-    return total if reduction == "sum" else total / (target != ignore_index).sum().clamp(min=1)
+    if reduction == "sum":
+        return total
+    V = weight.shape[0]
+    counts = target.clamp(0, V - 1) == target
+    if 0 <= ignore_index < V:
+        counts = counts & (target != ignore_index)
+    return total / counts.sum().clamp(min=1)

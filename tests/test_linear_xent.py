@@ -449,3 +449,19 @@ def test_gradients_of_very_large_logits(power):
     # are no target), an exponential good to 2^-20.
     assert ((dw[:, 3].double() - want).abs() <= (2 * H + 2.0 ** -19) * want.abs() + TINY).all()
     assert (dw[:, :3] == 0).all() and (dw[:, 4:] == 0).all()
+
+
+@pytest.mark.gpu
+def test_the_mean_is_over_the_rows_that_carry_a_loss():
+    from adaln_layernorm_modulate_gb300.autograd import linear_cross_entropy
+    x, w, t, _, _ = inputs(300, 400, 64, 0.2, seed=23)
+    t[17], t[200], t[299] = 400, -1, 2 ** 40  # no words: they carry none
+    on = (t >= 0) & (t < 400)
+    rows = linear_cross_entropy(x, w, t, reduction="none")
+    assert torch.equal(linear_cross_entropy(x, w, t), rows.sum() / on.sum())
+    # ignore_index may be a word of the vocabulary.
+    t[on] = t[on].clamp(max=398)
+    t[:5] = 399
+    on = (t >= 0) & (t < 399)
+    rows = linear_cross_entropy(x, w, t, ignore_index=399, reduction="none")
+    assert torch.equal(linear_cross_entropy(x, w, t, ignore_index=399), rows.sum() / on.sum())
