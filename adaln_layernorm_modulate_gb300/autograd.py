@@ -22,6 +22,7 @@ vocabulary loss without its logits (``linear_cross_entropy``).
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
@@ -54,6 +55,14 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _on(t: torch.Tensor):
+    """The library plans for the current device and launches on its current stream: a context in
+    which that is t's device."""
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
 def _check_status(ws: torch.Tensor, what: str) -> None:
     st = adaln_read_status(ws)
     if st != 0:
@@ -77,6 +86,8 @@ class AdaLNModulateFunction(torch.autograd.Function):
         scale = scale.contiguous()
         if shift.dtype != x.dtype or scale.dtype != x.dtype:
             raise TypeError("x, shift and scale must share one dtype")
+        if shift.device != x.device or scale.device != x.device:
+            raise ValueError("x, shift and scale must be on one device")
         dt = _code(x)
         D = x.shape[-1]
         packed = cu_seqlens is not None
@@ -89,11 +100,12 @@ class AdaLNModulateFunction(torch.autograd.Function):
             R, nseg, nmod = x.shape[0], mod.numel(), shift.shape[0]
             mean = torch.empty(R, dtype=torch.float32, device=x.device)
             rstd = torch.empty(R, dtype=torch.float32, device=x.device)
-            nb = adaln_fwd_varlen_workspace_size(R, nseg, D, dt)
-            ws = _workspace(nb, x.device)
-            adaln_fwd_varlen(x, shift, scale, y, mean, rstd, cu, mod, nseg, R, nmod, D, eps, ws, nb, dt)
-            if check_tables:
-                _check_status(ws, "adaln_fwd_varlen")
+            with _on(x):
+                nb = adaln_fwd_varlen_workspace_size(R, nseg, D, dt)
+                ws = _workspace(nb, x.device)
+                adaln_fwd_varlen(x, shift, scale, y, mean, rstd, cu, mod, nseg, R, nmod, D, eps, ws, nb, dt)
+                if check_tables:
+                    _check_status(ws, "adaln_fwd_varlen")
             kept = (mean, rstd) if save_stats else (mean[:0], rstd[:0])
             ctx.save_for_backward(x, scale, *kept, cu, mod)
         else:
@@ -102,7 +114,8 @@ class AdaLNModulateFunction(torch.autograd.Function):
             Bt, N = x.shape[0], x.shape[1]
             mean = torch.empty((Bt, N), dtype=torch.float32, device=x.device)
             rstd = torch.empty((Bt, N), dtype=torch.float32, device=x.device)
-            adaln_fwd(x, shift, scale, y, mean, rstd, Bt, N, D, eps, dt)
+            with _on(x):
+                adaln_fwd(x, shift, scale, y, mean, rstd, Bt, N, D, eps, dt)
             kept = (mean, rstd) if save_stats else (mean[:0], rstd[:0])
             ctx.save_for_backward(x, scale, *kept)
         ctx.packed = packed
@@ -123,31 +136,32 @@ class AdaLNModulateFunction(torch.autograd.Function):
         dx = torch.empty_like(x)
         dshift = torch.empty((nmod, D), dtype=torch.float32, device=x.device)
         dscale = torch.empty((nmod, D), dtype=torch.float32, device=x.device)
-        if ctx.packed:
-            cu, mod = ctx.saved_tensors[4:]
-            R, nseg = x.shape[0], mod.numel()
-            if ctx.save_stats:
-                nb = adaln_bwd_varlen_workspace_size(R, nseg, nmod, D, dt)
-                ws = _workspace(nb, x.device)
-                adaln_bwd_varlen(dy, x, mean, rstd, scale, dx, dshift, dscale, cu, mod, nseg, R, nmod,
-                                 D, ws, nb, dt)
+        with _on(x):
+            if ctx.packed:
+                cu, mod = ctx.saved_tensors[4:]
+                R, nseg = x.shape[0], mod.numel()
+                if ctx.save_stats:
+                    nb = adaln_bwd_varlen_workspace_size(R, nseg, nmod, D, dt)
+                    ws = _workspace(nb, x.device)
+                    adaln_bwd_varlen(dy, x, mean, rstd, scale, dx, dshift, dscale, cu, mod, nseg, R, nmod,
+                                     D, ws, nb, dt)
+                else:
+                    nb = adaln_bwd_varlen_recompute_workspace_size(R, nseg, nmod, D, dt)
+                    ws = _workspace(nb, x.device)
+                    adaln_bwd_varlen_recompute(dy, x, scale, dx, dshift, dscale, cu, mod, nseg, R, nmod, D,
+                                               ctx.eps, ws, nb, dt)
+                if ctx.check_tables:
+                    _check_status(ws, "adaln_bwd_varlen")
             else:
-                nb = adaln_bwd_varlen_recompute_workspace_size(R, nseg, nmod, D, dt)
-                ws = _workspace(nb, x.device)
-                adaln_bwd_varlen_recompute(dy, x, scale, dx, dshift, dscale, cu, mod, nseg, R, nmod, D,
-                                           ctx.eps, ws, nb, dt)
-            if ctx.check_tables:
-                _check_status(ws, "adaln_bwd_varlen")
-        else:
-            Bt, N = x.shape[0], x.shape[1]
-            if ctx.save_stats:
-                nb = adaln_bwd_workspace_size(Bt, N, D, dt)
-                ws = _workspace(nb, x.device)
-                adaln_bwd(dy, x, mean, rstd, scale, dx, dshift, dscale, ws, nb, Bt, N, D, dt)
-            else:
-                nb = adaln_bwd_recompute_workspace_size(Bt, N, D, dt)
-                ws = _workspace(nb, x.device)
-                adaln_bwd_recompute(dy, x, scale, dx, dshift, dscale, ws, nb, Bt, N, D, ctx.eps, dt)
+                Bt, N = x.shape[0], x.shape[1]
+                if ctx.save_stats:
+                    nb = adaln_bwd_workspace_size(Bt, N, D, dt)
+                    ws = _workspace(nb, x.device)
+                    adaln_bwd(dy, x, mean, rstd, scale, dx, dshift, dscale, ws, nb, Bt, N, D, dt)
+                else:
+                    nb = adaln_bwd_recompute_workspace_size(Bt, N, D, dt)
+                    ws = _workspace(nb, x.device)
+                    adaln_bwd_recompute(dy, x, scale, dx, dshift, dscale, ws, nb, Bt, N, D, ctx.eps, dt)
         return (dx, dshift.to(ctx.shift_dtype), dscale.to(ctx.shift_dtype), None, None, None, None, None)
 
 
@@ -202,8 +216,9 @@ class LayerNormFunction(torch.autograd.Function):
         y = torch.empty_like(x)
         mean = torch.empty(R, dtype=torch.float32, device=x.device)
         rstd = torch.empty(R, dtype=torch.float32, device=x.device)
-        adaln_layernorm_fwd(x, weight, None if bias is None else bias.contiguous(), y, mean, rstd, R, D, eps,
-                            dt)
+        with _on(x):
+            adaln_layernorm_fwd(x, weight, None if bias is None else bias.contiguous(), y, mean, rstd, R, D,
+                                eps, dt)
         ctx.save_for_backward(x, weight, mean, rstd)
         return y
 
@@ -217,9 +232,10 @@ class LayerNormFunction(torch.autograd.Function):
         want_w, want_b = weight is not None and ctx.needs_input_grad[1], ctx.needs_input_grad[2]
         dweight = torch.empty(D, dtype=torch.float32, device=x.device) if want_w else None
         dbias = torch.empty(D, dtype=torch.float32, device=x.device) if want_b else None
-        nb = adaln_layernorm_bwd_workspace_size(R, D, dt)
-        ws = _workspace(nb, x.device)
-        adaln_layernorm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, ws, nb, R, D, dt)
+        with _on(x):
+            nb = adaln_layernorm_bwd_workspace_size(R, D, dt)
+            ws = _workspace(nb, x.device)
+            adaln_layernorm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, ws, nb, R, D, dt)
         return (dx, dweight.to(x.dtype) if want_w else None, dbias.to(x.dtype) if want_b else None, None)
 
 
@@ -272,11 +288,12 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
         N = target.numel()
         loss = torch.empty(target.shape, dtype=torch.float32, device=x.device)
         lse = torch.empty(target.shape, dtype=torch.float32, device=x.device)
-        nb = adaln_linear_xent_fwd_workspace_size(N, V, D, ADALN_BF16)
-        ws = _workspace(nb, x.device)
-        adaln_linear_xent_fwd(x, weight, target, loss, lse, N, V, D, ignore_index, ws, nb, ADALN_BF16)
-        if check_targets:
-            _check_status(ws, "adaln_linear_xent_fwd")
+        with _on(x):
+            nb = adaln_linear_xent_fwd_workspace_size(N, V, D, ADALN_BF16)
+            ws = _workspace(nb, x.device)
+            adaln_linear_xent_fwd(x, weight, target, loss, lse, N, V, D, ignore_index, ws, nb, ADALN_BF16)
+            if check_targets:
+                _check_status(ws, "adaln_linear_xent_fwd")
         ctx.save_for_backward(x, weight, target, lse)
         ctx.ignore_index = ignore_index
         ctx.set_materialize_grads(False)
@@ -295,10 +312,11 @@ class LinearCrossEntropyFunction(torch.autograd.Function):
         dlse = None if dlse is None else dlse.contiguous()
         dx = torch.empty_like(x) if want_x else None
         dweight = torch.empty_like(weight) if want_w else None
-        nb = adaln_linear_xent_bwd_workspace_size(N, V, D, ADALN_BF16)
-        ws = _workspace(nb, x.device)
-        adaln_linear_xent_bwd(x, weight, target, lse, dloss, dlse, dx, dweight, N, V, D, ctx.ignore_index, ws,
-                              nb, ADALN_BF16)
+        with _on(x):
+            nb = adaln_linear_xent_bwd_workspace_size(N, V, D, ADALN_BF16)
+            ws = _workspace(nb, x.device)
+            adaln_linear_xent_bwd(x, weight, target, lse, dloss, dlse, dx, dweight, N, V, D, ctx.ignore_index,
+                                  ws, nb, ADALN_BF16)
         return dx, dweight, None, None, None
 
 

@@ -76,3 +76,80 @@ def _dx_terms(w, mean, rstd):
     g = dy * (1 + synth.widen(w.scale, w.dtype)[m_of_row])
     xhat = (x - mean[:, None]) * rstd[:, None]
     return rstd, mean, xhat, g.mean(axis=1), (g * xhat).mean(axis=1)
+
+
+class Context:
+    """What a node's forward keeps for its backward."""
+    needs_input_grad = (True,) * 8
+
+    def save_for_backward(self, *tensors):
+        self.saved_tensors = tensors
+
+    def mark_non_differentiable(self, *tensors):
+        pass
+
+    def set_materialize_grads(self, value):
+        pass
+
+
+@pytest.mark.parametrize("node", ["dense", "packed", "packed-recomputed", "norm", "loss"])
+def test_nodes_launch_on_their_tensors_device(monkeypatch, node):
+    # Tensors on device 1 while device 0 is current: every call of the library has to see device 1
+    # as the current one. No GPU: the tensors hold nothing, the calls and the current device are fakes.
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    from adaln_layernorm_modulate_gb300 import autograd as G
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *error):
+            current[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for name in dir(G):
+        if name.startswith("adaln_") and name != "adaln_modulate":
+            def call(*args, name=name):
+                seen.append((name, current[0]))
+                return 256 if name.endswith("_size") else 0
+            monkeypatch.setattr(G, name, call)
+    with FakeTensorMode():
+        make = lambda *shape, dtype=torch.bfloat16: torch.empty(*shape, dtype=dtype, device="cuda:1")
+        ctx, row, table = Context(), make(12, 64), make(3, 64)
+        if node == "dense":
+            x = make(3, 4, 64)
+            G.AdaLNModulateFunction.forward(ctx, x, table, table)
+            G.AdaLNModulateFunction.backward(ctx, x, None, None)
+        elif node.startswith("packed"):
+            cu, mod = make(4, dtype=torch.int32), make(3, dtype=torch.int32)
+            G.AdaLNModulateFunction.forward(ctx, row, table, table, cu, mod, 1e-6, True, node == "packed")
+            G.AdaLNModulateFunction.backward(ctx, row, None, None)
+        elif node == "norm":
+            G.LayerNormFunction.forward(ctx, row, make(64), make(64))
+            G.LayerNormFunction.backward(ctx, row)
+        else:
+            target, up = make(12, dtype=torch.int64), make(12, dtype=torch.float32)
+            G.LinearCrossEntropyFunction.forward(ctx, row, make(100, 64), target, -100, True)
+            G.LinearCrossEntropyFunction.backward(ctx, up, None)
+    assert len(seen) >= 3 and all(device == 1 for _, device in seen), seen
+    assert current == [0]
+
+
+def test_modulation_tables_of_another_device_are_refused():
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    from adaln_layernorm_modulate_gb300.autograd import AdaLNModulateFunction
+    with FakeTensorMode():
+        x, near = (torch.empty(1, 4, 64, device="cuda:0"), torch.empty(1, 64, device="cuda:0"))
+        for far in (torch.empty(1, 64), torch.empty(1, 64, device="cuda:1")):
+            for tables in ((near, far), (far, near)):
+                with pytest.raises(ValueError, match="one device"):
+                    AdaLNModulateFunction.forward(Context(), x, *tables)
