@@ -95,6 +95,10 @@ class AdaLNModulateFunction(torch.autograd.Function):
         if packed:
             if x.dim() != 2 or mod_idx is None:
                 raise ValueError("packed input: x [R, D] with cu_seqlens and mod_idx")
+            if cu_seqlens.dim() != 1 or mod_idx.shape != (cu_seqlens.shape[0] - 1,):
+                raise ValueError("packed input: cu_seqlens [nseg + 1] and mod_idx [nseg]")
+            if shift.dim() != 2 or shift.shape[1] != D or scale.shape != shift.shape:
+                raise ValueError("packed input: shift and scale [nmod, D]")
             cu = cu_seqlens.to(device=x.device, dtype=torch.int32).contiguous()
             mod = mod_idx.to(device=x.device, dtype=torch.int32).contiguous()
             R, nseg, nmod = x.shape[0], mod.numel(), shift.shape[0]

@@ -153,3 +153,19 @@ def test_modulation_tables_of_another_device_are_refused():
             for tables in ((near, far), (far, near)):
                 with pytest.raises(ValueError, match="one device"):
                     AdaLNModulateFunction.forward(Context(), x, *tables)
+
+
+@pytest.mark.parametrize("shift,scale,cu,mod", [((3, 56), (3, 64), 4, 3), ((3, 64), (2, 64), 4, 3), ((64,), (64,), 4, 3),
+                                                ((3, 64), (3, 64), 3, 3), ((3, 64), (3, 64), 4, 4),
+                                                ((3, 64), (3, 64), 0, 0)])
+def test_packed_tables_of_other_shapes_are_refused(shift, scale, cu, mod):
+    # The kernels would read past the shorter of them.
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    from adaln_layernorm_modulate_gb300.autograd import AdaLNModulateFunction
+    with FakeTensorMode():
+        make = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device="cuda")
+        with pytest.raises(ValueError, match="packed input"):
+            AdaLNModulateFunction.forward(Context(), make(9, 64), make(*shift), make(*scale),
+                                          make(cu, dtype=torch.int32), make(mod, dtype=torch.int32))
