@@ -865,7 +865,11 @@ int adaln_layernorm_fwd(const void* x, const void* weight, const void* bias, voi
 
 size_t adaln_layernorm_bwd_workspace_size(int64_t R, int64_t D, adaln_dtype dtype) {
     if (check_shape(D, dtype) || R < 0) return 0;
-    const int64_t G = bwd_tiles(R, D, kAffine, dtype);
+    int64_t G = bwd_tiles(R, D, kAffine, dtype);
+    // Past the SM count the tiles are halved: what R holds has to hold fewer rows too.
+    int dev = 0;
+    const int sms = current_sms(&dev);
+    if (G >= 0 && sms > 0 && R > sms) G = std::max(G, bwd_tiles(sms, D, kAffine, dtype));
     return G < 0 ? 0 : bwd_need(G, 1, D);
 }
 

@@ -239,3 +239,20 @@ def test_side_stream_and_graph_replay():
         v.zero_()
     graph.replay()
     assert all(torch.equal(out[k], want[k]) for k in want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 1152, 5120, 16384])
+def test_a_workspace_holds_every_smaller_batch(D, dtype):
+    dt = A.ADALN_BF16 if dtype == torch.bfloat16 else A.ADALN_F32
+    sizes = [A.adaln_layernorm_bwd_workspace_size(R, D, dt) for R in range(0, 2000)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    x, w, b, dy = inputs(sms, D, dtype, True, True, seed=17)
+    want = call(x, w, b, dy)
+    dx, dw, db = (torch.empty_like(want[k]) for k in ("dx", "dw", "db"))
+    nb = sizes[sms + 1]
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    A.adaln_layernorm_bwd(dy, x, want["mean"], want["rstd"], w, dx, dw, db, ws, nb, sms, D)
+    assert torch.equal(dx, want["dx"]) and torch.equal(dw, want["dw"]) and torch.equal(db, want["db"])
