@@ -909,6 +909,7 @@ struct XentPlan {
     int64_t piece;       // backward: columns of a piece (a multiple of kTileN)
     int splits;          // backward: parts of dx's sum over a piece
     size_t nact, row, tgt, f0, f1, f2, f3, hits, words, xp, big, dxacc, bytes;  // workspace offsets
+    size_t most;         // bytes of any plan of at most as many rows
 };
 
 // Workspace: [header | status words | nact | row | tgt | four row arrays | rows of each word as
@@ -951,6 +952,24 @@ XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
     p.big = take(bwd ? rows * (size_t)p.piece * 2 : rows * (size_t)p.tiles * 2 * sizeof(float2));
     if (bwd) p.dxacc = take(rows * (size_t)p.splits * (size_t)D * 4);
     p.bytes = at;
+    // The last two do not grow with the rows alone: fewer rows go in fewer, wider pieces, in narrower
+    // tiles, in more parts. Bounds that do grow with them:
+    size_t big, acc = 0;
+    const int64_t words = round_up(V, kTileN);
+    if (bwd) {
+        // A piece is no wider than the vocabulary, and than `wide`.
+        big = std::min<size_t>(rows * (size_t)words, std::max<size_t>(kProbsBytes / 2, rows * (size_t)kMinPiece)) * 2;
+        // steps = 2 mt dt kv, and a share is at least 8/9 of steps / kPairs (rounded down, but at least
+        // 8), so mt * splits <= mt * (kv / share + 1) <= 9/16 kPairs / dt + mt.
+        const int64_t parts = std::min(16 * mt, mt + (9 * kPairs + 15) / 16 / ((D + kTileN - 1) / kTileN));
+        acc = (size_t)parts * kTileM * (size_t)D * 4;
+    } else {
+        // Narrow tiles, twice as many, up to the row tiles that leave no pair without a wide one.
+        const int64_t narrow = std::min(mt, (kPairs - 1) / (words / kTileN));
+        big = (size_t)kTileM * 2 * sizeof(float2) *
+              (size_t)std::max(mt * (words / kTileN), narrow * ((V + kTileN / 2 - 1) / (kTileN / 2)));
+    }
+    p.most = std::max(p.bytes, p.big + big + acc);
     return p;
 }
 
@@ -994,7 +1013,7 @@ PackArgs xent_pack(const XentPlan& p, void* ws, const void* x, const int64_t* ta
 extern "C" {
 
 size_t adaln_linear_xent_fwd_workspace_size(int64_t N, int64_t V, int64_t D, adaln_dtype dtype) {
-    return xent_check(N, V, D, dtype) ? 0 : xent_plan(N, V, D, false).bytes;
+    return xent_check(N, V, D, dtype) ? 0 : xent_plan(N, V, D, false).most;
 }
 
 int adaln_linear_xent_fwd(const void* x, const void* weight, const int64_t* target, float* loss, float* lse,
@@ -1043,7 +1062,7 @@ int adaln_linear_xent_fwd(const void* x, const void* weight, const int64_t* targ
 }
 
 size_t adaln_linear_xent_bwd_workspace_size(int64_t N, int64_t V, int64_t D, adaln_dtype dtype) {
-    return xent_check(N, V, D, dtype) ? 0 : xent_plan(N, V, D, true).bytes;
+    return xent_check(N, V, D, dtype) ? 0 : xent_plan(N, V, D, true).most;
 }
 
 int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* target, const float* lse,

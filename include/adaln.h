@@ -50,7 +50,9 @@
  *
  * Workspace. The packed forward and both backwards take a caller-allocated device
  * workspace of at least the size the matching *_workspace_size function returns for the
- * CURRENT device (the size depends on its SM count). It needs no initialisation.
+ * CURRENT device (the size depends on its SM count). It needs no initialisation. With the other
+ * arguments the same, a size never falls as Bt, N, total_tokens or R grows: a workspace
+ * for the largest batch serves every smaller one.
  * Determinism holds for a fixed device model: the tile split follows its SM count.
  */
 #ifndef ADALN_H_

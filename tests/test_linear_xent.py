@@ -465,3 +465,44 @@ def test_the_mean_is_over_the_rows_that_carry_a_loss():
     on = (t >= 0) & (t < 399)
     rows = linear_cross_entropy(x, w, t, ignore_index=399, reduction="none")
     assert torch.equal(linear_cross_entropy(x, w, t, ignore_index=399), rows.sum() / on.sum())
+
+
+def pieces(N, V):
+    """The vocabulary pieces of a backward, from the limits in the library's source."""
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(A.__file__), "csrc", "adaln.cu")).read()
+    mib, = re.findall(r"kProbsBytes = \(int64_t\)(\d+) << 20;", src)
+    least, = re.findall(r"kMinPiece = (\d+);", src)
+    rows = -(-max(N, 1) // 256) * 256
+    wide = max((int(mib) << 20) // 2 // rows // 256 * 256, int(least))
+    return -(-V // wide)
+
+
+@pytest.mark.parametrize("V,D", [(1, 8), (300, 64), (8192, 1024), (32000, 1536), (50257, 2048), (131072, 1024),
+                                 (1 << 20, 4096)])
+def test_a_workspace_holds_every_smaller_batch(V, D):
+    for size in (A.adaln_linear_xent_fwd_workspace_size, A.adaln_linear_xent_bwd_workspace_size):
+        sizes = [size(n, V, D, 1) for n in list(range(0, 600, 37)) + list(range(768, 40000, 256))]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.gpu
+def test_a_smaller_batch_in_a_larger_ones_workspace():
+    # 2560 rows keep dz of all 50257 words at once, 2816 rows in two pieces; 512 rows have narrower
+    # tiles, and so more partial sums of the forward, than 768.
+    V, D = 50257, 64
+    assert pieces(2560, V) == 1 and pieces(2816, V) == 2
+    for most, N, words in ((2816, 2560, V), (768, 512, 8192)):
+        x, w, t, up, ul = inputs(N, words, D, 0.1, seed=25)
+        want = call(x, w, t, up, ul)
+        loss, lse, dx, dw = (torch.empty_like(v) for v in want)
+        for forward in (True, False):
+            size = A.adaln_linear_xent_fwd_workspace_size if forward else A.adaln_linear_xent_bwd_workspace_size
+            nb = size(most, words, D, 1)
+            ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+            if forward:
+                A.adaln_linear_xent_fwd(x, w, t, loss, lse, N, words, D, IGNORE, ws, nb)
+            else:
+                A.adaln_linear_xent_bwd(x, w, t, lse, up, ul, dx, dw, N, words, D, IGNORE, ws, nb)
+        assert all(torch.equal(a, b) for a, b in zip((loss, lse, dx, dw), want))
