@@ -25,6 +25,11 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// A word of either CTA's shared memory (a cluster address).
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // One lane of the warp (all of whose lanes are here), the same every time. Code that issues loads
 // and products keeps the whole warp in its loops and lets this lane issue: the loops' values then
 // stay warp-uniform, where a branch for one lane moves each operand to a uniform register anew.

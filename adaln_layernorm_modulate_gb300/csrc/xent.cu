@@ -234,6 +234,7 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
     extern __shared__ uint4 dyn[];
     __shared__ __align__(8) uint64_t bars[2 * kGemmStages + 2 * kAccs + 1];
     __shared__ uint32_t tmem_base;
+    __shared__ uint32_t fills[4];  // CTA 0: stages filled by each loading warp of the pair
     __shared__ int abort_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_ctarank();
@@ -262,6 +263,7 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
     const uint32_t tmem = tmem_base;
     pdl_wait();
     const uint32_t units = count();
+    bool issued = false;  // products, by warp 1 of CTA 0
 
     const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);  // the warp's number, known to be uniform
     if (role == 0 || role == 3) {
@@ -300,23 +302,15 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
                 }
             }
         }
-        // After a timeout, copies may still be on their way into the pair's memory: CTA 0 gives
-        // each stage's last ones a further bounded wait, CTA 1 meets it at the cluster barrier.
-        if (rank == 0 && !is_b && lane == 0 && *(volatile int*)&abort_flag) {
-            volatile int never = 0;
-            for (int q = 0; q < kGemmStages; ++q) {
-                if (q >= s && lap == 0) continue;
-                const uint32_t last = q < s ? lap : lap - 1;
-                mbar_wait_bounded(full + 8u * q, last & 1u, &never);
-            }
-        }
+        if (lane == 0)
+            st_cluster_u32(cluster_map(smem_addr(fills) + 4u * (2 * rank + (is_b ? 1 : 0)), 0), lap * kGemmStages + s);
     } else if (role == 1) {
         if (rank == 0) {
             // Descriptors of stage 0; a stage and a K step move the address field (the low bits).
             const uint64_t da0 = smem_desc(data, kMnBlock), db0 = smem_desc(data + kABytes, kMnBlock);
             int s = 0, acc = 0;
             uint32_t lap = 0, alap = 0;
-            bool live = true, issued = false;
+            bool live = true;
             for (uint32_t u = first; live && u < units; u += step) {
                 const Unit t = decode(u);
                 const uint32_t idesc = mma_desc(kTileM, TN, t.a_mn, t.b_mn);
@@ -352,13 +346,6 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
                     ++alap;
                 }
             }
-            __syncwarp();
-            // After a timeout, products in flight end before their memory is given back.
-            if (__any_sync(0xFFFFFFFFu, issued && *(volatile int*)&abort_flag != 0) && elect_lane()) {
-                volatile int never = 0;
-                mma_commit(drain);
-                mbar_wait_bounded(drain, 0, &never);
-            }
         }
     } else if (role >= kEpiWarp) {
         const int q = warp & 3, half = (warp - kEpiWarp) >> 2;
@@ -387,7 +374,25 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // no product, copy or arrival of the pair is left
+    if (tid == 0 && *(volatile int*)&abort_flag) st_cluster_u32(cluster_map(smem_addr(&abort_flag), rank ^ 1u), 1);
+    cluster_sync();  // every wait of the pair is over, nothing more is issued, and both flags agree
+    // Without a timeout no product, copy or arrival is left. After one, whichever warp's it was,
+    // copies and products may still be on their way: CTA 0 gives each stage's last copies and the
+    // products a further bounded wait before memory is given back.
+    if (__builtin_expect(*(volatile int*)&abort_flag, 0)) {
+        volatile int never = 0;
+        if (rank == 0 && tid == 0) {
+            const uint32_t most = max(max(fills[0], fills[1]), max(fills[2], fills[3]));
+            for (uint32_t q = 0; q < min(most, (uint32_t)kGemmStages); ++q)
+                mbar_wait_bounded(full + 8u * q, ((most - 1 - q) / kGemmStages) & 1u, &never);
+        }
+        if (rank == 0 && warp == 1 && issued && elect_lane()) {
+            mma_commit(drain);
+            mbar_wait_bounded(drain, 0, &never);
+        }
+        __syncwarp();
+        cluster_sync();
+    }
     tc_fence_after();
     if (warp == 2) tmem_free(tmem, kAccs * kTileN);
     __syncwarp();

@@ -154,3 +154,18 @@ def test_header_compiles_as_c_and_a_c_program_links(tmp_path):
                     str(src), "-L", libdir, "-ladaln", "-Wl,-rpath," + libdir, "-o", str(exe)],
                    check=True, capture_output=True)
     assert subprocess.run([str(exe)]).returncode == 0
+
+
+def test_products_drain_only_after_the_last_wait_may_have_run_out():
+    """After a timed-out wait the tensor-core kernels give the copies and products in flight a further
+    bounded wait (on a flag `never` that nothing sets). Which warp's wait runs out last is not known,
+    so that a warp that looks at the flag when its own work is done may see it too early: these waits
+    stand behind the barriers at which all warps of both CTAs have met. (Shown on the source: no
+    test makes a copy hang.)"""
+    text = open(os.path.join(ROOT, "adaln_layernorm_modulate_gb300", "csrc", "xent.cu")).read()
+    loop = text[text.index("__device__ __forceinline__ void gemm_loop("):text.index("// The tile's logits, as")]
+    met = loop.index("cluster_sync();", loop.rindex("__syncthreads();"))
+    drains = [i for i in range(len(loop)) if loop.startswith("&never)", i)]
+    assert len(drains) == 2 and all(i > met for i in drains)
+    assert all(i < loop.index("tmem_free(") for i in drains)
+    assert "mbar_wait_bounded(full" in loop[met:] and "mbar_wait_bounded(drain" in loop[met:]
