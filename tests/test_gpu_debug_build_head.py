@@ -65,3 +65,26 @@ def test_debug_build_checks_pass_and_match_the_release_build(debug_lib, name):  
         word = A.adaln_debug_read(reset=True)
     assert word == 0, {v: n for v, n in A.DEBUG_CLASSES.items() if word & v}
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+# A vocabulary in two pieces, the last one narrower; 256-column tiles of dx and dweight.
+PIECES = {
+    "loss-8192x20001x72": lambda A: _loss(A, 8192, 20001, 72, 0.3),
+    "loss-8192x17000x520": lambda A: _loss(A, 8192, 17000, 520, 0.0),
+}
+
+
+@pytest.mark.parametrize("name", sorted(PIECES))
+def test_debug_build_checks_pass_over_several_pieces(debug_lib, name):  # noqa: F811
+    import torch
+
+    from tests.test_linear_xent import pieces
+    N, V = (int(v) for v in name.split("-")[1].split("x")[:2])
+    assert pieces(N, V) == 2
+    with library("release") as A:
+        want = PIECES[name](A)
+    with library("debug") as A:
+        got = PIECES[name](A)
+        word = A.adaln_debug_read(reset=True)
+    assert word == 0, {v: n for v, n in A.DEBUG_CLASSES.items() if word & v}
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

@@ -479,6 +479,24 @@ def pieces(N, V):
     return -(-V // wide)
 
 
+def test_the_tests_vocabularies_go_in_several_pieces():
+    assert pieces(8192, 20001) == 2 and pieces(2049, 70000) == 2 and pieces(8191, 17000) == 2
+    assert pieces(2500, 120001) == 3 and pieces(8192, 9001) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,V,D,ignored,n", [(600, 9000, 1288, 0.0, 1), (8191, 17000, 648, 0.4, 2),
+                                             (4100, 24, 264, 0.1, 1), (3000, 256, 640, 0.0, 1),
+                                             (2500, 120001, 328, 0.2, 3)])
+def test_full_tiles(N, V, D, ignored, n):
+    # Both gradients from 256-column tiles with several tiles and K steps each way, in one piece and
+    # in more; thousands of rows of a few words.
+    assert pieces(N, V) == n
+    x, w, t, up, ul = inputs(N, V, D, ignored, seed=24)
+    t[0], t[1] = 0, V - 1
+    check(x, w, t, up, ul, call(x, w, t, up, ul))
+
+
 @pytest.mark.parametrize("V,D", [(1, 8), (300, 64), (8192, 1024), (32000, 1536), (50257, 2048), (131072, 1024),
                                  (1 << 20, 4096)])
 def test_a_workspace_holds_every_smaller_batch(V, D):
