@@ -908,12 +908,15 @@ struct XentPlan {
     int64_t tiles;       // forward: column tiles
     int64_t piece;       // backward: columns of a piece (a multiple of kTileN)
     int splits;          // backward: parts of dx's sum over a piece
-    size_t nact, row, tgt, f0, f1, f2, f3, hits, words, xp, big, dxacc, bytes;  // workspace offsets
+    int64_t slots;       // backward: words that may be the target of more than kHits rows
+    // Workspace offsets.
+    size_t nact, row, tgt, f0, f1, f2, f3, hits, words, many_word, many_slot, many_sums, xp, big,
+        dxacc, bytes;
     size_t most;         // bytes of any plan of at most as many rows
 };
 
-// Workspace: [header | status words | nact | row | tgt | four row arrays | rows of each word as
-// a target (backward) | packed x |
+// Workspace: [header | status words | nact and the count of words of many rows | row | tgt | four row arrays | rows of
+// each word as a target, words of many rows (backward) | packed x |
 // partials (forward) or dz (backward) | dx in fp32 (backward)].
 XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
     XentPlan p{};
@@ -939,7 +942,7 @@ XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
         return o;
     };
     const size_t rows = (size_t)p.Np;
-    p.nact = take(sizeof(int32_t));
+    p.nact = take(2 * sizeof(int32_t));
     p.row = take(rows * 4);
     p.tgt = take(rows * 4);
     p.f0 = take(rows * 4);
@@ -948,6 +951,12 @@ XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
     p.f3 = take(rows * 4);
     if (bwd) p.hits = take((size_t)V * 4);
     if (bwd) p.words = take((size_t)V * kHits * 4);
+    if (bwd) {
+        p.slots = std::min(V, N / (kHits + 1));
+        p.many_word = take((size_t)p.slots * 4);
+        p.many_slot = take((size_t)V * 4);
+        p.many_sums = take((size_t)p.slots * (size_t)D * 4);
+    }
     p.xp = take(rows * (size_t)D * 2);
     p.big = take(bwd ? rows * (size_t)p.piece * 2 : rows * (size_t)p.tiles * 2 * sizeof(float2));
     if (bwd) p.dxacc = take(rows * (size_t)p.splits * (size_t)D * 4);
@@ -1091,20 +1100,24 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
     k.row_gs = at<float>(workspace, p.f1);
     k.row_gt = at<float>(workspace, p.f2);
     k.dx = dx;
-    k.word_hits = dweight ? at<int32_t>(workspace, p.hits) : nullptr;
+    if (dweight) {
+        k.word_hits = at<int32_t>(workspace, p.hits);
+        k.many = {k.nact + 1, at<int32_t>(workspace, p.many_word), at<int32_t>(workspace, p.many_slot),
+                  at<float>(workspace, p.many_sums), p.slots};
+    }
     const int ctas = pack_ctas(N);
     if (int rc = launched(launch_pack(k, ctas, stream))) return rc;
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
         LogitsArgs g{};
         g.nact = k.nact;
         g.tgt = k.tgt;
-        g.xp = at<__nv_bfloat16>(workspace, p.xp);
         g.row_lse = k.row_lse;
         g.row_gs = k.row_gs;
         g.row_gt = k.row_gt;
         g.row_lo = at<float>(workspace, p.f3);
         g.word_hits = k.word_hits;
         g.word_rows = at<int32_t>(workspace, p.words);
+        g.many = k.many;
         g.probs = at<__nv_bfloat16>(workspace, p.big);
         g.ldp = p.piece;
         g.status = k.status + ctas;
@@ -1122,6 +1135,7 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
         d.xp = k.xp;
         d.word_hits = g.word_hits;
         d.word_rows = g.word_rows;
+        d.many = k.many;
         d.row_lo = g.row_lo;
         d.status = g.status;
         d.Np = p.Np;
@@ -1133,20 +1147,24 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
         d.tn = p.tng;
         if (int rc = launched(launch_grad(d, g.probs, p.piece, k.xp, weight, sms, stream))) return rc;
     }
-    if (!dx) return ADALN_OK;
-    DxArgs d{};
+    if (!dx && N <= kHits) return ADALN_OK;
+    FinishArgs d{};
     d.nact = k.nact;
     d.row = k.row;
     d.dxacc = at<float>(workspace, p.dxacc);
     d.weight = weight;
     d.tgt = k.tgt;
+    d.xp = k.xp;
     d.row_lo = at<float>(workspace, p.f3);
+    d.many = k.many;
     d.dx = dx;
+    d.dweight = N > kHits ? static_cast<__nv_bfloat16*>(dweight) : nullptr;
     d.N = N;
     d.Np = p.Np;
     d.D = D;
+    d.V = V;
     d.splits = p.splits;
-    return launched(launch_dx(d, sms, stream));
+    return launched(launch_finish(d, sms, stream));
 }
 
 }  // extern "C"

@@ -11,14 +11,17 @@
 //             row and half tile; lse_kernel joins them in a fixed order;
 //   backward, a piece of the vocabulary at a time: logits_kernel<true> computes the piece's
 //             tiles again and writes dz in bf16; grad_kernel forms dW of the piece (whole) and
-//             adds the piece's part of dx to an fp32 buffer; dx_kernel rounds dx once.
+//             adds the piece's part of dx to an fp32 buffer; finish_kernel rounds dx once.
 // The products run on the tensor cores with fp32 accumulators; exp, sums and lse are fp32. dz is
-// rounded to bf16 as an operand of the next two products (up to half a step, 2^-8, of each value;
-// what that leaves off the target's dz is added in fp32).
+// rounded to bf16 as an operand of the next two products (up to half a step, 2^-8, of each value).
+// The target's dz is often most of its row's and its word's gradient, and much the same in all rows
+// of a word (a mean's, of small probabilities), so that its roundings need not average out: what
+// they leave off is kept and added in fp32, to dx, and to dW in the order of the word's rows.
 //
 // Bound by the tensor cores from a few hundred rows on: 8192 rows, 50,257 words, D = 2048 take
 // 0.81 ms forward (2.1 PFLOP/s, the tensor pipe 97% active) and 2.8 ms backward; with a few rows by
 // the chain of launches (1 row, 1000 words, D = 512: 9.4 us forward, 16.5 us backward on the device).
+#include <algorithm>
 #include <atomic>
 
 #include "tensor.cuh"
@@ -47,18 +50,6 @@ __device__ __forceinline__ float exp2_ftz(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-// The bits of d as bf16, rounded away from zero where the draw's upper half is beyond the share of
-// the step that is left, else towards it. The draw comes from what the row holds, not from its
-// place: a row's dx is the same wherever the row stands.
-__device__ __forceinline__ uint32_t target_dz(float d, uint32_t draw) {
-    if (d != d) return 0x7FC0u;
-    return (__float_as_uint(d) + (draw >> 16)) >> 16;
-}
-// A multiplicative hash, twice (the golden ratio's odd multiplier).
-__device__ __forceinline__ uint32_t spread(uint32_t h) {
-    h = (h ^ h >> 16) * 0x9E3779B9u;
-    return (h ^ h >> 15) * 0x9E3779B9u;
 }
 // The epilogue warps' own barrier; true if `ok` is, in all of them.
 __device__ __forceinline__ bool epilogue_all(bool ok) {
@@ -190,7 +181,10 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
             a.tgt[r] = -1;
             if (a.lse) a.row_lse[r] = a.row_gt[r] = a.row_gs[r] = 0.0f;
         }
-        if (tid == 0) *a.nact = base;
+        if (tid == 0) {
+            *a.nact = base;
+            if (a.many.count) *a.many.count = 0;
+        }
     }
     const bool any_bad = __syncthreads_or(bad);
     if (tid == 0) {
@@ -437,7 +431,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
     int tgt = -1;
     int64_t mine = -1;
     [[maybe_unused]] float lse = 0.0f, gs = 0.0f, gt = 0.0f;
-    [[maybe_unused]] uint32_t draw = 0;
     auto prologue = [&](const Unit& t) {
         const int64_t row = t.m0 + rank0 + (threadIdx.x & 127);
         if (row == mine || !ADALN_IN_LOSS(row < a.Np)) return;
@@ -447,8 +440,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
             lse = a.row_lse[row];
             gs = a.row_gs[row];
             gt = a.row_gt[row];
-            const uint4 first = *reinterpret_cast<const uint4*>(a.xp + row * a.D);
-            draw = spread(spread(spread(spread(first.x ^ __float_as_uint(lse)) + first.y) + first.z) + first.w);
         }
     };
     gemm_loop<TN>(count, a.status, decode, prologue, [&](const Unit& t, uint32_t src, int r, int half,
@@ -506,7 +497,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                 if (hit >= 0) {
                     // The target's dz: what its rounding leaves off is kept.
                     const float d = exp2_ftz((zt - lse) * kLog2e) * gs - gt;
-                    const uint32_t bits = target_dz(d, draw);
+                    const uint32_t bits = __bfloat16_as_ushort(__float2bfloat16_rn(d));
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (j == hit >> 1) w[j] = hit & 1 ? (w[j] & 0xFFFFu) | bits << 16 : (w[j] & 0xFFFF0000u) | bits;
@@ -514,6 +505,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_co
                     if (in && a.word_hits && ADALN_IN_LOSS(tgt < a.V)) {
                         const int k = atomicAdd(a.word_hits + tgt, 1);
                         if (k < kHits) a.word_rows[(int64_t)tgt * kHits + k] = (int32_t)row;
+                        if (k == kHits) {  // more than the epilogue of dweight takes
+                            const int slot = atomicAdd(a.many.count, 1);
+                            if (ADALN_IN_LOSS(slot < a.many.slots)) {
+                                a.many.word[slot] = tgt;
+                                a.many.slot[tgt] = slot;
+                            }
+                        }
                     }
                 }
                 // Columns past the vocabulary and rows past the packed ones, up to a whole K step of
@@ -601,17 +599,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
         }
         return t;
     };
-    // dweight: the rows whose target is this thread's word, if they are at most kHits.
+    // dweight: the rows whose target is this thread's word, if they are at most kHits; else its place
+    // among the words of more.
     const int64_t rank0 = (int64_t)cluster_ctarank() * kCtaM;
-    int hits = 0;
+    int hits = 0, slot = -1;
     int32_t hit_row[kHits];
     auto prologue = [&](const Unit& t) {
         hits = 0;
+        slot = -1;
         if (t.kind != 2) return;
         const int64_t word = a.v0 + t.m0 + rank0 + (threadIdx.x & 127);
         if (word >= a.v1 || !ADALN_IN_LOSS(word < a.V)) return;
         hits = a.word_hits[word];
-        if (hits > kHits) hits = 0;
+        if (hits > kHits) {
+            slot = a.many.slot[word];
+            hits = 0;
+        }
         if (hits == 0) return;
         const int4* list = reinterpret_cast<const int4*>(a.word_rows + word * kHits);
         const int4 lo = list[0], hi = list[1];
@@ -680,6 +683,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) grad_kernel(const __grid_cons
                         }
                     }
                 }
+                // A word of more rows is left to finish_kernel, unrounded.
+                if (slot >= 0 && ADALN_IN_LOSS(slot < a.many.slots)) {
+                    float4* sum = reinterpret_cast<float4*>(a.many.sums + (int64_t)slot * a.D + col);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (col + 4 * j < a.D) sum[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                }
                 uint32_t w[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -746,12 +756,135 @@ __global__ void __launch_bounds__(1024) lse_kernel(const LseArgs a) {
     }
 }
 
+// dweight of the words of more than kHits rows: what the products left, and the remainders of all their
+// rows' targets. A CTA takes a word and some columns at a time: it lists the word's rows, in their
+// order, from the targets of kListRows rows, and adds them up in groups of threads, every group a fixed
+// share of the list; then the groups' sums in their order. The more such words, the more columns at a
+// time (64 columns are 32 groups of 8 threads): as few as leave no CTA a second word, so that a few words
+// of many rows are shared out and many words are listed once or twice. What it adds to a backward, without
+// such words and with them: nothing at 96 x 8192 x 1024 (30.2 us), 29.7 -> 33.4 us at 4096 x 24 x 256,
+// 96 -> 108 us at 8192 x 1000 x 1024, 48 -> 64 us at 8192 x 2 x 512.
+constexpr int kListRows = 8192;
+__device__ __forceinline__ void add_remainders(const FinishArgs& a, int64_t nact) {
+    __shared__ uint16_t list[kListRows];
+    __shared__ int totals[8][8];
+    __shared__ __align__(16) float red[2048];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // Thread tid looks at rows r0 + 1024 j + 4 tid ..; the first ones before anything else is known.
+    int4 t[8];
+    auto targets = [&](int64_t r0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t row = r0 + 1024 * j + 4 * tid;
+            t[j] = make_int4(-1, -1, -1, -1);
+            if (row < nact && ADALN_IN_LOSS(row + 4 <= a.Np)) t[j] = *reinterpret_cast<const int4*>(a.tgt + row);
+        }
+    };
+    targets(0);
+    const int64_t n = *a.many.count;
+    int lanes = 8;  // threads a group
+    while (lanes < 256 && 8 * lanes < a.D && n * ((a.D + 8 * lanes - 1) / (8 * lanes)) > a.many_ctas) lanes *= 2;
+    const int groups = 256 / lanes, group = tid / lanes, cols = 8 * lanes;
+    const int64_t chunks = (a.D + cols - 1) / cols;
+    for (int64_t u = blockIdx.x; u < n * chunks; u += a.many_ctas) {
+        const int64_t slot = u / chunks, col = u % chunks * cols + tid % lanes * 8;
+        if (!ADALN_IN_LOSS(slot < a.many.slots)) break;
+        const int32_t word = a.many.word[slot];
+        const char* x = reinterpret_cast<const char*>(a.xp) + col * 2;
+        f2r s[4] = {kPairZero, kPairZero, kPairZero, kPairZero};
+        for (int64_t r0 = 0; r0 < nact; r0 += kListRows) {
+            if (r0 > 0 || u != blockIdx.x) targets(r0);
+            uint32_t on[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t row = r0 + 1024 * j + 4 * tid;
+                on[j] = (t[j].x == word) | (t[j].y == word && row + 1 < nact) << 1 |
+                        (t[j].z == word && row + 2 < nact) << 2 | (t[j].w == word && row + 3 < nact) << 3;
+            }
+            int before[8];  // of the warp's rows of this j
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                int all = 0;
+                before[j] = 0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t b = __ballot_sync(0xFFFFFFFFu, on[j] >> c & 1u);
+                    before[j] += __popc(b & ((1u << lane) - 1u));
+                    all += __popc(b);
+                }
+                if (lane == 0) totals[j][warp] = all;
+            }
+            __syncthreads();
+            int count = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    before[j] += w < warp ? totals[j][w] : 0;
+                }
+                before[j] += count;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) count += totals[j][w];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (on[j] >> c & 1u) list[before[j]++] = (uint16_t)(1024 * j + 4 * tid + c);
+                }
+            }
+            __syncthreads();
+            for (int k = group; k < count; k += 8 * groups) {  // eight loads on their way
+                uint4 q[8];
+                float lo[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    q[j] = make_uint4(0, 0, 0, 0);
+                    lo[j] = 0.0f;
+                    if (k + j * groups < count) {
+                        const int64_t row = r0 + list[k + j * groups];
+                        if (!ADALN_IN_LOSS(row < nact)) continue;
+                        lo[j] = a.row_lo[row];
+                        if (col < a.D) q[j] = ld_keep(x + row * a.D * 2);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    f2r v[4];
+                    Io<__nv_bfloat16>::unpackp(q[j], v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[e] = p_fma(p_splat(lo[j]), v[e], s[e]);
+                }
+            }
+            __syncthreads();  // the list has been read
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<float2*>(red + 8 * tid + 2 * e) = p_get(s[e]);
+        __syncthreads();
+        for (int c = tid; c < cols; c += 256) {
+            const int64_t out = u % chunks * cols + c;
+            if (out >= a.D || !ADALN_IN_LOSS(word >= 0 && word < a.V)) break;
+            float sum = a.many.sums[slot * a.D + out];
+            for (int g = 0; g < groups; ++g) sum += red[g * cols + c];
+            a.dweight[word * a.D + out] = __float2bfloat16_rn(sum);
+        }
+        __syncthreads();
+    }
+}
+
 // dx of the packed rows: the parts added in order, then what rounding dz of the target left off,
-// rounded once, back to the rows' places. 28 us for 8192 rows of 2048 (4.8 TB/s).
-__global__ void __launch_bounds__(256) dx_kernel(const DxArgs a) {
+// rounded once, back to the rows' places. 28 us for 8192 rows of 2048 (4.8 TB/s). MANY: the first
+// a.many_ctas CTAs have dweight of the words of more than kHits rows instead.
+template <bool MANY>
+__global__ void __launch_bounds__(256, MANY ? 2 : 3) finish_kernel(const FinishArgs a) {
     pdl_begin();
     const int64_t nact = *a.nact, vecs = a.D / 8;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < nact * vecs; i += (int64_t)gridDim.x * 256) {
+    if constexpr (MANY) {
+        if ((int)blockIdx.x < a.many_ctas) {
+            add_remainders(a, nact);
+            return;
+        }
+    }
+    const int many = MANY ? a.many_ctas : 0;
+    const int64_t block = (int64_t)blockIdx.x - many, step = (int64_t)(gridDim.x - many) * 256;
+    for (int64_t i = block * 256 + threadIdx.x; i < nact * vecs; i += step) {
         const int64_t p = i / vecs, v = i % vecs;
         if (!ADALN_IN_LOSS(p < a.Np)) continue;
         const int64_t r = a.row[p];
@@ -875,12 +1008,17 @@ cudaError_t launch_lse(const LseArgs& args, int sms, cudaStream_t stream) {
                             dim3(1024), params, 0, stream);
 }
 
-cudaError_t launch_dx(const DxArgs& args, int sms, cudaStream_t stream) {
-    DxArgs a = args;
+cudaError_t launch_finish(const FinishArgs& args, int sms, cudaStream_t stream) {
+    FinishArgs a = args;
     void* params[] = {&a};
-    const int64_t want = (a.Np * (a.D / 8) + 255) / 256;
-    return launch_dependent(reinterpret_cast<const void*>(&dx_kernel), dim3(cap(want, 8 * (int64_t)sms)), dim3(256),
-                            params, 0, stream);
+    const bool many = a.dweight != nullptr;
+    // One of the two CTAs that an SM holds; the other is left to dx (both: the same time; the last CTAs
+    // instead of the first: 119 us against 108 at 8192 x 1000 x 1024).
+    a.many_ctas = many ? (int)cap(a.many.slots * ((a.D + 63) / 64), (int64_t)sms) : 0;
+    const unsigned dx_ctas = a.dx ? cap((a.Np * (a.D / 8) + 255) / 256, 8 * (int64_t)sms) : 0;
+    const void* fn = many ? reinterpret_cast<const void*>(&finish_kernel<true>)
+                          : reinterpret_cast<const void*>(&finish_kernel<false>);
+    return launch_dependent(fn, dim3(a.many_ctas + dx_ctas), dim3(256), params, 0, stream);
 }
 
 cudaError_t debug_word_xent(uint32_t* out, bool reset) { return debug_word(out, reset); }

@@ -19,11 +19,21 @@ constexpr int kPairs = 76;  // CTA pairs the tiles are shared out to
 inline int tile_cols(int64_t row_tiles, int64_t cols) {
     return row_tiles * ((cols + kTileN - 1) / kTileN) < kPairs ? kTileN / 2 : kTileN;
 }
-// dweight takes what rounding dz of the target left off in fp32 for words that are the target of
-// at most this many rows; over more rows the roundings, made by chance (target_dz), average out.
+// dweight takes what rounding dz of the target left off in fp32: from a list of the word's rows in the
+// epilogue of its products if they are at most kHits, else in finish_kernel.
 constexpr int kHits = 8;
 constexpr int kPackThreads = 256;
 constexpr int kPackCtas = 608;  // four per SM: every CTA also counts the rows before its own
+
+// Words that are the target of more than kHits rows: at most slots, a place each, in the order in
+// which they were found (nothing that is computed depends on it).
+struct ManyRows {
+    int32_t* count;   // places taken
+    int32_t* word;    // [slots]
+    int32_t* slot;    // [V]: the place of a word that has one
+    float* sums;      // [slots][D]: dweight without the remainders
+    int64_t slots;
+};
 
 struct PackArgs {
     const void* x;          // [N, D]
@@ -39,6 +49,7 @@ struct PackArgs {
     float* row_gt;
     int32_t* nact;          // packed rows
     int32_t* word_hits;     // backward: zeros [V], or null
+    ManyRows many;          // backward with word_hits: its count, zero
     float* loss_out;        // forward: zeros for rows without a loss, or null
     float* lse_out;
     void* dx;               // backward: zeros for rows without a loss, or null
@@ -52,13 +63,13 @@ struct LogitsArgs {
     const int32_t* tgt;
     float2* parts;          // statistics: [2 * tiles][Np] (max, sum exp)
     float* zt;              // statistics: [Np], the target's logit
-    const __nv_bfloat16* xp;  // dz: packed rows [Np, D]
-    const float* row_lse;
+    const float* row_lse;   // dz
     const float* row_gs;
     const float* row_gt;
     float* row_lo;          // dz: [Np], what rounding dz of the target left off
     int32_t* word_hits;     // dz: rows whose target each word is [V], and the first kHits of them
     int32_t* word_rows;     // in the order they came [V, kHits]; or null
+    ManyRows many;          // dz, with word_hits: count, word and slot
     __nv_bfloat16* probs;   // dz [Np, ldp]
     int64_t ldp;
     uint32_t* status;
@@ -73,6 +84,7 @@ struct GradArgs {
     const void* xp;
     const int32_t* word_hits;
     const int32_t* word_rows;
+    ManyRows many;          // writes sums
     const float* row_lo;
     uint32_t* status;
     int64_t Np, D, V, v0, v1;
@@ -91,16 +103,20 @@ struct LseArgs {
     int nparts;
 };
 
-struct DxArgs {
+struct FinishArgs {
     const int32_t* nact;
     const int32_t* row;
     const float* dxacc;
     const void* weight;
+    const void* xp;
     const int32_t* tgt;
     const float* row_lo;
-    void* dx;
-    int64_t N, Np, D;
+    ManyRows many;
+    void* dx;               // or null
+    __nv_bfloat16* dweight; // or null
+    int64_t N, Np, D, V;
     int splits;
+    int many_ctas;          // set by launch_finish
 };
 
 cudaError_t launch_pack(const PackArgs& args, int ctas, cudaStream_t stream);
@@ -109,7 +125,7 @@ cudaError_t launch_logits(const LogitsArgs& args, bool probs, const void* xp, co
 cudaError_t launch_grad(const GradArgs& args, const void* probs, int64_t ldp, const void* xp, const void* weight,
                         int sms, cudaStream_t stream);
 cudaError_t launch_lse(const LseArgs& args, int sms, cudaStream_t stream);
-cudaError_t launch_dx(const DxArgs& args, int sms, cudaStream_t stream);
+cudaError_t launch_finish(const FinishArgs& args, int sms, cudaStream_t stream);
 cudaError_t debug_word_xent(uint32_t* out, bool reset);
 
 }  // namespace adaln

@@ -88,3 +88,23 @@ def test_debug_build_checks_pass_over_several_pieces(debug_lib, name):  # noqa: 
         word = A.adaln_debug_read(reset=True)
     assert word == 0, {v: n for v, n in A.DEBUG_CLASSES.items() if word & v}
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+# Words of many rows, their rows listed in one part and in two.
+WORDS = {
+    "loss-3000x20x264": lambda A: _loss(A, 3000, 20, 264, 0.1),
+    "loss-20000x300x72": lambda A: _loss(A, 20000, 300, 72, 0.3),
+    "loss-900x70x2056": lambda A: _loss(A, 900, 70, 2056, 0.0),
+}
+
+
+@pytest.mark.parametrize("name", sorted(WORDS))
+def test_debug_build_checks_pass_with_words_of_many_rows(debug_lib, name):  # noqa: F811
+    import torch
+    with library("release") as A:
+        want = WORDS[name](A)
+    with library("debug") as A:
+        got = WORDS[name](A)
+        word = A.adaln_debug_read(reset=True)
+    assert word == 0, {v: n for v, n in A.DEBUG_CLASSES.items() if word & v}
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

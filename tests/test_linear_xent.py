@@ -524,3 +524,31 @@ def test_a_smaller_batch_in_a_larger_ones_workspace():
             else:
                 A.adaln_linear_xent_bwd(x, w, t, lse, up, ul, dx, dw, N, words, D, IGNORE, ws, nb)
         assert all(torch.equal(a, b) for a, b in zip((loss, lse, dx, dw), want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ignored", [0.0, 0.3])
+@pytest.mark.parametrize("N,V,D", [(4096, 24, 256), (8192, 16, 520), (20001, 5, 264), (3001, 300, 1032),
+                                   (2000, 100, 4104), (700, 2, 72), (9, 1, 8)])
+def test_words_of_many_rows_keep_their_targets_remainders(N, V, D, ignored):
+    # Every target's rounding is given back in fp32, however many rows a word has: what is left is the
+    # rounding of the other elements of dz, and the result's.
+    x, w, t, up, ul = inputs(N, V, D, ignored, seed=26)
+    got = call(x, w, t, up, ul)
+    check(x, w, t, up, ul, got)
+    again = call(x, w, t, up, ul, want_x=False)
+    assert torch.equal(again[3], got[3])
+    on = (t >= 0) & (t < V)
+    xd, td = x[on].double(), t[on]
+    z = xd @ w.double().t()
+    dz = torch.exp(z - torch.logsumexp(z, 1, keepdim=True)) * (up + ul)[on].double()[:, None]
+    rows = torch.arange(len(td), device="cuda")
+    others = dz.clone()
+    others[rows, td] = 0
+    dz[rows, td] -= up[on].double()
+    ref = dz.t() @ xd
+    # A rounding is even over its half step: h / sqrt(3) at most, root mean square, all independent. A
+    # twentieth more for the sample of D * V of them (a quarter below 10,000), and the fp32 sums.
+    size = (H ** 2 / 3 * (ref.norm() ** 2 + ((others ** 2).t() @ xd ** 2).sum())) ** 0.5
+    fp32 = 2.0 ** -18 * (dz.t().abs() @ xd.abs()).norm()
+    assert (got[3].double() - ref).norm() <= (1.05 if D * V > 10000 else 1.25) * size + fp32
