@@ -552,3 +552,17 @@ def test_words_of_many_rows_keep_their_targets_remainders(N, V, D, ignored):
     size = (H ** 2 / 3 * (ref.norm() ** 2 + ((others ** 2).t() @ xd ** 2).sum())) ** 0.5
     fp32 = 2.0 ** -18 * (dz.t().abs() @ xd.abs()).norm()
     assert (got[3].double() - ref).norm() <= (1.05 if D * V > 10000 else 1.25) * size + fp32
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,V,D", [(300, 16, 2048), (2000, 24, 2048)])
+def test_losses_of_wide_rows_and_few_words_keep_a_millionth(N, V, D):
+    # The tensor cores cut a sum after each 16 products, always towards zero, so that the errors of
+    # D / 16 steps add up. Losses of a few words (2 or 3) show it most; 2^-20 of them is asked for.
+    x, w, t, up, ul = inputs(N, V, D, seed=27)
+    loss, lse = call(x, w, t, up, ul, backward=False)
+    z = x.double() @ w.double().t()
+    L = torch.logsumexp(z, 1)
+    want = L - z.gather(1, t[:, None]).squeeze(1)
+    assert (lse.double() - L).norm() <= 2.0 ** -20 * L.norm()
+    assert (loss.double() - want).norm() <= 2.0 ** -20 * want.norm()
