@@ -271,8 +271,10 @@ bool make_plan(Kind kind, adaln_dtype dtype, int64_t D, int form, int64_t R, Pla
     // 68.1 -> 67.2 us). One-warp CTAs are faster in a single wave.
     if (kind == kFwd && p->ring == kRingBulk && p->c.tpb > 32) p->G = std::min<int64_t>(2 * p->G, kMaxCtas);
     // The affine layer norm's backward gives every tile two rows before it gives every row a tile,
-    // once there are more rows than SMs: half the partials to add (bf16 257 x 1152: 9.4 -> 8.0 us,
-    // 257 x 1536: 9.9 -> 8.8; 600 rows and more measured the same).
+    // once there are more rows than SMs: half the partials to add. Every row a tile -> two: bf16 D=1152
+    // 153 rows 8.7 -> 7.2 us, 257 rows 9.4 -> 8.1, 600 rows 9.2 -> 9.1; D=512 6.8 -> 6.4, 7.7 -> 6.9,
+    // 8.9 -> 7.8; D=5120 9.1 -> 9.2, 9.4, 10.9; D=16384 20.2 -> 18.2, 20.5 -> 21.0, 24.8 -> 24.9; fp32
+    // D=1536 7.1 -> 7.3, 8.9 -> 9.0, 9.2 -> 9.8; D=8192 13.3 -> 11.9, 13.6 -> 13.7, 16.7.
     if (kind == kBwd && form == kAffine && R > p->sms) p->G = std::min(p->G, (R + 1) / 2);
     if (p->G > R) p->G = R;
     if (p->G < 1) p->G = 1;
@@ -896,7 +898,7 @@ namespace {
 // Pieces of the vocabulary in the backward: dz of one piece is at most this large unless a
 // piece would be narrower than kMinPiece columns. Each piece adds to the fp32 dx once more and ends
 // in a partly filled wave: 8192 x 50257 x 2048, backward: 64 MiB 3.3 ms, 128 MiB 3.0 ms, 256 MiB
-// 2.9 ms, 512 MiB 2.8 ms.
+// 2.9 ms, 512 MiB 2.8 ms; 256 because the workspace, mostly dz, would double for the last 3%.
 constexpr int64_t kProbsBytes = (int64_t)256 << 20;
 constexpr int64_t kMinPiece = 2048;
 

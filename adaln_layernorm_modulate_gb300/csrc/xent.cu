@@ -19,8 +19,8 @@
 // they leave off is kept and added in fp32, to dx, and to dW in the order of the word's rows.
 //
 // Bound by the tensor cores from a few hundred rows on: 8192 rows, 50,257 words, D = 2048 take
-// 0.81 ms forward (2.1 PFLOP/s, the tensor pipe 97% active) and 2.8 ms backward; with a few rows by
-// the chain of launches (1 row, 1000 words, D = 512: 9.4 us forward, 16.5 us backward on the device).
+// 0.81 ms forward (2.1 PFLOP/s, the tensor pipe 96% active) and 2.8 ms backward; with a few rows by
+// the chain of launches (1 row, 1000 words, D = 512: 9.6 us forward, 17.2 us backward on the device).
 #include <algorithm>
 #include <atomic>
 
@@ -402,8 +402,8 @@ __device__ __forceinline__ void gemm_loop(Units count, uint32_t* status, Decode 
 }
 
 // The tile's logits, as row statistics (PROBS false) or as dz (PROBS true). Tiles of all rows first:
-// x stays in L2 and the weight is read once. 8192 x 50257 x 2048: 793 us for the statistics (2.13
-// PFLOP/s); dz, whose epilogue also writes 0.8 GB through shared memory, 909 us (1.86 PFLOP/s).
+// x stays in L2 and the weight is read once. 8192 x 50257 x 2048: 782 us for the statistics (2.16
+// PFLOP/s); dz, whose epilogue also writes 0.8 GB through shared memory, 929 us (1.82 PFLOP/s).
 template <bool PROBS, int TN>
 __global__ void __launch_bounds__(kGemmThreads, 1) logits_kernel(const __grid_constant__ CUtensorMap mx,
                                                               const __grid_constant__ CUtensorMap mw,
@@ -887,7 +887,7 @@ __device__ __forceinline__ void add_remainders(const FinishArgs& a, int64_t nact
 }
 
 // dx of the packed rows: the parts added in order, then what rounding dz of the target left off,
-// rounded once, back to the rows' places. 28 us for 8192 rows of 2048 (4.8 TB/s). MANY: the first
+// rounded once, back to the rows' places. 32 us for 8192 rows of 2048 (4.2 TB/s). MANY: the first
 // a.many_ctas CTAs have dweight of the words of more than kHits rows instead.
 template <bool MANY>
 __global__ void __launch_bounds__(256, MANY ? 2 : 3) finish_kernel(const FinishArgs a) {

@@ -15,7 +15,7 @@ constexpr int kCtaM = kTileM / 2;
 constexpr int kPairs = 76;  // CTA pairs the tiles are shared out to
 // Columns a tile: 256, or 128 where that leaves pairs without one: a pair's product takes the same
 // time a column whatever its rows hold, so a few rows are through sooner in narrower tiles (96 x
-// 8192 x 1024, forward: 12.6 us against 14.8; backward 32.0 against 34.3).
+// 8192 x 1024, forward: 12.8 us against 14.8; backward 31.0 against 33.6).
 inline int tile_cols(int64_t row_tiles, int64_t cols) {
     return row_tiles * ((cols + kTileN - 1) / kTileN) < kPairs ? kTileN / 2 : kTileN;
 }

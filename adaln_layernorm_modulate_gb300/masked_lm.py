@@ -5,7 +5,8 @@ loss: the operators of this package together, as a training step uses them.
 
 Every sequence draws a noise level t in (0.1, 1] and hides each of its tokens with probability t.
 The model sees the rest; its rows pass one AdaLN-modulated block (a sequence's shift and scale
-come from its t) with a mixing step along the sequence, a final affine layer norm and the
+come from its t) with a mixing step along the packed rows (each with the row before and the one
+after it, which at a sequence's ends are its neighbours' in the pack), a final affine layer norm and the
 vocabulary head, whose loss counts the hidden tokens only, weighted by 1 / t. Tokens follow a
 fixed successor table, so a hidden token can be told from its neighbours and the loss falls.
 """

@@ -19,7 +19,9 @@
  * The backward reduces dshift/dscale with threads pinned to a feature index d that
  * accumulate down the sequence (the section's "D-tile coalesced reduction"), into per-tile
  * fp32 partials that a second, fixed-order stage sums: results are bitwise reproducible
- * run to run on the same device with the same arguments. No float atomics are used.
+ * run to run on the same device with the same arguments. No float atomics are used whose order
+ * could show (the vocabulary loss adds each later piece's part of dx in place, one addition to an
+ * element and launch).
  *
  * Layouts (all row-major, D contiguous):
  *   x, y, dy, dx      [R, D]   in `dtype`       R = Bt*N (dense) or total_tokens (packed)
@@ -266,8 +268,11 @@ int adaln_layernorm_bwd(const void* dy, const void* x, const float* mean, const 
  *
  * x, weight, dx, dweight: `dtype` ADALN_BF16 (ADALN_F32 is ADALN_ERR_UNSUPPORTED: the products
  * run on the tensor cores, whose operands are bf16), 16-byte aligned, contiguous; loss, lse,
- * dloss, dlse: fp32. Products accumulate in fp32; dz is rounded to bf16 before its two
- * products, dx and dweight once at the end. Results are bitwise reproducible.
+ * dloss, dlse: fp32. Products accumulate in fp32 on the tensor cores, which cut sums towards zero
+ * after every 16 terms (losses are good to 1e-6 of themselves at D = 2048). dz is rounded to bf16
+ * before its two products, but the target's remainder is added to both in fp32; dx and dweight are
+ * rounded once at the end. The loss is taken from the distance to the row's largest logit, so it
+ * is not negative and small losses are exact to fp32. Results are bitwise reproducible.
  * N >= 0, 1 <= V, D as everywhere. dlse may be null (lse is not differentiated); dx or dweight
  * may be null (not wanted). With N = 0 the backward writes zero dweight. The backward takes the
  * forward's lse and must get its ignore_index. Workspace as *_workspace_size says (they do not
