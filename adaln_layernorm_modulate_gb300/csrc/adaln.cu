@@ -912,12 +912,12 @@ struct XentPlan {
     int splits;          // backward: parts of dx's sum over a piece
     int64_t slots;       // backward: words that may be the target of more than kHits rows
     // Workspace offsets.
-    size_t nact, row, tgt, f0, f1, f2, f3, hits, words, many_word, many_slot, many_sums, xp, big,
-        dxacc, bytes;
+    size_t nact, row, tgt, f0, f1, f2, f3, hits, words, many_word, many_slot, many_sums, many_first,
+        many_next, many_rows, xp, big, dxacc, bytes;
     size_t most;         // bytes of any plan of at most as many rows
 };
 
-// Workspace: [header | status words | nact and the count of words of many rows | row | tgt | four row arrays | rows of
+// Workspace: [header | status words | nact and two counts of words of many rows | row | tgt | four row arrays | rows of
 // each word as a target, words of many rows (backward) | packed x |
 // partials (forward) or dz (backward) | dx in fp32 (backward)].
 XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
@@ -944,7 +944,7 @@ XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
         return o;
     };
     const size_t rows = (size_t)p.Np;
-    p.nact = take(2 * sizeof(int32_t));
+    p.nact = take(3 * sizeof(int32_t));
     p.row = take(rows * 4);
     p.tgt = take(rows * 4);
     p.f0 = take(rows * 4);
@@ -958,6 +958,11 @@ XentPlan xent_plan(int64_t N, int64_t V, int64_t D, bool bwd) {
         p.many_word = take((size_t)p.slots * 4);
         p.many_slot = take((size_t)V * 4);
         p.many_sums = take((size_t)p.slots * (size_t)D * 4);
+        if (N > kListRows) {
+            p.many_first = take((size_t)p.slots * 4);
+            p.many_next = take((size_t)p.slots * 4);
+            p.many_rows = take(rows * 4);
+        }
     }
     p.xp = take(rows * (size_t)D * 2);
     p.big = take(bwd ? rows * (size_t)p.piece * 2 : rows * (size_t)p.tiles * 2 * sizeof(float2));
@@ -1105,7 +1110,13 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
     if (dweight) {
         k.word_hits = at<int32_t>(workspace, p.hits);
         k.many = {k.nact + 1, at<int32_t>(workspace, p.many_word), at<int32_t>(workspace, p.many_slot),
-                  at<float>(workspace, p.many_sums), p.slots};
+                  at<float>(workspace, p.many_sums), p.slots, nullptr, nullptr, nullptr, nullptr};
+        if (N > kListRows) {
+            k.many.listed = k.nact + 2;
+            k.many.first = at<int32_t>(workspace, p.many_first);
+            k.many.next = at<int32_t>(workspace, p.many_next);
+            k.many.rows = at<int32_t>(workspace, p.many_rows);
+        }
     }
     const int ctas = pack_ctas(N);
     if (int rc = launched(launch_pack(k, ctas, stream))) return rc;
@@ -1158,6 +1169,7 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
     d.tgt = k.tgt;
     d.xp = k.xp;
     d.row_lo = at<float>(workspace, p.f3);
+    d.word_hits = k.word_hits;
     d.many = k.many;
     d.dx = dx;
     d.dweight = N > kHits ? static_cast<__nv_bfloat16*>(dweight) : nullptr;
@@ -1166,6 +1178,9 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
     d.D = D;
     d.V = V;
     d.splits = p.splits;
+    if (d.many.listed) {
+        if (int rc = launched(launch_lists(d, sms, stream))) return rc;
+    }
     return launched(launch_finish(d, sms, stream));
 }
 

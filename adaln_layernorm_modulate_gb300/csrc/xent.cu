@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
         if (tid == 0) {
             *a.nact = base;
             if (a.many.count) *a.many.count = 0;
+            if (a.many.listed) *a.many.listed = 0;
         }
     }
     const bool any_bad = __syncthreads_or(bad);
@@ -773,21 +774,53 @@ __global__ void __launch_bounds__(1024) lse_kernel(const LseArgs a) {
     }
 }
 
+// Lists the rows of the words of more than kHits: room for each word's, then the rows.
+__global__ void __launch_bounds__(256) list_words_kernel(const FinishArgs a) {
+    pdl_begin();
+    const int n = *a.many.count, lane = threadIdx.x & 31;
+    for (int s0 = blockIdx.x * 256; s0 < n; s0 += gridDim.x * 256) {
+        const int s = s0 + threadIdx.x;
+        const bool in = s < n && ADALN_IN_LOSS(s < a.many.slots);
+        const int hits = in ? a.word_hits[a.many.word[s]] : 0;
+        int upto = hits;
+        for (int o = 1; o < 32; o *= 2) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        int at = 0;
+        if (lane == 31) at = atomicAdd(a.many.listed, upto);
+        at = __shfl_sync(0xFFFFFFFFu, at, 31) + upto - hits;
+        if (in) a.many.first[s] = a.many.next[s] = at;
+    }
+}
+__global__ void __launch_bounds__(256) list_rows_kernel(const FinishArgs a) {
+    pdl_begin();
+    const int64_t nact = *a.nact;
+    for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < nact; r += (int64_t)gridDim.x * 256) {
+        if (!ADALN_IN_LOSS(r < a.Np)) continue;
+        const int32_t word = a.tgt[r];
+        if (!ADALN_IN_LOSS(word >= 0 && word < a.V) || a.word_hits[word] <= kHits) continue;
+        const int32_t slot = a.many.slot[word];
+        if (!ADALN_IN_LOSS(slot >= 0 && slot < a.many.slots)) continue;
+        const int at = atomicAdd(a.many.next + slot, 1);
+        if (ADALN_IN_LOSS(at >= 0 && at < a.Np)) a.many.rows[at] = (int32_t)r;
+    }
+}
+
 // dweight of the words of more than kHits rows: what the products left, and the remainders of all their
-// rows' targets. A CTA takes a word and some columns at a time: it lists the word's rows, in their
-// order, from the targets of kListRows rows, and adds them up in groups of threads, every group a fixed
+// rows' targets. A CTA takes a word and some columns at a time: it puts the word's rows in order, from
+// the targets of kListRows rows at a time or from the word's list, and adds them up in groups of threads, every group a fixed
 // share of the list; then the groups' sums in their order. The more such words, the more columns at a
 // time (64 columns are 32 groups of 8 threads): as few as leave no CTA a second word, so that a few words
 // of many rows are shared out and many words are listed once or twice. What it adds to a backward, without
 // such words and with them: nothing at 96 x 8192 x 1024 (30.2 us), 29.7 -> 33.4 us at 4096 x 24 x 256,
 // 96 -> 108 us at 8192 x 1000 x 1024, 48 -> 64 us at 8192 x 2 x 512.
-constexpr int kListRows = 8192;
 __device__ __forceinline__ void add_remainders(const FinishArgs& a, int64_t nact) {
-    __shared__ uint16_t list[kListRows];
+    __shared__ __align__(16) uint16_t list[kListRows];
     __shared__ int totals[8][8];
     __shared__ __align__(16) float red[2048];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // Thread tid looks at rows r0 + 1024 j + 4 tid ..; the first ones before anything else is known.
+    // Thread tid looks at rows r0 + 1024 j + 4 tid ..; without lists before anything else is known.
     int4 t[8];
     auto targets = [&](int64_t r0) {
 #pragma unroll
@@ -797,7 +830,7 @@ __device__ __forceinline__ void add_remainders(const FinishArgs& a, int64_t nact
             if (row < nact && ADALN_IN_LOSS(row + 4 <= a.Np)) t[j] = *reinterpret_cast<const int4*>(a.tgt + row);
         }
     };
-    targets(0);
+    if (!a.many.listed) targets(0);
     const int64_t n = *a.many.count;
     int lanes = 8;  // threads a group
     while (lanes < 256 && 8 * lanes < a.D && n * ((a.D + 8 * lanes - 1) / (8 * lanes)) > a.many_ctas) lanes *= 2;
@@ -809,8 +842,51 @@ __device__ __forceinline__ void add_remainders(const FinishArgs& a, int64_t nact
         const int32_t word = a.many.word[slot];
         const char* x = reinterpret_cast<const char*>(a.xp) + col * 2;
         f2r s[4] = {kPairZero, kPairZero, kPairZero, kPairZero};
-        for (int64_t r0 = 0; r0 < nact; r0 += kListRows) {
-            if (r0 > 0 || u != blockIdx.x) targets(r0);
+        auto add = [&](int count, auto row_of) {
+            for (int k = group; k < count; k += 8 * groups) {  // eight loads on their way
+                uint4 q[8];
+                float lo[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    q[j] = make_uint4(0, 0, 0, 0);
+                    lo[j] = 0.0f;
+                    if (k + j * groups < count) {
+                        const int64_t row = row_of(k + j * groups);
+                        if (!ADALN_IN_LOSS(row >= 0 && row < nact)) continue;
+                        lo[j] = a.row_lo[row];
+                        if (col < a.D) q[j] = ld_keep(x + row * a.D * 2);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    f2r v[4];
+                    Io<__nv_bfloat16>::unpackp(q[j], v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[e] = p_fma(p_splat(lo[j]), v[e], s[e]);
+                }
+            }
+            __syncthreads();  // the list has been read
+        };
+        const int hits = a.many.listed && ADALN_IN_LOSS(word >= 0 && word < a.V) ? a.word_hits[word] : INT32_MAX;
+        if (hits <= kSortRows) {
+            // In order: a row's place is the number of rows before it.
+            int* unsorted = reinterpret_cast<int*>(list);
+            int* sorted = unsorted + kSortRows;
+            const int64_t first = a.many.first[slot];
+            for (int k = tid; k < hits; k += 256)
+                unsorted[k] = ADALN_IN_LOSS(first + k < a.Np) ? a.many.rows[first + k] : 0;
+            __syncthreads();
+            for (int k = tid; k < hits; k += 256) {
+                const int row = unsorted[k];
+                int place = 0;
+                for (int i = 0; i < hits; ++i) place += unsorted[i] < row;
+                sorted[place] = row;
+            }
+            __syncthreads();
+            add(hits, [&](int k) { return (int64_t)sorted[k]; });
+        }
+        for (int64_t r0 = 0; hits > kSortRows && r0 < nact; r0 += kListRows) {
+            if (a.many.listed) targets(r0);  // else all of them are in one look
             uint32_t on[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -848,29 +924,7 @@ __device__ __forceinline__ void add_remainders(const FinishArgs& a, int64_t nact
                 }
             }
             __syncthreads();
-            for (int k = group; k < count; k += 8 * groups) {  // eight loads on their way
-                uint4 q[8];
-                float lo[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    q[j] = make_uint4(0, 0, 0, 0);
-                    lo[j] = 0.0f;
-                    if (k + j * groups < count) {
-                        const int64_t row = r0 + list[k + j * groups];
-                        if (!ADALN_IN_LOSS(row < nact)) continue;
-                        lo[j] = a.row_lo[row];
-                        if (col < a.D) q[j] = ld_keep(x + row * a.D * 2);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    f2r v[4];
-                    Io<__nv_bfloat16>::unpackp(q[j], v);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[e] = p_fma(p_splat(lo[j]), v[e], s[e]);
-                }
-            }
-            __syncthreads();  // the list has been read
+            add(count, [&](int k) { return r0 + list[k]; });
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) *reinterpret_cast<float2*>(red + 8 * tid + 2 * e) = p_get(s[e]);
@@ -1023,6 +1077,16 @@ cudaError_t launch_lse(const LseArgs& args, int sms, cudaStream_t stream) {
     void* params[] = {&a};
     return launch_dependent(reinterpret_cast<const void*>(&lse_kernel), dim3(cap(a.Np / 32, 2 * (int64_t)sms)),
                             dim3(1024), params, 0, stream);
+}
+
+cudaError_t launch_lists(const FinishArgs& args, int sms, cudaStream_t stream) {
+    FinishArgs a = args;
+    void* params[] = {&a};
+    const unsigned words = cap((a.many.slots + 255) / 256, 4 * (int64_t)sms), rows = cap(a.Np / 256, 8 * (int64_t)sms);
+    if (cudaError_t e = launch_dependent(reinterpret_cast<const void*>(&list_words_kernel), dim3(words), dim3(256), params,
+                                         0, stream))
+        return e;
+    return launch_dependent(reinterpret_cast<const void*>(&list_rows_kernel), dim3(rows), dim3(256), params, 0, stream);
 }
 
 cudaError_t launch_finish(const FinishArgs& args, int sms, cudaStream_t stream) {

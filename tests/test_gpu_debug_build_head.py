@@ -90,10 +90,11 @@ def test_debug_build_checks_pass_over_several_pieces(debug_lib, name):  # noqa: 
     assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
-# Words of many rows, their rows listed in one part and in two.
+# Words of many rows: looked for among all targets, in one look and in three, and listed.
 WORDS = {
     "loss-3000x20x264": lambda A: _loss(A, 3000, 20, 264, 0.1),
     "loss-20000x300x72": lambda A: _loss(A, 20000, 300, 72, 0.3),
+    "loss-20000x9x72": lambda A: _loss(A, 20000, 9, 72, 0.3),
     "loss-900x70x2056": lambda A: _loss(A, 900, 70, 2056, 0.0),
 }
 

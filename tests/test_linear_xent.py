@@ -529,7 +529,7 @@ def test_a_smaller_batch_in_a_larger_ones_workspace():
 @pytest.mark.gpu
 @pytest.mark.parametrize("ignored", [0.0, 0.3])
 @pytest.mark.parametrize("N,V,D", [(4096, 24, 256), (8192, 16, 520), (20001, 5, 264), (3001, 300, 1032),
-                                   (2000, 100, 4104), (700, 2, 72), (9, 1, 8)])
+                                   (2000, 100, 4104), (700, 2, 72), (9, 1, 8), (40000, 900, 72)])
 def test_words_of_many_rows_keep_their_targets_remainders(N, V, D, ignored):
     # Every target's rounding is given back in fp32, however many rows a word has: what is left is the
     # rounding of the other elements of dz, and the result's.
@@ -552,6 +552,19 @@ def test_words_of_many_rows_keep_their_targets_remainders(N, V, D, ignored):
     size = (H ** 2 / 3 * (ref.norm() ** 2 + ((others ** 2).t() @ xd ** 2).sum())) ** 0.5
     fp32 = 2.0 ** -18 * (dz.t().abs() @ xd.abs()).norm()
     assert (got[3].double() - ref).norm() <= (1.05 if D * V > 10000 else 1.25) * size + fp32
+
+
+@pytest.mark.gpu
+def test_words_of_many_and_of_very_many_rows():
+    # More rows than are looked at together: words of a few hundred rows go by lists, the others not.
+    N, V, D = 30000, 400, 136
+    x, w, t, up, ul = inputs(N, V, D, 0.1, seed=28)
+    t[::3] = torch.where(t[::3] == IGNORE, t[::3], t[::3] % 4)
+    t[7:7 + 512 * 2:2] = 399
+    t[N - 1] = 399
+    got = call(x, w, t, up, ul)
+    check(x, w, t, up, ul, got)
+    assert all(torch.equal(a, b) for a, b in zip(call(x, w, t, up, ul), got))
 
 
 @pytest.mark.gpu
