@@ -37,6 +37,9 @@ EXPORTS = (
     "adaln_layernorm_fwd", "adaln_layernorm_bwd_workspace_size", "adaln_layernorm_bwd",
     "adaln_linear_xent_fwd_workspace_size", "adaln_linear_xent_fwd",
     "adaln_linear_xent_bwd_workspace_size", "adaln_linear_xent_bwd",
+    "adaln_qk_norm_rope_fwd", "adaln_qk_norm_rope_bwd_workspace_size", "adaln_qk_norm_rope_bwd",
+    "adaln_attention_fwd_workspace_size", "adaln_attention_fwd",
+    "adaln_attention_bwd_workspace_size", "adaln_attention_bwd",
     "adaln_bucket_batch", "adaln_bucket_batch_real",
     "adaln_fit_step_cost", "adaln_bucket_load_cv", "adaln_status_string",
 )
@@ -88,6 +91,15 @@ def _load() -> ctypes.CDLL:
         "adaln_linear_xent_fwd": ([vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, sz, ci, vp], ci),
         "adaln_linear_xent_bwd_workspace_size": ([i64, i64, i64, ci], sz),
         "adaln_linear_xent_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, sz, ci, vp], ci),
+        "adaln_qk_norm_rope_fwd": ([vp] * 7 + [i64, i32, i32, i32] + [i64] * 4
+                                   + [vp, i32, ctypes.c_double, f32, ci, ci, vp], ci),
+        "adaln_qk_norm_rope_bwd_workspace_size": ([i64, i32, i32, i32, ci], sz),
+        "adaln_qk_norm_rope_bwd": ([vp] * 12 + [sz, i64, i32, i32, i32] + [i64] * 6
+                                   + [vp, i32, ctypes.c_double, f32, ci, ci, vp], ci),
+        "adaln_attention_fwd_workspace_size": ([i64, i64, i64, i32, i32, i32, ci], sz),
+        "adaln_attention_fwd": ([vp] * 7 + [i64] * 3 + [i32] * 3 + [i64] * 4 + [f32, ci, vp, sz, ci, vp], ci),
+        "adaln_attention_bwd_workspace_size": ([i64, i64, i64, i32, i32, i32, ci], sz),
+        "adaln_attention_bwd": ([vp] * 11 + [i64] * 3 + [i32] * 3 + [i64] * 8 + [f32, ci, vp, sz, ci, vp], ci),
         "adaln_sum_ranks": ([vp, vp, i32, i64, vp], ci),
         "adaln_debug_read": ([vp, ci], ci),
         "adaln_bucket_batch": ([i64, i64, i64, i32], i64),
@@ -311,13 +323,70 @@ def adaln_linear_xent_bwd(x, weight, target, lse, dloss, dlse, dx, dweight, N, V
         N, V, D, ignore_index, _ptr(workspace), workspace_bytes, _dtype(dtype, x), _stream(stream)))
 
 
+def _axes_array(axes):
+    """Host array of the axes' widths: (kept alive by the caller, address, length)."""
+    if axes is None or len(axes) == 0:
+        return None, None, 0
+    arr = (ctypes.c_int32 * len(axes))(*axes)
+    return arr, ctypes.addressof(arr), len(axes)
+
+
+def adaln_qk_norm_rope_fwd(q, k, q_weight, k_weight, pos, q_out, k_out, R, Hq, Hk, d, q_ld, k_ld, q_out_ld,
+                           k_out_ld, axes, theta=10000.0, eps=1e-6, norm=True, dtype=None, stream=None):
+    """axes: the widths of the axes (a sequence, or None with pos None)."""
+    arr, axes_p, naxes = _axes_array(axes)
+    _check("adaln_qk_norm_rope_fwd", lib().adaln_qk_norm_rope_fwd(
+        _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(pos), _ptr(q_out), _ptr(k_out), R, Hq, Hk, d,
+        q_ld, k_ld, q_out_ld, k_out_ld, axes_p, naxes, theta, eps, int(norm),
+        _dtype(dtype, k if q is None else q), _stream(stream)))
+
+
+def adaln_qk_norm_rope_bwd_workspace_size(R, Hq, Hk, d, dtype) -> int:
+    return int(lib().adaln_qk_norm_rope_bwd_workspace_size(R, Hq, Hk, d, int(dtype)))
+
+
+def adaln_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, pos, dq, dk, dq_weight, dk_weight,
+                           workspace, workspace_bytes, R, Hq, Hk, d, dq_out_ld, dk_out_ld, q_ld, k_ld, dq_ld,
+                           dk_ld, axes, theta=10000.0, eps=1e-6, norm=True, dtype=None, stream=None):
+    arr, axes_p, naxes = _axes_array(axes)
+    _check("adaln_qk_norm_rope_bwd", lib().adaln_qk_norm_rope_bwd(
+        _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(pos), _ptr(dq),
+        _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace), workspace_bytes, R, Hq, Hk, d, dq_out_ld,
+        dk_out_ld, q_ld, k_ld, dq_ld, dk_ld, axes_p, naxes, theta, eps, int(norm),
+        _dtype(dtype, dk_out if dq_out is None else dq_out), _stream(stream)))
+
+
+def adaln_attention_fwd_workspace_size(nseg, Rq, Rk, Hq, Hk, d, dtype) -> int:
+    return int(lib().adaln_attention_fwd_workspace_size(nseg, Rq, Rk, Hq, Hk, d, int(dtype)))
+
+
+def adaln_attention_fwd(q, k, v, o, lse, cu_q, cu_k, nseg, Rq, Rk, Hq, Hk, d, q_ld, k_ld, v_ld, o_ld, scale, causal,
+                        workspace, workspace_bytes, dtype=None, stream=None):
+    _check("adaln_attention_fwd", lib().adaln_attention_fwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_q), _ptr(cu_k), nseg, Rq, Rk, Hq, Hk, d, q_ld, k_ld,
+        v_ld, o_ld, scale, int(causal), _ptr(workspace), workspace_bytes, _dtype(dtype, q), _stream(stream)))
+
+
+def adaln_attention_bwd_workspace_size(nseg, Rq, Rk, Hq, Hk, d, dtype) -> int:
+    return int(lib().adaln_attention_bwd_workspace_size(nseg, Rq, Rk, Hq, Hk, d, int(dtype)))
+
+
+def adaln_attention_bwd(dout, q, k, v, o, lse, dq, dk, dv, cu_q, cu_k, nseg, Rq, Rk, Hq, Hk, d, dout_ld, q_ld, k_ld,
+                        v_ld, o_ld, dq_ld, dk_ld, dv_ld, scale, causal, workspace, workspace_bytes, dtype=None,
+                        stream=None):
+    _check("adaln_attention_bwd", lib().adaln_attention_bwd(
+        _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(cu_q),
+        _ptr(cu_k), nseg, Rq, Rk, Hq, Hk, d, dout_ld, q_ld, k_ld, v_ld, o_ld, dq_ld, dk_ld, dv_ld, scale, int(causal),
+        _ptr(workspace), workspace_bytes, _dtype(dtype, q), _stream(stream)))
+
+
 def adaln_sum_ranks(parts, out, world, n, stream=None):
     """out[i] = parts[0][i] + ... + parts[world - 1][i], added in rank order (device fp32)."""
     _check("adaln_sum_ranks", lib().adaln_sum_ranks(_ptr(parts), _ptr(out), world, n, _stream(stream)))
 
 
 DEBUG_CLASSES = {1: "rows", 2: "stats", 4: "mod", 8: "partials", 16: "segments", 32: "shared",
-                 64: "grads", 128: "ranks", 256: "status", 512: "loss"}  # ADALN_DEBUG_* bits
+                 64: "grads", 128: "ranks", 256: "status", 512: "loss", 1024: "heads", 2048: "attn"}  # ADALN_DEBUG_* bits
 
 
 def adaln_debug_read(reset=False) -> int:

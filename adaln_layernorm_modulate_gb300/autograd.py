@@ -17,6 +17,9 @@ through PyTorch's allocator and passes pointers. dshift and dscale come out of t
 library in fp32; autograd wants gradients in the parameters' dtype, so they are rounded
 once to it (a no-op for fp32 parameters).
 
+Between two such nodes: the norms of queries and keys for each head with their rotation by positions
+(``qk_norm_rope``, ``QKNormRope``), and attention over packed or dense sequences (``attention``).
+
 Then the end of such a network: the affine layer norm (``layer_norm``, ``LayerNorm``) and the
 vocabulary loss without its logits (``linear_cross_entropy``).
 """
@@ -28,16 +31,19 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (ADALN_BF16, ADALN_F32, AdalnError, adaln_bwd, adaln_bwd_recompute,
+from . import (ADALN_BF16, ADALN_F32, AdalnError, adaln_attention_bwd, adaln_attention_bwd_workspace_size,
+               adaln_attention_fwd, adaln_attention_fwd_workspace_size, adaln_bwd, adaln_bwd_recompute,
                adaln_bwd_recompute_workspace_size, adaln_bwd_varlen, adaln_bwd_varlen_recompute,
                adaln_bwd_varlen_recompute_workspace_size, adaln_bwd_varlen_workspace_size,
                adaln_bwd_workspace_size, adaln_fwd, adaln_fwd_varlen, adaln_fwd_varlen_workspace_size,
                adaln_layernorm_bwd, adaln_layernorm_bwd_workspace_size, adaln_layernorm_fwd,
                adaln_linear_xent_bwd, adaln_linear_xent_bwd_workspace_size, adaln_linear_xent_fwd,
-               adaln_linear_xent_fwd_workspace_size, adaln_read_status)
+               adaln_linear_xent_fwd_workspace_size, adaln_qk_norm_rope_bwd,
+               adaln_qk_norm_rope_bwd_workspace_size, adaln_qk_norm_rope_fwd, adaln_read_status)
 
 __all__ = ["AdaLNModulateFunction", "AdaLNModulate", "adaln_modulate", "LayerNormFunction", "LayerNorm",
-           "layer_norm", "LinearCrossEntropyFunction", "linear_cross_entropy"]
+           "layer_norm", "LinearCrossEntropyFunction", "linear_cross_entropy", "QKNormRopeFunction",
+           "QKNormRope", "qk_norm_rope", "AttentionFunction", "attention"]
 
 
 def _code(t: torch.Tensor) -> int:
@@ -348,3 +354,195 @@ def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Te
     if 0 <= ignore_index < V:
         counts = counts & (target != ignore_index)
     return total / counts.sum().clamp(min=1)
+
+
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """t [R, H, d] with heads side by side in rows the library takes, copied only if they are not:
+    parts of a joint projection's rows go as they are."""
+    R, H, d = t.shape
+    if ((d <= 1 or t.stride(2) == 1) and (H <= 1 or t.stride(1) == d) and t.data_ptr() % 16 == 0
+            and (R <= 1 or (t.stride(0) >= H * d and t.stride(0) % 8 == 0))):
+        return t
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
+def _ld(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+class QKNormRopeFunction(torch.autograd.Function):
+    """(q', k') of q [..., Hq, d] and k [..., Hk, d] (the same leading sizes): an RMS norm of each head
+    with the weights [d], then the rotation by positions [..., axes]. Saves q, k (as they come: parts of
+    a projection's rows are not copied), the weights and positions."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, axes, theta: float, eps: float, norm: bool):
+        if not q.is_cuda:
+            raise ValueError("qk_norm_rope runs on CUDA tensors")
+        if q.dim() < 2 or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+            raise ValueError("qk_norm_rope: q [..., Hq, d] and k [..., Hk, d] with the same leading sizes")
+        Hq, Hk, d = q.shape[-2], k.shape[-2], q.shape[-1]
+        for w in (q_weight, k_weight):
+            if w is not None and w.shape != (d,):
+                raise ValueError("qk_norm_rope: weights are [d]")
+            if w is not None and not norm:
+                raise ValueError("qk_norm_rope: weights go with the norm")
+        if any(t is not None and t.device != q.device for t in (k, q_weight, k_weight, positions)):
+            raise ValueError("q, k, weights and positions must be on one device")
+        if any(t is not None and t.dtype != q.dtype for t in (k, q_weight, k_weight)):
+            raise TypeError("q, k and the weights must share one dtype")
+        dt = _code(q)
+        axes = tuple(int(w) for w in axes) if axes is not None else ()
+        if positions is not None:
+            if positions.dtype.is_floating_point or positions.dtype.is_complex or positions.dtype == torch.bool:
+                raise TypeError("qk_norm_rope: positions are whole numbers")
+            if positions.shape != q.shape[:-2] + (len(axes),) or not axes:
+                raise ValueError("qk_norm_rope: positions [..., axes], one width of `axes` each")
+            positions = positions.to(torch.int32).contiguous()
+        lead = q.shape[:-2]
+        qr, kr = _rows(q.reshape(-1, Hq, d)), _rows(k.reshape(-1, Hk, d))
+        R = qr.shape[0]
+        q_weight = None if q_weight is None else q_weight.contiguous()
+        k_weight = None if k_weight is None else k_weight.contiguous()
+        qo = torch.empty((R, Hq, d), dtype=q.dtype, device=q.device)
+        ko = torch.empty((R, Hk, d), dtype=q.dtype, device=q.device)
+        with _on(q):
+            adaln_qk_norm_rope_fwd(qr, kr, q_weight, k_weight, positions, qo, ko, R, Hq, Hk, d, _ld(qr), _ld(kr),
+                                   Hq * d, Hk * d, axes, theta, eps, norm, dt)
+        ctx.save_for_backward(*((qr, kr) if norm else (qo[:0], ko[:0])), q_weight, k_weight, positions)
+        ctx.sizes = lead, R, Hq, Hk, d
+        ctx.args = axes, theta, eps, norm
+        return qo.view(*lead, Hq, d), ko.view(*lead, Hk, d)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dqo, dko):
+        q, k, q_weight, k_weight, positions = ctx.saved_tensors
+        lead, R, Hq, Hk, d = ctx.sizes
+        axes, theta, eps, norm = ctx.args
+        dt = _code(dqo)
+        dqo, dko = _rows(dqo.reshape(R, Hq, d)), _rows(dko.reshape(R, Hk, d))
+        dq = torch.empty((R, Hq, d), dtype=dqo.dtype, device=dqo.device)
+        dk = torch.empty((R, Hk, d), dtype=dqo.dtype, device=dqo.device)
+        dwq, dwk = (torch.empty(d, dtype=torch.float32, device=dqo.device) if w is not None and need else None
+                    for w, need in ((q_weight, ctx.needs_input_grad[2]), (k_weight, ctx.needs_input_grad[3])))
+        with _on(dqo):
+            nb = adaln_qk_norm_rope_bwd_workspace_size(R, Hq, Hk, d, dt)
+            ws = _workspace(nb, dqo.device)
+            adaln_qk_norm_rope_bwd(dqo, dko, q if norm else None, k if norm else None, q_weight, k_weight, positions,
+                                   dq, dk, dwq, dwk, ws, nb, R, Hq, Hk, d, _ld(dqo), _ld(dko), _ld(q) if norm else 0,
+                                   _ld(k) if norm else 0, Hq * d, Hk * d, axes, theta, eps, norm, dt)
+        return (dq.view(*lead, Hq, d), dk.view(*lead, Hk, d), None if dwq is None else dwq.to(dq.dtype),
+                None if dwk is None else dwk.to(dq.dtype), None, None, None, None, None)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Tensor] = None, axes=None,
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                 theta: float = 10000.0, eps: float = 1e-6, norm: bool = True):
+    """Differentiable norms of each head of q [..., Hq, d] and k [..., Hk, d] and their rotation by
+    positions [..., len(axes)] (whole numbers): pairs of neighbouring elements turn, the first axes[0]
+    elements with the first position, and so on; elements behind the axes do not turn. Returns (q', k').
+    norm=False: the rotation alone; positions=None: the norms alone."""
+    return QKNormRopeFunction.apply(q, k, q_weight, k_weight, positions, axes, float(theta), float(eps), bool(norm))
+
+
+class QKNormRope(torch.nn.Module):
+    """``QKNormRope(d, axes)(q, k, positions)``: head norms with learned weights (ones), and the
+    rotation."""
+
+    def __init__(self, d: int, axes=None, theta: float = 10000.0, eps: float = 1e-6, device=None, dtype=None):
+        super().__init__()
+        self.axes = None if axes is None else tuple(int(w) for w in axes)
+        self.theta, self.eps, self.d = float(theta), float(eps), int(d)
+        self.q_weight = torch.nn.Parameter(torch.ones(d, device=device, dtype=dtype))
+        self.k_weight = torch.nn.Parameter(torch.ones(d, device=device, dtype=dtype))
+
+    def forward(self, q, k, positions=None):
+        axes = self.axes if positions is not None else None
+        return qk_norm_rope(q, k, positions, axes, self.q_weight, self.k_weight, self.theta, self.eps)
+
+    def extra_repr(self) -> str:
+        return "%d, axes=%s, theta=%g, eps=%g" % (self.d, self.axes, self.theta, self.eps)
+
+
+class AttentionFunction(torch.autograd.Function):
+    """(o, lse) of packed q [Rq, Hq, d], k and v [Rk, Hk, d] (see ``attention``). lse [Hq, Rq] fp32 carries no
+    gradient. Saves q, k, v (as they come), o and lse, no scores."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, cu_q, cu_k, nseg: int, causal: bool, scale: float, check_tables: bool):
+        (Rq, Hq, d), (Rk, Hk, _) = q.shape, k.shape
+        q, k, v = _rows(q), _rows(k), _rows(v)
+        o = torch.empty((Rq, Hq, d), dtype=q.dtype, device=q.device)
+        lse = torch.empty((Hq, Rq), dtype=torch.float32, device=q.device)
+        with _on(q):
+            nb = adaln_attention_fwd_workspace_size(nseg, Rq, Rk, Hq, Hk, d, ADALN_BF16)
+            ws = _workspace(nb, q.device)
+            adaln_attention_fwd(q, k, v, o, lse, cu_q, cu_k, nseg, Rq, Rk, Hq, Hk, d, _ld(q), _ld(k), _ld(v), Hq * d,
+                                scale, causal, ws, nb, ADALN_BF16)
+            if check_tables:
+                _check_status(ws, "adaln_attention_fwd")
+        ctx.save_for_backward(q, k, v, o, lse, cu_q, cu_k)
+        ctx.args = nseg, causal, scale, check_tables
+        ctx.mark_non_differentiable(lse)
+        return o, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout, _dlse):
+        q, k, v, o, lse, cu_q, cu_k = ctx.saved_tensors
+        nseg, causal, scale, check_tables = ctx.args
+        (Rq, Hq, d), (Rk, Hk, _) = q.shape, k.shape
+        dout = _rows(dout)
+        want_q, want_kv = ctx.needs_input_grad[0], ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
+        dq = torch.empty((Rq, Hq, d), dtype=q.dtype, device=q.device) if want_q else None
+        dk, dv = (torch.empty((Rk, Hk, d), dtype=q.dtype, device=q.device) if want_kv else None for _ in range(2))
+        with _on(q):
+            nb = adaln_attention_bwd_workspace_size(nseg, Rq, Rk, Hq, Hk, d, ADALN_BF16)
+            ws = _workspace(nb, q.device)
+            adaln_attention_bwd(dout, q, k, v, o, lse, dq, dk, dv, cu_q, cu_k, nseg, Rq, Rk, Hq, Hk, d, _ld(dout),
+                                _ld(q), _ld(k), _ld(v), Hq * d, Hq * d, Hk * d, Hk * d, scale, causal, ws, nb,
+                                ADALN_BF16)
+            if check_tables:
+                _check_status(ws, "adaln_attention_bwd")
+        return dq, dk, dv, None, None, None, None, None, None
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+              cu_seqlens_k: Optional[torch.Tensor] = None, causal: bool = False, scale: Optional[float] = None,
+              check_tables: bool = False, return_lse: bool = False):
+    """Differentiable softmax attention (bfloat16).
+
+    Packed: q [Rq, Hq, d], k and v [Rk, Hk, d] with cu_seqlens [nseg + 1] of the queries and cu_seqlens_k
+    of the keys (the queries' if absent). Dense: q [B, N, Hq, d], k and v [B, M, Hk, d], no tables. Hq is a
+    multiple of Hk, d a multiple of 8 up to 128. causal: query i of n sees keys j <= i + m - n. scale:
+    d ** -0.5 if None. Returns o like q; with return_lse also lse, [Hq, Rq] or [Hq, B, N], which carries no
+    gradient. ``check_tables`` reads the call's device status (it synchronises the stream)."""
+    if not q.is_cuda:
+        raise ValueError("attention runs on CUDA tensors")
+    if any(t.dtype != torch.bfloat16 for t in (q, k, v)):
+        raise TypeError("attention takes bfloat16 q, k and v, got %s, %s and %s" % (q.dtype, k.dtype, v.dtype))
+    packed = cu_seqlens is not None
+    n = 3 if packed else 4
+    if q.dim() != n or k.dim() != n or v.shape != k.shape or k.shape[-1] != q.shape[-1] or (
+            not packed and k.shape[0] != q.shape[0]):
+        raise ValueError("attention: packed q [Rq, Hq, d], k and v [Rk, Hk, d] with cu_seqlens, or dense "
+                         "q [B, N, Hq, d], k and v [B, M, Hk, d]")
+    if any(t is not None and t.device != q.device for t in (k, v, cu_seqlens, cu_seqlens_k)):
+        raise ValueError("q, k, v and the tables must be on one device")
+    scale = q.shape[-1] ** -0.5 if scale is None else float(scale)
+    if packed:
+        cu_seqlens_k = cu_seqlens if cu_seqlens_k is None else cu_seqlens_k
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape != cu_seqlens_k.shape or cu_seqlens.numel() == 0:
+            raise ValueError("attention: cu_seqlens and cu_seqlens_k are [nseg + 1]")
+        cu_q, cu_k = (c.to(torch.int32).contiguous() for c in (cu_seqlens, cu_seqlens_k))
+        o, lse = AttentionFunction.apply(q, k, v, cu_q, cu_k, cu_q.numel() - 1, bool(causal), scale, check_tables)
+        return (o, lse) if return_lse else o
+    if cu_seqlens_k is not None:
+        raise ValueError("attention: cu_seqlens_k goes with cu_seqlens")
+    B, N = q.shape[:2]
+    o, lse = AttentionFunction.apply(q.flatten(0, 1), k.flatten(0, 1), v.flatten(0, 1), None, None, B, bool(causal),
+                                     scale, check_tables)
+    o = o.view(B, N, *o.shape[1:])
+    return (o, lse.view(-1, B, N)) if return_lse else o

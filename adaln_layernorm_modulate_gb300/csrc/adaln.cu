@@ -10,7 +10,9 @@
 #include <tuple>
 #include <vector>
 
+#include "attn.h"
 #include "launch.h"
+#include "rope.h"
 #include "xent.h"
 
 using namespace adaln;
@@ -834,11 +836,12 @@ extern "C" int adaln_debug_read(uint32_t* word, int reset) {
 #ifdef ADALN_DEBUG
     if (word == nullptr) return ADALN_ERR_INVALID_ARG;
     if (cudaDeviceSynchronize() != cudaSuccess) return ADALN_ERR_CUDA;
-    uint32_t f = 0, b = 0, x = 0;
+    uint32_t f = 0, b = 0, x = 0, r = 0, t = 0;
     if (debug_word_fwd(&f, reset != 0) != cudaSuccess || debug_word_bwd(&b, reset != 0) != cudaSuccess ||
-        debug_word_xent(&x, reset != 0) != cudaSuccess)
+        debug_word_xent(&x, reset != 0) != cudaSuccess || debug_word_rope(&r, reset != 0) != cudaSuccess ||
+        debug_word_attn(&t, reset != 0) != cudaSuccess)
         return ADALN_ERR_CUDA;
-    *word = f | b | x;
+    *word = f | b | x | r | t;
     return ADALN_OK;
 #else
     (void)word;
@@ -1182,6 +1185,395 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
         if (int rc = launched(launch_lists(d, sms, stream))) return rc;
     }
     return launched(launch_finish(d, sms, stream));
+}
+
+}  // extern "C"
+
+// ---- Head norms with rotation by positions ---------------------------------------------------
+
+namespace {
+
+// Resident CTAs of the kernel on the current device (cached), or 0 on failure.
+int rope_resident(int dtype, int d, bool bwd, int dev, int sms) {
+    static int cached[kMaxDevices][2][2][6];
+    int lanes = 0;
+    while ((1 << lanes) < rope_lanes(d)) ++lanes;
+    int bps = 0;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        bps = cached[dev][dtype][bwd][lanes];
+    }
+    if (bps == 0) {
+        if (rope_blocks_per_sm(dtype, d, bwd, &bps) != cudaSuccess || bps <= 0) return 0;
+        std::lock_guard<std::mutex> lock(g_mu);
+        cached[dev][dtype][bwd][lanes] = bps;
+    }
+    return std::min(bps * sms, kMaxCtas);
+}
+
+int rope_check(int64_t R, int32_t Hq, int32_t Hk, int32_t d, adaln_dtype dtype) {
+    if (dtype != ADALN_F32 && dtype != ADALN_BF16) return ADALN_ERR_INVALID_ARG;
+    if (d < 8 || d > kRopeMaxD || d % 8 != 0) return ADALN_ERR_UNSUPPORTED;
+    if (R < 0 || Hq < 0 || Hk < 0 || Hq > 16384 || Hk > 16384) return ADALN_ERR_INVALID_ARG;
+    return ADALN_OK;
+}
+
+// Rows of `heads` heads: ld apart, not overlapping, all of them addressable, on 16-byte boundaries.
+int check_rows(const void* p, int64_t R, int32_t heads, int32_t d, int64_t ld) {
+    if (!p) return ADALN_ERR_INVALID_ARG;
+    if (!aligned(p, 16)) return ADALN_ERR_ALIGNMENT;
+    if (ld % 8 != 0) return ADALN_ERR_ALIGNMENT;
+    if (ld < (int64_t)heads * d || !rows_fit(R, ld)) return ADALN_ERR_INVALID_ARG;
+    return ADALN_OK;
+}
+
+// The pairs' axes and frequencies: theta^(-2i / w) / (2 pi) turns a step, as fractions of 2^64.
+int rope_axes(const int32_t* axes, int32_t naxes, double theta, int32_t d, const int32_t* pos, RopeArgs* a) {
+    a->pos = pos;
+    a->naxes = naxes;
+    if (!pos) return naxes == 0 || axes ? ADALN_OK : ADALN_ERR_INVALID_ARG;
+    if (!aligned(pos, 4)) return ADALN_ERR_ALIGNMENT;
+    if (!axes || naxes < 1 || naxes > kRopeMaxAxes || !(theta >= 1.0) || !std::isfinite(theta))
+        return ADALN_ERR_INVALID_ARG;
+    int64_t pair = 0;
+    for (int32_t x = 0; x < naxes; ++x) {
+        if (axes[x] < 0 || axes[x] % 2 != 0 || 2 * pair + axes[x] > d) return ADALN_ERR_INVALID_ARG;
+        for (int32_t i = 0; i < axes[x] / 2; ++i, ++pair) {
+            const double turns = std::pow(theta, -2.0 * i / axes[x]) / 6.283185307179586476925;
+            a->freq[pair] = (unsigned long long)std::ldexp(turns, 64);  // turns < 1/6
+            a->axis[pair] = (unsigned char)x;
+        }
+    }
+    return ADALN_OK;
+}
+
+// Work items: a token's heads in as few chunks as give every resident group of lanes one.
+void rope_items(RopeArgs* a, bool bwd, int64_t resident, int64_t* G) {
+    const int64_t heads = a->side[0].heads + a->side[1].heads, at_once = bwd ? 2 : 4;
+    const int64_t groups = kRopeThreads / rope_lanes(a->d), slots = resident * groups;
+    const int64_t want = std::max<int64_t>(1, std::min((heads + at_once - 1) / at_once, (slots + a->R - 1) / a->R));
+    a->chunk = (int)(((heads + want - 1) / want + at_once - 1) / at_once * at_once);
+    a->chunks = (int)((heads + a->chunk - 1) / a->chunk);
+    *G = std::min(resident, (a->R * a->chunks + groups - 1) / groups);
+}
+
+}  // namespace
+
+extern "C" {
+
+int adaln_qk_norm_rope_fwd(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                           const int32_t* pos, void* q_out, void* k_out, int64_t R, int32_t Hq, int32_t Hk,
+                           int32_t d, int64_t q_ld, int64_t k_ld, int64_t q_out_ld, int64_t k_out_ld,
+                           const int32_t* axes, int32_t naxes, double theta, float eps, int norm,
+                           adaln_dtype dtype, cudaStream_t stream) {
+    if (int rc = rope_check(R, Hq, Hk, d, dtype)) return rc;
+    if (norm ? !(eps > 0.0f) || !std::isfinite(eps) : q_weight || k_weight) return ADALN_ERR_INVALID_ARG;
+    if (!aligned(q_weight, 16) || !aligned(k_weight, 16)) return ADALN_ERR_ALIGNMENT;
+    RopeArgs a{};
+    if (int rc = rope_axes(axes, naxes, theta, d, pos, &a)) return rc;
+    if (R == 0 || Hq + Hk == 0) return ADALN_OK;
+    if (Hq > 0) {
+        if (int rc = check_rows(q, R, Hq, d, q_ld)) return rc;
+        if (int rc = check_rows(q_out, R, Hq, d, q_out_ld)) return rc;
+    }
+    if (Hk > 0) {
+        if (int rc = check_rows(k, R, Hk, d, k_ld)) return rc;
+        if (int rc = check_rows(k_out, R, Hk, d, k_out_ld)) return rc;
+    }
+    int dev = 0;
+    const int sms = current_sms(&dev);
+    if (sms <= 0) return ADALN_ERR_CUDA;
+    const int resident = rope_resident((int)dtype, d, false, dev, sms);
+    if (resident <= 0) return ADALN_ERR_CUDA;
+    a.side[0] = RopeSide{q, nullptr, q_weight, q_out, q_ld, 0, q_out_ld, Hq};
+    a.side[1] = RopeSide{k, nullptr, k_weight, k_out, k_ld, 0, k_out_ld, Hk};
+    a.R = R;
+    a.d = d;
+    a.norm = norm != 0;
+    a.eps = eps;
+    int64_t G = 0;
+    rope_items(&a, false, resident, &G);
+    return launched(launch_rope(a, (int)dtype, false, G, stream));
+}
+
+size_t adaln_qk_norm_rope_bwd_workspace_size(int64_t R, int32_t Hq, int32_t Hk, int32_t d, adaln_dtype dtype) {
+    if (rope_check(R, Hq, Hk, d, dtype)) return 0;
+    int dev = 0;
+    const int sms = current_sms(&dev);
+    const int resident = sms > 0 ? rope_resident((int)dtype, d, true, dev, sms) : 0;
+    return resident <= 0 ? 0 : kPartialsOffset + (size_t)resident * 2 * (size_t)d * sizeof(float);
+}
+
+int adaln_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                           const void* q_weight, const void* k_weight, const int32_t* pos, void* dq, void* dk,
+                           float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes, int64_t R,
+                           int32_t Hq, int32_t Hk, int32_t d, int64_t dq_out_ld, int64_t dk_out_ld, int64_t q_ld,
+                           int64_t k_ld, int64_t dq_ld, int64_t dk_ld, const int32_t* axes, int32_t naxes,
+                           double theta, float eps, int norm, adaln_dtype dtype, cudaStream_t stream) {
+    if (int rc = rope_check(R, Hq, Hk, d, dtype)) return rc;
+    if (norm ? !(eps > 0.0f) || !std::isfinite(eps) : q_weight || k_weight || dq_weight || dk_weight)
+        return ADALN_ERR_INVALID_ARG;
+    if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(dq_weight, 4) || !aligned(dk_weight, 4))
+        return ADALN_ERR_ALIGNMENT;
+    RopeArgs a{};
+    if (int rc = rope_axes(axes, naxes, theta, d, pos, &a)) return rc;
+    if (R > 0 && Hq > 0) {
+        if (int rc = check_rows(dq_out, R, Hq, d, dq_out_ld)) return rc;
+        if (int rc = check_rows(dq, R, Hq, d, dq_ld)) return rc;
+        if (int rc = norm ? check_rows(q, R, Hq, d, q_ld) : ADALN_OK) return rc;
+    }
+    if (R > 0 && Hk > 0) {
+        if (int rc = check_rows(dk_out, R, Hk, d, dk_out_ld)) return rc;
+        if (int rc = check_rows(dk, R, Hk, d, dk_ld)) return rc;
+        if (int rc = norm ? check_rows(k, R, Hk, d, k_ld) : ADALN_OK) return rc;
+    }
+    int dev = 0;
+    const int sms = current_sms(&dev);
+    if (sms <= 0) return ADALN_ERR_CUDA;
+    const int resident = rope_resident((int)dtype, d, true, dev, sms);
+    if (resident <= 0) return ADALN_ERR_CUDA;
+    if (int rc = check_workspace(workspace, workspace_bytes,
+                                 kPartialsOffset + (size_t)resident * 2 * (size_t)d * sizeof(float)))
+        return rc;
+    // Without rows or heads one CTA still leaves the status and zero sums.
+    const bool none = R == 0 || Hq + Hk == 0;
+    a.side[0] = RopeSide{q, dq_out, q_weight, dq, q_ld, dq_out_ld, dq_ld, Hq};
+    a.side[1] = RopeSide{k, dk_out, k_weight, dk, k_ld, dk_out_ld, dk_ld, Hk};
+    a.R = none ? 0 : R;
+    a.d = d;
+    a.norm = norm != 0;
+    a.eps = eps;
+    a.chunk = a.chunks = 1;
+    a.status = at<uint32_t>(workspace, kHeaderBytes);
+    a.header = at<WsHeader>(workspace, 0);
+    const bool sums = dq_weight || dk_weight;
+    a.partials = sums ? at<float>(workspace, kPartialsOffset) : nullptr;
+    int64_t G = 1;
+    if (!none) rope_items(&a, true, resident, &G);
+    if (int rc = launched(launch_rope(a, (int)dtype, true, G, stream))) return rc;
+    if (!sums) return ADALN_OK;
+    RopeReduceArgs r{};
+    r.partials = a.partials;
+    r.dw[0] = dq_weight;
+    r.dw[1] = dk_weight;
+    r.G = G;
+    r.d = d;
+    return launched(launch_rope_reduce(r, stream));
+}
+
+}  // extern "C"
+
+// ---- Attention over packed sequences ----------------------------------------------------------
+
+namespace {
+
+constexpr int kAttnMaxSplits = 64;
+
+int attn_check(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d, adaln_dtype dtype) {
+    if (dtype != ADALN_F32 && dtype != ADALN_BF16) return ADALN_ERR_INVALID_ARG;
+    if (d < 8 || d > kAttnMaxD || d % 8 != 0 || dtype != ADALN_BF16) return ADALN_ERR_UNSUPPORTED;
+    if (nseg < 0 || Rq < 0 || Rk < 0 || nseg > kAttnMaxRows || Rq > kAttnMaxRows || Rk > kAttnMaxRows)
+        return ADALN_ERR_INVALID_ARG;
+    if (Hq < 1 || Hk < 1 || Hq > 16384 || Hq % Hk != 0) return ADALN_ERR_INVALID_ARG;
+    return ADALN_OK;
+}
+
+// The call's sequences: tables, or segments of equal lengths.
+int attn_tables(const int32_t* cu_q, const int32_t* cu_k, int64_t nseg, int64_t Rq, int64_t Rk, int causal,
+                AttnTables* t) {
+    if (!aligned(cu_q, 4) || !aligned(cu_k, 4)) return ADALN_ERR_ALIGNMENT;
+    if (nseg == 0 ? Rq != 0 || Rk != 0 : (!cu_q && Rq % nseg != 0) || (!cu_k && Rk % nseg != 0))
+        return ADALN_ERR_INVALID_ARG;
+    *t = AttnTables{cu_q, cu_k, nseg, Rq, Rk, causal != 0};
+    return ADALN_OK;
+}
+
+struct AttnPlan {
+    int tile;                 // forward: queries a work item
+    int64_t most_q, most_k;   // work items
+    int splits;               // forward: parts of the keys
+    size_t count, items_q, items_k, part, ml, lse2, delta, bytes;
+};
+
+AttnPlan attn_plan(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t d, bool bwd, int sms) {
+    AttnPlan p{};
+    auto items = [&](int64_t R, int tile) { return R / tile + std::min(nseg, R); };
+    p.tile = 2 * kAttnTile;
+    if (bwd || items(Rq, p.tile) * Hq < sms) p.tile = kAttnTile;
+    p.most_q = items(Rq, p.tile);
+    p.most_k = items(Rk, kAttnTile);
+    p.splits = 1;
+    const int64_t units = p.most_q * Hq;
+    if (!bwd && units > 0 && 2 * units <= sms)
+        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({sms / units, Rk / (4 * kAttnTile), kAttnMaxSplits}));
+    size_t at = kPartialsOffset;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at = (at + bytes + 255) / 256 * 256;
+        return o;
+    };
+    p.count = take(2 * sizeof(int32_t));
+    p.items_q = take((size_t)items(Rq, kAttnTile) * sizeof(AttnItem));
+    if (bwd) {
+        p.items_k = take((size_t)p.most_k * sizeof(AttnItem));
+        p.lse2 = take((size_t)Rq * Hq * sizeof(float));
+        p.delta = take((size_t)Rq * Hq * sizeof(float));
+    } else {
+        // With splits a row has most_q * Hq * splits <= sms units, each of at most a tile of rows; the bound
+        // holds for calls of fewer rows too.
+        const size_t rows = (size_t)sms * (size_t)std::min<int64_t>(kAttnTile, Rq);
+        p.part = take(rows * (size_t)d * sizeof(float));
+        p.ml = take(rows * sizeof(float2));
+    }
+    p.bytes = at;
+    return p;
+}
+
+AttnPlanArgs attn_plan_args(const AttnTables& t, const AttnPlan& p, void* ws, bool bwd) {
+    AttnPlanArgs a{};
+    a.t = t;
+    a.items[0] = at<AttnItem>(ws, p.items_q);
+    a.items[1] = bwd ? at<AttnItem>(ws, p.items_k) : nullptr;
+    a.count = at<int32_t>(ws, p.count);
+    a.most[0] = p.most_q;
+    a.most[1] = p.most_k;
+    a.tile[0] = p.tile;
+    a.tile[1] = kAttnTile;
+    a.status = at<uint32_t>(ws, kHeaderBytes);
+    a.header = at<WsHeader>(ws, 0);
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t adaln_attention_fwd_workspace_size(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d,
+                                          adaln_dtype dtype) {
+    int dev = 0;
+    if (attn_check(nseg, Rq, Rk, Hq, Hk, d, dtype)) return 0;
+    const int sms = current_sms(&dev);
+    return sms <= 0 ? 0 : attn_plan(nseg, Rq, Rk, Hq, d, false, sms).bytes;
+}
+
+int adaln_attention_fwd(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_q,
+                        const int32_t* cu_k, int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d,
+                        int64_t q_ld, int64_t k_ld, int64_t v_ld, int64_t o_ld, float scale, int causal,
+                        void* workspace, size_t workspace_bytes, adaln_dtype dtype, cudaStream_t stream) {
+    if (int rc = attn_check(nseg, Rq, Rk, Hq, Hk, d, dtype)) return rc;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return ADALN_ERR_INVALID_ARG;
+    AttnTables t;
+    if (int rc = attn_tables(cu_q, cu_k, nseg, Rq, Rk, causal, &t)) return rc;
+    if (Rq > 0) {
+        if (int rc = check_rows(q, Rq, Hq, d, q_ld)) return rc;
+        if (int rc = check_rows(o, Rq, Hq, d, o_ld)) return rc;
+        if (int rc = check_io({}, {lse})) return rc;
+    }
+    if (Rk > 0) {
+        if (int rc = check_rows(k, Rk, Hk, d, k_ld)) return rc;
+        if (int rc = check_rows(v, Rk, Hk, d, v_ld)) return rc;
+    }
+    int dev = 0;
+    const int sms = current_sms(&dev);
+    if (sms <= 0) return ADALN_ERR_CUDA;
+    const AttnPlan p = attn_plan(nseg, Rq, Rk, Hq, d, false, sms);
+    if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
+    const AttnPlanArgs l = attn_plan_args(t, p, workspace, false);
+    if (int rc = launched(launch_attn_plan(l, stream))) return rc;
+    if (Rq == 0) return ADALN_OK;
+    AttnFwdArgs a{};
+    a.items = l.items[0];
+    a.count = l.count;
+    a.o = o;
+    a.lse = lse;
+    a.part = at<float>(workspace, p.part);
+    a.ml = at<float2>(workspace, p.ml);
+    a.status = l.status + 1;
+    a.Rq = Rq;
+    a.o_ld = o_ld;
+    a.most = p.most_q;
+    a.Hq = Hq;
+    a.group = Hq / Hk;
+    a.d = d;
+    a.splits = p.splits;
+    a.scale = scale;
+    if (int rc = launched(launch_attn_fwd(a, {q, Rq, q_ld, Hq}, {k, Rk, k_ld, Hk}, {v, Rk, v_ld, Hk}, sms, stream)))
+        return rc;
+    if (p.splits == 1) return ADALN_OK;
+    const AttnJoinArgs j{a.part, a.ml, o, lse, Rq, o_ld, Hq, d, p.splits, scale, l.status};
+    return launched(launch_attn_join(j, sms, stream));
+}
+
+size_t adaln_attention_bwd_workspace_size(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d,
+                                          adaln_dtype dtype) {
+    int dev = 0;
+    if (attn_check(nseg, Rq, Rk, Hq, Hk, d, dtype)) return 0;
+    const int sms = current_sms(&dev);
+    return sms <= 0 ? 0 : attn_plan(nseg, Rq, Rk, Hq, d, true, sms).bytes;
+}
+
+int adaln_attention_bwd(const void* dout, const void* q, const void* k, const void* v, const void* o, const float* lse,
+                        void* dq, void* dk, void* dv, const int32_t* cu_q, const int32_t* cu_k, int64_t nseg,
+                        int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d, int64_t dout_ld, int64_t q_ld,
+                        int64_t k_ld, int64_t v_ld, int64_t o_ld, int64_t dq_ld, int64_t dk_ld, int64_t dv_ld,
+                        float scale, int causal, void* workspace, size_t workspace_bytes, adaln_dtype dtype,
+                        cudaStream_t stream) {
+    if (int rc = attn_check(nseg, Rq, Rk, Hq, Hk, d, dtype)) return rc;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return ADALN_ERR_INVALID_ARG;
+    AttnTables t;
+    if (int rc = attn_tables(cu_q, cu_k, nseg, Rq, Rk, causal, &t)) return rc;
+    if ((dk != nullptr) != (dv != nullptr) || (!dq && !dk && Rq + Rk > 0)) return ADALN_ERR_INVALID_ARG;
+    if (Rq > 0) {
+        if (int rc = check_rows(dout, Rq, Hq, d, dout_ld)) return rc;
+        if (int rc = check_rows(q, Rq, Hq, d, q_ld)) return rc;
+        if (int rc = check_rows(o, Rq, Hq, d, o_ld)) return rc;
+        if (int rc = check_io({}, {lse})) return rc;
+        if (int rc = dq ? check_rows(dq, Rq, Hq, d, dq_ld) : ADALN_OK) return rc;
+    }
+    if (Rk > 0) {
+        if (int rc = check_rows(k, Rk, Hk, d, k_ld)) return rc;
+        if (int rc = check_rows(v, Rk, Hk, d, v_ld)) return rc;
+        if (int rc = dk ? check_rows(dk, Rk, Hk, d, dk_ld) : ADALN_OK) return rc;
+        if (int rc = dv ? check_rows(dv, Rk, Hk, d, dv_ld) : ADALN_OK) return rc;
+    }
+    int dev = 0;
+    const int sms = current_sms(&dev);
+    if (sms <= 0) return ADALN_ERR_CUDA;
+    const AttnPlan p = attn_plan(nseg, Rq, Rk, Hq, d, true, sms);
+    if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
+    const AttnPlanArgs l = attn_plan_args(t, p, workspace, true);
+    if (int rc = launched(launch_attn_plan(l, stream))) return rc;
+    const AttnDeltaArgs e{dout, o, lse, at<float>(workspace, p.delta), at<float>(workspace, p.lse2), Rq, dout_ld, o_ld, Hq, d};
+    if (int rc = Rq > 0 ? launched(launch_attn_delta(e, sms, stream)) : ADALN_OK) return rc;
+    const AttnRows rdo{dout, Rq, dout_ld, Hq}, rq{q, Rq, q_ld, Hq}, rk{k, Rk, k_ld, Hk}, rv{v, Rk, v_ld, Hk};
+    AttnBwdArgs a{};
+    a.delta = e.delta;
+    a.lse2 = e.lse2;
+    a.status = l.status + 1;
+    a.Rq = Rq;
+    a.Hq = Hq;
+    a.group = Hq / Hk;
+    a.d = d;
+    a.scale = scale;
+    if (dk && Rk > 0) {
+        a.items = l.items[1];
+        a.count = l.count + 1;
+        a.dx = dk;
+        a.dv = dv;
+        a.dx_ld = dk_ld;
+        a.dv_ld = dv_ld;
+        a.most = p.most_k;
+        if (int rc = launched(launch_attn_dkv(a, rdo, rq, rk, rv, sms, stream))) return rc;
+    }
+    if (dq && Rq > 0) {
+        a.items = l.items[0];
+        a.count = l.count;
+        a.dx = dq;
+        a.dx_ld = dq_ld;
+        a.most = p.most_q;
+        if (int rc = launched(launch_attn_dq(a, rdo, rq, rk, rv, sms, stream))) return rc;
+    }
+    return ADALN_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,1338 @@
+// Softmax attention over packed sequences, with its gradient; the scores are never kept.
+//
+//     z = scale q k^T (masked),  lse = log sum_j exp(z_j),  p = exp(z - lse),  o = p v
+//     dv = p^T dout,  dp = dout v^T,  dz = p (dp - delta),  delta = dout . o
+//     dq = scale dz k,  dk = scale dz^T q
+//
+// A plan kernel lists the tiles of rows of all segments, the ones that meet most first; persistent
+// CTAs walk the list, a head at a time. Every product is a tcgen05.mma of 128 rows with its
+// accumulator in tensor memory, its operands brought by TMA; p and dz (bf16, the products' types) are
+// written back to tensor memory over the scores that they come from and are operands from there, so that
+// they never pass through shared memory.
+//
+//   attn_fwd_kernel: two tiles of 128 queries share the keys and values in shared memory; a
+//       warpgroup each has a thread a row, so that the softmax needs no exchange between threads. The
+//       two alternate: while one computes exponentials, the tensor cores run the other's products.
+//   attn_dq_kernel: a tile of 128 queries over its keys: z, dp, dq += dz k.
+//   attn_dkv_kernel: a tile of 128 keys over its queries, transposed: z^T, dp^T, dv += p^T dout,
+//       dk += dz^T q, over all heads that share the keys.
+//
+// dq and dk, dv are two kernels that both compute z and dp (7 products where one kernel would need 5):
+// each sum then stays in tensor memory in a fixed order, without atomics and without an fp32 dq in
+// memory.
+//
+// Sums, maxima, exponentials and lse are fp32. Rounded to bf16 as operands: p (half a step, 2^-8 of
+// each value) and dz.
+#include <algorithm>
+#include <atomic>
+
+#include "attn.h"
+#include "tensor.cuh"
+
+namespace adaln {
+
+#define ADALN_IN_ATTN(cond) ADALN_IN(::adaln::kDbgAttn, cond)
+
+constexpr int kAttnThreads = 384;  // two warpgroups of rows, one warp of products, one of loads
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kAllocWarp = 10;
+constexpr uint32_t kPanel = kAttnTile * 128;  // 128 rows of 64 elements, 128-byte swizzle
+
+// Shared memory: two resident tiles, then a ring. STATS: room for the row statistics of dk and dv.
+template <int DP, bool STATS = false>
+struct AttnShape {
+    static constexpr uint32_t kTile = DP / 64 * kPanel;
+    static constexpr int kStages = DP == 128 ? (STATS ? 4 : 5) : 8;
+    static constexpr size_t kSmem = 1024 + (2 + kStages) * (size_t)kTile;
+};
+
+// ---- work list -----------------------------------------------------------------------------
+__device__ __forceinline__ int64_t attn_start(const int32_t* cu, int64_t s, int64_t nseg, int64_t R) {
+    if (!ADALN_IN_ATTN(s >= 0 && s <= nseg)) return 0;
+    return cu ? (int64_t)__ldg(cu + s) : s * (R / nseg);
+}
+
+__device__ __forceinline__ int attn_class(int cost) {
+    if (cost <= 0) return 0;
+    const int c = 1 + (int)(__float_as_uint((float)cost) >> 21) - (127 << 2);
+    return min(c, kAttnClasses - 1);
+}
+
+// One CTA a list. Two passes over the tiles: how many of each cost class, then each to its place
+// (any order within a class: nothing that is computed depends on it).
+__global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnPlanArgs a) {
+    pdl_begin();
+    __shared__ int bins[kAttnClasses], place[kAttnClasses];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, list = blockIdx.x;
+    const AttnTables& t = a.t;
+    bool bad = false;
+    for (int64_t s = tid; s < t.nseg; s += 1024) {
+        const int64_t q0 = attn_start(t.cu_q, s, t.nseg, t.Rq), q1 = attn_start(t.cu_q, s + 1, t.nseg, t.Rq);
+        const int64_t k0 = attn_start(t.cu_k, s, t.nseg, t.Rk), k1 = attn_start(t.cu_k, s + 1, t.nseg, t.Rk);
+        bad |= q0 < 0 || q1 < q0 || q1 > t.Rq || k0 < 0 || k1 < k0 || k1 > t.Rk;
+    }
+    if (tid == 0) {
+        if (t.cu_q) bad |= __ldg(t.cu_q) != 0 || (int64_t)__ldg(t.cu_q + t.nseg) != t.Rq;
+        if (t.cu_k) bad |= __ldg(t.cu_k) != 0 || (int64_t)__ldg(t.cu_k + t.nseg) != t.Rk;
+        if (t.nseg == 0) bad |= t.Rq != 0 || t.Rk != 0;
+    }
+    if (tid < kAttnClasses) bins[tid] = 0;
+    const bool any_bad = __syncthreads_or(bad);
+    if (tid == 0 && list == 0) {
+        a.status[0] = any_bad ? kErrSeqlens : 0u;
+        a.status[1] = 0u;  // the kernels' word
+        a.header->magic = kStatusMagic;
+        a.header->nwords = 2;
+    }
+    if (any_bad) {
+        if (tid == 0) a.count[list] = 0;
+        return;
+    }
+    const int tile = a.tile[list];
+    auto each = [&](auto use) {
+        for (int64_t base = 32 * (int64_t)warp; base < t.nseg; base += 1024) {
+            const int64_t s = base + lane;
+            int q0 = 0, nq = 0, k0 = 0, nk = 0;
+            if (s < t.nseg) {
+                q0 = (int)attn_start(t.cu_q, s, t.nseg, t.Rq);
+                nq = (int)attn_start(t.cu_q, s + 1, t.nseg, t.Rq) - q0;
+                k0 = (int)attn_start(t.cu_k, s, t.nseg, t.Rk);
+                nk = (int)attn_start(t.cu_k, s + 1, t.nseg, t.Rk) - k0;
+            }
+            for (int i = 0; i < 32 && base + i < t.nseg; ++i) {
+                const int Q0 = __shfl_sync(0xFFFFFFFFu, q0, i), NQ = __shfl_sync(0xFFFFFFFFu, nq, i);
+                const int K0 = __shfl_sync(0xFFFFFFFFu, k0, i), NK = __shfl_sync(0xFFFFFFFFu, nk, i);
+                const int len = list ? NK : NQ;
+                for (int64_t at = (int64_t)lane * tile; at < len; at += 32 * (int64_t)tile) {
+                    AttnItem it{};
+                    it.rows = min(tile, len - (int)at);
+                    if (list == 0) {
+                        it.row0 = Q0 + (int)at;
+                        it.other0 = K0;
+                        it.others = NK;
+                        it.shift = t.causal ? (int)at + NK - NQ : NK;
+                        it.end = K0 + NK == (int)t.Rk;
+                        const int seen = max(0, min(NK, it.shift + it.rows));
+                        use(it, (seen + kAttnTile - 1) / kAttnTile);
+                    } else {
+                        it.row0 = K0 + (int)at;
+                        it.other0 = Q0;
+                        it.others = NQ;
+                        it.shift = t.causal ? (int)at - NK + NQ : -kAttnTile;
+                        it.end = Q0 + NQ == (int)t.Rq;
+                        use(it, (NQ - min(NQ, max(0, it.shift)) + kAttnTile - 1) / kAttnTile);
+                    }
+                }
+            }
+        }
+    };
+    each([&](const AttnItem&, int cost) { atomicAdd(&bins[attn_class(cost)], 1); });
+    __syncthreads();
+    if (warp == 0) {
+        // Places in descending order of the classes.
+        int v[kAttnClasses / 32], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kAttnClasses / 32; ++i) sum += v[i] = bins[kAttnClasses - 1 - (lane * (kAttnClasses / 32) + i)];
+        int before = sum;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xFFFFFFFFu, before, o);
+            if (lane >= o) before += x;
+        }
+        if (lane == 31) a.count[list] = (int)min((int64_t)before, a.most[list]);
+        before -= sum;
+#pragma unroll
+        for (int i = 0; i < kAttnClasses / 32; ++i) {
+            place[kAttnClasses - 1 - (lane * (kAttnClasses / 32) + i)] = before;
+            before += v[i];
+        }
+    }
+    __syncthreads();
+    each([&](const AttnItem& it, int cost) {
+        const int at = atomicAdd(&place[attn_class(cost)], 1);
+        if (at < a.most[list]) a.items[list][at] = it;
+    });
+}
+
+__device__ __forceinline__ AttnItem attn_item(const AttnItem* items, int64_t i, int64_t most) {
+    AttnItem it{};
+    if (!ADALN_IN_ATTN(i >= 0 && i < most)) return it;
+    const int4 a = __ldg(reinterpret_cast<const int4*>(items + i));
+    const int2 b = __ldg(reinterpret_cast<const int2*>(items + i) + 2);
+    it.row0 = a.x;
+    it.rows = a.y;
+    it.other0 = a.z;
+    it.others = a.w;
+    it.shift = b.x;
+    it.end = b.y;
+    return it;
+}
+// The k-th unit of this CTA: forth and back over the CTAs, so that the first ones do not get the
+// longest of every lap.
+__device__ __forceinline__ int64_t attn_unit(int64_t lap) {
+    const int64_t G = gridDim.x, b = blockIdx.x;
+    return lap * G + ((lap & 1) ? G - 1 - b : b);
+}
+
+// ---- operands --------------------------------------------------------------------------------
+template <int DP>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int head, int row, uint32_t bar) {
+    tma_load3(dst, map, 0, head, row, bar);
+    if (DP == 128) tma_load3(dst + kPanel, map, 64, head, row, bar);
+}
+// Rows [from, 128) of a tile become zeros: what follows a segment may hold anything, and 0 * NaN is NaN.
+template <int DP>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int lane) {
+#pragma unroll
+    for (int p = 0; p < DP / 64; ++p) {
+        for (uint32_t at = (uint32_t)from * 128 + 16 * lane; at < kPanel; at += 512)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + p * kPanel + at), "r"(0u) : "memory");
+    }
+}
+// D = A B^T over d: both tiles with d contiguous.
+template <int DP>
+__device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint32_t a, uint32_t b, int d) {
+    const uint64_t da = smem_desc(a, 0), db = smem_desc(b, 0);
+    constexpr uint32_t idesc = mma_desc(128, kAttnTile, false, false);
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k) {
+        const uint64_t off = (uint64_t)((k & 3) * 2 + (k >> 2) * (kPanel >> 4));
+        if (16 * k < d) mma_bf16_ss(d_tmem, da + off, db + off, idesc, k > 0);
+    }
+}
+// D (+)= A B with A [128, 128] bf16 in tensor memory, its columns 0..63 from `a`, the others from
+// `a2`; B a tile whose 128 rows are the sum's, d columns.
+__device__ __forceinline__ void mma_cols(uint32_t d_tmem, uint32_t a, uint32_t a2, uint32_t b, int d, bool accumulate) {
+    const uint64_t db = smem_desc(b, kPanel);
+    const uint32_t idesc = mma_desc(128, (d + 15) / 16 * 16, false, true);
+#pragma unroll
+    for (int k = 0; k < kAttnTile / 16; ++k)
+        mma_bf16_ts(d_tmem, k < 4 ? a + 8 * k : a2 + 8 * (k - 4), db + (uint64_t)(k * (2048 >> 4)), idesc,
+                    accumulate || k > 0);
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
+// 32 columns of a row to memory as bf16, as far as the row's d elements go.
+__device__ __forceinline__ void store32(void* row, int col, int d, const float (&v)[32], float f) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        if (col + 8 * g >= d) break;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack2(v[8 * g + 2 * j] * f, v[8 * g + 2 * j + 1] * f);
+        st_vec(reinterpret_cast<__nv_bfloat16*>(row) + col + 8 * g, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+}
+__device__ __forceinline__ void store_zeros(void* row, int c0, int c1, int d) {
+    for (int c = c0; c < min(c1, d); c += 8)
+        st_vec(reinterpret_cast<__nv_bfloat16*>(row) + c, make_uint4(0, 0, 0, 0));
+}
+
+// What a CTA has issued, for the drain after a timeout: copies and products must not land in memory
+// that has been given back.
+struct AttnIssued {
+    uint32_t ring = 0, pair = 0, tail = 0;  // fills of the ring, of the resident tiles, of tails
+    bool mma = false;
+};
+
+// ---- forward ---------------------------------------------------------------------------------
+template <int DP>
+__global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_constant__ CUtensorMap mq,
+                                                                const __grid_constant__ CUtensorMap mk,
+                                                                const __grid_constant__ CUtensorMap mv,
+                                                                const AttnFwdArgs a) {
+    using S = AttnShape<DP>;
+    constexpr int ST = S::kStages;
+    extern __shared__ uint4 dyn[];
+    __shared__ __align__(8) uint64_t bars[2 * ST + 12];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t qt = (smem_addr(dyn) + 1023u) & ~1023u, ring = qt + 2 * S::kTile;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * ST, qfull = empty + 8 * ST, qempty = qfull + 8;
+    const uint32_t sfull = qempty + 8, pfull = sfull + 16, odone = pfull + 16, ofree = odone + 16;
+    const uint32_t tail = ofree + 16, drain = tail + 8;
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        mbar_init(qfull, 1);
+        mbar_init(qempty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sfull + 8 * i, 1);
+            mbar_init(pfull + 8 * i, 4);
+            mbar_init(odone + 8 * i, 1);
+            mbar_init(ofree + 8 * i, 4);
+        }
+        mbar_init(tail, 1);
+        mbar_init(drain, 1);
+        abort_flag = 0;
+        mbar_fence_init();
+        tma_prefetch_map(&mq);
+        tma_prefetch_map(&mk);
+        tma_prefetch_map(&mv);
+    }
+    if (warp == kAllocWarp) tmem_alloc1(smem_addr(&tmem_base), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();  // behind the allocation: a dependent CTA on this SM must not get the columns first
+    const uint32_t tmem = tmem_base;
+    pdl_wait();
+    const int64_t units = (int64_t)*a.count * a.Hq * a.splits;
+    AttnIssued issued;
+    const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);
+
+    // A unit: an item, a head and a split; tiles [t0, t1[i]) of keys for the two tiles of queries.
+    AttnItem it;
+    int head = 0, split = 0, t0 = 0, t1[2];
+    auto decode = [&](int64_t u) {
+        head = (int)(u % a.Hq);
+        u /= a.Hq;
+        split = (int)(u % a.splits);
+        it = attn_item(a.items, u / a.splits, a.most);
+        int n[2], most = 0;
+        for (int i = 0; i < 2; ++i) {
+            const int rows = min(max(it.rows - i * kAttnTile, 0), kAttnTile);
+            const int seen = rows > 0 ? max(0, min(it.others, it.shift + i * kAttnTile + rows)) : 0;
+            n[i] = (seen + kAttnTile - 1) / kAttnTile;
+            most = max(most, n[i]);
+        }
+        t0 = (int)((int64_t)most * split / a.splits);
+        const int end = (int)((int64_t)most * (split + 1) / a.splits);
+        for (int i = 0; i < 2; ++i) t1[i] = max(t0, min(n[i], end));
+    };
+
+    if (role == kLoadWarp) {
+        bool live = true;
+        fence_async_proxy();
+        for (int64_t lap = 0; live; ++lap) {
+            const int64_t u = attn_unit(lap);
+            if (lap * gridDim.x >= units) break;
+            if (u >= units) continue;
+            decode(u);
+            const int end = max(t1[0], t1[1]);
+            if (end == t0) continue;
+            live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(qempty, (issued.pair - 1) & 1u, &abort_flag));
+            if (!live) break;
+            const int tiles = it.rows > kAttnTile ? 2 : 1;
+            if (elect_lane()) {
+                mbar_arrive_expect_tx(qfull, tiles * S::kTile);
+                for (int i = 0; i < tiles; ++i)
+                    load_tile<DP>(qt + i * S::kTile, &mq, head, it.row0 + i * kAttnTile, qfull);
+            }
+            ++issued.pair;
+            const int kv = head / a.group;
+            for (int t = t0; t < end && live; ++t) {
+                const int row = it.other0 + t * kAttnTile, left = it.others - t * kAttnTile;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t s = issued.ring % ST, lap_ = issued.ring / ST;
+                    live = __all_sync(0xFFFFFFFFu, lap_ == 0 || mbar_wait_bounded(empty + 8 * s, (lap_ - 1) & 1u, &abort_flag));
+                    if (!live) break;
+                    const uint32_t dst = ring + s * S::kTile;
+                    // The values' last tile of a segment that something follows goes through this warp.
+                    const bool cut = x == 1 && left < kAttnTile && !it.end;
+                    if (elect_lane()) {
+                        const uint32_t bar = cut ? tail : full + 8 * s;
+                        mbar_arrive_expect_tx(bar, S::kTile);
+                        load_tile<DP>(dst, x ? &mv : &mk, kv, row, bar);
+                    }
+                    if (cut) {
+                        live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail, issued.tail & 1u, &abort_flag));
+                        ++issued.tail;
+                        if (live) {
+                            zero_rows<DP>(dst, left, lane);
+                            fence_shared_async();
+                        }
+                        __syncwarp();
+                        if (elect_lane()) mbar_arrive(full + 8 * s);
+                    }
+                    ++issued.ring;
+                    if (!live) break;
+                }
+            }
+        }
+    } else if (role == kMmaWarp) {
+        bool live = true;
+        uint32_t used = 0, pairs = 0, np[2] = {0, 0}, nu[2] = {0, 0};  // ring tiles, units, tiles and units a warpgroup
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            live = live && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity & 1u, &abort_flag));
+            return live;
+        };
+        auto stage = [&](uint32_t n) { return n % ST; };
+        auto scores = [&](int i, uint32_t n) {
+            if (elect_lane()) {
+                mma_rows<DP>(tmem + 128 * i, qt + i * S::kTile, ring + stage(n) * S::kTile, a.d);
+                mma_commit1(sfull + 8 * i);
+            }
+        };
+        for (int64_t lap = 0; live; ++lap) {
+            const int64_t u = attn_unit(lap);
+            if (lap * gridDim.x >= units) break;
+            if (u >= units) continue;
+            decode(u);
+            const int end = max(t1[0], t1[1]);
+            if (end == t0) continue;
+            if (!wait(qfull, pairs) || !wait(full + 8 * stage(used), used / ST)) break;
+            tc_fence_after();
+            issued.mma = true;
+            for (int i = 0; i < 2; ++i)
+                if (t1[i] > t0) scores(i, used);
+            if (elect_lane()) mma_commit1(empty + 8 * stage(used));
+            for (int t = t0; t < end; ++t, used += 2) {
+                const bool more = t + 1 < end;
+                if (more && !wait(full + 8 * stage(used + 2), (used + 2) / ST)) break;
+                if (!wait(full + 8 * stage(used + 1), (used + 1) / ST)) break;
+                for (int i = 0; i < 2; ++i) {
+                    if (t >= t1[i]) continue;
+                    if (t == t0 && nu[i] > 0 && !wait(ofree + 8 * i, nu[i] - 1)) break;
+                    if (!wait(pfull + 8 * i, np[i])) break;
+                    tc_fence_after();
+                    if (elect_lane()) {
+                        mma_cols(tmem + 256 + 128 * i, tmem + 128 * i, tmem + 128 * i + 32, ring + stage(used + 1) * S::kTile,
+                                 a.d, t > t0);
+                        mma_commit1(odone + 8 * i);
+                    }
+                    ++np[i];
+                    if (t + 1 < t1[i]) scores(i, used + 2);
+                }
+                if (!live) break;
+                if (elect_lane()) {
+                    mma_commit1(empty + 8 * stage(used + 1));
+                    if (more) mma_commit1(empty + 8 * stage(used + 2));
+                }
+            }
+            if (!live) break;
+            if (elect_lane()) mma_commit1(qempty);
+            ++pairs;
+            for (int i = 0; i < 2; ++i)
+                if (t1[i] > t0) ++nu[i];
+        }
+    } else if (role < kMmaWarp) {
+        const int i = warp >> 2;  // this warpgroup's tile of queries
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), st = lanes + 128 * i, ot = lanes + 256 + 128 * i;
+        const int r = (warp & 3) * 32 + lane;
+        const float sl2 = a.scale * kLog2e;
+        uint32_t tiles = 0;
+        bool live = true;
+        for (int64_t lap = 0; live; ++lap) {
+            const int64_t u = attn_unit(lap);
+            if (lap * gridDim.x >= units) break;
+            if (u >= units) continue;
+            decode(u);
+            const int row = i * kAttnTile + r, end = i ? t1[1] : t1[0];
+            // Keys that this row sees.
+            const int seen = max(0, min(it.others, it.shift + row + 1));
+            float m = neg_inf(), l = 0.0f;  // the exponentials' reference, their sum
+            for (int t = t0; t < end; ++t, ++tiles) {
+                live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sfull + 8 * i, tiles & 1u, &abort_flag));
+                if (!live) break;
+                tc_fence_after();
+                float v[64], w[64];
+                tmem_ld64(st, v);
+                tmem_ld64(st + 64, w);
+                const int lim = seen - t * kAttnTile;
+                if (__any_sync(0xFFFFFFFFu, lim < kAttnTile)) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) {
+                        v[j] = j < lim ? v[j] : neg_inf();
+                        w[j] = 64 + j < lim ? w[j] : neg_inf();
+                    }
+                }
+                float m4[4] = {v[0], v[1], w[0], w[1]};
+#pragma unroll
+                for (int j = 2; j < 64; j += 2) {
+                    m4[0] = fmaxf(m4[0], v[j]);
+                    m4[1] = fmaxf(m4[1], v[j + 1]);
+                    m4[2] = fmaxf(m4[2], w[j]);
+                    m4[3] = fmaxf(m4[3], w[j + 1]);
+                }
+                const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                if (t == t0) {
+                    m = mt;
+                } else if (__any_sync(0xFFFFFFFFu, (mt - m) * sl2 > 8.0f)) {
+                    // The reference may lag behind the maximum by 2^8, which fp32 sums and bf16 p take as
+                    // well as 1; beyond it, what has been summed is brought to the new one.
+                    const float to = fmaxf(m, mt), f = to == m ? 1.0f : exp2_ftz((m - to) * sl2);
+                    live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
+                    if (!live) break;
+                    tc_fence_after();
+                    l *= f;
+                    m = to;
+#pragma unroll 1
+                    for (int c = 0; c < a.d; c += 32) {
+                        float o[32];
+                        uint32_t b[32];
+                        tmem_ld32(ot + c, o);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) b[j] = __float_as_uint(o[j] * f);
+                        tmem_st32(ot + c, b);
+                    }
+                }
+                // A row that has seen nothing yet: every exponential is 0 (and NaN stays).
+                const f2r s2 = p_splat(sl2), c2 = p_splat(m == neg_inf() ? 0.0f : -m * sl2);
+                f2r sum[2] = {kPairZero, kPairZero};
+                uint32_t b[32];
+                auto half = [&](const float (&x)[64], uint32_t to) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float2 e = p_get(p_fma(p_make(x[2 * j], x[2 * j + 1]), s2, c2));
+                        const float e0 = exp2_ftz(e.x), e1 = exp2_ftz(e.y);
+                        sum[j & 1] = p_add(sum[j & 1], p_make(e0, e1));
+                        b[j] = pack2(e0, e1);
+                    }
+                    tmem_st32(to, b);
+                };
+                half(v, st);
+                half(w, st + 32);
+                l += p_hsum(p_add(sum[0], sum[1]));
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfull + 8 * i);
+            }
+            if (!live) break;
+            const bool mine = row < it.rows;
+            const int64_t at = (int64_t)it.row0 + row;
+            const bool in = mine && ADALN_IN_ATTN(at >= 0 && at < a.Rq && head < a.Hq);
+            if (end > t0) {
+                live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
+                if (!live) break;
+                tc_fence_after();
+            }
+            const bool none = l == 0.0f;
+            if (a.splits == 1) {
+                __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + at * a.o_ld + (int64_t)head * a.d;
+                if (end > t0) {
+                    const float f = 1.0f / l;
+#pragma unroll 1
+                    for (int c = 0; c < a.d; c += 32) {
+                        float o[32];
+                        tmem_ld32(ot + c, o);
+                        if (in && !none) store32(out, c, a.d, o, f);
+                    }
+                }
+                if (in && none) store_zeros(out, 0, a.d, a.d);
+                if (in) a.lse[(int64_t)head * a.Rq + at] = none ? neg_inf() : fmaf(m, a.scale, logf(l));
+            } else {
+                const int64_t slot = ((int64_t)split * a.Hq + head) * a.Rq + at;
+                if (end > t0) {
+#pragma unroll 1
+                    for (int c = 0; c < a.d; c += 32) {
+                        float o[32];
+                        tmem_ld32(ot + c, o);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            if (in && c + j < a.d)
+                                *reinterpret_cast<float4*>(a.part + slot * a.d + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    }
+                }
+                if (in) a.ml[slot] = make_float2(m, l);
+            }
+            if (end > t0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ofree + 8 * i);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (__builtin_expect(*(volatile int*)&abort_flag, 0)) {
+        volatile int never = 0;
+        if (warp == kLoadWarp && lane == 0) {
+            if (issued.pair) mbar_wait_bounded(qfull, (issued.pair - 1) & 1u, &never);
+            if (issued.tail) mbar_wait_bounded(tail, (issued.tail - 1) & 1u, &never);
+            for (uint32_t s = 0; s < min(issued.ring, (uint32_t)ST); ++s)
+                mbar_wait_bounded(full + 8 * s, ((issued.ring - 1 - s) / ST) & 1u, &never);
+        }
+        if (warp == kMmaWarp && issued.mma && elect_lane()) {
+            mma_commit1(drain);
+            mbar_wait_bounded(drain, 0, &never);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == kAllocWarp) tmem_free1(tmem, 512);
+    if (tid == 0 && abort_flag) atomicOr(a.status, kErrTimeout);
+}
+
+// The splits of a row joined in their order: o = sum_s w_s o_s / sum_s w_s l_s, w_s = 2^(m_s - max m).
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnJoinArgs a) {
+    pdl_begin();
+    if (*a.bad) return;
+    const float sl2 = a.scale * kLog2e;
+    const int vecs = a.d / 8;
+    const int64_t total = a.Rq * a.Hq * vecs, plane = a.Rq * a.Hq;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int v = (int)(i % vecs);
+        const int64_t hr = i / vecs;  // head * Rq + row
+        if (!ADALN_IN_ATTN(hr < plane)) continue;
+        float top = neg_inf(), l = 0.0f, o[8] = {};
+        for (int s = 0; s < a.splits; ++s) {
+            const float2 ml = a.ml[s * plane + hr];
+            if (ml.y != 0.0f) top = fmaxf(top, ml.x);
+        }
+        for (int s = 0; s < a.splits; ++s) {
+            const float2 ml = a.ml[s * plane + hr];
+            if (ml.y == 0.0f) continue;  // a split that this row sees nothing of
+            const float w = top == neg_inf() ? 1.0f : exp2_ftz((ml.x - top) * sl2);
+            const float4* p = reinterpret_cast<const float4*>(a.part + (s * plane + hr) * a.d + 8 * v);
+            const float4 x = p[0], y = p[1];
+            l = fmaf(w, ml.y, l);
+            o[0] = fmaf(w, x.x, o[0]);
+            o[1] = fmaf(w, x.y, o[1]);
+            o[2] = fmaf(w, x.z, o[2]);
+            o[3] = fmaf(w, x.w, o[3]);
+            o[4] = fmaf(w, y.x, o[4]);
+            o[5] = fmaf(w, y.y, o[5]);
+            o[6] = fmaf(w, y.z, o[6]);
+            o[7] = fmaf(w, y.w, o[7]);
+        }
+        const float f = l == 0.0f ? 0.0f : 1.0f / l;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack2(o[2 * j] * f, o[2 * j + 1] * f);
+        const int64_t h = hr / a.Rq, r = hr % a.Rq;
+        st_vec(reinterpret_cast<__nv_bfloat16*>(a.o) + r * a.o_ld + h * a.d + 8 * v, make_uint4(w[0], w[1], w[2], w[3]));
+        if (v == 0) a.lse[hr] = l == 0.0f ? neg_inf() : fmaf(top, a.scale, logf(l));
+    }
+}
+
+// ---- backward --------------------------------------------------------------------------------
+// delta = dout . o of every row and head, and lse in units of log 2: 16 lanes a row of a head.
+__global__ void __launch_bounds__(256) attn_delta_kernel(const AttnDeltaArgs a) {
+    pdl_begin();
+    constexpr int U = 4;
+    const int lane = threadIdx.x & 15, vecs = a.d / 8;
+    const int64_t total = a.Rq * a.Hq, step = (int64_t)gridDim.x * 16;
+    const int64_t first = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    for (int64_t base = first - (first & 1); base < total; base += U * step) {  // both groups of a warp together
+        uint4 x[U], y[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t i = base + (first & 1) + j * step;
+            x[j] = y[j] = make_uint4(0, 0, 0, 0);
+            if (i < total && lane < vecs && ADALN_IN_ATTN(i >= 0)) {
+                const int64_t r = i / a.Hq, h = i % a.Hq;
+                x[j] = ld_stream(reinterpret_cast<const __nv_bfloat16*>(a.dout) + r * a.do_ld + h * a.d + 8 * lane);
+                y[j] = ld_stream(reinterpret_cast<const __nv_bfloat16*>(a.o) + r * a.o_ld + h * a.d + 8 * lane);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t i = base + (first & 1) + j * step;
+            f2r p[4], q[4], sum = kPairZero;
+            Io<__nv_bfloat16>::unpackp(x[j], p);
+            Io<__nv_bfloat16>::unpackp(y[j], q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum = p_fma(p[e], q[e], sum);
+            float v = p_hsum(sum);
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            if (lane == 0 && i < total && ADALN_IN_ATTN(i >= 0)) {
+                const int64_t at = i % a.Hq * a.Rq + i / a.Hq;
+                a.delta[at] = v;
+                a.lse2[at] = a.lse[at] * kLog2e;
+            }
+        }
+    }
+}
+
+// 64 scores of a row to exponentials, those outside [from, to) 0.
+__device__ __forceinline__ void mask64(float (&p)[64], int from, int to) {
+#pragma unroll
+    for (int j = 0; j < 64; ++j) p[j] = j >= from && j < to ? p[j] : 0.0f;
+}
+
+// dq of a tile of 128 queries. Its scores have two places in tensor memory: dz goes over the scores that
+// it came from, and the next scores and dp are formed while the warps are at it. The two warpgroups
+// take 64 keys of a step each, a thread a row.
+template <int DP>
+__global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_constant__ CUtensorMap mdo,
+                                                               const __grid_constant__ CUtensorMap mq,
+                                                               const __grid_constant__ CUtensorMap mk,
+                                                               const __grid_constant__ CUtensorMap mv,
+                                                               const AttnBwdArgs a) {
+    using S = AttnShape<DP>;
+    constexpr int ST = S::kStages;
+    extern __shared__ uint4 dyn[];
+    __shared__ __align__(8) uint64_t bars[2 * ST + 11];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t qt = (smem_addr(dyn) + 1023u) & ~1023u, ring = qt + 2 * S::kTile;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * ST, qfull = empty + 8 * ST, qempty = qfull + 8;
+    const uint32_t sfull = qempty + 8, pfull = sfull + 16, pfree = pfull + 8, dsfull = pfree + 8;
+    const uint32_t done = dsfull + 8, freed = done + 8, tail = freed + 8, drain = tail + 8;
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        mbar_init(qfull, 1);
+        mbar_init(qempty, 1);
+        mbar_init(sfull, 1);
+        mbar_init(sfull + 8, 1);
+        mbar_init(pfull, 1);
+        mbar_init(pfree, 8);
+        mbar_init(dsfull, 8);
+        mbar_init(done, 1);
+        mbar_init(freed, 8);
+        mbar_init(tail, 1);
+        mbar_init(drain, 1);
+        abort_flag = 0;
+        mbar_fence_init();
+        tma_prefetch_map(&mdo);
+        tma_prefetch_map(&mq);
+        tma_prefetch_map(&mk);
+        tma_prefetch_map(&mv);
+    }
+    if (warp == kAllocWarp) tmem_alloc1(smem_addr(&tmem_base), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();
+    const uint32_t tmem = tmem_base, dp_tmem = tmem + 256, acc = tmem + 384;
+    pdl_wait();
+    const int64_t units = (int64_t)*a.count * a.Hq;
+    AttnIssued issued;
+    const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);
+    AttnItem it;
+    int head = 0, n = 0;
+    auto decode = [&](int64_t u) {
+        head = (int)(u % a.Hq);
+        it = attn_item(a.items, u / a.Hq, a.most);
+        n = (max(0, min(it.others, it.shift + it.rows)) + kAttnTile - 1) / kAttnTile;
+    };
+
+    if (role == kLoadWarp) {
+        bool live = true;
+        fence_async_proxy();
+        for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
+            const int64_t u = attn_unit(lap);
+            if (u >= units) continue;
+            decode(u);
+            if (n == 0) continue;
+            live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(qempty, (issued.pair - 1) & 1u, &abort_flag));
+            if (!live) break;
+            if (elect_lane()) {
+                mbar_arrive_expect_tx(qfull, 2 * S::kTile);
+                load_tile<DP>(qt, &mq, head, it.row0, qfull);
+                load_tile<DP>(qt + S::kTile, &mdo, head, it.row0, qfull);
+            }
+            ++issued.pair;
+            const int kv = head / a.group;
+            for (int t = 0; t < n && live; ++t) {
+                const int row = it.other0 + t * kAttnTile, left = it.others - t * kAttnTile;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t s = issued.ring % ST, l = issued.ring / ST;
+                    live = __all_sync(0xFFFFFFFFu, l == 0 || mbar_wait_bounded(empty + 8 * s, (l - 1) & 1u, &abort_flag));
+                    if (!live) break;
+                    const uint32_t dst = ring + s * S::kTile;
+                    const bool cut = x == 0 && left < kAttnTile && !it.end;  // dz k: keys past the segment's end
+                    if (elect_lane()) {
+                        const uint32_t bar = cut ? tail : full + 8 * s;
+                        mbar_arrive_expect_tx(bar, S::kTile);
+                        load_tile<DP>(dst, x ? &mv : &mk, kv, row, bar);
+                    }
+                    if (cut) {
+                        live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail, issued.tail & 1u, &abort_flag));
+                        ++issued.tail;
+                        if (live) {
+                            zero_rows<DP>(dst, left, lane);
+                            fence_shared_async();
+                        }
+                        __syncwarp();
+                        if (elect_lane()) mbar_arrive(full + 8 * s);
+                    }
+                    ++issued.ring;
+                    if (!live) break;
+                }
+            }
+        }
+    } else if (role == kMmaWarp) {
+        bool live = true;
+        uint32_t used = 0, laps = 0, steps = 0;  // ring tiles; units; steps
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            live = live && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity & 1u, &abort_flag));
+            return live;
+        };
+        auto tile = [&](uint32_t x) { return ring + x % ST * S::kTile; };
+        auto loaded = [&](uint32_t x) { return wait(full + 8 * (x % ST), x / ST); };
+        // z of step j (of this unit), dp of step j.
+        auto scores = [&](int j) {
+            const uint32_t b = (steps + j) & 1u;
+            if (elect_lane()) {
+                mma_rows<DP>(tmem + 128 * b, qt, tile(used + 2 * j), a.d);
+                mma_commit1(sfull + 8 * b);
+            }
+        };
+        auto dprobs = [&](int j) {
+            if (elect_lane()) {
+                mma_rows<DP>(dp_tmem, qt + S::kTile, tile(used + 2 * j + 1), a.d);
+                mma_commit1(pfull);
+                mma_commit1(empty + 8 * ((used + 2 * j + 1) % ST));
+            }
+        };
+        for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
+            const int64_t u = attn_unit(lap);
+            if (u >= units) continue;
+            decode(u);
+            if (n == 0) continue;
+            if (!wait(qfull, laps) || !loaded(used)) break;
+            tc_fence_after();
+            issued.mma = true;
+            scores(0);
+            if (!loaded(used + 1)) break;
+            tc_fence_after();
+            dprobs(0);
+            if (n > 1) {
+                if (!loaded(used + 2)) break;
+                tc_fence_after();
+                scores(1);
+            }
+            for (int j = 0; j < n; ++j) {
+                if (j + 1 < n) {
+                    if (!loaded(used + 2 * j + 3) || !wait(pfree, steps + j)) break;
+                    tc_fence_after();
+                    dprobs(j + 1);
+                }
+                if (j == 0 && laps > 0 && !wait(freed, laps - 1)) break;
+                if (!wait(dsfull, steps + j)) break;
+                tc_fence_after();
+                if (elect_lane()) {
+                    const uint32_t z = tmem + 128 * ((steps + j) & 1u);
+                    mma_cols(acc, z, z + 64, tile(used + 2 * j), a.d, j > 0);
+                    mma_commit1(empty + 8 * ((used + 2 * j) % ST));
+                }
+                if (j + 2 < n) {
+                    if (!loaded(used + 2 * j + 4)) break;
+                    tc_fence_after();
+                    scores(j + 2);
+                }
+            }
+            if (!live) break;
+            if (elect_lane()) {
+                mma_commit1(done);
+                mma_commit1(qempty);
+            }
+            used += 2 * n;
+            steps += n;
+            ++laps;
+        }
+    } else if (role < kMmaWarp) {
+        const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const float sl2 = a.scale * kLog2e;
+        const f2r s2 = p_splat(sl2);
+        uint32_t steps = 0, laps = 0;
+        bool live = true;
+        for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
+            const int64_t u = attn_unit(lap);
+            if (u >= units) continue;
+            decode(u);
+            const int64_t at = (int64_t)it.row0 + r;
+            const bool in = r < it.rows && ADALN_IN_ATTN(at >= 0 && at < a.Rq && head < a.Hq);
+            const float lse2 = in ? __ldg(a.lse2 + (int64_t)head * a.Rq + at) : 0.0f;
+            const float delta = in ? __ldg(a.delta + (int64_t)head * a.Rq + at) : 0.0f;
+            const int seen = max(0, min(it.others, it.shift + r + 1));
+            const f2r nl = p_splat(-lse2), nd = p_splat(-delta);
+            for (int t = 0; t < n; ++t, ++steps) {
+                const uint32_t b = steps & 1u, z = tmem + lanes + 128 * b + 64 * wg;
+                live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sfull + 8 * b, (steps >> 1) & 1u, &abort_flag));
+                if (!live) break;
+                tc_fence_after();
+                float p[64];
+                tmem_ld64(z, p);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float2 e = p_get(p_fma(p_make(p[2 * j], p[2 * j + 1]), s2, nl));
+                    p[2 * j] = exp2_ftz(e.x);
+                    p[2 * j + 1] = exp2_ftz(e.y);
+                }
+                const int lim = seen - t * kAttnTile - 64 * wg;
+                const bool cut = __any_sync(0xFFFFFFFFu, lim < 64);
+                live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(pfull, steps & 1u, &abort_flag));
+                if (!live) break;
+                tc_fence_after();
+                float dp[64];
+                tmem_ld64(dp_tmem + lanes + 64 * wg, dp);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfree);
+                if (cut) {
+                    mask64(p, 0, lim);
+                    mask64(dp, 0, lim);
+                }
+                uint32_t w[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float2 x = p_get(p_mul(p_add(p_make(dp[2 * j], dp[2 * j + 1]), nd), p_make(p[2 * j], p[2 * j + 1])));
+                    w[j] = pack2(x.x, x.y);
+                }
+                tmem_st32(z, w);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dsfull);
+            }
+            if (!live) break;
+            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.dx) + at * a.dx_ld + (int64_t)head * a.d;
+            if (n == 0) {
+                if (in) store_zeros(out, wg * (DP / 2), (wg + 1) * (DP / 2), a.d);
+                continue;
+            }
+            live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(done, laps & 1u, &abort_flag));
+            if (!live) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = wg * (DP / 2); c < min((wg + 1) * (DP / 2), a.d); c += 32) {
+                float o[32];
+                tmem_ld32(acc + lanes + c, o);
+                if (in) store32(out, c, a.d, o, a.scale);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(freed);
+            ++laps;
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (__builtin_expect(*(volatile int*)&abort_flag, 0)) {
+        volatile int never = 0;
+        if (warp == kLoadWarp && lane == 0) {
+            if (issued.pair) mbar_wait_bounded(qfull, (issued.pair - 1) & 1u, &never);
+            if (issued.tail) mbar_wait_bounded(tail, (issued.tail - 1) & 1u, &never);
+            for (uint32_t s = 0; s < min(issued.ring, (uint32_t)ST); ++s)
+                mbar_wait_bounded(full + 8 * s, ((issued.ring - 1 - s) / ST) & 1u, &never);
+        }
+        if (warp == kMmaWarp && issued.mma && elect_lane()) {
+            mma_commit1(drain);
+            mbar_wait_bounded(drain, 0, &never);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == kAllocWarp) tmem_free1(tmem, 512);
+    if (tid == 0 && abort_flag) atomicOr(a.status, kErrTimeout);
+}
+
+// dk and dv of a tile of 128 keys, over the queries of all heads that share them; everything transposed,
+// a thread a key. The two warpgroups take 64 queries of a step each. p goes over the scores and dz
+// over dp; the tensor cores form dv and the next scores while the warps are at dz, dk and the next dp while
+// they are at the next p.
+template <int DP>
+__global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_constant__ CUtensorMap mdo,
+                                                                const __grid_constant__ CUtensorMap mq,
+                                                                const __grid_constant__ CUtensorMap mk,
+                                                                const __grid_constant__ CUtensorMap mv,
+                                                                const AttnBwdArgs a) {
+    using S = AttnShape<DP, true>;
+    constexpr int ST = S::kStages, SS = 4;  // slots of row statistics
+    extern __shared__ uint4 dyn[];
+    __shared__ __align__(16) float stats[SS][2][kAttnTile];  // lse (units of log 2) and delta of a step's queries
+    __shared__ __align__(8) uint64_t bars[2 * ST + SS + 11];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t kt = (smem_addr(dyn) + 1023u) & ~1023u, ring = kt + 2 * S::kTile;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * ST, sready = empty + 8 * ST, kfull = sready + 8 * SS;
+    const uint32_t kempty = kfull + 8, sfull = kempty + 8, pready = sfull + 8, pfull = pready + 8, dsready = pfull + 8;
+    const uint32_t done = dsready + 8, freed = done + 8, tail = freed + 8, drain = tail + 8;
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < SS; ++i) mbar_init(sready + 8 * i, 32);
+        mbar_init(kfull, 1);
+        mbar_init(kempty, 1);
+        mbar_init(sfull, 1);
+        mbar_init(pready, 8);
+        mbar_init(pfull, 1);
+        mbar_init(dsready, 8);
+        mbar_init(done, 1);
+        mbar_init(freed, 8);
+        mbar_init(tail, 1);
+        mbar_init(drain, 1);
+        abort_flag = 0;
+        mbar_fence_init();
+        tma_prefetch_map(&mdo);
+        tma_prefetch_map(&mq);
+        tma_prefetch_map(&mk);
+        tma_prefetch_map(&mv);
+    }
+    if (warp == kAllocWarp) tmem_alloc1(smem_addr(&tmem_base), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();
+    const uint32_t tmem = tmem_base, dp_tmem = tmem + 128, dv_tmem = tmem + 256, dk_tmem = tmem + 384;
+    pdl_wait();
+    const int Hk = a.Hq / a.group;
+    const int64_t units = (int64_t)*a.count * Hk;
+    AttnIssued issued;
+    const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);
+    AttnItem it;
+    int head = 0, first = 0, tiles = 0, n = 0;  // key head; first tile of queries that sees a key, their number; steps
+    auto decode = [&](int64_t u) {
+        head = (int)(u % Hk);
+        it = attn_item(a.items, u / Hk, a.most);
+        first = max(0, it.shift) / kAttnTile;
+        tiles = max(0, (it.others + kAttnTile - 1) / kAttnTile - first);
+        n = tiles * a.group;
+    };
+
+    if (role == kLoadWarp) {
+        bool live = true;
+        uint32_t slots = 0;
+        fence_async_proxy();
+        for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
+            const int64_t u = attn_unit(lap);
+            if (u >= units) continue;
+            decode(u);
+            if (n == 0) continue;
+            live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(kempty, (issued.pair - 1) & 1u, &abort_flag));
+            if (!live) break;
+            if (elect_lane()) {
+                mbar_arrive_expect_tx(kfull, 2 * S::kTile);
+                load_tile<DP>(kt, &mk, head, it.row0, kfull);
+                load_tile<DP>(kt + S::kTile, &mv, head, it.row0, kfull);
+            }
+            ++issued.pair;
+            for (int j = 0; j < n && live; ++j, ++slots) {
+                const int h = head * a.group + j / tiles, t = first + j % tiles;
+                const int row = it.other0 + t * kAttnTile, left = it.others - t * kAttnTile;
+                const bool cut = left < kAttnTile && !it.end;  // both are operands of sums over the queries
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t s = issued.ring % ST, l = issued.ring / ST;
+                    live = __all_sync(0xFFFFFFFFu, l == 0 || mbar_wait_bounded(empty + 8 * s, (l - 1) & 1u, &abort_flag));
+                    if (!live) break;
+                    const uint32_t dst = ring + s * S::kTile;
+                    if (elect_lane()) {
+                        const uint32_t bar = cut ? tail : full + 8 * s;
+                        mbar_arrive_expect_tx(bar, S::kTile);
+                        load_tile<DP>(dst, x ? &mdo : &mq, h, row, bar);
+                    }
+                    if (x == 0) {
+                        // The slot's last readers were done before the tile that went was freed.
+                        const uint32_t dst2 = smem_addr(&stats[slots % SS][0][0]);
+                        for (int c = lane; c < 2 * kAttnTile; c += 32) {
+                            const int q = c & (kAttnTile - 1);
+                            const float* src = (c < kAttnTile ? a.lse2 : a.delta) + (int64_t)h * a.Rq + row + q;
+                            const bool in = q < left && ADALN_IN_ATTN(row >= 0 && (int64_t)row + q < a.Rq && h < a.Hq);
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst2 + 4 * c),
+                                         "l"(in ? src : a.lse2), "r"(in ? 4 : 0)
+                                         : "memory");
+                        }
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sready + 8 * (slots % SS))
+                                     : "memory");
+                    }
+                    if (cut) {
+                        live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail, issued.tail & 1u, &abort_flag));
+                        ++issued.tail;
+                        if (live) {
+                            zero_rows<DP>(dst, left, lane);
+                            fence_shared_async();
+                        }
+                        __syncwarp();
+                        if (elect_lane()) mbar_arrive(full + 8 * s);
+                    }
+                    ++issued.ring;
+                    if (!live) break;
+                }
+            }
+        }
+        cp_async_wait_all();
+    } else if (role == kMmaWarp) {
+        bool live = true;
+        uint32_t used = 0, laps = 0, steps = 0;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            live = live && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity & 1u, &abort_flag));
+            return live;
+        };
+        auto tile = [&](uint32_t x) { return ring + x % ST * S::kTile; };
+        auto loaded = [&](uint32_t x) { return wait(full + 8 * (x % ST), x / ST); };
+        auto scores = [&](int j) {
+            if (elect_lane()) {
+                mma_rows<DP>(tmem, kt, tile(used + 2 * j), a.d);
+                mma_commit1(sfull);
+            }
+        };
+        auto dprobs = [&](int j) {
+            if (elect_lane()) {
+                mma_rows<DP>(dp_tmem, kt + S::kTile, tile(used + 2 * j + 1), a.d);
+                mma_commit1(pfull);
+            }
+        };
+        for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
+            const int64_t u = attn_unit(lap);
+            if (u >= units) continue;
+            decode(u);
+            if (n == 0) continue;
+            if (!wait(kfull, laps) || !loaded(used)) break;
+            tc_fence_after();
+            issued.mma = true;
+            scores(0);
+            if (!loaded(used + 1)) break;
+            tc_fence_after();
+            dprobs(0);
+            if (laps > 0 && !wait(freed, laps - 1)) break;
+            for (int j = 0; j < n; ++j) {
+                if (!wait(pready, steps + j)) break;
+                tc_fence_after();
+                if (elect_lane()) {
+                    mma_cols(dv_tmem, tmem, tmem + 64, tile(used + 2 * j + 1), a.d, j > 0);
+                    mma_commit1(empty + 8 * ((used + 2 * j + 1) % ST));
+                }
+                if (j + 1 < n) {
+                    if (!loaded(used + 2 * j + 2)) break;
+                    tc_fence_after();
+                    scores(j + 1);
+                }
+                if (!wait(dsready, steps + j)) break;
+                tc_fence_after();
+                if (elect_lane()) {
+                    mma_cols(dk_tmem, dp_tmem, dp_tmem + 64, tile(used + 2 * j), a.d, j > 0);
+                    mma_commit1(empty + 8 * ((used + 2 * j) % ST));
+                }
+                if (j + 1 < n) {
+                    if (!loaded(used + 2 * j + 3)) break;
+                    tc_fence_after();
+                    dprobs(j + 1);
+                }
+            }
+            if (!live) break;
+            if (elect_lane()) {
+                mma_commit1(done);
+                mma_commit1(kempty);
+            }
+            used += 2 * n;
+            steps += n;
+            ++laps;
+        }
+    } else if (role < kMmaWarp) {
+        const int wg = warp >> 2, c = (warp & 3) * 32 + lane;  // this thread's key of the tile
+        const uint32_t lanes = ((uint32_t)(warp & 3) << 21) + 64 * wg;
+        const f2r s2 = p_splat(a.scale * kLog2e);
+        uint32_t steps = 0, laps = 0;
+        bool live = true;
+        for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
+            const int64_t u = attn_unit(lap);
+            if (u >= units) continue;
+            decode(u);
+            const int from = max(0, it.shift + c);  // the first query that sees this key
+            for (int j = 0; j < n; ++j, ++steps) {
+                const int q0 = (first + j % tiles) * kAttnTile + 64 * wg;
+                const bool cut = __any_sync(0xFFFFFFFFu, from > q0 || it.others < q0 + 64);
+                const uint32_t slot = smem_addr(&stats[steps % SS][0][0]) + 256 * wg;
+                live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sready + 8 * (steps % SS), (steps / SS) & 1u, &abort_flag) &&
+                                                   mbar_wait_bounded(sfull, steps & 1u, &abort_flag));
+                if (!live) break;
+                tc_fence_after();
+                float p[64];
+                tmem_ld64(tmem + lanes, p);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint4 l = lds128(slot + 16 * i);
+                    const f2r x = p_fma(p_make(p[4 * i], p[4 * i + 1]), s2, p_make(-__uint_as_float(l.x), -__uint_as_float(l.y)));
+                    const f2r y = p_fma(p_make(p[4 * i + 2], p[4 * i + 3]), s2, p_make(-__uint_as_float(l.z), -__uint_as_float(l.w)));
+                    p[4 * i] = exp2_ftz(p_get(x).x);
+                    p[4 * i + 1] = exp2_ftz(p_get(x).y);
+                    p[4 * i + 2] = exp2_ftz(p_get(y).x);
+                    p[4 * i + 3] = exp2_ftz(p_get(y).y);
+                }
+                if (cut) mask64(p, from - q0, it.others - q0);
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) w[i] = pack2(p[2 * i], p[2 * i + 1]);
+                tmem_st32(tmem + lanes, w);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pready);
+                live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(pfull, steps & 1u, &abort_flag));
+                if (!live) break;
+                tc_fence_after();
+                float dp[64];
+                tmem_ld64(dp_tmem + lanes, dp);
+                if (cut) mask64(dp, from - q0, it.others - q0);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint4 l = lds128(slot + 512 + 16 * i);
+                    const f2r x = p_mul(p_sub(p_make(dp[4 * i], dp[4 * i + 1]), p_make(__uint_as_float(l.x), __uint_as_float(l.y))),
+                                        p_make(p[4 * i], p[4 * i + 1]));
+                    const f2r y = p_mul(p_sub(p_make(dp[4 * i + 2], dp[4 * i + 3]), p_make(__uint_as_float(l.z), __uint_as_float(l.w))),
+                                        p_make(p[4 * i + 2], p[4 * i + 3]));
+                    w[2 * i] = pack2(p_get(x).x, p_get(x).y);
+                    w[2 * i + 1] = pack2(p_get(y).x, p_get(y).y);
+                }
+                tmem_st32(dp_tmem + lanes, w);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dsready);
+            }
+            if (!live) break;
+            // One warpgroup writes dv, the other dk.
+            const int64_t at = (int64_t)it.row0 + c;
+            const bool in = c < it.rows && ADALN_IN_ATTN(at >= 0 && head < Hk);
+            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(wg ? a.dx : a.dv) + at * (wg ? a.dx_ld : a.dv_ld) +
+                                 (int64_t)head * a.d;
+            if (n == 0) {
+                if (in) store_zeros(out, 0, a.d, a.d);
+                continue;
+            }
+            live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(done, laps & 1u, &abort_flag));
+            if (!live) break;
+            tc_fence_after();
+            const uint32_t src = (wg ? dk_tmem : dv_tmem) + ((uint32_t)(warp & 3) << 21);
+            const float f = wg ? a.scale : 1.0f;
+#pragma unroll 1
+            for (int x = 0; x < a.d; x += 32) {
+                float o[32];
+                tmem_ld32(src + x, o);
+                if (in) store32(out, x, a.d, o, f);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(freed);
+            ++laps;
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (__builtin_expect(*(volatile int*)&abort_flag, 0)) {
+        volatile int never = 0;
+        if (warp == kLoadWarp && lane == 0) {
+            if (issued.pair) mbar_wait_bounded(kfull, (issued.pair - 1) & 1u, &never);
+            if (issued.tail) mbar_wait_bounded(tail, (issued.tail - 1) & 1u, &never);
+            for (uint32_t s = 0; s < min(issued.ring, (uint32_t)ST); ++s)
+                mbar_wait_bounded(full + 8 * s, ((issued.ring - 1 - s) / ST) & 1u, &never);
+        }
+        if (warp == kMmaWarp && issued.mma && elect_lane()) {
+            mma_commit1(drain);
+            mbar_wait_bounded(drain, 0, &never);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == kAllocWarp) tmem_free1(tmem, 512);
+    if (tid == 0 && abort_flag) atomicOr(a.status, kErrTimeout);
+}
+
+// ---- launches ------------------------------------------------------------------------------
+namespace {
+
+unsigned cap(int64_t want, int64_t most) { return (unsigned)(want < 1 ? 1 : want < most ? want : most); }
+
+// Lets kernel variant `which` use its shared memory, once a device.
+cudaError_t allow_attn_smem(const void* fn, int which, size_t bytes) {
+    constexpr int kDevices = 64;
+    static std::atomic<bool> done[kDevices][6];
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev >= 0 && dev < kDevices && done[dev][which].load(std::memory_order_acquire)) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < kDevices) done[dev][which].store(true, std::memory_order_release);
+    return e;
+}
+
+// Tensor map of rows of H heads of d elements: boxes of 64 elements of one head by 128 rows, 128-byte
+// swizzle; what is past d, or past the last row, arrives as zeros.
+bool rows_map(CUtensorMap* m, const AttnRows& x, int d) {
+    const TensorMapEncode encode = tensor_map_encode();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)x.H, (cuuint64_t)x.R};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)x.ld * 2};
+    const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)kAttnTile}, one[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_attn_plan(const AttnPlanArgs& args, cudaStream_t stream) {
+    AttnPlanArgs a = args;
+    void* params[] = {&a};
+    return launch_dependent(reinterpret_cast<const void*>(&attn_plan_kernel), dim3(a.items[1] ? 2 : 1), dim3(1024),
+                            params, 0, stream);
+}
+
+cudaError_t launch_attn_fwd(const AttnFwdArgs& args, const AttnRows& q, const AttnRows& k, const AttnRows& v, int sms,
+                            cudaStream_t stream) {
+    AttnFwdArgs a = args;
+    CUtensorMap mq, mk, mv;
+    // Without keys nothing is loaded; the maps still have to be maps.
+    if (!rows_map(&mq, q, a.d) || !rows_map(&mk, k.R ? k : q, a.d) || !rows_map(&mv, k.R ? v : q, a.d))
+        return cudaErrorInvalidValue;
+    const bool wide = a.d > 64;
+    const void* fn = wide ? reinterpret_cast<const void*>(&attn_fwd_kernel<128>)
+                          : reinterpret_cast<const void*>(&attn_fwd_kernel<64>);
+    const size_t smem = wide ? AttnShape<128>::kSmem : AttnShape<64>::kSmem;
+    if (cudaError_t e = allow_attn_smem(fn, wide ? 1 : 0, smem)) return e;
+    void* params[] = {&mq, &mk, &mv, &a};
+    return launch_dependent(fn, dim3(cap(a.most * a.Hq * a.splits, sms)), dim3(kAttnThreads), params, smem, stream);
+}
+
+cudaError_t launch_attn_join(const AttnJoinArgs& args, int sms, cudaStream_t stream) {
+    AttnJoinArgs a = args;
+    void* params[] = {&a};
+    return launch_dependent(reinterpret_cast<const void*>(&attn_join_kernel),
+                            dim3(cap((a.Rq * a.Hq * (a.d / 8) + 255) / 256, 8 * (int64_t)sms)), dim3(256), params, 0, stream);
+}
+
+cudaError_t launch_attn_delta(const AttnDeltaArgs& args, int sms, cudaStream_t stream) {
+    AttnDeltaArgs a = args;
+    void* params[] = {&a};
+    return launch_dependent(reinterpret_cast<const void*>(&attn_delta_kernel),
+                            dim3(cap((a.Rq * a.Hq + 63) / 64, 8 * (int64_t)sms)), dim3(256), params, 0, stream);
+}
+
+cudaError_t launch_attn_dq(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
+                           const AttnRows& v, int sms, cudaStream_t stream) {
+    AttnBwdArgs a = args;
+    CUtensorMap mdo, mq, mk, mv;
+    if (!rows_map(&mdo, dout, a.d) || !rows_map(&mq, q, a.d) || !rows_map(&mk, k.R ? k : q, a.d) ||
+        !rows_map(&mv, k.R ? v : q, a.d))
+        return cudaErrorInvalidValue;
+    const bool wide = a.d > 64;
+    const void* fn = wide ? reinterpret_cast<const void*>(&attn_dq_kernel<128>)
+                          : reinterpret_cast<const void*>(&attn_dq_kernel<64>);
+    const size_t smem = wide ? AttnShape<128>::kSmem : AttnShape<64>::kSmem;
+    if (cudaError_t e = allow_attn_smem(fn, wide ? 3 : 2, smem)) return e;
+    void* params[] = {&mdo, &mq, &mk, &mv, &a};
+    return launch_dependent(fn, dim3(cap(a.most * a.Hq, sms)), dim3(kAttnThreads), params, smem, stream);
+}
+
+cudaError_t launch_attn_dkv(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
+                            const AttnRows& v, int sms, cudaStream_t stream) {
+    AttnBwdArgs a = args;
+    CUtensorMap mdo, mq, mk, mv;
+    if (!rows_map(&mdo, q.R ? dout : k, a.d) || !rows_map(&mq, q.R ? q : k, a.d) || !rows_map(&mk, k, a.d) ||
+        !rows_map(&mv, v, a.d))
+        return cudaErrorInvalidValue;
+    const bool wide = a.d > 64;
+    const void* fn = wide ? reinterpret_cast<const void*>(&attn_dkv_kernel<128>)
+                          : reinterpret_cast<const void*>(&attn_dkv_kernel<64>);
+    const size_t smem = wide ? AttnShape<128, true>::kSmem : AttnShape<64, true>::kSmem;
+    if (cudaError_t e = allow_attn_smem(fn, wide ? 5 : 4, smem)) return e;
+    void* params[] = {&mdo, &mq, &mk, &mv, &a};
+    return launch_dependent(fn, dim3(cap(a.most * (a.Hq / a.group), sms)), dim3(kAttnThreads), params, smem, stream);
+}
+
+cudaError_t debug_word_attn(uint32_t* out, bool reset) { return debug_word(out, reset); }
+
+}  // namespace adaln

@@ -1,0 +1,294 @@
+// Norms of queries and keys for each head, with their rotation by positions, in one pass:
+//
+//     xhat = x / sqrt(mean(x^2) + eps),  y = xhat * w,
+//     (out[2i], out[2i+1]) = (y[2i] cos t - y[2i+1] sin t,  y[2i] sin t + y[2i+1] cos t)
+//
+// t = position * theta^(-2i / w) on the pair's axis (of w elements). Backward, with dy the outputs'
+// gradient turned back by t:
+//
+//     dw = sum dy * xhat,  g = dy * w,  dx = rstd * (g - xhat * mean(g * xhat))
+//
+// Bound by HBM. A power of two of lanes shares a head, eight elements a lane, so that a head's sums
+// are a few shuffles and a pair never leaves its lane. A group of lanes takes a token and goes through
+// its heads, four (backward: two) at a time on their way: the token's angles are computed once for all
+// of them. Short batches go in items of fewer heads, so that every SM has some.
+//
+// Angles: a position times a frequency is far more than fp32 holds (position 500,000 at frequency 1 is
+// off by 0.03 rad). Frequencies are turns as binary fractions of 64 bits; the product with the integer
+// position wraps at whole turns by itself, so that what is left, the fraction of a turn, is good to
+// 2^-32 of a turn at any position.
+#include <atomic>
+
+#include "rope.h"
+
+namespace adaln {
+
+#define ADALN_IN_HEADS(cond) ADALN_IN(::adaln::kDbgHeads, cond)
+
+template <typename T>
+struct Lane {
+    static constexpr int VE = Io<T>::VE;   // elements of a 16-byte vector
+    static constexpr int NV = 8 / VE;      // vectors a lane: v = lane + j * GL of the head's
+    static constexpr int NP = VE / 2;      // pairs of a vector
+};
+
+template <int GL>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = GL / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// (a, b) -> (a c - b s, a s + b c)
+__device__ __forceinline__ f2r turn(f2r x, float c, float s) {
+    const float2 f = p_get(x);
+    return p_make(fmaf(-f.y, s, f.x * c), fmaf(f.x, s, f.y * c));
+}
+
+template <typename T, int GL, bool BWD>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+    using L = Lane<T>;
+    constexpr int U = BWD ? 2 : 4;  // heads on their way
+    constexpr int GROUPS = kRopeThreads / GL;
+    const int lane = threadIdx.x % GL, group = threadIdx.x / GL;
+    const int vecs = a.d / L::VE;
+    bool on[L::NV];
+    unsigned long long freq[L::NV][L::NP];
+    int axis[L::NV][L::NP];
+#pragma unroll
+    for (int j = 0; j < L::NV; ++j) {
+        const int v = lane + j * GL;
+        on[j] = v < vecs;
+#pragma unroll
+        for (int p = 0; p < L::NP; ++p) {
+            freq[j][p] = on[j] ? a.freq[v * L::NP + p] : 0;
+            axis[j][p] = on[j] ? a.axis[v * L::NP + p] : 0;
+        }
+    }
+    const float inv_d = 1.0f / (float)a.d;
+    pdl_begin();
+    // Both weights, as they come.
+    uint4 w[2][L::NV];
+    [[maybe_unused]] f2r dw[2][L::NV][L::NP];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int j = 0; j < L::NV; ++j) {
+            f2r one[L::NP];
+#pragma unroll
+            for (int p = 0; p < L::NP; ++p) {
+                one[p] = p_splat(1.0f);
+                if (BWD) dw[s][j][p] = kPairZero;
+            }
+            w[s][j] = Io<T>::packp(one);
+            if (a.side[s].weight && on[j]) w[s][j] = ld_keep(reinterpret_cast<const uint4*>(a.side[s].weight) + lane + j * GL);
+        }
+    }
+
+    const int64_t items = a.R * a.chunks, step = (int64_t)gridDim.x * GROUPS;
+    // The lanes of a warp stay together: its groups run as many rounds as its first one.
+    const int64_t first = (int64_t)blockIdx.x * GROUPS + group;
+    const int64_t warp_first = (int64_t)blockIdx.x * GROUPS + (threadIdx.x & ~31) / GL;
+    for (int64_t off = 0; warp_first + off < items; off += step) {
+        const int64_t item = first + off;
+        const bool live = item < items;
+        const int64_t r = live ? item / a.chunks : 0;
+        const int h0 = live ? (int)(item % a.chunks) * a.chunk : 0;
+        float c[L::NV][L::NP], sn[L::NV][L::NP];
+#pragma unroll
+        for (int j = 0; j < L::NV; ++j) {
+#pragma unroll
+            for (int p = 0; p < L::NP; ++p) {
+                c[j][p] = 1.0f;
+                sn[j][p] = 0.0f;
+                if (a.pos && ADALN_IN_HEADS(r < a.R)) {
+                    const long long at = __ldg(a.pos + r * a.naxes + axis[j][p]);
+                    const int turn32 = (int)(((unsigned long long)at * freq[j][p]) >> 32);
+                    sincospif((float)turn32 * 0x1p-31f, &sn[j][p], &c[j][p]);  // half turns
+                }
+            }
+        }
+        // One side's heads [b, e).
+        auto heads = [&](int s, int b, int e) {
+            const RopeSide& sd = a.side[s];
+            const int most = __reduce_max_sync(0xFFFFFFFFu, live ? e - b : 0);
+            for (int i = 0; i < most; i += U) {
+                uint4 x[U][L::NV];
+                [[maybe_unused]] uint4 y[U][L::NV];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int h = b + i + u;
+#pragma unroll
+                    for (int j = 0; j < L::NV; ++j) {
+                        x[u][j] = make_uint4(0, 0, 0, 0);
+                        if (BWD) y[u][j] = x[u][j];
+                        if (live && h < e && on[j] && ADALN_IN_HEADS(r >= 0 && r < a.R && h >= 0 && h < sd.heads)) {
+                            const int64_t at = (int64_t)h * a.d + (lane + j * GL) * L::VE;
+                            if (!BWD || a.norm) x[u][j] = ld_stream(reinterpret_cast<const T*>(sd.x) + r * sd.x_ld + at);
+                            if (BWD) y[u][j] = ld_stream(reinterpret_cast<const T*>(sd.dy) + r * sd.dy_ld + at);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int h = b + i + u;
+                    f2r f[L::NV][L::NP], g[L::NV][L::NP];
+                    f2r ss = kPairZero, gs = kPairZero;
+#pragma unroll
+                    for (int j = 0; j < L::NV; ++j) {
+                        Io<T>::unpackp(x[u][j], f[j]);
+                        Io<T>::unpackp(w[s][j], g[j]);
+                        if (BWD) {
+                            f2r dy[L::NP];
+                            Io<T>::unpackp(y[u][j], dy);
+#pragma unroll
+                            for (int p = 0; p < L::NP; ++p) {
+                                dy[p] = turn(dy[p], c[j][p], -sn[j][p]);
+                                g[j][p] = p_mul(g[j][p], dy[p]);
+                                gs = p_fma(g[j][p], f[j][p], gs);
+                            }
+#pragma unroll
+                            for (int p = 0; p < L::NP; ++p) ss = p_fma(f[j][p], f[j][p], ss);
+                        } else {
+#pragma unroll
+                            for (int p = 0; p < L::NP; ++p) ss = p_fma(f[j][p], f[j][p], ss);
+                        }
+                    }
+                    float rstd = 1.0f;
+                    if (a.norm) rstd = __frsqrt_rn(fmaf(group_sum<GL>(p_hsum(ss)), inv_d, a.eps));
+                    const f2r rs = p_splat(rstd);
+                    if constexpr (!BWD) {
+#pragma unroll
+                        for (int j = 0; j < L::NV; ++j) {
+                            f2r o[L::NP];
+#pragma unroll
+                            for (int p = 0; p < L::NP; ++p)
+                                o[p] = turn(a.norm ? p_mul(p_mul(f[j][p], rs), g[j][p]) : f[j][p], c[j][p], sn[j][p]);
+                            if (live && h < e && on[j] && ADALN_IN_HEADS(r < a.R && h < sd.heads))
+                                st_vec(reinterpret_cast<T*>(sd.out) + r * sd.out_ld + (int64_t)h * a.d +
+                                           (lane + j * GL) * L::VE,
+                                       Io<T>::packp(o));
+                        }
+                    } else {
+                        float m = 0.0f;
+                        if (a.norm) m = group_sum<GL>(p_hsum(gs)) * rstd * inv_d;
+                        const f2r nm = p_splat(-m);
+#pragma unroll
+                        for (int j = 0; j < L::NV; ++j) {
+                            f2r o[L::NP], dy[L::NP];
+                            Io<T>::unpackp(y[u][j], dy);
+#pragma unroll
+                            for (int p = 0; p < L::NP; ++p) {
+                                const f2r xhat = p_mul(f[j][p], rs);
+                                o[p] = g[j][p];
+                                if (a.norm) {
+                                    dw[s][j][p] = p_fma(turn(dy[p], c[j][p], -sn[j][p]), xhat, dw[s][j][p]);
+                                    o[p] = p_mul(rs, p_fma(xhat, nm, g[j][p]));
+                                }
+                            }
+                            if (live && h < e && on[j] && ADALN_IN_HEADS(r < a.R && h < sd.heads))
+                                st_vec(reinterpret_cast<T*>(sd.out) + r * sd.out_ld + (int64_t)h * a.d +
+                                           (lane + j * GL) * L::VE,
+                                       Io<T>::packp(o));
+                        }
+                    }
+                }
+            }
+        };
+        const int Hq = a.side[0].heads, h1 = min(h0 + a.chunk, Hq + a.side[1].heads);
+        heads(0, h0, min(h1, Hq));
+        heads(1, max(h0, Hq) - Hq, h1 - Hq);
+    }
+
+    if constexpr (BWD) {
+        if (a.partials) {
+            // The groups' sums, added in the groups' order.
+            __shared__ float red[2 * 8 * kRopeThreads];
+            const int n = 8 * GL;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                for (int j = 0; j < L::NV; ++j) {
+#pragma unroll
+                    for (int p = 0; p < L::NP; ++p)
+                        *reinterpret_cast<float2*>(red + (s * GROUPS + group) * n + (lane + j * GL) * L::VE + 2 * p) =
+                            p_get(dw[s][j][p]);
+                }
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < 2 * a.d; i += kRopeThreads) {
+                const int s = i >= a.d, col = i - s * a.d;
+                float sum = 0.0f;
+                for (int q = 0; q < GROUPS; ++q) sum += red[(s * GROUPS + q) * n + col];
+                a.partials[(int64_t)blockIdx.x * 2 * a.d + i] = sum;
+            }
+        }
+        publish_status(0, a.status, a.header);
+    }
+}
+
+// Columns of the partials, 32 a CTA: 32 threads a column take every 32nd row each, then add up in a
+// fixed order.
+__global__ void __launch_bounds__(1024) rope_reduce_kernel(const RopeReduceArgs a) {
+    pdl_begin();
+    __shared__ float red[32][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + x;
+    float sum = 0.0f;
+    if (col < 2 * a.d) {
+#pragma unroll 4
+        for (int64_t g = y; g < a.G; g += 32) sum += a.partials[g * 2 * a.d + col];
+    }
+    red[y][x] = sum;
+    __syncthreads();
+    float v[1] = {red[x][y]};
+    warp_sum(v);
+    const int out = blockIdx.x * 32 + y;
+    if (x == 0 && out < 2 * a.d) {
+        const int s = out >= a.d;
+        if (a.dw[s]) a.dw[s][out - s * a.d] = v[0];
+    }
+}
+
+namespace {
+
+template <typename T, bool BWD>
+const void* rope_fn(int lanes) {
+    switch (lanes) {
+        case 1: return reinterpret_cast<const void*>(&rope_kernel<T, 1, BWD>);
+        case 2: return reinterpret_cast<const void*>(&rope_kernel<T, 2, BWD>);
+        case 4: return reinterpret_cast<const void*>(&rope_kernel<T, 4, BWD>);
+        case 8: return reinterpret_cast<const void*>(&rope_kernel<T, 8, BWD>);
+        case 16: return reinterpret_cast<const void*>(&rope_kernel<T, 16, BWD>);
+        default: return reinterpret_cast<const void*>(&rope_kernel<T, 32, BWD>);
+    }
+}
+
+const void* rope_fn(int dtype, int d, bool bwd) {
+    const int lanes = rope_lanes(d);
+    if (dtype == 0) return bwd ? rope_fn<float, true>(lanes) : rope_fn<float, false>(lanes);
+    return bwd ? rope_fn<__nv_bfloat16, true>(lanes) : rope_fn<__nv_bfloat16, false>(lanes);
+}
+
+}  // namespace
+
+cudaError_t rope_blocks_per_sm(int dtype, int d, bool bwd, int* out) {
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, rope_fn(dtype, d, bwd), kRopeThreads, 0);
+}
+
+cudaError_t launch_rope(const RopeArgs& args, int dtype, bool bwd, int64_t G, cudaStream_t stream) {
+    RopeArgs a = args;
+    void* params[] = {&a};
+    return launch_dependent(rope_fn(dtype, a.d, bwd), dim3((unsigned)G), dim3(kRopeThreads), params, 0, stream);
+}
+
+cudaError_t launch_rope_reduce(const RopeReduceArgs& args, cudaStream_t stream) {
+    RopeReduceArgs a = args;
+    void* params[] = {&a};
+    return launch_dependent(reinterpret_cast<const void*>(&rope_reduce_kernel), dim3((unsigned)((2 * a.d + 31) / 32)),
+                            dim3(1024), params, 0, stream);
+}
+
+cudaError_t debug_word_rope(uint32_t* out, bool reset) { return debug_word(out, reset); }
+
+}  // namespace adaln

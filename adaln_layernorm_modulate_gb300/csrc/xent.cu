@@ -40,17 +40,9 @@ constexpr int kGemmStages = 5;
 constexpr uint32_t kOutBytes = 32 * 128;  // an epilogue warp's rows on their way out
 constexpr size_t kGemmSmem = 1024 + (size_t)kGemmStages * kStageBytes + (size_t)kEpiWarps * kOutBytes;
 constexpr uint32_t kMnBlock = 64 * kTileK * 2;  // 64 m of all the tile's k (MN-major operands)
-constexpr float kLog2e = 1.4426950408889634f;
 
 #define ADALN_IN_LOSS(cond) ADALN_IN(::adaln::kDbgLoss, cond)
 
-__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
-// 2^x, results below 2^-126 as 0.
-__device__ __forceinline__ float exp2_ftz(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // The epilogue warps' own barrier; true if `ok` is, in all of them.
 __device__ __forceinline__ bool epilogue_all(bool ok) {
     uint32_t r;
@@ -1006,18 +998,7 @@ cudaError_t allow_gemm_smem(const void* fn, int which) {
 // boxes of 128 bytes of a row by `box_rows` rows, 128-byte swizzle.
 bool tile_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows,
               bool f32 = false) {
-    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static const Encode encode = [] {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult res;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &res) !=
-                cudaSuccess ||
-            res != cudaDriverEntryPointSuccess)
-            fn = nullptr;
-        return reinterpret_cast<Encode>(fn);
-    }();
+    const TensorMapEncode encode = tensor_map_encode();
     if (!encode) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)ld * (f32 ? 4 : 2)};

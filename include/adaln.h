@@ -287,6 +287,83 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
                           int64_t D, int64_t ignore_index, void* workspace, size_t workspace_bytes,
                           adaln_dtype dtype, cudaStream_t stream);
 
+/* ---- Head norms with rotation by positions -----------------------------------------------
+ * Queries and keys on their way from a projection into attention: an RMS norm of each head, and the
+ * rotation of its pairs of neighbouring elements by angles that follow from the row's positions, in
+ * one pass over both.
+ *     xhat = x / sqrt(mean_d(x^2) + eps),  y = xhat * weight                (norm != 0; else y = x)
+ *     out[2i] = y[2i] cos t - y[2i+1] sin t,  out[2i+1] = y[2i] sin t + y[2i+1] cos t
+ *     t = pos[r, a] * theta^(-2j / axes[a])     for the pair j = 0 .. axes[a] / 2 - 1 of axis a
+ * and, with dy the outputs' gradient turned back by t,
+ *     dweight = sum over rows and heads of dy * xhat,  dx = rstd (g - xhat mean_d(g xhat)), g = dy * weight
+ *
+ * q [R, Hq, d] and k [R, Hk, d], d contiguous, heads d apart, rows *_ld elements apart (so that they may
+ * be parts of a joint projection's rows); outputs and gradients likewise, each with a row distance of
+ * its own. 8 <= d <= 256, d % 8 == 0; ADALN_F32 or ADALN_BF16, fp32 arithmetic, one rounding at the end.
+ * Row distances are multiples of 8 and at least H * d; pointers are 16-byte aligned (pos and the weights'
+ * gradients 4). Hq or Hk may be 0 (its pointers are not looked at): queries and keys with positions of
+ * their own are two calls.
+ *   - q_weight, k_weight [d], in `dtype`, each may be null (ones); without a norm both must be.
+ *   - pos [R, naxes] (device int32), any values; null: no rotation. axes[naxes] (host, at most 8): the even
+ *     widths of the axes, side by side from element 0; a head's elements behind them are not
+ *     rotated. theta >= 1. Angles are exact to 2^-31 of a turn at any position.
+ *   - dq_weight, dk_weight [d] fp32, overwritten; each may be null (not wanted). Without a norm q and k
+ *     of the backward are not looked at.
+ * R = 0 is valid (zero weight gradients). One launch forward, two backward (one without weight
+ * gradients); sums are added in a fixed order. */
+int adaln_qk_norm_rope_fwd(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                           const int32_t* pos, void* q_out, void* k_out, int64_t R, int32_t Hq, int32_t Hk,
+                           int32_t d, int64_t q_ld, int64_t k_ld, int64_t q_out_ld, int64_t k_out_ld,
+                           const int32_t* axes, int32_t naxes, double theta, float eps, int norm,
+                           adaln_dtype dtype, cudaStream_t stream);
+size_t adaln_qk_norm_rope_bwd_workspace_size(int64_t R, int32_t Hq, int32_t Hk, int32_t d, adaln_dtype dtype);
+int adaln_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                           const void* q_weight, const void* k_weight, const int32_t* pos, void* dq, void* dk,
+                           float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes, int64_t R,
+                           int32_t Hq, int32_t Hk, int32_t d, int64_t dq_out_ld, int64_t dk_out_ld, int64_t q_ld,
+                           int64_t k_ld, int64_t dq_ld, int64_t dk_ld, const int32_t* axes, int32_t naxes,
+                           double theta, float eps, int norm, adaln_dtype dtype, cudaStream_t stream);
+
+/* ---- Attention over packed sequences -----------------------------------------------------
+ * Softmax attention of every segment's queries over the same segment's keys, without the scores:
+ *     z = scale q k^T,  lse = log sum_j exp(z_j),  p = exp(z - lse),  o = p v
+ *     dv = p^T dout,  dz = p (dout v^T - rowsum(dout o)),  dq = scale dz k,  dk = scale dz^T q
+ * q, o, dout, dq [Rq, Hq, d]; k, v, dk, dv [Rk, Hk, d], d contiguous, heads d apart, rows *_ld elements
+ * apart (parts of a joint projection's rows go as they are); lse [Hq, Rq] fp32. Heads are grouped: query
+ * head h meets key head h / (Hq / Hk), and dk, dv are sums over the group.
+ *   - cu_q, cu_k [nseg + 1] (device int32, as cu_seqlens everywhere): segment s has the queries
+ *     cu_q[s] .. and the keys cu_k[s] ..; both tables may be the same. A null table: nseg segments of
+ *     Rq / nseg (Rk / nseg) rows. Lengths may be 0 and differ between the two sides.
+ *   - causal != 0: query i of a segment of n queries and m keys sees the keys j <= i + m - n (the last
+ *     query sees all).
+ *   - A query that sees no key has o = 0, lse = -inf and dq = 0, and adds nothing to dk and dv.
+ *   - scale > 0.
+ * bf16 only (ADALN_F32 is ADALN_ERR_UNSUPPORTED: the products run on the tensor cores); 8 <= d <= 128,
+ * d % 8 == 0; Hq a multiple of Hk; Rq, Rk, nseg <= 2^30. Row distances are multiples of 8 and at least
+ * H * d; pointers 16-byte aligned (lse and the tables 4). Products accumulate in fp32; maxima, sums and lse
+ * are fp32; p and dz are rounded to bf16 as operands of the next product; o, dq, dk and dv once at
+ * the end. What lies behind a segment's last row reaches nothing of it, NaN included; NaN or infinity in a
+ * key or value reaches the rows of its own segment (masked ones too). Results are bitwise reproducible; a
+ * segment's may differ in the last bits with what it is packed with (the tiles follow the
+ * call's sizes).
+ * The backward takes the forward's o and lse. dq may be null, or dk and dv both (not wanted).
+ * Malformed tables are recorded (ADALN_ERR_BAD_SEQLENS in adaln_read_status) and nothing is computed:
+ * outputs stay as they were. Two or three launches forward, two to four backward. */
+size_t adaln_attention_fwd_workspace_size(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d,
+                                          adaln_dtype dtype);
+int adaln_attention_fwd(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_q,
+                        const int32_t* cu_k, int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d,
+                        int64_t q_ld, int64_t k_ld, int64_t v_ld, int64_t o_ld, float scale, int causal,
+                        void* workspace, size_t workspace_bytes, adaln_dtype dtype, cudaStream_t stream);
+size_t adaln_attention_bwd_workspace_size(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d,
+                                          adaln_dtype dtype);
+int adaln_attention_bwd(const void* dout, const void* q, const void* k, const void* v, const void* o, const float* lse,
+                        void* dq, void* dk, void* dv, const int32_t* cu_q, const int32_t* cu_k, int64_t nseg,
+                        int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d, int64_t dout_ld, int64_t q_ld,
+                        int64_t k_ld, int64_t v_ld, int64_t o_ld, int64_t dq_ld, int64_t dk_ld, int64_t dv_ld,
+                        float scale, int causal, void* workspace, size_t workspace_bytes, adaln_dtype dtype,
+                        cudaStream_t stream);
+
 /* ---- Row sharding across ranks ----------------------------------------------------------
  * A batch can be split into contiguous, segment-aligned row shards, one per rank (the pages
  * train on 8- and 16-GPU clusters, AdaptiveLoad technical summary sections 2.A and 4). The
@@ -320,6 +397,8 @@ int adaln_sum_ranks(const float* parts, float* out, int32_t world, int64_t n, cu
 #define ADALN_DEBUG_RANKS    128u /* adaln_sum_ranks: [0, n) of each rank's row              */
 #define ADALN_DEBUG_STATUS   256u /* workspace status words                                   */
 #define ADALN_DEBUG_LOSS     512u /* vocabulary loss: rows, packed rows, partials, gradients  */
+#define ADALN_DEBUG_HEADS    1024u /* head norm and rotation: rows, heads, positions          */
+#define ADALN_DEBUG_ATTN     2048u /* attention: rows, heads, work items, partial results     */
 int adaln_debug_read(uint32_t* word, int reset);
 
 /* Dual-constraint bucket size, AdaptiveLoad technical summary section 2.A:
