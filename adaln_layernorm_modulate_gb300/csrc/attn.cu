@@ -663,14 +663,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     using S = AttnShape<DP>;
     constexpr int ST = S::kStages;
     extern __shared__ uint4 dyn[];
-    __shared__ __align__(8) uint64_t bars[2 * ST + 11];
+    __shared__ __align__(8) uint64_t bars[2 * ST + 12];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t qt = (smem_addr(dyn) + 1023u) & ~1023u, ring = qt + 2 * S::kTile;
     const uint32_t full = smem_addr(bars), empty = full + 8 * ST, qfull = empty + 8 * ST, qempty = qfull + 8;
     const uint32_t sfull = qempty + 8, pfull = sfull + 16, pfree = pfull + 8, dsfull = pfree + 8;
-    const uint32_t done = dsfull + 8, freed = done + 8, tail = freed + 8, drain = tail + 8;
+    const uint32_t done = dsfull + 16, freed = done + 8, tail = freed + 8, drain = tail + 8;
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(full + 8 * i, 1);
@@ -682,7 +682,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         mbar_init(sfull + 8, 1);
         mbar_init(pfull, 1);
         mbar_init(pfree, 8);
+        // Two: a warp may be through a step before another one has written its dz of the step before (dp
+        // of a step needs only that the last dp has been read), but not two.
         mbar_init(dsfull, 8);
+        mbar_init(dsfull + 8, 8);
         mbar_init(done, 1);
         mbar_init(freed, 8);
         mbar_init(tail, 1);
@@ -806,7 +809,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
                     dprobs(j + 1);
                 }
                 if (j == 0 && laps > 0 && !wait(freed, laps - 1)) break;
-                if (!wait(dsfull, steps + j)) break;
+                if (!wait(dsfull + 8 * ((steps + j) & 1u), (steps + j) >> 1)) break;
                 tc_fence_after();
                 if (elect_lane()) {
                     const uint32_t z = tmem + 128 * ((steps + j) & 1u);
@@ -881,7 +884,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
                 tmem_st32(z, w);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(dsfull);
+                if (lane == 0) mbar_arrive(dsfull + 8 * b);
             }
             if (!live) break;
             __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.dx) + at * a.dx_ld + (int64_t)head * a.d;

@@ -453,6 +453,30 @@ def test_repeat_side_stream_and_graph_replay(lens_k):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_calls_back_to_back(d):
+    # Many steps a CTA, kernels queued behind each other: warps run apart as far as the barriers let them.
+    i = inputs([9000, 3000], [500, 260], 8, 4, d, seed=15)
+    want = call(i, pad=0)
+    (Rq, Hq, _), (Rk, Hk, _) = i["q"].shape, i["k"].shape
+    sizes = (2, Rq, Rk, Hq, Hk, d)
+    nb = A.adaln_attention_bwd_workspace_size(*sizes, 1)
+    runs = []
+    for _ in range(12):
+        out = {n: torch.empty_like(want[n]) for n in ("dq", "dk", "dv")}
+        ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+        runs.append((out, ws))
+    torch.cuda.synchronize()
+    lq, lk = Hq * d, Hk * d
+    for out, ws in runs:
+        A.adaln_attention_bwd(i["dout"], i["q"], i["k"], i["v"], want["o"], want["lse"], out["dq"], out["dk"], out["dv"],
+                              i["cu_q"], i["cu_k"], *sizes, lq, lq, lk, lk, lq, lq, lk, lk, d ** -0.5, False, ws, nb)
+    for out, ws in runs:
+        assert A.adaln_read_status(ws) == 0
+        assert all(torch.equal(out[n], want[n]) for n in out)
+
+
+@pytest.mark.gpu
 def test_workspaces_hold_fewer_rows_too():
     for Hq, nseg in ((1, 1), (3, 1), (12, 4), (40, 2)):
         for size in (A.adaln_attention_fwd_workspace_size, A.adaln_attention_bwd_workspace_size):
