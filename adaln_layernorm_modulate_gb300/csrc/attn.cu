@@ -383,7 +383,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
             issued.mma = true;
             for (int i = 0; i < 2; ++i)
                 if (t1[i] > t0) scores(i, used);
-            if (elect_lane()) mma_commit1(empty + 8 * stage(used));
+            if (elect_lane()) {
+                mma_commit1(empty + 8 * stage(used));
+                if (end == t0 + 1) mma_commit1(qempty);
+            }
             for (int t = t0; t < end; ++t, used += 2) {
                 const bool more = t + 1 < end;
                 if (more && !wait(full + 8 * stage(used + 2), (used + 2) / ST)) break;
@@ -402,13 +405,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                     if (t + 1 < t1[i]) scores(i, used + 2);
                 }
                 if (!live) break;
+                if (t + 2 == end && elect_lane()) mma_commit1(qempty);  // behind the unit's last scores
                 if (elect_lane()) {
                     mma_commit1(empty + 8 * stage(used + 1));
                     if (more) mma_commit1(empty + 8 * stage(used + 2));
                 }
             }
             if (!live) break;
-            if (elect_lane()) mma_commit1(qempty);
             ++pairs;
             for (int i = 0; i < 2; ++i)
                 if (t1[i] > t0) ++nu[i];
@@ -661,7 +664,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
                                                                const __grid_constant__ CUtensorMap mv,
                                                                const AttnBwdArgs a) {
     using S = AttnShape<DP>;
-    constexpr int ST = S::kStages;
+    // Keys are held from their scores to dq, two steps on; values from dp of their step alone. With a ring
+    // for both, a values' tile would wait for the keys three tiles before it.
+    constexpr int KS = DP == 128 ? 3 : 4, VS = DP == 128 ? 2 : 4, ST = KS + VS;
+    static_assert(ST == S::kStages, "the rings fill the shared memory");
     extern __shared__ uint4 dyn[];
     __shared__ __align__(8) uint64_t bars[2 * ST + 12];
     __shared__ uint32_t tmem_base;
@@ -717,6 +723,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
 
     if (role == kLoadWarp) {
         bool live = true;
+        uint32_t steps = 0;
         fence_async_proxy();
         for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
             const int64_t u = attn_unit(lap);
@@ -732,11 +739,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
             }
             ++issued.pair;
             const int kv = head / a.group;
-            for (int t = 0; t < n && live; ++t) {
+            for (int t = 0; t < n && live; ++t, ++steps) {
                 const int row = it.other0 + t * kAttnTile, left = it.others - t * kAttnTile;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const uint32_t s = issued.ring % ST, l = issued.ring / ST;
+                    const uint32_t s = x ? KS + steps % VS : steps % KS, l = x ? steps / VS : steps / KS;
                     live = __all_sync(0xFFFFFFFFu, l == 0 || mbar_wait_bounded(empty + 8 * s, (l - 1) & 1u, &abort_flag));
                     if (!live) break;
                     const uint32_t dst = ring + s * S::kTile;
@@ -763,26 +770,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         }
     } else if (role == kMmaWarp) {
         bool live = true;
-        uint32_t used = 0, laps = 0, steps = 0;  // ring tiles; units; steps
+        uint32_t laps = 0, steps = 0;  // units, steps
         auto wait = [&](uint32_t bar, uint32_t parity) {
             live = live && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity & 1u, &abort_flag));
             return live;
         };
-        auto tile = [&](uint32_t x) { return ring + x % ST * S::kTile; };
-        auto loaded = [&](uint32_t x) { return wait(full + 8 * (x % ST), x / ST); };
+        // Places of the keys and the values of step j of this unit, and waits for them.
+        auto kslot = [&](int j) { return (steps + j) % KS; };
+        auto vslot = [&](int j) { return KS + (steps + j) % VS; };
+        auto keys = [&](int j) { return wait(full + 8 * kslot(j), (steps + j) / KS); };
+        auto values = [&](int j) { return wait(full + 8 * vslot(j), (steps + j) / VS); };
         // z of step j (of this unit), dp of step j.
         auto scores = [&](int j) {
             const uint32_t b = (steps + j) & 1u;
             if (elect_lane()) {
-                mma_rows<DP>(tmem + 128 * b, qt, tile(used + 2 * j), a.d);
+                mma_rows<DP>(tmem + 128 * b, qt, ring + kslot(j) * S::kTile, a.d);
                 mma_commit1(sfull + 8 * b);
             }
         };
         auto dprobs = [&](int j) {
             if (elect_lane()) {
-                mma_rows<DP>(dp_tmem, qt + S::kTile, tile(used + 2 * j + 1), a.d);
+                mma_rows<DP>(dp_tmem, qt + S::kTile, ring + vslot(j) * S::kTile, a.d);
                 mma_commit1(pfull);
-                mma_commit1(empty + 8 * ((used + 2 * j + 1) % ST));
+                mma_commit1(empty + 8 * vslot(j));
             }
         };
         for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
@@ -790,21 +800,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
             if (u >= units) continue;
             decode(u);
             if (n == 0) continue;
-            if (!wait(qfull, laps) || !loaded(used)) break;
+            if (!wait(qfull, laps) || !keys(0)) break;
             tc_fence_after();
             issued.mma = true;
             scores(0);
-            if (!loaded(used + 1)) break;
+            if (!values(0)) break;
             tc_fence_after();
             dprobs(0);
             if (n > 1) {
-                if (!loaded(used + 2)) break;
+                if (!keys(1)) break;
                 tc_fence_after();
                 scores(1);
             }
             for (int j = 0; j < n; ++j) {
                 if (j + 1 < n) {
-                    if (!loaded(used + 2 * j + 3) || !wait(pfree, steps + j)) break;
+                    if (!values(j + 1) || !wait(pfree, steps + j)) break;
                     tc_fence_after();
                     dprobs(j + 1);
                 }
@@ -813,11 +823,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
                 tc_fence_after();
                 if (elect_lane()) {
                     const uint32_t z = tmem + 128 * ((steps + j) & 1u);
-                    mma_cols(acc, z, z + 64, tile(used + 2 * j), a.d, j > 0);
-                    mma_commit1(empty + 8 * ((used + 2 * j) % ST));
+                    mma_cols(acc, z, z + 64, ring + kslot(j) * S::kTile, a.d, j > 0);
+                    mma_commit1(empty + 8 * kslot(j));
                 }
                 if (j + 2 < n) {
-                    if (!loaded(used + 2 * j + 4)) break;
+                    if (!keys(j + 2)) break;
                     tc_fence_after();
                     scores(j + 2);
                 }
@@ -827,7 +837,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
                 mma_commit1(done);
                 mma_commit1(qempty);
             }
-            used += 2 * n;
             steps += n;
             ++laps;
         }
@@ -915,8 +924,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         if (warp == kLoadWarp && lane == 0) {
             if (issued.pair) mbar_wait_bounded(qfull, (issued.pair - 1) & 1u, &never);
             if (issued.tail) mbar_wait_bounded(tail, (issued.tail - 1) & 1u, &never);
-            for (uint32_t s = 0; s < min(issued.ring, (uint32_t)ST); ++s)
-                mbar_wait_bounded(full + 8 * s, ((issued.ring - 1 - s) / ST) & 1u, &never);
+            // ring counts tiles of both rings, the keys' first.
+            const uint32_t ks = (issued.ring + 1) / 2, vs = issued.ring / 2;
+            for (uint32_t s = 0; s < min(ks, (uint32_t)KS); ++s)
+                mbar_wait_bounded(full + 8 * s, ((ks - 1 - s) / KS) & 1u, &never);
+            for (uint32_t s = 0; s < min(vs, (uint32_t)VS); ++s)
+                mbar_wait_bounded(full + 8 * (KS + s), ((vs - 1 - s) / VS) & 1u, &never);
         }
         if (warp == kMmaWarp && issued.mma && elect_lane()) {
             mma_commit1(drain);
