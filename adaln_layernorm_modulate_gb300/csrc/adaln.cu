@@ -1367,14 +1367,14 @@ int adaln_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q
 
 namespace {
 
-constexpr int kAttnMaxSplits = 64;
-
 int attn_check(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d, adaln_dtype dtype) {
     if (dtype != ADALN_F32 && dtype != ADALN_BF16) return ADALN_ERR_INVALID_ARG;
     if (d < 8 || d > kAttnMaxD || d % 8 != 0 || dtype != ADALN_BF16) return ADALN_ERR_UNSUPPORTED;
     if (nseg < 0 || Rq < 0 || Rk < 0 || nseg > kAttnMaxRows || Rq > kAttnMaxRows || Rk > kAttnMaxRows)
         return ADALN_ERR_INVALID_ARG;
     if (Hq < 1 || Hk < 1 || Hq > 16384 || Hq % Hk != 0) return ADALN_ERR_INVALID_ARG;
+    // Work items are counted in 32 bits, times the heads.
+    if ((std::max(Rq, Rk) / kAttnTile + std::min(nseg, std::max(Rq, Rk))) * Hq > INT32_MAX) return ADALN_ERR_INVALID_ARG;
     return ADALN_OK;
 }
 
@@ -1389,23 +1389,16 @@ int attn_tables(const int32_t* cu_q, const int32_t* cu_k, int64_t nseg, int64_t 
 }
 
 struct AttnPlan {
-    int tile;                 // forward: queries a work item
-    int64_t most_q, most_k;   // work items
-    int splits;               // forward: parts of the keys
-    size_t count, items_q, items_k, part, ml, lse2, delta, bytes;
+    AttnList list[2];         // offsets in place of pointers
+    size_t items[2], count, segs[2], cursors[2], part[2], ml, lse2, delta, bytes;
+    int slot_rows[2];
+    bool pieces[2];           // units may be cut
 };
 
-AttnPlan attn_plan(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t d, bool bwd, int sms) {
+AttnPlan attn_plan(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d, bool bwd, int sms) {
     AttnPlan p{};
     auto items = [&](int64_t R, int tile) { return R / tile + std::min(nseg, R); };
-    p.tile = 2 * kAttnTile;
-    if (bwd || items(Rq, p.tile) * Hq < sms) p.tile = kAttnTile;
-    p.most_q = items(Rq, p.tile);
-    p.most_k = items(Rk, kAttnTile);
-    p.splits = 1;
-    const int64_t units = p.most_q * Hq;
-    if (!bwd && units > 0 && 2 * units <= sms)
-        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({sms / units, Rk / (4 * kAttnTile), kAttnMaxSplits}));
+    auto tiles = [](int64_t R) { return (R + kAttnTile - 1) / kAttnTile; };
     size_t at = kPartialsOffset;
     auto take = [&](size_t bytes) {
         const size_t o = at;
@@ -1413,17 +1406,34 @@ AttnPlan attn_plan(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t d, 
         return o;
     };
     p.count = take(2 * sizeof(int32_t));
-    p.items_q = take((size_t)items(Rq, kAttnTile) * sizeof(AttnItem));
+    for (int x = 0; x < (bwd ? 2 : 1); ++x) {
+        const int64_t R = x ? Rk : Rq;
+        const int heads = x ? Hk : Hq, group = x ? Hq / Hk : 1;
+        AttnList& l = p.list[x];
+        // Forward: two tiles of queries an entry, which share keys and values in shared memory and take
+        // turns at the tensor cores; one where that leaves SMs without a unit.
+        l.tile = kAttnTile;
+        if (!bwd && items(R, 2 * kAttnTile) * heads >= sms) l.tile = 2 * kAttnTile;
+        l.most = items(R, l.tile);
+        l.heads = heads;
+        l.group = group;
+        // A unit has at most this many steps, and is cut in pieces of no fewer than kAttnMinPiece.
+        const int64_t steps = tiles(x ? Rq : Rk) * group;
+        p.pieces[x] = steps >= 2 * kAttnMinPiece;
+        l.ctas = (int)std::max<int64_t>(
+            1, std::min<int64_t>(sms, l.most * heads * std::max<int64_t>(1, steps / kAttnMinPiece)));
+        p.items[x] = take((size_t)items(R, kAttnTile) * sizeof(AttnItem));
+        p.segs[x] = take((size_t)nseg * sizeof(longlong2));
+        p.cursors[x] = take((size_t)(sms + 1) * sizeof(AttnCursor));
+        // Two pieces a CTA; sized for calls of fewer rows too.
+        p.slot_rows[x] = (int)std::min<int64_t>(R, bwd ? kAttnTile : 2 * kAttnTile);
+        const size_t rows = 2 * (size_t)sms * (size_t)p.slot_rows[x];
+        p.part[x] = take(rows * (size_t)d * (x ? 2 : 1) * sizeof(float));
+        if (!bwd) p.ml = take(rows * sizeof(float2));
+    }
     if (bwd) {
-        p.items_k = take((size_t)p.most_k * sizeof(AttnItem));
         p.lse2 = take((size_t)Rq * Hq * sizeof(float));
         p.delta = take((size_t)Rq * Hq * sizeof(float));
-    } else {
-        // With splits a row has most_q * Hq * splits <= sms units, each of at most a tile of rows; the bound
-        // holds for calls of fewer rows too.
-        const size_t rows = (size_t)sms * (size_t)std::min<int64_t>(kAttnTile, Rq);
-        p.part = take(rows * (size_t)d * sizeof(float));
-        p.ml = take(rows * sizeof(float2));
     }
     p.bytes = at;
     return p;
@@ -1432,13 +1442,13 @@ AttnPlan attn_plan(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t d, 
 AttnPlanArgs attn_plan_args(const AttnTables& t, const AttnPlan& p, void* ws, bool bwd) {
     AttnPlanArgs a{};
     a.t = t;
-    a.items[0] = at<AttnItem>(ws, p.items_q);
-    a.items[1] = bwd ? at<AttnItem>(ws, p.items_k) : nullptr;
-    a.count = at<int32_t>(ws, p.count);
-    a.most[0] = p.most_q;
-    a.most[1] = p.most_k;
-    a.tile[0] = p.tile;
-    a.tile[1] = kAttnTile;
+    for (int x = 0; x < (bwd ? 2 : 1); ++x) {
+        a.list[x] = p.list[x];
+        a.list[x].items = at<AttnItem>(ws, p.items[x]);
+        a.list[x].count = at<int32_t>(ws, p.count) + x;
+        a.list[x].segs = at<longlong2>(ws, p.segs[x]);
+        a.list[x].cursors = at<AttnCursor>(ws, p.cursors[x]);
+    }
     a.status = at<uint32_t>(ws, kHeaderBytes);
     a.header = at<WsHeader>(ws, 0);
     return a;
@@ -1453,7 +1463,7 @@ size_t adaln_attention_fwd_workspace_size(int64_t nseg, int64_t Rq, int64_t Rk, 
     int dev = 0;
     if (attn_check(nseg, Rq, Rk, Hq, Hk, d, dtype)) return 0;
     const int sms = current_sms(&dev);
-    return sms <= 0 ? 0 : attn_plan(nseg, Rq, Rk, Hq, d, false, sms).bytes;
+    return sms <= 0 ? 0 : attn_plan(nseg, Rq, Rk, Hq, Hk, d, false, sms).bytes;
 }
 
 int adaln_attention_fwd(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_q,
@@ -1476,32 +1486,40 @@ int adaln_attention_fwd(const void* q, const void* k, const void* v, void* o, fl
     int dev = 0;
     const int sms = current_sms(&dev);
     if (sms <= 0) return ADALN_ERR_CUDA;
-    const AttnPlan p = attn_plan(nseg, Rq, Rk, Hq, d, false, sms);
+    const AttnPlan p = attn_plan(nseg, Rq, Rk, Hq, Hk, d, false, sms);
     if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
     const AttnPlanArgs l = attn_plan_args(t, p, workspace, false);
     if (int rc = launched(launch_attn_plan(l, stream))) return rc;
     if (Rq == 0) return ADALN_OK;
     AttnFwdArgs a{};
-    a.items = l.items[0];
-    a.count = l.count;
+    a.list = l.list[0];
     a.o = o;
     a.lse = lse;
-    a.part = at<float>(workspace, p.part);
+    a.part = at<float>(workspace, p.part[0]);
     a.ml = at<float2>(workspace, p.ml);
     a.status = l.status + 1;
     a.Rq = Rq;
     a.o_ld = o_ld;
-    a.most = p.most_q;
     a.Hq = Hq;
     a.group = Hq / Hk;
     a.d = d;
-    a.splits = p.splits;
+    a.slot_rows = p.slot_rows[0];
     a.scale = scale;
-    if (int rc = launched(launch_attn_fwd(a, {q, Rq, q_ld, Hq}, {k, Rk, k_ld, Hk}, {v, Rk, v_ld, Hk}, sms, stream)))
+    if (int rc = launched(launch_attn_fwd(a, {q, Rq, q_ld, Hq}, {k, Rk, k_ld, Hk}, {v, Rk, v_ld, Hk}, stream)))
         return rc;
-    if (p.splits == 1) return ADALN_OK;
-    const AttnJoinArgs j{a.part, a.ml, o, lse, Rq, o_ld, Hq, d, p.splits, scale, l.status};
-    return launched(launch_attn_join(j, sms, stream));
+    if (!p.pieces[0]) return ADALN_OK;
+    AttnJoinArgs j{};
+    j.list[0] = a.list;
+    j.part[0] = a.part;
+    j.ml = a.ml;
+    j.out[0] = o;
+    j.ld[0] = o_ld;
+    j.lse = lse;
+    j.Rq = Rq;
+    j.d = d;
+    j.slot_rows[0] = a.slot_rows;
+    j.scale = scale;
+    return launched(launch_attn_join(j, false, stream));
 }
 
 size_t adaln_attention_bwd_workspace_size(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d,
@@ -1509,7 +1527,7 @@ size_t adaln_attention_bwd_workspace_size(int64_t nseg, int64_t Rq, int64_t Rk, 
     int dev = 0;
     if (attn_check(nseg, Rq, Rk, Hq, Hk, d, dtype)) return 0;
     const int sms = current_sms(&dev);
-    return sms <= 0 ? 0 : attn_plan(nseg, Rq, Rk, Hq, d, true, sms).bytes;
+    return sms <= 0 ? 0 : attn_plan(nseg, Rq, Rk, Hq, Hk, d, true, sms).bytes;
 }
 
 int adaln_attention_bwd(const void* dout, const void* q, const void* k, const void* v, const void* o, const float* lse,
@@ -1539,7 +1557,7 @@ int adaln_attention_bwd(const void* dout, const void* q, const void* k, const vo
     int dev = 0;
     const int sms = current_sms(&dev);
     if (sms <= 0) return ADALN_ERR_CUDA;
-    const AttnPlan p = attn_plan(nseg, Rq, Rk, Hq, d, true, sms);
+    const AttnPlan p = attn_plan(nseg, Rq, Rk, Hq, Hk, d, true, sms);
     if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
     const AttnPlanArgs l = attn_plan_args(t, p, workspace, true);
     if (int rc = launched(launch_attn_plan(l, stream))) return rc;
@@ -1555,25 +1573,41 @@ int adaln_attention_bwd(const void* dout, const void* q, const void* k, const vo
     a.group = Hq / Hk;
     a.d = d;
     a.scale = scale;
+    AttnJoinArgs j{};
+    j.d = d;
+    j.Rq = Rq;
+    j.scale = scale;
     if (dk && Rk > 0) {
-        a.items = l.items[1];
-        a.count = l.count + 1;
+        a.list = l.list[1];
         a.dx = dk;
         a.dv = dv;
         a.dx_ld = dk_ld;
         a.dv_ld = dv_ld;
-        a.most = p.most_k;
-        if (int rc = launched(launch_attn_dkv(a, rdo, rq, rk, rv, sms, stream))) return rc;
+        a.part = at<float>(workspace, p.part[1]);
+        a.slot_rows = p.slot_rows[1];
+        if (int rc = launched(launch_attn_dkv(a, rdo, rq, rk, rv, stream))) return rc;
+        if (p.pieces[1]) j.list[1] = a.list;
+        j.part[1] = a.part;
+        j.slot_rows[1] = a.slot_rows;
+        j.out[1] = dk;
+        j.dv = dv;
+        j.ld[1] = dk_ld;
+        j.dv_ld = dv_ld;
     }
     if (dq && Rq > 0) {
-        a.items = l.items[0];
-        a.count = l.count;
+        a.list = l.list[0];
         a.dx = dq;
         a.dx_ld = dq_ld;
-        a.most = p.most_q;
-        if (int rc = launched(launch_attn_dq(a, rdo, rq, rk, rv, sms, stream))) return rc;
+        a.part = at<float>(workspace, p.part[0]);
+        a.slot_rows = p.slot_rows[0];
+        if (int rc = launched(launch_attn_dq(a, rdo, rq, rk, rv, stream))) return rc;
+        if (p.pieces[0]) j.list[0] = a.list;
+        j.part[0] = a.part;
+        j.slot_rows[0] = a.slot_rows;
+        j.out[0] = dq;
+        j.ld[0] = dq_ld;
     }
-    return ADALN_OK;
+    return j.list[0].items || j.list[1].items ? launched(launch_attn_join(j, true, stream)) : ADALN_OK;
 }
 
 }  // extern "C"

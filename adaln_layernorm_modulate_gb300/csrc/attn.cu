@@ -51,19 +51,56 @@ __device__ __forceinline__ int64_t attn_start(const int32_t* cu, int64_t s, int6
     return cu ? (int64_t)__ldg(cu + s) : s * (R / nseg);
 }
 
-__device__ __forceinline__ int attn_class(int cost) {
-    if (cost <= 0) return 0;
-    const int c = 1 + (int)(__float_as_uint((float)cost) >> 21) - (127 << 2);
-    return min(c, kAttnClasses - 1);
+// The rows of segment s on both sides.
+struct AttnSegment {
+    int q0, nq, k0, nk;
+};
+
+// Entry `at / tile` of a list's segment, and its steps.
+__device__ __forceinline__ int attn_steps(const AttnTables& t, const AttnList& l, int list, const AttnSegment& g, int at,
+                                          AttnItem* it) {
+    const int len = list ? g.nk : g.nq;
+    it->rows = min(l.tile, len - at);
+    if (list == 0) {
+        it->row0 = g.q0 + at;
+        it->other0 = g.k0;
+        it->others = g.nk;
+        it->shift = t.causal ? at + g.nk - g.nq : g.nk;
+        it->end = g.k0 + g.nk == (int)t.Rk;
+        const int seen = max(0, min(g.nk, it->shift + it->rows));
+        return (seen + kAttnTile - 1) / kAttnTile;
+    }
+    it->row0 = g.k0 + at;
+    it->other0 = g.q0;
+    it->others = g.nq;
+    it->shift = t.causal ? at - g.nk + g.nq : -kAttnTile;
+    it->end = g.q0 + g.nq == (int)t.Rq;
+    const int first = max(0, it->shift) / kAttnTile;  // tiles of queries are counted from the segment's first row
+    return max(0, (g.nq + kAttnTile - 1) / kAttnTile - first) * l.group;
 }
 
-// One CTA a list. Two passes over the tiles: how many of each cost class, then each to its place
-// (any order within a class: nothing that is computed depends on it).
-__global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnPlanArgs a) {
+__device__ __forceinline__ int64_t warp_before(int64_t v, int lane, int64_t* total) {
+    int64_t s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += x;
+    }
+    *total = __shfl_sync(0xFFFFFFFFu, s, 31);
+    return s - v;
+}
+
+// One CTA a list. The entries are in the order of the rows: first what each segment has and costs (a warp
+// a segment, its lanes the tiles), then sums over the segments before it, then the entries, then where
+// each CTA begins. Everything follows from the tables alone, so that pieces, and with them the order of
+// sums, are the same every time.
+__global__ void __launch_bounds__(1024) attn_plan_kernel(const __grid_constant__ AttnPlanArgs a) {
     pdl_begin();
-    __shared__ int bins[kAttnClasses], place[kAttnClasses];
+    __shared__ int64_t sums[2][32];
+    __shared__ int64_t run[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, list = blockIdx.x;
     const AttnTables& t = a.t;
+    const AttnList& l = a.list[list];
     bool bad = false;
     for (int64_t s = tid; s < t.nseg; s += 1024) {
         const int64_t q0 = attn_start(t.cu_q, s, t.nseg, t.Rq), q1 = attn_start(t.cu_q, s + 1, t.nseg, t.Rq);
@@ -73,9 +110,7 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnPlanArgs a) {
     if (tid == 0) {
         if (t.cu_q) bad |= __ldg(t.cu_q) != 0 || (int64_t)__ldg(t.cu_q + t.nseg) != t.Rq;
         if (t.cu_k) bad |= __ldg(t.cu_k) != 0 || (int64_t)__ldg(t.cu_k + t.nseg) != t.Rk;
-        if (t.nseg == 0) bad |= t.Rq != 0 || t.Rk != 0;
     }
-    if (tid < kAttnClasses) bins[tid] = 0;
     const bool any_bad = __syncthreads_or(bad);
     if (tid == 0 && list == 0) {
         a.status[0] = any_bad ? kErrSeqlens : 0u;
@@ -83,80 +118,116 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnPlanArgs a) {
         a.header->magic = kStatusMagic;
         a.header->nwords = 2;
     }
+    if (l.items == nullptr) return;
     if (any_bad) {
-        if (tid == 0) a.count[list] = 0;
+        if (tid == 0) *l.count = 0;
+        for (int c = tid; c <= l.ctas; c += 1024) l.cursors[c] = AttnCursor{0, 0};
         return;
     }
-    const int tile = a.tile[list];
+    // Segments base .. base + 31 of a warp's turn, one at a time with their lanes.
     auto each = [&](auto use) {
         for (int64_t base = 32 * (int64_t)warp; base < t.nseg; base += 1024) {
             const int64_t s = base + lane;
-            int q0 = 0, nq = 0, k0 = 0, nk = 0;
+            AttnSegment g{0, 0, 0, 0};
             if (s < t.nseg) {
-                q0 = (int)attn_start(t.cu_q, s, t.nseg, t.Rq);
-                nq = (int)attn_start(t.cu_q, s + 1, t.nseg, t.Rq) - q0;
-                k0 = (int)attn_start(t.cu_k, s, t.nseg, t.Rk);
-                nk = (int)attn_start(t.cu_k, s + 1, t.nseg, t.Rk) - k0;
+                g.q0 = (int)attn_start(t.cu_q, s, t.nseg, t.Rq);
+                g.nq = (int)attn_start(t.cu_q, s + 1, t.nseg, t.Rq) - g.q0;
+                g.k0 = (int)attn_start(t.cu_k, s, t.nseg, t.Rk);
+                g.nk = (int)attn_start(t.cu_k, s + 1, t.nseg, t.Rk) - g.k0;
             }
             for (int i = 0; i < 32 && base + i < t.nseg; ++i) {
-                const int Q0 = __shfl_sync(0xFFFFFFFFu, q0, i), NQ = __shfl_sync(0xFFFFFFFFu, nq, i);
-                const int K0 = __shfl_sync(0xFFFFFFFFu, k0, i), NK = __shfl_sync(0xFFFFFFFFu, nk, i);
-                const int len = list ? NK : NQ;
-                for (int64_t at = (int64_t)lane * tile; at < len; at += 32 * (int64_t)tile) {
-                    AttnItem it{};
-                    it.rows = min(tile, len - (int)at);
-                    if (list == 0) {
-                        it.row0 = Q0 + (int)at;
-                        it.other0 = K0;
-                        it.others = NK;
-                        it.shift = t.causal ? (int)at + NK - NQ : NK;
-                        it.end = K0 + NK == (int)t.Rk;
-                        const int seen = max(0, min(NK, it.shift + it.rows));
-                        use(it, (seen + kAttnTile - 1) / kAttnTile);
-                    } else {
-                        it.row0 = K0 + (int)at;
-                        it.other0 = Q0;
-                        it.others = NQ;
-                        it.shift = t.causal ? (int)at - NK + NQ : -kAttnTile;
-                        it.end = Q0 + NQ == (int)t.Rq;
-                        use(it, (NQ - min(NQ, max(0, it.shift)) + kAttnTile - 1) / kAttnTile);
-                    }
-                }
+                const AttnSegment one{__shfl_sync(0xFFFFFFFFu, g.q0, i), __shfl_sync(0xFFFFFFFFu, g.nq, i),
+                                      __shfl_sync(0xFFFFFFFFu, g.k0, i), __shfl_sync(0xFFFFFFFFu, g.nk, i)};
+                const int tiles = ((list ? one.nk : one.nq) + l.tile - 1) / l.tile;
+                use(base + i, one, tiles);
             }
         }
     };
-    each([&](const AttnItem&, int cost) { atomicAdd(&bins[attn_class(cost)], 1); });
-    __syncthreads();
-    if (warp == 0) {
-        // Places in descending order of the classes.
-        int v[kAttnClasses / 32], sum = 0;
-#pragma unroll
-        for (int i = 0; i < kAttnClasses / 32; ++i) sum += v[i] = bins[kAttnClasses - 1 - (lane * (kAttnClasses / 32) + i)];
-        int before = sum;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xFFFFFFFFu, before, o);
-            if (lane >= o) before += x;
+    each([&](int64_t s, const AttnSegment& g, int tiles) {
+        int64_t cost = 0, all;
+        for (int i = lane; i < tiles; i += 32) {
+            AttnItem it;
+            cost += attn_steps(t, l, list, g, i * l.tile, &it) + kAttnUnitCost;
         }
-        if (lane == 31) a.count[list] = (int)min((int64_t)before, a.most[list]);
-        before -= sum;
-#pragma unroll
-        for (int i = 0; i < kAttnClasses / 32; ++i) {
-            place[kAttnClasses - 1 - (lane * (kAttnClasses / 32) + i)] = before;
-            before += v[i];
-        }
-    }
-    __syncthreads();
-    each([&](const AttnItem& it, int cost) {
-        const int at = atomicAdd(&place[attn_class(cost)], 1);
-        if (at < a.most[list]) a.items[list][at] = it;
+        warp_before(cost, lane, &all);
+        if (lane == 0) l.segs[s] = make_longlong2(tiles, all);
     });
+    if (tid < 2) run[tid] = 0;
+    __syncthreads();
+    for (int64_t base = 0; base < t.nseg; base += 1024) {
+        const int64_t s = base + tid;
+        const longlong2 v = s < t.nseg ? l.segs[s] : make_longlong2(0, 0);
+        int64_t all[2], before[2] = {warp_before(v.x, lane, &all[0]), warp_before(v.y, lane, &all[1])};
+        if (lane == 0) {
+            sums[0][warp] = all[0];
+            sums[1][warp] = all[1];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            before[x] += run[x];
+            for (int w = 0; w < warp; ++w) before[x] += sums[x][w];
+        }
+        __syncthreads();
+        if (tid == 1023) {
+            run[0] = before[0] + v.x;
+            run[1] = before[1] + v.y;
+        }
+        if (s < t.nseg) l.segs[s] = make_longlong2(before[0], before[1]);
+        __syncthreads();
+    }
+    const int64_t count = min(run[0], l.most), total = run[1];
+    if (tid == 0) *l.count = (int32_t)count;
+    each([&](int64_t s, const AttnSegment& g, int tiles) {
+        const longlong2 before = l.segs[s];
+        int64_t cost = before.y;
+        for (int i0 = 0; i0 < tiles; i0 += 32) {
+            const int i = i0 + lane;
+            AttnItem it{};
+            const int64_t mine = i < tiles ? attn_steps(t, l, list, g, i * l.tile, &it) + kAttnUnitCost : 0;
+            int64_t all;
+            it.before = cost + warp_before(mine, lane, &all);
+            cost += all;
+            const int64_t at = before.x + i;
+            if (i < tiles && at < l.most && ADALN_IN_ATTN(at >= 0)) l.items[at] = it;
+        }
+    });
+    __syncthreads();
+    // CTA c begins at cost c / ctas of all heads' together.
+    const int64_t every = total * l.heads;
+    for (int c = tid; c <= l.ctas; c += 1024) {
+        AttnCursor cur{(int32_t)(count * l.heads), 0};
+        if (c < l.ctas && total > 0) {
+            const int64_t x = every / l.ctas * c + every % l.ctas * c / l.ctas;
+            const int64_t head = x / total, in = x % total;
+            int64_t lo = 0, hi = count - 1;  // the last entry that begins at or before `in`
+            while (lo < hi) {
+                const int64_t mid = (lo + hi + 1) >> 1;
+                if (l.items[mid].before <= in) lo = mid;
+                else hi = mid - 1;
+            }
+            const int64_t end = lo + 1 < count ? l.items[lo + 1].before : total;
+            const int n = (int)(end - l.items[lo].before) - kAttnUnitCost;
+            int tile = (int)(in - l.items[lo].before) - kAttnUnitCost / 2;
+            cur.unit = (int32_t)(head * count + lo);
+            if (tile < kAttnMinPiece) tile = 0;
+            if (tile > 0 && n - tile < kAttnMinPiece) {
+                tile = 0;
+                ++cur.unit;
+            }
+            cur.tile = tile;
+        }
+        l.cursors[c] = cur;
+    }
 }
 
-__device__ __forceinline__ AttnItem attn_item(const AttnItem* items, int64_t i, int64_t most) {
+// The work list is written by the kernel ahead, which this kernel may have been scheduled before: read
+// from L2.
+__device__ __forceinline__ AttnItem attn_item(const AttnList& l, int64_t i) {
     AttnItem it{};
-    if (!ADALN_IN_ATTN(i >= 0 && i < most)) return it;
-    const int4 a = __ldg(reinterpret_cast<const int4*>(items + i));
-    const int2 b = __ldg(reinterpret_cast<const int2*>(items + i) + 2);
+    if (!ADALN_IN_ATTN(i >= 0 && i < l.most)) return it;
+    const int4 a = __ldcg(reinterpret_cast<const int4*>(l.items + i));
+    const int2 b = __ldcg(reinterpret_cast<const int2*>(l.items + i) + 2);
     it.row0 = a.x;
     it.rows = a.y;
     it.other0 = a.z;
@@ -165,12 +236,42 @@ __device__ __forceinline__ AttnItem attn_item(const AttnItem* items, int64_t i, 
     it.end = b.y;
     return it;
 }
-// The k-th unit of this CTA: forth and back over the CTAs, so that the first ones do not get the
-// longest of every lap.
-__device__ __forceinline__ int64_t attn_unit(int64_t lap) {
-    const int64_t G = gridDim.x, b = blockIdx.x;
-    return lap * G + ((lap & 1) ? G - 1 - b : b);
+__device__ __forceinline__ AttnCursor attn_cursor(const AttnList& l, int c) {
+    if (!ADALN_IN_ATTN(c >= 0 && c <= l.ctas)) return AttnCursor{0, 0};
+    const int2 v = __ldcg(reinterpret_cast<const int2*>(l.cursors + c));
+    return AttnCursor{v.x, v.y};
 }
+
+// The units of this CTA, one after another: entry and head, and the steps [t0, t1) of the unit's n that are
+// its own.
+struct AttnWalk {
+    const AttnList& l;
+    AttnCursor from, to;
+    int count, unit;
+    AttnItem it;
+    int head, t0, t1;
+    __device__ __forceinline__ AttnWalk(const AttnList& list) : l(list) {
+        from = attn_cursor(l, blockIdx.x);
+        to = attn_cursor(l, blockIdx.x + 1);
+        count = __ldcg(l.count);
+        unit = from.unit - 1;
+    }
+    __device__ __forceinline__ bool next() {
+        ++unit;
+        if (unit > to.unit || (unit == to.unit && to.tile == 0)) return false;
+        head = unit / count;
+        it = attn_item(l, unit % count);
+        return true;
+    }
+    // With the unit's steps known.
+    __device__ __forceinline__ void steps(int n) {
+        t0 = unit == from.unit ? from.tile : 0;
+        t1 = unit == to.unit ? to.tile : n;
+    }
+    __device__ __forceinline__ bool whole(int n) const { return t0 == 0 && t1 == n; }
+    // Where a piece goes: a CTA has at most one that does not begin its unit and one that does.
+    __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0); }
+};
 
 // ---- operands --------------------------------------------------------------------------------
 template <int DP>
@@ -231,6 +332,13 @@ __device__ __forceinline__ void store_zeros(void* row, int c0, int c1, int d) {
         st_vec(reinterpret_cast<__nv_bfloat16*>(row) + c, make_uint4(0, 0, 0, 0));
 }
 
+// 32 columns of a row to a piece.
+__device__ __forceinline__ void store_piece32(float* row, int col, int d, const float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4)
+        if (col + j < d) *reinterpret_cast<float4*>(row + col + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+}
+
 // What a CTA has issued, for the drain after a timeout: copies and products must not land in memory
 // that has been given back.
 struct AttnIssued {
@@ -283,38 +391,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
     pdl_trigger();  // behind the allocation: a dependent CTA on this SM must not get the columns first
     const uint32_t tmem = tmem_base;
     pdl_wait();
-    const int64_t units = (int64_t)*a.count * a.Hq * a.splits;
     AttnIssued issued;
     const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);
 
-    // A unit: an item, a head and a split; tiles [t0, t1[i]) of keys for the two tiles of queries.
-    AttnItem it;
-    int head = 0, split = 0, t0 = 0, t1[2];
-    auto decode = [&](int64_t u) {
-        head = (int)(u % a.Hq);
-        u /= a.Hq;
-        split = (int)(u % a.splits);
-        it = attn_item(a.items, u / a.splits, a.most);
-        int n[2], most = 0;
+    // Steps [t0, t1[i]) of a unit for its two tiles of queries; n of the unit in all.
+    AttnWalk walk(a.list);
+    int t0 = 0, t1[2], n = 0;
+    auto next = [&]() {
+        if (!walk.next()) return false;
+        int of[2];
+        n = 0;
         for (int i = 0; i < 2; ++i) {
-            const int rows = min(max(it.rows - i * kAttnTile, 0), kAttnTile);
-            const int seen = rows > 0 ? max(0, min(it.others, it.shift + i * kAttnTile + rows)) : 0;
-            n[i] = (seen + kAttnTile - 1) / kAttnTile;
-            most = max(most, n[i]);
+            const int rows = min(max(walk.it.rows - i * kAttnTile, 0), kAttnTile);
+            const int seen = rows > 0 ? max(0, min(walk.it.others, walk.it.shift + i * kAttnTile + rows)) : 0;
+            of[i] = (seen + kAttnTile - 1) / kAttnTile;
+            n = max(n, of[i]);
         }
-        t0 = (int)((int64_t)most * split / a.splits);
-        const int end = (int)((int64_t)most * (split + 1) / a.splits);
-        for (int i = 0; i < 2; ++i) t1[i] = max(t0, min(n[i], end));
+        walk.steps(n);
+        t0 = walk.t0;
+        for (int i = 0; i < 2; ++i) t1[i] = max(t0, min(of[i], walk.t1));
+        return true;
     };
+    const AttnItem& it = walk.it;
+    const int& head = walk.head;
 
     if (role == kLoadWarp) {
         bool live = true;
         fence_async_proxy();
-        for (int64_t lap = 0; live; ++lap) {
-            const int64_t u = attn_unit(lap);
-            if (lap * gridDim.x >= units) break;
-            if (u >= units) continue;
-            decode(u);
+        while (live && next()) {
             const int end = max(t1[0], t1[1]);
             if (end == t0) continue;
             live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(qempty, (issued.pair - 1) & 1u, &abort_flag));
@@ -371,11 +475,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                 mma_commit1(sfull + 8 * i);
             }
         };
-        for (int64_t lap = 0; live; ++lap) {
-            const int64_t u = attn_unit(lap);
-            if (lap * gridDim.x >= units) break;
-            if (u >= units) continue;
-            decode(u);
+        while (live && next()) {
             const int end = max(t1[0], t1[1]);
             if (end == t0) continue;
             if (!wait(qfull, pairs) || !wait(full + 8 * stage(used), used / ST)) break;
@@ -423,11 +523,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
         const float sl2 = a.scale * kLog2e;
         uint32_t tiles = 0;
         bool live = true;
-        for (int64_t lap = 0; live; ++lap) {
-            const int64_t u = attn_unit(lap);
-            if (lap * gridDim.x >= units) break;
-            if (u >= units) continue;
-            decode(u);
+        while (live && next()) {
             const int row = i * kAttnTile + r, end = i ? t1[1] : t1[0];
             // Keys that this row sees.
             const int seen = max(0, min(it.others, it.shift + row + 1));
@@ -508,7 +604,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                 tc_fence_after();
             }
             const bool none = l == 0.0f;
-            if (a.splits == 1) {
+            if (walk.whole(n)) {
                 __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + at * a.o_ld + (int64_t)head * a.d;
                 if (end > t0) {
                     const float f = 1.0f / l;
@@ -522,19 +618,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                 if (in && none) store_zeros(out, 0, a.d, a.d);
                 if (in) a.lse[(int64_t)head * a.Rq + at] = none ? neg_inf() : fmaf(m, a.scale, logf(l));
             } else {
-                const int64_t slot = ((int64_t)split * a.Hq + head) * a.Rq + at;
+                const int64_t place = (int64_t)walk.slot() * a.slot_rows + row;
                 if (end > t0) {
 #pragma unroll 1
                     for (int c = 0; c < a.d; c += 32) {
                         float o[32];
                         tmem_ld32(ot + c, o);
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            if (in && c + j < a.d)
-                                *reinterpret_cast<float4*>(a.part + slot * a.d + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        if (in && ADALN_IN_ATTN(row < a.slot_rows)) store_piece32(a.part + place * a.d, c, a.d, o);
                     }
                 }
-                if (in) a.ml[slot] = make_float2(m, l);
+                if (in && ADALN_IN_ATTN(row < a.slot_rows)) a.ml[place] = make_float2(m, l);
             }
             if (end > t0) {
                 tc_fence_before();
@@ -566,45 +659,82 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
     if (tid == 0 && abort_flag) atomicOr(a.status, kErrTimeout);
 }
 
-// The splits of a row joined in their order: o = sum_s w_s o_s / sum_s w_s l_s, w_s = 2^(m_s - max m).
-__global__ void __launch_bounds__(256) attn_join_kernel(const AttnJoinArgs a) {
+// Pieces joined, in the order of the CTAs that left them. CTA (c, y, list): if CTA c of the list is the first
+// that began inside its unit, every 8th row from y of that unit. Forward: o = sum_s w_s o_s / sum_s w_s l_s
+// with w_s = 2^(m_s - max m); backward: plain sums.
+template <bool BWD>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnJoinArgs a) {
     pdl_begin();
-    if (*a.bad) return;
+    const int list = blockIdx.z, c = blockIdx.x;
+    const AttnList& l = a.list[list];
+    if (l.items == nullptr || c == 0 || c >= l.ctas) return;
+    const AttnCursor cur = attn_cursor(l, c), prev = attn_cursor(l, c - 1);
+    if (cur.tile == 0 || (prev.unit == cur.unit && prev.tile > 0)) return;
+    // The pieces: CTA c - 1's, which begins the unit, then of every CTA that begins inside it and has
+    // steps of it, up to `last`.
+    int last = c;
+    while (last + 1 < l.ctas) {
+        const AttnCursor q = attn_cursor(l, last + 1);
+        if (q.unit != cur.unit) break;
+        ++last;
+    }
+    const int count = __ldcg(l.count), head = cur.unit / count;
+    const AttnItem it = attn_item(l, cur.unit % count);
+    const int vecs = a.d / 8, rows = a.slot_rows[list], parts = BWD && list == 1 ? 2 : 1;
+    const int64_t plane = (int64_t)rows * a.d;
     const float sl2 = a.scale * kLog2e;
-    const int vecs = a.d / 8;
-    const int64_t total = a.Rq * a.Hq * vecs, plane = a.Rq * a.Hq;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int v = (int)(i % vecs);
-        const int64_t hr = i / vecs;  // head * Rq + row
-        if (!ADALN_IN_ATTN(hr < plane)) continue;
-        float top = neg_inf(), l = 0.0f, o[8] = {};
-        for (int s = 0; s < a.splits; ++s) {
-            const float2 ml = a.ml[s * plane + hr];
-            if (ml.y != 0.0f) top = fmaxf(top, ml.x);
+    // The piece of CTA x, or -1: two CTAs that begin at one place, the first has none.
+    auto slot = [&](int x) {
+        if (x == c - 1) return 2 * x + 1;
+        if (x < last && attn_cursor(l, x).tile == attn_cursor(l, x + 1).tile) return -1;
+        return 2 * x;
+    };
+    const int items = ((it.rows - (int)blockIdx.y + 7) / 8) * vecs * parts;
+    for (int i = threadIdx.x; i < items; i += 256) {
+        const int v = i % vecs, part = i / vecs % parts, row = i / vecs / parts * 8 + blockIdx.y;
+        const int64_t at = (int64_t)it.row0 + row;
+        if (!ADALN_IN_ATTN(row < rows && row < it.rows)) continue;
+        float top = neg_inf(), sum = 0.0f, o[8] = {};
+        if (!BWD) {
+            for (int x = c - 1; x <= last; ++x) {
+                const int s = slot(x);
+                if (s < 0) continue;
+                const float2 ml = __ldcg(a.ml + (int64_t)s * rows + row);
+                if (ml.y != 0.0f) top = fmaxf(top, ml.x);
+            }
         }
-        for (int s = 0; s < a.splits; ++s) {
-            const float2 ml = a.ml[s * plane + hr];
-            if (ml.y == 0.0f) continue;  // a split that this row sees nothing of
-            const float w = top == neg_inf() ? 1.0f : exp2_ftz((ml.x - top) * sl2);
-            const float4* p = reinterpret_cast<const float4*>(a.part + (s * plane + hr) * a.d + 8 * v);
-            const float4 x = p[0], y = p[1];
-            l = fmaf(w, ml.y, l);
-            o[0] = fmaf(w, x.x, o[0]);
-            o[1] = fmaf(w, x.y, o[1]);
-            o[2] = fmaf(w, x.z, o[2]);
-            o[3] = fmaf(w, x.w, o[3]);
-            o[4] = fmaf(w, y.x, o[4]);
-            o[5] = fmaf(w, y.y, o[5]);
-            o[6] = fmaf(w, y.z, o[6]);
-            o[7] = fmaf(w, y.w, o[7]);
+        for (int x = c - 1; x <= last; ++x) {
+            const int s = slot(x);
+            if (s < 0) continue;
+            float w = 1.0f;
+            if (!BWD) {
+                const float2 ml = __ldcg(a.ml + (int64_t)s * rows + row);
+                if (ml.y == 0.0f) continue;  // a piece that this row sees nothing of
+                if (top != neg_inf()) w = exp2_ftz((ml.x - top) * sl2);
+                sum = fmaf(w, ml.y, sum);
+            }
+            const float4* p = reinterpret_cast<const float4*>(a.part[list] + ((int64_t)s * parts + part) * plane +
+                                                              (int64_t)row * a.d + 8 * v);
+            const float4 f = __ldcg(p), g = __ldcg(p + 1);
+            o[0] = fmaf(w, f.x, o[0]);
+            o[1] = fmaf(w, f.y, o[1]);
+            o[2] = fmaf(w, f.z, o[2]);
+            o[3] = fmaf(w, f.w, o[3]);
+            o[4] = fmaf(w, g.x, o[4]);
+            o[5] = fmaf(w, g.y, o[5]);
+            o[6] = fmaf(w, g.z, o[6]);
+            o[7] = fmaf(w, g.w, o[7]);
         }
-        const float f = l == 0.0f ? 0.0f : 1.0f / l;
+        float f = a.scale;  // dq and dk
+        if (!BWD) f = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (BWD && list == 1 && part == 0) f = 1.0f;  // dv
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = pack2(o[2 * j] * f, o[2 * j + 1] * f);
-        const int64_t h = hr / a.Rq, r = hr % a.Rq;
-        st_vec(reinterpret_cast<__nv_bfloat16*>(a.o) + r * a.o_ld + h * a.d + 8 * v, make_uint4(w[0], w[1], w[2], w[3]));
-        if (v == 0) a.lse[hr] = l == 0.0f ? neg_inf() : fmaf(top, a.scale, logf(l));
+        const bool dv = BWD && list == 1 && part == 0;
+        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(dv ? a.dv : a.out[list]) + at * (dv ? a.dv_ld : a.ld[list]);
+        st_vec(out + (int64_t)head * a.d + 8 * v, make_uint4(w[0], w[1], w[2], w[3]));
+        if (!BWD && v == 0) a.lse[(int64_t)head * a.Rq + at] = sum == 0.0f ? neg_inf() : fmaf(top, a.scale, logf(sum));
     }
 }
 
@@ -710,25 +840,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     pdl_trigger();
     const uint32_t tmem = tmem_base, dp_tmem = tmem + 256, acc = tmem + 384;
     pdl_wait();
-    const int64_t units = (int64_t)*a.count * a.Hq;
     AttnIssued issued;
     const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);
-    AttnItem it;
-    int head = 0, n = 0;
-    auto decode = [&](int64_t u) {
-        head = (int)(u % a.Hq);
-        it = attn_item(a.items, u / a.Hq, a.most);
-        n = (max(0, min(it.others, it.shift + it.rows)) + kAttnTile - 1) / kAttnTile;
+    // n steps of a unit, from step t0 of it on; `all` is the unit's.
+    AttnWalk walk(a.list);
+    int t0 = 0, n = 0, all = 0;
+    auto next = [&]() {
+        if (!walk.next()) return false;
+        all = (max(0, min(walk.it.others, walk.it.shift + walk.it.rows)) + kAttnTile - 1) / kAttnTile;
+        walk.steps(all);
+        t0 = walk.t0;
+        n = walk.t1 - t0;
+        return true;
     };
+    const AttnItem& it = walk.it;
+    const int& head = walk.head;
 
     if (role == kLoadWarp) {
         bool live = true;
         uint32_t steps = 0;
         fence_async_proxy();
-        for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
-            const int64_t u = attn_unit(lap);
-            if (u >= units) continue;
-            decode(u);
+        while (live && next()) {
             if (n == 0) continue;
             live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(qempty, (issued.pair - 1) & 1u, &abort_flag));
             if (!live) break;
@@ -739,7 +871,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
             }
             ++issued.pair;
             const int kv = head / a.group;
-            for (int t = 0; t < n && live; ++t, ++steps) {
+            for (int t = t0; t < t0 + n && live; ++t, ++steps) {
                 const int row = it.other0 + t * kAttnTile, left = it.others - t * kAttnTile;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -795,10 +927,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
                 mma_commit1(empty + 8 * vslot(j));
             }
         };
-        for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
-            const int64_t u = attn_unit(lap);
-            if (u >= units) continue;
-            decode(u);
+        while (live && next()) {
             if (n == 0) continue;
             if (!wait(qfull, laps) || !keys(0)) break;
             tc_fence_after();
@@ -847,17 +976,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         const f2r s2 = p_splat(sl2);
         uint32_t steps = 0, laps = 0;
         bool live = true;
-        for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
-            const int64_t u = attn_unit(lap);
-            if (u >= units) continue;
-            decode(u);
+        while (live && next()) {
             const int64_t at = (int64_t)it.row0 + r;
             const bool in = r < it.rows && ADALN_IN_ATTN(at >= 0 && at < a.Rq && head < a.Hq);
-            const float lse2 = in ? __ldg(a.lse2 + (int64_t)head * a.Rq + at) : 0.0f;
-            const float delta = in ? __ldg(a.delta + (int64_t)head * a.Rq + at) : 0.0f;
+            const float lse2 = in ? __ldcg(a.lse2 + (int64_t)head * a.Rq + at) : 0.0f;
+            const float delta = in ? __ldcg(a.delta + (int64_t)head * a.Rq + at) : 0.0f;
             const int seen = max(0, min(it.others, it.shift + r + 1));
             const f2r nl = p_splat(-lse2), nd = p_splat(-delta);
-            for (int t = 0; t < n; ++t, ++steps) {
+            for (int t = t0; t < t0 + n; ++t, ++steps) {
                 const uint32_t b = steps & 1u, z = tmem + lanes + 128 * b + 64 * wg;
                 live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sfull + 8 * b, (steps >> 1) & 1u, &abort_flag));
                 if (!live) break;
@@ -897,18 +1023,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
             }
             if (!live) break;
             __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.dx) + at * a.dx_ld + (int64_t)head * a.d;
-            if (n == 0) {
-                if (in) store_zeros(out, wg * (DP / 2), (wg + 1) * (DP / 2), a.d);
+            if (n == 0) {  // nothing of the unit, or nothing in it
+                if (in && all == 0) store_zeros(out, wg * (DP / 2), (wg + 1) * (DP / 2), a.d);
                 continue;
             }
             live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(done, laps & 1u, &abort_flag));
             if (!live) break;
             tc_fence_after();
+            const bool whole = walk.whole(all);
+            float* piece = a.part + ((int64_t)walk.slot() * a.slot_rows + r) * a.d;
 #pragma unroll 1
             for (int c = wg * (DP / 2); c < min((wg + 1) * (DP / 2), a.d); c += 32) {
                 float o[32];
                 tmem_ld32(acc + lanes + c, o);
-                if (in) store32(out, c, a.d, o, a.scale);
+                if (in && whole) store32(out, c, a.d, o, a.scale);
+                if (in && !whole && ADALN_IN_ATTN(r < a.slot_rows)) store_piece32(piece, c, a.d, o);
             }
             tc_fence_before();
             __syncwarp();
@@ -995,28 +1124,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     pdl_trigger();
     const uint32_t tmem = tmem_base, dp_tmem = tmem + 128, dv_tmem = tmem + 256, dk_tmem = tmem + 384;
     pdl_wait();
-    const int Hk = a.Hq / a.group;
-    const int64_t units = (int64_t)*a.count * Hk;
     AttnIssued issued;
     const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);
-    AttnItem it;
-    int head = 0, first = 0, tiles = 0, n = 0;  // key head; first tile of queries that sees a key, their number; steps
-    auto decode = [&](int64_t u) {
-        head = (int)(u % Hk);
-        it = attn_item(a.items, u / Hk, a.most);
-        first = max(0, it.shift) / kAttnTile;
-        tiles = max(0, (it.others + kAttnTile - 1) / kAttnTile - first);
-        n = tiles * a.group;
+    // n steps of a unit, from step t0 of it on; `all` is the unit's: `tiles` of queries, from the first
+    // that sees one of the keys, for every head of the group.
+    AttnWalk walk(a.list);
+    int first = 0, tiles = 0, t0 = 0, n = 0, all = 0;
+    auto next = [&]() {
+        if (!walk.next()) return false;
+        first = max(0, walk.it.shift) / kAttnTile;
+        tiles = max(0, (walk.it.others + kAttnTile - 1) / kAttnTile - first);
+        all = tiles * a.group;
+        walk.steps(all);
+        t0 = walk.t0;
+        n = walk.t1 - t0;
+        return true;
     };
+    const AttnItem& it = walk.it;
+    const int& head = walk.head;
 
     if (role == kLoadWarp) {
         bool live = true;
         uint32_t slots = 0;
         fence_async_proxy();
-        for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
-            const int64_t u = attn_unit(lap);
-            if (u >= units) continue;
-            decode(u);
+        while (live && next()) {
             if (n == 0) continue;
             live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(kempty, (issued.pair - 1) & 1u, &abort_flag));
             if (!live) break;
@@ -1027,9 +1158,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
             }
             ++issued.pair;
             for (int j = 0; j < n && live; ++j, ++slots) {
-                const int h = head * a.group + j / tiles, t = first + j % tiles;
+                const int h = head * a.group + (t0 + j) / tiles, t = first + (t0 + j) % tiles;
                 const int row = it.other0 + t * kAttnTile, left = it.others - t * kAttnTile;
                 const bool cut = left < kAttnTile && !it.end;  // both are operands of sums over the queries
+                float stat[8];  // four rows' lse, then their delta
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int q = (lane + 32 * i) & (kAttnTile - 1);
+                    const bool in = q < left && ADALN_IN_ATTN(row >= 0 && (int64_t)row + q < a.Rq && h < a.Hq);
+                    stat[i] = in ? __ldcg((i < 4 ? a.lse2 : a.delta) + (int64_t)h * a.Rq + row + q) : 0.0f;
+                }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const uint32_t s = issued.ring % ST, l = issued.ring / ST;
@@ -1041,19 +1179,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
                         mbar_arrive_expect_tx(bar, S::kTile);
                         load_tile<DP>(dst, x ? &mdo : &mq, h, row, bar);
                     }
-                    if (x == 0) {
+                    if (x == 1) {
                         // The slot's last readers were done before the tile that went was freed.
-                        const uint32_t dst2 = smem_addr(&stats[slots % SS][0][0]);
-                        for (int c = lane; c < 2 * kAttnTile; c += 32) {
-                            const int q = c & (kAttnTile - 1);
-                            const float* src = (c < kAttnTile ? a.lse2 : a.delta) + (int64_t)h * a.Rq + row + q;
-                            const bool in = q < left && ADALN_IN_ATTN(row >= 0 && (int64_t)row + q < a.Rq && h < a.Hq);
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst2 + 4 * c),
-                                         "l"(in ? src : a.lse2), "r"(in ? 4 : 0)
-                                         : "memory");
-                        }
-                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sready + 8 * (slots % SS))
-                                     : "memory");
+                        float* dst2 = &stats[slots % SS][0][0];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dst2[lane + 32 * i] = stat[i];
+                        mbar_arrive(sready + 8 * (slots % SS));
                     }
                     if (cut) {
                         live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail, issued.tail & 1u, &abort_flag));
@@ -1070,7 +1201,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
                 }
             }
         }
-        cp_async_wait_all();
     } else if (role == kMmaWarp) {
         bool live = true;
         uint32_t used = 0, laps = 0, steps = 0;
@@ -1092,10 +1222,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
                 mma_commit1(pfull);
             }
         };
-        for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
-            const int64_t u = attn_unit(lap);
-            if (u >= units) continue;
-            decode(u);
+        while (live && next()) {
             if (n == 0) continue;
             if (!wait(kfull, laps) || !loaded(used)) break;
             tc_fence_after();
@@ -1144,13 +1271,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         const f2r s2 = p_splat(a.scale * kLog2e);
         uint32_t steps = 0, laps = 0;
         bool live = true;
-        for (int64_t lap = 0; live && lap * gridDim.x < units; ++lap) {
-            const int64_t u = attn_unit(lap);
-            if (u >= units) continue;
-            decode(u);
+        while (live && next()) {
             const int from = max(0, it.shift + c);  // the first query that sees this key
             for (int j = 0; j < n; ++j, ++steps) {
-                const int q0 = (first + j % tiles) * kAttnTile + 64 * wg;
+                const int q0 = (first + (t0 + j) % tiles) * kAttnTile + 64 * wg;
                 const bool cut = __any_sync(0xFFFFFFFFu, from > q0 || it.others < q0 + 64);
                 const uint32_t slot = smem_addr(&stats[steps % SS][0][0]) + 256 * wg;
                 live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sready + 8 * (steps % SS), (steps / SS) & 1u, &abort_flag) &&
@@ -1201,11 +1325,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
             if (!live) break;
             // One warpgroup writes dv, the other dk.
             const int64_t at = (int64_t)it.row0 + c;
-            const bool in = c < it.rows && ADALN_IN_ATTN(at >= 0 && head < Hk);
+            const bool in = c < it.rows && ADALN_IN_ATTN(at >= 0 && head < a.Hq / a.group);
             __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(wg ? a.dx : a.dv) + at * (wg ? a.dx_ld : a.dv_ld) +
                                  (int64_t)head * a.d;
             if (n == 0) {
-                if (in) store_zeros(out, 0, a.d, a.d);
+                if (in && all == 0) store_zeros(out, 0, a.d, a.d);
                 continue;
             }
             live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(done, laps & 1u, &abort_flag));
@@ -1213,11 +1337,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
             tc_fence_after();
             const uint32_t src = (wg ? dk_tmem : dv_tmem) + ((uint32_t)(warp & 3) << 21);
             const float f = wg ? a.scale : 1.0f;
+            const bool whole = walk.whole(all);
+            float* piece = a.part + (((int64_t)walk.slot() * 2 + wg) * a.slot_rows + c) * a.d;
 #pragma unroll 1
             for (int x = 0; x < a.d; x += 32) {
                 float o[32];
                 tmem_ld32(src + x, o);
-                if (in) store32(out, x, a.d, o, f);
+                if (in && whole) store32(out, x, a.d, o, f);
+                if (in && !whole && ADALN_IN_ATTN(c < a.slot_rows)) store_piece32(piece, x, a.d, o);
             }
             tc_fence_before();
             __syncwarp();
@@ -1283,11 +1410,11 @@ bool rows_map(CUtensorMap* m, const AttnRows& x, int d) {
 cudaError_t launch_attn_plan(const AttnPlanArgs& args, cudaStream_t stream) {
     AttnPlanArgs a = args;
     void* params[] = {&a};
-    return launch_dependent(reinterpret_cast<const void*>(&attn_plan_kernel), dim3(a.items[1] ? 2 : 1), dim3(1024),
+    return launch_dependent(reinterpret_cast<const void*>(&attn_plan_kernel), dim3(a.list[1].items ? 2 : 1), dim3(1024),
                             params, 0, stream);
 }
 
-cudaError_t launch_attn_fwd(const AttnFwdArgs& args, const AttnRows& q, const AttnRows& k, const AttnRows& v, int sms,
+cudaError_t launch_attn_fwd(const AttnFwdArgs& args, const AttnRows& q, const AttnRows& k, const AttnRows& v,
                             cudaStream_t stream) {
     AttnFwdArgs a = args;
     CUtensorMap mq, mk, mv;
@@ -1300,14 +1427,16 @@ cudaError_t launch_attn_fwd(const AttnFwdArgs& args, const AttnRows& q, const At
     const size_t smem = wide ? AttnShape<128>::kSmem : AttnShape<64>::kSmem;
     if (cudaError_t e = allow_attn_smem(fn, wide ? 1 : 0, smem)) return e;
     void* params[] = {&mq, &mk, &mv, &a};
-    return launch_dependent(fn, dim3(cap(a.most * a.Hq * a.splits, sms)), dim3(kAttnThreads), params, smem, stream);
+    return launch_dependent(fn, dim3((unsigned)a.list.ctas), dim3(kAttnThreads), params, smem, stream);
 }
 
-cudaError_t launch_attn_join(const AttnJoinArgs& args, int sms, cudaStream_t stream) {
+cudaError_t launch_attn_join(const AttnJoinArgs& args, bool bwd, cudaStream_t stream) {
     AttnJoinArgs a = args;
     void* params[] = {&a};
-    return launch_dependent(reinterpret_cast<const void*>(&attn_join_kernel),
-                            dim3(cap((a.Rq * a.Hq * (a.d / 8) + 255) / 256, 8 * (int64_t)sms)), dim3(256), params, 0, stream);
+    const void* fn = bwd ? reinterpret_cast<const void*>(&attn_join_kernel<true>)
+                         : reinterpret_cast<const void*>(&attn_join_kernel<false>);
+    const int ctas = std::max(a.list[0].ctas, bwd ? a.list[1].ctas : 0);
+    return launch_dependent(fn, dim3((unsigned)ctas, 8, bwd ? 2 : 1), dim3(256), params, 0, stream);
 }
 
 cudaError_t launch_attn_delta(const AttnDeltaArgs& args, int sms, cudaStream_t stream) {
@@ -1318,7 +1447,7 @@ cudaError_t launch_attn_delta(const AttnDeltaArgs& args, int sms, cudaStream_t s
 }
 
 cudaError_t launch_attn_dq(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
-                           const AttnRows& v, int sms, cudaStream_t stream) {
+                           const AttnRows& v, cudaStream_t stream) {
     AttnBwdArgs a = args;
     CUtensorMap mdo, mq, mk, mv;
     if (!rows_map(&mdo, dout, a.d) || !rows_map(&mq, q, a.d) || !rows_map(&mk, k.R ? k : q, a.d) ||
@@ -1330,11 +1459,11 @@ cudaError_t launch_attn_dq(const AttnBwdArgs& args, const AttnRows& dout, const 
     const size_t smem = wide ? AttnShape<128>::kSmem : AttnShape<64>::kSmem;
     if (cudaError_t e = allow_attn_smem(fn, wide ? 3 : 2, smem)) return e;
     void* params[] = {&mdo, &mq, &mk, &mv, &a};
-    return launch_dependent(fn, dim3(cap(a.most * a.Hq, sms)), dim3(kAttnThreads), params, smem, stream);
+    return launch_dependent(fn, dim3((unsigned)a.list.ctas), dim3(kAttnThreads), params, smem, stream);
 }
 
 cudaError_t launch_attn_dkv(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
-                            const AttnRows& v, int sms, cudaStream_t stream) {
+                            const AttnRows& v, cudaStream_t stream) {
     AttnBwdArgs a = args;
     CUtensorMap mdo, mq, mk, mv;
     if (!rows_map(&mdo, q.R ? dout : k, a.d) || !rows_map(&mq, q.R ? q : k, a.d) || !rows_map(&mk, k, a.d) ||
@@ -1346,7 +1475,7 @@ cudaError_t launch_attn_dkv(const AttnBwdArgs& args, const AttnRows& dout, const
     const size_t smem = wide ? AttnShape<128, true>::kSmem : AttnShape<64, true>::kSmem;
     if (cudaError_t e = allow_attn_smem(fn, wide ? 5 : 4, smem)) return e;
     void* params[] = {&mdo, &mq, &mk, &mv, &a};
-    return launch_dependent(fn, dim3(cap(a.most * (a.Hq / a.group), sms)), dim3(kAttnThreads), params, smem, stream);
+    return launch_dependent(fn, dim3((unsigned)a.list.ctas), dim3(kAttnThreads), params, smem, stream);
 }
 
 cudaError_t debug_word_attn(uint32_t* out, bool reset) { return debug_word(out, reset); }

@@ -20,11 +20,21 @@ struct AttnItem {
     // Queries: row r of the tile sees the keys j < min(others, shift + r + 1) of its segment. Keys: key c
     // of the tile is seen by the queries i >= max(0, shift + c) of its segment.
     int32_t shift;
-    int32_t end;     // the segment's last row is the tensor's last: nothing follows (bit 0: of the other side)
-    int32_t pad[2];
+    int32_t end;     // the segment's last row of the other side is the tensor's last: nothing follows
+    int64_t before;  // cost of the items before it
 };
 
-constexpr int kAttnClasses = 128;    // work items in descending order of cost, a quarter octave each
+// A unit of work is an item and a head: unit u is head u / items, item u % items. Its cost is its
+// steps (tiles of the other side) and what its beginning and end take, in steps. Units are laid end to end and
+// shared out evenly, so that a CTA may begin or end inside one; what it computes of such a unit is a
+// piece, left in fp32 and joined with the others in their order by another kernel. With whole units a CTA,
+// 64 x 12 units on 152 SMs would take six rounds for 5.05.
+constexpr int kAttnUnitCost = 2;
+// A piece has at least this many steps: writing and joining one costs about as much as two.
+constexpr int kAttnMinPiece = 4;
+struct AttnCursor {
+    int32_t unit, tile;
+};
 
 struct AttnTables {
     const int32_t* cu_q;  // [nseg + 1], or null: nseg segments of Rq / nseg rows
@@ -33,38 +43,62 @@ struct AttnTables {
     int causal;
 };
 
+// A work list.
+struct AttnList {
+    AttnItem* items;
+    int32_t* count;       // its entries
+    longlong2* segs;      // [nseg]: entries and cost of a segment, then of those before it
+    AttnCursor* cursors;  // [ctas + 1]: where each CTA begins
+    int64_t most;         // entries it has room for
+    int tile;             // rows an entry
+    int heads;            // units an entry
+    int group;            // keys: heads of queries that a step is repeated for
+    int ctas;
+};
+
 struct AttnPlanArgs {
     AttnTables t;
-    AttnItem* items[2];   // list 0 over queries, list 1 over keys (or null)
-    int32_t* count;       // [2]
-    int64_t most[2];      // entries of the lists
-    int tile[2];          // rows a tile
+    AttnList list[2];     // over queries; over keys (items null: none)
     uint32_t* status;     // [2]
     WsHeader* header;
 };
 
 struct AttnFwdArgs {
-    const AttnItem* items;
-    const int32_t* count;
+    AttnList list;
     void* o;
     float* lse;            // [Hq, Rq]
-    float* part;           // splits > 1: [splits][Hq][Rq][d] sums of p v
-    float2* ml;            // and [splits][Hq][Rq] (maximum, sum of p)
+    float* part;           // pieces: [2 * ctas][slot_rows][d] sums of p v
+    float2* ml;            // and [2 * ctas][slot_rows] (maximum, sum of p)
     uint32_t* status;
-    int64_t Rq, o_ld, most;
-    int Hq, group, d, splits;
+    int64_t Rq, o_ld;
+    int Hq, group, d, slot_rows;
     float scale;
 };
 
-struct AttnJoinArgs {
-    const float* part;
-    const float2* ml;
-    void* o;
-    float* lse;
-    int64_t Rq, o_ld;
-    int Hq, d, splits;
+struct AttnBwdArgs {
+    AttnList list;
+    const float* delta;
+    const float* lse2;
+    void* dx;              // dq; dk
+    void* dv;
+    float* part;           // pieces: [2 * ctas][slot_rows][d] of dq; [2 * ctas][2][slot_rows][d] of dv, dk
+    uint32_t* status;
+    int64_t Rq, dx_ld, dv_ld;
+    int Hq, group, d, slot_rows;
     float scale;
-    const uint32_t* bad;   // the plan's status: nothing was computed
+};
+
+// Pieces of up to two lists joined: the forward's, or dq's and dk's and dv's.
+struct AttnJoinArgs {
+    AttnList list[2];
+    const float* part[2];
+    const float2* ml;      // forward
+    void* out[2];          // o, or dq; dk
+    void* dv;
+    float* lse;
+    int64_t Rq, ld[2], dv_ld;
+    int d, slot_rows[2];
+    float scale;
 };
 
 struct AttnDeltaArgs {
@@ -77,19 +111,6 @@ struct AttnDeltaArgs {
     int Hq, d;
 };
 
-struct AttnBwdArgs {
-    const AttnItem* items;
-    const int32_t* count;
-    const float* delta;
-    const float* lse2;
-    void* dx;              // dq; dk
-    void* dv;
-    uint32_t* status;
-    int64_t Rq, dx_ld, dv_ld, most;
-    int Hq, group, d;
-    float scale;
-};
-
 // A side's rows as the kernels' TMA maps take them.
 struct AttnRows {
     const void* p;
@@ -98,14 +119,14 @@ struct AttnRows {
 };
 
 cudaError_t launch_attn_plan(const AttnPlanArgs& args, cudaStream_t stream);
-cudaError_t launch_attn_fwd(const AttnFwdArgs& args, const AttnRows& q, const AttnRows& k, const AttnRows& v, int sms,
+cudaError_t launch_attn_fwd(const AttnFwdArgs& args, const AttnRows& q, const AttnRows& k, const AttnRows& v,
                             cudaStream_t stream);
-cudaError_t launch_attn_join(const AttnJoinArgs& args, int sms, cudaStream_t stream);
+cudaError_t launch_attn_join(const AttnJoinArgs& args, bool bwd, cudaStream_t stream);
 cudaError_t launch_attn_delta(const AttnDeltaArgs& args, int sms, cudaStream_t stream);
 cudaError_t launch_attn_dq(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
-                           const AttnRows& v, int sms, cudaStream_t stream);
+                           const AttnRows& v, cudaStream_t stream);
 cudaError_t launch_attn_dkv(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
-                            const AttnRows& v, int sms, cudaStream_t stream);
+                            const AttnRows& v, cudaStream_t stream);
 cudaError_t debug_word_attn(uint32_t* out, bool reset);
 
 }  // namespace adaln

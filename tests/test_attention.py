@@ -207,6 +207,10 @@ CASES = {
     "split-causal": ([40], [3000], 2, 2, 64, True),
     "split-ragged": ([3, 2], [2000, 1], 2, 1, 72, False),
     "many": ([(7 * s) % 61 for s in range(90)], None, 2, 2, 64, True),
+    "pieces": ([1100, 40], [2300, 700], 3, 3, 64, False),
+    "pieces-causal": ([3000, 1500], None, 2, 1, 128, True),
+    "pieces-groups": ([40, 1500], [1000, 1200], 8, 1, 72, False),
+    "pieces-many": ([9, 700, 0, 2100, 130], [4000, 1, 50, 1030, 0], 1, 1, 32, False),
     "full-waves": ([2500, 1300], None, 12, 4, 64, False),
     "full-waves-wide": ([2000, 777, 1400], None, 12, 12, 128, True),
 }
@@ -474,6 +478,27 @@ def test_calls_back_to_back(d):
     for out, ws in runs:
         assert A.adaln_read_status(ws) == 0
         assert all(torch.equal(out[n], want[n]) for n in out)
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_changing_inputs():
+    # What a call leaves in the workspace, or a cache holds of it, is nothing to the next.
+    lens = [([700, 300], [700, 300]), ([200, 800], [500, 500]), ([999, 1], [1, 999])]
+    sets = [inputs(q, k, 4, 2, 64, seed=20 + n) for n, (q, k) in enumerate(lens)]
+    want = [call(i, pad=0) for i in sets]
+    sizes = (2, 1000, 1000, 4, 2, 64)
+    nb = max(A.adaln_attention_fwd_workspace_size(*sizes, 1), A.adaln_attention_bwd_workspace_size(*sizes, 1))
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    outs = [{n: torch.empty_like(t) for n, t in want[x % 3].items()} for x in range(15)]
+    torch.cuda.synchronize()
+    for x, out in enumerate(outs):
+        i = sets[x % 3]
+        A.adaln_attention_fwd(i["q"], i["k"], i["v"], out["o"], out["lse"], i["cu_q"], i["cu_k"], *sizes, 256, 128, 128, 256,
+                              0.125, False, ws, nb)
+        A.adaln_attention_bwd(i["dout"], i["q"], i["k"], i["v"], out["o"], out["lse"], out["dq"], out["dk"], out["dv"],
+                              i["cu_q"], i["cu_k"], *sizes, 256, 256, 128, 128, 256, 256, 128, 128, 0.125, False, ws, nb)
+    for x, out in enumerate(outs):
+        assert all(torch.equal(out[n], want[x % 3][n]) for n in out), x
 
 
 @pytest.mark.gpu
