@@ -37,12 +37,15 @@ constexpr int kAttnThreads = 384;  // two warpgroups of rows, one warp of produc
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kAllocWarp = 10;
 constexpr uint32_t kPanel = kAttnTile * 128;  // 128 rows of 64 elements, 128-byte swizzle
 
-// Shared memory: two resident tiles, then a ring. STATS: room for the row statistics of dk and dv.
-template <int DP, bool STATS = false>
+// Shared memory: two resident tiles, a ring of tiles, and in the forward 4 KB a warp for its results on
+// their way out; dk and dv need room for the row statistics.
+enum AttnKernel : int { kAttnFwd = 0, kAttnDq = 1, kAttnDkv = 2 };
+constexpr uint32_t kAttnOut = 32 * 128;  // 32 rows of 64 elements
+template <int DP, int KIND>
 struct AttnShape {
     static constexpr uint32_t kTile = DP / 64 * kPanel;
-    static constexpr int kStages = DP == 128 ? (STATS ? 4 : 5) : 8;
-    static constexpr size_t kSmem = 1024 + (2 + kStages) * (size_t)kTile;
+    static constexpr int kStages = DP == 128 ? (KIND == kAttnDq ? 5 : 4) : 8;
+    static constexpr size_t kSmem = 1024 + (2 + kStages) * (size_t)kTile + (KIND == kAttnFwd ? 8 * kAttnOut : 0);
 };
 
 // ---- work list -----------------------------------------------------------------------------
@@ -247,20 +250,31 @@ __device__ __forceinline__ AttnCursor attn_cursor(const AttnList& l, int c) {
 struct AttnWalk {
     const AttnList& l;
     AttnCursor from, to;
-    int count, unit;
-    AttnItem it;
+    int count, unit, entry;
+    AttnItem it, ahead;
     int head, t0, t1;
     __device__ __forceinline__ AttnWalk(const AttnList& list) : l(list) {
         from = attn_cursor(l, blockIdx.x);
         to = attn_cursor(l, blockIdx.x + 1);
         count = __ldcg(l.count);
         unit = from.unit - 1;
+        head = count > 0 ? from.unit / count : 0;
+        entry = count > 0 ? from.unit % count - 1 : 0;
+        fetch();
+    }
+    // Loads the next unit's entry, once before every next(): early, since it takes as long as a step.
+    __device__ __forceinline__ void fetch() {
+        const int u = unit + 1;
+        if (u < to.unit || (u == to.unit && to.tile > 0)) ahead = attn_item(l, entry + 1 < count ? entry + 1 : 0);
     }
     __device__ __forceinline__ bool next() {
         ++unit;
         if (unit > to.unit || (unit == to.unit && to.tile == 0)) return false;
-        head = unit / count;
-        it = attn_item(l, unit % count);
+        if (++entry == count) {
+            entry = 0;
+            ++head;
+        }
+        it = ahead;
         return true;
     }
     // With the unit's steps known.
@@ -310,6 +324,15 @@ __device__ __forceinline__ void mma_cols(uint32_t d_tmem, uint32_t a, uint32_t a
                     accumulate || k > 0);
 }
 
+// The same over 64 of the sum's rows.
+__device__ __forceinline__ void mma_cols64(uint32_t d_tmem, uint32_t a, uint32_t b, int d, bool accumulate) {
+    const uint64_t db = smem_desc(b, kPanel);
+    const uint32_t idesc = mma_desc(128, (d + 15) / 16 * 16, false, true);
+#pragma unroll
+    for (int k = 0; k < kAttnTile / 32; ++k)
+        mma_bf16_ts(d_tmem, a + 8 * k, db + (uint64_t)(k * (2048 >> 4)), idesc, accumulate || k > 0);
+}
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t w;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
@@ -326,6 +349,33 @@ __device__ __forceinline__ void store32(void* row, int col, int d, const float (
         for (int j = 0; j < 4; ++j) w[j] = pack2(v[8 * g + 2 * j] * f, v[8 * g + 2 * j + 1] * f);
         st_vec(reinterpret_cast<__nv_bfloat16*>(row) + col + 8 * g, make_uint4(w[0], w[1], w[2], w[3]));
     }
+}
+// A warp's 32 rows, 64 columns from `col` on, through its 4 KB of shared memory and out by one TMA store
+// (every lane's own 16-byte stores took 10,000 cycles for two tiles of 128 x 128); rows that another
+// segment follows within the warp's 32 go directly. The buffer's last store has been read.
+__device__ __forceinline__ void out64(const CUtensorMap* map, uint32_t buf, const uint32_t (&w)[32], int col, int head,
+                                      int64_t row0, int rows, void* row, int d, int lane) {
+    if (rows >= 32) {
+        const uint32_t to = buf + 128 * lane;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) st_swizzled(to, lane, c, w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        fence_shared_async();
+        __syncwarp();
+        if (elect_lane()) tma_store3(map, col, head, (int)row0, buf);
+    } else if (lane < rows) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (col + 8 * c < d)
+                st_vec(reinterpret_cast<__nv_bfloat16*>(row) + col + 8 * c,
+                       make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
+    }
+}
+// 64 accumulator columns times f, rounded.
+__device__ __forceinline__ void read64(uint32_t from, float f, uint32_t (&w)[32]) {
+    float v[64];
+    tmem_ld64(from, v);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) w[j] = pack2(v[2 * j] * f, v[2 * j + 1] * f);
 }
 __device__ __forceinline__ void store_zeros(void* row, int c0, int c1, int d) {
     for (int c = c0; c < min(c1, d); c += 8)
@@ -351,17 +401,18 @@ template <int DP>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_constant__ CUtensorMap mq,
                                                                 const __grid_constant__ CUtensorMap mk,
                                                                 const __grid_constant__ CUtensorMap mv,
+                                                                const __grid_constant__ CUtensorMap mo,
                                                                 const AttnFwdArgs a) {
-    using S = AttnShape<DP>;
+    using S = AttnShape<DP, kAttnFwd>;
     constexpr int ST = S::kStages;
     extern __shared__ uint4 dyn[];
-    __shared__ __align__(8) uint64_t bars[2 * ST + 12];
+    __shared__ __align__(8) uint64_t bars[2 * ST + 14];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t qt = (smem_addr(dyn) + 1023u) & ~1023u, ring = qt + 2 * S::kTile;
     const uint32_t full = smem_addr(bars), empty = full + 8 * ST, qfull = empty + 8 * ST, qempty = qfull + 8;
-    const uint32_t sfull = qempty + 8, pfull = sfull + 16, odone = pfull + 16, ofree = odone + 16;
+    const uint32_t sfull = qempty + 8, pfull = sfull + 16, pfull2 = pfull + 16, odone = pfull2 + 16, ofree = odone + 16;
     const uint32_t tail = ofree + 16, drain = tail + 8;
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
@@ -373,6 +424,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
         for (int i = 0; i < 2; ++i) {
             mbar_init(sfull + 8 * i, 1);
             mbar_init(pfull + 8 * i, 4);
+            mbar_init(pfull2 + 8 * i, 4);
             mbar_init(odone + 8 * i, 1);
             mbar_init(ofree + 8 * i, 4);
         }
@@ -383,6 +435,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
         tma_prefetch_map(&mq);
         tma_prefetch_map(&mk);
         tma_prefetch_map(&mv);
+        tma_prefetch_map(&mo);
     }
     if (warp == kAllocWarp) tmem_alloc1(smem_addr(&tmem_base), 512);
     tc_fence_before();
@@ -393,7 +446,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
     pdl_wait();
     AttnIssued issued;
     const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);
-
     // Steps [t0, t1[i]) of a unit for its two tiles of queries; n of the unit in all.
     AttnWalk walk(a.list);
     int t0 = 0, t1[2], n = 0;
@@ -415,10 +467,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
     const AttnItem& it = walk.it;
     const int& head = walk.head;
 
+    // Registers: the launch's 384 x 168 go as 256 x 208 to the rows' warps, which hold 128 scores each, and
+    // 128 x 88 to the others.
+    if (role >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (role == kLoadWarp) {
         bool live = true;
         fence_async_proxy();
         while (live && next()) {
+            walk.fetch();
             const int end = max(t1[0], t1[1]);
             if (end == t0) continue;
             live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(qempty, (issued.pair - 1) & 1u, &abort_flag));
@@ -476,6 +533,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
             }
         };
         while (live && next()) {
+            walk.fetch();
             const int end = max(t1[0], t1[1]);
             if (end == t0) continue;
             if (!wait(qfull, pairs) || !wait(full + 8 * stage(used), used / ST)) break;
@@ -494,11 +552,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                 for (int i = 0; i < 2; ++i) {
                     if (t >= t1[i]) continue;
                     if (t == t0 && nu[i] > 0 && !wait(ofree + 8 * i, nu[i] - 1)) break;
+                    // Each half of the keys as soon as its p is there.
+                    const uint32_t acc = tmem + 256 + 128 * i, v = ring + stage(used + 1) * S::kTile;
                     if (!wait(pfull + 8 * i, np[i])) break;
                     tc_fence_after();
+                    if (elect_lane()) mma_cols64(acc, tmem + 128 * i, v, a.d, t > t0);
+                    if (!wait(pfull2 + 8 * i, np[i])) break;
+                    tc_fence_after();
                     if (elect_lane()) {
-                        mma_cols(tmem + 256 + 128 * i, tmem + 128 * i, tmem + 128 * i + 32, ring + stage(used + 1) * S::kTile,
-                                 a.d, t > t0);
+                        mma_cols64(acc, tmem + 128 * i + 32, v + kPanel / 2, a.d, true);
                         mma_commit1(odone + 8 * i);
                     }
                     ++np[i];
@@ -516,11 +578,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
             for (int i = 0; i < 2; ++i)
                 if (t1[i] > t0) ++nu[i];
         }
-    } else if (role < kMmaWarp) {
+    }
+    } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int i = warp >> 2;  // this warpgroup's tile of queries
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), st = lanes + 128 * i, ot = lanes + 256 + 128 * i;
         const int r = (warp & 3) * 32 + lane;
         const float sl2 = a.scale * kLog2e;
+        const uint32_t out_buf = ring + ST * S::kTile + warp * kAttnOut;
         uint32_t tiles = 0;
         bool live = true;
         while (live && next()) {
@@ -533,10 +598,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                 if (!live) break;
                 tc_fence_after();
                 float v[64], w[64];
-                tmem_ld64(st, v);
-                tmem_ld64(st + 64, w);
                 const int lim = seen - t * kAttnTile;
-                if (__any_sync(0xFFFFFFFFu, lim < kAttnTile)) {
+                const bool cut = __any_sync(0xFFFFFFFFu, lim < kAttnTile);
+                tmem_ld128(st, v, w);
+                if (cut) {
 #pragma unroll
                     for (int j = 0; j < 64; ++j) {
                         v[j] = j < lim ? v[j] : neg_inf();
@@ -552,32 +617,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                     m4[3] = fmaxf(m4[3], w[j + 1]);
                 }
                 const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                if (t == t0) {
-                    m = mt;
-                } else if (__any_sync(0xFFFFFFFFu, (mt - m) * sl2 > 8.0f)) {
-                    // The reference may lag behind the maximum by 2^8, which fp32 sums and bf16 p take as
-                    // well as 1; beyond it, what has been summed is brought to the new one.
-                    const float to = fmaxf(m, mt), f = to == m ? 1.0f : exp2_ftz((m - to) * sl2);
-                    live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
-                    if (!live) break;
-                    tc_fence_after();
-                    l *= f;
-                    m = to;
-#pragma unroll 1
-                    for (int c = 0; c < a.d; c += 32) {
-                        float o[32];
-                        uint32_t b[32];
-                        tmem_ld32(ot + c, o);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) b[j] = __float_as_uint(o[j] * f);
-                        tmem_st32(ot + c, b);
-                    }
-                }
-                // A row that has seen nothing yet: every exponential is 0 (and NaN stays).
-                const f2r s2 = p_splat(sl2), c2 = p_splat(m == neg_inf() ? 0.0f : -m * sl2);
-                f2r sum[2] = {kPairZero, kPairZero};
+                const f2r s2 = p_splat(sl2);
+                f2r c2, sum[2];
                 uint32_t b[32];
-                auto half = [&](const float (&x)[64], uint32_t to) {
+                // Exponentials of 64 scores against the reference, their sum; a row that has seen nothing yet
+                // has none but 0 (and NaN stays).
+                auto half = [&](const float (&x)[64]) {
+                    c2 = p_splat(m == neg_inf() ? 0.0f : -m * sl2);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         const float2 e = p_get(p_fma(p_make(x[2 * j], x[2 * j + 1]), s2, c2));
@@ -585,38 +631,76 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                         sum[j & 1] = p_add(sum[j & 1], p_make(e0, e1));
                         b[j] = pack2(e0, e1);
                     }
-                    tmem_st32(to, b);
                 };
-                half(v, st);
-                half(w, st + 32);
-                l += p_hsum(p_add(sum[0], sum[1]));
+                // The first half's against the reference of the step before, while the maximum is still being
+                // found; it seldom has to be done again.
+                sum[0] = sum[1] = kPairZero;
+                half(v);
+                if (__any_sync(0xFFFFFFFFu, t == t0 || (mt - m) * sl2 > 8.0f)) {
+                    // The reference may lag behind the maximum by 2^8, which fp32 sums and bf16 p take as
+                    // well as 1; beyond it, what has been summed is brought to the new one.
+                    const float to = t == t0 ? mt : fmaxf(m, mt);
+                    if (t > t0) {
+                        const float f = to == m ? 1.0f : exp2_ftz((m - to) * sl2);
+                        live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
+                        if (!live) break;
+                        tc_fence_after();
+                        l *= f;
+#pragma unroll 1
+                        for (int c = 0; c < a.d; c += 32) {
+                            float o[32];
+                            tmem_ld32(ot + c, o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) b[j] = __float_as_uint(o[j] * f);
+                            tmem_st32(ot + c, b);
+                        }
+                    }
+                    m = to;
+                    tmem_ld64(st, v);
+                    if (cut) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) v[j] = j < lim ? v[j] : neg_inf();
+                    }
+                    sum[0] = sum[1] = kPairZero;
+                    half(v);
+                }
+                tmem_st32(st, b);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(pfull + 8 * i);
+                half(w);
+                tmem_st32(st + 32, b);
+                l += p_hsum(p_add(sum[0], sum[1]));
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfull2 + 8 * i);
             }
             if (!live) break;
+            walk.fetch();
             const bool mine = row < it.rows;
             const int64_t at = (int64_t)it.row0 + row;
             const bool in = mine && ADALN_IN_ATTN(at >= 0 && at < a.Rq && head < a.Hq);
+            const bool none = l == 0.0f;  // no key seen: zeros
             if (end > t0) {
                 live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
                 if (!live) break;
                 tc_fence_after();
             }
-            const bool none = l == 0.0f;
             if (walk.whole(n)) {
-                __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + at * a.o_ld + (int64_t)head * a.d;
-                if (end > t0) {
-                    const float f = 1.0f / l;
-#pragma unroll 1
-                    for (int c = 0; c < a.d; c += 32) {
-                        float o[32];
-                        tmem_ld32(ot + c, o);
-                        if (in && !none) store32(out, c, a.d, o, f);
-                    }
-                }
-                if (in && none) store_zeros(out, 0, a.d, a.d);
                 if (in) a.lse[(int64_t)head * a.Rq + at] = none ? neg_inf() : fmaf(m, a.scale, logf(l));
+                const float f = 1.0f / l;
+                const int first = i * kAttnTile + (warp & 3) * 32, rows = min(32, it.rows - first);
+#pragma unroll 1
+                for (int c = 0; c < a.d && rows > 0; c += 64) {
+                    uint32_t b[32];
+                    if (end > t0) read64(ot + c, f, b);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) b[j] = none ? 0u : b[j];
+                    tma_store_read();  // the lane that issued the buffer's last store has it read
+                    __syncwarp();
+                    out64(&mo, out_buf, b, c, head, it.row0 + first, in || !mine ? rows : 0,
+                          reinterpret_cast<__nv_bfloat16*>(a.o) + at * a.o_ld + (int64_t)head * a.d, a.d, lane);
+                }
             } else {
                 const int64_t place = (int64_t)walk.slot() * a.slot_rows + row;
                 if (end > t0) {
@@ -635,6 +719,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                 if (lane == 0) mbar_arrive(ofree + 8 * i);
             }
         }
+        tma_store_wait();
     }
     __syncwarp();
     tc_fence_before();
@@ -793,7 +878,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
                                                                const __grid_constant__ CUtensorMap mk,
                                                                const __grid_constant__ CUtensorMap mv,
                                                                const AttnBwdArgs a) {
-    using S = AttnShape<DP>;
+    using S = AttnShape<DP, kAttnDq>;
     // Keys are held from their scores to dq, two steps on; values from dp of their step alone. With a ring
     // for both, a values' tile would wait for the keys three tiles before it.
     constexpr int KS = DP == 128 ? 3 : 4, VS = DP == 128 ? 2 : 4, ST = KS + VS;
@@ -861,6 +946,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         uint32_t steps = 0;
         fence_async_proxy();
         while (live && next()) {
+            walk.fetch();
             if (n == 0) continue;
             live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(qempty, (issued.pair - 1) & 1u, &abort_flag));
             if (!live) break;
@@ -928,6 +1014,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
             }
         };
         while (live && next()) {
+            walk.fetch();
             if (n == 0) continue;
             if (!wait(qfull, laps) || !keys(0)) break;
             tc_fence_after();
@@ -1022,6 +1109,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
                 if (lane == 0) mbar_arrive(dsfull + 8 * b);
             }
             if (!live) break;
+            walk.fetch();
             __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.dx) + at * a.dx_ld + (int64_t)head * a.d;
             if (n == 0) {  // nothing of the unit, or nothing in it
                 if (in && all == 0) store_zeros(out, wg * (DP / 2), (wg + 1) * (DP / 2), a.d);
@@ -1082,7 +1170,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
                                                                 const __grid_constant__ CUtensorMap mk,
                                                                 const __grid_constant__ CUtensorMap mv,
                                                                 const AttnBwdArgs a) {
-    using S = AttnShape<DP, true>;
+    using S = AttnShape<DP, kAttnDkv>;
     constexpr int ST = S::kStages, SS = 4;  // slots of row statistics
     extern __shared__ uint4 dyn[];
     __shared__ __align__(16) float stats[SS][2][kAttnTile];  // lse (units of log 2) and delta of a step's queries
@@ -1148,6 +1236,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         uint32_t slots = 0;
         fence_async_proxy();
         while (live && next()) {
+            walk.fetch();
             if (n == 0) continue;
             live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(kempty, (issued.pair - 1) & 1u, &abort_flag));
             if (!live) break;
@@ -1223,6 +1312,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
             }
         };
         while (live && next()) {
+            walk.fetch();
             if (n == 0) continue;
             if (!wait(kfull, laps) || !loaded(used)) break;
             tc_fence_after();
@@ -1323,6 +1413,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
                 if (lane == 0) mbar_arrive(dsready);
             }
             if (!live) break;
+            walk.fetch();
             // One warpgroup writes dv, the other dk.
             const int64_t at = (int64_t)it.row0 + c;
             const bool in = c < it.rows && ADALN_IN_ATTN(at >= 0 && head < a.Hq / a.group);
@@ -1394,12 +1485,12 @@ cudaError_t allow_attn_smem(const void* fn, int which, size_t bytes) {
 
 // Tensor map of rows of H heads of d elements: boxes of 64 elements of one head by 128 rows, 128-byte
 // swizzle; what is past d, or past the last row, arrives as zeros.
-bool rows_map(CUtensorMap* m, const AttnRows& x, int d) {
+bool rows_map(CUtensorMap* m, const AttnRows& x, int d, int box_rows = kAttnTile) {
     const TensorMapEncode encode = tensor_map_encode();
     if (!encode) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)x.H, (cuuint64_t)x.R};
     const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)x.ld * 2};
-    const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)kAttnTile}, one[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)box_rows}, one[3] = {1, 1, 1};
     return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x.p), dims, strides, box, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1417,16 +1508,17 @@ cudaError_t launch_attn_plan(const AttnPlanArgs& args, cudaStream_t stream) {
 cudaError_t launch_attn_fwd(const AttnFwdArgs& args, const AttnRows& q, const AttnRows& k, const AttnRows& v,
                             cudaStream_t stream) {
     AttnFwdArgs a = args;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     // Without keys nothing is loaded; the maps still have to be maps.
-    if (!rows_map(&mq, q, a.d) || !rows_map(&mk, k.R ? k : q, a.d) || !rows_map(&mv, k.R ? v : q, a.d))
+    if (!rows_map(&mq, q, a.d) || !rows_map(&mk, k.R ? k : q, a.d) || !rows_map(&mv, k.R ? v : q, a.d) ||
+        !rows_map(&mo, {a.o, q.R, a.o_ld, q.H}, a.d, 32))
         return cudaErrorInvalidValue;
     const bool wide = a.d > 64;
     const void* fn = wide ? reinterpret_cast<const void*>(&attn_fwd_kernel<128>)
                           : reinterpret_cast<const void*>(&attn_fwd_kernel<64>);
-    const size_t smem = wide ? AttnShape<128>::kSmem : AttnShape<64>::kSmem;
+    const size_t smem = wide ? AttnShape<128, kAttnFwd>::kSmem : AttnShape<64, kAttnFwd>::kSmem;
     if (cudaError_t e = allow_attn_smem(fn, wide ? 1 : 0, smem)) return e;
-    void* params[] = {&mq, &mk, &mv, &a};
+    void* params[] = {&mq, &mk, &mv, &mo, &a};
     return launch_dependent(fn, dim3((unsigned)a.list.ctas), dim3(kAttnThreads), params, smem, stream);
 }
 
@@ -1456,7 +1548,7 @@ cudaError_t launch_attn_dq(const AttnBwdArgs& args, const AttnRows& dout, const 
     const bool wide = a.d > 64;
     const void* fn = wide ? reinterpret_cast<const void*>(&attn_dq_kernel<128>)
                           : reinterpret_cast<const void*>(&attn_dq_kernel<64>);
-    const size_t smem = wide ? AttnShape<128>::kSmem : AttnShape<64>::kSmem;
+    const size_t smem = wide ? AttnShape<128, kAttnDq>::kSmem : AttnShape<64, kAttnDq>::kSmem;
     if (cudaError_t e = allow_attn_smem(fn, wide ? 3 : 2, smem)) return e;
     void* params[] = {&mdo, &mq, &mk, &mv, &a};
     return launch_dependent(fn, dim3((unsigned)a.list.ctas), dim3(kAttnThreads), params, smem, stream);
@@ -1472,7 +1564,7 @@ cudaError_t launch_attn_dkv(const AttnBwdArgs& args, const AttnRows& dout, const
     const bool wide = a.d > 64;
     const void* fn = wide ? reinterpret_cast<const void*>(&attn_dkv_kernel<128>)
                           : reinterpret_cast<const void*>(&attn_dkv_kernel<64>);
-    const size_t smem = wide ? AttnShape<128, true>::kSmem : AttnShape<64, true>::kSmem;
+    const size_t smem = wide ? AttnShape<128, kAttnDkv>::kSmem : AttnShape<64, kAttnDkv>::kSmem;
     if (cudaError_t e = allow_attn_smem(fn, wide ? 5 : 4, smem)) return e;
     void* params[] = {&mdo, &mq, &mk, &mv, &a};
     return launch_dependent(fn, dim3((unsigned)a.list.ctas), dim3(kAttnThreads), params, smem, stream);
