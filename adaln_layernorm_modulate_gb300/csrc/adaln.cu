@@ -1489,7 +1489,7 @@ int adaln_attention_fwd(const void* q, const void* k, const void* v, void* o, fl
     const AttnPlan p = attn_plan(nseg, Rq, Rk, Hq, Hk, d, false, sms);
     if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
     const AttnPlanArgs l = attn_plan_args(t, p, workspace, false);
-    if (int rc = launched(launch_attn_plan(l, stream))) return rc;
+    if (int rc = launched(launch_attn_prepare(l, AttnDeltaArgs{}, sms, stream))) return rc;
     if (Rq == 0) return ADALN_OK;
     AttnFwdArgs a{};
     a.list = l.list[0];
@@ -1560,9 +1560,8 @@ int adaln_attention_bwd(const void* dout, const void* q, const void* k, const vo
     const AttnPlan p = attn_plan(nseg, Rq, Rk, Hq, Hk, d, true, sms);
     if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
     const AttnPlanArgs l = attn_plan_args(t, p, workspace, true);
-    if (int rc = launched(launch_attn_plan(l, stream))) return rc;
     const AttnDeltaArgs e{dout, o, lse, at<float>(workspace, p.delta), at<float>(workspace, p.lse2), Rq, dout_ld, o_ld, Hq, d};
-    if (int rc = Rq > 0 ? launched(launch_attn_delta(e, sms, stream)) : ADALN_OK) return rc;
+    if (int rc = launched(launch_attn_prepare(l, e, sms, stream))) return rc;
     const AttnRows rdo{dout, Rq, dout_ld, Hq}, rq{q, Rq, q_ld, Hq}, rk{k, Rk, k_ld, Hk}, rv{v, Rk, v_ld, Hk};
     AttnBwdArgs a{};
     a.delta = e.delta;

@@ -93,15 +93,18 @@ __device__ __forceinline__ int64_t warp_before(int64_t v, int lane, int64_t* tot
     return s - v;
 }
 
+constexpr int kAttnFewSegs = 1024, kAttnFewItems = 2048;  // kept in shared memory while they are planned
+
 // One CTA a list. The entries are in the order of the rows: first what each segment has and costs (a warp
 // a segment, its lanes the tiles), then sums over the segments before it, then the entries, then where
 // each CTA begins. Everything follows from the tables alone, so that pieces, and with them the order of
 // sums, are the same every time.
-__global__ void __launch_bounds__(1024) attn_plan_kernel(const __grid_constant__ AttnPlanArgs a) {
-    pdl_begin();
+__device__ __forceinline__ void attn_plan(const AttnPlanArgs& a, int list) {
     __shared__ int64_t sums[2][32];
     __shared__ int64_t run[2];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, list = blockIdx.x;
+    __shared__ longlong2 few[kAttnFewSegs];
+    __shared__ int64_t begins[kAttnFewItems];  // of the first entries
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const AttnTables& t = a.t;
     const AttnList& l = a.list[list];
     bool bad = false;
@@ -122,6 +125,7 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const __grid_constant__
         a.header->nwords = 2;
     }
     if (l.items == nullptr) return;
+    longlong2* segs = t.nseg <= kAttnFewSegs ? few : l.segs;
     if (any_bad) {
         if (tid == 0) *l.count = 0;
         for (int c = tid; c <= l.ctas; c += 1024) l.cursors[c] = AttnCursor{0, 0};
@@ -153,13 +157,13 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const __grid_constant__
             cost += attn_steps(t, l, list, g, i * l.tile, &it) + kAttnUnitCost;
         }
         warp_before(cost, lane, &all);
-        if (lane == 0) l.segs[s] = make_longlong2(tiles, all);
+        if (lane == 0) segs[s] = make_longlong2(tiles, all);
     });
     if (tid < 2) run[tid] = 0;
     __syncthreads();
     for (int64_t base = 0; base < t.nseg; base += 1024) {
         const int64_t s = base + tid;
-        const longlong2 v = s < t.nseg ? l.segs[s] : make_longlong2(0, 0);
+        const longlong2 v = s < t.nseg ? segs[s] : make_longlong2(0, 0);
         int64_t all[2], before[2] = {warp_before(v.x, lane, &all[0]), warp_before(v.y, lane, &all[1])};
         if (lane == 0) {
             sums[0][warp] = all[0];
@@ -176,13 +180,13 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const __grid_constant__
             run[0] = before[0] + v.x;
             run[1] = before[1] + v.y;
         }
-        if (s < t.nseg) l.segs[s] = make_longlong2(before[0], before[1]);
+        if (s < t.nseg) segs[s] = make_longlong2(before[0], before[1]);
         __syncthreads();
     }
     const int64_t count = min(run[0], l.most), total = run[1];
     if (tid == 0) *l.count = (int32_t)count;
     each([&](int64_t s, const AttnSegment& g, int tiles) {
-        const longlong2 before = l.segs[s];
+        const longlong2 before = segs[s];
         int64_t cost = before.y;
         for (int i0 = 0; i0 < tiles; i0 += 32) {
             const int i = i0 + lane;
@@ -192,11 +196,15 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const __grid_constant__
             it.before = cost + warp_before(mine, lane, &all);
             cost += all;
             const int64_t at = before.x + i;
-            if (i < tiles && at < l.most && ADALN_IN_ATTN(at >= 0)) l.items[at] = it;
+            if (i < tiles && at < l.most && ADALN_IN_ATTN(at >= 0)) {
+                l.items[at] = it;
+                if (at < kAttnFewItems) begins[at] = it.before;
+            }
         }
     });
     __syncthreads();
     // CTA c begins at cost c / ctas of all heads' together.
+    auto begin = [&](int64_t i) { return i < kAttnFewItems ? begins[i] : l.items[i].before; };
     const int64_t every = total * l.heads;
     for (int c = tid; c <= l.ctas; c += 1024) {
         AttnCursor cur{(int32_t)(count * l.heads), 0};
@@ -206,12 +214,12 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const __grid_constant__
             int64_t lo = 0, hi = count - 1;  // the last entry that begins at or before `in`
             while (lo < hi) {
                 const int64_t mid = (lo + hi + 1) >> 1;
-                if (l.items[mid].before <= in) lo = mid;
+                if (begin(mid) <= in) lo = mid;
                 else hi = mid - 1;
             }
-            const int64_t end = lo + 1 < count ? l.items[lo + 1].before : total;
-            const int n = (int)(end - l.items[lo].before) - kAttnUnitCost;
-            int tile = (int)(in - l.items[lo].before) - kAttnUnitCost / 2;
+            const int64_t end = lo + 1 < count ? begin(lo + 1) : total;
+            const int n = (int)(end - begin(lo)) - kAttnUnitCost;
+            int tile = (int)(in - begin(lo)) - kAttnUnitCost / 2;
             cur.unit = (int32_t)(head * count + lo);
             if (tile < kAttnMinPiece) tile = 0;
             if (tile > 0 && n - tile < kAttnMinPiece) {
@@ -222,6 +230,54 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const __grid_constant__
         }
         l.cursors[c] = cur;
     }
+}
+
+// delta = dout . o of every row and head, and lse in units of log 2: 16 lanes a row of a head.
+__device__ __forceinline__ void attn_delta(const AttnDeltaArgs& a, int64_t block, int64_t blocks) {
+    constexpr int U = 4;
+    const int lane = threadIdx.x & 15, vecs = a.d / 8;
+    const int64_t total = a.Rq * a.Hq, step = blocks * 64;
+    const int64_t first = block * 64 + (threadIdx.x >> 4);
+    for (int64_t base = first - (first & 1); base < total; base += U * step) {  // both groups of a warp together
+        uint4 x[U], y[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t i = base + (first & 1) + j * step;
+            x[j] = y[j] = make_uint4(0, 0, 0, 0);
+            if (i < total && lane < vecs && ADALN_IN_ATTN(i >= 0)) {
+                const int64_t r = i / a.Hq, h = i % a.Hq;
+                x[j] = ld_stream(reinterpret_cast<const __nv_bfloat16*>(a.dout) + r * a.do_ld + h * a.d + 8 * lane);
+                y[j] = ld_stream(reinterpret_cast<const __nv_bfloat16*>(a.o) + r * a.o_ld + h * a.d + 8 * lane);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t i = base + (first & 1) + j * step;
+            f2r p[4], q[4], sum = kPairZero;
+            Io<__nv_bfloat16>::unpackp(x[j], p);
+            Io<__nv_bfloat16>::unpackp(y[j], q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum = p_fma(p[e], q[e], sum);
+            float v = p_hsum(sum);
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            if (lane == 0 && i < total && ADALN_IN_ATTN(i >= 0)) {
+                const int64_t at = i % a.Hq * a.Rq + i / a.Hq;
+                a.delta[at] = v;
+                a.lse2[at] = a.lse[at] * kLog2e;
+            }
+        }
+    }
+}
+
+// The work lists, a CTA each, and beside them, backward, delta.
+__global__ void __launch_bounds__(1024) attn_prepare_kernel(const __grid_constant__ AttnPlanArgs p,
+                                                            const __grid_constant__ AttnDeltaArgs d, int lists) {
+    pdl_begin();
+    if ((int)blockIdx.x < lists)
+        attn_plan(p, blockIdx.x);
+    else
+        attn_delta(d, (int)blockIdx.x - lists, (int)gridDim.x - lists);
 }
 
 // The work list is written by the kernel ahead, which this kernel may have been scheduled before: read
@@ -252,7 +308,7 @@ struct AttnWalk {
     AttnCursor from, to;
     int count, unit, entry;
     AttnItem it, ahead;
-    int head, t0, t1;
+    int head, t0, t1, all, shift, elapsed = 0;
     __device__ __forceinline__ AttnWalk(const AttnList& list) : l(list) {
         from = attn_cursor(l, blockIdx.x);
         to = attn_cursor(l, blockIdx.x + 1);
@@ -277,11 +333,19 @@ struct AttnWalk {
         it = ahead;
         return true;
     }
-    // With the unit's steps known.
-    __device__ __forceinline__ void steps(int n) {
+    // With the unit's steps known. `turn`: its steps may go in any order; a whole unit then begins with the step
+    // that the CTA would be at had it begun with step 0 of its first unit, and goes round. CTAs that work on
+    // one head so read the same tiles at about the same time, wherever they began (32760 x 12 x 128: the keys
+    // and values of all heads are more than L2 holds; TURNTIMES).
+    __device__ __forceinline__ void steps(int n, bool turn) {
         t0 = unit == from.unit ? from.tile : 0;
         t1 = unit == to.unit ? to.tile : n;
+        all = n;
+        shift = turn && n > 0 && whole(n) ? elapsed % n : 0;
+        elapsed += t1 - t0;
     }
+    // The tile of step t of the unit.
+    __device__ __forceinline__ int tile(int t) const { return t + shift < all ? t + shift : t + shift - all; }
     __device__ __forceinline__ bool whole(int n) const { return t0 == 0 && t1 == n; }
     // Where a piece goes: a CTA has at most one that does not begin its unit and one that does.
     __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0); }
@@ -382,11 +446,13 @@ __device__ __forceinline__ void store_zeros(void* row, int c0, int c1, int d) {
         st_vec(reinterpret_cast<__nv_bfloat16*>(row) + c, make_uint4(0, 0, 0, 0));
 }
 
-// 32 columns of a row to a piece.
-__device__ __forceinline__ void store_piece32(float* row, int col, int d, const float (&v)[32]) {
+// 32 columns of a row to a piece, which holds [d / 4][rows] vectors of four columns: the lanes of a warp, a row
+// each, write side by side.
+__device__ __forceinline__ void store_piece32(float* piece, int row, int rows, int col, int d, const float (&v)[32]) {
 #pragma unroll
     for (int j = 0; j < 32; j += 4)
-        if (col + j < d) *reinterpret_cast<float4*>(row + col + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        if (col + j < d)
+            reinterpret_cast<float4*>(piece)[(int64_t)((col + j) / 4) * rows + row] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
 }
 
 // What a CTA has issued, for the drain after a timeout: copies and products must not land in memory
@@ -448,6 +514,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
     const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);
     // Steps [t0, t1[i]) of a unit for its two tiles of queries; n of the unit in all.
     AttnWalk walk(a.list);
+    const AttnItem& it = walk.it;
+    const int& head = walk.head;
     int t0 = 0, t1[2], n = 0;
     auto next = [&]() {
         if (!walk.next()) return false;
@@ -459,13 +527,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
             of[i] = (seen + kAttnTile - 1) / kAttnTile;
             n = max(n, of[i]);
         }
-        walk.steps(n);
+        walk.steps(n, of[0] == n && (of[1] == n || it.rows <= kAttnTile));
         t0 = walk.t0;
         for (int i = 0; i < 2; ++i) t1[i] = max(t0, min(of[i], walk.t1));
         return true;
     };
-    const AttnItem& it = walk.it;
-    const int& head = walk.head;
 
     // Registers: the launch's 384 x 168 go as 256 x 208 to the rows' warps, which hold 128 scores each, and
     // 128 x 88 to the others.
@@ -489,7 +555,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
             ++issued.pair;
             const int kv = head / a.group;
             for (int t = t0; t < end && live; ++t) {
-                const int row = it.other0 + t * kAttnTile, left = it.others - t * kAttnTile;
+                const int at = walk.tile(t) * kAttnTile, row = it.other0 + at, left = it.others - at;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const uint32_t s = issued.ring % ST, lap_ = issued.ring / ST;
@@ -598,7 +664,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                 if (!live) break;
                 tc_fence_after();
                 float v[64], w[64];
-                const int lim = seen - t * kAttnTile;
+                const int lim = seen - walk.tile(t) * kAttnTile;
                 const bool cut = __any_sync(0xFFFFFFFFu, lim < kAttnTile);
                 tmem_ld128(st, v, w);
                 if (cut) {
@@ -708,7 +774,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                     for (int c = 0; c < a.d; c += 32) {
                         float o[32];
                         tmem_ld32(ot + c, o);
-                        if (in && ADALN_IN_ATTN(row < a.slot_rows)) store_piece32(a.part + place * a.d, c, a.d, o);
+                        if (in && ADALN_IN_ATTN(row < a.slot_rows))
+                            store_piece32(a.part + (int64_t)walk.slot() * a.slot_rows * a.d, row, a.slot_rows, c, a.d, o);
                     }
                 }
                 if (in && ADALN_IN_ATTN(row < a.slot_rows)) a.ml[place] = make_float2(m, l);
@@ -745,7 +812,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
 }
 
 // Pieces joined, in the order of the CTAs that left them. CTA (c, y, list): if CTA c of the list is the first
-// that began inside its unit, every 8th row from y of that unit. Forward: o = sum_s w_s o_s / sum_s w_s l_s
+// that began inside its unit, the y-th eighth of that unit's rows. Forward: o = sum_s w_s o_s / sum_s w_s l_s
 // with w_s = 2^(m_s - max m); backward: plain sums.
 template <bool BWD>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnJoinArgs a) {
@@ -774,11 +841,12 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         if (x < last && attn_cursor(l, x).tile == attn_cursor(l, x + 1).tile) return -1;
         return 2 * x;
     };
-    const int items = ((it.rows - (int)blockIdx.y + 7) / 8) * vecs * parts;
+    const int per = (rows + 7) / 8, items = per * vecs * parts;
     for (int i = threadIdx.x; i < items; i += 256) {
-        const int v = i % vecs, part = i / vecs % parts, row = i / vecs / parts * 8 + blockIdx.y;
+        // Rows side by side, as the pieces have them.
+        const int row = (int)blockIdx.y * per + i % per, v = i / per % vecs, part = i / per / vecs;
         const int64_t at = (int64_t)it.row0 + row;
-        if (!ADALN_IN_ATTN(row < rows && row < it.rows)) continue;
+        if (row >= it.rows || !ADALN_IN_ATTN(row < rows)) continue;
         float top = neg_inf(), sum = 0.0f, o[8] = {};
         if (!BWD) {
             for (int x = c - 1; x <= last; ++x) {
@@ -798,9 +866,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
                 if (top != neg_inf()) w = exp2_ftz((ml.x - top) * sl2);
                 sum = fmaf(w, ml.y, sum);
             }
-            const float4* p = reinterpret_cast<const float4*>(a.part[list] + ((int64_t)s * parts + part) * plane +
-                                                              (int64_t)row * a.d + 8 * v);
-            const float4 f = __ldcg(p), g = __ldcg(p + 1);
+            const float4* p = reinterpret_cast<const float4*>(a.part[list] + ((int64_t)s * parts + part) * plane) +
+                              (int64_t)2 * v * rows + row;
+            const float4 f = __ldcg(p), g = __ldcg(p + rows);
             o[0] = fmaf(w, f.x, o[0]);
             o[1] = fmaf(w, f.y, o[1]);
             o[2] = fmaf(w, f.z, o[2]);
@@ -824,45 +892,6 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 }
 
 // ---- backward --------------------------------------------------------------------------------
-// delta = dout . o of every row and head, and lse in units of log 2: 16 lanes a row of a head.
-__global__ void __launch_bounds__(256) attn_delta_kernel(const AttnDeltaArgs a) {
-    pdl_begin();
-    constexpr int U = 4;
-    const int lane = threadIdx.x & 15, vecs = a.d / 8;
-    const int64_t total = a.Rq * a.Hq, step = (int64_t)gridDim.x * 16;
-    const int64_t first = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-    for (int64_t base = first - (first & 1); base < total; base += U * step) {  // both groups of a warp together
-        uint4 x[U], y[U];
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int64_t i = base + (first & 1) + j * step;
-            x[j] = y[j] = make_uint4(0, 0, 0, 0);
-            if (i < total && lane < vecs && ADALN_IN_ATTN(i >= 0)) {
-                const int64_t r = i / a.Hq, h = i % a.Hq;
-                x[j] = ld_stream(reinterpret_cast<const __nv_bfloat16*>(a.dout) + r * a.do_ld + h * a.d + 8 * lane);
-                y[j] = ld_stream(reinterpret_cast<const __nv_bfloat16*>(a.o) + r * a.o_ld + h * a.d + 8 * lane);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int64_t i = base + (first & 1) + j * step;
-            f2r p[4], q[4], sum = kPairZero;
-            Io<__nv_bfloat16>::unpackp(x[j], p);
-            Io<__nv_bfloat16>::unpackp(y[j], q);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum = p_fma(p[e], q[e], sum);
-            float v = p_hsum(sum);
-#pragma unroll
-            for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            if (lane == 0 && i < total && ADALN_IN_ATTN(i >= 0)) {
-                const int64_t at = i % a.Hq * a.Rq + i / a.Hq;
-                a.delta[at] = v;
-                a.lse2[at] = a.lse[at] * kLog2e;
-            }
-        }
-    }
-}
-
 // 64 scores of a row to exponentials, those outside [from, to) 0.
 __device__ __forceinline__ void mask64(float (&p)[64], int from, int to) {
 #pragma unroll
@@ -877,6 +906,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
                                                                const __grid_constant__ CUtensorMap mq,
                                                                const __grid_constant__ CUtensorMap mk,
                                                                const __grid_constant__ CUtensorMap mv,
+                                                               const __grid_constant__ CUtensorMap mdq,
                                                                const AttnBwdArgs a) {
     using S = AttnShape<DP, kAttnDq>;
     // Keys are held from their scores to dq, two steps on; values from dp of their step alone. With a ring
@@ -898,7 +928,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
             mbar_init(empty + 8 * i, 1);
         }
         mbar_init(qfull, 1);
-        mbar_init(qempty, 1);
+        mbar_init(qempty, 9);  // the products that read it, and the warps that sent dq out through it
         mbar_init(sfull, 1);
         mbar_init(sfull + 8, 1);
         mbar_init(pfull, 1);
@@ -917,6 +947,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         tma_prefetch_map(&mq);
         tma_prefetch_map(&mk);
         tma_prefetch_map(&mv);
+        tma_prefetch_map(&mdq);
     }
     if (warp == kAllocWarp) tmem_alloc1(smem_addr(&tmem_base), 512);
     tc_fence_before();
@@ -933,7 +964,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     auto next = [&]() {
         if (!walk.next()) return false;
         all = (max(0, min(walk.it.others, walk.it.shift + walk.it.rows)) + kAttnTile - 1) / kAttnTile;
-        walk.steps(all);
+        walk.steps(all, true);
         t0 = walk.t0;
         n = walk.t1 - t0;
         return true;
@@ -958,7 +989,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
             ++issued.pair;
             const int kv = head / a.group;
             for (int t = t0; t < t0 + n && live; ++t, ++steps) {
-                const int row = it.other0 + t * kAttnTile, left = it.others - t * kAttnTile;
+                const int at = walk.tile(t) * kAttnTile, row = it.other0 + at, left = it.others - at;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const uint32_t s = x ? KS + steps % VS : steps % KS, l = x ? steps / VS : steps / KS;
@@ -1083,7 +1114,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
                     p[2 * j] = exp2_ftz(e.x);
                     p[2 * j + 1] = exp2_ftz(e.y);
                 }
-                const int lim = seen - t * kAttnTile - 64 * wg;
+                const int lim = seen - walk.tile(t) * kAttnTile - 64 * wg;
                 const bool cut = __any_sync(0xFFFFFFFFu, lim < 64);
                 live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(pfull, steps & 1u, &abort_flag));
                 if (!live) break;
@@ -1118,20 +1149,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
             live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(done, laps & 1u, &abort_flag));
             if (!live) break;
             tc_fence_after();
-            const bool whole = walk.whole(all);
-            float* piece = a.part + ((int64_t)walk.slot() * a.slot_rows + r) * a.d;
+            // 64 columns a warpgroup, out through the queries' shared memory.
+            if (walk.whole(all)) {
+                const int rows = min(32, it.rows - (warp & 3) * 32);
+                if (64 * wg < a.d && rows > 0) {
+                    uint32_t w[32];
+                    read64(acc + lanes + 64 * wg, a.scale, w);
+                    out64(&mdq, qt + warp * kAttnOut, w, 64 * wg, head, it.row0 + (warp & 3) * 32, rows, out, a.d, lane);
+                    tma_store_read();
+                }
+            } else {
+                float* piece = a.part + (int64_t)walk.slot() * a.slot_rows * a.d;
 #pragma unroll 1
-            for (int c = wg * (DP / 2); c < min((wg + 1) * (DP / 2), a.d); c += 32) {
-                float o[32];
-                tmem_ld32(acc + lanes + c, o);
-                if (in && whole) store32(out, c, a.d, o, a.scale);
-                if (in && !whole && ADALN_IN_ATTN(r < a.slot_rows)) store_piece32(piece, c, a.d, o);
+                for (int c = 64 * wg; c < min(64 * (wg + 1), a.d); c += 32) {
+                    float o[32];
+                    tmem_ld32(acc + lanes + c, o);
+                    if (in && ADALN_IN_ATTN(r < a.slot_rows)) store_piece32(piece, r, a.slot_rows, c, a.d, o);
+                }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(freed);
+            if (lane == 0) {
+                mbar_arrive(freed);
+                mbar_arrive(qempty);
+            }
             ++laps;
         }
+        tma_store_wait();
     }
     __syncwarp();
     tc_fence_before();
@@ -1169,6 +1213,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
                                                                 const __grid_constant__ CUtensorMap mq,
                                                                 const __grid_constant__ CUtensorMap mk,
                                                                 const __grid_constant__ CUtensorMap mv,
+                                                                const __grid_constant__ CUtensorMap mdk,
+                                                                const __grid_constant__ CUtensorMap mdv,
                                                                 const AttnBwdArgs a) {
     using S = AttnShape<DP, kAttnDkv>;
     constexpr int ST = S::kStages, SS = 4;  // slots of row statistics
@@ -1189,7 +1235,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         }
         for (int i = 0; i < SS; ++i) mbar_init(sready + 8 * i, 32);
         mbar_init(kfull, 1);
-        mbar_init(kempty, 1);
+        mbar_init(kempty, 9);  // the products that read them, and the warps that sent dk and dv out through them
         mbar_init(sfull, 1);
         mbar_init(pready, 8);
         mbar_init(pfull, 1);
@@ -1204,6 +1250,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         tma_prefetch_map(&mq);
         tma_prefetch_map(&mk);
         tma_prefetch_map(&mv);
+        tma_prefetch_map(&mdk);
+        tma_prefetch_map(&mdv);
     }
     if (warp == kAllocWarp) tmem_alloc1(smem_addr(&tmem_base), 512);
     tc_fence_before();
@@ -1223,7 +1271,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         first = max(0, walk.it.shift) / kAttnTile;
         tiles = max(0, (walk.it.others + kAttnTile - 1) / kAttnTile - first);
         all = tiles * a.group;
-        walk.steps(all);
+        walk.steps(all, true);
         t0 = walk.t0;
         n = walk.t1 - t0;
         return true;
@@ -1247,7 +1295,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
             }
             ++issued.pair;
             for (int j = 0; j < n && live; ++j, ++slots) {
-                const int h = head * a.group + (t0 + j) / tiles, t = first + (t0 + j) % tiles;
+                const int step = walk.tile(t0 + j), h = head * a.group + step / tiles, t = first + step % tiles;
                 const int row = it.other0 + t * kAttnTile, left = it.others - t * kAttnTile;
                 const bool cut = left < kAttnTile && !it.end;  // both are operands of sums over the queries
                 float stat[8];  // four rows' lse, then their delta
@@ -1364,7 +1412,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         while (live && next()) {
             const int from = max(0, it.shift + c);  // the first query that sees this key
             for (int j = 0; j < n; ++j, ++steps) {
-                const int q0 = (first + (t0 + j) % tiles) * kAttnTile + 64 * wg;
+                const int q0 = (first + walk.tile(t0 + j) % tiles) * kAttnTile + 64 * wg;
                 const bool cut = __any_sync(0xFFFFFFFFu, from > q0 || it.others < q0 + 64);
                 const uint32_t slot = smem_addr(&stats[steps % SS][0][0]) + 256 * wg;
                 live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sready + 8 * (steps % SS), (steps / SS) & 1u, &abort_flag) &&
@@ -1428,20 +1476,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
             tc_fence_after();
             const uint32_t src = (wg ? dk_tmem : dv_tmem) + ((uint32_t)(warp & 3) << 21);
             const float f = wg ? a.scale : 1.0f;
-            const bool whole = walk.whole(all);
-            float* piece = a.part + (((int64_t)walk.slot() * 2 + wg) * a.slot_rows + c) * a.d;
+            if (walk.whole(all)) {
+                const int rows = min(32, it.rows - (warp & 3) * 32);
 #pragma unroll 1
-            for (int x = 0; x < a.d; x += 32) {
-                float o[32];
-                tmem_ld32(src + x, o);
-                if (in && whole) store32(out, x, a.d, o, f);
-                if (in && !whole && ADALN_IN_ATTN(c < a.slot_rows)) store_piece32(piece, x, a.d, o);
+                for (int x = 0; x < a.d && rows > 0; x += 64) {
+                    uint32_t w[32];
+                    read64(src + x, f, w);
+                    out64(wg ? &mdk : &mdv, kt + warp * (DP / 64 * kAttnOut) + x / 64 * kAttnOut, w, x, head,
+                          it.row0 + (warp & 3) * 32, rows, out, a.d, lane);
+                }
+                tma_store_read();
+            } else {
+                float* piece = a.part + ((int64_t)walk.slot() * 2 + wg) * a.slot_rows * a.d;
+#pragma unroll 1
+                for (int x = 0; x < a.d; x += 32) {
+                    float o[32];
+                    tmem_ld32(src + x, o);
+                    if (in && ADALN_IN_ATTN(c < a.slot_rows)) store_piece32(piece, c, a.slot_rows, x, a.d, o);
+                }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(freed);
+            if (lane == 0) {
+                mbar_arrive(freed);
+                mbar_arrive(kempty);
+            }
             ++laps;
         }
+        tma_store_wait();
     }
     __syncwarp();
     tc_fence_before();
@@ -1498,11 +1560,14 @@ bool rows_map(CUtensorMap* m, const AttnRows& x, int d, int box_rows = kAttnTile
 
 }  // namespace
 
-cudaError_t launch_attn_plan(const AttnPlanArgs& args, cudaStream_t stream) {
-    AttnPlanArgs a = args;
-    void* params[] = {&a};
-    return launch_dependent(reinterpret_cast<const void*>(&attn_plan_kernel), dim3(a.list[1].items ? 2 : 1), dim3(1024),
-                            params, 0, stream);
+cudaError_t launch_attn_prepare(const AttnPlanArgs& plan, const AttnDeltaArgs& delta, int sms, cudaStream_t stream) {
+    AttnPlanArgs p = plan;
+    AttnDeltaArgs d = delta;
+    int lists = p.list[1].items ? 2 : 1;
+    const unsigned ctas = d.delta && d.Rq > 0 ? cap((d.Rq * d.Hq + 255) / 256, 2 * (int64_t)sms) : 0;
+    void* params[] = {&p, &d, &lists};
+    return launch_dependent(reinterpret_cast<const void*>(&attn_prepare_kernel), dim3(lists + ctas), dim3(1024), params,
+                            0, stream);
 }
 
 cudaError_t launch_attn_fwd(const AttnFwdArgs& args, const AttnRows& q, const AttnRows& k, const AttnRows& v,
@@ -1531,42 +1596,37 @@ cudaError_t launch_attn_join(const AttnJoinArgs& args, bool bwd, cudaStream_t st
     return launch_dependent(fn, dim3((unsigned)ctas, 8, bwd ? 2 : 1), dim3(256), params, 0, stream);
 }
 
-cudaError_t launch_attn_delta(const AttnDeltaArgs& args, int sms, cudaStream_t stream) {
-    AttnDeltaArgs a = args;
-    void* params[] = {&a};
-    return launch_dependent(reinterpret_cast<const void*>(&attn_delta_kernel),
-                            dim3(cap((a.Rq * a.Hq + 63) / 64, 8 * (int64_t)sms)), dim3(256), params, 0, stream);
-}
-
 cudaError_t launch_attn_dq(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
                            const AttnRows& v, cudaStream_t stream) {
     AttnBwdArgs a = args;
-    CUtensorMap mdo, mq, mk, mv;
+    CUtensorMap mdo, mq, mk, mv, mdq;
     if (!rows_map(&mdo, dout, a.d) || !rows_map(&mq, q, a.d) || !rows_map(&mk, k.R ? k : q, a.d) ||
-        !rows_map(&mv, k.R ? v : q, a.d))
+        !rows_map(&mv, k.R ? v : q, a.d) ||
+        !rows_map(&mdq, {a.dx, q.R, a.dx_ld, q.H}, a.d, 32))
         return cudaErrorInvalidValue;
     const bool wide = a.d > 64;
     const void* fn = wide ? reinterpret_cast<const void*>(&attn_dq_kernel<128>)
                           : reinterpret_cast<const void*>(&attn_dq_kernel<64>);
     const size_t smem = wide ? AttnShape<128, kAttnDq>::kSmem : AttnShape<64, kAttnDq>::kSmem;
     if (cudaError_t e = allow_attn_smem(fn, wide ? 3 : 2, smem)) return e;
-    void* params[] = {&mdo, &mq, &mk, &mv, &a};
+    void* params[] = {&mdo, &mq, &mk, &mv, &mdq, &a};
     return launch_dependent(fn, dim3((unsigned)a.list.ctas), dim3(kAttnThreads), params, smem, stream);
 }
 
 cudaError_t launch_attn_dkv(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
                             const AttnRows& v, cudaStream_t stream) {
     AttnBwdArgs a = args;
-    CUtensorMap mdo, mq, mk, mv;
+    CUtensorMap mdo, mq, mk, mv, mdk, mdv;
     if (!rows_map(&mdo, q.R ? dout : k, a.d) || !rows_map(&mq, q.R ? q : k, a.d) || !rows_map(&mk, k, a.d) ||
-        !rows_map(&mv, v, a.d))
+        !rows_map(&mv, v, a.d) ||
+        !rows_map(&mdk, {a.dx, k.R, a.dx_ld, k.H}, a.d, 32) || !rows_map(&mdv, {a.dv, k.R, a.dv_ld, k.H}, a.d, 32))
         return cudaErrorInvalidValue;
     const bool wide = a.d > 64;
     const void* fn = wide ? reinterpret_cast<const void*>(&attn_dkv_kernel<128>)
                           : reinterpret_cast<const void*>(&attn_dkv_kernel<64>);
     const size_t smem = wide ? AttnShape<128, kAttnDkv>::kSmem : AttnShape<64, kAttnDkv>::kSmem;
     if (cudaError_t e = allow_attn_smem(fn, wide ? 5 : 4, smem)) return e;
-    void* params[] = {&mdo, &mq, &mk, &mv, &a};
+    void* params[] = {&mdo, &mq, &mk, &mv, &mdk, &mdv, &a};
     return launch_dependent(fn, dim3((unsigned)a.list.ctas), dim3(kAttnThreads), params, smem, stream);
 }
 

@@ -67,7 +67,7 @@ struct AttnFwdArgs {
     AttnList list;
     void* o;
     float* lse;            // [Hq, Rq]
-    float* part;           // pieces: [2 * ctas][slot_rows][d] sums of p v
+    float* part;           // pieces: [2 * ctas][d / 4][slot_rows][4] sums of p v
     float2* ml;            // and [2 * ctas][slot_rows] (maximum, sum of p)
     uint32_t* status;
     int64_t Rq, o_ld;
@@ -81,7 +81,7 @@ struct AttnBwdArgs {
     const float* lse2;
     void* dx;              // dq; dk
     void* dv;
-    float* part;           // pieces: [2 * ctas][slot_rows][d] of dq; [2 * ctas][2][slot_rows][d] of dv, dk
+    float* part;           // pieces: [2 * ctas][d / 4][slot_rows][4] of dq; [2 * ctas][2].. of dv, dk
     uint32_t* status;
     int64_t Rq, dx_ld, dv_ld;
     int Hq, group, d, slot_rows;
@@ -118,11 +118,11 @@ struct AttnRows {
     int H;
 };
 
-cudaError_t launch_attn_plan(const AttnPlanArgs& args, cudaStream_t stream);
+// The work lists and, with delta.delta, delta.
+cudaError_t launch_attn_prepare(const AttnPlanArgs& plan, const AttnDeltaArgs& delta, int sms, cudaStream_t stream);
 cudaError_t launch_attn_fwd(const AttnFwdArgs& args, const AttnRows& q, const AttnRows& k, const AttnRows& v,
                             cudaStream_t stream);
 cudaError_t launch_attn_join(const AttnJoinArgs& args, bool bwd, cudaStream_t stream);
-cudaError_t launch_attn_delta(const AttnDeltaArgs& args, int sms, cudaStream_t stream);
 cudaError_t launch_attn_dq(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
                            const AttnRows& v, cudaStream_t stream);
 cudaError_t launch_attn_dkv(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
