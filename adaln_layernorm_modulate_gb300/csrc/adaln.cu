@@ -1421,7 +1421,7 @@ AttnPlan attn_plan(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk,
         const int64_t steps = tiles(x ? Rq : Rk) * group;
         p.pieces[x] = steps >= 2 * kAttnMinPiece;
         l.ctas = (int)std::max<int64_t>(
-            1, std::min<int64_t>(sms, l.most * heads * std::max<int64_t>(1, steps / kAttnMinPiece)));
+            1, std::min<int64_t>(std::min(sms, kAttnMaxCtas), l.most * heads * std::max<int64_t>(1, steps / kAttnMinPiece)));
         p.items[x] = take((size_t)items(R, kAttnTile) * sizeof(AttnItem));
         p.segs[x] = take((size_t)nseg * sizeof(longlong2));
         p.cursors[x] = take((size_t)(sms + 1) * sizeof(AttnCursor));

@@ -54,32 +54,52 @@ __device__ __forceinline__ int64_t attn_start(const int32_t* cu, int64_t s, int6
     return cu ? (int64_t)__ldg(cu + s) : s * (R / nseg);
 }
 
-// The rows of segment s on both sides.
+// A segment's rows on both sides.
 struct AttnSegment {
     int q0, nq, k0, nk;
 };
+__device__ __forceinline__ int floor_div(int a, int b) { return a >= 0 ? a / b : -((b - 1 - a) / b); }
 
-// Entry `at / tile` of a list's segment, and its steps.
-__device__ __forceinline__ int attn_steps(const AttnTables& t, const AttnList& l, int list, const AttnSegment& g, int at,
-                                          AttnItem* it) {
+// Entry `at / tile` of a list's segment.
+__device__ __forceinline__ AttnItem attn_entry(const AttnTables& t, const AttnList& l, int list, const AttnSegment& g,
+                                               int at) {
+    AttnItem it{};
     const int len = list ? g.nk : g.nq;
-    it->rows = min(l.tile, len - at);
-    if (list == 0) {
-        it->row0 = g.q0 + at;
-        it->other0 = g.k0;
-        it->others = g.nk;
-        it->shift = t.causal ? at + g.nk - g.nq : g.nk;
-        it->end = g.k0 + g.nk == (int)t.Rk;
-        const int seen = max(0, min(g.nk, it->shift + it->rows));
-        return (seen + kAttnTile - 1) / kAttnTile;
+    it.rows = min(l.tile, len - at);
+    it.row0 = (list ? g.k0 : g.q0) + at;
+    it.other0 = list ? g.q0 : g.k0;
+    it.others = list ? g.nq : g.nk;
+    it.end = it.other0 + it.others == (int)(list ? t.Rq : t.Rk);
+    if (list == 0)
+        it.shift = t.causal ? at + g.nk - g.nq : g.nk;
+    else
+        it.shift = t.causal ? at - g.nk + g.nq : -kAttnTile;
+    return it;
+}
+
+// Cost of a segment's first `tiles` entries: their steps (as the kernels count them from the entry) and
+// kAttnUnitCost each, summed in closed form.
+__device__ __forceinline__ int64_t attn_cost(const AttnTables& t, const AttnList& l, int list, const AttnSegment& g,
+                                             int tiles) {
+    const int len = list ? g.nk : g.nq, other = list ? g.nq : g.nk;
+    const int64_t steps = (other + kAttnTile - 1) / kAttnTile;
+    int64_t sum = 0;
+    if (!t.causal) {
+        sum = steps * tiles;
+    } else if (list == 0) {
+        // A full entry's last query, (i + 1) k tiles of 128 on, sees a + (i + 1) k tiles of keys; the last
+        // entry, full or not, sees all keys.
+        const int k = l.tile / kAttnTile, a = -floor_div(g.nq - g.nk, kAttnTile);
+        const int64_t full = min(tiles, len / l.tile), none = a + k > 0 ? 0 : min((int64_t)(-a / k), full);
+        sum = (full - none) * a + k * (full * (full + 1) - none * (none + 1)) / 2;
+        if (tiles > full) sum += steps;
+    } else {
+        // Entry i is seen by the tiles of queries from max(0, b + i) on.
+        const int64_t b = floor_div(g.nq - g.nk, kAttnTile), n = tiles;
+        const int64_t whole = min(max(1 - b, (int64_t)0), n), end = min(n, max(whole, steps - b));
+        sum = whole * steps + (end - whole) * (steps - b) - (end * (end - 1) - whole * (whole - 1)) / 2;
     }
-    it->row0 = g.k0 + at;
-    it->other0 = g.q0;
-    it->others = g.nq;
-    it->shift = t.causal ? at - g.nk + g.nq : -kAttnTile;
-    it->end = g.q0 + g.nq == (int)t.Rq;
-    const int first = max(0, it->shift) / kAttnTile;  // tiles of queries are counted from the segment's first row
-    return max(0, (g.nq + kAttnTile - 1) / kAttnTile - first) * l.group;
+    return sum * l.group + (int64_t)kAttnUnitCost * tiles;
 }
 
 __device__ __forceinline__ int64_t warp_before(int64_t v, int lane, int64_t* total) {
@@ -93,31 +113,60 @@ __device__ __forceinline__ int64_t warp_before(int64_t v, int lane, int64_t* tot
     return s - v;
 }
 
-constexpr int kAttnFewSegs = 1024, kAttnFewItems = 2048;  // kept in shared memory while they are planned
+constexpr int kPlanThreads = 512;
+constexpr int kAttnFewSegs = 512;  // kept in shared memory while they are planned
 
-// One CTA a list. The entries are in the order of the rows: first what each segment has and costs (a warp
-// a segment, its lanes the tiles), then sums over the segments before it, then the entries, then where
-// each CTA begins. Everything follows from the tables alone, so that pieces, and with them the order of
-// sums, are the same every time.
+// One CTA a list. The entries are in the order of the rows: entries and cost of every segment, sums over
+// those before it, then the entries (a warp a segment) and where each CTA begins. Everything follows
+// from the tables alone, so that pieces, and with them the order of sums, are the same every time.
 __device__ __forceinline__ void attn_plan(const AttnPlanArgs& a, int list) {
-    __shared__ int64_t sums[2][32];
-    __shared__ int64_t run[2];
+    constexpr int NW = kPlanThreads / 32;
+    __shared__ int64_t sums[2][NW];
     __shared__ longlong2 few[kAttnFewSegs];
-    __shared__ int64_t begins[kAttnFewItems];  // of the first entries
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const AttnTables& t = a.t;
     const AttnList& l = a.list[list];
-    bool bad = false;
-    for (int64_t s = tid; s < t.nseg; s += 1024) {
+    longlong2* segs = t.nseg <= kAttnFewSegs ? few : l.segs;
+    auto segment = [&](int64_t s, bool* bad) {
         const int64_t q0 = attn_start(t.cu_q, s, t.nseg, t.Rq), q1 = attn_start(t.cu_q, s + 1, t.nseg, t.Rq);
         const int64_t k0 = attn_start(t.cu_k, s, t.nseg, t.Rk), k1 = attn_start(t.cu_k, s + 1, t.nseg, t.Rk);
-        bad |= q0 < 0 || q1 < q0 || q1 > t.Rq || k0 < 0 || k1 < k0 || k1 > t.Rk;
+        *bad |= q0 < 0 || q1 < q0 || q1 > t.Rq || k0 < 0 || k1 < k0 || k1 > t.Rk;
+        *bad |= (s == 0 && (q0 != 0 || k0 != 0)) || (s == t.nseg - 1 && (q1 != t.Rq || k1 != t.Rk));
+        return AttnSegment{(int)q0, (int)(q1 - q0), (int)k0, (int)(k1 - k0)};
+    };
+    auto tiles_of = [&](const AttnSegment& g) { return ((list ? g.nk : g.nq) + l.tile - 1) / l.tile; };
+    bool any_bad = t.nseg == 0 && (t.Rq != 0 || t.Rk != 0);
+    int64_t run[2] = {0, 0};  // entries and cost so far
+    for (int64_t base = 0; base < t.nseg && !any_bad; base += kPlanThreads) {
+        const int64_t s = base + tid;
+        bool bad = false;
+        int64_t v[2] = {0, 0}, all[2];
+        if (s < t.nseg) {
+            const AttnSegment g = segment(s, &bad);
+            if (!bad) {
+                v[0] = tiles_of(g);
+                v[1] = attn_cost(t, l, list, g, (int)v[0]);
+            }
+        }
+        int64_t before[2] = {warp_before(v[0], lane, &all[0]), warp_before(v[1], lane, &all[1])};
+        if (lane == 0) {
+            sums[0][warp] = all[0];
+            sums[1][warp] = all[1];
+        }
+        any_bad = __syncthreads_or(bad);
+        const int warps = (int)min((int64_t)NW, (t.nseg - base + 31) / 32);  // that have segments
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            before[x] += run[x];
+            for (int w = 0; w < warps; ++w) {
+                const int64_t n = sums[x][w];
+                before[x] += w < warp ? n : 0;
+                run[x] += n;
+            }
+        }
+        if (s < t.nseg) segs[s] = make_longlong2(before[0], before[1]);
+        __syncthreads();
     }
-    if (tid == 0) {
-        if (t.cu_q) bad |= __ldg(t.cu_q) != 0 || (int64_t)__ldg(t.cu_q + t.nseg) != t.Rq;
-        if (t.cu_k) bad |= __ldg(t.cu_k) != 0 || (int64_t)__ldg(t.cu_k + t.nseg) != t.Rk;
-    }
-    const bool any_bad = __syncthreads_or(bad);
     if (tid == 0 && list == 0) {
         a.status[0] = any_bad ? kErrSeqlens : 0u;
         a.status[1] = 0u;  // the kernels' word
@@ -125,102 +174,34 @@ __device__ __forceinline__ void attn_plan(const AttnPlanArgs& a, int list) {
         a.header->nwords = 2;
     }
     if (l.items == nullptr) return;
-    longlong2* segs = t.nseg <= kAttnFewSegs ? few : l.segs;
-    if (any_bad) {
-        if (tid == 0) *l.count = 0;
-        for (int c = tid; c <= l.ctas; c += 1024) l.cursors[c] = AttnCursor{0, 0};
-        return;
-    }
-    // Segments base .. base + 31 of a warp's turn, one at a time with their lanes.
-    auto each = [&](auto use) {
-        for (int64_t base = 32 * (int64_t)warp; base < t.nseg; base += 1024) {
-            const int64_t s = base + lane;
-            AttnSegment g{0, 0, 0, 0};
-            if (s < t.nseg) {
-                g.q0 = (int)attn_start(t.cu_q, s, t.nseg, t.Rq);
-                g.nq = (int)attn_start(t.cu_q, s + 1, t.nseg, t.Rq) - g.q0;
-                g.k0 = (int)attn_start(t.cu_k, s, t.nseg, t.Rk);
-                g.nk = (int)attn_start(t.cu_k, s + 1, t.nseg, t.Rk) - g.k0;
-            }
-            for (int i = 0; i < 32 && base + i < t.nseg; ++i) {
-                const AttnSegment one{__shfl_sync(0xFFFFFFFFu, g.q0, i), __shfl_sync(0xFFFFFFFFu, g.nq, i),
-                                      __shfl_sync(0xFFFFFFFFu, g.k0, i), __shfl_sync(0xFFFFFFFFu, g.nk, i)};
-                const int tiles = ((list ? one.nk : one.nq) + l.tile - 1) / l.tile;
-                use(base + i, one, tiles);
-            }
-        }
-    };
-    each([&](int64_t s, const AttnSegment& g, int tiles) {
-        int64_t cost = 0, all;
-        for (int i = lane; i < tiles; i += 32) {
-            AttnItem it;
-            cost += attn_steps(t, l, list, g, i * l.tile, &it) + kAttnUnitCost;
-        }
-        warp_before(cost, lane, &all);
-        if (lane == 0) segs[s] = make_longlong2(tiles, all);
-    });
-    if (tid < 2) run[tid] = 0;
-    __syncthreads();
-    for (int64_t base = 0; base < t.nseg; base += 1024) {
-        const int64_t s = base + tid;
-        const longlong2 v = s < t.nseg ? segs[s] : make_longlong2(0, 0);
-        int64_t all[2], before[2] = {warp_before(v.x, lane, &all[0]), warp_before(v.y, lane, &all[1])};
-        if (lane == 0) {
-            sums[0][warp] = all[0];
-            sums[1][warp] = all[1];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            before[x] += run[x];
-            for (int w = 0; w < warp; ++w) before[x] += sums[x][w];
-        }
-        __syncthreads();
-        if (tid == 1023) {
-            run[0] = before[0] + v.x;
-            run[1] = before[1] + v.y;
-        }
-        if (s < t.nseg) segs[s] = make_longlong2(before[0], before[1]);
-        __syncthreads();
-    }
-    const int64_t count = min(run[0], l.most), total = run[1];
+    const int64_t count = any_bad ? 0 : min(run[0], l.most), total = any_bad ? 0 : run[1];
     if (tid == 0) *l.count = (int32_t)count;
-    each([&](int64_t s, const AttnSegment& g, int tiles) {
-        const longlong2 before = segs[s];
-        int64_t cost = before.y;
-        for (int i0 = 0; i0 < tiles; i0 += 32) {
-            const int i = i0 + lane;
-            AttnItem it{};
-            const int64_t mine = i < tiles ? attn_steps(t, l, list, g, i * l.tile, &it) + kAttnUnitCost : 0;
-            int64_t all;
-            it.before = cost + warp_before(mine, lane, &all);
-            cost += all;
-            const int64_t at = before.x + i;
-            if (i < tiles && at < l.most && ADALN_IN_ATTN(at >= 0)) {
-                l.items[at] = it;
-                if (at < kAttnFewItems) begins[at] = it.before;
-            }
-        }
-    });
-    __syncthreads();
     // CTA c begins at cost c / ctas of all heads' together.
-    auto begin = [&](int64_t i) { return i < kAttnFewItems ? begins[i] : l.items[i].before; };
     const int64_t every = total * l.heads;
-    for (int c = tid; c <= l.ctas; c += 1024) {
+    for (int c = tid; c <= l.ctas; c += kPlanThreads) {
         AttnCursor cur{(int32_t)(count * l.heads), 0};
         if (c < l.ctas && total > 0) {
             const int64_t x = every / l.ctas * c + every % l.ctas * c / l.ctas;
-            const int64_t head = x / total, in = x % total;
-            int64_t lo = 0, hi = count - 1;  // the last entry that begins at or before `in`
+            const int64_t head = x / total, in = x - head * total;
+            int64_t lo = 0, hi = t.nseg - 1;  // the last segment that begins at or before `in`
             while (lo < hi) {
                 const int64_t mid = (lo + hi + 1) >> 1;
-                if (begin(mid) <= in) lo = mid;
+                if (segs[mid].y <= in) lo = mid;
                 else hi = mid - 1;
             }
-            const int64_t end = lo + 1 < count ? begin(lo + 1) : total;
-            const int n = (int)(end - begin(lo)) - kAttnUnitCost;
-            int tile = (int)(in - begin(lo)) - kAttnUnitCost / 2;
-            cur.unit = (int32_t)(head * count + lo);
+            bool bad = false;
+            const AttnSegment g = segment(lo, &bad);
+            const int64_t rest = in - segs[lo].y;
+            int first = 0, last = tiles_of(g) - 1;  // and its last entry that does
+            while (first < last) {
+                const int mid = (first + last + 1) >> 1;
+                if (attn_cost(t, l, list, g, mid) <= rest) first = mid;
+                else last = mid - 1;
+            }
+            const int64_t begin = attn_cost(t, l, list, g, first);
+            const int n = (int)(attn_cost(t, l, list, g, first + 1) - begin) - kAttnUnitCost;
+            int tile = (int)(rest - begin) - kAttnUnitCost / 2;
+            cur.unit = (int32_t)(head * count + segs[lo].x + first);
             if (tile < kAttnMinPiece) tile = 0;
             if (tile > 0 && n - tile < kAttnMinPiece) {
                 tile = 0;
@@ -230,48 +211,61 @@ __device__ __forceinline__ void attn_plan(const AttnPlanArgs& a, int list) {
         }
         l.cursors[c] = cur;
     }
+    if (any_bad) return;
+    for (int64_t s = NW - 1 - warp; s < t.nseg; s += NW) {  // the first warps have the cursors
+        bool bad = false;
+        const AttnSegment g = segment(s, &bad);
+        const int64_t before = segs[s].x;
+        const int tiles = tiles_of(g);
+        for (int i = lane; i < tiles; i += 32)
+            if (before + i < l.most && ADALN_IN_ATTN(before >= 0)) l.items[before + i] = attn_entry(t, l, list, g, i * l.tile);
+    }
 }
 
-// delta = dout . o of every row and head, and lse in units of log 2: 16 lanes a row of a head.
+// delta = dout . o of every row and head, and lse in units of log 2: a warp a row, 16 lanes a head.
 __device__ __forceinline__ void attn_delta(const AttnDeltaArgs& a, int64_t block, int64_t blocks) {
-    constexpr int U = 4;
-    const int lane = threadIdx.x & 15, vecs = a.d / 8;
-    const int64_t total = a.Rq * a.Hq, step = blocks * 64;
-    const int64_t first = block * 64 + (threadIdx.x >> 4);
-    for (int64_t base = first - (first & 1); base < total; base += U * step) {  // both groups of a warp together
-        uint4 x[U], y[U];
+    constexpr int U = 4;  // pairs of heads on their way
+    const int lane = threadIdx.x & 15, group = threadIdx.x >> 4 & 1, vecs = a.d / 8;
+    constexpr int NW = kPlanThreads / 32;
+    for (int64_t r = block * NW + (threadIdx.x >> 5); r < a.Rq; r += blocks * NW) {
+        const __nv_bfloat16* x0 = reinterpret_cast<const __nv_bfloat16*>(a.dout) + r * a.do_ld + 8 * lane;
+        const __nv_bfloat16* y0 = reinterpret_cast<const __nv_bfloat16*>(a.o) + r * a.o_ld + 8 * lane;
+        for (int h0 = group; h0 - group < a.Hq; h0 += 2 * U) {
+            uint4 x[U], y[U];
+            float lse[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int64_t i = base + (first & 1) + j * step;
-            x[j] = y[j] = make_uint4(0, 0, 0, 0);
-            if (i < total && lane < vecs && ADALN_IN_ATTN(i >= 0)) {
-                const int64_t r = i / a.Hq, h = i % a.Hq;
-                x[j] = ld_stream(reinterpret_cast<const __nv_bfloat16*>(a.dout) + r * a.do_ld + h * a.d + 8 * lane);
-                y[j] = ld_stream(reinterpret_cast<const __nv_bfloat16*>(a.o) + r * a.o_ld + h * a.d + 8 * lane);
+            for (int j = 0; j < U; ++j) {
+                const int h = h0 + 2 * j;
+                x[j] = y[j] = make_uint4(0, 0, 0, 0);
+                lse[j] = 0.0f;
+                if (h < a.Hq && lane < vecs && ADALN_IN_ATTN(r >= 0 && r < a.Rq)) {
+                    x[j] = ld_stream(x0 + (int64_t)h * a.d);
+                    y[j] = __ldcg(reinterpret_cast<const uint4*>(y0 + (int64_t)h * a.d));  // of a kernel that may be close ahead
+                    if (lane == 0) lse[j] = __ldcg(a.lse + (int64_t)h * a.Rq + r);
+                }
             }
-        }
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int64_t i = base + (first & 1) + j * step;
-            f2r p[4], q[4], sum = kPairZero;
-            Io<__nv_bfloat16>::unpackp(x[j], p);
-            Io<__nv_bfloat16>::unpackp(y[j], q);
+            for (int j = 0; j < U; ++j) {
+                const int h = h0 + 2 * j;
+                f2r p[4], q[4], sum = kPairZero;
+                Io<__nv_bfloat16>::unpackp(x[j], p);
+                Io<__nv_bfloat16>::unpackp(y[j], q);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum = p_fma(p[e], q[e], sum);
-            float v = p_hsum(sum);
+                for (int e = 0; e < 4; ++e) sum = p_fma(p[e], q[e], sum);
+                float v = p_hsum(sum);
 #pragma unroll
-            for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            if (lane == 0 && i < total && ADALN_IN_ATTN(i >= 0)) {
-                const int64_t at = i % a.Hq * a.Rq + i / a.Hq;
-                a.delta[at] = v;
-                a.lse2[at] = a.lse[at] * kLog2e;
+                for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+                if (lane == 0 && h < a.Hq && ADALN_IN_ATTN(r < a.Rq)) {
+                    a.delta[(int64_t)h * a.Rq + r] = v;
+                    a.lse2[(int64_t)h * a.Rq + r] = lse[j] * kLog2e;
+                }
             }
         }
     }
 }
 
 // The work lists, a CTA each, and beside them, backward, delta.
-__global__ void __launch_bounds__(1024) attn_prepare_kernel(const __grid_constant__ AttnPlanArgs p,
+__global__ void __launch_bounds__(kPlanThreads) attn_prepare_kernel(const __grid_constant__ AttnPlanArgs p,
                                                             const __grid_constant__ AttnDeltaArgs d, int lists) {
     pdl_begin();
     if ((int)blockIdx.x < lists)
@@ -822,72 +816,100 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     if (l.items == nullptr || c == 0 || c >= l.ctas) return;
     const AttnCursor cur = attn_cursor(l, c), prev = attn_cursor(l, c - 1);
     if (cur.tile == 0 || (prev.unit == cur.unit && prev.tile > 0)) return;
-    // The pieces: CTA c - 1's, which begins the unit, then of every CTA that begins inside it and has
-    // steps of it, up to `last`.
-    int last = c;
-    while (last + 1 < l.ctas) {
-        const AttnCursor q = attn_cursor(l, last + 1);
-        if (q.unit != cur.unit) break;
-        ++last;
+    // The pieces: CTA c - 1's, which begins the unit, then of every CTA that begins inside it (one of two that
+    // begin at one place has none).
+    __shared__ int16_t slots[kAttnMaxCtas + 1];
+    __shared__ float weight[BWD ? 1 : 32][kAttnMaxCtas + 1];  // forward: of a row's pieces, 0 for none
+    int begun = 0;
+    for (int x0 = c + 1; x0 < l.ctas; x0 += 256) {
+        const int x = x0 + threadIdx.x;
+        begun += __syncthreads_count(x < l.ctas && attn_cursor(l, x).unit == cur.unit);
     }
+    const int pieces = 2 + begun;
+    for (int x = threadIdx.x; x < pieces; x += 256) {
+        const int at = c - 1 + x;
+        const bool none = x > 0 && x < pieces - 1 && attn_cursor(l, at).tile == attn_cursor(l, at + 1).tile;
+        slots[x] = none ? -1 : (int16_t)(x == 0 ? 2 * at + 1 : 2 * at);
+    }
+    __syncthreads();
     const int count = __ldcg(l.count), head = cur.unit / count;
     const AttnItem it = attn_item(l, cur.unit % count);
     const int vecs = a.d / 8, rows = a.slot_rows[list], parts = BWD && list == 1 ? 2 : 1;
     const int64_t plane = (int64_t)rows * a.d;
     const float sl2 = a.scale * kLog2e;
-    // The piece of CTA x, or -1: two CTAs that begin at one place, the first has none.
-    auto slot = [&](int x) {
-        if (x == c - 1) return 2 * x + 1;
-        if (x < last && attn_cursor(l, x).tile == attn_cursor(l, x + 1).tile) return -1;
-        return 2 * x;
-    };
     const int per = (rows + 7) / 8, items = per * vecs * parts;
-    for (int i = threadIdx.x; i < items; i += 256) {
-        // Rows side by side, as the pieces have them.
-        const int row = (int)blockIdx.y * per + i % per, v = i / per % vecs, part = i / per / vecs;
-        const int64_t at = (int64_t)it.row0 + row;
-        if (row >= it.rows || !ADALN_IN_ATTN(row < rows)) continue;
-        float top = neg_inf(), sum = 0.0f, o[8] = {};
-        if (!BWD) {
-            for (int x = c - 1; x <= last; ++x) {
-                const int s = slot(x);
-                if (s < 0) continue;
-                const float2 ml = __ldcg(a.ml + (int64_t)s * rows + row);
+    if (!BWD) {
+        // A warp a row, a lane a piece: the maximum, the weights, the sum.
+        const int lane = threadIdx.x & 31;
+        for (int k = threadIdx.x >> 5; k < per; k += 8) {
+            const int row = (int)blockIdx.y * per + k;
+            const int64_t at = (int64_t)it.row0 + row;
+            if (row >= it.rows || !ADALN_IN_ATTN(row < rows && k < 32)) continue;
+            float top = neg_inf(), sum = 0.0f;
+            auto load = [&](int x) {
+                const int s = x < pieces ? slots[x] : -1;
+                return s < 0 ? make_float2(0.0f, 0.0f) : __ldcg(a.ml + (int64_t)s * rows + row);
+            };
+            float2 first = load(lane);  // (sum 0: the row sees nothing of the piece)
+            for (int x = lane; x < pieces; x += 32) {
+                const float2 ml = x == lane ? first : load(x);
                 if (ml.y != 0.0f) top = fmaxf(top, ml.x);
             }
-        }
-        for (int x = c - 1; x <= last; ++x) {
-            const int s = slot(x);
-            if (s < 0) continue;
-            float w = 1.0f;
-            if (!BWD) {
-                const float2 ml = __ldcg(a.ml + (int64_t)s * rows + row);
-                if (ml.y == 0.0f) continue;  // a piece that this row sees nothing of
-                if (top != neg_inf()) w = exp2_ftz((ml.x - top) * sl2);
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            for (int x = lane; x < pieces; x += 32) {
+                const float2 ml = x == lane ? first : load(x);
+                const float w = ml.y == 0.0f ? 0.0f : top == neg_inf() ? 1.0f : exp2_ftz((ml.x - top) * sl2);
+                weight[k][x] = ml.y == 0.0f ? 0.0f : w;
                 sum = fmaf(w, ml.y, sum);
             }
-            const float4* p = reinterpret_cast<const float4*>(a.part[list] + ((int64_t)s * parts + part) * plane) +
-                              (int64_t)2 * v * rows + row;
-            const float4 f = __ldcg(p), g = __ldcg(p + rows);
-            o[0] = fmaf(w, f.x, o[0]);
-            o[1] = fmaf(w, f.y, o[1]);
-            o[2] = fmaf(w, f.z, o[2]);
-            o[3] = fmaf(w, f.w, o[3]);
-            o[4] = fmaf(w, g.x, o[4]);
-            o[5] = fmaf(w, g.y, o[5]);
-            o[6] = fmaf(w, g.z, o[6]);
-            o[7] = fmaf(w, g.w, o[7]);
+            float v[1] = {sum};
+            warp_sum(v);
+            sum = v[0];
+            for (int x = lane; x < pieces; x += 32) weight[k][x] *= sum == 0.0f ? 0.0f : 1.0f / sum;
+            if (lane == 0) a.lse[(int64_t)head * a.Rq + at] = sum == 0.0f ? neg_inf() : fmaf(top, a.scale, logf(sum));
         }
-        float f = a.scale;  // dq and dk
-        if (!BWD) f = sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (BWD && list == 1 && part == 0) f = 1.0f;  // dv
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < items; i += 256) {
+        // Rows side by side, as the pieces have them.
+        const int k = i % per, row = (int)blockIdx.y * per + k, v = i / per % vecs, part = i / per / vecs;
+        const int64_t at = (int64_t)it.row0 + row;
+        if (row >= it.rows || !ADALN_IN_ATTN(row < rows)) continue;
+        float o[8] = {};
+        for (int x0 = 0; x0 < pieces; x0 += 4) {  // four pieces on their way
+            float4 f[4], g[4];
+            float w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int x = x0 + j, s = x < pieces ? slots[x] : -1;
+                w[j] = s < 0 ? 0.0f : BWD ? 1.0f : weight[BWD ? 0 : k][x];
+                f[j] = g[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (w[j] == 0.0f) continue;
+                const float4* p = reinterpret_cast<const float4*>(a.part[list] + ((int64_t)s * parts + part) * plane) +
+                                  (int64_t)2 * v * rows + row;
+                f[j] = __ldcg(p);
+                g[j] = __ldcg(p + rows);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                o[0] = fmaf(w[j], f[j].x, o[0]);
+                o[1] = fmaf(w[j], f[j].y, o[1]);
+                o[2] = fmaf(w[j], f[j].z, o[2]);
+                o[3] = fmaf(w[j], f[j].w, o[3]);
+                o[4] = fmaf(w[j], g[j].x, o[4]);
+                o[5] = fmaf(w[j], g[j].y, o[5]);
+                o[6] = fmaf(w[j], g[j].z, o[6]);
+                o[7] = fmaf(w[j], g[j].w, o[7]);
+            }
+        }
+        const bool dv = BWD && list == 1 && part == 0;
+        const float f = !BWD || dv ? 1.0f : a.scale;
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = pack2(o[2 * j] * f, o[2 * j + 1] * f);
-        const bool dv = BWD && list == 1 && part == 0;
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(dv ? a.dv : a.out[list]) + at * (dv ? a.dv_ld : a.ld[list]);
         st_vec(out + (int64_t)head * a.d + 8 * v, make_uint4(w[0], w[1], w[2], w[3]));
-        if (!BWD && v == 0) a.lse[(int64_t)head * a.Rq + at] = sum == 0.0f ? neg_inf() : fmaf(top, a.scale, logf(sum));
     }
 }
 
@@ -1564,9 +1586,9 @@ cudaError_t launch_attn_prepare(const AttnPlanArgs& plan, const AttnDeltaArgs& d
     AttnPlanArgs p = plan;
     AttnDeltaArgs d = delta;
     int lists = p.list[1].items ? 2 : 1;
-    const unsigned ctas = d.delta && d.Rq > 0 ? cap((d.Rq * d.Hq + 255) / 256, 2 * (int64_t)sms) : 0;
+    const unsigned ctas = d.delta && d.Rq > 0 ? cap((d.Rq + kPlanThreads / 32 - 1) / (kPlanThreads / 32), 4 * (int64_t)sms) : 0;
     void* params[] = {&p, &d, &lists};
-    return launch_dependent(reinterpret_cast<const void*>(&attn_prepare_kernel), dim3(lists + ctas), dim3(1024), params,
+    return launch_dependent(reinterpret_cast<const void*>(&attn_prepare_kernel), dim3(lists + ctas), dim3(kPlanThreads), params,
                             0, stream);
 }
 

@@ -9,6 +9,7 @@ namespace adaln {
 
 constexpr int kAttnTile = 128;       // rows of an operand tile, keys of a step
 constexpr int kAttnMaxD = 128;       // elements of a head
+constexpr int kAttnMaxCtas = 256;    // of one launch
 constexpr int kAttnMaxRows = 1 << 30;  // of either side: row and key numbers and their sums are 32 bits
 
 // One tile of rows of a segment (of queries; of keys for dk and dv) and what it meets.
@@ -21,7 +22,7 @@ struct AttnItem {
     // of the tile is seen by the queries i >= max(0, shift + c) of its segment.
     int32_t shift;
     int32_t end;     // the segment's last row of the other side is the tensor's last: nothing follows
-    int64_t before;  // cost of the items before it
+    int32_t pad[2];
 };
 
 // A unit of work is an item and a head: unit u is head u / items, item u % items. Its cost is its
@@ -47,7 +48,7 @@ struct AttnTables {
 struct AttnList {
     AttnItem* items;
     int32_t* count;       // its entries
-    longlong2* segs;      // [nseg]: entries and cost of a segment, then of those before it
+    longlong2* segs;      // [nseg]: entries and cost of the segments before each
     AttnCursor* cursors;  // [ctas + 1]: where each CTA begins
     int64_t most;         // entries it has room for
     int tile;             // rows an entry
