@@ -10,8 +10,10 @@
 //
 // Bound by HBM. A power of two of lanes shares a head, eight elements a lane, so that a head's sums
 // are a few shuffles and a pair never leaves its lane. A group of lanes takes a token and goes through
-// its heads, four (backward: two) at a time on their way: the token's angles are computed once for all
-// of them. Short batches go in items of fewer heads, so that every SM has some.
+// its heads, several on their way at once: the token's angles are computed once for all of them. Short
+// batches go in items of fewer heads (rope_items). 32760 x 12 x 128 (queries and keys each), bf16: 75 us
+// forward (5.4 TB/s), 118 us backward (5.1 TB/s); 40 heads 225 us (6.0 TB/s); fp32 128 and 195 us
+// (6.3 and 6.2 TB/s). Heads whose eighths are no power of two leave lanes idle (15000 x 12 x 72: 3.3 TB/s).
 //
 // Angles: a position times a frequency is far more than fp32 holds (position 500,000 at frequency 1 is
 // off by 0.03 rad). Frequencies are turns as binary fractions of 64 bits; the product with the integer
@@ -39,49 +41,40 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// (a, b) -> (a c - b s, a s + b c)
-__device__ __forceinline__ f2r turn(f2r x, float c, float s) {
-    const float2 f = p_get(x);
-    return p_make(fmaf(-f.y, s, f.x * c), fmaf(f.x, s, f.y * c));
+// Heads on their way at once, and CTAs an SM that the registers are to hold. Forward, bf16, 32760 x 40 x
+// 128: four heads and three CTAs 225 us; two and four 256, six and three 231, eight and two 218 (but 81
+// instead of 75 us for 12 heads). Backward, bf16, 32760 x 12 x 128: four and two 118 us; two and two 141,
+// two and three 140, six and two 114 (but slower with few rows). fp32 backward, 32760 x 12 x 128: two and
+// two 195 us, four and one 229.
+template <typename T, bool BWD>
+__host__ __device__ constexpr int rope_heads() { return sizeof(T) == 4 && BWD ? 2 : 4; }
+template <typename T, bool BWD>
+__host__ __device__ constexpr int rope_ctas() { return sizeof(T) == 2 && !BWD ? 3 : 2; }
+
+template <typename T>
+__device__ __forceinline__ float inv_sqrt(float v) {
+    return sizeof(T) == 2 ? rsqrtf(v) : __frsqrt_rn(v);  // (2 steps of fp32 are nothing to bf16)
 }
 
+// What a token's heads share is in registers: the angles' cosines and sines, forward times the weights.
 template <typename T, int GL, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, rope_ctas<T, BWD>()) rope_kernel(const __grid_constant__ RopeArgs a) {
     using L = Lane<T>;
-    constexpr int U = BWD ? 2 : 4;  // heads on their way
+    constexpr int U = rope_heads<T, BWD>();
     constexpr int GROUPS = kRopeThreads / GL;
     const int lane = threadIdx.x % GL, group = threadIdx.x / GL;
     const int vecs = a.d / L::VE;
-    bool on[L::NV];
-    unsigned long long freq[L::NV][L::NP];
-    int axis[L::NV][L::NP];
-#pragma unroll
-    for (int j = 0; j < L::NV; ++j) {
-        const int v = lane + j * GL;
-        on[j] = v < vecs;
-#pragma unroll
-        for (int p = 0; p < L::NP; ++p) {
-            freq[j][p] = on[j] ? a.freq[v * L::NP + p] : 0;
-            axis[j][p] = on[j] ? a.axis[v * L::NP + p] : 0;
-        }
-    }
     const float inv_d = 1.0f / (float)a.d;
     pdl_begin();
-    // Both weights, as they come.
-    uint4 w[2][L::NV];
     [[maybe_unused]] f2r dw[2][L::NV][L::NP];
+    if constexpr (BWD) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 2; ++s) {
 #pragma unroll
-        for (int j = 0; j < L::NV; ++j) {
-            f2r one[L::NP];
+            for (int j = 0; j < L::NV; ++j) {
 #pragma unroll
-            for (int p = 0; p < L::NP; ++p) {
-                one[p] = p_splat(1.0f);
-                if (BWD) dw[s][j][p] = kPairZero;
+                for (int p = 0; p < L::NP; ++p) dw[s][j][p] = kPairZero;
             }
-            w[s][j] = Io<T>::packp(one);
-            if (a.side[s].weight && on[j]) w[s][j] = ld_keep(reinterpret_cast<const uint4*>(a.side[s].weight) + lane + j * GL);
         }
     }
 
@@ -92,18 +85,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     for (int64_t off = 0; warp_first + off < items; off += step) {
         const int64_t item = first + off;
         const bool live = item < items;
-        const int64_t r = live ? item / a.chunks : 0;
-        const int h0 = live ? (int)(item % a.chunks) * a.chunk : 0;
+        const int64_t r = !live ? 0 : a.chunks == 1 ? item : item / a.chunks;
+        const int h0 = !live || a.chunks == 1 ? 0 : (int)(item % a.chunks) * a.chunk;
         float c[L::NV][L::NP], sn[L::NV][L::NP];
 #pragma unroll
         for (int j = 0; j < L::NV; ++j) {
+            const int v = lane + j * GL;
 #pragma unroll
             for (int p = 0; p < L::NP; ++p) {
                 c[j][p] = 1.0f;
                 sn[j][p] = 0.0f;
-                if (a.pos && ADALN_IN_HEADS(r < a.R)) {
-                    const long long at = __ldg(a.pos + r * a.naxes + axis[j][p]);
-                    const int turn32 = (int)(((unsigned long long)at * freq[j][p]) >> 32);
+                if (a.pos && v < vecs && ADALN_IN_HEADS(r < a.R)) {
+                    const long long at = __ldg(a.pos + r * a.naxes + a.axis[v * L::NP + p]);
+                    const int turn32 = (int)(((unsigned long long)at * a.freq[v * L::NP + p]) >> 32);
                     sincospif((float)turn32 * 0x1p-31f, &sn[j][p], &c[j][p]);  // half turns
                 }
             }
@@ -112,85 +106,96 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         auto heads = [&](int s, int b, int e) {
             const RopeSide& sd = a.side[s];
             const int most = __reduce_max_sync(0xFFFFFFFFu, live ? e - b : 0);
+            if (most <= 0) return;
+            f2r w[L::NV][L::NP];
+#pragma unroll
+            for (int j = 0; j < L::NV; ++j) {
+#pragma unroll
+                for (int p = 0; p < L::NP; ++p) w[j][p] = p_splat(1.0f);
+                if (sd.weight && lane + j * GL < vecs)
+                    Io<T>::unpackp(ld_keep(reinterpret_cast<const uint4*>(sd.weight) + lane + j * GL), w[j]);
+            }
+            // Forward: out = x0 * ac + x1 * bd, what the pair's elements have of both results.
+            [[maybe_unused]] float2 ac[L::NV][L::NP], bd[L::NV][L::NP];
+            if constexpr (!BWD) {
+#pragma unroll
+                for (int j = 0; j < L::NV; ++j) {
+#pragma unroll
+                    for (int p = 0; p < L::NP; ++p) {
+                        const float2 f = p_get(w[j][p]);
+                        ac[j][p] = make_float2(f.x * c[j][p], f.x * sn[j][p]);
+                        bd[j][p] = make_float2(-f.y * sn[j][p], f.y * c[j][p]);
+                    }
+                }
+            }
+            const T* x0 = reinterpret_cast<const T*>(sd.x) + r * sd.x_ld + lane * L::VE;
+            [[maybe_unused]] const T* y0 = reinterpret_cast<const T*>(sd.dy) + r * sd.dy_ld + lane * L::VE;
+            T* o0 = reinterpret_cast<T*>(sd.out) + r * sd.out_ld + lane * L::VE;
             for (int i = 0; i < most; i += U) {
                 uint4 x[U][L::NV];
                 [[maybe_unused]] uint4 y[U][L::NV];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int h = b + i + u;
+                    const int h = b + i + u, at = h * a.d;
 #pragma unroll
                     for (int j = 0; j < L::NV; ++j) {
                         x[u][j] = make_uint4(0, 0, 0, 0);
                         if (BWD) y[u][j] = x[u][j];
-                        if (live && h < e && on[j] && ADALN_IN_HEADS(r >= 0 && r < a.R && h >= 0 && h < sd.heads)) {
-                            const int64_t at = (int64_t)h * a.d + (lane + j * GL) * L::VE;
-                            if (!BWD || a.norm) x[u][j] = ld_stream(reinterpret_cast<const T*>(sd.x) + r * sd.x_ld + at);
-                            if (BWD) y[u][j] = ld_stream(reinterpret_cast<const T*>(sd.dy) + r * sd.dy_ld + at);
+                        if (live && h < e && lane + j * GL < vecs && ADALN_IN_HEADS(r < a.R && h >= 0 && h < sd.heads)) {
+                            if (!BWD || a.norm) x[u][j] = ld_stream(x0 + at + j * GL * L::VE);
+                            if (BWD) y[u][j] = ld_stream(y0 + at + j * GL * L::VE);
                         }
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int h = b + i + u;
-                    f2r f[L::NV][L::NP], g[L::NV][L::NP];
+                    const int h = b + i + u, at = h * a.d;
+                    f2r f[L::NV][L::NP];
+                    [[maybe_unused]] f2r g[L::NV][L::NP], dy[L::NV][L::NP];
                     f2r ss = kPairZero, gs = kPairZero;
 #pragma unroll
                     for (int j = 0; j < L::NV; ++j) {
                         Io<T>::unpackp(x[u][j], f[j]);
-                        Io<T>::unpackp(w[s][j], g[j]);
-                        if (BWD) {
-                            f2r dy[L::NP];
-                            Io<T>::unpackp(y[u][j], dy);
+                        if (BWD) Io<T>::unpackp(y[u][j], dy[j]);
 #pragma unroll
-                            for (int p = 0; p < L::NP; ++p) {
-                                dy[p] = turn(dy[p], c[j][p], -sn[j][p]);
-                                g[j][p] = p_mul(g[j][p], dy[p]);
+                        for (int p = 0; p < L::NP; ++p) {
+                            ss = p_fma(f[j][p], f[j][p], ss);
+                            if constexpr (BWD) {
+                                const float2 d = p_get(dy[j][p]);
+                                dy[j][p] = p_make(fmaf(d.y, sn[j][p], d.x * c[j][p]), fmaf(d.y, c[j][p], -d.x * sn[j][p]));
+                                g[j][p] = p_mul(w[j][p], dy[j][p]);
                                 gs = p_fma(g[j][p], f[j][p], gs);
                             }
-#pragma unroll
-                            for (int p = 0; p < L::NP; ++p) ss = p_fma(f[j][p], f[j][p], ss);
-                        } else {
-#pragma unroll
-                            for (int p = 0; p < L::NP; ++p) ss = p_fma(f[j][p], f[j][p], ss);
                         }
                     }
-                    float rstd = 1.0f;
-                    if (a.norm) rstd = __frsqrt_rn(fmaf(group_sum<GL>(p_hsum(ss)), inv_d, a.eps));
+                    float rstd = 1.0f, m = 0.0f;
+                    if (a.norm) {
+                        rstd = inv_sqrt<T>(fmaf(group_sum<GL>(p_hsum(ss)), inv_d, a.eps));
+                        if (BWD) m = group_sum<GL>(p_hsum(gs)) * rstd * inv_d;
+                    }
                     const f2r rs = p_splat(rstd);
-                    if constexpr (!BWD) {
+                    [[maybe_unused]] const f2r nm = p_splat(-m);
 #pragma unroll
-                        for (int j = 0; j < L::NV; ++j) {
-                            f2r o[L::NP];
+                    for (int j = 0; j < L::NV; ++j) {
+                        f2r o[L::NP];
 #pragma unroll
-                            for (int p = 0; p < L::NP; ++p)
-                                o[p] = turn(a.norm ? p_mul(p_mul(f[j][p], rs), g[j][p]) : f[j][p], c[j][p], sn[j][p]);
-                            if (live && h < e && on[j] && ADALN_IN_HEADS(r < a.R && h < sd.heads))
-                                st_vec(reinterpret_cast<T*>(sd.out) + r * sd.out_ld + (int64_t)h * a.d +
-                                           (lane + j * GL) * L::VE,
-                                       Io<T>::packp(o));
-                        }
-                    } else {
-                        float m = 0.0f;
-                        if (a.norm) m = group_sum<GL>(p_hsum(gs)) * rstd * inv_d;
-                        const f2r nm = p_splat(-m);
-#pragma unroll
-                        for (int j = 0; j < L::NV; ++j) {
-                            f2r o[L::NP], dy[L::NP];
-                            Io<T>::unpackp(y[u][j], dy);
-#pragma unroll
-                            for (int p = 0; p < L::NP; ++p) {
-                                const f2r xhat = p_mul(f[j][p], rs);
+                        for (int p = 0; p < L::NP; ++p) {
+                            if constexpr (!BWD) {
+                                const float2 e2 = p_get(f[j][p]);
+                                o[p] = p_mul(p_make(fmaf(e2.y, bd[j][p].x, e2.x * ac[j][p].x),
+                                                    fmaf(e2.y, bd[j][p].y, e2.x * ac[j][p].y)),
+                                             rs);
+                            } else {
                                 o[p] = g[j][p];
                                 if (a.norm) {
-                                    dw[s][j][p] = p_fma(turn(dy[p], c[j][p], -sn[j][p]), xhat, dw[s][j][p]);
+                                    const f2r xhat = p_mul(f[j][p], rs);
+                                    dw[s][j][p] = p_fma(dy[j][p], xhat, dw[s][j][p]);
                                     o[p] = p_mul(rs, p_fma(xhat, nm, g[j][p]));
                                 }
                             }
-                            if (live && h < e && on[j] && ADALN_IN_HEADS(r < a.R && h < sd.heads))
-                                st_vec(reinterpret_cast<T*>(sd.out) + r * sd.out_ld + (int64_t)h * a.d +
-                                           (lane + j * GL) * L::VE,
-                                       Io<T>::packp(o));
                         }
+                        if (live && h < e && lane + j * GL < vecs && ADALN_IN_HEADS(r < a.R && h < sd.heads))
+                            st_vec(o0 + at + j * GL * L::VE, Io<T>::packp(o));
                     }
                 }
             }
