@@ -29,6 +29,9 @@
 #include "attn.h"
 #include "tensor.cuh"
 
+#ifndef DQK
+#define DQK 3
+#endif
 namespace adaln {
 
 #define ADALN_IN_ATTN(cond) ADALN_IN(::adaln::kDbgAttn, cond)
@@ -44,8 +47,12 @@ constexpr uint32_t kAttnOut = 32 * 128;  // 32 rows of 64 elements
 template <int DP, int KIND>
 struct AttnShape {
     static constexpr uint32_t kTile = DP / 64 * kPanel;
-    static constexpr int kStages = DP == 128 ? (KIND == kAttnDq ? 5 : 4) : 8;
-    static constexpr size_t kSmem = 1024 + (2 + kStages) * (size_t)kTile + (KIND == kAttnFwd ? 8 * kAttnOut : 0);
+    static constexpr int kStages = DP == 128 ? (KIND == kAttnFwd ? 4 : 5) : 8;
+    static constexpr uint32_t kTiles = (2 + kStages) * kTile;
+    // dk and dv keep nothing in static shared memory: the dynamic memory then begins on a 1024-byte
+    // boundary, without which a fifth stage would not fit. Behind the tiles: barriers, statistics.
+    static constexpr size_t kSmem = KIND == kAttnDkv ? kTiles + 256 + 2048
+                                                     : 1024 + kTiles + (KIND == kAttnFwd ? 8 * kAttnOut : 0);
 };
 
 // ---- work list -----------------------------------------------------------------------------
@@ -78,7 +85,7 @@ __device__ __forceinline__ AttnItem attn_entry(const AttnTables& t, const AttnLi
 }
 
 // Cost of a segment's first `tiles` entries: their steps (as the kernels count them from the entry) and
-// kAttnUnitCost each, summed in closed form.
+// l.unit_cost each, summed in closed form.
 __device__ __forceinline__ int64_t attn_cost(const AttnTables& t, const AttnList& l, int list, const AttnSegment& g,
                                              int tiles) {
     const int len = list ? g.nk : g.nq, other = list ? g.nq : g.nk;
@@ -99,7 +106,7 @@ __device__ __forceinline__ int64_t attn_cost(const AttnTables& t, const AttnList
         const int64_t whole = min(max(1 - b, (int64_t)0), n), end = min(n, max(whole, steps - b));
         sum = whole * steps + (end - whole) * (steps - b) - (end * (end - 1) - whole * (whole - 1)) / 2;
     }
-    return sum * l.group + (int64_t)kAttnUnitCost * tiles;
+    return sum * l.group + (int64_t)l.unit_cost * tiles;
 }
 
 __device__ __forceinline__ int64_t warp_before(int64_t v, int lane, int64_t* total) {
@@ -199,8 +206,8 @@ __device__ __forceinline__ void attn_plan(const AttnPlanArgs& a, int list) {
                 else last = mid - 1;
             }
             const int64_t begin = attn_cost(t, l, list, g, first);
-            const int n = (int)(attn_cost(t, l, list, g, first + 1) - begin) - kAttnUnitCost;
-            int tile = (int)(rest - begin) - kAttnUnitCost / 2;
+            const int n = (int)(attn_cost(t, l, list, g, first + 1) - begin) - l.unit_cost;
+            int tile = (int)(rest - begin) - l.unit_cost / 2;
             cur.unit = (int32_t)(head * count + segs[lo].x + first);
             if (tile < kAttnMinPiece) tile = 0;
             if (tile > 0 && n - tile < kAttnMinPiece) {
@@ -933,7 +940,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     using S = AttnShape<DP, kAttnDq>;
     // Keys are held from their scores to dq, two steps on; values from dp of their step alone. With a ring
     // for both, a values' tile would wait for the keys three tiles before it.
-    constexpr int KS = DP == 128 ? 3 : 4, VS = DP == 128 ? 2 : 4, ST = KS + VS;
+    constexpr int KS = DP == 128 ? DQK : 4, VS = DP == 128 ? 5 - DQK : 4, ST = KS + VS;
     static_assert(ST == S::kStages, "the rings fill the shared memory");
     extern __shared__ uint4 dyn[];
     __shared__ __align__(8) uint64_t bars[2 * ST + 12];
@@ -1239,15 +1246,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
                                                                 const __grid_constant__ CUtensorMap mdv,
                                                                 const AttnBwdArgs a) {
     using S = AttnShape<DP, kAttnDkv>;
-    constexpr int ST = S::kStages, SS = 4;  // slots of row statistics
-    extern __shared__ uint4 dyn[];
-    __shared__ __align__(16) float stats[SS][2][kAttnTile];  // lse (units of log 2) and delta of a step's queries
-    __shared__ __align__(8) uint64_t bars[2 * ST + SS + 11];
-    __shared__ uint32_t tmem_base;
-    __shared__ int abort_flag;
+    constexpr int ST = S::kStages, SS = 2;  // slots of row statistics
+    extern __shared__ __align__(1024) unsigned char dkv_shared[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(dkv_shared + S::kTiles);  // 2 * ST + 2 * SS + 11 of them, in 248 bytes
+    static_assert((2 * ST + 2 * SS + 11) * 8 <= 248, "barriers and two words in 256 bytes");
+    uint32_t* tmem_word = reinterpret_cast<uint32_t*>(dkv_shared + S::kTiles + 248);
+    volatile int& abort_flag = *reinterpret_cast<volatile int*>(dkv_shared + S::kTiles + 252);
+    // lse (units of log 2) and delta of a step's queries: [SS][2][kAttnTile]
+    float* stats = reinterpret_cast<float*>(dkv_shared + S::kTiles + 256);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t kt = (smem_addr(dyn) + 1023u) & ~1023u, ring = kt + 2 * S::kTile;
-    const uint32_t full = smem_addr(bars), empty = full + 8 * ST, sready = empty + 8 * ST, kfull = sready + 8 * SS;
+    const uint32_t kt = smem_addr(dkv_shared), ring = kt + 2 * S::kTile;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * ST, sready = empty + 8 * ST, sfree = sready + 8 * SS, kfull = sfree + 8 * SS;
     const uint32_t kempty = kfull + 8, sfull = kempty + 8, pready = sfull + 8, pfull = pready + 8, dsready = pfull + 8;
     const uint32_t done = dsready + 8, freed = done + 8, tail = freed + 8, drain = tail + 8;
     if (tid == 0) {
@@ -1255,7 +1264,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
         }
-        for (int i = 0; i < SS; ++i) mbar_init(sready + 8 * i, 32);
+        for (int i = 0; i < SS; ++i) {
+            mbar_init(sready + 8 * i, 32);
+            mbar_init(sfree + 8 * i, 8);
+        }
         mbar_init(kfull, 1);
         mbar_init(kempty, 9);  // the products that read them, and the warps that sent dk and dv out through them
         mbar_init(sfull, 1);
@@ -1275,12 +1287,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         tma_prefetch_map(&mdk);
         tma_prefetch_map(&mdv);
     }
-    if (warp == kAllocWarp) tmem_alloc1(smem_addr(&tmem_base), 512);
+    if (warp == kAllocWarp) tmem_alloc1(smem_addr(tmem_word), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_trigger();
-    const uint32_t tmem = tmem_base, dp_tmem = tmem + 128, dv_tmem = tmem + 256, dk_tmem = tmem + 384;
+    const uint32_t tmem = *tmem_word, dp_tmem = tmem + 128, dv_tmem = tmem + 256, dk_tmem = tmem + 384;
     pdl_wait();
     AttnIssued issued;
     const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);
@@ -1339,8 +1351,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
                         load_tile<DP>(dst, x ? &mdo : &mq, h, row, bar);
                     }
                     if (x == 1) {
-                        // The slot's last readers were done before the tile that went was freed.
-                        float* dst2 = &stats[slots % SS][0][0];
+                        if (slots >= SS)
+                            live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sfree + 8 * (slots % SS), (slots / SS - 1) & 1u, &abort_flag));
+                        float* dst2 = stats + slots % SS * 2 * kAttnTile;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) dst2[lane + 32 * i] = stat[i];
                         mbar_arrive(sready + 8 * (slots % SS));
@@ -1436,7 +1449,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
             for (int j = 0; j < n; ++j, ++steps) {
                 const int q0 = (first + walk.tile(t0 + j) % tiles) * kAttnTile + 64 * wg;
                 const bool cut = __any_sync(0xFFFFFFFFu, from > q0 || it.others < q0 + 64);
-                const uint32_t slot = smem_addr(&stats[steps % SS][0][0]) + 256 * wg;
+                const uint32_t slot = smem_addr(stats) + steps % SS * 1024 + 256 * wg;
                 live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sready + 8 * (steps % SS), (steps / SS) & 1u, &abort_flag) &&
                                                    mbar_wait_bounded(sfull, steps & 1u, &abort_flag));
                 if (!live) break;
@@ -1480,7 +1493,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
                 tmem_st32(dp_tmem + lanes, w);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(dsready);
+                if (lane == 0) {
+                    mbar_arrive(dsready);
+                    mbar_arrive(sfree + 8 * (steps % SS));
+                }
             }
             if (!live) break;
             walk.fetch();
@@ -1530,7 +1546,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (__builtin_expect(*(volatile int*)&abort_flag, 0)) {
+    if (__builtin_expect(abort_flag, 0)) {
         volatile int never = 0;
         if (warp == kLoadWarp && lane == 0) {
             if (issued.pair) mbar_wait_bounded(kfull, (issued.pair - 1) & 1u, &never);

@@ -30,7 +30,6 @@ struct AttnItem {
 // shared out evenly, so that a CTA may begin or end inside one; what it computes of such a unit is a
 // piece, left in fp32 and joined with the others in their order by another kernel. With whole units a CTA,
 // 64 x 12 units on 152 SMs would take six rounds for 5.05.
-constexpr int kAttnUnitCost = 2;
 // A piece has at least this many steps: writing and joining one costs about as much as two.
 constexpr int kAttnMinPiece = 4;
 struct AttnCursor {
@@ -54,6 +53,7 @@ struct AttnList {
     int tile;             // rows an entry
     int heads;            // units an entry
     int group;            // keys: heads of queries that a step is repeated for
+    int unit_cost;        // what a unit takes beside its steps, in steps
     int ctas;
 };
 
