@@ -1578,40 +1578,41 @@ int adaln_attention_bwd(const void* dout, const void* q, const void* k, const vo
     a.group = Hq / Hk;
     a.d = d;
     a.scale = scale;
+    AttnBwdArgs dkv = a, dx = a;
     AttnJoinArgs j{};
     j.d = d;
     j.Rq = Rq;
     j.scale = scale;
     if (dk && Rk > 0) {
-        a.list = l.list[1];
-        a.dx = dk;
-        a.dv = dv;
-        a.dx_ld = dk_ld;
-        a.dv_ld = dv_ld;
-        a.part = at<float>(workspace, p.part[1]);
-        a.slot_rows = p.slot_rows[1];
-        if (int rc = launched(launch_attn_dkv(a, rdo, rq, rk, rv, stream))) return rc;
-        if (p.pieces[1]) j.list[1] = a.list;
-        j.part[1] = a.part;
-        j.slot_rows[1] = a.slot_rows;
+        dkv.list = l.list[1];
+        dkv.dx = dk;
+        dkv.dv = dv;
+        dkv.dx_ld = dk_ld;
+        dkv.dv_ld = dv_ld;
+        dkv.part = at<float>(workspace, p.part[1]);
+        dkv.slot_rows = p.slot_rows[1];
+        if (p.pieces[1]) j.list[1] = dkv.list;
+        j.part[1] = dkv.part;
+        j.slot_rows[1] = dkv.slot_rows;
         j.out[1] = dk;
         j.dv = dv;
         j.ld[1] = dk_ld;
         j.dv_ld = dv_ld;
     }
     if (dq && Rq > 0) {
-        a.list = l.list[0];
-        a.dx = dq;
-        a.dx_ld = dq_ld;
-        a.part = at<float>(workspace, p.part[0]);
-        a.slot_rows = p.slot_rows[0];
-        if (int rc = launched(launch_attn_dq(a, rdo, rq, rk, rv, stream))) return rc;
-        if (p.pieces[0]) j.list[0] = a.list;
-        j.part[0] = a.part;
-        j.slot_rows[0] = a.slot_rows;
+        dx.list = l.list[0];
+        dx.dx = dq;
+        dx.dx_ld = dq_ld;
+        dx.part = at<float>(workspace, p.part[0]);
+        dx.slot_rows = p.slot_rows[0];
+        if (p.pieces[0]) j.list[0] = dx.list;
+        j.part[0] = dx.part;
+        j.slot_rows[0] = dx.slot_rows;
         j.out[0] = dq;
         j.ld[0] = dq_ld;
     }
+    if (dkv.list.ctas + dx.list.ctas == 0) return ADALN_OK;
+    if (int rc = launched(launch_attn_bwd(dkv, dx, rdo, rq, rk, rv, stream))) return rc;
     return j.list[0].items || j.list[1].items ? launched(launch_attn_join(j, true, stream)) : ADALN_OK;
 }
 

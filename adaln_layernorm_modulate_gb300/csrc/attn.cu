@@ -13,8 +13,8 @@
 //   attn_fwd_kernel: two tiles of 128 queries share the keys and values in shared memory; a
 //       warpgroup each has a thread a row, so that the softmax needs no exchange between threads. The
 //       two alternate: while one computes exponentials, the tensor cores run the other's products.
-//   attn_dq_kernel: a tile of 128 queries over its keys: z, dp, dq += dz k.
-//   attn_dkv_kernel: a tile of 128 keys over its queries, transposed: z^T, dp^T, dv += p^T dout,
+//   attn_dq: a tile of 128 queries over its keys: z, dp, dq += dz k.
+//   attn_dkv: a tile of 128 keys over its queries, transposed: z^T, dp^T, dv += p^T dout,
 //       dk += dz^T q, over all heads that share the keys.
 //
 // dq and dk, dv are two kernels that both compute z and dp (7 products where one kernel would need 5):
@@ -29,9 +29,6 @@
 #include "attn.h"
 #include "tensor.cuh"
 
-#ifndef DQK
-#define DQK 3
-#endif
 namespace adaln {
 
 #define ADALN_IN_ATTN(cond) ADALN_IN(::adaln::kDbgAttn, cond)
@@ -41,7 +38,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kAllocWarp = 10;
 constexpr uint32_t kPanel = kAttnTile * 128;  // 128 rows of 64 elements, 128-byte swizzle
 
 // Shared memory: two resident tiles, a ring of tiles, and in the forward 4 KB a warp for its results on
-// their way out; dk and dv need room for the row statistics.
+// their way out.
 enum AttnKernel : int { kAttnFwd = 0, kAttnDq = 1, kAttnDkv = 2 };
 constexpr uint32_t kAttnOut = 32 * 128;  // 32 rows of 64 elements
 template <int DP, int KIND>
@@ -49,10 +46,10 @@ struct AttnShape {
     static constexpr uint32_t kTile = DP / 64 * kPanel;
     static constexpr int kStages = DP == 128 ? (KIND == kAttnFwd ? 4 : 5) : 8;
     static constexpr uint32_t kTiles = (2 + kStages) * kTile;
-    // dk and dv keep nothing in static shared memory: the dynamic memory then begins on a 1024-byte
-    // boundary, without which a fifth stage would not fit. Behind the tiles: barriers, statistics.
-    static constexpr size_t kSmem = KIND == kAttnDkv ? kTiles + 256 + 2048
-                                                     : 1024 + kTiles + (KIND == kAttnFwd ? 8 * kAttnOut : 0);
+    // The gradients keep nothing in static shared memory: the dynamic memory then begins on a 1024-byte
+    // boundary, without which the fifth stage would not fit. Behind the tiles: barriers and two words, for
+    // dk and dv the row statistics.
+    static constexpr size_t kSmem = KIND == kAttnFwd ? 1024 + kTiles + 8 * kAttnOut : kTiles + 256 + 2048;
 };
 
 // ---- work list -----------------------------------------------------------------------------
@@ -306,13 +303,14 @@ __device__ __forceinline__ AttnCursor attn_cursor(const AttnList& l, int c) {
 // its own.
 struct AttnWalk {
     const AttnList& l;
+    int cta;
     AttnCursor from, to;
     int count, unit, entry;
     AttnItem it, ahead;
     int head, t0, t1, all, shift, elapsed = 0;
-    __device__ __forceinline__ AttnWalk(const AttnList& list) : l(list) {
-        from = attn_cursor(l, blockIdx.x);
-        to = attn_cursor(l, blockIdx.x + 1);
+    __device__ __forceinline__ AttnWalk(const AttnList& list, int at) : l(list), cta(at) {
+        from = attn_cursor(l, cta);
+        to = attn_cursor(l, cta + 1);
         count = __ldcg(l.count);
         unit = from.unit - 1;
         head = count > 0 ? from.unit / count : 0;
@@ -349,7 +347,7 @@ struct AttnWalk {
     __device__ __forceinline__ int tile(int t) const { return t + shift < all ? t + shift : t + shift - all; }
     __device__ __forceinline__ bool whole(int n) const { return t0 == 0 && t1 == n; }
     // Where a piece goes: a CTA has at most one that does not begin its unit and one that does.
-    __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (t0 == 0 ? 1 : 0); }
+    __device__ __forceinline__ int slot() const { return 2 * cta + (t0 == 0 ? 1 : 0); }
 };
 
 // ---- operands --------------------------------------------------------------------------------
@@ -514,7 +512,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
     AttnIssued issued;
     const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);
     // Steps [t0, t1[i]) of a unit for its two tiles of queries; n of the unit in all.
-    AttnWalk walk(a.list);
+    AttnWalk walk(a.list, blockIdx.x);
     const AttnItem& it = walk.it;
     const int& head = walk.head;
     int t0 = 0, t1[2], n = 0;
@@ -931,23 +929,20 @@ __device__ __forceinline__ void mask64(float (&p)[64], int from, int to) {
 // it came from, and the next scores and dp are formed while the warps are at it. The two warpgroups
 // take 64 keys of a step each, a thread a row.
 template <int DP>
-__global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_constant__ CUtensorMap mdo,
-                                                               const __grid_constant__ CUtensorMap mq,
-                                                               const __grid_constant__ CUtensorMap mk,
-                                                               const __grid_constant__ CUtensorMap mv,
-                                                               const __grid_constant__ CUtensorMap mdq,
-                                                               const AttnBwdArgs a) {
+__device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMap& mq, const CUtensorMap& mk,
+                                        const CUtensorMap& mv, const CUtensorMap& mdq, const AttnBwdArgs& a, int cta) {
     using S = AttnShape<DP, kAttnDq>;
     // Keys are held from their scores to dq, two steps on; values from dp of their step alone. With a ring
     // for both, a values' tile would wait for the keys three tiles before it.
-    constexpr int KS = DP == 128 ? DQK : 4, VS = DP == 128 ? 5 - DQK : 4, ST = KS + VS;
+    constexpr int KS = DP == 128 ? 3 : 4, VS = DP == 128 ? 2 : 4, ST = KS + VS;
     static_assert(ST == S::kStages, "the rings fill the shared memory");
-    extern __shared__ uint4 dyn[];
-    __shared__ __align__(8) uint64_t bars[2 * ST + 12];
-    __shared__ uint32_t tmem_base;
-    __shared__ int abort_flag;
+    extern __shared__ __align__(1024) unsigned char bwd_shared[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(bwd_shared + S::kTiles);
+    static_assert((2 * ST + 12) * 8 <= 248, "barriers and two words in 256 bytes");
+    uint32_t* tmem_word = reinterpret_cast<uint32_t*>(bwd_shared + S::kTiles + 248);
+    volatile int& abort_flag = *reinterpret_cast<volatile int*>(bwd_shared + S::kTiles + 252);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t qt = (smem_addr(dyn) + 1023u) & ~1023u, ring = qt + 2 * S::kTile;
+    const uint32_t qt = smem_addr(bwd_shared), ring = qt + 2 * S::kTile;
     const uint32_t full = smem_addr(bars), empty = full + 8 * ST, qfull = empty + 8 * ST, qempty = qfull + 8;
     const uint32_t sfull = qempty + 8, pfull = sfull + 16, pfree = pfull + 8, dsfull = pfree + 8;
     const uint32_t done = dsfull + 16, freed = done + 8, tail = freed + 8, drain = tail + 8;
@@ -978,17 +973,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         tma_prefetch_map(&mv);
         tma_prefetch_map(&mdq);
     }
-    if (warp == kAllocWarp) tmem_alloc1(smem_addr(&tmem_base), 512);
+    if (warp == kAllocWarp) tmem_alloc1(smem_addr(tmem_word), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_trigger();
-    const uint32_t tmem = tmem_base, dp_tmem = tmem + 256, acc = tmem + 384;
+    const uint32_t tmem = *tmem_word, dp_tmem = tmem + 256, acc = tmem + 384;
     pdl_wait();
     AttnIssued issued;
     const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);
     // n steps of a unit, from step t0 of it on; `all` is the unit's.
-    AttnWalk walk(a.list);
+    AttnWalk walk(a.list, cta);
     int t0 = 0, n = 0, all = 0;
     auto next = [&]() {
         if (!walk.next()) return false;
@@ -1209,7 +1204,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (__builtin_expect(*(volatile int*)&abort_flag, 0)) {
+    if (__builtin_expect(abort_flag, 0)) {
         volatile int never = 0;
         if (warp == kLoadWarp && lane == 0) {
             if (issued.pair) mbar_wait_bounded(qfull, (issued.pair - 1) & 1u, &never);
@@ -1238,24 +1233,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
 // over dp; the tensor cores form dv and the next scores while the warps are at dz, dk and the next dp while
 // they are at the next p.
 template <int DP>
-__global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_constant__ CUtensorMap mdo,
-                                                                const __grid_constant__ CUtensorMap mq,
-                                                                const __grid_constant__ CUtensorMap mk,
-                                                                const __grid_constant__ CUtensorMap mv,
-                                                                const __grid_constant__ CUtensorMap mdk,
-                                                                const __grid_constant__ CUtensorMap mdv,
-                                                                const AttnBwdArgs a) {
+__device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorMap& mq, const CUtensorMap& mk,
+                                         const CUtensorMap& mv, const CUtensorMap& mdk, const CUtensorMap& mdv,
+                                         const AttnBwdArgs& a, int cta) {
     using S = AttnShape<DP, kAttnDkv>;
     constexpr int ST = S::kStages, SS = 2;  // slots of row statistics
-    extern __shared__ __align__(1024) unsigned char dkv_shared[];
-    uint64_t* bars = reinterpret_cast<uint64_t*>(dkv_shared + S::kTiles);  // 2 * ST + 2 * SS + 11 of them, in 248 bytes
+    extern __shared__ __align__(1024) unsigned char bwd_shared[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(bwd_shared + S::kTiles);  // 2 * ST + 2 * SS + 11 of them, in 248 bytes
     static_assert((2 * ST + 2 * SS + 11) * 8 <= 248, "barriers and two words in 256 bytes");
-    uint32_t* tmem_word = reinterpret_cast<uint32_t*>(dkv_shared + S::kTiles + 248);
-    volatile int& abort_flag = *reinterpret_cast<volatile int*>(dkv_shared + S::kTiles + 252);
+    uint32_t* tmem_word = reinterpret_cast<uint32_t*>(bwd_shared + S::kTiles + 248);
+    volatile int& abort_flag = *reinterpret_cast<volatile int*>(bwd_shared + S::kTiles + 252);
     // lse (units of log 2) and delta of a step's queries: [SS][2][kAttnTile]
-    float* stats = reinterpret_cast<float*>(dkv_shared + S::kTiles + 256);
+    float* stats = reinterpret_cast<float*>(bwd_shared + S::kTiles + 256);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t kt = smem_addr(dkv_shared), ring = kt + 2 * S::kTile;
+    const uint32_t kt = smem_addr(bwd_shared), ring = kt + 2 * S::kTile;
     const uint32_t full = smem_addr(bars), empty = full + 8 * ST, sready = empty + 8 * ST, sfree = sready + 8 * SS, kfull = sfree + 8 * SS;
     const uint32_t kempty = kfull + 8, sfull = kempty + 8, pready = sfull + 8, pfull = pready + 8, dsready = pfull + 8;
     const uint32_t done = dsready + 8, freed = done + 8, tail = freed + 8, drain = tail + 8;
@@ -1298,7 +1289,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     const int role = __shfl_sync(0xFFFFFFFFu, warp, 0);
     // n steps of a unit, from step t0 of it on; `all` is the unit's: `tiles` of queries, from the first
     // that sees one of the keys, for every head of the group.
-    AttnWalk walk(a.list);
+    AttnWalk walk(a.list, cta);
     int first = 0, tiles = 0, t0 = 0, n = 0, all = 0;
     auto next = [&]() {
         if (!walk.next()) return false;
@@ -1566,6 +1557,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     if (tid == 0 && abort_flag) atomicOr(a.status, kErrTimeout);
 }
 
+// Both gradients in one launch: with few units the two run side by side (17 + 130 + 5 + 1 rows, 4 heads:
+// BWDTIMES), with many one begins on the SMs that the other leaves.
+template <int DP>
+__global__ void __launch_bounds__(kAttnThreads, 1) attn_bwd_kernel(const __grid_constant__ CUtensorMap mdo,
+                                                                const __grid_constant__ CUtensorMap mq,
+                                                                const __grid_constant__ CUtensorMap mk,
+                                                                const __grid_constant__ CUtensorMap mv,
+                                                                const __grid_constant__ CUtensorMap mdq,
+                                                                const __grid_constant__ CUtensorMap mdk,
+                                                                const __grid_constant__ CUtensorMap mdv,
+                                                                const __grid_constant__ AttnBwdArgs dkv,
+                                                                const __grid_constant__ AttnBwdArgs dq) {
+    if ((int)blockIdx.x < dkv.list.ctas)
+        attn_dkv<DP>(mdo, mq, mk, mv, mdk, mdv, dkv, blockIdx.x);
+    else
+        attn_dq<DP>(mdo, mq, mk, mv, mdq, dq, (int)blockIdx.x - dkv.list.ctas);
+}
+
 // ---- launches ------------------------------------------------------------------------------
 namespace {
 
@@ -1574,7 +1583,7 @@ unsigned cap(int64_t want, int64_t most) { return (unsigned)(want < 1 ? 1 : want
 // Lets kernel variant `which` use its shared memory, once a device.
 cudaError_t allow_attn_smem(const void* fn, int which, size_t bytes) {
     constexpr int kDevices = 64;
-    static std::atomic<bool> done[kDevices][6];
+    static std::atomic<bool> done[kDevices][4];
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     if (dev >= 0 && dev < kDevices && done[dev][which].load(std::memory_order_acquire)) return cudaSuccess;
@@ -1634,38 +1643,27 @@ cudaError_t launch_attn_join(const AttnJoinArgs& args, bool bwd, cudaStream_t st
     return launch_dependent(fn, dim3((unsigned)ctas, 8, bwd ? 2 : 1), dim3(256), params, 0, stream);
 }
 
-cudaError_t launch_attn_dq(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
-                           const AttnRows& v, cudaStream_t stream) {
-    AttnBwdArgs a = args;
-    CUtensorMap mdo, mq, mk, mv, mdq;
-    if (!rows_map(&mdo, dout, a.d) || !rows_map(&mq, q, a.d) || !rows_map(&mk, k.R ? k : q, a.d) ||
-        !rows_map(&mv, k.R ? v : q, a.d) ||
-        !rows_map(&mdq, {a.dx, q.R, a.dx_ld, q.H}, a.d, 32))
+cudaError_t launch_attn_bwd(const AttnBwdArgs& dkv_args, const AttnBwdArgs& dq_args, const AttnRows& dout,
+                            const AttnRows& q, const AttnRows& k, const AttnRows& v, cudaStream_t stream) {
+    AttnBwdArgs dkv = dkv_args, dq = dq_args;
+    const int d = dkv.list.ctas ? dkv.d : dq.d;
+    CUtensorMap mdo, mq, mk, mv, mdq{}, mdk{}, mdv{};
+    // A side without rows is not loaded; the maps still have to be maps.
+    const AttnRows some = q.R ? q : k;
+    if (!rows_map(&mdo, q.R ? dout : some, d) || !rows_map(&mq, some, d) || !rows_map(&mk, k.R ? k : some, d) ||
+        !rows_map(&mv, k.R ? v : some, d) || !rows_map(&mdq, dq.list.ctas ? AttnRows{dq.dx, q.R, dq.dx_ld, q.H} : some, d, 32) ||
+        !rows_map(&mdk, dkv.list.ctas ? AttnRows{dkv.dx, k.R, dkv.dx_ld, k.H} : some, d, 32) ||
+        !rows_map(&mdv, dkv.list.ctas ? AttnRows{dkv.dv, k.R, dkv.dv_ld, k.H} : some, d, 32))
         return cudaErrorInvalidValue;
-    const bool wide = a.d > 64;
-    const void* fn = wide ? reinterpret_cast<const void*>(&attn_dq_kernel<128>)
-                          : reinterpret_cast<const void*>(&attn_dq_kernel<64>);
-    const size_t smem = wide ? AttnShape<128, kAttnDq>::kSmem : AttnShape<64, kAttnDq>::kSmem;
-    if (cudaError_t e = allow_attn_smem(fn, wide ? 3 : 2, smem)) return e;
-    void* params[] = {&mdo, &mq, &mk, &mv, &mdq, &a};
-    return launch_dependent(fn, dim3((unsigned)a.list.ctas), dim3(kAttnThreads), params, smem, stream);
-}
-
-cudaError_t launch_attn_dkv(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
-                            const AttnRows& v, cudaStream_t stream) {
-    AttnBwdArgs a = args;
-    CUtensorMap mdo, mq, mk, mv, mdk, mdv;
-    if (!rows_map(&mdo, q.R ? dout : k, a.d) || !rows_map(&mq, q.R ? q : k, a.d) || !rows_map(&mk, k, a.d) ||
-        !rows_map(&mv, v, a.d) ||
-        !rows_map(&mdk, {a.dx, k.R, a.dx_ld, k.H}, a.d, 32) || !rows_map(&mdv, {a.dv, k.R, a.dv_ld, k.H}, a.d, 32))
-        return cudaErrorInvalidValue;
-    const bool wide = a.d > 64;
-    const void* fn = wide ? reinterpret_cast<const void*>(&attn_dkv_kernel<128>)
-                          : reinterpret_cast<const void*>(&attn_dkv_kernel<64>);
+    const bool wide = d > 64;
+    const void* fn = wide ? reinterpret_cast<const void*>(&attn_bwd_kernel<128>)
+                          : reinterpret_cast<const void*>(&attn_bwd_kernel<64>);
     const size_t smem = wide ? AttnShape<128, kAttnDkv>::kSmem : AttnShape<64, kAttnDkv>::kSmem;
-    if (cudaError_t e = allow_attn_smem(fn, wide ? 5 : 4, smem)) return e;
-    void* params[] = {&mdo, &mq, &mk, &mv, &mdk, &mdv, &a};
-    return launch_dependent(fn, dim3((unsigned)a.list.ctas), dim3(kAttnThreads), params, smem, stream);
+    static_assert(AttnShape<128, kAttnDkv>::kSmem == AttnShape<128, kAttnDq>::kSmem &&
+                      AttnShape<64, kAttnDkv>::kSmem == AttnShape<64, kAttnDq>::kSmem, "one launch holds both");
+    if (cudaError_t e = allow_attn_smem(fn, wide ? 3 : 2, smem)) return e;
+    void* params[] = {&mdo, &mq, &mk, &mv, &mdq, &mdk, &mdv, &dkv, &dq};
+    return launch_dependent(fn, dim3((unsigned)(dkv.list.ctas + dq.list.ctas)), dim3(kAttnThreads), params, smem, stream);
 }
 
 cudaError_t debug_word_attn(uint32_t* out, bool reset) { return debug_word(out, reset); }

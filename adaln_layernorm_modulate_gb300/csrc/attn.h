@@ -124,10 +124,9 @@ cudaError_t launch_attn_prepare(const AttnPlanArgs& plan, const AttnDeltaArgs& d
 cudaError_t launch_attn_fwd(const AttnFwdArgs& args, const AttnRows& q, const AttnRows& k, const AttnRows& v,
                             cudaStream_t stream);
 cudaError_t launch_attn_join(const AttnJoinArgs& args, bool bwd, cudaStream_t stream);
-cudaError_t launch_attn_dq(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
-                           const AttnRows& v, cudaStream_t stream);
-cudaError_t launch_attn_dkv(const AttnBwdArgs& args, const AttnRows& dout, const AttnRows& q, const AttnRows& k,
-                            const AttnRows& v, cudaStream_t stream);
+// dk and dv, dq; either's list may have no CTAs.
+cudaError_t launch_attn_bwd(const AttnBwdArgs& dkv, const AttnBwdArgs& dq, const AttnRows& dout, const AttnRows& q,
+                            const AttnRows& k, const AttnRows& v, cudaStream_t stream);
 cudaError_t debug_word_attn(uint32_t* out, bool reset);
 
 }  // namespace adaln
