@@ -307,7 +307,8 @@ struct AttnWalk {
     AttnCursor from, to;
     int count, unit, entry;
     AttnItem it, ahead;
-    int head, t0, t1, all, shift, elapsed = 0;
+    int head, t0, t1, all, shift;
+    uint32_t elapsed = 0;  // steps so far
     __device__ __forceinline__ AttnWalk(const AttnList& list, int at) : l(list), cta(at) {
         from = attn_cursor(l, cta);
         to = attn_cursor(l, cta + 1);
@@ -335,13 +336,13 @@ struct AttnWalk {
     // With the unit's steps known. `turn`: its steps may go in any order; a whole unit then begins with the step
     // that the CTA would be at had it begun with step 0 of its first unit, and goes round. CTAs that work on
     // one head so read the same tiles at about the same time, wherever they began (32760 x 12 x 128: the keys
-    // and values of all heads are more than L2 holds; TURNTIMES).
+    // and values of all heads are more than L2 holds; 5065 us without, 4315 with).
     __device__ __forceinline__ void steps(int n, bool turn) {
         t0 = unit == from.unit ? from.tile : 0;
         t1 = unit == to.unit ? to.tile : n;
         all = n;
-        shift = turn && n > 0 && whole(n) ? elapsed % n : 0;
-        elapsed += t1 - t0;
+        shift = turn && n > 0 && whole(n) ? (int)(elapsed % (uint32_t)n) : 0;
+        elapsed += (uint32_t)(t1 - t0);
     }
     // The tile of step t of the unit.
     __device__ __forceinline__ int tile(int t) const { return t + shift < all ? t + shift : t + shift - all; }
@@ -461,6 +462,10 @@ struct AttnIssued {
     bool mma = false;
 };
 
+// Registers a thread of the forward: at launch, then of the rows' warps and of the others.
+constexpr int kFwdRegs = 168, kRowRegs = 208, kOtherRegs = 88;
+static_assert(256 * kRowRegs + 128 * kOtherRegs <= kAttnThreads * kFwdRegs, "no more than the launch brought");
+
 // ---- forward ---------------------------------------------------------------------------------
 template <int DP>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_constant__ CUtensorMap mq,
@@ -535,257 +540,257 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
     // Registers: the launch's 384 x 168 go as 256 x 208 to the rows' warps, which hold 128 scores each, and
     // 128 x 88 to the others.
     if (role >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (role == kLoadWarp) {
-        bool live = true;
-        fence_async_proxy();
-        while (live && next()) {
-            walk.fetch();
-            const int end = max(t1[0], t1[1]);
-            if (end == t0) continue;
-            live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(qempty, (issued.pair - 1) & 1u, &abort_flag));
-            if (!live) break;
-            const int tiles = it.rows > kAttnTile ? 2 : 1;
-            if (elect_lane()) {
-                mbar_arrive_expect_tx(qfull, tiles * S::kTile);
-                for (int i = 0; i < tiles; ++i)
-                    load_tile<DP>(qt + i * S::kTile, &mq, head, it.row0 + i * kAttnTile, qfull);
-            }
-            ++issued.pair;
-            const int kv = head / a.group;
-            for (int t = t0; t < end && live; ++t) {
-                const int at = walk.tile(t) * kAttnTile, row = it.other0 + at, left = it.others - at;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t s = issued.ring % ST, lap_ = issued.ring / ST;
-                    live = __all_sync(0xFFFFFFFFu, lap_ == 0 || mbar_wait_bounded(empty + 8 * s, (lap_ - 1) & 1u, &abort_flag));
-                    if (!live) break;
-                    const uint32_t dst = ring + s * S::kTile;
-                    // The values' last tile of a segment that something follows goes through this warp.
-                    const bool cut = x == 1 && left < kAttnTile && !it.end;
-                    if (elect_lane()) {
-                        const uint32_t bar = cut ? tail : full + 8 * s;
-                        mbar_arrive_expect_tx(bar, S::kTile);
-                        load_tile<DP>(dst, x ? &mv : &mk, kv, row, bar);
-                    }
-                    if (cut) {
-                        live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail, issued.tail & 1u, &abort_flag));
-                        ++issued.tail;
-                        if (live) {
-                            zero_rows<DP>(dst, left, lane);
-                            fence_shared_async();
-                        }
-                        __syncwarp();
-                        if (elect_lane()) mbar_arrive(full + 8 * s);
-                    }
-                    ++issued.ring;
-                    if (!live) break;
-                }
-            }
-        }
-    } else if (role == kMmaWarp) {
-        bool live = true;
-        uint32_t used = 0, pairs = 0, np[2] = {0, 0}, nu[2] = {0, 0};  // ring tiles, units, tiles and units a warpgroup
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            live = live && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity & 1u, &abort_flag));
-            return live;
-        };
-        auto stage = [&](uint32_t n) { return n % ST; };
-        auto scores = [&](int i, uint32_t n) {
-            if (elect_lane()) {
-                mma_rows<DP>(tmem + 128 * i, qt + i * S::kTile, ring + stage(n) * S::kTile, a.d);
-                mma_commit1(sfull + 8 * i);
-            }
-        };
-        while (live && next()) {
-            walk.fetch();
-            const int end = max(t1[0], t1[1]);
-            if (end == t0) continue;
-            if (!wait(qfull, pairs) || !wait(full + 8 * stage(used), used / ST)) break;
-            tc_fence_after();
-            issued.mma = true;
-            for (int i = 0; i < 2; ++i)
-                if (t1[i] > t0) scores(i, used);
-            if (elect_lane()) {
-                mma_commit1(empty + 8 * stage(used));
-                if (end == t0 + 1) mma_commit1(qempty);
-            }
-            for (int t = t0; t < end; ++t, used += 2) {
-                const bool more = t + 1 < end;
-                if (more && !wait(full + 8 * stage(used + 2), (used + 2) / ST)) break;
-                if (!wait(full + 8 * stage(used + 1), (used + 1) / ST)) break;
-                for (int i = 0; i < 2; ++i) {
-                    if (t >= t1[i]) continue;
-                    if (t == t0 && nu[i] > 0 && !wait(ofree + 8 * i, nu[i] - 1)) break;
-                    // Each half of the keys as soon as its p is there.
-                    const uint32_t acc = tmem + 256 + 128 * i, v = ring + stage(used + 1) * S::kTile;
-                    if (!wait(pfull + 8 * i, np[i])) break;
-                    tc_fence_after();
-                    if (elect_lane()) mma_cols64(acc, tmem + 128 * i, v, a.d, t > t0);
-                    if (!wait(pfull2 + 8 * i, np[i])) break;
-                    tc_fence_after();
-                    if (elect_lane()) {
-                        mma_cols64(acc, tmem + 128 * i + 32, v + kPanel / 2, a.d, true);
-                        mma_commit1(odone + 8 * i);
-                    }
-                    ++np[i];
-                    if (t + 1 < t1[i]) scores(i, used + 2);
-                }
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (role == kLoadWarp) {
+            bool live = true;
+            fence_async_proxy();
+            while (live && next()) {
+                walk.fetch();
+                const int end = max(t1[0], t1[1]);
+                if (end == t0) continue;
+                live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(qempty, (issued.pair - 1) & 1u, &abort_flag));
                 if (!live) break;
-                if (t + 2 == end && elect_lane()) mma_commit1(qempty);  // behind the unit's last scores
+                const int tiles = it.rows > kAttnTile ? 2 : 1;
                 if (elect_lane()) {
-                    mma_commit1(empty + 8 * stage(used + 1));
-                    if (more) mma_commit1(empty + 8 * stage(used + 2));
+                    mbar_arrive_expect_tx(qfull, tiles * S::kTile);
+                    for (int i = 0; i < tiles; ++i)
+                        load_tile<DP>(qt + i * S::kTile, &mq, head, it.row0 + i * kAttnTile, qfull);
+                }
+                ++issued.pair;
+                const int kv = head / a.group;
+                for (int t = t0; t < end && live; ++t) {
+                    const int at = walk.tile(t) * kAttnTile, row = it.other0 + at, left = it.others - at;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t s = issued.ring % ST, lap_ = issued.ring / ST;
+                        live = __all_sync(0xFFFFFFFFu, lap_ == 0 || mbar_wait_bounded(empty + 8 * s, (lap_ - 1) & 1u, &abort_flag));
+                        if (!live) break;
+                        const uint32_t dst = ring + s * S::kTile;
+                        // The values' last tile of a segment that something follows goes through this warp.
+                        const bool cut = x == 1 && left < kAttnTile && !it.end;
+                        if (elect_lane()) {
+                            const uint32_t bar = cut ? tail : full + 8 * s;
+                            mbar_arrive_expect_tx(bar, S::kTile);
+                            load_tile<DP>(dst, x ? &mv : &mk, kv, row, bar);
+                        }
+                        if (cut) {
+                            live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail, issued.tail & 1u, &abort_flag));
+                            ++issued.tail;
+                            if (live) {
+                                zero_rows<DP>(dst, left, lane);
+                                fence_shared_async();
+                            }
+                            __syncwarp();
+                            if (elect_lane()) mbar_arrive(full + 8 * s);
+                        }
+                        ++issued.ring;
+                        if (!live) break;
+                    }
                 }
             }
-            if (!live) break;
-            ++pairs;
-            for (int i = 0; i < 2; ++i)
-                if (t1[i] > t0) ++nu[i];
-        }
-    }
-    } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        const int i = warp >> 2;  // this warpgroup's tile of queries
-        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), st = lanes + 128 * i, ot = lanes + 256 + 128 * i;
-        const int r = (warp & 3) * 32 + lane;
-        const float sl2 = a.scale * kLog2e;
-        const uint32_t out_buf = ring + ST * S::kTile + warp * kAttnOut;
-        uint32_t tiles = 0;
-        bool live = true;
-        while (live && next()) {
-            const int row = i * kAttnTile + r, end = i ? t1[1] : t1[0];
-            // Keys that this row sees.
-            const int seen = max(0, min(it.others, it.shift + row + 1));
-            float m = neg_inf(), l = 0.0f;  // the exponentials' reference, their sum
-            for (int t = t0; t < end; ++t, ++tiles) {
-                live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sfull + 8 * i, tiles & 1u, &abort_flag));
-                if (!live) break;
+        } else if (role == kMmaWarp) {
+            bool live = true;
+            uint32_t used = 0, pairs = 0, np[2] = {0, 0}, nu[2] = {0, 0};  // ring tiles, units, tiles and units a warpgroup
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                live = live && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity & 1u, &abort_flag));
+                return live;
+            };
+            auto stage = [&](uint32_t n) { return n % ST; };
+            auto scores = [&](int i, uint32_t n) {
+                if (elect_lane()) {
+                    mma_rows<DP>(tmem + 128 * i, qt + i * S::kTile, ring + stage(n) * S::kTile, a.d);
+                    mma_commit1(sfull + 8 * i);
+                }
+            };
+            while (live && next()) {
+                walk.fetch();
+                const int end = max(t1[0], t1[1]);
+                if (end == t0) continue;
+                if (!wait(qfull, pairs) || !wait(full + 8 * stage(used), used / ST)) break;
                 tc_fence_after();
-                float v[64], w[64];
-                const int lim = seen - walk.tile(t) * kAttnTile;
-                const bool cut = __any_sync(0xFFFFFFFFu, lim < kAttnTile);
-                tmem_ld128(st, v, w);
-                if (cut) {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) {
-                        v[j] = j < lim ? v[j] : neg_inf();
-                        w[j] = 64 + j < lim ? w[j] : neg_inf();
-                    }
+                issued.mma = true;
+                for (int i = 0; i < 2; ++i)
+                    if (t1[i] > t0) scores(i, used);
+                if (elect_lane()) {
+                    mma_commit1(empty + 8 * stage(used));
+                    if (end == t0 + 1) mma_commit1(qempty);
                 }
-                float m4[4] = {v[0], v[1], w[0], w[1]};
-#pragma unroll
-                for (int j = 2; j < 64; j += 2) {
-                    m4[0] = fmaxf(m4[0], v[j]);
-                    m4[1] = fmaxf(m4[1], v[j + 1]);
-                    m4[2] = fmaxf(m4[2], w[j]);
-                    m4[3] = fmaxf(m4[3], w[j + 1]);
-                }
-                const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                const f2r s2 = p_splat(sl2);
-                f2r c2, sum[2];
-                uint32_t b[32];
-                // Exponentials of 64 scores against the reference, their sum; a row that has seen nothing yet
-                // has none but 0 (and NaN stays).
-                auto half = [&](const float (&x)[64]) {
-                    c2 = p_splat(m == neg_inf() ? 0.0f : -m * sl2);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float2 e = p_get(p_fma(p_make(x[2 * j], x[2 * j + 1]), s2, c2));
-                        const float e0 = exp2_ftz(e.x), e1 = exp2_ftz(e.y);
-                        sum[j & 1] = p_add(sum[j & 1], p_make(e0, e1));
-                        b[j] = pack2(e0, e1);
-                    }
-                };
-                // The first half's against the reference of the step before, while the maximum is still being
-                // found; it seldom has to be done again.
-                sum[0] = sum[1] = kPairZero;
-                half(v);
-                if (__any_sync(0xFFFFFFFFu, t == t0 || (mt - m) * sl2 > 8.0f)) {
-                    // The reference may lag behind the maximum by 2^8, which fp32 sums and bf16 p take as
-                    // well as 1; beyond it, what has been summed is brought to the new one.
-                    const float to = t == t0 ? mt : fmaxf(m, mt);
-                    if (t > t0) {
-                        const float f = to == m ? 1.0f : exp2_ftz((m - to) * sl2);
-                        live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
-                        if (!live) break;
+                for (int t = t0; t < end; ++t, used += 2) {
+                    const bool more = t + 1 < end;
+                    if (more && !wait(full + 8 * stage(used + 2), (used + 2) / ST)) break;
+                    if (!wait(full + 8 * stage(used + 1), (used + 1) / ST)) break;
+                    for (int i = 0; i < 2; ++i) {
+                        if (t >= t1[i]) continue;
+                        if (t == t0 && nu[i] > 0 && !wait(ofree + 8 * i, nu[i] - 1)) break;
+                        // Each half of the keys as soon as its p is there.
+                        const uint32_t acc = tmem + 256 + 128 * i, v = ring + stage(used + 1) * S::kTile;
+                        if (!wait(pfull + 8 * i, np[i])) break;
                         tc_fence_after();
-                        l *= f;
+                        if (elect_lane()) mma_cols64(acc, tmem + 128 * i, v, a.d, t > t0);
+                        if (!wait(pfull2 + 8 * i, np[i])) break;
+                        tc_fence_after();
+                        if (elect_lane()) {
+                            mma_cols64(acc, tmem + 128 * i + 32, v + kPanel / 2, a.d, true);
+                            mma_commit1(odone + 8 * i);
+                        }
+                        ++np[i];
+                        if (t + 1 < t1[i]) scores(i, used + 2);
+                    }
+                    if (!live) break;
+                    if (t + 2 == end && elect_lane()) mma_commit1(qempty);  // behind the unit's last scores
+                    if (elect_lane()) {
+                        mma_commit1(empty + 8 * stage(used + 1));
+                        if (more) mma_commit1(empty + 8 * stage(used + 2));
+                    }
+                }
+                if (!live) break;
+                ++pairs;
+                for (int i = 0; i < 2; ++i)
+                    if (t1[i] > t0) ++nu[i];
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
+            const int i = warp >> 2;  // this warpgroup's tile of queries
+            const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), st = lanes + 128 * i, ot = lanes + 256 + 128 * i;
+            const int r = (warp & 3) * 32 + lane;
+            const float sl2 = a.scale * kLog2e;
+            const uint32_t out_buf = ring + ST * S::kTile + warp * kAttnOut;
+            uint32_t tiles = 0;
+            bool live = true;
+            while (live && next()) {
+                const int row = i * kAttnTile + r, end = i ? t1[1] : t1[0];
+                // Keys that this row sees.
+                const int seen = max(0, min(it.others, it.shift + row + 1));
+                float m = neg_inf(), l = 0.0f;  // the exponentials' reference, their sum
+                for (int t = t0; t < end; ++t, ++tiles) {
+                    live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sfull + 8 * i, tiles & 1u, &abort_flag));
+                    if (!live) break;
+                    tc_fence_after();
+                    float v[64], w[64];
+                    const int lim = seen - walk.tile(t) * kAttnTile;
+                    const bool cut = __any_sync(0xFFFFFFFFu, lim < kAttnTile);
+                    tmem_ld128(st, v, w);
+                    if (cut) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) {
+                            v[j] = j < lim ? v[j] : neg_inf();
+                            w[j] = 64 + j < lim ? w[j] : neg_inf();
+                        }
+                    }
+                    float m4[4] = {v[0], v[1], w[0], w[1]};
+#pragma unroll
+                    for (int j = 2; j < 64; j += 2) {
+                        m4[0] = fmaxf(m4[0], v[j]);
+                        m4[1] = fmaxf(m4[1], v[j + 1]);
+                        m4[2] = fmaxf(m4[2], w[j]);
+                        m4[3] = fmaxf(m4[3], w[j + 1]);
+                    }
+                    const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    const f2r s2 = p_splat(sl2);
+                    f2r c2, sum[2];
+                    uint32_t b[32];
+                    // Exponentials of 64 scores against the reference, their sum; a row that has seen nothing yet
+                    // has none but 0 (and NaN stays).
+                    auto half = [&](const float (&x)[64]) {
+                        c2 = p_splat(m == neg_inf() ? 0.0f : -m * sl2);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float2 e = p_get(p_fma(p_make(x[2 * j], x[2 * j + 1]), s2, c2));
+                            const float e0 = exp2_ftz(e.x), e1 = exp2_ftz(e.y);
+                            sum[j & 1] = p_add(sum[j & 1], p_make(e0, e1));
+                            b[j] = pack2(e0, e1);
+                        }
+                    };
+                    // The first half's against the reference of the step before, while the maximum is still being
+                    // found; it seldom has to be done again.
+                    sum[0] = sum[1] = kPairZero;
+                    half(v);
+                    if (__any_sync(0xFFFFFFFFu, t == t0 || (mt - m) * sl2 > 8.0f)) {
+                        // The reference may lag behind the maximum by 2^8, which fp32 sums and bf16 p take as
+                        // well as 1; beyond it, what has been summed is brought to the new one.
+                        const float to = t == t0 ? mt : fmaxf(m, mt);
+                        if (t > t0) {
+                            const float f = to == m ? 1.0f : exp2_ftz((m - to) * sl2);
+                            live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
+                            if (!live) break;
+                            tc_fence_after();
+                            l *= f;
+#pragma unroll 1
+                            for (int c = 0; c < a.d; c += 32) {
+                                float o[32];
+                                tmem_ld32(ot + c, o);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) b[j] = __float_as_uint(o[j] * f);
+                                tmem_st32(ot + c, b);
+                            }
+                        }
+                        m = to;
+                        tmem_ld64(st, v);
+                        if (cut) {
+#pragma unroll
+                            for (int j = 0; j < 64; ++j) v[j] = j < lim ? v[j] : neg_inf();
+                        }
+                        sum[0] = sum[1] = kPairZero;
+                        half(v);
+                    }
+                    tmem_st32(st, b);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pfull + 8 * i);
+                    half(w);
+                    tmem_st32(st + 32, b);
+                    l += p_hsum(p_add(sum[0], sum[1]));
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pfull2 + 8 * i);
+                }
+                if (!live) break;
+                walk.fetch();
+                const bool mine = row < it.rows;
+                const int64_t at = (int64_t)it.row0 + row;
+                const bool in = mine && ADALN_IN_ATTN(at >= 0 && at < a.Rq && head < a.Hq);
+                const bool none = l == 0.0f;  // no key seen: zeros
+                if (end > t0) {
+                    live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
+                    if (!live) break;
+                    tc_fence_after();
+                }
+                if (walk.whole(n)) {
+                    if (in) a.lse[(int64_t)head * a.Rq + at] = none ? neg_inf() : fmaf(m, a.scale, logf(l));
+                    const float f = 1.0f / l;
+                    const int first = i * kAttnTile + (warp & 3) * 32, rows = min(32, it.rows - first);
+#pragma unroll 1
+                    for (int c = 0; c < a.d && rows > 0; c += 64) {
+                        uint32_t b[32];
+                        if (end > t0) read64(ot + c, f, b);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) b[j] = none ? 0u : b[j];
+                        tma_store_read();  // the lane that issued the buffer's last store has it read
+                        __syncwarp();
+                        out64(&mo, out_buf, b, c, head, it.row0 + first, in || !mine ? rows : 0,
+                              reinterpret_cast<__nv_bfloat16*>(a.o) + at * a.o_ld + (int64_t)head * a.d, a.d, lane);
+                    }
+                } else {
+                    const int64_t place = (int64_t)walk.slot() * a.slot_rows + row;
+                    if (end > t0) {
 #pragma unroll 1
                         for (int c = 0; c < a.d; c += 32) {
                             float o[32];
                             tmem_ld32(ot + c, o);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) b[j] = __float_as_uint(o[j] * f);
-                            tmem_st32(ot + c, b);
+                            if (in && ADALN_IN_ATTN(row < a.slot_rows))
+                                store_piece32(a.part + (int64_t)walk.slot() * a.slot_rows * a.d, row, a.slot_rows, c, a.d, o);
                         }
                     }
-                    m = to;
-                    tmem_ld64(st, v);
-                    if (cut) {
-#pragma unroll
-                        for (int j = 0; j < 64; ++j) v[j] = j < lim ? v[j] : neg_inf();
-                    }
-                    sum[0] = sum[1] = kPairZero;
-                    half(v);
+                    if (in && ADALN_IN_ATTN(row < a.slot_rows)) a.ml[place] = make_float2(m, l);
                 }
-                tmem_st32(st, b);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(pfull + 8 * i);
-                half(w);
-                tmem_st32(st + 32, b);
-                l += p_hsum(p_add(sum[0], sum[1]));
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(pfull2 + 8 * i);
-            }
-            if (!live) break;
-            walk.fetch();
-            const bool mine = row < it.rows;
-            const int64_t at = (int64_t)it.row0 + row;
-            const bool in = mine && ADALN_IN_ATTN(at >= 0 && at < a.Rq && head < a.Hq);
-            const bool none = l == 0.0f;  // no key seen: zeros
-            if (end > t0) {
-                live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
-                if (!live) break;
-                tc_fence_after();
-            }
-            if (walk.whole(n)) {
-                if (in) a.lse[(int64_t)head * a.Rq + at] = none ? neg_inf() : fmaf(m, a.scale, logf(l));
-                const float f = 1.0f / l;
-                const int first = i * kAttnTile + (warp & 3) * 32, rows = min(32, it.rows - first);
-#pragma unroll 1
-                for (int c = 0; c < a.d && rows > 0; c += 64) {
-                    uint32_t b[32];
-                    if (end > t0) read64(ot + c, f, b);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) b[j] = none ? 0u : b[j];
-                    tma_store_read();  // the lane that issued the buffer's last store has it read
-                    __syncwarp();
-                    out64(&mo, out_buf, b, c, head, it.row0 + first, in || !mine ? rows : 0,
-                          reinterpret_cast<__nv_bfloat16*>(a.o) + at * a.o_ld + (int64_t)head * a.d, a.d, lane);
-                }
-            } else {
-                const int64_t place = (int64_t)walk.slot() * a.slot_rows + row;
                 if (end > t0) {
-#pragma unroll 1
-                    for (int c = 0; c < a.d; c += 32) {
-                        float o[32];
-                        tmem_ld32(ot + c, o);
-                        if (in && ADALN_IN_ATTN(row < a.slot_rows))
-                            store_piece32(a.part + (int64_t)walk.slot() * a.slot_rows * a.d, row, a.slot_rows, c, a.d, o);
-                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ofree + 8 * i);
                 }
-                if (in && ADALN_IN_ATTN(row < a.slot_rows)) a.ml[place] = make_float2(m, l);
             }
-            if (end > t0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(ofree + 8 * i);
-            }
-        }
-        tma_store_wait();
+            tma_store_wait();
     }
     __syncwarp();
     tc_fence_before();
@@ -1558,7 +1563,7 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
 }
 
 // Both gradients in one launch: with few units the two run side by side (17 + 130 + 5 + 1 rows, 4 heads:
-// BWDTIMES), with many one begins on the SMs that the other leaves.
+// 23.1 us one after the other, 16.7 together), with many one begins on the SMs that the other leaves.
 template <int DP>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_bwd_kernel(const __grid_constant__ CUtensorMap mdo,
                                                                 const __grid_constant__ CUtensorMap mq,
@@ -1580,14 +1585,18 @@ namespace {
 
 unsigned cap(int64_t want, int64_t most) { return (unsigned)(want < 1 ? 1 : want < most ? want : most); }
 
-// Lets kernel variant `which` use its shared memory, once a device.
-cudaError_t allow_attn_smem(const void* fn, int which, size_t bytes) {
+// Lets kernel variant `which` use its shared memory, once a device. `regs`: what its threads must have been
+// given at launch (setmaxnreg would wait forever for more).
+cudaError_t allow_attn_smem(const void* fn, int which, size_t bytes, int regs = 0) {
     constexpr int kDevices = 64;
     static std::atomic<bool> done[kDevices][4];
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     if (dev >= 0 && dev < kDevices && done[dev][which].load(std::memory_order_acquire)) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    cudaFuncAttributes attr{};
+    cudaError_t e = cudaFuncGetAttributes(&attr, fn);
+    if (e == cudaSuccess && attr.numRegs < regs) e = cudaErrorInvalidKernelImage;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e == cudaSuccess && dev >= 0 && dev < kDevices) done[dev][which].store(true, std::memory_order_release);
     return e;
 }
@@ -1629,7 +1638,7 @@ cudaError_t launch_attn_fwd(const AttnFwdArgs& args, const AttnRows& q, const At
     const void* fn = wide ? reinterpret_cast<const void*>(&attn_fwd_kernel<128>)
                           : reinterpret_cast<const void*>(&attn_fwd_kernel<64>);
     const size_t smem = wide ? AttnShape<128, kAttnFwd>::kSmem : AttnShape<64, kAttnFwd>::kSmem;
-    if (cudaError_t e = allow_attn_smem(fn, wide ? 1 : 0, smem)) return e;
+    if (cudaError_t e = allow_attn_smem(fn, wide ? 1 : 0, smem, kFwdRegs)) return e;
     void* params[] = {&mq, &mk, &mv, &mo, &a};
     return launch_dependent(fn, dim3((unsigned)a.list.ctas), dim3(kAttnThreads), params, smem, stream);
 }

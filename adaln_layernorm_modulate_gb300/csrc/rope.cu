@@ -17,8 +17,8 @@
 //
 // Angles: a position times a frequency is far more than fp32 holds (position 500,000 at frequency 1 is
 // off by 0.03 rad). Frequencies are turns as binary fractions of 64 bits; the product with the integer
-// position wraps at whole turns by itself, so that what is left, the fraction of a turn, is good to
-// 2^-32 of a turn at any position.
+// position wraps at whole turns by itself, so that what is left, the fraction of a turn, is good to 2^-32
+// of a turn and the frequency's own rounding (a double's) at any position.
 #include <atomic>
 
 #include "rope.h"

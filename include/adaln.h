@@ -306,7 +306,8 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
  *   - q_weight, k_weight [d], in `dtype`, each may be null (ones); without a norm both must be.
  *   - pos [R, naxes] (device int32), any values; null: no rotation. axes[naxes] (host, at most 8): the even
  *     widths of the axes, side by side from element 0; a head's elements behind them are not
- *     rotated. theta >= 1. Angles are exact to 2^-31 of a turn at any position.
+ *     rotated. theta >= 1. Angles are good to 2^-31 of a turn and the frequencies' own rounding (2^-53 of
+ *     the angle), at any position.
  *   - dq_weight, dk_weight [d] fp32, overwritten; each may be null (not wanted). Without a norm q and k
  *     of the backward are not looked at.
  * R = 0 is valid (zero weight gradients). One launch forward, two backward (one without weight
@@ -348,7 +349,7 @@ int adaln_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q
  * call's sizes).
  * The backward takes the forward's o and lse. dq may be null, or dk and dv both (not wanted).
  * Malformed tables are recorded (ADALN_ERR_BAD_SEQLENS in adaln_read_status) and nothing is computed:
- * outputs stay as they were. Two or three launches forward, two to four backward. */
+ * outputs stay as they were. Two or three launches either way. */
 size_t adaln_attention_fwd_workspace_size(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d,
                                           adaln_dtype dtype);
 int adaln_attention_fwd(const void* q, const void* k, const void* v, void* o, float* lse, const int32_t* cu_q,
