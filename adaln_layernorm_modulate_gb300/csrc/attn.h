@@ -7,6 +7,7 @@
 
 namespace adaln {
 
+constexpr uint32_t kDbgAttn = 2048u;  // debug builds: rows, heads, work items, statistics, pieces
 constexpr int kAttnTile = 128;       // rows of an operand tile, keys of a step
 constexpr int kAttnMaxD = 128;       // elements of a head
 constexpr int kAttnMaxCtas = 256;    // of one launch

@@ -60,8 +60,6 @@ enum : uint32_t {
     kDbgRanks = 128u,    // rank sum: [0, n) of each rank's array and of the output
     kDbgStatus = 256u,   // status words: [0, kMaxCtas)
     kDbgLoss = 512u,     // vocabulary loss: rows, packed rows, partials, dz, dx and dweight
-    kDbgHeads = 1024u,   // head norm and rotation: rows, heads, positions
-    kDbgAttn = 2048u,    // attention: rows, heads, work items, statistics, partial results
 };
 #ifdef ADALN_DEBUG
 static __device__ unsigned int g_adaln_debug;  // one per translation unit (module)

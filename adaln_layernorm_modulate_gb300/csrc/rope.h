@@ -7,6 +7,7 @@
 
 namespace adaln {
 
+constexpr uint32_t kDbgHeads = 1024u;  // debug builds: rows, heads, positions
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxD = 256;      // elements of a head
 constexpr int kRopeMaxAxes = 8;
