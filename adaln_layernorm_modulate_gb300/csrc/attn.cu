@@ -47,9 +47,10 @@ struct AttnShape {
     static constexpr int kStages = DP == 128 ? (KIND == kAttnFwd ? 4 : 5) : 8;
     static constexpr uint32_t kTiles = (2 + kStages) * kTile;
     // The gradients keep nothing in static shared memory: the dynamic memory then begins on a 1024-byte
-    // boundary, without which the fifth stage would not fit. Behind the tiles: barriers and two words, for
-    // dk and dv the row statistics.
-    static constexpr size_t kSmem = KIND == kAttnFwd ? 1024 + kTiles + 8 * kAttnOut : kTiles + 256 + 2048;
+    // boundary, without which the fifth stage would not fit. Behind the tiles: results on their way out (of
+    // wide heads they fit the second resident tile), barriers and two words, for dk and dv the row statistics.
+    static constexpr uint32_t kOut = DP == 64 ? 8 * kAttnOut : 0, kBars = kTiles + kOut;
+    static constexpr size_t kSmem = KIND == kAttnFwd ? 1024 + kTiles + 8 * kAttnOut : kBars + 320 + 2048;
 };
 
 // ---- work list -----------------------------------------------------------------------------
@@ -93,8 +94,8 @@ __device__ __forceinline__ int64_t attn_cost(const AttnTables& t, const AttnList
     } else if (list == 0) {
         // A full entry's last query, (i + 1) k tiles of 128 on, sees a + (i + 1) k tiles of keys; the last
         // entry, full or not, sees all keys.
-        const int k = l.tile / kAttnTile, a = -floor_div(g.nq - g.nk, kAttnTile);
-        const int64_t full = min(tiles, len / l.tile), none = a + k > 0 ? 0 : min((int64_t)(-a / k), full);
+        const int k = l.tile / kAttnTile /* 1 or 2 */, a = -floor_div(g.nq - g.nk, kAttnTile);
+        const int64_t full = min(tiles, len / l.tile), none = a + k > 0 ? 0 : min((int64_t)(-a >> (k - 1)), full);
         sum = (full - none) * a + k * (full * (full + 1) - none * (none + 1)) / 2;
         if (tiles > full) sum += steps;
     } else {
@@ -458,7 +459,7 @@ __device__ __forceinline__ void store_piece32(float* piece, int row, int rows, i
 // What a CTA has issued, for the drain after a timeout: copies and products must not land in memory
 // that has been given back.
 struct AttnIssued {
-    uint32_t ring = 0, pair = 0, tail = 0;  // fills of the ring, of the resident tiles, of tails
+    uint32_t ring = 0, pair = 0, pair2 = 0, tail = 0;  // fills of the ring, of the resident tiles (of the second), of tails
     bool mma = false;
 };
 
@@ -932,7 +933,8 @@ __device__ __forceinline__ void mask64(float (&p)[64], int from, int to) {
 
 // dq of a tile of 128 queries. Its scores have two places in tensor memory: dz goes over the scores that
 // it came from, and the next scores and dp are formed while the warps are at it. The two warpgroups
-// take 64 keys of a step each, a thread a row.
+// take 64 keys of a step each, a thread a row. The queries' shared memory is free behind the unit's last
+// scores, so that the next unit's scores are there when dq has gone out, through dout's.
 template <int DP>
 __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMap& mq, const CUtensorMap& mk,
                                         const CUtensorMap& mv, const CUtensorMap& mdq, const AttnBwdArgs& a, int cta) {
@@ -942,13 +944,13 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMa
     constexpr int KS = DP == 128 ? 3 : 4, VS = DP == 128 ? 2 : 4, ST = KS + VS;
     static_assert(ST == S::kStages, "the rings fill the shared memory");
     extern __shared__ __align__(1024) unsigned char bwd_shared[];
-    uint64_t* bars = reinterpret_cast<uint64_t*>(bwd_shared + S::kTiles);
-    static_assert((2 * ST + 12) * 8 <= 248, "barriers and two words in 256 bytes");
-    uint32_t* tmem_word = reinterpret_cast<uint32_t*>(bwd_shared + S::kTiles + 248);
-    volatile int& abort_flag = *reinterpret_cast<volatile int*>(bwd_shared + S::kTiles + 252);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(bwd_shared + S::kBars);
+    static_assert((2 * ST + 14) * 8 <= 312, "barriers and two words in 320 bytes");
+    uint32_t* tmem_word = reinterpret_cast<uint32_t*>(bwd_shared + S::kBars + 312);
+    volatile int& abort_flag = *reinterpret_cast<volatile int*>(bwd_shared + S::kBars + 316);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t qt = smem_addr(bwd_shared), ring = qt + 2 * S::kTile;
-    const uint32_t full = smem_addr(bars), empty = full + 8 * ST, qfull = empty + 8 * ST, qempty = qfull + 8;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * ST, qfull = empty + 8 * ST, dofull = qfull + 8, doempty = dofull + 8, qempty = doempty + 8;
     const uint32_t sfull = qempty + 8, pfull = sfull + 16, pfree = pfull + 8, dsfull = pfree + 8;
     const uint32_t done = dsfull + 16, freed = done + 8, tail = freed + 8, drain = tail + 8;
     if (tid == 0) {
@@ -957,7 +959,9 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMa
             mbar_init(empty + 8 * i, 1);
         }
         mbar_init(qfull, 1);
-        mbar_init(qempty, 9);  // the products that read it, and the warps that sent dq out through it
+        mbar_init(qempty, 1);
+        mbar_init(dofull, 1);
+        mbar_init(doempty, 9);  // the products that read it, and the warps that sent dq out through it
         mbar_init(sfull, 1);
         mbar_init(sfull + 8, 1);
         mbar_init(pfull, 1);
@@ -1011,9 +1015,8 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMa
             live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(qempty, (issued.pair - 1) & 1u, &abort_flag));
             if (!live) break;
             if (elect_lane()) {
-                mbar_arrive_expect_tx(qfull, 2 * S::kTile);
+                mbar_arrive_expect_tx(qfull, S::kTile);
                 load_tile<DP>(qt, &mq, head, it.row0, qfull);
-                load_tile<DP>(qt + S::kTile, &mdo, head, it.row0, qfull);
             }
             ++issued.pair;
             const int kv = head / a.group;
@@ -1043,6 +1046,16 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMa
                     }
                     ++issued.ring;
                     if (!live) break;
+                    if (n > 1 ? x == 0 && t == t0 + 1 : x == 1) {  // dout behind what goes before it
+                        live = __all_sync(0xFFFFFFFFu,
+                                          issued.pair2 == 0 || mbar_wait_bounded(doempty, (issued.pair2 - 1) & 1u, &abort_flag));
+                        if (!live) break;
+                        if (elect_lane()) {
+                            mbar_arrive_expect_tx(dofull, S::kTile);
+                            load_tile<DP>(qt + S::kTile, &mdo, head, it.row0, dofull);
+                        }
+                        ++issued.pair2;
+                    }
                 }
             }
         }
@@ -1080,14 +1093,15 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMa
             tc_fence_after();
             issued.mma = true;
             scores(0);
-            if (!values(0)) break;
-            tc_fence_after();
-            dprobs(0);
             if (n > 1) {
                 if (!keys(1)) break;
                 tc_fence_after();
                 scores(1);
             }
+            if (n <= 2 && elect_lane()) mma_commit1(qempty);
+            if (!wait(dofull, laps) || !values(0)) break;
+            tc_fence_after();
+            dprobs(0);
             for (int j = 0; j < n; ++j) {
                 if (j + 1 < n) {
                     if (!values(j + 1) || !wait(pfree, steps + j)) break;
@@ -1106,12 +1120,13 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMa
                     if (!keys(j + 2)) break;
                     tc_fence_after();
                     scores(j + 2);
+                    if (j + 3 == n && elect_lane()) mma_commit1(qempty);  // behind the unit's last scores
                 }
             }
             if (!live) break;
             if (elect_lane()) {
                 mma_commit1(done);
-                mma_commit1(qempty);
+                mma_commit1(doempty);
             }
             steps += n;
             ++laps;
@@ -1178,13 +1193,13 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMa
             live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(done, laps & 1u, &abort_flag));
             if (!live) break;
             tc_fence_after();
-            // 64 columns a warpgroup, out through the queries' shared memory.
+            // 64 columns a warpgroup, out through dout's shared memory.
             if (walk.whole(all)) {
                 const int rows = min(32, it.rows - (warp & 3) * 32);
                 if (64 * wg < a.d && rows > 0) {
                     uint32_t w[32];
                     read64(acc + lanes + 64 * wg, a.scale, w);
-                    out64(&mdq, qt + warp * kAttnOut, w, 64 * wg, head, it.row0 + (warp & 3) * 32, rows, out, a.d, lane);
+                    out64(&mdq, (DP == 64 ? qt + S::kTiles : qt + S::kTile) + warp * kAttnOut, w, 64 * wg, head, it.row0 + (warp & 3) * 32, rows, out, a.d, lane);
                     tma_store_read();
                 }
             } else {
@@ -1200,7 +1215,7 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMa
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(freed);
-                mbar_arrive(qempty);
+                mbar_arrive(doempty);
             }
             ++laps;
         }
@@ -1213,6 +1228,7 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMa
         volatile int never = 0;
         if (warp == kLoadWarp && lane == 0) {
             if (issued.pair) mbar_wait_bounded(qfull, (issued.pair - 1) & 1u, &never);
+            if (issued.pair2) mbar_wait_bounded(dofull, (issued.pair2 - 1) & 1u, &never);
             if (issued.tail) mbar_wait_bounded(tail, (issued.tail - 1) & 1u, &never);
             // ring counts tiles of both rings, the keys' first.
             const uint32_t ks = (issued.ring + 1) / 2, vs = issued.ring / 2;
@@ -1236,7 +1252,8 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMa
 // dk and dv of a tile of 128 keys, over the queries of all heads that share them; everything transposed,
 // a thread a key. The two warpgroups take 64 queries of a step each. p goes over the scores and dz
 // over dp; the tensor cores form dv and the next scores while the warps are at dz, dk and the next dp while
-// they are at the next p.
+// they are at the next p. The keys' shared memory is free behind the unit's last scores; dk and dv go out
+// through the values'.
 template <int DP>
 __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorMap& mq, const CUtensorMap& mk,
                                          const CUtensorMap& mv, const CUtensorMap& mdk, const CUtensorMap& mdv,
@@ -1244,16 +1261,16 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
     using S = AttnShape<DP, kAttnDkv>;
     constexpr int ST = S::kStages, SS = 2;  // slots of row statistics
     extern __shared__ __align__(1024) unsigned char bwd_shared[];
-    uint64_t* bars = reinterpret_cast<uint64_t*>(bwd_shared + S::kTiles);  // 2 * ST + 2 * SS + 11 of them, in 248 bytes
-    static_assert((2 * ST + 2 * SS + 11) * 8 <= 248, "barriers and two words in 256 bytes");
-    uint32_t* tmem_word = reinterpret_cast<uint32_t*>(bwd_shared + S::kTiles + 248);
-    volatile int& abort_flag = *reinterpret_cast<volatile int*>(bwd_shared + S::kTiles + 252);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(bwd_shared + S::kBars);  // 2 * ST + 2 * SS + 13 of them, in 312 bytes
+    static_assert((2 * ST + 2 * SS + 13) * 8 <= 312, "barriers and two words in 320 bytes");
+    uint32_t* tmem_word = reinterpret_cast<uint32_t*>(bwd_shared + S::kBars + 312);
+    volatile int& abort_flag = *reinterpret_cast<volatile int*>(bwd_shared + S::kBars + 316);
     // lse (units of log 2) and delta of a step's queries: [SS][2][kAttnTile]
-    float* stats = reinterpret_cast<float*>(bwd_shared + S::kTiles + 256);
+    float* stats = reinterpret_cast<float*>(bwd_shared + S::kBars + 320);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t kt = smem_addr(bwd_shared), ring = kt + 2 * S::kTile;
-    const uint32_t full = smem_addr(bars), empty = full + 8 * ST, sready = empty + 8 * ST, sfree = sready + 8 * SS, kfull = sfree + 8 * SS;
-    const uint32_t kempty = kfull + 8, sfull = kempty + 8, pready = sfull + 8, pfull = pready + 8, dsready = pfull + 8;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * ST, sready = empty + 8 * ST, sfree = sready + 8 * SS, kfull = sfree + 8 * SS, vfull = kfull + 8;
+    const uint32_t kempty = vfull + 8, vempty = kempty + 8, sfull = vempty + 8, pready = sfull + 8, pfull = pready + 8, dsready = pfull + 8;
     const uint32_t done = dsready + 8, freed = done + 8, tail = freed + 8, drain = tail + 8;
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
@@ -1265,7 +1282,9 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
             mbar_init(sfree + 8 * i, 8);
         }
         mbar_init(kfull, 1);
-        mbar_init(kempty, 9);  // the products that read them, and the warps that sent dk and dv out through them
+        mbar_init(kempty, 1);
+        mbar_init(vfull, 1);
+        mbar_init(vempty, 9);  // the products that read them, and the warps that sent dk and dv out through them
         mbar_init(sfull, 1);
         mbar_init(pready, 8);
         mbar_init(pfull, 1);
@@ -1319,9 +1338,8 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
             live = __all_sync(0xFFFFFFFFu, issued.pair == 0 || mbar_wait_bounded(kempty, (issued.pair - 1) & 1u, &abort_flag));
             if (!live) break;
             if (elect_lane()) {
-                mbar_arrive_expect_tx(kfull, 2 * S::kTile);
+                mbar_arrive_expect_tx(kfull, S::kTile);
                 load_tile<DP>(kt, &mk, head, it.row0, kfull);
-                load_tile<DP>(kt + S::kTile, &mv, head, it.row0, kfull);
             }
             ++issued.pair;
             for (int j = 0; j < n && live; ++j, ++slots) {
@@ -1366,6 +1384,16 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
                     }
                     ++issued.ring;
                     if (!live) break;
+                    if (n > 1 ? x == 0 && j == 1 : x == 1) {  // the values behind what goes before them
+                        live = __all_sync(0xFFFFFFFFu,
+                                          issued.pair2 == 0 || mbar_wait_bounded(vempty, (issued.pair2 - 1) & 1u, &abort_flag));
+                        if (!live) break;
+                        if (elect_lane()) {
+                            mbar_arrive_expect_tx(vfull, S::kTile);
+                            load_tile<DP>(kt + S::kTile, &mv, head, it.row0, vfull);
+                        }
+                        ++issued.pair2;
+                    }
                 }
             }
         }
@@ -1397,7 +1425,8 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
             tc_fence_after();
             issued.mma = true;
             scores(0);
-            if (!loaded(used + 1)) break;
+            if (n == 1 && elect_lane()) mma_commit1(kempty);
+            if (!wait(vfull, laps) || !loaded(used + 1)) break;
             tc_fence_after();
             dprobs(0);
             if (laps > 0 && !wait(freed, laps - 1)) break;
@@ -1412,6 +1441,7 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
                     if (!loaded(used + 2 * j + 2)) break;
                     tc_fence_after();
                     scores(j + 1);
+                    if (j + 2 == n && elect_lane()) mma_commit1(kempty);  // behind the unit's last scores
                 }
                 if (!wait(dsready, steps + j)) break;
                 tc_fence_after();
@@ -1428,7 +1458,7 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
             if (!live) break;
             if (elect_lane()) {
                 mma_commit1(done);
-                mma_commit1(kempty);
+                mma_commit1(vempty);
             }
             used += 2 * n;
             steps += n;
@@ -1438,6 +1468,7 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
         const int wg = warp >> 2, c = (warp & 3) * 32 + lane;  // this thread's key of the tile
         const uint32_t lanes = ((uint32_t)(warp & 3) << 21) + 64 * wg;
         const f2r s2 = p_splat(a.scale * kLog2e);
+        const uint32_t out_buf = (DP == 64 ? kt + S::kTiles : kt + S::kTile) + warp * kAttnOut;
         uint32_t steps = 0, laps = 0;
         bool live = true;
         while (live && next()) {
@@ -1516,8 +1547,9 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
                 for (int x = 0; x < a.d && rows > 0; x += 64) {
                     uint32_t w[32];
                     read64(src + x, f, w);
-                    out64(wg ? &mdk : &mdv, kt + warp * (DP / 64 * kAttnOut) + x / 64 * kAttnOut, w, x, head,
-                          it.row0 + (warp & 3) * 32, rows, out, a.d, lane);
+                    tma_store_read();  // the first half, out of the buffer
+                    __syncwarp();
+                    out64(wg ? &mdk : &mdv, out_buf, w, x, head, it.row0 + (warp & 3) * 32, rows, out, a.d, lane);
                 }
                 tma_store_read();
             } else {
@@ -1533,7 +1565,7 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(freed);
-                mbar_arrive(kempty);
+                mbar_arrive(vempty);
             }
             ++laps;
         }
@@ -1546,6 +1578,7 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
         volatile int never = 0;
         if (warp == kLoadWarp && lane == 0) {
             if (issued.pair) mbar_wait_bounded(kfull, (issued.pair - 1) & 1u, &never);
+            if (issued.pair2) mbar_wait_bounded(vfull, (issued.pair2 - 1) & 1u, &never);
             if (issued.tail) mbar_wait_bounded(tail, (issued.tail - 1) & 1u, &never);
             for (uint32_t s = 0; s < min(issued.ring, (uint32_t)ST); ++s)
                 mbar_wait_bounded(full + 8 * s, ((issued.ring - 1 - s) / ST) & 1u, &never);
