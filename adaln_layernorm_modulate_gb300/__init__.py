@@ -139,9 +139,20 @@ def _ptr(t: Any) -> int:
     return int(t.data_ptr())
 
 
+_torch = None  # the module, from the first call that needs it on (an import statement a call takes 0.3 us)
+
+
+def _lazy_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _stream(s: Any) -> int:
     if s is None:
-        import torch
+        torch = _torch or _lazy_torch()
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 1 us less than a Stream object
         if raw is not None:
             return int(raw(torch.cuda.current_device()))
@@ -153,10 +164,11 @@ def _stream(s: Any) -> int:
 
 def _dtype(dtype: Any, t: Any) -> int:
     if dtype is None:
-        import torch
-        if t.dtype == torch.bfloat16:
+        torch = _torch or _lazy_torch()
+        kind = t.dtype
+        if kind == torch.bfloat16:
             return ADALN_BF16
-        if t.dtype == torch.float32:
+        if kind == torch.float32:
             return ADALN_F32
         raise TypeError("unsupported tensor dtype %s" % t.dtype)
     return int(dtype)
@@ -323,12 +335,17 @@ def adaln_linear_xent_bwd(x, weight, target, lse, dloss, dlse, dx, dweight, N, V
         N, V, D, ignore_index, _ptr(workspace), workspace_bytes, _dtype(dtype, x), _stream(stream)))
 
 
+_AXES = [ctypes.c_int32 * n for n in range(9)]  # array types, made once
+
+
 def _axes_array(axes):
     """Host array of the axes' widths: (kept alive by the caller, address, length)."""
-    if axes is None or len(axes) == 0:
+    n = 0 if axes is None else len(axes)
+    if n == 0:
         return None, None, 0
-    arr = (ctypes.c_int32 * len(axes))(*axes)
-    return arr, ctypes.addressof(arr), len(axes)
+    kind = _AXES[n] if n < len(_AXES) else ctypes.c_int32 * n
+    arr = kind(*axes)
+    return arr, ctypes.addressof(arr), n
 
 
 def adaln_qk_norm_rope_fwd(q, k, q_weight, k_weight, pos, q_out, k_out, R, Hq, Hk, d, q_ld, k_ld, q_out_ld,

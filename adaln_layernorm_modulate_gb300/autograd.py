@@ -441,7 +441,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
                  q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
                  theta: float = 10000.0, eps: float = 1e-6, norm: bool = True):
     """Differentiable norms of each head of q [..., Hq, d] and k [..., Hk, d] and their rotation by
-    positions [..., len(axes)] (whole numbers): pairs of neighbouring elements turn, the first axes[0]
+    positions [..., len(axes)] (whole numbers of 32 bits): pairs of neighbouring elements turn, the first axes[0]
     elements with the first position, and so on; elements behind the axes do not turn. Returns (q', k').
     norm=False: the rotation alone; positions=None: the norms alone."""
     return QKNormRopeFunction.apply(q, k, q_weight, k_weight, positions, axes, float(theta), float(eps), bool(norm))

@@ -1238,9 +1238,13 @@ int rope_axes(const int32_t* axes, int32_t naxes, double theta, int32_t d, const
     int64_t pair = 0;
     for (int32_t x = 0; x < naxes; ++x) {
         if (axes[x] < 0 || axes[x] % 2 != 0 || 2 * pair + axes[x] > d) return ADALN_ERR_INVALID_ARG;
+        // Powers of eight neighbours, times one for every eight: a pow each is a third of a small call's time.
+        double near[8] = {1.0}, eighth = 1.0;
+        for (int32_t i = 1; i < std::min(axes[x] / 2, 8); ++i) near[i] = std::pow(theta, -2.0 * i / axes[x]);
         for (int32_t i = 0; i < axes[x] / 2; ++i, ++pair) {
-            const double turns = std::pow(theta, -2.0 * i / axes[x]) / 6.283185307179586476925;
-            a->freq[pair] = (unsigned long long)std::ldexp(turns, 64);  // turns < 1/6
+            if (i % 8 == 0) eighth = i ? std::pow(theta, -2.0 * i / axes[x]) : 1.0;
+            const double turns = eighth * near[i % 8] * 0.159154943091895335769;  // 1 / (2 pi): at most 1/6
+            a->freq[pair] = (unsigned long long)(turns * 18446744073709551616.0);
             a->axis[pair] = (unsigned char)x;
         }
     }

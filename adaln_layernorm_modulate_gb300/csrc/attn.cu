@@ -4,11 +4,11 @@
 //     dv = p^T dout,  dp = dout v^T,  dz = p (dp - delta),  delta = dout . o
 //     dq = scale dz k,  dk = scale dz^T q
 //
-// A plan kernel lists the tiles of rows of all segments, the ones that meet most first; persistent
-// CTAs walk the list, a head at a time. Every product is a tcgen05.mma of 128 rows with its
-// accumulator in tensor memory, its operands brought by TMA; p and dz (bf16, the products' types) are
-// written back to tensor memory over the scores that they come from and are operands from there, so that
-// they never pass through shared memory.
+// attn_prepare_kernel lists the tiles of rows of all segments and cuts them, with the heads, into equal shares;
+// persistent CTAs, one an SM, walk theirs. Every product is a tcgen05.mma of 128 rows with its accumulator in
+// tensor memory, its operands brought by TMA; p and dz (bf16, the products' types) are written back to
+// tensor memory over the scores that they come from and are operands from there, so that they never pass
+// through shared memory.
 //
 //   attn_fwd_kernel: two tiles of 128 queries share the keys and values in shared memory; a
 //       warpgroup each has a thread a row, so that the softmax needs no exchange between threads. The
@@ -17,12 +17,17 @@
 //   attn_dkv: a tile of 128 keys over its queries, transposed: z^T, dp^T, dv += p^T dout,
 //       dk += dz^T q, over all heads that share the keys.
 //
-// dq and dk, dv are two kernels that both compute z and dp (7 products where one kernel would need 5):
-// each sum then stays in tensor memory in a fixed order, without atomics and without an fp32 dq in
-// memory.
+// dq and dk, dv are CTAs of their own that both compute z and dp (7 products where one would need 5): each
+// sum then stays in tensor memory in a fixed order, without atomics and without an fp32 dq in memory.
 //
 // Sums, maxima, exponentials and lse are fp32. Rounded to bf16 as operands: p (half a step, 2^-8 of
-// each value) and dz.
+// each value) and dz. delta is taken from the caller's bf16 o.
+//
+// Bound by the tensor cores from some thousand rows on: 32760 rows, 12 heads of 128, 4.2 ms forward (1.55
+// PFLOP/s, the tensor pipe 72% active; a step of 128 keys and 256 queries takes 2,800 cycles, its products 2,048).
+// 16384 rows 1.0 ms forward (1.66 PFLOP/s) and 3.5 ms backward (1.18 PFLOP/s, 1.65 with the second z and
+// dp; 75% active: operands and incoming tiles take all that shared memory gives). Short segments by the units'
+// beginnings and ends, the smallest calls by the chain of launches (153 rows: 11 + 17 us).
 #include <algorithm>
 #include <atomic>
 
@@ -404,17 +409,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return w;
 }
 
-// 32 columns of a row to memory as bf16, as far as the row's d elements go.
-__device__ __forceinline__ void store32(void* row, int col, int d, const float (&v)[32], float f) {
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        if (col + 8 * g >= d) break;
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack2(v[8 * g + 2 * j] * f, v[8 * g + 2 * j + 1] * f);
-        st_vec(reinterpret_cast<__nv_bfloat16*>(row) + col + 8 * g, make_uint4(w[0], w[1], w[2], w[3]));
-    }
-}
 // A warp's 32 rows, 64 columns from `col` on, through its 4 KB of shared memory and out by one TMA store
 // (every lane's own 16-byte stores took 10,000 cycles for two tiles of 128 x 128); rows that another
 // segment follows within the warp's 32 go directly. The buffer's last store has been read.
@@ -652,146 +646,146 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
-            const int i = warp >> 2;  // this warpgroup's tile of queries
-            const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), st = lanes + 128 * i, ot = lanes + 256 + 128 * i;
-            const int r = (warp & 3) * 32 + lane;
-            const float sl2 = a.scale * kLog2e;
-            const uint32_t out_buf = ring + ST * S::kTile + warp * kAttnOut;
-            uint32_t tiles = 0;
-            bool live = true;
-            while (live && next()) {
-                const int row = i * kAttnTile + r, end = i ? t1[1] : t1[0];
-                // Keys that this row sees.
-                const int seen = max(0, min(it.others, it.shift + row + 1));
-                float m = neg_inf(), l = 0.0f;  // the exponentials' reference, their sum
-                for (int t = t0; t < end; ++t, ++tiles) {
-                    live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sfull + 8 * i, tiles & 1u, &abort_flag));
-                    if (!live) break;
-                    tc_fence_after();
-                    float v[64], w[64];
-                    const int lim = seen - walk.tile(t) * kAttnTile;
-                    const bool cut = __any_sync(0xFFFFFFFFu, lim < kAttnTile);
-                    tmem_ld128(st, v, w);
-                    if (cut) {
-#pragma unroll
-                        for (int j = 0; j < 64; ++j) {
-                            v[j] = j < lim ? v[j] : neg_inf();
-                            w[j] = 64 + j < lim ? w[j] : neg_inf();
-                        }
-                    }
-                    float m4[4] = {v[0], v[1], w[0], w[1]};
-#pragma unroll
-                    for (int j = 2; j < 64; j += 2) {
-                        m4[0] = fmaxf(m4[0], v[j]);
-                        m4[1] = fmaxf(m4[1], v[j + 1]);
-                        m4[2] = fmaxf(m4[2], w[j]);
-                        m4[3] = fmaxf(m4[3], w[j + 1]);
-                    }
-                    const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    const f2r s2 = p_splat(sl2);
-                    f2r c2, sum[2];
-                    uint32_t b[32];
-                    // Exponentials of 64 scores against the reference, their sum; a row that has seen nothing yet
-                    // has none but 0 (and NaN stays).
-                    auto half = [&](const float (&x)[64]) {
-                        c2 = p_splat(m == neg_inf() ? 0.0f : -m * sl2);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float2 e = p_get(p_fma(p_make(x[2 * j], x[2 * j + 1]), s2, c2));
-                            const float e0 = exp2_ftz(e.x), e1 = exp2_ftz(e.y);
-                            sum[j & 1] = p_add(sum[j & 1], p_make(e0, e1));
-                            b[j] = pack2(e0, e1);
-                        }
-                    };
-                    // The first half's against the reference of the step before, while the maximum is still being
-                    // found; it seldom has to be done again.
-                    sum[0] = sum[1] = kPairZero;
-                    half(v);
-                    if (__any_sync(0xFFFFFFFFu, t == t0 || (mt - m) * sl2 > 8.0f)) {
-                        // The reference may lag behind the maximum by 2^8, which fp32 sums and bf16 p take as
-                        // well as 1; beyond it, what has been summed is brought to the new one.
-                        const float to = t == t0 ? mt : fmaxf(m, mt);
-                        if (t > t0) {
-                            const float f = to == m ? 1.0f : exp2_ftz((m - to) * sl2);
-                            live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
-                            if (!live) break;
-                            tc_fence_after();
-                            l *= f;
-#pragma unroll 1
-                            for (int c = 0; c < a.d; c += 32) {
-                                float o[32];
-                                tmem_ld32(ot + c, o);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) b[j] = __float_as_uint(o[j] * f);
-                                tmem_st32(ot + c, b);
-                            }
-                        }
-                        m = to;
-                        tmem_ld64(st, v);
-                        if (cut) {
-#pragma unroll
-                            for (int j = 0; j < 64; ++j) v[j] = j < lim ? v[j] : neg_inf();
-                        }
-                        sum[0] = sum[1] = kPairZero;
-                        half(v);
-                    }
-                    tmem_st32(st, b);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(pfull + 8 * i);
-                    half(w);
-                    tmem_st32(st + 32, b);
-                    l += p_hsum(p_add(sum[0], sum[1]));
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(pfull2 + 8 * i);
-                }
+        const int i = warp >> 2;  // this warpgroup's tile of queries
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), st = lanes + 128 * i, ot = lanes + 256 + 128 * i;
+        const int r = (warp & 3) * 32 + lane;
+        const float sl2 = a.scale * kLog2e;
+        const uint32_t out_buf = ring + ST * S::kTile + warp * kAttnOut;
+        uint32_t tiles = 0;
+        bool live = true;
+        while (live && next()) {
+            const int row = i * kAttnTile + r, end = i ? t1[1] : t1[0];
+            // Keys that this row sees.
+            const int seen = max(0, min(it.others, it.shift + row + 1));
+            float m = neg_inf(), l = 0.0f;  // the exponentials' reference, their sum
+            for (int t = t0; t < end; ++t, ++tiles) {
+                live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(sfull + 8 * i, tiles & 1u, &abort_flag));
                 if (!live) break;
-                walk.fetch();
-                const bool mine = row < it.rows;
-                const int64_t at = (int64_t)it.row0 + row;
-                const bool in = mine && ADALN_IN_ATTN(at >= 0 && at < a.Rq && head < a.Hq);
-                const bool none = l == 0.0f;  // no key seen: zeros
-                if (end > t0) {
-                    live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
-                    if (!live) break;
-                    tc_fence_after();
-                }
-                if (walk.whole(n)) {
-                    if (in) a.lse[(int64_t)head * a.Rq + at] = none ? neg_inf() : fmaf(m, a.scale, logf(l));
-                    const float f = 1.0f / l;
-                    const int first = i * kAttnTile + (warp & 3) * 32, rows = min(32, it.rows - first);
-#pragma unroll 1
-                    for (int c = 0; c < a.d && rows > 0; c += 64) {
-                        uint32_t b[32];
-                        if (end > t0) read64(ot + c, f, b);
+                tc_fence_after();
+                float v[64], w[64];
+                const int lim = seen - walk.tile(t) * kAttnTile;
+                const bool cut = __any_sync(0xFFFFFFFFu, lim < kAttnTile);
+                tmem_ld128(st, v, w);
+                if (cut) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) b[j] = none ? 0u : b[j];
-                        tma_store_read();  // the lane that issued the buffer's last store has it read
-                        __syncwarp();
-                        out64(&mo, out_buf, b, c, head, it.row0 + first, in || !mine ? rows : 0,
-                              reinterpret_cast<__nv_bfloat16*>(a.o) + at * a.o_ld + (int64_t)head * a.d, a.d, lane);
+                    for (int j = 0; j < 64; ++j) {
+                        v[j] = j < lim ? v[j] : neg_inf();
+                        w[j] = 64 + j < lim ? w[j] : neg_inf();
                     }
-                } else {
-                    const int64_t place = (int64_t)walk.slot() * a.slot_rows + row;
-                    if (end > t0) {
+                }
+                float m4[4] = {v[0], v[1], w[0], w[1]};
+#pragma unroll
+                for (int j = 2; j < 64; j += 2) {
+                    m4[0] = fmaxf(m4[0], v[j]);
+                    m4[1] = fmaxf(m4[1], v[j + 1]);
+                    m4[2] = fmaxf(m4[2], w[j]);
+                    m4[3] = fmaxf(m4[3], w[j + 1]);
+                }
+                const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                const f2r s2 = p_splat(sl2);
+                f2r c2, sum[2];
+                uint32_t b[32];
+                // Exponentials of 64 scores against the reference, their sum; a row that has seen nothing yet
+                // has none but 0 (and NaN stays).
+                auto half = [&](const float (&x)[64]) {
+                    c2 = p_splat(m == neg_inf() ? 0.0f : -m * sl2);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float2 e = p_get(p_fma(p_make(x[2 * j], x[2 * j + 1]), s2, c2));
+                        const float e0 = exp2_ftz(e.x), e1 = exp2_ftz(e.y);
+                        sum[j & 1] = p_add(sum[j & 1], p_make(e0, e1));
+                        b[j] = pack2(e0, e1);
+                    }
+                };
+                // The first half's against the reference of the step before, while the maximum is still being
+                // found; it seldom has to be done again.
+                sum[0] = sum[1] = kPairZero;
+                half(v);
+                if (__any_sync(0xFFFFFFFFu, t == t0 || (mt - m) * sl2 > 8.0f)) {
+                    // The reference may lag behind the maximum by 2^8, which fp32 sums and bf16 p take as
+                    // well as 1; beyond it, what has been summed is brought to the new one.
+                    const float to = t == t0 ? mt : fmaxf(m, mt);
+                    if (t > t0) {
+                        const float f = to == m ? 1.0f : exp2_ftz((m - to) * sl2);
+                        live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
+                        if (!live) break;
+                        tc_fence_after();
+                        l *= f;
 #pragma unroll 1
                         for (int c = 0; c < a.d; c += 32) {
                             float o[32];
                             tmem_ld32(ot + c, o);
-                            if (in && ADALN_IN_ATTN(row < a.slot_rows))
-                                store_piece32(a.part + (int64_t)walk.slot() * a.slot_rows * a.d, row, a.slot_rows, c, a.d, o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) b[j] = __float_as_uint(o[j] * f);
+                            tmem_st32(ot + c, b);
                         }
                     }
-                    if (in && ADALN_IN_ATTN(row < a.slot_rows)) a.ml[place] = make_float2(m, l);
+                    m = to;
+                    tmem_ld64(st, v);
+                    if (cut) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) v[j] = j < lim ? v[j] : neg_inf();
+                    }
+                    sum[0] = sum[1] = kPairZero;
+                    half(v);
                 }
-                if (end > t0) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(ofree + 8 * i);
-                }
+                tmem_st32(st, b);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfull + 8 * i);
+                half(w);
+                tmem_st32(st + 32, b);
+                l += p_hsum(p_add(sum[0], sum[1]));
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfull2 + 8 * i);
             }
-            tma_store_wait();
+            if (!live) break;
+            walk.fetch();
+            const bool mine = row < it.rows;
+            const int64_t at = (int64_t)it.row0 + row;
+            const bool in = mine && ADALN_IN_ATTN(at >= 0 && at < a.Rq && head < a.Hq);
+            const bool none = l == 0.0f;  // no key seen: zeros
+            if (end > t0) {
+                live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));
+                if (!live) break;
+                tc_fence_after();
+            }
+            if (walk.whole(n)) {
+                if (in) a.lse[(int64_t)head * a.Rq + at] = none ? neg_inf() : fmaf(m, a.scale, logf(l));
+                const float f = 1.0f / l;
+                const int first = i * kAttnTile + (warp & 3) * 32, rows = min(32, it.rows - first);
+#pragma unroll 1
+                for (int c = 0; c < a.d && rows > 0; c += 64) {
+                    uint32_t b[32];
+                    if (end > t0) read64(ot + c, f, b);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) b[j] = none ? 0u : b[j];
+                    tma_store_read();  // the lane that issued the buffer's last store has it read
+                    __syncwarp();
+                    out64(&mo, out_buf, b, c, head, it.row0 + first, in || !mine ? rows : 0,
+                          reinterpret_cast<__nv_bfloat16*>(a.o) + at * a.o_ld + (int64_t)head * a.d, a.d, lane);
+                }
+            } else {
+                const int64_t place = (int64_t)walk.slot() * a.slot_rows + row;
+                if (end > t0) {
+#pragma unroll 1
+                    for (int c = 0; c < a.d; c += 32) {
+                        float o[32];
+                        tmem_ld32(ot + c, o);
+                        if (in && ADALN_IN_ATTN(row < a.slot_rows))
+                            store_piece32(a.part + (int64_t)walk.slot() * a.slot_rows * a.d, row, a.slot_rows, c, a.d, o);
+                    }
+                }
+                if (in && ADALN_IN_ATTN(row < a.slot_rows)) a.ml[place] = make_float2(m, l);
+            }
+            if (end > t0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ofree + 8 * i);
+            }
+        }
+        tma_store_wait();
     }
     __syncwarp();
     tc_fence_before();
