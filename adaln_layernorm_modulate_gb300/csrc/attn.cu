@@ -124,10 +124,10 @@ __device__ __forceinline__ int64_t warp_before(int64_t v, int lane, int64_t* tot
 }
 
 constexpr int kPlanThreads = 512;
-constexpr int kAttnFewSegs = 512;  // kept in shared memory while they are planned
+constexpr int kAttnFewSegs = 1024;  // kept in shared memory while they are planned
 
 // One CTA a list. The entries are in the order of the rows: entries and cost of every segment, sums over
-// those before it, then the entries (a warp a segment) and where each CTA begins. Everything follows
+// those before it, then the entries and where each CTA begins. Everything follows
 // from the tables alone, so that pieces, and with them the order of sums, are the same every time.
 __device__ __forceinline__ void attn_plan(const AttnPlanArgs& a, int list) {
     constexpr int NW = kPlanThreads / 32;
@@ -221,54 +221,69 @@ __device__ __forceinline__ void attn_plan(const AttnPlanArgs& a, int list) {
         }
         l.cursors[c] = cur;
     }
-    if (any_bad) return;
-    for (int64_t s = NW - 1 - warp; s < t.nseg; s += NW) {  // the first warps have the cursors
+    // A thread an entry, the last ones first: the first threads have the cursors.
+    for (int64_t i = kPlanThreads - 1 - tid; i < count; i += kPlanThreads) {
+        int64_t lo = 0, hi = t.nseg - 1;  // the last segment that begins at or before the entry
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) >> 1;
+            if (segs[mid].x <= i) lo = mid;
+            else hi = mid - 1;
+        }
         bool bad = false;
-        const AttnSegment g = segment(s, &bad);
-        const int64_t before = segs[s].x;
-        const int tiles = tiles_of(g);
-        for (int i = lane; i < tiles; i += 32)
-            if (before + i < l.most && ADALN_IN_ATTN(before >= 0)) l.items[before + i] = attn_entry(t, l, list, g, i * l.tile);
+        const AttnSegment g = segment(lo, &bad);
+        if (ADALN_IN_ATTN(i < l.most)) l.items[i] = attn_entry(t, l, list, g, (int)(i - segs[lo].x) * l.tile);
     }
 }
 
-// delta = dout . o of every row and head, and lse in units of log 2: a warp a row, 16 lanes a head.
+// delta = dout . o of every row and head, and lse in units of log 2: 16 lanes a head, a warp two heads of a row,
+// four such pairs on their way.
 __device__ __forceinline__ void attn_delta(const AttnDeltaArgs& a, int64_t block, int64_t blocks) {
-    constexpr int U = 4;  // pairs of heads on their way
-    const int lane = threadIdx.x & 15, group = threadIdx.x >> 4 & 1, vecs = a.d / 8;
-    constexpr int NW = kPlanThreads / 32;
-    for (int64_t r = block * NW + (threadIdx.x >> 5); r < a.Rq; r += blocks * NW) {
-        const __nv_bfloat16* x0 = reinterpret_cast<const __nv_bfloat16*>(a.dout) + r * a.do_ld + 8 * lane;
-        const __nv_bfloat16* y0 = reinterpret_cast<const __nv_bfloat16*>(a.o) + r * a.o_ld + 8 * lane;
-        for (int h0 = group; h0 - group < a.Hq; h0 += 2 * U) {
-            uint4 x[U], y[U];
-            float lse[U];
+    constexpr int U = 4, NW = kPlanThreads / 32;
+    const int lane = threadIdx.x & 15, group = threadIdx.x >> 4 & 1, vecs = a.d / 8, pairs = (a.Hq + 1) / 2;
+    const int64_t first = block * NW + (threadIdx.x >> 5), step = blocks * NW;
+    // The warp's next pair, and what a step adds to it.
+    int64_t r = first / pairs;
+    int at = (int)(first % pairs);
+    const int64_t dr = step / pairs;
+    const int da = (int)(step % pairs);
+    while (r < a.Rq) {
+        uint4 x[U], y[U];
+        float lse[U];
+        int64_t rows[U];
+        int heads[U];
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int h = h0 + 2 * j;
-                x[j] = y[j] = make_uint4(0, 0, 0, 0);
-                lse[j] = 0.0f;
-                if (h < a.Hq && lane < vecs && ADALN_IN_ATTN(r >= 0 && r < a.Rq)) {
-                    x[j] = ld_stream(x0 + (int64_t)h * a.d);
-                    y[j] = __ldcg(reinterpret_cast<const uint4*>(y0 + (int64_t)h * a.d));  // of a kernel that may be close ahead
-                    if (lane == 0) lse[j] = __ldcg(a.lse + (int64_t)h * a.Rq + r);
-                }
+        for (int j = 0; j < U; ++j) {
+            const int h = heads[j] = 2 * at + group;
+            rows[j] = r;
+            x[j] = y[j] = make_uint4(0, 0, 0, 0);
+            lse[j] = 0.0f;
+            if (r < a.Rq && h < a.Hq && lane < vecs && ADALN_IN_ATTN(r >= 0)) {
+                const int64_t off = (int64_t)h * a.d + 8 * lane;
+                x[j] = ld_stream(reinterpret_cast<const __nv_bfloat16*>(a.dout) + r * a.do_ld + off);
+                // (o and lse are of a kernel that may be close ahead: from L2.)
+                y[j] = __ldcg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.o) + r * a.o_ld + off));
+                if (lane == 0) lse[j] = __ldcg(a.lse + (int64_t)h * a.Rq + r);
             }
+            r += dr;
+            at += da;
+            if (at >= pairs) {
+                at -= pairs;
+                ++r;
+            }
+        }
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int h = h0 + 2 * j;
-                f2r p[4], q[4], sum = kPairZero;
-                Io<__nv_bfloat16>::unpackp(x[j], p);
-                Io<__nv_bfloat16>::unpackp(y[j], q);
+        for (int j = 0; j < U; ++j) {
+            f2r p[4], q[4], sum = kPairZero;
+            Io<__nv_bfloat16>::unpackp(x[j], p);
+            Io<__nv_bfloat16>::unpackp(y[j], q);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sum = p_fma(p[e], q[e], sum);
-                float v = p_hsum(sum);
+            for (int e = 0; e < 4; ++e) sum = p_fma(p[e], q[e], sum);
+            float v = p_hsum(sum);
 #pragma unroll
-                for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-                if (lane == 0 && h < a.Hq && ADALN_IN_ATTN(r < a.Rq)) {
-                    a.delta[(int64_t)h * a.Rq + r] = v;
-                    a.lse2[(int64_t)h * a.Rq + r] = lse[j] * kLog2e;
-                }
+            for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            if (lane == 0 && rows[j] < a.Rq && heads[j] < a.Hq && ADALN_IN_ATTN(rows[j] >= 0)) {
+                a.delta[(int64_t)heads[j] * a.Rq + rows[j]] = v;
+                a.lse2[(int64_t)heads[j] * a.Rq + rows[j]] = lse[j] * kLog2e;
             }
         }
     }
@@ -1647,7 +1662,7 @@ cudaError_t launch_attn_prepare(const AttnPlanArgs& plan, const AttnDeltaArgs& d
     AttnPlanArgs p = plan;
     AttnDeltaArgs d = delta;
     int lists = p.list[1].items ? 2 : 1;
-    const unsigned ctas = d.delta && d.Rq > 0 ? cap((d.Rq + kPlanThreads / 32 - 1) / (kPlanThreads / 32), 4 * (int64_t)sms) : 0;
+    const unsigned ctas = d.delta && d.Rq > 0 ? cap((d.Rq * ((d.Hq + 1) / 2) + 63) / 64, 4 * (int64_t)sms) : 0;
     void* params[] = {&p, &d, &lists};
     return launch_dependent(reinterpret_cast<const void*>(&attn_prepare_kernel), dim3(lists + ctas), dim3(kPlanThreads), params,
                             0, stream);
