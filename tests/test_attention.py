@@ -481,6 +481,54 @@ def test_calls_back_to_back(d):
 
 
 @pytest.mark.gpu
+def test_two_streams_at_once():
+    sets = [inputs([900, 300], [900, 300], 4, 2, 64, seed=30), inputs([5, 400], [3000, 200], 2, 2, 128, seed=31)]
+    want = [call(i, pad=0) for i in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for n, i in enumerate(sets):
+            with torch.cuda.stream(streams[n]):
+                (Rq, Hq, d), (Rk, Hk, _) = i["q"].shape, i["k"].shape
+                sizes = (2, Rq, Rk, Hq, Hk, d)
+                out = {m: torch.empty_like(t) for m, t in want[n].items()}
+                nb = max(A.adaln_attention_fwd_workspace_size(*sizes, 1), A.adaln_attention_bwd_workspace_size(*sizes, 1))
+                ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+                lq, lk, sc = Hq * d, Hk * d, d ** -0.5
+                A.adaln_attention_fwd(i["q"], i["k"], i["v"], out["o"], out["lse"], i["cu_q"], i["cu_k"], *sizes, lq, lk, lk, lq,
+                                      sc, False, ws, nb)
+                A.adaln_attention_bwd(i["dout"], i["q"], i["k"], i["v"], out["o"], out["lse"], out["dq"], out["dk"], out["dv"],
+                                      i["cu_q"], i["cu_k"], *sizes, lq, lq, lk, lk, lq, lq, lk, lk, sc, False, ws, nb)
+                got[n].append((out, ws))
+    torch.cuda.synchronize()
+    for n in range(2):
+        for out, ws in got[n]:
+            assert A.adaln_read_status(ws) == 0
+            assert all(torch.equal(out[m], want[n][m]) for m in out), n
+
+
+@pytest.mark.gpu
+def test_thousands_of_segments():
+    # More segments than the work list keeps on chip. Rows of at most one tile of keys do not depend on what they
+    # are packed with.
+    lens = [(7 * s) % 23 for s in range(2500)]
+    i = inputs(lens, lens, 2, 1, 64, seed=32)
+    whole = call(i, True, pad=0)
+    cut = sum(lens[:900])
+    for rows, part in ((slice(0, cut), lens[:900]), (slice(cut, None), lens[900:])):
+        cu = torch.tensor([0] + part, device="cuda").cumsum(0).to(torch.int32)
+        j = dict({n: i[n][rows] for n in ("q", "k", "v", "dout")}, cu_q=cu, cu_k=cu, lens_q=part, lens_k=part)
+        got = call(j, True, pad=0)
+        assert all(torch.equal(got[n], whole[n][rows]) for n in ("o", "dq", "dk", "dv"))
+        assert torch.equal(got["lse"], whole["lse"][:, rows])
+    few = dict({n: i[n][:cut] for n in ("q", "k", "v", "dout")}, lens_q=lens[:60], lens_k=lens[:60])
+    rows = sum(lens[:60])
+    few = {n: (t[:rows] if torch.is_tensor(t) else t) for n, t in few.items()}
+    check(few, {n: (t[:, :rows] if n == "lse" else t[:rows]) for n, t in whole.items()}, True)
+
+
+@pytest.mark.gpu
 def test_one_workspace_for_changing_inputs():
     # What a call leaves in the workspace, or a cache holds of it, is nothing to the next.
     lens = [([700, 300], [700, 300]), ([200, 800], [500, 500]), ([999, 1], [1, 999])]
