@@ -26,6 +26,7 @@ vocabulary loss without its logits (``linear_cross_entropy``).
 from __future__ import annotations
 
 import contextlib
+import math
 from typing import Optional
 
 import torch
@@ -401,19 +402,19 @@ class QKNormRopeFunction(torch.autograd.Function):
                 raise ValueError("qk_norm_rope: positions [..., axes], one width of `axes` each")
             positions = positions.to(torch.int32).contiguous()
         lead = q.shape[:-2]
-        qr, kr = _rows(q.reshape(-1, Hq, d)), _rows(k.reshape(-1, Hk, d))
-        R = qr.shape[0]
+        R = math.prod(lead)
+        qr, kr = _rows(q.reshape(R, Hq, d)), _rows(k.reshape(R, Hk, d))
         q_weight = None if q_weight is None else q_weight.contiguous()
         k_weight = None if k_weight is None else k_weight.contiguous()
-        qo = torch.empty((R, Hq, d), dtype=q.dtype, device=q.device)
-        ko = torch.empty((R, Hk, d), dtype=q.dtype, device=q.device)
+        # (In their own shape, and not saved: views would refuse to be changed in place.)
+        qo, ko = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k))
         with _on(q):
             adaln_qk_norm_rope_fwd(qr, kr, q_weight, k_weight, positions, qo, ko, R, Hq, Hk, d, _ld(qr), _ld(kr),
                                    Hq * d, Hk * d, axes, theta, eps, norm, dt)
-        ctx.save_for_backward(*((qr, kr) if norm else (qo[:0], ko[:0])), q_weight, k_weight, positions)
+        ctx.save_for_backward(*((qr, kr) if norm else (None, None)), q_weight, k_weight, positions)
         ctx.sizes = lead, R, Hq, Hk, d
         ctx.args = axes, theta, eps, norm
-        return qo.view(*lead, Hq, d), ko.view(*lead, Hk, d)
+        return qo, ko
 
     @staticmethod
     @once_differentiable
@@ -430,7 +431,7 @@ class QKNormRopeFunction(torch.autograd.Function):
         with _on(dqo):
             nb = adaln_qk_norm_rope_bwd_workspace_size(R, Hq, Hk, d, dt)
             ws = _workspace(nb, dqo.device)
-            adaln_qk_norm_rope_bwd(dqo, dko, q if norm else None, k if norm else None, q_weight, k_weight, positions,
+            adaln_qk_norm_rope_bwd(dqo, dko, q, k, q_weight, k_weight, positions,
                                    dq, dk, dwq, dwk, ws, nb, R, Hq, Hk, d, _ld(dqo), _ld(dko), _ld(q) if norm else 0,
                                    _ld(k) if norm else 0, Hq * d, Hk * d, axes, theta, eps, norm, dt)
         return (dq.view(*lead, Hq, d), dk.view(*lead, Hk, d), None if dwq is None else dwq.to(dq.dtype),

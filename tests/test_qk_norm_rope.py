@@ -355,3 +355,33 @@ def test_repeat_side_stream_and_graph_replay():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(out[n], want[n]) for n in want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("norm", [True, False])
+def test_outputs_changed_in_place(norm):
+    # Halving is exact, forward and backward.
+    from adaln_layernorm_modulate_gb300.autograd import qk_norm_rope
+    i = inputs(30, 4, 2, 64, (32, 32), torch.bfloat16, weights=norm, seed=14)
+    want = call(i, norm=norm, sums=norm)
+    q, k = (i[n].clone().requires_grad_(True) for n in "qk")
+    qo, ko = qk_norm_rope(q, k, i["pos"], (32, 32), *i["w"], norm=norm)
+    qo.mul_(0.5)
+    ko *= 2
+    torch.autograd.backward([qo, ko], [i["dq_out"], i["dk_out"]])
+    assert torch.equal(qo.detach(), 0.5 * want["q_out"]) and torch.equal(ko.detach(), 2 * want["k_out"])
+    assert torch.equal(q.grad, 0.5 * want["dq"]) and torch.equal(k.grad, 2 * want["dk"])
+
+
+@pytest.mark.gpu
+def test_node_without_rows_or_heads():
+    from adaln_layernorm_modulate_gb300.autograd import QKNormRope
+    m = QKNormRope(64, (64,), device="cuda", dtype=torch.bfloat16)
+    for shape, heads in (((0, 5), 2), ((3, 0), 2), ((3, 5), 0), ((0,), 0)):
+        q = torch.ones(*shape, 2, 64, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+        k = torch.ones(*shape, heads, 64, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+        qo, ko = m(q, k, torch.zeros(*shape, 1, dtype=torch.int32, device="cuda"))
+        assert qo.shape == q.shape and ko.shape == k.shape
+        (qo.sum() + ko.sum()).backward()
+        assert q.grad.shape == q.shape and k.grad.shape == k.shape and (m.k_weight.grad == 0).all()
+        m.zero_grad()
