@@ -546,4 +546,4 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Opt
     o, lse = AttentionFunction.apply(q.flatten(0, 1), k.flatten(0, 1), v.flatten(0, 1), None, None, B, bool(causal),
                                      scale, check_tables)
     o = o.view(B, N, *o.shape[1:])
-    return (o, lse.view(-1, B, N)) if return_lse else o
+    return (o, lse.view(lse.shape[0], B, N)) if return_lse else o

@@ -595,3 +595,16 @@ def test_with_head_norms_and_rotation():
     # A handful of bf16 roundings in the chain (q', k', p, dz, their gradients), independent between elements.
     for got, want in ((rows.grad, rd.grad), (w[0].grad, wd[0].grad), (w[1].grad, wd[1].grad)):
         assert (got.double() - want).norm() <= 6 * H * want.norm()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,N,M", [(0, 5, 7), (3, 0, 7), (3, 5, 0), (0, 0, 0)])
+def test_node_without_rows(B, N, M):
+    from adaln_layernorm_modulate_gb300.autograd import attention
+    q, k, v = (torch.randn(B, n, h, 64, device="cuda", dtype=torch.bfloat16).requires_grad_(True)
+               for n, h in ((N, 4), (M, 2), (M, 2)))
+    for causal in (False, True):
+        o, lse = attention(q, k, v, causal=causal, return_lse=True, check_tables=True)
+        assert o.shape == q.shape and lse.shape == (4, B, N) and (o == 0).all() and (lse == -math.inf).all()
+        o.sum().backward()
+        assert all(t.grad.shape == t.shape and (t.grad == 0).all() for t in (q, k, v))
