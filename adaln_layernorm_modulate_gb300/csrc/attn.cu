@@ -716,10 +716,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                 // found; it seldom has to be done again.
                 sum[0] = sum[1] = kPairZero;
                 half(v);
-                if (__any_sync(0xFFFFFFFFu, t == t0 || (mt - m) * sl2 > 8.0f)) {
-                    // The reference may lag behind the maximum by 2^8, which fp32 sums and bf16 p take as
-                    // well as 1; beyond it, what has been summed is brought to the new one.
-                    const float to = t == t0 ? mt : fmaxf(m, mt);
+                // The reference may lag behind the maximum by 2^8, which fp32 sums and bf16 p take as well as 1;
+                // beyond it, what has been summed is brought to the new one. Each row goes by its own scores: the
+                // others' decide only whether the warp comes here, where a row whose reference stays is
+                // multiplied by 1. Rows behind the segment's last, which meet its keys too, do not ask for it.
+                const bool jump = (mt - m) * sl2 > 8.0f;
+                if (__any_sync(0xFFFFFFFFu, t == t0 || (jump && row < it.rows))) {
+                    const float to = t == t0 || jump ? mt : m;
                     if (t > t0) {
                         const float f = to == m ? 1.0f : exp2_ftz((m - to) * sl2);
                         live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(odone + 8 * i, (tiles - 1) & 1u, &abort_flag));

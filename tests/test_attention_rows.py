@@ -1,0 +1,44 @@
+"""What reaches a row of attention and what does not: other rows of its tile, other segments."""
+import pytest
+import torch
+
+from tests.test_attention import call, inputs
+
+
+def changed(i, **rows):
+    """A copy of the inputs; name -> (rows, factor)."""
+    j = {n: (v.clone() if torch.is_tensor(v) else v) for n, v in i.items()}
+    for n, (at, f) in rows.items():
+        j[n][at] = (j[n][at].float() * f).bfloat16()
+    return j
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens_q,lens_k,causal", [([70, 60], [600, 600], False), ([9, 200], [3000, 300], False),
+                                                  ([270, 300], [900, 300], True), ([1, 500], [5000, 500], False)])
+def test_finite_neighbours_do_not_matter(lens_q, lens_k, causal, d):
+    # The second segment's queries share a tile with the first one's; their scores on its keys differ by
+    # hundreds from tile to tile. The keys grow along the segment, so that the maxima do.
+    i = inputs(lens_q, lens_k, 4, 2, d, seed=40)
+    n, m = lens_q[0], lens_k[0]
+    ramp = 0.5 + torch.arange(m, device="cuda")[:, None, None] / m
+    i = changed(i, k=(slice(0, m), ramp))
+    want = call(i, causal)
+    got = call(changed(i, q=(slice(n, None), 50), dout=(slice(n, None), 7), v=(slice(m, None), 3)), causal)
+    for x, at in (("o", n), ("dq", n), ("dk", m), ("dv", m)):
+        assert torch.equal(got[x][:at], want[x][:at]), x
+    assert torch.equal(got["lse"][:, :n], want["lse"][:, :n])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,m,causal", [(128, 700, False), (1000, 1000, True), (5, 4000, False)])
+def test_a_row_does_not_depend_on_the_rows_beside_it(n, m, causal, d):
+    i = inputs([n], [m], 2, 1, d, seed=41)
+    want = call(i, causal)
+    odd = torch.arange(n, device="cuda") % 2 == 1
+    got = call(changed(i, q=(odd, 40), dout=(odd, 3)), causal)
+    for x in ("o", "dq"):
+        assert torch.equal(got[x][~odd], want[x][~odd]), x
+    assert torch.equal(got["lse"][:, ~odd], want["lse"][:, ~odd])
