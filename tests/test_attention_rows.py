@@ -1,8 +1,11 @@
-"""What reaches a row of attention and what does not: other rows of its tile, other segments."""
+"""What reaches a row of attention and what does not: other rows of its tile, other segments; and that every
+output is written."""
 import pytest
 import torch
 
-from tests.test_attention import call, inputs
+from tests.test_attention import CASES, call, check, inputs
+
+GRADS = ("o", "dq", "dk", "dv")
 
 
 def changed(i, **rows):
@@ -42,3 +45,14 @@ def test_a_row_does_not_depend_on_the_rows_beside_it(n, m, causal, d):
     for x in ("o", "dq"):
         assert torch.equal(got[x][~odd], want[x][~odd]), x
     assert torch.equal(got["lse"][:, ~odd], want["lse"][:, ~odd])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", list(CASES))
+def test_every_output_is_written(name):
+    # (check() takes a dq that is NaN throughout for one that was not asked for.)
+    lens_q, lens_k, Hq, Hk, d, causal = CASES[name]
+    i = inputs(lens_q, lens_q if lens_k is None else lens_k, Hq, Hk, d, seed=50 + len(name))
+    got = call(i, causal)
+    assert not any(got[n].isnan().any() for n in GRADS + ("lse",))
+    check(i, got, causal)
