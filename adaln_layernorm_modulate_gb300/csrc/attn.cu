@@ -84,6 +84,7 @@ __device__ __forceinline__ AttnItem attn_entry(const AttnTables& t, const AttnLi
         it.shift = t.causal ? at + g.nk - g.nq : g.nk;
     else
         it.shift = t.causal ? at - g.nk + g.nq : -kAttnTile;
+    it.unseen = list && t.causal ? max(0, g.nq - g.nk) : 0;
     return it;
 }
 
@@ -305,13 +306,14 @@ __device__ __forceinline__ AttnItem attn_item(const AttnList& l, int64_t i) {
     AttnItem it{};
     if (!ADALN_IN_ATTN(i >= 0 && i < l.most)) return it;
     const int4 a = __ldcg(reinterpret_cast<const int4*>(l.items + i));
-    const int2 b = __ldcg(reinterpret_cast<const int2*>(l.items + i) + 2);
+    const int4 b = __ldcg(reinterpret_cast<const int4*>(l.items + i) + 1);
     it.row0 = a.x;
     it.rows = a.y;
     it.other0 = a.z;
     it.others = a.w;
     it.shift = b.x;
     it.end = b.y;
+    it.unseen = b.z;
     return it;
 }
 __device__ __forceinline__ AttnCursor attn_cursor(const AttnList& l, int c) {
@@ -378,12 +380,12 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
     tma_load3(dst, map, 0, head, row, bar);
     if (DP == 128) tma_load3(dst + kPanel, map, 64, head, row, bar);
 }
-// Rows [from, 128) of a tile become zeros: what follows a segment may hold anything, and 0 * NaN is NaN.
+// Rows [from, to) of a tile become zeros: what follows a segment may hold anything, and 0 * NaN is NaN.
 template <int DP>
-__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int lane) {
+__device__ __forceinline__ void zero_rows(uint32_t tile, int from, int to, int lane) {
 #pragma unroll
     for (int p = 0; p < DP / 64; ++p) {
-        for (uint32_t at = (uint32_t)from * 128 + 16 * lane; at < kPanel; at += 512)
+        for (uint32_t at = (uint32_t)from * 128 + 16 * lane; at < (uint32_t)to * 128; at += 512)
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + p * kPanel + at), "r"(0u) : "memory");
     }
 }
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_fwd_kernel(const __grid_
                             live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail, issued.tail & 1u, &abort_flag));
                             ++issued.tail;
                             if (live) {
-                                zero_rows<DP>(dst, left, lane);
+                                zero_rows<DP>(dst, left, kAttnTile, lane);
                                 fence_shared_async();
                             }
                             __syncwarp();
@@ -937,7 +939,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 }
 
 // ---- backward --------------------------------------------------------------------------------
-// 64 scores of a row to exponentials, those outside [from, to) 0.
+// 64 values of a row, those outside [from, to) 0.
 __device__ __forceinline__ void mask64(float (&p)[64], int from, int to) {
 #pragma unroll
     for (int j = 0; j < 64; ++j) p[j] = j >= from && j < to ? p[j] : 0.0f;
@@ -1050,7 +1052,7 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMa
                         live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail, issued.tail & 1u, &abort_flag));
                         ++issued.tail;
                         if (live) {
-                            zero_rows<DP>(dst, left, lane);
+                            zero_rows<DP>(dst, left, kAttnTile, lane);
                             fence_shared_async();
                         }
                         __syncwarp();
@@ -1180,16 +1182,16 @@ __device__ __forceinline__ void attn_dq(const CUtensorMap& mdo, const CUtensorMa
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(pfree);
-                if (cut) {
-                    mask64(p, 0, lim);
-                    mask64(dp, 0, lim);
-                }
                 uint32_t w[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     const float2 x = p_get(p_mul(p_add(p_make(dp[2 * j], dp[2 * j + 1]), nd), p_make(p[2 * j], p[2 * j + 1])));
-                    w[j] = pack2(x.x, x.y);
+                    dp[2 * j] = x.x;
+                    dp[2 * j + 1] = x.y;
                 }
+                if (cut) mask64(dp, 0, lim);  // dz itself: p, dp and delta of what is masked may be infinite or NaN
+#pragma unroll
+                for (int j = 0; j < 32; ++j) w[j] = pack2(dp[2 * j], dp[2 * j + 1]);
                 tmem_st32(z, w);
                 tc_fence_before();
                 __syncwarp();
@@ -1357,7 +1359,10 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
             for (int j = 0; j < n && live; ++j, ++slots) {
                 const int step = walk.tile(t0 + j), h = head * a.group + step / tiles, t = first + step % tiles;
                 const int row = it.other0 + t * kAttnTile, left = it.others - t * kAttnTile;
-                const bool cut = left < kAttnTile && !it.end;  // both are operands of sums over the queries
+                // Both are operands of sums over the queries: what follows the segment, and queries that see no
+                // key (a gradient of theirs may be infinite or NaN, where a loss divides by what they saw).
+                const int unseen = it.unseen - t * kAttnTile;
+                const bool cut = (left < kAttnTile && !it.end) || unseen > 0;
                 float stat[8];  // four rows' lse, then their delta
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -1388,7 +1393,8 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
                         live = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(tail, issued.tail & 1u, &abort_flag));
                         ++issued.tail;
                         if (live) {
-                            zero_rows<DP>(dst, left, lane);
+                            if (unseen > 0) zero_rows<DP>(dst, 0, min(unseen, kAttnTile), lane);
+                            if (left < kAttnTile) zero_rows<DP>(dst, left, kAttnTile, lane);
                             fence_shared_async();
                         }
                         __syncwarp();
@@ -1518,7 +1524,6 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
                 tc_fence_after();
                 float dp[64];
                 tmem_ld64(dp_tmem + lanes, dp);
-                if (cut) mask64(dp, from - q0, it.others - q0);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const uint4 l = lds128(slot + 512 + 16 * i);
@@ -1526,9 +1531,14 @@ __device__ __forceinline__ void attn_dkv(const CUtensorMap& mdo, const CUtensorM
                                         p_make(p[4 * i], p[4 * i + 1]));
                     const f2r y = p_mul(p_sub(p_make(dp[4 * i + 2], dp[4 * i + 3]), p_make(__uint_as_float(l.z), __uint_as_float(l.w))),
                                         p_make(p[4 * i + 2], p[4 * i + 3]));
-                    w[2 * i] = pack2(p_get(x).x, p_get(x).y);
-                    w[2 * i + 1] = pack2(p_get(y).x, p_get(y).y);
+                    dp[4 * i] = p_get(x).x;
+                    dp[4 * i + 1] = p_get(x).y;
+                    dp[4 * i + 2] = p_get(y).x;
+                    dp[4 * i + 3] = p_get(y).y;
                 }
+                if (cut) mask64(dp, from - q0, it.others - q0);  // dz itself: dp and delta may be infinite or NaN
+#pragma unroll
+                for (int i = 0; i < 32; ++i) w[i] = pack2(dp[2 * i], dp[2 * i + 1]);
                 tmem_st32(dp_tmem + lanes, w);
                 tc_fence_before();
                 __syncwarp();

@@ -23,7 +23,8 @@ struct AttnItem {
     // of the tile is seen by the queries i >= max(0, shift + c) of its segment.
     int32_t shift;
     int32_t end;     // the segment's last row of the other side is the tensor's last: nothing follows
-    int32_t pad[2];
+    int32_t unseen;  // keys: the segment's first queries that see no key at all
+    int32_t pad;
 };
 
 // A unit of work is an item and a head: unit u is head u / items, item u % items. Its cost is its

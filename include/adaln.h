@@ -337,16 +337,17 @@ int adaln_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q
  *     Rq / nseg (Rk / nseg) rows. Lengths may be 0 and differ between the two sides.
  *   - causal != 0: query i of a segment of n queries and m keys sees the keys j <= i + m - n (the last
  *     query sees all).
- *   - A query that sees no key has o = 0, lse = -inf and dq = 0, and adds nothing to dk and dv.
+ *   - A query that sees no key has o = 0, lse = -inf and dq = 0, and adds nothing to dk and dv, whatever it
+ *     and its dout hold.
  *   - scale > 0.
  * bf16 only (ADALN_F32 is ADALN_ERR_UNSUPPORTED: the products run on the tensor cores); 8 <= d <= 128,
  * d % 8 == 0; Hq a multiple of Hk; Rq, Rk, nseg <= 2^30. Row distances are multiples of 8 and at least
  * H * d; pointers 16-byte aligned (lse and the tables 4). Products accumulate in fp32; maxima, sums and lse
  * are fp32; p and dz are rounded to bf16 as operands of the next product; o, dq, dk and dv once at
  * the end. What lies behind a segment's last row reaches nothing of it, NaN included; NaN or infinity in a
- * key or value reaches the rows of its own segment (masked ones too). Results are bitwise reproducible; a
- * segment's may differ in the last bits with what it is packed with (the tiles follow the
- * call's sizes).
+ * key or value reaches the rows of its own segment, in a query that sees a key or its dout dk and dv of the
+ * segment's keys (masked ones too). Results are bitwise reproducible; a segment's may differ in the last bits
+ * with what it is packed with (the tiles follow the call's sizes), not with what the other segments hold.
  * The backward takes the forward's o and lse. dq may be null, or dk and dv both (not wanted).
  * Malformed tables are recorded (ADALN_ERR_BAD_SEQLENS in adaln_read_status) and nothing is computed:
  * outputs stay as they were. Two or three launches either way. */

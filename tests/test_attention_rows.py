@@ -1,5 +1,7 @@
-"""What reaches a row of attention and what does not: other rows of its tile, other segments; and that every
-output is written."""
+"""What reaches a row of attention and what does not: other rows of its tile, other segments, queries that
+see no key; and that every output is written."""
+import math
+
 import pytest
 import torch
 
@@ -56,3 +58,19 @@ def test_every_output_is_written(name):
     got = call(i, causal)
     assert not any(got[n].isnan().any() for n in GRADS + ("lse",))
     check(i, got, causal)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens_q,lens_k", [([300, 129], [200, 40]), ([400, 5, 90], [150, 5, 0]), ([2000], [700])])
+@pytest.mark.parametrize("q_value,dout_value", [(1.0, math.inf), (1.0, math.nan), (math.nan, 1.0), (-math.inf, math.nan)])
+def test_queries_that_see_no_key(lens_q, lens_k, d, q_value, dout_value):
+    # Causal, more queries than keys: the first queries of a segment see nothing. They may hold anything.
+    i = inputs(lens_q, lens_k, 4, 2, d, seed=42)
+    want = call(i, True)
+    none = torch.cat([torch.arange(n, device="cuda") < n - m for n, m in zip(lens_q, lens_k)])
+    got = call(changed(i, q=(none, q_value), dout=(none, dout_value)), True)
+    for n in GRADS:
+        assert torch.equal(got[n], want[n]), n
+    assert torch.equal(got["lse"], want["lse"])
+    assert (got["o"][none] == 0).all() and (got["dq"][none] == 0).all() and (got["lse"][:, none] == -math.inf).all()
