@@ -1569,7 +1569,10 @@ int adaln_attention_bwd(const void* dout, const void* q, const void* k, const vo
     if (sms <= 0) return ADALN_ERR_CUDA;
     const AttnPlan p = attn_plan(nseg, Rq, Rk, Hq, Hk, d, true, sms);
     if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
-    const AttnPlanArgs l = attn_plan_args(t, p, workspace, true);
+    AttnPlanArgs l = attn_plan_args(t, p, workspace, true);
+    // A list that is not wanted is not made (the tables are checked all the same, with the first).
+    if (!dq) l.list[0].items = nullptr;
+    if (!dk) l.list[1].items = nullptr;
     const AttnDeltaArgs e{dout, o, lse, at<float>(workspace, p.delta), at<float>(workspace, p.lse2), Rq, dout_ld, o_ld, Hq, d};
     if (int rc = launched(launch_attn_prepare(l, e, sms, stream))) return rc;
     const AttnRows rdo{dout, Rq, dout_ld, Hq}, rq{q, Rq, q_ld, Hq}, rk{k, Rk, k_ld, Hk}, rv{v, Rk, v_ld, Hk};

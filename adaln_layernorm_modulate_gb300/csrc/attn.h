@@ -61,7 +61,7 @@ struct AttnList {
 
 struct AttnPlanArgs {
     AttnTables t;
-    AttnList list[2];     // over queries; over keys (items null: none)
+    AttnList list[2];     // over queries; over keys (items null: not wanted)
     uint32_t* status;     // [2]
     WsHeader* header;
 };

@@ -1,10 +1,11 @@
 """What reaches a row of attention and what does not: other rows of its tile, other segments, queries that
-see no key; and that every output is written."""
+see no key; that every output is written, and nothing that is not asked for."""
 import math
 
 import pytest
 import torch
 
+import adaln_layernorm_modulate_gb300 as A
 from tests.test_attention import CASES, call, check, inputs
 
 GRADS = ("o", "dq", "dk", "dv")
@@ -74,3 +75,35 @@ def test_queries_that_see_no_key(lens_q, lens_k, d, q_value, dout_value):
         assert torch.equal(got[n], want[n]), n
     assert torch.equal(got["lse"], want["lse"])
     assert (got["o"][none] == 0).all() and (got["dq"][none] == 0).all() and (got["lse"][:, none] == -math.inf).all()
+
+
+@pytest.mark.gpu
+def test_a_list_that_is_not_wanted_is_not_made():
+    # 2000 segments of a query and a key: an entry of 32 bytes each in either work list.
+    i = inputs([1] * 2000, [1] * 2000, 2, 2, 64, seed=43)
+    (R, H, d), nseg = i["q"].shape, 2000
+    o, lse = torch.empty_like(i["q"]), torch.empty(H, R, device="cuda")
+    nb = max(f(nseg, R, R, H, H, d, 1) for f in (A.adaln_attention_fwd_workspace_size, A.adaln_attention_bwd_workspace_size))
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    A.adaln_attention_fwd(i["q"], i["k"], i["v"], o, lse, i["cu_q"], i["cu_k"], nseg, R, R, H, H, d, *[H * d] * 4,
+                          0.125, False, ws, nb)
+    written = {}
+    for name, want_q, want_kv in (("both", True, True), ("q", True, False), ("kv", False, True)):
+        dx = [torch.empty_like(i["q"]) for _ in range(3)]
+        ws.fill_(255)
+        A.adaln_attention_bwd(i["dout"], i["q"], i["k"], i["v"], o, lse, dx[0] if want_q else None,
+                              *(dx[1:] if want_kv else (None, None)), i["cu_q"], i["cu_k"], nseg, R, R, H, H, d,
+                              *[H * d] * 8, 0.125, False, ws, nb)
+        assert A.adaln_read_status(ws) == 0
+        written[name] = int((ws != 255).sum())
+    # (Numbers below 2000 have no byte of 255 but their lowest, one in 256 of them.)
+    assert written["both"] - written["q"] >= 2000 * 28 and written["both"] - written["kv"] >= 2000 * 28, written
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("want_q", [True, False])
+def test_one_list_alone_checks_the_tables_too(want_q):
+    i = inputs([40, 60], [40, 60], 2, 2, 64, seed=44)
+    j = dict(i, cu_q=torch.tensor([0, 60, 40], dtype=torch.int32, device="cuda"))
+    got = call(j, status=6, want_q=want_q, want_kv=not want_q)
+    assert all(t.isnan().all() for t in got.values())
