@@ -1435,9 +1435,9 @@ AttnPlan attn_plan(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk,
         p.items[x] = take((size_t)items(R, kAttnTile) * sizeof(AttnItem));
         p.segs[x] = take((size_t)nseg * sizeof(longlong2));
         p.cursors[x] = take((size_t)(sms + 1) * sizeof(AttnCursor));
-        // Two pieces a CTA; sized for calls of fewer rows too.
+        // Two pieces a CTA, where a unit can be cut at all; sized for calls of fewer rows too.
         p.slot_rows[x] = (int)std::min<int64_t>(R, bwd ? kAttnTile : 2 * kAttnTile);
-        const size_t rows = 2 * (size_t)sms * (size_t)p.slot_rows[x];
+        const size_t rows = p.pieces[x] ? 2 * (size_t)sms * (size_t)p.slot_rows[x] : 0;
         p.part[x] = take(rows * (size_t)d * (x ? 2 : 1) * sizeof(float));
         if (!bwd) p.ml = take(rows * sizeof(float2));
     }

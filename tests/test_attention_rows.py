@@ -107,3 +107,24 @@ def test_one_list_alone_checks_the_tables_too(want_q):
     j = dict(i, cu_q=torch.tensor([0, 60, 40], dtype=torch.int32, device="cuda"))
     got = call(j, status=6, want_q=want_q, want_kv=not want_q)
     assert all(t.isnan().all() for t in got.values())
+
+
+@pytest.mark.gpu
+def test_workspace_has_no_room_for_pieces_that_cannot_be():
+    # Units of fewer than eight steps are never cut. 32 segments of 256: the status, work lists and
+    # statistics of the rows, nothing else.
+    R, H, d = 32 * 256, 12, 128
+    fwd, bwd = A.adaln_attention_fwd_workspace_size, A.adaln_attention_bwd_workspace_size
+    assert fwd(32, R, 7 * 128, H, H, d, 1) <= 65536
+    assert bwd(32, 7 * 128, 7 * 128, H, H, d, 1) <= 65536 + 8 * H * 7 * 128
+    assert fwd(32, R, 8 * 128, H, H, d, 1) > 1 << 20 and bwd(32, R, R, H, H, d, 1) > 1 << 20
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [896, 897])  # seven tiles, eight
+@pytest.mark.parametrize("d", [64, 128])
+def test_both_sides_of_the_pieces_border(n, d):
+    for heads, kv in ((1, 1), (3, 3), (2, 1)):
+        i = inputs([n], [n], heads, kv, d, seed=45)
+        check(i, call(i))
+        check(i, call(i, True), True)
