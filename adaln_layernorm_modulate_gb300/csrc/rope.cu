@@ -17,8 +17,10 @@
 //
 // Angles: a position times a frequency is far more than fp32 holds (position 500,000 at frequency 1 is
 // off by 0.03 rad). Frequencies are turns as binary fractions of 64 bits; the product with the integer
-// position wraps at whole turns by itself, so that what is left, the fraction of a turn, is good to 2^-32
-// of a turn and the frequency's own rounding (a double's) at any position.
+// position wraps at whole turns by itself. What is left, the fraction of a turn, has the frequency's own
+// rounding (a double's, five times 2^-53 of the angle at most), its cut after 64 bits (2^-33 of a turn at any
+// position), the product's after 32, and the rounding to the fp32 argument of sine and cosine: 2^-26 of a
+// turn, the largest.
 #include <atomic>
 
 #include "rope.h"

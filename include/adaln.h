@@ -306,8 +306,8 @@ int adaln_linear_xent_bwd(const void* x, const void* weight, const int64_t* targ
  *   - q_weight, k_weight [d], in `dtype`, each may be null (ones); without a norm both must be.
  *   - pos [R, naxes] (device int32), any values; null: no rotation. axes[naxes] (host, at most 8): the even
  *     widths of the axes, side by side from element 0; a head's elements behind them are not
- *     rotated. theta >= 1. Angles are good to 2^-31 of a turn and the frequencies' own rounding (2^-51 of
- *     the angle), at any position.
+ *     rotated. theta >= 1. Angles are good to 2^-25 of a turn (half of it the fp32 argument of sine and cosine)
+ *     and the frequencies' own rounding (2^-50 of the angle), at any position.
  *   - dq_weight, dk_weight [d] fp32, overwritten; each may be null (not wanted). Without a norm q and k
  *     of the backward are not looked at.
  * R = 0 is valid (zero weight gradients). One launch forward, two backward (one without weight
