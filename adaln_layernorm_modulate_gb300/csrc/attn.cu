@@ -25,9 +25,11 @@
 //
 // Bound by the tensor cores from some thousand rows on: 32760 rows, 12 heads of 128, 4.2 ms forward (1.55
 // PFLOP/s, the tensor pipe 72% active; a step of 128 keys and 256 queries takes 2,800 cycles, its products 2,048).
-// 16384 rows 1.0 ms forward (1.66 PFLOP/s) and 3.5 ms backward (1.18 PFLOP/s, 1.65 with the second z and
-// dp; 75% active: operands and incoming tiles take all that shared memory gives). Short segments by the units'
-// beginnings and ends, the smallest calls by the chain of launches (153 rows: 11 + 17 us).
+// 16384 rows 1.0 ms forward (1.6 PFLOP/s) and 3.4-3.6 ms backward (1.13-1.2 PFLOP/s, 1.6-1.7 with the second z
+// and dp; 75% active: operands and incoming tiles take all that shared memory gives), causal 0.54 and 1.8 ms. Short
+// segments by the units' beginnings and ends, the smallest calls by the chain of launches (153 rows: 11 + 17 us).
+// Times of one direction are of replayed graphs of 20 equal calls; a pass with changing inputs takes 2-5% more
+// than their sum (16384: 4.6-4.7 ms).
 #include <algorithm>
 #include <atomic>
 
@@ -474,7 +476,8 @@ struct AttnIssued {
     bool mma = false;
 };
 
-// Registers a thread of the forward: at launch, then of the rows' warps and of the others.
+// Registers a thread of the forward: at launch, then of the rows' warps and of the others. (The compiler keeps
+// to the launch's and spills: -Xptxas -v, 232 bytes of loads at 128 elements, 220 at 64.)
 constexpr int kFwdRegs = 168, kRowRegs = 208, kOtherRegs = 88;
 static_assert(256 * kRowRegs + 128 * kOtherRegs <= kAttnThreads * kFwdRegs, "no more than the launch brought");
 

@@ -60,6 +60,7 @@ enum : uint32_t {
     kDbgRanks = 128u,    // rank sum: [0, n) of each rank's array and of the output
     kDbgStatus = 256u,   // status words: [0, kMaxCtas)
     kDbgLoss = 512u,     // vocabulary loss: rows, packed rows, partials, dz, dx and dweight
+    // 1024 and 2048 stand beside their kernels: kDbgHeads (rope.h) and kDbgAttn (attn.h).
 };
 #ifdef ADALN_DEBUG
 static __device__ unsigned int g_adaln_debug;  // one per translation unit (module)
