@@ -1550,7 +1550,8 @@ int adaln_attention_bwd(const void* dout, const void* q, const void* k, const vo
     if (!(scale > 0.0f) || !std::isfinite(scale)) return ADALN_ERR_INVALID_ARG;
     AttnTables t;
     if (int rc = attn_tables(cu_q, cu_k, nseg, Rq, Rk, causal, &t)) return rc;
-    if ((dk != nullptr) != (dv != nullptr) || (!dq && !dk && Rq + Rk > 0)) return ADALN_ERR_INVALID_ARG;
+    // (A gradient without rows may be wanted and have no address.)
+    if ((dk != nullptr) != (dv != nullptr) || (!dq && !dk && Rq > 0 && Rk > 0)) return ADALN_ERR_INVALID_ARG;
     if (Rq > 0) {
         if (int rc = check_rows(dout, Rq, Hq, d, dout_ld)) return rc;
         if (int rc = check_rows(q, Rq, Hq, d, q_ld)) return rc;

@@ -128,3 +128,20 @@ def test_both_sides_of_the_pieces_border(n, d):
         i = inputs([n], [n], heads, kv, d, seed=45)
         check(i, call(i))
         check(i, call(i, True), True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,M", [(5, 0), (0, 7), (0, 0), (5, 7)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_node_with_gradients_of_one_side(N, M, packed):
+    # A side that wants its gradient may have no rows.
+    from adaln_layernorm_modulate_gb300.autograd import attention
+    for wanted in ("q", "k", "v", "kv"):
+        q, k, v = (torch.randn(3, n, h, 64, device="cuda", dtype=torch.bfloat16) for n, h in ((N, 4), (M, 2), (M, 2)))
+        cu = [torch.arange(4, device="cuda", dtype=torch.int32) * n for n in (N, M)] if packed else []
+        x = [(t.flatten(0, 1) if packed else t).requires_grad_(n in wanted) for n, t in zip("qkv", (q, k, v))]
+        attention(*x, *cu, check_tables=True).sum().backward()
+        for n, t in zip("qkv", x):
+            assert (t.grad is None) == (n not in wanted)
+            assert t.grad is None or (t.grad.shape == t.shape and not t.grad.isnan().any())
+            assert t.grad is None or (N and M) or (t.grad == 0).all()
