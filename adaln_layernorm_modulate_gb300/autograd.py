@@ -520,7 +520,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Opt
     multiple of Hk, d a multiple of 8 up to 128. causal: query i of n sees keys j <= i + m - n. scale:
     d ** -0.5 if None. Returns o like q; with return_lse also lse, [Hq, Rq] or [Hq, B, N], which carries no
     gradient. Sums and lse are fp32; probabilities and their gradients are rounded to bfloat16 for the next
-    product, and the backward takes the bfloat16 o: errors of 1.4 roundings in o and dv, 1.5 to 2 in dq and dk.
+    product, and the backward takes the bfloat16 o: errors of 1.4 roundings in o and dv, 1.4 to 1.8 in dq and dk.
     q, k and v whose heads or rows the library cannot take as they lie (a slice of a dense batch's rows among
     them) are copied. ``check_tables`` reads the call's device status (it synchronises the stream); without it
     malformed tables leave the outputs unwritten."""

@@ -1574,7 +1574,8 @@ int adaln_attention_bwd(const void* dout, const void* q, const void* k, const vo
     // A list that is not wanted is not made (the tables are checked all the same, with the first).
     if (!dq) l.list[0].items = nullptr;
     if (!dk) l.list[1].items = nullptr;
-    const AttnDeltaArgs e{dout, o, lse, at<float>(workspace, p.delta), at<float>(workspace, p.lse2), Rq, dout_ld, o_ld, Hq, d};
+    const AttnDeltaArgs e{dout, o, lse, at<float>(workspace, p.delta), at<float>(workspace, p.lse2), Rq, dout_ld, o_ld,
+                          Hq, d, q, k, v, Rk, q_ld, k_ld, v_ld, Hq / Hk, 0, scale};
     if (int rc = launched(launch_attn_prepare(l, e, sms, stream))) return rc;
     const AttnRows rdo{dout, Rq, dout_ld, Hq}, rq{q, Rq, q_ld, Hq}, rk{k, Rk, k_ld, Hk}, rv{v, Rk, v_ld, Hk};
     AttnBwdArgs a{};

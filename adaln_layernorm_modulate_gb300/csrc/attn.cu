@@ -21,13 +21,13 @@
 // sum then stays in tensor memory in a fixed order, without atomics and without an fp32 dq in memory.
 //
 // Sums, maxima, exponentials and lse are fp32. Rounded to bf16 as operands: p (half a step, 2^-8 of
-// each value) and dz. delta is taken from the caller's bf16 o.
+// each value) and dz. delta is taken from the caller's bf16 o, of rows of few keys from the scores.
 //
 // Bound by the tensor cores from some thousand rows on: 32760 rows, 12 heads of 128, 4.2 ms forward (1.55
 // PFLOP/s, the tensor pipe 72% active; a step of 128 keys and 256 queries takes 2,800 cycles, its products 2,048).
 // 16384 rows 1.0 ms forward (1.6 PFLOP/s) and 3.4-3.6 ms backward (1.13-1.2 PFLOP/s, 1.6-1.7 with the second z
 // and dp; 75% active: operands and incoming tiles take all that shared memory gives), causal 0.54 and 1.8 ms. Short
-// segments by the units' beginnings and ends, the smallest calls by the chain of launches (153 rows: 11 + 17 us).
+// segments by the units' beginnings and ends, the smallest calls by the chain of launches (153 rows: 11 + 20 us).
 // Times of one direction are of replayed graphs of 20 equal calls; a pass with changing inputs takes 2-5% more
 // than their sum (16384: 4.6-4.7 ms).
 #include <algorithm>
@@ -238,9 +238,33 @@ __device__ __forceinline__ void attn_plan(const AttnPlanArgs& a, int list) {
     }
 }
 
+// What row r of the queries sees: `seen` keys from k0 on, of segment s; -1 where the tables say nothing usable (they
+// are reported, and nothing is computed).
+struct AttnSeen {
+    int s, k0, seen;
+    __device__ __forceinline__ bool few() const { return seen > 0 && seen <= kAttnFewKeys; }
+};
+__device__ __forceinline__ AttnSeen attn_seen(const AttnTables& t, int64_t s, int64_t r) {
+    const int64_t q0 = attn_start(t.cu_q, s, t.nseg, t.Rq), q1 = attn_start(t.cu_q, s + 1, t.nseg, t.Rq);
+    const int64_t k0 = attn_start(t.cu_k, s, t.nseg, t.Rk), k1 = attn_start(t.cu_k, s + 1, t.nseg, t.Rk);
+    if (r < q0 || r >= q1 || k0 < 0 || k1 < k0 || k1 > t.Rk) return AttnSeen{(int)s, 0, -1};
+    const int64_t seen = t.causal ? min(k1 - k0, r + 1 - q1 + k1 - k0) : k1 - k0;
+    return AttnSeen{(int)s, (int)k0, (int)max(seen, (int64_t)0)};
+}
+__device__ __forceinline__ AttnSeen attn_seen(const AttnTables& t, int64_t r) {
+    int64_t lo = 0, hi = t.nseg - 1;  // the last segment that begins at or before r
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) >> 1;
+        if (attn_start(t.cu_q, mid, t.nseg, t.Rq) <= r) lo = mid;
+        else hi = mid - 1;
+    }
+    return attn_seen(t, lo, r);
+}
+
 // delta = dout . o of every row and head, and lse in units of log 2: 16 lanes a head, a warp two heads of a row,
-// four such pairs on their way.
-__device__ __forceinline__ void attn_delta(const AttnDeltaArgs& a, int64_t block, int64_t blocks) {
+// four such pairs on their way. FEW: there may be rows of few keys, whose delta is attn_delta_few's.
+template <bool FEW>
+__device__ __forceinline__ void attn_delta(const AttnTables& t, const AttnDeltaArgs& a, int64_t block, int64_t blocks) {
     constexpr int U = 4, NW = kPlanThreads / 32;
     const int lane = threadIdx.x & 15, group = threadIdx.x >> 4 & 1, vecs = a.d / 8, pairs = (a.Hq + 1) / 2;
     const int64_t first = block * NW + (threadIdx.x >> 5), step = blocks * NW;
@@ -249,11 +273,13 @@ __device__ __forceinline__ void attn_delta(const AttnDeltaArgs& a, int64_t block
     int at = (int)(first % pairs);
     const int64_t dr = step / pairs;
     const int da = (int)(step % pairs);
-    while (r < a.Rq) {
+    uint32_t few = 0;  // of the warp's next 32 pairs, those whose row is attn_delta_few's
+    for (int n = 0; r < a.Rq; n += U) {
         uint4 x[U], y[U];
-        float lse[U];
+        float lse[U], v[U];
         int64_t rows[U];
         int heads[U];
+        const int64_t pair = r * pairs + at;
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const int h = heads[j] = 2 * at + group;
@@ -281,25 +307,148 @@ __device__ __forceinline__ void attn_delta(const AttnDeltaArgs& a, int64_t block
             Io<__nv_bfloat16>::unpackp(y[j], q);
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum = p_fma(p[e], q[e], sum);
-            float v = p_hsum(sum);
+            v[j] = p_hsum(sum);
 #pragma unroll
-            for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            for (int o = 8; o >= 1; o >>= 1) v[j] += __shfl_xor_sync(0xFFFFFFFFu, v[j], o);
+        }
+        if (FEW) few >>= U;
+        if (FEW && n % 32 == 0) {  // a lane a pair, behind the loads
+            const int64_t row = (pair + (threadIdx.x & 31) * step) / pairs;
+            few = __ballot_sync(0xFFFFFFFFu, row < a.Rq && attn_seen(t, row).few());
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
             if (lane == 0 && rows[j] < a.Rq && heads[j] < a.Hq && ADALN_IN_ATTN(rows[j] >= 0)) {
-                a.delta[(int64_t)heads[j] * a.Rq + rows[j]] = v;
+                if (!FEW || !(few >> j & 1)) a.delta[(int64_t)heads[j] * a.Rq + rows[j]] = v[j];
                 a.lse2[(int64_t)heads[j] * a.Rq + rows[j]] = lse[j] * kLog2e;
             }
         }
     }
 }
 
-// The work lists, a CTA each, and beside them, backward, delta.
-__global__ void __launch_bounds__(kPlanThreads) attn_prepare_kernel(const __grid_constant__ AttnPlanArgs p,
-                                                            const __grid_constant__ AttnDeltaArgs d, int lists) {
+__device__ __forceinline__ void mma_m16n8k16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// delta of rows that see at most kAttnFewKeys keys, from its definition: sum p dp. delta = dout . o has the rounding of
+// the caller's bf16 o, and of p in it: little beside what a row of many keys sums, but with few keys dp - delta is
+// a difference of near values. In the 2-norm, where one rounding is 0.0017, dq of rows over 2, 3, 8, 17, 33 keys was
+// off by 0.0048, 0.0040, 0.0032, 0.0029, 0.0028 (three rows of three: 0.0060) and now 0.0024 up to 32, 0.0030 at
+// worst. Backward of 153 causal rows 17.2 -> 19.9 us, causal 15927 x 16 x 64 679 -> 684, 200 causal segments of 200
+// 364 -> 392, 1000 of 30 688 -> 762, 32760 rows over 16 keys 179 -> 276 (12 heads of 128); rows of 64 keys too:
+// 23 us for the 153 rows and 440 for the 200 segments. Calls without such rows as before.
+//
+// A warp takes 16 rows and a head (tcgen05's tiles of 128 rows would be mostly empty), the keys of one segment after
+// another's, 16 at a time. The sum over a head's elements may go in any order: lane t of four holds elements
+// 8 t .. 8 t + 7 of every 32, one 16-byte load, as two steps of the product.
+__device__ __forceinline__ void attn_delta_few(const AttnTables& t, const AttnDeltaArgs& a, int64_t block, int64_t blocks) {
+    constexpr int NW = kPlanThreads / 32, NT = 2;  // tiles of 8 keys at once
+    using T = __nv_bfloat16;
+    const int lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
+    // Causal: the first rows of every segment that see a key. Else all groups of 16 rows are looked at.
+    const int64_t units = (t.causal ? t.nseg * kAttnFewBlocks : (a.Rq + 15) / 16) * a.Hq;
+    const float sl2 = a.scale * kLog2e;
+    auto load = [&](const void* p, int64_t ld, int64_t row, bool in, int head, int e) {
+        return in && e < a.d ? *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p) + row * ld + (int64_t)head * a.d + e)
+                             : make_uint4(0, 0, 0, 0);
+    };
+    for (int64_t u = block * NW + (threadIdx.x >> 5); u < units; u += blocks * NW) {
+        const int h = (int)(u % a.Hq), kv = h / a.group;
+        int64_t r0 = u / a.Hq * 16;
+        AttnSeen own{-1, 0, -1};  // lanes 0 .. 15: a row each
+        if (t.causal) {
+            const int64_t s = u / a.Hq / kAttnFewBlocks;
+            const int64_t q0 = attn_start(t.cu_q, s, t.nseg, t.Rq), q1 = attn_start(t.cu_q, s + 1, t.nseg, t.Rq);
+            const int64_t nk = attn_start(t.cu_k, s + 1, t.nseg, t.Rk) - attn_start(t.cu_k, s, t.nseg, t.Rk);
+            if (q0 < 0 || q1 > a.Rq) continue;
+            r0 = max(q0, q1 - nk) + 16 * (u / a.Hq % kAttnFewBlocks);
+            if (lane < 16) own = attn_seen(t, s, r0 + lane);
+        } else if (lane < 16 && r0 + lane < a.Rq) {
+            own = attn_seen(t, r0 + lane);
+        }
+        uint32_t left = __ballot_sync(0xFFFFFFFFu, own.few());
+        if (left == 0) continue;
+        // This lane's two rows: as the products have them.
+        const int64_t ra = r0 + g, rb = ra + 8;
+        const bool ina = ra < a.Rq && ADALN_IN_ATTN(ra >= 0 && h < a.Hq), inb = rb < a.Rq && ADALN_IN_ATTN(rb >= 0);
+        const float la = ina ? __ldcg(a.lse + (int64_t)h * a.Rq + ra) * kLog2e : 0.0f;
+        const float lb = inb ? __ldcg(a.lse + (int64_t)h * a.Rq + rb) * kLog2e : 0.0f;
+        const int sa = __shfl_sync(0xFFFFFFFFu, own.seen, g), sb = __shfl_sync(0xFFFFFFFFu, own.seen, g + 8);
+        while (left) {
+            const int lead = 31 - __clz(left);  // a segment's last row here sees most
+            const int s = __shfl_sync(0xFFFFFFFFu, own.s, lead), k0 = __shfl_sync(0xFFFFFFFFu, own.k0, lead);
+            const int keys = __shfl_sync(0xFFFFFFFFu, own.seen, lead);
+            const uint32_t mine = left & __ballot_sync(0xFFFFFFFFu, own.s == s);
+            left &= ~mine;
+            float va = 0.0f, vb = 0.0f;
+            for (int j0 = 0; j0 < keys; j0 += 8 * NT) {
+                float z[NT][4] = {}, dp[NT][4] = {};
+#pragma unroll 1
+                for (int e = 8 * q4; e - 8 * q4 < a.d; e += 32) {
+                    const uint4 xa = load(a.q, a.q_ld, ra, ina, h, e), xb = load(a.q, a.q_ld, rb, inb, h, e);
+                    const uint4 ya = load(a.dout, a.do_ld, ra, ina, h, e), yb = load(a.dout, a.do_ld, rb, inb, h, e);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int j = j0 + 8 * n + g;
+                        const bool in = j < keys && ADALN_IN_ATTN(k0 >= 0 && (int64_t)k0 + j < a.Rk);
+                        const uint4 k = load(a.k, a.k_ld, (int64_t)k0 + j, in, kv, e), v = load(a.v, a.v_ld, (int64_t)k0 + j, in, kv, e);
+                        mma_m16n8k16(z[n], xa.x, xb.x, xa.y, xb.y, k.x, k.y);
+                        mma_m16n8k16(z[n], xa.z, xb.z, xa.w, xb.w, k.z, k.w);
+                        mma_m16n8k16(dp[n], ya.x, yb.x, ya.y, yb.y, v.x, v.y);
+                        mma_m16n8k16(dp[n], ya.z, yb.z, ya.w, yb.w, v.z, v.w);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int j = j0 + 8 * n + 2 * q4 + c;
+                        if (j < sa) va = fmaf(exp2_ftz(fmaf(z[n][c], sl2, -la)), dp[n][c], va);
+                        if (j < sb) vb = fmaf(exp2_ftz(fmaf(z[n][2 + c], sl2, -lb)), dp[n][2 + c], vb);
+                    }
+                }
+            }
+#pragma unroll
+            for (int o = 2; o >= 1; o >>= 1) {
+                va += __shfl_xor_sync(0xFFFFFFFFu, va, o);
+                vb += __shfl_xor_sync(0xFFFFFFFFu, vb, o);
+            }
+            if (q4 == 0 && (mine >> g & 1) && ina) a.delta[(int64_t)h * a.Rq + ra] = va;
+            if (q4 == 0 && (mine >> (g + 8) & 1) && inb) a.delta[(int64_t)h * a.Rq + rb] = vb;
+        }
+    }
+}
+
+// Whether any row sees 1 .. kAttnFewKeys keys: the whole CTA looks through the tables. (Causal: the first rows of
+// every segment do.)
+__device__ __forceinline__ bool attn_any_few(const AttnTables& t) {
+    bool any = t.causal != 0;
+    for (int64_t s = threadIdx.x; s < t.nseg && !any; s += kPlanThreads) {
+        const int64_t nk = attn_start(t.cu_k, s + 1, t.nseg, t.Rk) - attn_start(t.cu_k, s, t.nseg, t.Rk);
+        any = nk > 0 && nk <= kAttnFewKeys;
+    }
+    return __syncthreads_or(any);
+}
+
+// The work lists, a CTA each, and beside them, backward, delta: CTAs for rows of few keys, which wait for copies most of
+// the time, and the others in turn.
+__global__ void __launch_bounds__(kPlanThreads, 2) attn_prepare_kernel(const __grid_constant__ AttnPlanArgs p,
+                                                               const __grid_constant__ AttnDeltaArgs d, int lists) {
     pdl_begin();
-    if ((int)blockIdx.x < lists)
+    const int at = (int)blockIdx.x - lists, all = (int)gridDim.x - lists - d.few, both = 2 * min(d.few, all);
+    if (at < 0) {
         attn_plan(p, blockIdx.x);
-    else
-        attn_delta(d, (int)blockIdx.x - lists, (int)gridDim.x - lists);
+        return;
+    }
+    const bool any_few = d.few > 0 && attn_any_few(p.t);
+    if (at < both ? at % 2 != 0 : d.few <= all)
+        any_few ? attn_delta<true>(p.t, d, at < both ? at / 2 : at - d.few, all)
+                : attn_delta<false>(p.t, d, at < both ? at / 2 : at - d.few, all);
+    else if (any_few)
+        attn_delta_few(p.t, d, at < both ? at / 2 : at - all, d.few);
 }
 
 // The work list is written by the kernel ahead, which this kernel may have been scheduled before: read
@@ -1678,7 +1827,11 @@ cudaError_t launch_attn_prepare(const AttnPlanArgs& plan, const AttnDeltaArgs& d
     AttnPlanArgs p = plan;
     AttnDeltaArgs d = delta;
     int lists = p.list[1].items ? 2 : 1;
-    const unsigned ctas = d.delta && d.Rq > 0 ? cap((d.Rq * ((d.Hq + 1) / 2) + 63) / 64, 4 * (int64_t)sms) : 0;
+    unsigned ctas = d.delta && d.Rq > 0 ? cap((d.Rq * ((d.Hq + 1) / 2) + 63) / 64, 4 * (int64_t)sms) : 0;
+    // Segments of equal lengths tell whether any row sees few keys; tables are on the device.
+    const bool few = ctas && (p.t.causal || p.t.Rk <= kAttnFewKeys * p.t.nseg || (p.t.nseg > 1 && p.t.cu_k));
+    d.few = few ? (int)cap((p.t.causal ? p.t.nseg * kAttnFewBlocks : (d.Rq + 15) / 16) * d.Hq / 16 + 1, 4 * (int64_t)sms) : 0;
+    ctas += d.few;
     void* params[] = {&p, &d, &lists};
     return launch_dependent(reinterpret_cast<const void*>(&attn_prepare_kernel), dim3(lists + ctas), dim3(kPlanThreads), params,
                             0, stream);

@@ -11,6 +11,8 @@ constexpr uint32_t kDbgAttn = 2048u;  // debug builds: rows, heads, work items, 
 constexpr int kAttnTile = 128;       // rows of an operand tile, keys of a step
 constexpr int kAttnMaxD = 128;       // elements of a head
 constexpr int kAttnMaxCtas = 256;    // of one launch
+constexpr int kAttnFewKeys = 32;     // rows of queries that see no more take delta from the scores
+constexpr int kAttnFewBlocks = kAttnFewKeys / 16;  // of 16 such rows, a causal segment
 constexpr int kAttnMaxRows = 1 << 30;  // of either side: row and key numbers and their sums are 32 bits
 
 // One tile of rows of a segment (of queries; of keys for dk and dv) and what it meets.
@@ -112,6 +114,10 @@ struct AttnDeltaArgs {
     float* lse2;           // [Hq, Rq] lse in units of log 2
     int64_t Rq, do_ld, o_ld;
     int Hq, d;
+    const void *q, *k, *v;  // rows of few keys
+    int64_t Rk, q_ld, k_ld, v_ld;
+    int group, few;         // CTAs for them (of the launch; 0: there are none)
+    float scale;
 };
 
 // A side's rows as the kernels' TMA maps take them.

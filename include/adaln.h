@@ -348,7 +348,8 @@ int adaln_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q
  * key or value reaches the rows of its own segment, in a query that sees a key or its dout dk and dv of the
  * segment's keys (masked ones too). Results are bitwise reproducible; a segment's may differ in the last bits
  * with what it is packed with (the tiles follow the call's sizes), not with what the other segments hold.
- * The backward takes the forward's o and lse. dq may be null, or dk and dv both (not wanted).
+ * The backward takes the forward's o and lse (rowsum(dout o) of queries that see at most 32 keys from the
+ * scores: a rounded o is too far off where few keys share a row). dq may be null, or dk and dv both (not wanted).
  * Malformed tables are recorded (ADALN_ERR_BAD_SEQLENS in adaln_read_status) and nothing is computed:
  * outputs stay as they were. Two or three launches either way. */
 size_t adaln_attention_fwd_workspace_size(int64_t nseg, int64_t Rq, int64_t Rk, int32_t Hq, int32_t Hk, int32_t d,

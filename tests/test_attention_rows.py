@@ -9,6 +9,7 @@ import adaln_layernorm_modulate_gb300 as A
 from tests.test_attention import CASES, call, check, inputs
 
 GRADS = ("o", "dq", "dk", "dv")
+H, U = 2.0 ** -8, 2.0 ** -24
 
 
 def changed(i, **rows):
@@ -145,3 +146,59 @@ def test_node_with_gradients_of_one_side(N, M, packed):
             assert (t.grad is None) == (n not in wanted)
             assert t.grad is None or (t.grad.shape == t.shape and not t.grad.isnan().any())
             assert t.grad is None or (N and M) or (t.grad == 0).all()
+
+
+def average_errors(i, causal):
+    """Errors of dq, dk and dv in the 2-norm, over what independent roundings leave: results and dz (for dv: p) are
+    off by at most H of each value, H / sqrt(3) in the mean square where all have the worst mantissa."""
+    got = call(i, causal)
+    q, k, v, do = (i[n].double() for n in ("q", "k", "v", "dout"))
+    group, scale = q.shape[1] // k.shape[1], q.shape[2] ** -0.5
+    bad, size = torch.zeros(3, dtype=torch.float64), torch.zeros(3, dtype=torch.float64)
+    a = b = 0
+    for n, m in zip(i["lens_q"], i["lens_k"]):
+        Q, D = (t[a: a + n].transpose(0, 1) for t in (q, do))
+        K, V = (t[b: b + m].repeat_interleave(group, 1).transpose(0, 1) for t in (k, v))
+        z = scale * Q @ K.transpose(1, 2)
+        if causal:
+            z = z.masked_fill(torch.ones(n, m, dtype=torch.bool, device="cuda").triu(m - n + 1), -math.inf)
+        p = torch.softmax(z, 2).nan_to_num(0)
+        dp = D @ V.transpose(1, 2)
+        dz = scale * p * (dp - (p * dp).sum(2, keepdim=True))
+        shared = lambda t: t.unflatten(0, (-1, group)).sum(1)
+        ref = dz @ K, shared(dz.transpose(1, 2) @ Q), shared(p.transpose(1, 2) @ D)
+        terms = (dz ** 2) @ K ** 2, shared((dz ** 2).transpose(1, 2) @ Q ** 2), shared((p ** 2).transpose(1, 2) @ D ** 2)
+        for x, (name, r0, r1) in enumerate((("dq", a, a + n), ("dk", b, b + m), ("dv", b, b + m))):
+            bad[x] += (got[name][r0:r1].double().transpose(0, 1) - ref[x]).square().sum().cpu()
+            size[x] += (ref[x].square().sum() + terms[x].sum()).cpu()
+        a, b = a + n, b + m
+    return (bad / (size * H ** 2 / 3)).sqrt()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [8, 40, 64, 128])
+@pytest.mark.parametrize("n,m,causal", [(400, 2, False), (400, 3, False), (77, 16, False), (200, 32, False), (2, 2, True),
+                                        (3, 3, True), (17, 17, True), (31, 33, True), (40, 8, True)])
+def test_gradients_of_rows_of_few_keys(n, m, causal, d):
+    # dp - delta is a difference of near values there: delta of a rounded o would be off by as much as dz is.
+    # Many short segments of other lengths among them, so that groups of rows hold several.
+    times = max(1, 1200 // n)
+    lens_q, lens_k = [n] * times + [0, n, 1, 5], [m] * times + [m, 0, 1, 4]
+    i = inputs(lens_q, lens_k, 4, 2, d, seed=46)
+    # More roundings than a thousand, so that their mean square is near its expectation; fp32's own errors are
+    # far below.
+    assert (average_errors(i, causal) <= 1.1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [False, True])
+def test_rows_of_one_key_have_no_gradient(causal):
+    # p = 1 and dp = delta: what is left is the difference of two sums of d products in fp32, 2 (d / 16 + 12) U of
+    # their sizes, and p's own error of 2^-20.
+    i = inputs([1] * 700, [1] * 700, 4, 2, 64, seed=47)
+    got = call(i, causal)
+    dp = (i["dout"].double().unflatten(1, (2, 2)).abs() * i["v"].double().abs()[:, :, None]).sum(3, keepdim=True)
+    err = 64 ** -0.5 * (2 * 16 * U + 2.0 ** -20) * dp
+    K, Q = i["k"].double().abs()[:, :, None], i["q"].double().abs().unflatten(1, (2, 2))
+    assert (got["dq"].double().abs().unflatten(1, (2, 2)) <= err * K).all()
+    assert (got["dk"].double().abs() <= (err * Q).sum(2)).all()
