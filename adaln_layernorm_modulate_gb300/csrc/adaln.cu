@@ -1499,7 +1499,7 @@ int adaln_attention_fwd(const void* q, const void* k, const void* v, void* o, fl
     const AttnPlan p = attn_plan(nseg, Rq, Rk, Hq, Hk, d, false, sms);
     if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
     const AttnPlanArgs l = attn_plan_args(t, p, workspace, false);
-    if (int rc = launched(launch_attn_prepare(l, AttnDeltaArgs{}, sms, stream))) return rc;
+    if (int rc = launched(launch_attn_plan(l, stream))) return rc;
     if (Rq == 0) return ADALN_OK;
     AttnFwdArgs a{};
     a.list = l.list[0];

@@ -4,7 +4,7 @@
 //     dv = p^T dout,  dp = dout v^T,  dz = p (dp - delta),  delta = dout . o
 //     dq = scale dz k,  dk = scale dz^T q
 //
-// attn_prepare_kernel lists the tiles of rows of all segments and cuts them, with the heads, into equal shares;
+// attn_plan lists the tiles of rows of all segments and cuts them, with the heads, into equal shares;
 // persistent CTAs, one an SM, walk theirs. Every product is a tcgen05.mma of 128 rows with its accumulator in
 // tensor memory, its operands brought by TMA; p and dz (bf16, the products' types) are written back to
 // tensor memory over the scores that they come from and are operands from there, so that they never pass
@@ -433,8 +433,15 @@ __device__ __forceinline__ bool attn_any_few(const AttnTables& t) {
     return __syncthreads_or(any);
 }
 
-// The work lists, a CTA each, and beside them, backward, delta: CTAs for rows of few keys, which wait for copies most of
-// the time, and the others in turn.
+// The forward's work list. (A kernel of its own: as a part of the backward's, with its spills, 1 over 32760 took 52.4 us
+// instead of 50.2.)
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnPlanArgs p) {
+    pdl_begin();
+    attn_plan(p, 0);
+}
+
+// The backward's work lists, a CTA each, and beside them delta: CTAs for rows of few keys, which wait for copies most of
+// the time, and the others in turn. Two CTAs an SM: delta needs their loads (32760 over 512: 344 us with one).
 __global__ void __launch_bounds__(kPlanThreads, 2) attn_prepare_kernel(const __grid_constant__ AttnPlanArgs p,
                                                                const __grid_constant__ AttnDeltaArgs d, int lists) {
     pdl_begin();
@@ -1823,11 +1830,17 @@ bool rows_map(CUtensorMap* m, const AttnRows& x, int d, int box_rows = kAttnTile
 
 }  // namespace
 
+cudaError_t launch_attn_plan(const AttnPlanArgs& plan, cudaStream_t stream) {
+    AttnPlanArgs p = plan;
+    void* params[] = {&p};
+    return launch_dependent(reinterpret_cast<const void*>(&attn_plan_kernel), dim3(1), dim3(kPlanThreads), params, 0, stream);
+}
+
 cudaError_t launch_attn_prepare(const AttnPlanArgs& plan, const AttnDeltaArgs& delta, int sms, cudaStream_t stream) {
     AttnPlanArgs p = plan;
     AttnDeltaArgs d = delta;
     int lists = p.list[1].items ? 2 : 1;
-    unsigned ctas = d.delta && d.Rq > 0 ? cap((d.Rq * ((d.Hq + 1) / 2) + 63) / 64, 4 * (int64_t)sms) : 0;
+    unsigned ctas = d.Rq > 0 ? cap((d.Rq * ((d.Hq + 1) / 2) + 63) / 64, 4 * (int64_t)sms) : 0;
     // Segments of equal lengths tell whether any row sees few keys; tables are on the device.
     const bool few = ctas && (p.t.causal || p.t.Rk <= kAttnFewKeys * p.t.nseg || (p.t.nseg > 1 && p.t.cu_k));
     d.few = few ? (int)cap((p.t.causal ? p.t.nseg * kAttnFewBlocks : (d.Rq + 15) / 16) * d.Hq / 16 + 1, 4 * (int64_t)sms) : 0;

@@ -127,7 +127,8 @@ struct AttnRows {
     int H;
 };
 
-// The work lists and, with delta.delta, delta.
+// The forward's work list; the backward's lists and delta.
+cudaError_t launch_attn_plan(const AttnPlanArgs& plan, cudaStream_t stream);
 cudaError_t launch_attn_prepare(const AttnPlanArgs& plan, const AttnDeltaArgs& delta, int sms, cudaStream_t stream);
 cudaError_t launch_attn_fwd(const AttnFwdArgs& args, const AttnRows& q, const AttnRows& k, const AttnRows& v,
                             cudaStream_t stream);
